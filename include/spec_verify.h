@@ -67,11 +67,13 @@ typedef enum {
   SV_ERR_MISALIGNED = 5,          /* a pointer is not aligned to its element type (workspace: 16 B) */
   SV_ERR_CUDA = 6,                /* a CUDA runtime call failed (device query or launch)          */
   SV_ERR_UNSUPPORTED_DEVICE = 7,  /* the current device is not compute capability 10.3           */
-  SV_ERR_SCRATCH_TOO_SMALL = 8    /* spec_verify_noalloc: the sizes need more scratch than
+  SV_ERR_SCRATCH_TOO_SMALL = 8,   /* spec_verify_noalloc: the sizes need more scratch than
                                      SV_NOALLOC_SCRATCH_BYTES                                     */
+  SV_ERR_OVERLAP = 9              /* an output array is also an input that the call reads         */
 } sv_status;
 
-typedef enum { SV_DTYPE_F32 = 0, SV_DTYPE_BF16 = 1 } sv_dtype;
+/* Logits are SV_DTYPE_F32 or SV_DTYPE_BF16, paged caches SV_DTYPE_BF16 or SV_DTYPE_F16. */
+typedef enum { SV_DTYPE_F32 = 0, SV_DTYPE_BF16 = 1, SV_DTYPE_F16 = 2 } sv_dtype;
 
 #define SV_MAX_GAMMA 64
 #define SV_VERSION 1
@@ -274,6 +276,122 @@ int spec_verify_kv_rollback(const int32_t* prefix_len, const int32_t* draft_len,
                             int32_t* target_len_out, int32_t* drafter_len_out, void* cache,
                             int64_t cache_row_stride, int32_t entry_bytes, int32_t cache_entries,
                             int32_t B, int32_t gamma_max, void* cuda_stream);
+
+/* ------------------------------------------------------------------------------------------------
+ * The paged cache of a round: append, attention, attention weights, eviction.
+ *
+ * [R] "Speculative decoding", rayaq.ca ml-models -- Verification attention and the cache: one pass of
+ * the target attends the round's tokens over the cache, then the cache keeps what was accepted.
+ * [B] "Inference: distillation and speculative decoding", brunomaga.github.io -- Medusa: the nodes of
+ * a candidate tree attend their own ancestors.
+ *
+ * Entry j of row b sits in slot j % page_size of page page_table[b, j / page_size]. Row b holds n_b =
+ * prefix_len[b] entries before the round; the round's token i is entry n_b + i. Per entry and key head
+ * there are D = head_dim keys and D values, and, when weight is given, one fp32 attention weight
+ * (what the tokens so far gave to that entry: the sum of their softmax probabilities).
+ *
+ * k, v         pages of `dtype`, element (page, head, slot, d) at page * page_stride + head *
+ *              head_stride + slot * slot_stride + d elements: any order of pages, heads and slots with
+ *              the D elements of one head together. 16-byte aligned bases, strides multiples of 8
+ *              (else SV_ERR_MISALIGNED).
+ * weight       [num_pages, heads, page_size] fp32, contiguous, or NULL.
+ * page_table   [B, max_pages] int32; only the entries that a row's length reaches are read.
+ * heads        key heads; a call's query heads are a multiple of it (query head h reads key head
+ *              h / (query heads / heads)).
+ * head_dim     64, 128 or 256. page_size: 16, 32, 64, 128 or 256. dtype: SV_DTYPE_BF16 or SV_DTYPE_F16.
+ *              max_pages * page_size <= 1048576 entries a row.
+ * The struct is host memory, read before the call returns; the arrays are caller-owned device memory.
+ * Rows may share pages that are only read (a common prefix); spec_verify_kv_append and
+ * spec_verify_kv_evict need the pages they write to be the row's own.
+ *
+ * Data errors never trap. A row is in error when a length or count is out of range, its entries
+ * exceed max_pages * page_size, or a page number that its entries reach is outside [0, num_pages). */
+typedef struct {
+  void* k;
+  void* v;
+  float* weight;
+  const int32_t* page_table;
+  int64_t page_stride, head_stride, slot_stride;
+  int32_t num_pages, page_size, max_pages, heads, head_dim, dtype;
+} sv_paged_cache;
+
+/* Writes a round's keys and values into the cache: entry prefix_len[b] + d of row b takes token d of
+ * the row, or token path[b, d] when a path is given (the kept path of a verified tree:
+ * spec_verify_tree_greedy's out_path and out_path_len). The weight of a written entry becomes 0.
+ *
+ * k_new, v_new   [B, N, heads, D] of the cache's dtype; token i of row b at b * row_stride +
+ *                i * token_stride elements, its heads together (a slice of a fused projection).
+ *                16-byte aligned bases, strides multiples of 8. They must not overlap the cache.
+ * num_new        [B] int32, tokens to write, 0..N; NULL: N. -1 (a row error of the verification)
+ *                writes nothing and is not an error here: out_len is prefix_len.
+ * path           [B, N] int32 or NULL.
+ * out_len        [B] int32, entries after the call: prefix_len + num_new; -1 for a row in error, or one
+ *                with a path entry outside [0, N), of which nothing is written. May be NULL.
+ * 1 <= N <= SV_MAX_GAMMA + 1. One launch on cuda_stream. */
+int spec_verify_kv_append(const void* k_new, const void* v_new, int64_t row_stride,
+                          int64_t token_stride, const sv_paged_cache* cache,
+                          const int32_t* prefix_len, const int32_t* num_new, const int32_t* path,
+                          int32_t* out_len, int32_t B, int32_t N, void* cuda_stream);
+
+/* Attention of a round's tokens over the paged cache, which already holds the round's own entries.
+ * Token i < m_b = num_queries[b] of row b attends the n_b entries before the round, itself, and of the
+ * round's other tokens those before it (a chain), or its ancestors when tree_parents is given:
+ *   s_ij = scale * q_i . k_j,  lse_i = log sum_j exp(s_ij),  out_i = sum_j exp(s_ij - lse_i) v_j.
+ * An entry that a token does not attend has no part in its outputs, whatever it holds (NaN included).
+ * m_b = 1 is the attention of one new token.
+ *
+ * q              [B, N, Hq, D] of the cache's dtype, strides as k_new's in spec_verify_kv_append
+ * num_queries    [B] int32, 0..N (draft_len + 1, or tree_size); NULL: N
+ * tree_parents   [B, N] int32 as in spec_verify_tree_greedy (-1 at the root, parents before children),
+ *                or NULL for a chain
+ * scale          > 0 and finite
+ * out            [B, N, Hq, D] of the cache's dtype, contiguous; 0 for i >= m_b
+ * out_lse        [B, N, Hq] fp32, contiguous; 0 for i >= m_b. May be NULL.
+ * workspace      device scratch of spec_verify_paged_attention_workspace_size(...) bytes, 256-byte
+ *                aligned. Its first SV_ATTEND_COUNTER_BYTES must be zero before its first use, and
+ *                every call leaves them zero; one workspace serves one call at a time, of any sizes.
+ * A row in error gets NaN in all its outputs (a bad page or tree: in those of its m_b tokens).
+ * The softmax and the sums run in fp32; the probabilities are rounded to the cache's dtype for the
+ * product with the values. 1 <= N <= SV_MAX_GAMMA + 1, Hq <= 1024. */
+#define SV_ATTEND_COUNTER_BYTES 4096
+size_t spec_verify_paged_attention_workspace_size(int32_t N, int32_t Hq,
+                                                  const sv_paged_cache* cache);
+int spec_verify_paged_attention(const void* q, int64_t q_row_stride, int64_t q_token_stride,
+                                const sv_paged_cache* cache, const int32_t* prefix_len,
+                                const int32_t* num_queries, const int32_t* tree_parents, float scale,
+                                void* out, float* out_lse, int32_t B, int32_t N, int32_t Hq,
+                                void* workspace, size_t workspace_bytes, void* cuda_stream);
+
+/* Adds to the cache's weights what the kept tokens of a round gave to each entry: for every entry j and
+ * key head of row b, weight_j += sum over the kept tokens d < num_kept[b] with n_b + d >= j and over the
+ * query heads of that key head of exp(scale * q . k_j - lse), where q and lse are those of token d, or
+ * of token path[b, d] when a path is given (a tree's kept path, appended again as a chain).
+ *
+ * q, lse         as in spec_verify_paged_attention (lse: its out_lse)
+ * prefix_len     [B] int32, n_b: the entries before the round
+ * num_kept       [B] int32, 0..N (out_num_emitted, or out_path_len); NULL: N. -1 adds nothing.
+ * path           [B, N] int32 or NULL.
+ * A row whose length or count is out of range, or with a path entry outside [0, N), adds nothing;
+ * entries on a page number out of range are passed over. Weights of entries that rows share take every
+ * row's part, in any order (the only case in which two equal calls may round differently). One launch.
+ * cache->weight is required. */
+int spec_verify_kv_weights(const void* q, int64_t q_row_stride, int64_t q_token_stride,
+                           const float* lse, const sv_paged_cache* cache, const int32_t* prefix_len,
+                           const int32_t* num_kept, const int32_t* path, float scale, int32_t B,
+                           int32_t N, int32_t Hq, void* cuda_stream);
+
+/* Evicts entries by their attention weight: a row with length[b] > budget keeps its last `recent`
+ * entries and, per key head on its own, of the others the budget - recent with the largest weight (of
+ * equal weights the entry that comes first; NaN counts as the largest). The kept entries move up to
+ * 0..budget - 1 in their order, keys, values and weights; slots from budget on are left as they were.
+ * A row with length[b] <= budget is left alone.
+ *
+ * length         [B] int32, entries per row
+ * out_len        [B] int32: min(length, budget); -1 for a row in error, which is left alone. Not the
+ *                same array as length (SV_ERR_OVERLAP).
+ * budget >= 1, 0 <= recent <= budget (else SV_ERR_BAD_SHAPE). cache->weight is required. One launch. */
+int spec_verify_kv_evict(const sv_paged_cache* cache, const int32_t* length, int32_t budget,
+                         int32_t recent, int32_t* out_len, int32_t B, void* cuda_stream);
 
 /* spec_verify_ex for callers that cannot allocate device memory. The pages have no counterpart:
  * this is a deployment convenience, not part of the method.

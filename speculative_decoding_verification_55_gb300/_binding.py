@@ -14,19 +14,23 @@ from .build import LIB_PATH
 SV_OK = 0
 SV_DTYPE_F32 = 0
 SV_DTYPE_BF16 = 1
+SV_DTYPE_F16 = 2
 SV_MAX_GAMMA = 64
 
 STATUS_NAMES = {
     0: "SV_OK", 1: "SV_ERR_NULL_POINTER", 2: "SV_ERR_BAD_SHAPE", 3: "SV_ERR_BAD_DTYPE",
     4: "SV_ERR_WORKSPACE_TOO_SMALL", 5: "SV_ERR_MISALIGNED", 6: "SV_ERR_CUDA",
     7: "SV_ERR_UNSUPPORTED_DEVICE", 8: "SV_ERR_SCRATCH_TOO_SMALL",
+    9: "SV_ERR_OVERLAP",
 }
 SV_ERR_SCRATCH_TOO_SMALL = 8
 SV_NOALLOC_SCRATCH_BYTES = 1 << 20
 
 EXPORTED = ("spec_verify", "spec_verify_ex", "spec_verify_noalloc", "spec_verify_onehot",
             "spec_verify_filtered", "spec_verify_filter_thresholds", "spec_verify_tree_greedy",
-            "spec_verify_kv_rollback",
+            "spec_verify_kv_rollback", "spec_verify_kv_append", "spec_verify_paged_attention",
+            "spec_verify_paged_attention_workspace_size", "spec_verify_kv_weights",
+            "spec_verify_kv_evict",
             "spec_verify_workspace_size", "spec_verify_filtered_workspace_size",
             "spec_verify_workspace_status", "spec_verify_status_string",
             "spec_verify_version")
@@ -92,6 +96,19 @@ def lib() -> ctypes.CDLL:
                                              vp, ctypes.c_size_t, vp, ctypes.c_size_t,
                                              ctypes.POINTER(ctypes.c_size_t), vp]
             L.spec_verify_staged.restype = ctypes.c_int
+            i64, sz = ctypes.c_int64, ctypes.c_size_t
+            L.spec_verify_kv_append.argtypes = [vp, vp, i64, i64, vp, i32p, i32p, i32p, i32p, i32, i32, vp]
+            L.spec_verify_kv_append.restype = ctypes.c_int
+            L.spec_verify_paged_attention.argtypes = [vp, i64, i64, vp, i32p, i32p, i32p, ctypes.c_float,
+                                                      vp, f32p, i32, i32, i32, vp, sz, vp]
+            L.spec_verify_paged_attention.restype = ctypes.c_int
+            L.spec_verify_paged_attention_workspace_size.argtypes = [i32, i32, vp]
+            L.spec_verify_paged_attention_workspace_size.restype = sz
+            L.spec_verify_kv_weights.argtypes = [vp, i64, i64, f32p, vp, i32p, i32p, i32p, ctypes.c_float,
+                                                 i32, i32, i32, vp]
+            L.spec_verify_kv_weights.restype = ctypes.c_int
+            L.spec_verify_kv_evict.argtypes = [vp, i32p, i32, i32, i32p, i32, vp]
+            L.spec_verify_kv_evict.restype = ctypes.c_int
             _lib = L
     return _lib
 

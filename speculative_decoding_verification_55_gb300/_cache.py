@@ -1,0 +1,219 @@
+"""ctypes binding of the paged-cache calls of include/spec_verify.h under the same names.
+
+Argument marshalling only, as in _binding: torch tensors supply device memory and the stream.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+
+from ._binding import (SV_DTYPE_BF16, SV_DTYPE_F16, SV_OK, SpecVerifyError, _on, _ptr,
+                       _stream_handle, lib)
+
+SV_ATTEND_COUNTER_BYTES = 4096
+
+
+class _CacheStruct(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p),
+                ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("slot_stride", ctypes.c_int64),
+                ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class PagedCache:
+    """A batch's paged key-value cache (sv_paged_cache): k and v [num_pages, heads, page_size, D] in
+    bfloat16 or float16 with D contiguous and any order of the other dimensions in memory (pass
+    ``x.transpose(1, 2)`` for pages of [page_size, heads, D]), page_table [B, max_pages] int32 and,
+    for the calls on attention weights, weight [num_pages, heads, page_size] float32. Holds the
+    tensors; their contents may change between calls."""
+
+    def __init__(self, k, v, page_table, weight=None):
+        import torch
+        if k.dim() != 4 or k.shape != v.shape:
+            raise ValueError(f"k and v must be [num_pages, heads, page_size, D] of one shape, got "
+                             f"{tuple(k.shape)} and {tuple(v.shape)}")
+        if k.dtype not in (torch.bfloat16, torch.float16) or v.dtype != k.dtype:
+            raise TypeError(f"k and v must both be bfloat16 or float16, got {k.dtype} and {v.dtype}")
+        P, H, S, D = k.shape
+        if page_table.dim() != 2 or page_table.dtype != torch.int32 or not page_table.is_contiguous():
+            raise ValueError("page_table must be a contiguous [B, max_pages] int32 tensor")
+        if weight is not None and (tuple(weight.shape) != (P, H, S) or weight.dtype != torch.float32
+                                   or not weight.is_contiguous()):
+            raise ValueError(f"weight must be a contiguous {(P, H, S)} float32 tensor")
+        for name, t in (("v", v), ("page_table", page_table), ("weight", weight)):
+            if t is not None and t.device != k.device:
+                raise ValueError(f"{name} must be on {k.device}, got {t.device}")
+        # The stride of a dimension of one element says nothing.
+        steps = [[st if n > 1 else D for n, st in zip(t.shape[:3], t.stride()[:3])] for t in (k, v)]
+        if D > 1 and (k.stride(3) != 1 or v.stride(3) != 1):
+            raise ValueError("the D elements of an entry must be contiguous")
+        if steps[0] != steps[1]:
+            raise ValueError(f"k and v must have the same strides, got {k.stride()} and {v.stride()}")
+        self.k, self.v, self.page_table, self.weight = k, v, page_table, weight
+        self.B, self.heads, self.head_dim, self.dtype, self.device = page_table.shape[0], H, D, k.dtype, k.device
+        self.struct = _CacheStruct(
+            k.data_ptr(), v.data_ptr(), None if weight is None else weight.data_ptr(),
+            page_table.data_ptr(), steps[0][0], steps[0][1], steps[0][2], P, S, page_table.shape[1],
+            H, D, SV_DTYPE_BF16 if k.dtype == torch.bfloat16 else SV_DTYPE_F16)
+        self.ref = ctypes.addressof(self.struct)
+
+
+def _tokens(x, name, cache, B=None, N=None):
+    """Checks a round's [B, N, heads, D] tensor; returns its strides over rows and tokens."""
+    if x.dim() != 4 or x.shape[0] != cache.B or x.shape[3] != cache.head_dim \
+            or (N is not None and x.shape[1] != N):
+        raise ValueError(f"{name} must be [{cache.B}, {'N' if N is None else N}, heads, "
+                         f"{cache.head_dim}], got {tuple(x.shape)}")
+    if x.dtype != cache.dtype:
+        raise TypeError(f"{name} must be {cache.dtype}, got {x.dtype}")
+    if x.device != cache.device:
+        raise ValueError(f"{name} must be on {cache.device}, got {x.device}")
+    s = x.stride()
+    heads, D = x.shape[2], x.shape[3]
+    if s[3] != 1 or (heads > 1 and s[2] != D):
+        raise ValueError(f"the heads of a token of {name} must be contiguous")
+    return (s[0] if x.shape[0] > 1 else heads * D * x.shape[1]), (s[1] if x.shape[1] > 1 else heads * D)
+
+
+def _ints(t, name, shape, device):
+    if t is None:
+        return None
+    import torch
+    if t.dtype != torch.int32:
+        raise TypeError(f"{name} must be torch.int32, got {t.dtype}")
+    if tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with shape {shape}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    return t.data_ptr()
+
+
+def _floats(t, name, shape, device):
+    import torch
+    if t is None:
+        return None
+    if t.dtype != torch.float32:
+        raise TypeError(f"{name} must be torch.float32, got {t.dtype}")
+    if tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with shape {shape}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    return t.data_ptr()
+
+
+def spec_verify_paged_attention_workspace_size(N: int, Hq: int, cache: PagedCache) -> int:
+    return int(lib().spec_verify_paged_attention_workspace_size(N, Hq, cache.ref))
+
+
+def spec_verify_kv_append(k_new, v_new, cache, prefix_len, num_new=None, path=None, out_len=None,
+                          stream=None) -> None:
+    """Calls the C ABI spec_verify_kv_append on torch tensors: token d (or path[:, d]) of k_new and
+    v_new [B, N, heads, D] becomes entry prefix_len + d. Raises SpecVerifyError on a nonzero status."""
+    dev, B, N = cache.device, cache.B, k_new.shape[1]
+    strides = _tokens(k_new, "k_new", cache)
+    if _tokens(v_new, "v_new", cache, N=N) != strides or k_new.shape[2] != cache.heads \
+            or v_new.shape[2] != cache.heads:
+        raise ValueError(f"k_new and v_new must have {cache.heads} heads and the same strides")
+    args = (_ints(prefix_len, "prefix_len", (B,), dev), _ints(num_new, "num_new", (B,), dev),
+            _ints(path, "path", (B, N), dev), _ints(out_len, "out_len", (B,), dev))
+    with _on(dev):
+        st = lib().spec_verify_kv_append(k_new.data_ptr(), v_new.data_ptr(), *strides, cache.ref, *args,
+                                         B, N, _stream_handle(stream, dev))
+    if st != SV_OK:
+        raise SpecVerifyError(st, "spec_verify_kv_append")
+
+
+def spec_verify_paged_attention(q, cache, prefix_len, num_queries, tree_parents, out, out_lse,
+                                workspace, scale=None, stream=None) -> None:
+    """Calls the C ABI spec_verify_paged_attention on torch tensors: q [B, N, Hq, D] (heads of a token
+    together), scale 1 / sqrt(D) unless given. Raises SpecVerifyError on a nonzero status."""
+    dev, B = cache.device, cache.B
+    strides = _tokens(q, "q", cache)
+    N, Hq = q.shape[1], q.shape[2]
+    if out.dtype != cache.dtype or tuple(out.shape) != (B, N, Hq, cache.head_dim) \
+            or not out.is_contiguous() or out.device != dev:
+        raise ValueError(f"out must be a contiguous {(B, N, Hq, cache.head_dim)} {cache.dtype} tensor "
+                         f"on {dev}")
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {dev}")
+    if scale is None:
+        scale = 1.0 / math.sqrt(cache.head_dim)
+    args = (_ints(prefix_len, "prefix_len", (B,), dev), _ints(num_queries, "num_queries", (B,), dev),
+            _ints(tree_parents, "tree_parents", (B, N), dev))
+    with _on(dev):
+        st = lib().spec_verify_paged_attention(
+            q.data_ptr(), *strides, cache.ref, *args, scale, out.data_ptr(),
+            _floats(out_lse, "out_lse", (B, N, Hq), dev), B, N, Hq, workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), _stream_handle(stream, dev))
+    if st != SV_OK:
+        raise SpecVerifyError(st, "spec_verify_paged_attention")
+
+
+def spec_verify_kv_weights(q, lse, cache, prefix_len, num_kept=None, path=None, scale=None,
+                           stream=None) -> None:
+    """Calls the C ABI spec_verify_kv_weights on torch tensors: cache.weight gains what the kept tokens
+    of q [B, N, Hq, D] gave to each entry (lse: spec_verify_paged_attention's out_lse). Raises
+    SpecVerifyError on a nonzero status."""
+    dev, B = cache.device, cache.B
+    strides = _tokens(q, "q", cache)
+    N, Hq = q.shape[1], q.shape[2]
+    if scale is None:
+        scale = 1.0 / math.sqrt(cache.head_dim)
+    args = (_ints(prefix_len, "prefix_len", (B,), dev), _ints(num_kept, "num_kept", (B,), dev),
+            _ints(path, "path", (B, N), dev))
+    with _on(dev):
+        st = lib().spec_verify_kv_weights(q.data_ptr(), *strides, _floats(lse, "lse", (B, N, Hq), dev),
+                                          cache.ref, *args, scale, B, N, Hq, _stream_handle(stream, dev))
+    if st != SV_OK:
+        raise SpecVerifyError(st, "spec_verify_kv_weights")
+
+
+def spec_verify_kv_evict(cache, length, budget, recent, out_len, stream=None) -> None:
+    """Calls the C ABI spec_verify_kv_evict on torch tensors: rows with more than budget entries keep
+    the last ``recent`` and, per head, the others of the largest cache.weight. Raises SpecVerifyError on
+    a nonzero status."""
+    dev, B = cache.device, cache.B
+    with _on(dev):
+        st = lib().spec_verify_kv_evict(cache.ref, _ints(length, "length", (B,), dev), budget, recent,
+                                        _ints(out_len, "out_len", (B,), dev), B,
+                                        _stream_handle(stream, dev))
+    if st != SV_OK:
+        raise SpecVerifyError(st, "spec_verify_kv_evict")
+
+
+_attend_ws = {}
+
+
+def _attend_workspace(N, Hq, cache, stream):
+    """A workspace with zeroed counters, cached per (device, stream) and grown on demand. A call that
+    is being captured gets one of its own, zeroed by the graph: replays of two graphs may overlap."""
+    import torch
+    need = spec_verify_paged_attention_workspace_size(N, Hq, cache)
+    if torch.cuda.is_current_stream_capturing():
+        ws = torch.empty(max(need, SV_ATTEND_COUNTER_BYTES), dtype=torch.uint8, device=cache.device)
+        ws[:SV_ATTEND_COUNTER_BYTES].zero_()
+        return ws
+    key = (cache.device, _stream_handle(stream, cache.device))
+    ws = _attend_ws.get(key)
+    if ws is None or ws.numel() < need:
+        ws = torch.zeros(max(need, SV_ATTEND_COUNTER_BYTES), dtype=torch.uint8, device=cache.device)
+        _attend_ws[key] = ws
+    return ws
+
+
+def attend(q, cache, prefix_len, num_queries=None, tree_parents=None, scale=None, stream=None):
+    """Allocates the outputs, runs spec_verify_paged_attention and returns (out [B, N, Hq, D],
+    lse [B, N, Hq])."""
+    import torch
+    if stream is not None:
+        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), cache.device)
+        with torch.cuda.stream(s):
+            return attend(q, cache, prefix_len, num_queries, tree_parents, scale)
+    out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+    ws = _attend_workspace(q.shape[1], q.shape[2], cache, None)
+    spec_verify_paged_attention(q, cache, prefix_len, num_queries, tree_parents, out, lse, ws, scale)
+    return out, lse

@@ -179,8 +179,8 @@ const char* spec_verify_status_string(int status) {
   switch (status) {
     case SV_OK: return "SV_OK: success";
     case SV_ERR_NULL_POINTER: return "SV_ERR_NULL_POINTER: a required pointer is NULL";
-    case SV_ERR_BAD_SHAPE: return "SV_ERR_BAD_SHAPE: B, gamma_max or V out of range";
-    case SV_ERR_BAD_DTYPE: return "SV_ERR_BAD_DTYPE: dtype is not SV_DTYPE_F32 or SV_DTYPE_BF16";
+    case SV_ERR_BAD_SHAPE: return "SV_ERR_BAD_SHAPE: a size is out of range";
+    case SV_ERR_BAD_DTYPE: return "SV_ERR_BAD_DTYPE: dtype is none of the types this call takes";
     case SV_ERR_WORKSPACE_TOO_SMALL: return "SV_ERR_WORKSPACE_TOO_SMALL: workspace missing or too small";
     case SV_ERR_MISALIGNED: return "SV_ERR_MISALIGNED: a pointer is not aligned to its element type";
     case SV_ERR_CUDA: return "SV_ERR_CUDA: a CUDA runtime call failed";
@@ -188,6 +188,7 @@ const char* spec_verify_status_string(int status) {
     case SV_ERR_SCRATCH_TOO_SMALL:
       return "SV_ERR_SCRATCH_TOO_SMALL: the sizes need more than the library's static scratch "
              "(SV_NOALLOC_SCRATCH_BYTES)";
+    case SV_ERR_OVERLAP: return "SV_ERR_OVERLAP: an output array is also an input";
     default: return "unknown sv_status";
   }
 }
@@ -301,6 +302,8 @@ int verify_impl(const void* target_logits, const void* draft_logits, const int32
 }  // namespace
 
 namespace sv {
+
+int current_device_status(int* dev) { return check_device(dev); }
 
 int verify_args_status(const void* target_logits, const void* draft_logits,
                        const int32_t* draft_tokens, const int32_t* draft_len,

@@ -1,0 +1,113 @@
+// What the kernels of the paged cache share: the cache as the device sees it, its entries' places,
+// the two storage types, and the checks that every entry point makes on the host.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/spec_verify.h"
+
+namespace sv {
+
+// Entries a row of the cache may hold: the eviction keeps one bit and one count per 32 of them in
+// shared memory.
+constexpr int kMaxEntries = 1 << 20;
+
+struct Cache {
+  char* k;
+  char* v;
+  float* weight;              // [num_pages, heads, page_size] or null
+  const int32_t* table;       // [B, max_pages]
+  long long page_stride, head_stride, slot_stride;   // bytes
+  int num_pages, page_size, page_log2, max_pages, heads, head_dim;
+};
+
+__device__ __forceinline__ int cache_page(const Cache& C, int b, int j) {
+  return __ldg(C.table + static_cast<size_t>(b) * C.max_pages + (j >> C.page_log2));
+}
+__device__ __forceinline__ bool page_ok(const Cache& C, int page) {
+  return static_cast<unsigned>(page) < static_cast<unsigned>(C.num_pages);
+}
+// Byte offset of an entry's D elements in k or v.
+__device__ __forceinline__ long long entry_offset(const Cache& C, int page, int h, int j) {
+  return page * C.page_stride + h * C.head_stride + (j & (C.page_size - 1)) * C.slot_stride;
+}
+__device__ __forceinline__ size_t weight_index(const Cache& C, int page, int h, int j) {
+  return (static_cast<size_t>(page) * C.heads + h) * C.page_size + (j & (C.page_size - 1));
+}
+
+// A row's entries before the round and its tokens; false when they are out of range. num: null means
+// N; -1 (a row error of the verification) counts as no token where none_ok.
+__device__ __forceinline__ bool round_lengths(const Cache& C, const int32_t* prefix,
+                                              const int32_t* num, int b, int N, bool none_ok, int* n,
+                                              int* m) {
+  *n = __ldg(prefix + b);
+  *m = num ? __ldg(num + b) : N;
+  if (none_ok && *m == -1) *m = 0;
+  if (*m < 0 || *m > N || *n < 0) return false;
+  return static_cast<long long>(*n) + *m <= static_cast<long long>(C.max_pages) * C.page_size;
+}
+
+inline bool misaligned(const void* p, uintptr_t a) {
+  return p && (reinterpret_cast<uintptr_t>(p) % a) != 0;
+}
+
+// The checks of a cache argument; fills the device form. need_weight: the call reads or writes weights.
+inline int check_cache(const sv_paged_cache* c, int32_t B, bool need_weight, Cache* out) {
+  if (!c || !c->k || !c->v || !c->page_table || (need_weight && !c->weight))
+    return SV_ERR_NULL_POINTER;
+  if (c->dtype != SV_DTYPE_BF16 && c->dtype != SV_DTYPE_F16) return SV_ERR_BAD_DTYPE;
+  if (B < 1 || B > (1 << 20) || c->heads < 1 || c->heads > 1024 || c->num_pages < 1 ||
+      c->max_pages < 1)
+    return SV_ERR_BAD_SHAPE;
+  if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return SV_ERR_BAD_SHAPE;
+  int lg = 4;
+  while (lg < 8 && (1 << lg) != c->page_size) ++lg;
+  if ((1 << lg) != c->page_size) return SV_ERR_BAD_SHAPE;
+  if (static_cast<long long>(c->max_pages) * c->page_size > kMaxEntries) return SV_ERR_BAD_SHAPE;
+  if (c->slot_stride < c->head_dim || (c->heads > 1 && c->head_stride < c->head_dim) ||
+      (c->num_pages > 1 && c->page_stride < c->head_dim))
+    return SV_ERR_BAD_SHAPE;
+  const int64_t most = static_cast<int64_t>(1) << 38;      // a tensor map's strides stay below 2^40
+  if (c->page_stride >= most || c->head_stride >= most || c->slot_stride >= most)
+    return SV_ERR_BAD_SHAPE;
+  if (misaligned(c->k, 16) || misaligned(c->v, 16) || misaligned(c->weight, 16) ||
+      misaligned(c->page_table, 4) || c->page_stride % 8 != 0 || c->head_stride % 8 != 0 ||
+      c->slot_stride % 8 != 0)
+    return SV_ERR_MISALIGNED;
+  out->k = static_cast<char*>(c->k);
+  out->v = static_cast<char*>(c->v);
+  out->weight = c->weight;
+  out->table = c->page_table;
+  out->page_stride = c->page_stride * 2;
+  out->head_stride = c->head_stride * 2;
+  out->slot_stride = c->slot_stride * 2;
+  out->num_pages = c->num_pages;
+  out->page_size = c->page_size;
+  out->page_log2 = lg;
+  out->max_pages = c->max_pages;
+  out->heads = c->heads;
+  out->head_dim = c->head_dim;
+  return SV_OK;
+}
+
+// The checks of a round's [B, N, heads, D] input x (its strides in elements, its heads together).
+inline int check_tokens(const void* x, int64_t row_stride, int64_t token_stride, int32_t B, int32_t N,
+                        int32_t heads, int32_t D) {
+  if (N < 1 || N > SV_MAX_GAMMA + 1 || heads < 1 || heads > 1024) return SV_ERR_BAD_SHAPE;
+  const int64_t most = static_cast<int64_t>(1) << 38;
+  if (row_stride < 0 || token_stride < 0 || row_stride >= most || token_stride >= most)
+    return SV_ERR_BAD_SHAPE;
+  if ((N > 1 && token_stride < static_cast<int64_t>(heads) * D) || (B > 1 && row_stride < heads * D))
+    return SV_ERR_BAD_SHAPE;
+  if (misaligned(x, 16) || row_stride % 8 != 0 || token_stride % 8 != 0) return SV_ERR_MISALIGNED;
+  return SV_OK;
+}
+
+// SV_OK when the current device is compute capability 10.3 (sv_api.cu).
+int current_device_status(int* dev);
+
+}  // namespace sv

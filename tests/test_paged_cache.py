@@ -1,0 +1,683 @@
+"""The paged cache of a round: oracle pins and refusals on the CPU, GPU parity of the append, the
+attention, the attention weights and the eviction against the fp64 oracle.
+
+Tolerances. A probability is rounded to the cache's type once (half a step, e = finfo.eps / 2) and the
+output once, so |out - exact| <= e (sum p|v| + |out|) plus fp32 arithmetic. A score is a sum of D
+products in fp32, off by at most (D + 2) 2^-24 sum |q k| scale, then an exponential of relative error
+2^-22 and, for lse, a logarithm of as much.
+"""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+
+from oracle import paged_cache_oracle as oracle
+
+torch = pytest.importorskip("torch")
+TYPES = {"bf16": torch.bfloat16, "f16": torch.float16}
+
+
+# ------------------------------------------------------------------------------------------------
+# Oracle pins (CPU)
+# ------------------------------------------------------------------------------------------------
+
+def small(rng, B=2, N=4, H=2, G=2, D=8, S=4, n=(5, 0), pages=9):
+    """A batch in NumPy: q, k, v, table, prefix (every row has room for N more entries)."""
+    q = rng.standard_normal((B, N, H * G, D))
+    k, v = rng.standard_normal((2, pages, H, S, D))
+    table = rng.permutation(pages)[:B * (pages // B)].reshape(B, -1).astype(np.int32)
+    return q, k, v, table, np.array(n, np.int32)
+
+
+def test_oracle_attention_pins():
+    rng = np.random.default_rng(1)
+    q, k, v, table, n = small(rng)
+    num = np.array([4, 4])
+    out, lse, _ = oracle.attention(q, k, v, table, n, num, None, 0.3)
+    # A row's first token on an empty cache attends itself alone: its own value, its own score.
+    page, slot = oracle.place(table, 1, 0, 4)
+    assert np.allclose(out[1, 0, 3], v[page, 1, slot])
+    assert np.isclose(lse[1, 0, 3], 0.3 * q[1, 0, 3] @ k[page, 1, slot])
+    # Equal keys give the mean of the values.
+    same, _, _ = oracle.attention(q, np.ones_like(k), v, table, n, num, None, 0.3)
+    assert np.allclose(same[0, 2, 0], oracle.entries(v, table, 0, 8)[0].mean(0))
+    # A chain is the tree whose parents are the tokens before.
+    chain = np.array([[-1, 0, 1, 2]] * 2)
+    again, _, _ = oracle.attention(q, k, v, table, n, num, chain, 0.3)
+    assert np.allclose(again, out)
+    # In a star every leaf attends the root and itself.
+    star = np.array([[-1, 0, 0, 0]] * 2)
+    assert oracle.attended(5, 4, 3, star[0]) == [0, 1, 2, 3, 4, 5, 8]
+
+
+def test_oracle_weight_pins():
+    """The softmax probabilities of a token sum to 1: the added weight is tokens times heads."""
+    rng = np.random.default_rng(2)
+    q, k, v, table, n = small(rng)
+    num = np.array([3, 2])
+    _, lse, _ = oracle.attention(q, k, v, table, n, np.array([4, 4]), None, 0.3)
+    w = oracle.weights(q, lse, k, np.zeros(k.shape[:3]), table, n, num, None, 0.3)
+    assert np.isclose(w.sum(), (3 + 2) * 4)
+    # Kept path [0, 2] of a star, appended again as a chain, is what token 2 saw in the tree.
+    star, path = np.array([[-1, 0, 0, 0]] * 2), np.array([[0, 2, -1, -1]] * 2)
+    _, lse, _ = oracle.attention(q, k, v, table, n, np.array([4, 4]), star, 0.3)
+    kn = np.stack([oracle.entries(k, table, b, n[b] + 4)[:, n[b]:].swapaxes(0, 1) for b in range(2)])
+    k2, _, _, _ = oracle.append(k, v, None, kn, kn, table, n, np.array([2, 2]), path)
+    w = oracle.weights(q, lse, k2, np.zeros(k.shape[:3]), table, n, np.array([2, 2]), path, 0.3)
+    assert np.isclose(w.sum(), (2 + 2) * 4)
+
+
+def test_oracle_evict_by_hand():
+    w = np.array([3.0, 1.0, 2.0, 1.0, 2.0, 0.0, 9.0])
+    assert oracle.kept_entries(w, 4, 1) == [0, 2, 4, 6]
+    assert oracle.kept_entries(w, 5, 1) == [0, 1, 2, 4, 6]     # of the equal ones the first
+    assert oracle.kept_entries(w, 3, 3) == [4, 5, 6]
+    assert oracle.kept_entries(w, 1, 0) == [6]
+    assert oracle.kept_entries(np.array([1.0, np.nan, np.inf]), 2, 0) == [1, 2]
+    assert oracle.kept_entries(np.array([-0.0, 0.0, -1.0]), 1, 0) == [0]
+
+
+# ------------------------------------------------------------------------------------------------
+# Refusals (CPU: no call gets as far as the device)
+# ------------------------------------------------------------------------------------------------
+
+FAKE = 0x7f0000000000
+
+
+@pytest.fixture(scope="module")
+def L():
+    import speculative_decoding_verification_55_gb300 as m
+    m.build_library()
+    return m.lib()
+
+
+def cache_struct(**kw):
+    from speculative_decoding_verification_55_gb300._cache import _CacheStruct
+    a = dict(k=FAKE, v=FAKE + (1 << 20), weight=FAKE + (2 << 20), page_table=FAKE + (3 << 20),
+             page_stride=8 * 16 * 128, head_stride=16 * 128, slot_stride=128, num_pages=7,
+             page_size=16, max_pages=5, heads=8, head_dim=128, dtype=1)
+    a.update(kw)
+    return _CacheStruct(*(a[f[0]] for f in _CacheStruct._fields_))
+
+
+def calls(L, cache, **kw):
+    """Status of each of the four calls for this cache and these arguments, by name."""
+    a = dict(q=FAKE + (4 << 20), rs=9 * 32 * 128, ts=32 * 128, pre=FAKE + (5 << 20), num=None,
+             par=None, scale=0.1, out=FAKE + (6 << 20), lse=FAKE + (7 << 20), B=2, N=9, Hq=32,
+             ws=FAKE + (8 << 20), wsb=1 << 30, budget=8, recent=2, olen=FAKE + (9 << 20))
+    a.update(kw)
+    c = None if cache is None else ctypes.byref(cache)
+    return {
+        "attend": L.spec_verify_paged_attention(a["q"], a["rs"], a["ts"], c, a["pre"], a["num"],
+                                                a["par"], a["scale"], a["out"], a["lse"], a["B"],
+                                                a["N"], a["Hq"], a["ws"], a["wsb"], None),
+        "weigh": L.spec_verify_kv_weights(a["q"], a["rs"], a["ts"], a["lse"], c, a["pre"], a["num"],
+                                          a["par"], a["scale"], a["B"], a["N"], a["Hq"], None),
+        "append": L.spec_verify_kv_append(a["q"], a["q"], a["rs"], a["ts"], c, a["pre"], a["num"],
+                                          a["par"], a["olen"], a["B"], a["N"], None),
+        "evict": L.spec_verify_kv_evict(c, a["pre"], a["budget"], a["recent"], a["olen"], a["B"], None),
+    }
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(k=None), 1), (dict(v=None), 1), (dict(page_table=None), 1),
+    (dict(dtype=0), 3), (dict(dtype=7), 3),
+    (dict(head_dim=96), 2), (dict(head_dim=0), 2), (dict(page_size=8), 2), (dict(page_size=24), 2),
+    (dict(page_size=512), 2), (dict(num_pages=0), 2), (dict(max_pages=0), 2), (dict(heads=0), 2),
+    (dict(max_pages=(1 << 16) + 1), 2),               # more than 1048576 entries a row
+    (dict(slot_stride=64), 2), (dict(head_stride=8), 2), (dict(page_stride=-128), 2),
+    (dict(page_stride=1 << 40), 2),
+    (dict(slot_stride=132), 5), (dict(page_stride=8 * 16 * 128 + 4), 5), (dict(k=FAKE + 8), 5),
+    (dict(v=FAKE + 2), 5), (dict(page_table=FAKE + 2), 5), (dict(weight=FAKE + 4), 5),
+])
+def test_cache_refusals(L, change, status):
+    got = calls(L, cache_struct(**change))
+    assert set(got.values()) == {status}, got
+
+
+def test_argument_refusals(L):
+    c = cache_struct()
+    assert set(calls(L, None).values()) == {1}
+    assert set(calls(L, c, B=0).values()) == {2}
+    assert set(calls(L, c, pre=None).values()) == {1}
+    assert set(calls(L, c, pre=FAKE + 2).values()) == {5}
+    for n in (0, 66):
+        got = calls(L, c, N=n)
+        assert (got["attend"], got["weigh"], got["append"]) == (2, 2, 2)
+    for change, status in ((dict(q=None), 1), (dict(q=FAKE + 8), 5), (dict(ts=32 * 128 + 4), 5),
+                           (dict(rs=-8), 2), (dict(ts=8), 2), (dict(num=FAKE + 1), 5),
+                           (dict(par=FAKE + 2), 5)):
+        got = calls(L, c, **change)
+        assert (got["attend"], got["weigh"], got["append"]) == (status,) * 3, (change, got)
+    for change, status in ((dict(Hq=0), 2), (dict(Hq=30), 2), (dict(scale=0.0), 2),
+                           (dict(scale=-1.0), 2), (dict(scale=math.inf), 2), (dict(scale=math.nan), 2)):
+        got = calls(L, c, **change)
+        assert (got["attend"], got["weigh"]) == (status,) * 2, (change, got)
+    assert calls(L, c, out=None)["attend"] == 1
+    assert calls(L, c, out=FAKE + 8)["attend"] == 5
+    assert calls(L, c, lse=None)["weigh"] == 1
+    assert calls(L, c, lse=FAKE + 2)["weigh"] == 5
+    assert calls(L, c, ws=None)["attend"] == 4
+    assert calls(L, c, wsb=64)["attend"] == 4
+    assert calls(L, c, ws=FAKE + 128)["attend"] == 5
+    assert calls(L, c, budget=0)["evict"] == 2
+    assert calls(L, c, recent=-1)["evict"] == 2
+    assert calls(L, c, recent=9)["evict"] == 2
+    assert calls(L, c, olen=None)["evict"] == 1
+    assert calls(L, c, olen=FAKE + (5 << 20))["evict"] == 9      # SV_ERR_OVERLAP: the lengths
+    assert calls(L, c, olen=FAKE + (5 << 20))["append"] == 9
+    got = calls(L, cache_struct(weight=None))
+    assert got["weigh"] == 1 and got["evict"] == 1
+
+
+def test_workspace_size(L):
+    import speculative_decoding_verification_55_gb300 as sv
+    f = L.spec_verify_paged_attention_workspace_size
+    assert f(9, 32, ctypes.byref(cache_struct())) >= sv.SV_ATTEND_COUNTER_BYTES
+    assert f(0, 32, ctypes.byref(cache_struct())) == 0
+    assert f(9, 30, ctypes.byref(cache_struct())) == 0
+    assert f(9, 32, None) == 0
+
+
+def test_binding_refusals():
+    """The binding's own checks, on CPU tensors (no call is made)."""
+    import speculative_decoding_verification_55_gb300 as sv
+    k = torch.zeros((5, 2, 16, 64), dtype=torch.bfloat16)
+    t = torch.zeros((3, 2), dtype=torch.int32)
+    with pytest.raises(TypeError):
+        sv.PagedCache(k.float(), k.float(), t)
+    with pytest.raises(ValueError, match="shape"):
+        sv.PagedCache(k, k[:4], t)
+    with pytest.raises(ValueError, match="strides"):
+        sv.PagedCache(k, torch.zeros((5, 16, 2, 64), dtype=torch.bfloat16).transpose(1, 2), t)
+    with pytest.raises(ValueError, match="contiguous"):
+        sv.PagedCache(k.transpose(2, 3).contiguous().transpose(2, 3), k.transpose(2, 3).contiguous().transpose(2, 3), t)
+    with pytest.raises(ValueError, match="page_table"):
+        sv.PagedCache(k, k, t.long())
+    with pytest.raises(ValueError, match="weight"):
+        sv.PagedCache(k, k, t, torch.zeros((5, 16, 2)))
+    c = sv.PagedCache(k, k, t)
+    q = torch.zeros((3, 4, 8, 64), dtype=torch.bfloat16)
+    pre = torch.zeros(3, dtype=torch.int32)
+    with pytest.raises(ValueError, match="q must be"):
+        sv.spec_verify_kv_weights(q[:2], None, c, pre)
+    with pytest.raises(TypeError, match="q must be"):
+        sv.spec_verify_kv_weights(q.half(), None, c, pre)
+    with pytest.raises(ValueError, match="heads of a token"):
+        sv.spec_verify_kv_weights(q.transpose(1, 2).contiguous().transpose(1, 2), None, c, pre)
+    with pytest.raises(TypeError, match="prefix_len"):
+        sv.spec_verify_kv_weights(q, torch.zeros((3, 4, 8)), c, pre.long())
+    with pytest.raises(ValueError, match="heads"):
+        sv.spec_verify_kv_append(q, q, c, pre)
+    with pytest.raises(ValueError, match="out_len"):
+        sv.spec_verify_kv_evict(c, pre, 4, 1, torch.zeros(2, dtype=torch.int32))
+
+
+# ------------------------------------------------------------------------------------------------
+# GPU parity
+# ------------------------------------------------------------------------------------------------
+
+@pytest.fixture(scope="module")
+def sv():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import speculative_decoding_verification_55_gb300 as m
+    m.build_library()
+    return m
+
+
+class Batch:
+    """A batch on the GPU whose unused slots hold NaN: pages in a random order, q, k_new and v_new as
+    slices of one projection's output."""
+
+    def __init__(self, prefix, N, H, G, D, S, dtype="bf16", nhd=False, seed=0, extra=0, poison=True):
+        g = torch.Generator().manual_seed(seed)
+        self.t, self.S, self.N, self.D = TYPES[dtype], S, N, D
+        self.prefix = np.array(prefix, np.int32)
+        B = len(prefix)
+        used = [-(-(int(n) + N) // S) for n in prefix]
+        self.table = np.full((B, max(used) + extra), 1 << 30, np.int32)
+        ids = torch.randperm(sum(used) + 2, generator=g).numpy()
+        at = 0
+        for b, u in enumerate(used):
+            self.table[b, :u] = ids[at:at + u]
+            at += u
+        shape = (len(ids), H, S, D)
+        k, v = torch.randn(shape, generator=g).to(self.t), torch.randn(shape, generator=g).to(self.t)
+        if poison:
+            held = torch.zeros(shape[0], S, dtype=torch.bool)
+            for b, n in enumerate(prefix):
+                for j in range(int(n) + N):
+                    p, s = oracle.place(self.table, b, j, S)
+                    held[p, s] = True
+            k[~held[:, None].expand(-1, H, -1)] = math.nan
+            v[~held[:, None].expand(-1, H, -1)] = math.nan
+        put = (lambda x: x.transpose(1, 2).contiguous().cuda().transpose(1, 2)) if nhd else (lambda x: x.cuda())
+        self.k, self.v = put(k), put(v)
+        self.weight = torch.rand(shape[:3], generator=g).cuda()
+        qkv = torch.randn((B, N, H * G + 2 * H, D), generator=g)
+        qkv[:, :, :H * G] *= 2
+        qkv = qkv.to(self.t).cuda()
+        self.q, self.k_new, self.v_new = qkv[:, :, :H * G], qkv[:, :, H * G:H * G + H], qkv[:, :, H * G + H:]
+        self.scale = 1 / math.sqrt(D)
+
+    def cache(self, sv, weight=True):
+        return sv.PagedCache(self.k, self.v, dev(self.table), self.weight if weight else None)
+
+
+def dev(a):
+    return None if a is None else torch.as_tensor(np.ascontiguousarray(a, np.int32)).cuda()
+
+
+def host(x):
+    return x.detach().double().cpu().numpy()
+
+
+def random_tree(rng, B, N):
+    return np.array([[-1] + [int(rng.integers(max(0, i - 5), i)) for i in range(1, N)] for _ in range(B)], np.int32)
+
+
+def score_error(batch):
+    """Bound on |score - exact| for normal inputs: (D + 2) 2^-24 times the largest sum |q k| scale."""
+    D = batch.D
+    q, k = host(batch.q).reshape(-1, D), np.nan_to_num(host(batch.k)).reshape(-1, D)
+    most = batch.scale * np.sqrt((q ** 2).sum(1).max() * (k ** 2).sum(1).max())
+    return (D + 2) * 2.0 ** -24 * most
+
+
+def check_attention(batch, out, lse, prefix, num, parents, scale=None):
+    scale = batch.scale if scale is None else scale
+    want, wlse, mag = oracle.attention(host(batch.q), host(batch.k), host(batch.v), batch.table, prefix,
+                                       num, parents, scale)
+    out, lse = host(out), host(lse)
+    assert np.array_equal(np.isnan(out), np.isnan(want)) and np.array_equal(np.isnan(lse), np.isnan(wlse))
+    e, s = torch.finfo(batch.t).eps / 2, score_error(batch) * scale / batch.scale
+    # 2 s: the errors of the entry's own score and of the normaliser; 1e-6: exponentials and sums.
+    # A half's smallest step is 2^-24: a probability below it rounds by half of that.
+    tiny = 2.0 ** -25 if batch.t == torch.float16 else 0.0
+    tol = e * (mag + np.abs(want)) * (1 + e) + (2 * s + 1e-6) * mag + tiny * (prefix.max() + 65) * 6 + 1e-30
+    fine = ~np.isnan(want)
+    worst = (np.abs(out - want) / tol)[fine]
+    assert worst.size == 0 or worst.max() <= 1, worst.max()
+    fine = ~np.isnan(wlse)
+    assert (np.abs(lse - wlse)[fine] <= s + 1e-6 + 2.0 ** -22 * np.abs(wlse)[fine]).all()
+
+
+ATTEND = [
+    # prefix lengths, N, Hkv, group, D, page, dtype, nhd
+    ((0,), 1, 1, 1, 64, 16, "bf16", False),
+    ((0, 1, 15, 16, 17, 63, 64, 65), 1, 2, 4, 128, 16, "bf16", False),
+    ((127, 128, 129, 300, 1000), 1, 2, 8, 128, 32, "f16", True),
+    ((5, 0, 250, 511, 77), 9, 2, 4, 128, 16, "bf16", True),
+    ((5, 0, 250, 511, 77), 9, 2, 4, 128, 16, "f16", False),
+    ((33, 700), 5, 3, 7, 64, 64, "bf16", False),
+    ((1, 200, 90), 4, 1, 16, 256, 32, "bf16", True),
+    ((40, 257), 17, 2, 3, 256, 16, "f16", False),
+    ((3, 130, 400), 31, 1, 8, 128, 16, "bf16", False),
+    ((3, 530), 65, 2, 2, 64, 128, "bf16", True),
+    ((2, 130), 65, 1, 16, 128, 256, "f16", False),
+    ((2500,), 2, 1, 5, 128, 16, "bf16", False),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("prefix,N,H,G,D,S,dtype,nhd", ATTEND)
+def test_gpu_attention(sv, prefix, N, H, G, D, S, dtype, nhd):
+    rng = np.random.default_rng(N * 31 + D)
+    a = Batch(prefix, N, H, G, D, S, dtype, nhd, seed=N + D)
+    B = len(prefix)
+    num = rng.integers(0, N + 1, B).astype(np.int32)
+    num[-1] = N
+    c = a.cache(sv, weight=False)
+    out, lse = sv.attend(a.q, c, dev(a.prefix), dev(num))
+    check_attention(a, out, lse, a.prefix, num, None)
+    again, lse2 = sv.attend(a.q, c, dev(a.prefix), dev(num))
+    assert torch.equal(again, out) and torch.equal(lse2, lse)          # the same call, the same bits
+    tree = random_tree(rng, B, N)
+    out, lse = sv.attend(a.q, c, dev(a.prefix), None, dev(tree), scale=0.25)
+    check_attention(a, out, lse, a.prefix, np.full(B, N), tree, 0.25)
+
+
+@pytest.mark.gpu
+def test_gpu_attention_many_rows(sv):
+    """More rows than the GPU holds blocks, most of them short, some without tokens or entries."""
+    rng = np.random.default_rng(5)
+    prefix = rng.integers(0, 40, 700)
+    prefix[::50] = 300
+    a = Batch(prefix, 2, 1, 4, 64, 16, seed=9)
+    num = rng.integers(0, 3, 700).astype(np.int32)
+    out, lse = sv.attend(a.q, a.cache(sv), dev(a.prefix), dev(num))
+    check_attention(a, out, lse, a.prefix, num, None)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N,G", [(3, 2), (9, 8), (31, 8)])
+def test_gpu_unattended_values_have_no_part(sv, N, G):
+    """Infinities and NaN in the values and keys of tokens that a token does not attend."""
+    rng = np.random.default_rng(6)
+    a = Batch((70, 0, 64, 129), N, 2, G, 128, 16, seed=3)
+    tree = random_tree(rng, 4, N)
+    for b in range(4):
+        p, s = oracle.place(a.table, b, int(a.prefix[b]) + N - 1, 16)      # the last token: a leaf
+        a.v[p, :, s, 1::2] = math.inf
+        a.v[p, 0, s, 4] = math.nan
+        if b == 2:
+            a.k[p, :, s] = math.nan
+    num = np.full(4, N)
+    for parents in (None, tree):
+        out, lse = sv.attend(a.q, a.cache(sv), dev(a.prefix), None, dev(parents))
+        out, lse = host(out), host(lse)
+        assert np.isfinite(out[:, :N - 1]).all() and np.isfinite(lse[:, :N - 1]).all()
+        k, v = np.nan_to_num(host(a.k), posinf=0), np.nan_to_num(host(a.v), posinf=0)
+        want, _, mag = oracle.attention(host(a.q), k, v, a.table, a.prefix, num, parents, a.scale)
+        tol = 2.0 ** -8 * (mag + np.abs(want)) * 1.01 + 1e-4 * mag
+        assert (np.abs(out - want)[:, :N - 1] <= tol[:, :N - 1]).all()
+        assert np.isinf(out[[0, 1, 3], N - 1][:, :, 1::2]).all()           # its own infinity is its own
+        assert np.isnan(out[[0, 1, 3], N - 1, :G, 4]).all()
+        assert np.isnan(out[2, N - 1]).all() and np.isnan(lse[2, N - 1]).all()
+        assert np.isfinite(out[[0, 1, 3], N - 1][:, G:, 0::2]).all()
+
+
+@pytest.mark.gpu
+def test_gpu_attention_row_errors(sv):
+    a = Batch((40, 40, 40, 40, 40, 40), 3, 2, 4, 128, 16, seed=4)
+    prefix = a.prefix.copy()
+    num = np.array([3, 4, -1, 3, 2, 3], np.int32)
+    prefix[3] = a.table.shape[1] * 16 - 2                  # one more entry than the table holds
+    a.table[4, 1] = len(a.k)                               # a page past the end
+    a.table[5, 2] = -1
+    tree = np.array([[-1, 0, 1]] * 6, np.int32)
+    for parents in (None, tree):
+        out, lse = sv.attend(a.q, a.cache(sv), dev(prefix), dev(num), dev(parents))
+        check_attention(a, out, lse, prefix, num, parents)
+    for bad in ([0, 0, 1], [-1, 1, 1], [-1, 0, -1], [-1, 2, 0]):
+        tree[0] = bad
+        out, lse = sv.attend(a.q, a.cache(sv), dev(prefix), dev(num), dev(tree))
+        check_attention(a, out, lse, prefix, num, tree)
+
+
+@pytest.mark.gpu
+def test_gpu_attention_extreme_scores(sv):
+    """Scores of hundreds, and a key that outweighs all others by far: the running maximum holds."""
+    a = Batch((200, 64), 2, 1, 4, 128, 16, seed=8)
+    a.k *= 8
+    a.q *= 8
+    for b, j in ((0, 199), (1, 0)):
+        p, s = oracle.place(a.table, b, j, 16)
+        a.k[p, :, s] = a.q[b, 0, :1]
+    out, lse = sv.attend(a.q, a.cache(sv), dev(a.prefix))
+    check_attention(a, out, lse, a.prefix, np.array([2, 2]), None)
+
+
+@pytest.mark.gpu
+def test_gpu_far_pages(sv):
+    """Offsets past 32 bits: pages that lie over 2^32 bytes into the cache."""
+    S, H, D, P = 16, 8, 128, (1 << 17) + 9                  # 4.3 GB of keys, as much of values
+    a = Batch((50, 20), 3, H, 2, D, S, seed=2)
+    big = [torch.zeros((P, H, S, D), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    w = torch.zeros((P, H, S), device="cuda")
+    n = len(a.k)
+    for x, y in zip(big, (a.k, a.v)):
+        x[P - n:] = y
+    table = a.table.astype(np.int64) + P - n
+    c = sv.PagedCache(*big, dev(np.minimum(table, 1 << 30)), w)
+    out, lse = sv.attend(a.q, c, dev(a.prefix))
+    check_attention(a, out, lse, a.prefix, np.array([3, 3]), None)
+    sv.spec_verify_kv_weights(a.q, lse, c, dev(a.prefix))
+    want = oracle.weights(host(a.q), host(lse), np.nan_to_num(host(a.k)), np.zeros(a.weight.shape), a.table, a.prefix, [3, 3], None, a.scale)
+    assert np.allclose(host(w[P - n:]), want, rtol=1e-4, atol=1e-7) and float(w[:P - n].abs().sum()) == 0
+    olen = dev([0, 0])
+    sv.spec_verify_kv_append(a.k_new, a.v_new, c, dev(a.prefix), None, None, olen)
+    k, v, _, n_out = oracle.append(host(a.k), host(a.v), None, host(a.k_new), host(a.v_new), a.table, a.prefix, [3, 3], None)
+    assert np.array_equal(host(big[0][P - n:]), k, equal_nan=True)
+    assert np.array_equal(host(big[1][P - n:]), v, equal_nan=True)
+    w[P - n:] = a.weight
+    sv.spec_verify_kv_evict(c, dev([53, 23]), 22, 5, olen)
+    k, v, w2, n_out = oracle.evict(k, v, host(a.weight), a.table, [53, 23], 22, 5)
+    assert np.array_equal(host(big[0][P - n:]), k, equal_nan=True) and olen.tolist() == n_out.tolist()
+    assert np.array_equal(host(w[P - n:]), w2)
+
+
+# ------------------------------------------------------------------------------------------------
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("prefix,N,H,G,D,S,dtype,nhd", ATTEND)
+def test_gpu_weights(sv, prefix, N, H, G, D, S, dtype, nhd):
+    rng = np.random.default_rng(N * 17 + D)
+    a = Batch(prefix, N, H, G, D, S, dtype, nhd, seed=N + D)
+    B = len(prefix)
+    for path in (None, np.array([np.sort(rng.permutation(N)) for _ in range(B)], np.int32)):
+        num = rng.integers(-1, N + 1, B).astype(np.int32)
+        num[-1] = N
+        _, lse, _ = oracle.attention(host(a.q), host(a.k), host(a.v), a.table, a.prefix, np.full(B, N), None, a.scale)
+        lse = torch.as_tensor(lse, dtype=torch.float32).cuda()
+        before = a.weight.clone()
+        sv.spec_verify_kv_weights(a.q, lse, a.cache(sv), dev(a.prefix), dev(num), dev(path))
+        want = oracle.weights(host(a.q), host(lse), host(a.k), host(before), a.table, a.prefix, num, path, a.scale)
+        got, old = host(a.weight), host(before)
+        # Each term: its score's error, the exponential's 2^-22, the exponent's own rounding (values of
+        # some tens: 2^-24 of them, twice); the sum: N G terms in fp32.
+        rel = score_error(a) + 2.0 ** -22 + 2.0 ** -23 * (np.abs(host(lse)).max() + 40) + N * G * 2.0 ** -24
+        tol = rel * (want - old) + 2.0 ** -23 * want
+        assert (np.abs(got - want) <= tol).all(), (np.abs(got - want) / tol).max()
+
+
+@pytest.mark.gpu
+def test_gpu_weights_errors(sv):
+    a = Batch((40, 40, 40, 40), 3, 2, 4, 64, 16, seed=4)
+    prefix = np.array([-1, a.table.shape[1] * 16 - 1, 40, 40], np.int32)
+    path = np.array([[0, 1, 2], [0, 1, 2], [0, 3, 1], [0, 2, -1]], np.int32)
+    num = np.array([3, 3, 2, 2], np.int32)
+    a.table[3, 1] = -5                                      # passed over
+    lse = torch.full((4, 3, 8), 3.0, device="cuda")
+    before = host(a.weight)
+    sv.spec_verify_kv_weights(a.q, lse, a.cache(sv), dev(prefix), dev(num), dev(path))
+    want = oracle.weights(host(a.q), host(lse), host(a.k), before, a.table, prefix, num, path, a.scale)
+    assert np.allclose(host(a.weight), want, rtol=1e-5, atol=0)
+
+
+EVICT = [
+    # lengths, budget, recent, Hkv, D, page, dtype, nhd
+    ((40, 33, 32, 31, 0, 200), 32, 4, 2, 128, 16, "bf16", False),
+    ((500, 129, 1000), 128, 0, 3, 64, 32, "f16", True),
+    ((500, 129, 1000), 128, 128, 1, 256, 16, "bf16", False),
+    ((3000, 2049), 2048, 100, 2, 128, 16, "bf16", True),
+    ((2, 5), 1, 0, 8, 128, 256, "f16", False),
+    ((2, 5), 1, 1, 1, 64, 16, "bf16", False),
+    (tuple(range(60, 160)), 63, 7, 4, 128, 64, "bf16", False),
+]
+
+
+def check_evict(sv, a, lengths, budget, recent):
+    before = [host(x) for x in (a.k, a.v, a.weight)]
+    olen = torch.full((len(lengths),), 77, dtype=torch.int32, device="cuda")
+    sv.spec_verify_kv_evict(a.cache(sv), dev(lengths), budget, recent, olen)
+    *want, n = oracle.evict(*before, a.table, lengths, budget, recent)
+    assert olen.tolist() == n.tolist()
+    for x, w in zip((a.k, a.v, a.weight), want):
+        assert np.array_equal(host(x), w, equal_nan=True)      # behind the budget too: left as it was
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("weights", ["random", "equal", "few values", "special"])
+@pytest.mark.parametrize("lengths,budget,recent,H,D,S,dtype,nhd", EVICT)
+def test_gpu_evict(sv, lengths, budget, recent, H, D, S, dtype, nhd, weights):
+    a = Batch(lengths, 1, H, 1, D, S, dtype, nhd, seed=budget + recent, poison=False)
+    if weights == "equal":
+        a.weight.fill_(0.5)
+    elif weights == "few values":
+        a.weight.mul_(4).floor_()
+    elif weights == "special":
+        r = a.weight.clone()
+        a.weight[r < 0.2] = 0.0
+        a.weight[(r >= 0.2) & (r < 0.3)] = -0.0
+        a.weight[(r >= 0.3) & (r < 0.4)] = math.inf
+        a.weight[(r >= 0.4) & (r < 0.5)] = -1.0
+        a.weight[(r >= 0.5) & (r < 0.6)] = math.nan
+        a.weight[(r >= 0.6) & (r < 0.7)] = 1e-42
+    check_evict(sv, a, np.array(lengths), budget, recent)
+
+
+@pytest.mark.gpu
+def test_gpu_evict_row_errors(sv):
+    a = Batch((100, 100, 100, 100), 1, 2, 1, 64, 16, seed=1, poison=False)
+    a.table[1, 5] = len(a.k)
+    check_evict(sv, a, np.array([-3, 90, a.table.shape[1] * 16 + 1, 100]), 50, 10)
+
+
+@pytest.mark.gpu
+def test_gpu_evict_few_heads_over_many_blocks(sv):
+    """One row and head whose columns are split over a cluster, repeated: the same result each time."""
+    first = None
+    for _ in range(5):
+        a = Batch((9000,), 1, 1, 1, 128, 16, seed=12, poison=False)
+        a.weight.mul_(50).floor_()
+        olen = dev([0])
+        sv.spec_verify_kv_evict(a.cache(sv), dev([9000]), 4000, 33, olen)
+        got = [x.clone() for x in (a.k, a.v, a.weight)]
+        if first is None:
+            first = got
+            b = Batch((9000,), 1, 1, 1, 128, 16, seed=12, poison=False)
+            b.weight.mul_(50).floor_()
+            check_evict(sv, b, np.array([9000]), 4000, 33)
+        assert all(torch.equal(x, y) for x, y in zip(got, first))
+
+
+# ------------------------------------------------------------------------------------------------
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("prefix,N,H,G,D,S,dtype,nhd", ATTEND)
+def test_gpu_append(sv, prefix, N, H, G, D, S, dtype, nhd):
+    rng = np.random.default_rng(N + D)
+    B = len(prefix)
+    for path in (None, np.array([np.sort(rng.permutation(N)) for _ in range(B)], np.int32)):
+        a = Batch(prefix, N, H, G, D, S, dtype, nhd, seed=N + D)
+        num = rng.integers(-1, N + 1, B).astype(np.int32)
+        num[-1] = N
+        want = oracle.append(host(a.k), host(a.v), host(a.weight), host(a.k_new), host(a.v_new), a.table, a.prefix, num, path)
+        olen = torch.full((B,), 77, dtype=torch.int32, device="cuda")
+        sv.spec_verify_kv_append(a.k_new, a.v_new, a.cache(sv), dev(a.prefix), dev(num), dev(path), olen)
+        for x, w in zip((a.k, a.v, a.weight), want):
+            assert np.array_equal(host(x), w, equal_nan=True)
+        assert olen.tolist() == want[3].tolist()
+
+
+@pytest.mark.gpu
+def test_gpu_append_row_errors(sv):
+    a = Batch((40, 40, 40, 40, 40, 40), 3, 2, 4, 64, 16, seed=4, extra=2)
+    prefix = np.array([-1, 40, 40, a.table.shape[1] * 16 - 2, 40, 47], np.int32)
+    num = np.array([3, 4, -2, 3, 2, 2], np.int32)
+    path = np.array([[0, 1, 2]] * 4 + [[0, 3, 0], [1, 2, -1]], np.int32)
+    assert a.table[5, 3] == 1 << 30                        # entry 48 of the last row has no page
+    before = [host(x) for x in (a.k, a.v, a.weight)]
+    olen = torch.full((6,), 77, dtype=torch.int32, device="cuda")
+    sv.spec_verify_kv_append(a.k_new, a.v_new, a.cache(sv), dev(prefix), dev(num), dev(path), olen)
+    assert olen.tolist() == [-1] * 6
+    for x, w in zip((a.k, a.v, a.weight), before):
+        assert np.array_equal(host(x), w, equal_nan=True)
+
+
+# ------------------------------------------------------------------------------------------------
+# Together, captured, on another stream
+# ------------------------------------------------------------------------------------------------
+
+@pytest.mark.gpu
+def test_gpu_rounds_together(sv):
+    """Two rounds as they are used: append, attention, verification of drafts from its output, rollback,
+    weights of what was kept, eviction to a budget; then a tree round with its kept path."""
+    rng = np.random.default_rng(3)
+    N, H, G, D, S, V, B = 5, 2, 4, 64, 16, 512, 6
+    a = Batch((30, 0, 64, 100, 47, 90), N + 40, H, G, D, S, seed=5, poison=False)
+    W = torch.randn((H * G * D, V), device="cuda") / 8
+    a.weight.zero_()
+    c = a.cache(sv)
+    n = a.prefix.copy()
+    k, v, w = (host(x) for x in (a.k, a.v, a.weight))
+    for rnd in range(3):
+        tree = random_tree(rng, B, N) if rnd == 2 else None
+        new = torch.as_tensor(rng.standard_normal((B, N, (G + 2) * H, D)), dtype=torch.float32).to(a.t).cuda()
+        a.q, kn, vn = new[:, :, :H * G], new[:, :, H * G:H * G + H], new[:, :, H * G + H:]
+        olen = dev(np.zeros(B))
+        sv.spec_verify_kv_append(kn, vn, c, dev(n), None, None, olen)
+        k, v, w, on = oracle.append(k, v, w, host(kn), host(vn), a.table, n, [N] * B, None)
+        assert olen.tolist() == on.tolist()
+        out, lse = sv.attend(a.q, c, dev(n), None, dev(tree))
+        check_attention(a, out, lse, n, np.full(B, N), tree)
+        logits = (out.float().reshape(B, N, -1) @ W).contiguous()
+        path = None
+        if tree is None:
+            draft = torch.randn((B, N - 1, V), device="cuda")
+            tok, num, _ = sv.verify(logits, draft, draft.argmax(-1).to(torch.int32), None,
+                                    torch.full((B,), 0.5, device="cuda"), torch.rand((B, N + 1), device="cuda"))
+        else:
+            toks = torch.randint(0, V, (B, N), dtype=torch.int32, device="cuda")
+            for b in range(B):                          # one child of the root is the target's choice
+                toks[b, 1] = logits[b, 0].argmax()
+            path, num, _, _ = sv.verify_tree(logits, toks, dev(tree))
+            sv.spec_verify_kv_append(kn, vn, c, dev(n), num, path, olen)
+            k, v, w, on = oracle.append(k, v, w, host(kn), host(vn), a.table, n, num.tolist(), path.cpu().numpy())
+            assert (num > 1).any() and olen.tolist() == on.tolist()
+        keep = torch.zeros_like(num)
+        sv.spec_verify_kv_rollback(dev(n), None, num, None, keep, None, gamma_max=N - 1)
+        assert keep.tolist() == (n + np.array(num.tolist())).tolist()
+        sv.spec_verify_kv_weights(a.q, lse, c, dev(n), num, path)
+        w = oracle.weights(host(a.q), host(lse), k, w, a.table, n, num.tolist(), None if path is None else path.cpu().numpy(), a.scale)
+        assert np.allclose(host(a.weight), w, rtol=1e-4, atol=1e-6)
+        # The probabilities of each kept token sum to 1 over its entries.
+        w = host(a.weight)                               # the eviction decides on the stored weights
+        sv.spec_verify_kv_evict(c, keep, 60, 12, olen)
+        k, v, w, on = oracle.evict(k, v, w, a.table, keep.tolist(), 60, 12)
+        for x, y in zip((a.k, a.v, a.weight), (k, v, w)):
+            assert np.array_equal(host(x), y)
+        assert olen.tolist() == on.tolist() and max(on) == 60
+        n = on.copy()
+
+
+@pytest.mark.gpu
+def test_gpu_captured_and_streams(sv):
+    """The calls in a CUDA graph (replayed on new lengths and contents) and on a side stream."""
+    a = Batch((30, 200, 64), 4, 2, 4, 128, 16, seed=6, extra=3)
+    c = a.cache(sv)
+    pre, num = dev(a.prefix), dev([4, 4, 4])
+    sv.attend(a.q, c, pre, num)
+    side = torch.cuda.Stream()
+    graph, outs = torch.cuda.CUDAGraph(), []
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        outs = sv.attend(a.q, c, pre, num)
+        sv.spec_verify_kv_weights(a.q, outs[1], c, pre, num)
+    for prefix, m in (((30, 200, 64), (4, 3, 0)), ((0, 150, 9), (1, 4, 2))):
+        pre.copy_(dev(prefix))
+        num.copy_(dev(m))
+        before = a.weight.clone()
+        graph.replay()
+        check_attention(a, *outs, np.array(prefix), np.array(m), None)
+        want = oracle.weights(host(a.q), host(outs[1]), host(a.k), host(before), a.table, prefix, m, None, a.scale)
+        assert np.allclose(host(a.weight), want, rtol=1e-4, atol=1e-7)
+    side.wait_stream(torch.cuda.current_stream())
+    out, lse = sv.attend(a.q, c, pre, num, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(out, outs[0]) and torch.equal(lse, outs[1])
+
+
+@pytest.mark.gpu
+def test_gpu_workspace_left_ready(sv):
+    """Calls of several sizes on one workspace: its counters are zero after each."""
+    ws = None
+    for prefix, N, H, G, D in (((900, 3), 1, 1, 2, 64), ((2000, 1000, 7), 9, 4, 8, 128), ((300,) * 40, 1, 2, 4, 256),
+                               ((64,), 65, 1, 4, 128)):
+        a = Batch(prefix, N, H, G, D, 16, seed=N)
+        c = a.cache(sv)
+        if ws is None:
+            ws = torch.zeros(1 << 28, dtype=torch.uint8, device="cuda")
+        assert sv.spec_verify_paged_attention_workspace_size(N, H * G, c) <= ws.numel()
+        B = len(prefix)
+        out = torch.empty((B, N, H * G, D), dtype=a.t, device="cuda")
+        lse = torch.empty((B, N, H * G), device="cuda")
+        sv.spec_verify_paged_attention(a.q, c, dev(a.prefix), None, None, out, lse, ws)
+        check_attention(a, out, lse, a.prefix, np.full(B, N), None)
+        assert int(ws[:sv.SV_ATTEND_COUNTER_BYTES].sum()) == 0
+        out2 = torch.empty_like(out)
+        sv.spec_verify_paged_attention(a.q, c, dev(a.prefix), None, None, out2, None, ws)
+        assert torch.equal(out, out2)
