@@ -102,6 +102,7 @@ int stream_cluster_size(long long row_bytes, bool bf16,
 
 std::mutex g_mu;
 int g_device_ok[64];                 // 0 unknown, 1 sm_103, 2 other
+int g_sms[64];                       // multiprocessors, 0 = not queried
 int g_max_clusters[64][2][3][5];     // by device, bf16, variant (narrow, wide, masked), log2(C);
                                      // 0 = not queried
 
@@ -304,6 +305,14 @@ int verify_impl(const void* target_logits, const void* draft_logits, const int32
 namespace sv {
 
 int current_device_status(int* dev) { return check_device(dev); }
+
+int device_sms(int dev) {
+  std::lock_guard<std::mutex> lock(g_mu);
+  if (g_sms[dev] == 0 &&
+      cudaDeviceGetAttribute(&g_sms[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    g_sms[dev] = 0;
+  return g_sms[dev];
+}
 
 int verify_args_status(const void* target_logits, const void* draft_logits,
                        const int32_t* draft_tokens, const int32_t* draft_len,

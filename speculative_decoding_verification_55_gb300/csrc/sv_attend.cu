@@ -4,133 +4,495 @@
 //   s_ij = scale q_i . k_j,  out_i = sum_j p_ij v_j,  p_ij = exp(s_ij - lse_i),  over the entries j < n_b
 //   of row b, token i itself, and the round's tokens before it (a chain) or above it (a tree).
 //
-// The simplest form: one CTA per row, token and query head; its warps take every fourth entry, a lane
-// D / 32 of its elements, with a running maximum and sum each, joined at the end.
+// One pass over keys and values with a running maximum and sum per query row. The query rows of a key
+// head (its query heads times the row's tokens) are the rows of the matrix products, so grouped heads
+// and a round's tokens share every key and value that is read. Persistent CTAs take equal runs of the
+// batch's key tiles (sv_tiles.cuh); an item that several CTAs share is joined by the last of them to
+// arrive, from partial sums in the workspace.
+//
+// A CTA is one producer warp, which copies key tiles from the pages into a ring, and four consumer
+// warps. Each takes 16 of a tile's 64 entries with a maximum, a sum and an accumulator of its own, so
+// that warps meet only at an item's end: S = Q K^T and O += P V are 16 x 8 x 16 matrix instructions, P
+// staying in registers between them.
+// Rounding: probabilities go to the cache's type for the product with the values (half a step of 2^-8
+// or 2^-11 relative, as the output's own rounding); maxima, sums, scores and accumulators are fp32.
 
 #include <cmath>
+#include <type_traits>
 
-#include "sv_cache.cuh"
-#include "sv_common.cuh"
+#include "sv_tiles.cuh"
 
 namespace {
 
-constexpr int kWarps = 4;
+using sv::kFull;
+using sv::kTile;
+
+constexpr int kWarps = 4;                      // consumer warps
+constexpr int kThreads = 32 * (kWarps + 1);
+constexpr int kConsumers = 32 * kWarps;
 
 struct AttendParams {
-  sv::Cache C;
+  sv::Round R;
   const char* q;
-  long long row_stride, token_stride;   // bytes
-  const int32_t* prefix;
-  const int32_t* num;
+  long long row_stride, token_stride;          // bytes
   const int32_t* parents;
   void* out;
   float* lse;
-  float c;                              // scale * log2(e)
-  int N, Hq, group;
+  float c;                                     // scale * log2(e)
+  int Hq;
+  unsigned* counters;                          // [grid] arrivals at the item whose first part it holds
+  float* part_o;                               // [2 grid][rows][D]
+  float2* part_ml;                             // [2 grid][rows] maximum and sum
 };
 
-template <typename T>
-__device__ __forceinline__ float to_f(T x) {
-  if constexpr (sizeof(T) == 2 && std::is_same<T, __half>::value) return __half2float(x);
-  else return __bfloat162float(x);
-}
-template <typename T>
-__device__ __forceinline__ T from_f(float x) {
-  if constexpr (std::is_same<T, __half>::value) return __float2half_rn(x);
-  else return __float2bfloat16_rn(x);
+template <int D>
+constexpr int kStageBytes = 2 * kTile * D * 2;
+template <int D>
+constexpr int kStageCount = D == 64 ? 6 : 3;
+// Queries of an item, then (the queries being read) the join of the warps' accumulators: maxima and
+// sums per warp and row, and two buffers of 16 rows by 16 columns per warp.
+template <int D, int MT>
+constexpr int kScratchBytes = MT * 16 * D * 2 > kWarps * MT * 16 * 8 + 2 * kWarps * 16 * 16 * 4
+                                  ? MT * 16 * D * 2
+                                  : kWarps * MT * 16 * 8 + 2 * kWarps * 16 * 16 * 4;
+template <int D, int MT>
+constexpr int kSmemBytes = 1024 + kStageCount<D> * kStageBytes<D> + kScratchBytes<D, MT>;
+
+template <bool F16>
+__device__ __forceinline__ float value_of(uint32_t h) {
+  if (F16) return __half2float(__ushort_as_half(static_cast<unsigned short>(h)));
+  return __uint_as_float(h << 16);
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(32 * kWarps) sv_attend_plain_kernel(const AttendParams P) {
-  const sv::Cache& C = P.C;
-  const int hq = blockIdx.x, i = blockIdx.y, b = blockIdx.z;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  constexpr int E = D / 32;
-  __shared__ float sm_m[kWarps], sm_l[kWarps], sm_o[kWarps][D];
-  __shared__ int sm_bad;
-  int n, m;
-  bool ok = sv::round_lengths(C, P.prefix, P.num, b, P.N, false, &n, &m);
-  T* out = static_cast<T*>(P.out) + ((static_cast<size_t>(b) * P.N + i) * P.Hq + hq) * D;
-  float* lse = P.lse ? P.lse + (static_cast<size_t>(b) * P.N + i) * P.Hq + hq : nullptr;
-  if (!ok || i >= m) {
-    const float v = ok ? 0.0f : __int_as_float(0x7fc00000);
-    for (int d = threadIdx.x; d < D; d += blockDim.x) out[d] = from_f<T>(v);
-    if (threadIdx.x == 0 && lse) *lse = v;
+// A register of two values with those of entries >= `total` (bit masks keep_lo, keep_hi) cleared, and
+// those that are not finite cleared and reported.
+template <bool F16>
+__device__ __forceinline__ uint32_t finite2(uint32_t x, uint32_t keep, bool& odd) {
+  constexpr uint32_t e = F16 ? 0x7c00u : 0x7f80u;
+  x &= keep;
+  if ((x & e) == e) {
+    odd = true;
+    x &= 0xffff0000u;
+  }
+  if (((x >> 16) & e) == e) {
+    odd = true;
+    x &= 0xffffu;
+  }
+  return x;
+}
+
+template <bool F16, int D, int MT>
+__global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2)
+    sv_attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap kmap,
+                     const __grid_constant__ CUtensorMap vmap) {
+  constexpr int kRows = 16 * MT, kStages = kStageCount<D>;
+  extern __shared__ unsigned char dyn[];
+  __shared__ __align__(8) unsigned long long full[kStages], empty[kStages];
+  __shared__ int bad_stage[kStages];
+  __shared__ unsigned long long masks[sv::kMaxTreeNodes];
+  __shared__ long long scan[kThreads / 32];
+  __shared__ sv::Plan plan;
+  __shared__ int sm_last, sm_flags;
+  const sv::Round& R = P.R;
+  const sv::Cache& C = R.C;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t ring = (sv::smem_addr(dyn) + 1023u) & ~1023u;
+  const uint32_t scratch = ring + kStages * kStageBytes<D>;
+  unsigned char* const scratch_p = dyn + (scratch - sv::smem_addr(dyn));
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      sv::mbar_init(sv::smem_addr(full + s), 1);
+      sv::mbar_init(sv::smem_addr(empty + s), kWarps);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  sv::make_plan<kThreads>(R, scan, &plan);
+
+  // Tokens behind a row's, and rows in error.
+  {
+    const int per = P.Hq * D / 8;
+    for (int b = blockIdx.x; b < R.B; b += gridDim.x) {
+      sv::RowWork w;
+      const bool ok = sv::row_work(R, b, &w);
+      const int i0 = ok ? w.m : 0;
+      const uint32_t v = ok ? 0u : 0x7fff7fffu;                 // NaN in both types
+      uint4* o = reinterpret_cast<uint4*>(P.out) + (static_cast<size_t>(b) * R.N + i0) * per;
+      for (int x = tid; x < (R.N - i0) * per; x += kThreads) o[x] = make_uint4(v, v, v, v);
+      if (P.lse) {
+        float* l = P.lse + (static_cast<size_t>(b) * R.N + i0) * P.Hq;
+        for (int x = tid; x < (R.N - i0) * P.Hq; x += kThreads) l[x] = ok ? 0.0f : __int_as_float(0x7fffffff);
+      }
+    }
+  }
+
+  sv::Walk W;
+  W.begin(R, plan);
+  if (warp == kWarps) {
+    // ---- Producer: page numbers are read one tile ahead of the copies that need them.
+    sv::TileLoader T;
+    T.init(C, 2);
+    int issued = 0;
+    bool gone = false;
+    while (!gone && W.next(R)) {
+      const int entries = W.w.n + W.w.m;
+      int p = T.page(C, W.row, W.first, entries, lane);
+      for (int t = W.first; t < W.first + W.count; ++t) {
+        const int p_next = t + 1 < W.first + W.count ? T.page(C, W.row, t + 1, entries, lane) : -1;
+        const int s = issued % kStages;
+        const uint32_t bar = sv::smem_addr(full + s);
+        if (issued >= kStages && !sv::mbar_wait(sv::smem_addr(empty + s), (issued / kStages - 1) & 1)) {
+          gone = true;
+          break;
+        }
+        const unsigned go = __ballot_sync(kFull, p >= 0), out = __ballot_sync(kFull, p == -2);
+        if (lane == 0) {
+          bad_stage[s] = out != 0;
+          sv::mbar_arrive_expect_tx(bar, static_cast<uint32_t>(__popc(go)) << (T.rows_log2 + 7));
+        }
+        __syncwarp();
+        if (p >= 0) T.load(C, &kmap, &vmap, t, W.head, p, lane, ring + s * kStageBytes<D>, bar);
+        ++issued;
+        p = p_next;
+      }
+    }
+    // No copy is in flight when the CTA ends.
+    for (int x = issued < kStages ? 0 : issued - kStages; x < issued; ++x)
+      sv::mbar_wait_drain(sv::smem_addr(full + x % kStages), (x / kStages) & 1);
     return;
   }
-  if (threadIdx.x == 0) sm_bad = 0;
-  // Ancestors of token i and the validity of the row's tree.
-  const int32_t* par = P.parents ? P.parents + static_cast<size_t>(b) * P.N : nullptr;
-  bool bad = false;
-  if (par)
-    for (int t = threadIdx.x; t < m; t += blockDim.x) {
-      const int p = __ldg(par + t);
-      bad |= t == 0 ? p != -1 : (p < 0 || p >= t);
-    }
-  bad = __syncthreads_or(bad);
-  unsigned long long seen = 0;          // tokens 1..64 that token i attends, as bits 0..63
-  if (par && !bad)
-    for (int t = i; t > 0; t = __ldg(par + t)) seen |= 1ull << (t - 1);
-  const int h = hq / P.group;
-  const T* q = reinterpret_cast<const T*>(P.q + b * P.row_stride + i * P.token_stride) + hq * D;
-  float qf[E], o[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    qf[e] = to_f<T>(q[lane * E + e]);
-    o[e] = 0.0f;
-  }
-  float mx = -INFINITY, l = 0.0f;
-  if (!bad)
-    for (int j = warp; j < n + m; j += kWarps) {
-      if (j >= n) {
-        const int t = j - n;
-        if (par ? (t > 0 && !((seen >> (t - 1)) & 1)) : t > i) continue;
+
+  // ---- Consumers
+  const int g = lane >> 2, t4 = lane & 3;
+  const float c = P.c;
+  int done = 0;                                // tiles taken from the ring
+  bool lost = false;                           // a wait gave up: every result from here on is NaN
+  while (W.next(R)) {
+    const int n = W.w.n, m = W.w.m, entries = n + m;
+    const int row0 = W.q_tile * kRows;         // query rows of the item: [row0, row0 + kRows)
+    const int rows = min(kRows, m * R.group - row0);
+    const char* qb = P.q + W.row * P.row_stride + static_cast<long long>(W.head) * R.group * (D * 2);
+    // Queries into shared memory, zeros in the rows past the last.
+    for (int x = tid; x < kRows * (D / 8); x += kConsumers) {
+      const int r = x / (D / 8), ch = x % (D / 8);
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (r < rows) {
+        const int i = (row0 + r) / R.group, hg = (row0 + r) - i * R.group;
+        v = __ldg(reinterpret_cast<const uint4*>(qb + i * P.token_stride + hg * (D * 2)) + ch);
       }
-      const int page = sv::cache_page(C, b, j);
-      if (!sv::page_ok(C, page)) {
-        bad = true;
-        break;
-      }
-      const long long at = sv::entry_offset(C, page, h, j);
-      const T* k = reinterpret_cast<const T*>(C.k + at);
-      const T* v = reinterpret_cast<const T*>(C.v + at);
-      float s = 0.0f;
-#pragma unroll
-      for (int e = 0; e < E; ++e) s = fmaf(qf[e], to_f<T>(k[lane * E + e]), s);
-#pragma unroll
-      for (int w = 16; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-      s *= P.c;
-      const float nm = fmaxf(mx, s);
-      const float f = mx == nm ? 1.0f : exp2f(mx - nm);
-      const float p = s == -INFINITY ? 0.0f : exp2f(s - nm);
-      l = l * f + p;
-#pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = o[e] * f + p * to_f<T>(v[lane * E + e]);
-      mx = nm;
+      const uint32_t a = sv::swizzled(scratch + (ch >> 3) * (kRows * 128), r, ch & 7);
+      *reinterpret_cast<uint4*>(scratch_p + (a - scratch)) = v;
     }
-  if (bad) sm_bad = 1;
+    if (tid == 0) sm_flags = 0;
+    bool bad = false;
+    const int last = W.first + W.count;
+    const bool tail = last * kTile > n;        // the run reaches the round's own entries
+    if (P.parents && tail)
+      bad = !sv::tree_masks(P.parents + static_cast<size_t>(W.row) * R.N, m, masks, tid, kConsumers);
+    else if (P.parents)                        // validity alone
+      for (int x = tid; x < m; x += kConsumers) {
+        const int p = __ldg(P.parents + static_cast<size_t>(W.row) * R.N + x);
+        bad |= x == 0 ? p != -1 : (p < 0 || p >= x);
+      }
+    sv::named_bar_sync(1, kConsumers);
+    int tok[2 * MT];                           // token of each of this thread's query rows
 #pragma unroll
-  for (int e = 0; e < E; ++e) sm_o[warp][lane * E + e] = o[e];
-  if (lane == 0) {
-    sm_m[warp] = mx;
-    sm_l[warp] = l;
+    for (int x = 0; x < 2 * MT; ++x)
+      tok[x] = min((row0 + 16 * (x >> 1) + 8 * (x & 1) + g) / R.group, m - 1);
+
+    float mx[2 * MT], l[2 * MT], o[MT][D / 8][4];
+#pragma unroll
+    for (int x = 0; x < 2 * MT; ++x) {
+      mx[x] = -INFINITY;
+      l[x] = 0.0f;
+    }
+#pragma unroll
+    for (int x = 0; x < MT; ++x)
+#pragma unroll
+      for (int y = 0; y < D / 8; ++y)
+#pragma unroll
+        for (int z = 0; z < 4; ++z) o[x][y][z] = 0.0f;
+    bool odd = false;                          // values that are not finite among the round's own
+
+    for (int t = W.first; t < last; ++t, ++done) {
+      const int s = done % kStages;
+      if (!lost && !sv::mbar_wait(sv::smem_addr(full + s), (done / kStages) & 1)) lost = true;
+      bad |= bad_stage[s] != 0;
+      const int j0 = t * kTile + 16 * warp;
+      if (j0 < entries && !lost) {
+        const uint32_t kb = ring + s * kStageBytes<D>, vb = kb + kTile * D * 2;
+        float sc[MT][2][4];
+#pragma unroll
+        for (int x = 0; x < MT; ++x)
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+#pragma unroll
+            for (int z = 0; z < 4; ++z) sc[x][y][z] = 0.0f;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          uint32_t kf[4];
+          sv::ldsm4(kf, sv::swizzled(kb + (kk >> 2) * (kTile * 128), 16 * warp + (lane & 7) + ((lane >> 4) << 3),
+                                     ((kk & 3) << 1) + ((lane >> 3) & 1)));
+#pragma unroll
+          for (int x = 0; x < MT; ++x) {
+            uint32_t qf[4];
+            sv::ldsm4(qf, sv::swizzled(scratch + (kk >> 2) * (kRows * 128), 16 * x + (lane & 15),
+                                       ((kk & 3) << 1) + (lane >> 4)));
+            sv::mma<F16>(sc[x][0], qf, kf[0], kf[1]);
+            sv::mma<F16>(sc[x][1], qf, kf[2], kf[3]);
+          }
+        }
+        const bool edge = j0 + 16 > n;         // entries of the round itself, or behind the last
+        if (edge) {
+#pragma unroll
+          for (int x = 0; x < MT; ++x)
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+#pragma unroll
+              for (int z = 0; z < 4; ++z) {
+                const int a = j0 + 8 * y + 2 * t4 + (z & 1) - n, i = tok[2 * x + (z >> 1)];
+                bool see = a <= i;
+                if (P.parents) see = a <= 0 || (a < m && ((masks[i] >> (a - 1)) & 1));
+                if (!see) sc[x][y][z] = -INFINITY;
+              }
+        }
+        // Running maximum; accumulators are rescaled only when one of the warp's rows grew.
+        float grow[2 * MT];
+        bool any = false;
+#pragma unroll
+        for (int x = 0; x < 2 * MT; ++x) {
+          const int a = x >> 1, z = (x & 1) * 2;
+          float v = fmaxf(fmaxf(sc[a][0][z], sc[a][0][z + 1]), fmaxf(sc[a][1][z], sc[a][1][z + 1]));
+          v = fmaxf(v, __shfl_xor_sync(kFull, v, 1));
+          v = fmaxf(v, __shfl_xor_sync(kFull, v, 2));
+          grow[x] = fmaxf(mx[x], v);
+          any |= grow[x] > mx[x];
+        }
+        if (__any_sync(kFull, any)) {
+#pragma unroll
+          for (int x = 0; x < 2 * MT; ++x) {
+            const float f = grow[x] == mx[x] ? 1.0f : sv::ex2((mx[x] - grow[x]) * c);
+            mx[x] = grow[x];
+            l[x] *= f;
+#pragma unroll
+            for (int y = 0; y < D / 8; ++y) {
+              o[x >> 1][y][(x & 1) * 2] *= f;
+              o[x >> 1][y][(x & 1) * 2 + 1] *= f;
+            }
+          }
+        }
+        uint32_t pf[MT][4];
+#pragma unroll
+        for (int x = 0; x < MT; ++x)
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+#pragma unroll
+            for (int z = 0; z < 4; z += 2) {
+              const int r = 2 * x + (z >> 1);
+              const float b = mx[r] == -INFINITY ? 0.0f : mx[r] * c;
+              const float p0 = sv::ex2(fmaf(sc[x][y][z], c, -b)), p1 = sv::ex2(fmaf(sc[x][y][z + 1], c, -b));
+              l[r] += p0 + p1;
+              pf[x][2 * y + (z >> 1)] = sv::pack2<F16>(p0, p1);
+            }
+        const uint32_t keep0 = edge ? (j0 + 2 * t4 < entries ? 0xffffu : 0u) | (j0 + 2 * t4 + 1 < entries ? 0xffff0000u : 0u) : 0u;
+        const uint32_t keep1 = edge ? (j0 + 8 + 2 * t4 < entries ? 0xffffu : 0u) | (j0 + 9 + 2 * t4 < entries ? 0xffff0000u : 0u) : 0u;
+#pragma unroll
+        for (int y = 0; y < D / 16; ++y) {
+          uint32_t vf[4];
+          sv::ldsm4_t(vf, sv::swizzled(vb + (y >> 2) * (kTile * 128), 16 * warp + (lane & 15),
+                                       ((y & 3) << 1) + (lane >> 4)));
+          if (edge) {
+            vf[0] = finite2<F16>(vf[0], keep0, odd);
+            vf[1] = finite2<F16>(vf[1], keep1, odd);
+            vf[2] = finite2<F16>(vf[2], keep0, odd);
+            vf[3] = finite2<F16>(vf[3], keep1, odd);
+          }
+#pragma unroll
+          for (int x = 0; x < MT; ++x) {
+            sv::mma<F16>(o[x][2 * y], pf[x], vf[0], vf[1]);
+            sv::mma<F16>(o[x][2 * y + 1], pf[x], vf[2], vf[3]);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) sv::mbar_arrive(sv::smem_addr(empty + s));
+    }
+
+    // Values of the round's own entries that are not finite were left out of the products, where their
+    // zero probability would have made NaN of them: they are added to the rows that attend them.
+    if (__any_sync(kFull, odd)) {
+      for (int j = max(n, W.first * kTile); j < min(entries, last * kTile); ++j) {
+        if (((j % kTile) >> 4) != warp) continue;
+        const int page = sv::cache_page(C, W.row, j);
+        if (!sv::page_ok(C, page)) continue;
+        const unsigned short* v = reinterpret_cast<const unsigned short*>(C.v + sv::entry_offset(C, page, W.head, j));
+        const int a = j - n;
+#pragma unroll
+        for (int y = 0; y < D / 8; ++y)
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            const float f = value_of<F16>(v[8 * y + 2 * t4 + (z & 1)]);
+            if (isfinite(f)) continue;
+#pragma unroll
+            for (int x = 0; x < MT; ++x) {
+              const int i = tok[2 * x + (z >> 1)];
+              bool see = a <= i;
+              if (P.parents) see = a <= 0 || ((masks[i] >> (a - 1)) & 1);
+              if (see) o[x][y][z] += f;
+            }
+          }
+      }
+    }
+    if (bad || lost) atomicOr(&sm_flags, 1);
+
+    // Join of the four warps: maxima and sums, then 16 columns at a time through two buffers.
+#pragma unroll
+    for (int x = 0; x < 2 * MT; ++x) {
+      l[x] += __shfl_xor_sync(kFull, l[x], 1);
+      l[x] += __shfl_xor_sync(kFull, l[x], 2);
+    }
+    sv::named_bar_sync(1, kConsumers);         // the queries have been read
+    float2* ml = reinterpret_cast<float2*>(scratch_p);                       // [kWarps][kRows]
+    float* buf = reinterpret_cast<float*>(scratch_p + kWarps * kRows * 8);   // [2][kWarps][16][16]
+    if (t4 == 0)
+#pragma unroll
+      for (int x = 0; x < 2 * MT; ++x)
+        ml[warp * kRows + 16 * (x >> 1) + 8 * (x & 1) + g] = make_float2(mx[x], l[x]);
+    sv::named_bar_sync(1, kConsumers);
+    const bool nan_item = sm_flags != 0;
+    float M[2 * MT], fw[2 * MT];
+#pragma unroll
+    for (int x = 0; x < 2 * MT; ++x) {
+      const int r = 16 * (x >> 1) + 8 * (x & 1) + g;
+      M[x] = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) M[x] = fmaxf(M[x], ml[w * kRows + r].x);
+      fw[x] = mx[x] == -INFINITY ? 0.0f : sv::ex2((mx[x] - M[x]) * c);
+    }
+    const bool whole = W.count == W.w.tiles;
+    const int slot = 2 * blockIdx.x + (W.first == 0 ? 1 : 0);
+    // This thread's place in the joined chunks: a row and two columns of each.
+    const int jr = tid >> 3, jc = (tid & 7) * 2;
+#pragma unroll
+    for (int x = 0; x < MT; ++x) {
+      const int r = 16 * x + jr;
+      float jm = -INFINITY, jl = 0.0f;
+      for (int w = 0; w < kWarps; ++w) jm = fmaxf(jm, ml[w * kRows + r].x);
+      for (int w = 0; w < kWarps; ++w) {
+        const float2 e = ml[w * kRows + r];
+        if (e.x > -INFINITY) jl += e.y * sv::ex2((e.x - jm) * c);
+        else jl += e.y;                        // 0, or NaN
+      }
+      if (nan_item) jl = __int_as_float(0x7fffffff);
+      const int i = (row0 + r) / R.group, hq = W.head * R.group + (row0 + r) - i * R.group;
+      const size_t at = (static_cast<size_t>(W.row) * R.N + i) * P.Hq + hq;
+      const float inv = 1.0f / jl;
+#pragma unroll
+      for (int y = 0; y < D / 16; ++y) {
+        float* bw = buf + ((x * (D / 16) + y) & 1) * (kWarps * 256);
+#pragma unroll
+        for (int z = 0; z < 2; ++z)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float f = fw[2 * x + e];
+            *reinterpret_cast<float2*>(bw + warp * 256 + (8 * e + g) * 16 + ((8 * z + 2 * t4) ^ ((g & 1) << 3))) =
+                make_float2(o[x][2 * y + z][2 * e] * f, o[x][2 * y + z][2 * e + 1] * f);
+          }
+        sv::named_bar_sync(1, kConsumers);
+        if (r < rows) {
+          float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) {
+            const float2 e = *reinterpret_cast<const float2*>(bw + w * 256 + jr * 16 + (jc ^ ((jr & 1) << 3)));
+            s0 += e.x;
+            s1 += e.y;
+          }
+          if (whole)
+            *reinterpret_cast<uint32_t*>(static_cast<char*>(P.out) + (at * D + 16 * y + jc) * 2) = sv::pack2<F16>(s0 * inv, s1 * inv);
+          else
+            *reinterpret_cast<float2*>(P.part_o + (static_cast<size_t>(slot) * kRows + r) * D + 16 * y + jc) = make_float2(s0, s1);
+        }
+      }
+      if ((tid & 7) == 0 && r < rows) {
+        if (!whole) P.part_ml[slot * kRows + r] = make_float2(jm, jl);
+        else if (P.lse) P.lse[at] = (jm * c + log2f(jl)) * 0.6931471805599453f;
+      }
+    }
+    if (whole) {
+      sv::named_bar_sync(1, kConsumers);       // the scratch is free for the next item's queries
+      continue;
+    }
+
+    // An item of several CTAs: the last to arrive joins the parts.
+    const long long item_at = W.at - W.first;
+    const int c0 = sv::tile_owner(item_at, plan), c1 = sv::tile_owner(item_at + W.w.tiles - 1, plan);
+    sv::named_bar_sync(1, kConsumers);
+    if (tid == 0) {
+      __threadfence();
+      const unsigned old = atomicAdd(P.counters + c0, 1u);
+      sm_last = old == static_cast<unsigned>(c1 - c0);
+      if (sm_last) P.counters[c0] = 0u;        // left zero for the next call
+      __threadfence();
+    }
+    sv::named_bar_sync(1, kConsumers);
+    if (!sm_last) continue;
+    float* fin = reinterpret_cast<float*>(scratch_p);          // per row: maximum, 1 / sum
+    if (tid < rows) {
+      float jm = -INFINITY, jl = 0.0f;
+      for (int p = c0; p <= c1; ++p) jm = fmaxf(jm, __ldcg(P.part_ml + (2 * p + (p == c0)) * kRows + tid).x);
+      for (int p = c0; p <= c1; ++p) {
+        const float2 e = __ldcg(P.part_ml + (2 * p + (p == c0)) * kRows + tid);
+        if (e.x > -INFINITY) jl += e.y * sv::ex2((e.x - jm) * c);
+        else jl += e.y;
+      }
+      fin[2 * tid] = jm;
+      fin[2 * tid + 1] = 1.0f / jl;
+      const int i = (row0 + tid) / R.group, hq = W.head * R.group + (row0 + tid) - i * R.group;
+      if (P.lse) P.lse[(static_cast<size_t>(W.row) * R.N + i) * P.Hq + hq] = (jm * c + log2f(jl)) * 0.6931471805599453f;
+    }
+    sv::named_bar_sync(1, kConsumers);
+    for (int x = tid; x < rows * (D / 4); x += kConsumers) {
+      const int r = x / (D / 4), col = (x % (D / 4)) * 4;
+      const float jm = fin[2 * r], inv = fin[2 * r + 1];
+      float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+      for (int p = c0; p <= c1; ++p) {
+        const int sl = 2 * p + (p == c0);
+        const float pm = __ldcg(&P.part_ml[sl * kRows + r].x);
+        const float4 e = __ldcg(reinterpret_cast<const float4*>(P.part_o + (static_cast<size_t>(sl) * kRows + r) * D + col));
+        const float f = pm == -INFINITY ? 0.0f : sv::ex2((pm - jm) * c);
+        a.x += e.x * f;
+        a.y += e.y * f;
+        a.z += e.z * f;
+        a.w += e.w * f;
+      }
+      const int i = (row0 + r) / R.group, hq = W.head * R.group + (row0 + r) - i * R.group;
+      uint2 v;
+      v.x = sv::pack2<F16>(a.x * inv, a.y * inv);
+      v.y = sv::pack2<F16>(a.z * inv, a.w * inv);
+      *reinterpret_cast<uint2*>(static_cast<char*>(P.out) + (((static_cast<size_t>(W.row) * R.N + i) * P.Hq + hq) * D + col) * 2) = v;
+    }
+    sv::named_bar_sync(1, kConsumers);
   }
-  __syncthreads();
-  float M = -INFINITY, L = 0.0f;
-  for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm_m[w]);
-  float f[kWarps];
-  for (int w = 0; w < kWarps; ++w) {
-    f[w] = sm_m[w] == -INFINITY ? 0.0f : exp2f(sm_m[w] - M);
-    L += sm_l[w] * f[w];
-  }
-  for (int d = threadIdx.x; d < D; d += blockDim.x) {
-    float x = 0.0f;
-    for (int w = 0; w < kWarps; ++w)
-      if (f[w] != 0.0f) x += sm_o[w][d] * f[w];
-    out[d] = from_f<T>(sm_bad ? __int_as_float(0x7fc00000) : x / L);
-  }
-  if (threadIdx.x == 0 && lse)
-    *lse = sm_bad ? __int_as_float(0x7fc00000) : (M + log2f(L)) * 0.6931471805599453f;
+}
+
+// Query rows of an item: 16 where a key head has no more, else 32 (heads of 256 keep 16: their
+// accumulators fill the registers).
+int row_tiles_of(int N, int group, int D) { return N * group <= 16 || D == 256 ? 1 : 2; }
+
+int grid_limit(int sms, int D) { return sms * (D == 256 ? 1 : 2); }
+constexpr int kMaxSms = 160;
+
+size_t part_bytes(int grid, int MT, int D) {
+  return static_cast<size_t>(2) * grid * 16 * MT * (D * 4 + 8);
+}
+
+template <bool F16, int D, int MT>
+int launch(const AttendParams& P, const CUtensorMap& k, const CUtensorMap& v, int grid, cudaStream_t st) {
+  auto kern = sv_attend_kernel<F16, D, MT>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (kSmemBytes<D, MT>)) != cudaSuccess)
+    return SV_ERR_CUDA;
+  kern<<<grid, kThreads, (kSmemBytes<D, MT>), st>>>(P, k, v);
+  return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 
 }  // namespace
@@ -138,9 +500,10 @@ __global__ void __launch_bounds__(32 * kWarps) sv_attend_plain_kernel(const Atte
 extern "C" size_t spec_verify_paged_attention_workspace_size(int32_t N, int32_t Hq,
                                                              const sv_paged_cache* cache) {
   if (!cache || N < 1 || N > SV_MAX_GAMMA + 1 || Hq < 1 || Hq > 1024 || cache->heads < 1 ||
-      Hq % cache->heads != 0)
+      Hq % cache->heads != 0 || cache->head_dim < 1 || cache->head_dim > 256)
     return 0;
-  return SV_ATTEND_COUNTER_BYTES;
+  const int D = cache->head_dim, MT = row_tiles_of(N, Hq / cache->heads, D);
+  return SV_ATTEND_COUNTER_BYTES + (part_bytes(grid_limit(kMaxSms, D), MT, D) + 255) / 256 * 256;
 }
 
 extern "C" int spec_verify_paged_attention(const void* q, int64_t q_row_stride,
@@ -151,7 +514,7 @@ extern "C" int spec_verify_paged_attention(const void* q, int64_t q_row_stride,
                                            void* workspace, size_t workspace_bytes,
                                            void* cuda_stream) {
   AttendParams P;
-  int st = sv::check_cache(cache, B, false, &P.C);
+  int st = sv::check_cache(cache, B, false, &P.R.C);
   if (st != SV_OK) return st;
   if (!q || !prefix_len || !out) return SV_ERR_NULL_POINTER;
   st = sv::check_tokens(q, q_row_stride, q_token_stride, B, N, Hq, cache->head_dim);
@@ -166,25 +529,46 @@ extern "C" int spec_verify_paged_attention(const void* q, int64_t q_row_stride,
   int dev = 0;
   st = sv::current_device_status(&dev);
   if (st != SV_OK) return st;
+  const int D = cache->head_dim, group = Hq / cache->heads, MT = row_tiles_of(N, group, D);
+  CUtensorMap kmap, vmap;
+  st = sv::cache_tensor_map(cache, cache->k, sv::box_rows(cache), &kmap);
+  if (st == SV_OK) st = sv::cache_tensor_map(cache, cache->v, sv::box_rows(cache), &vmap);
+  if (st != SV_OK) return st;
+  P.R.prefix = prefix_len;
+  P.R.num = num_queries;
+  P.R.B = B;
+  P.R.N = N;
+  P.R.group = group;
+  P.R.q_rows = 16 * MT;
+  P.R.none_ok = false;
   P.q = static_cast<const char*>(q);
   P.row_stride = q_row_stride * 2;
   P.token_stride = q_token_stride * 2;
-  P.prefix = prefix_len;
-  P.num = num_queries;
   P.parents = tree_parents;
   P.out = out;
   P.lse = out_lse;
   P.c = scale * sv::kLog2e;
-  P.N = N;
   P.Hq = Hq;
-  P.group = Hq / cache->heads;
+  // As many CTAs as the GPU holds, or as many as the batch can have tiles.
+  int sms = sv::device_sms(dev);
+  if (sms < 1) return SV_ERR_CUDA;
+  if (sms > kMaxSms) sms = kMaxSms;
+  const long long most = static_cast<long long>(B) * cache->heads * ((N * group + 16 * MT - 1) / (16 * MT)) *
+                         ((static_cast<long long>(cache->max_pages) * cache->page_size + kTile - 1) / kTile);
+  const int grid = static_cast<int>(most < grid_limit(sms, D) ? most : grid_limit(sms, D));
+  char* ws = static_cast<char*>(workspace);
+  P.counters = reinterpret_cast<unsigned*>(ws);
+  P.part_ml = reinterpret_cast<float2*>(ws + SV_ATTEND_COUNTER_BYTES);
+  P.part_o = reinterpret_cast<float*>(ws + SV_ATTEND_COUNTER_BYTES + static_cast<size_t>(2) * grid * 16 * MT * 8);
+  cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   const bool f16 = cache->dtype == SV_DTYPE_F16;
-  void (*kern)(const AttendParams) = nullptr;
-  switch (cache->head_dim) {
-    case 64: kern = f16 ? sv_attend_plain_kernel<__half, 64> : sv_attend_plain_kernel<__nv_bfloat16, 64>; break;
-    case 128: kern = f16 ? sv_attend_plain_kernel<__half, 128> : sv_attend_plain_kernel<__nv_bfloat16, 128>; break;
-    default: kern = f16 ? sv_attend_plain_kernel<__half, 256> : sv_attend_plain_kernel<__nv_bfloat16, 256>; break;
+  if (D == 64) {
+    if (MT == 1) return f16 ? launch<true, 64, 1>(P, kmap, vmap, grid, s) : launch<false, 64, 1>(P, kmap, vmap, grid, s);
+    return f16 ? launch<true, 64, 2>(P, kmap, vmap, grid, s) : launch<false, 64, 2>(P, kmap, vmap, grid, s);
   }
-  kern<<<dim3(Hq, N, B), 32 * kWarps, 0, static_cast<cudaStream_t>(cuda_stream)>>>(P);
-  return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+  if (D == 128) {
+    if (MT == 1) return f16 ? launch<true, 128, 1>(P, kmap, vmap, grid, s) : launch<false, 128, 1>(P, kmap, vmap, grid, s);
+    return f16 ? launch<true, 128, 2>(P, kmap, vmap, grid, s) : launch<false, 128, 2>(P, kmap, vmap, grid, s);
+  }
+  return f16 ? launch<true, 256, 1>(P, kmap, vmap, grid, s) : launch<false, 256, 1>(P, kmap, vmap, grid, s);
 }

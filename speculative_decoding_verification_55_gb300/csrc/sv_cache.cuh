@@ -2,6 +2,7 @@
 // the two storage types, and the checks that every entry point makes on the host.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -106,6 +107,14 @@ inline int check_tokens(const void* x, int64_t row_stride, int64_t token_stride,
   if (misaligned(x, 16) || row_stride % 8 != 0 || token_stride % 8 != 0) return SV_ERR_MISALIGNED;
   return SV_OK;
 }
+
+// A tensor map over the cache's keys or values (dimensions D, slot, head, page) whose boxes are 64
+// elements (128 bytes, swizzled) of `rows` slots of one page and head.
+int cache_tensor_map(const sv_paged_cache* c, const void* base, int rows, CUtensorMap* map);
+// Slots of one box: a page's, at most 64.
+inline int box_rows(const sv_paged_cache* c) { return c->page_size < 64 ? c->page_size : 64; }
+// Multiprocessors of a device (sv_api.cu).
+int device_sms(int dev);
 
 // SV_OK when the current device is compute capability 10.3 (sv_api.cu).
 int current_device_status(int* dev);

@@ -1,0 +1,246 @@
+// What the attention and weight kernels share: the split of a batch's key tiles over the CTAs, the
+// copies of a tile from the pages, and the matrix instructions.
+#pragma once
+
+#include "sv_cache.cuh"
+#include "sv_common.cuh"
+
+namespace sv {
+
+constexpr int kTile = 64;                 // entries of a key tile
+
+// The round a batch is in, and how its work divides. A row's work is one item per key head and tile of
+// query rows (row r = token r / group, query head r % group of the key head's); an item is
+// ceil((n + m) / kTile) key tiles. The batch's tiles, in the order (row, head, query tile, key tile),
+// are cut into equal runs, one per CTA: no CTA gets over one tile more than another, whatever the
+// lengths are, and only the items at a run's ends are shared with another CTA.
+struct Round {
+  Cache C;
+  const int32_t* prefix;
+  const int32_t* num;
+  int B, N, group, q_rows;                // q_rows: query rows of a query tile
+  bool none_ok;                           // num = -1 counts as no token
+};
+
+struct RowWork {
+  int n, m, tiles, q_tiles;
+};
+
+// False for a row in error (no work).
+__device__ __forceinline__ bool row_work(const Round& R, int b, RowWork* w) {
+  const bool ok = round_lengths(R.C, R.prefix, R.num, b, R.N, R.none_ok, &w->n, &w->m);
+  const bool some = ok && w->m > 0;
+  w->tiles = some ? (w->n + w->m + kTile - 1) / kTile : 0;
+  w->q_tiles = some ? (w->m * R.group + R.q_rows - 1) / R.q_rows : 0;
+  return ok;
+}
+__device__ __forceinline__ long long row_tiles(const Round& R, const RowWork& w) {
+  return static_cast<long long>(w.tiles) * w.q_tiles * R.C.heads;
+}
+
+struct Plan {
+  long long total;                        // tiles of the batch
+  long long parts;                        // CTAs with work: each of them has a tile at least
+  long long at;                           // first tile of this CTA's run
+  long long row_at;                       // first tile of the row that holds it
+  int row;
+};
+
+// Where this CTA's run begins; every thread of the CTA calls it (kThreads of them), `sh` and `plan` in
+// shared memory.
+template <int kThreads>
+__device__ void make_plan(const Round& R, long long (&sh)[kThreads / 32], Plan* plan) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (R.B + kThreads - 1) / kThreads;
+  const int b0 = min(tid * per, R.B), b1 = min(b0 + per, R.B);
+  long long sum = 0;
+  RowWork w;
+  for (int b = b0; b < b1; ++b) {
+    row_work(R, b, &w);
+    sum += row_tiles(R, w);
+  }
+  long long incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(kFull, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) sh[warp] = incl;
+  __syncthreads();
+  long long before = incl - sum, total = 0;
+#pragma unroll
+  for (int x = 0; x < kThreads / 32; ++x) {
+    if (x < warp) before += sh[x];
+    total += sh[x];
+  }
+  const long long parts = total < gridDim.x ? total : gridDim.x;
+  const long long at = blockIdx.x < parts ? total * blockIdx.x / parts : total;
+  if (tid == 0) {
+    plan->total = total;
+    plan->parts = parts;
+    plan->at = at;
+    plan->row = R.B;
+  }
+  __syncthreads();
+  if (at >= before && at < before + sum) {
+    long long run = before;
+    for (int b = b0; b < b1; ++b) {
+      row_work(R, b, &w);
+      const long long t = row_tiles(R, w);
+      if (at < run + t) {
+        plan->row = b;
+        plan->row_at = run;
+        break;
+      }
+      run += t;
+    }
+  }
+  __syncthreads();
+}
+
+// The CTA that holds tile t of the batch.
+__device__ __forceinline__ int tile_owner(long long t, const Plan& p) {
+  return static_cast<int>(((t + 1) * p.parts - 1) / p.total);
+}
+
+// A walk over the items of this CTA's run: begin(), then next() while it returns true.
+struct Walk {
+  long long at, end, row_at;
+  int row, head, q_tile, first, count;    // key tiles [first, first + count) of the item
+  RowWork w;
+
+  __device__ __forceinline__ void begin(const Round& R, const Plan& p) {
+    at = p.at;
+    end = blockIdx.x < p.parts ? p.total * (blockIdx.x + 1) / p.parts : at;
+    row = p.row;
+    row_at = p.row_at;
+    count = 0;
+    if (at < end) row_work(R, row, &w);
+  }
+  __device__ __forceinline__ bool next(const Round& R) {
+    at += count;
+    if (at >= end) return false;
+    while (at - row_at >= row_tiles(R, w)) {     // past this row: the next one with work
+      row_at += row_tiles(R, w);
+      ++row;
+      row_work(R, row, &w);
+    }
+    const int in_row = static_cast<int>(at - row_at), item = in_row / w.tiles;
+    first = in_row - item * w.tiles;
+    head = item / w.q_tiles;
+    q_tile = item - head * w.q_tiles;
+    const long long left = end - at;
+    count = left < w.tiles - first ? static_cast<int>(left) : w.tiles - first;
+    return true;
+  }
+};
+
+// ------------------------------------------------------------------------------------------------
+// Copies
+// ------------------------------------------------------------------------------------------------
+
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int slot,
+                                         int head, int page, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4, %5}], [%6];"
+      ::"r"(dst), "l"(map), "r"(x), "r"(slot), "r"(head), "r"(page), "r"(bar)
+      : "memory");
+}
+
+// The page numbers of a tile's boxes for lane `lane` of the producer warp: box x of an array covers
+// `rows` entries of one page and 64 of the D elements. Lanes take (array, box, 64 elements) in order.
+struct TileLoader {
+  int boxes_log2, halves_log2, rows_log2, ops;
+
+  __device__ __forceinline__ void init(const Cache& C, int arrays) {
+    rows_log2 = C.page_log2 < 6 ? C.page_log2 : 6;
+    boxes_log2 = 6 - rows_log2;
+    halves_log2 = C.head_dim == 64 ? 0 : (C.head_dim == 128 ? 1 : 2);
+    ops = arrays << (boxes_log2 + halves_log2);
+  }
+  // Page of operation `op` of a tile: -1 when it lies behind the row's entries, -2 when out of range.
+  __device__ __forceinline__ int page(const Cache& C, int row, int tile, int entries, int op) const {
+    const int box = (op >> halves_log2) & ((1 << boxes_log2) - 1);
+    const int j = tile * kTile + (box << rows_log2);
+    if (op >= ops || j >= entries) return -1;
+    const int p = cache_page(C, row, j);
+    return page_ok(C, p) ? p : -2;
+  }
+  // The copy of operation `op`: stage holds the arrays one after the other, each [D / 64][kTile][64].
+  __device__ __forceinline__ void load(const Cache& C, const CUtensorMap* k, const CUtensorMap* v,
+                                       int tile, int head, int p, int op, uint32_t stage,
+                                       uint32_t bar) const {
+    const int half = op & ((1 << halves_log2) - 1);
+    const int box = (op >> halves_log2) & ((1 << boxes_log2) - 1);
+    const int array = op >> (halves_log2 + boxes_log2);
+    const int j = tile * kTile + (box << rows_log2);
+    const uint32_t dst = stage + (((array << halves_log2) + half) << 13) + (box << (rows_log2 + 7));
+    tma_load(dst, array ? v : k, half * 64, j & (C.page_size - 1), head, p, bar);
+  }
+};
+
+// ------------------------------------------------------------------------------------------------
+// Matrix instructions and their operands in shared memory (rows of 128 bytes, 16-byte chunks swizzled
+// by the row's low three bits as the tensor maps write them)
+// ------------------------------------------------------------------------------------------------
+
+__device__ __forceinline__ uint32_t swizzled(uint32_t base, int row, int chunk) {
+  return base + row * 128 + ((chunk ^ (row & 7)) << 4);
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+
+template <bool F16>
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if (F16)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Two fp32 values rounded to the cache's type, lo in the low half.
+template <bool F16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  if (F16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// ------------------------------------------------------------------------------------------------
+// Which of the round's tokens a token attends
+// ------------------------------------------------------------------------------------------------
+
+// Per token of a tree the tokens 1..64 that it attends (its ancestors and itself; all attend token 0),
+// as bits 0..63. Called by `threads` threads, thread `tid`; returns whether this thread's nodes are
+// valid. A walk upwards ends: it stops at a parent that is not below its node.
+__device__ __forceinline__ bool tree_masks(const int32_t* parents, int m, unsigned long long* masks,
+                                           int tid, int threads) {
+  bool ok = true;
+  for (int t = tid; t < m; t += threads) {
+    const int p = __ldg(parents + t);
+    ok &= t == 0 ? p == -1 : (p >= 0 && p < t);
+    unsigned long long s = 0;
+    for (int x = t; x > 0;) {
+      s |= 1ull << (x - 1);
+      const int up = __ldg(parents + x);
+      if (up >= x) break;
+      x = up;
+    }
+    masks[t] = s;
+  }
+  return ok;
+}
+
+}  // namespace sv
