@@ -20,30 +20,19 @@
 #include <cmath>
 #include <type_traits>
 
-#include "sv_tiles.cuh"
+#include "sv_attend.cuh"
 
 namespace {
 
+using sv::AttendParams;
+using sv::finite2;
 using sv::kFull;
-using sv::kTile;
+using sv::value_of;
 
+constexpr int kTileLog2 = 6, kTile = 1 << kTileLog2;   // entries of a key tile
 constexpr int kWarps = 4;                      // consumer warps
 constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kConsumers = 32 * kWarps;
-
-struct AttendParams {
-  sv::Round R;
-  const char* q;
-  long long row_stride, token_stride;          // bytes
-  const int32_t* parents;
-  void* out;
-  float* lse;
-  float c;                                     // scale * log2(e)
-  int Hq;
-  unsigned* counters;                          // [grid] arrivals at the item whose first part it holds
-  float* part_o;                               // [2 grid][rows][D]
-  float2* part_ml;                             // [2 grid][rows] maximum and sum
-};
 
 template <int D>
 constexpr int kStageBytes = 2 * kTile * D * 2;
@@ -57,29 +46,6 @@ constexpr int kScratchBytes = MT * 16 * D * 2 > kWarps * MT * 16 * 8 + 2 * kWarp
                                   : kWarps * MT * 16 * 8 + 2 * kWarps * 16 * 16 * 4;
 template <int D, int MT>
 constexpr int kSmemBytes = 1024 + kStageCount<D> * kStageBytes<D> + kScratchBytes<D, MT>;
-
-template <bool F16>
-__device__ __forceinline__ float value_of(uint32_t h) {
-  if (F16) return __half2float(__ushort_as_half(static_cast<unsigned short>(h)));
-  return __uint_as_float(h << 16);
-}
-
-// A register of two values with those of entries >= `total` (bit masks keep_lo, keep_hi) cleared, and
-// those that are not finite cleared and reported.
-template <bool F16>
-__device__ __forceinline__ uint32_t finite2(uint32_t x, uint32_t keep, bool& odd) {
-  constexpr uint32_t e = F16 ? 0x7c00u : 0x7f80u;
-  x &= keep;
-  if ((x & e) == e) {
-    odd = true;
-    x &= 0xffff0000u;
-  }
-  if (((x >> 16) & e) == e) {
-    odd = true;
-    x &= 0xffffu;
-  }
-  return x;
-}
 
 template <bool F16, int D, int MT>
 __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2)
@@ -108,29 +74,14 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2)
   }
   sv::make_plan<kThreads>(R, scan, &plan);
 
-  // Tokens behind a row's, and rows in error.
-  {
-    const int per = P.Hq * D / 8;
-    for (int b = blockIdx.x; b < R.B; b += gridDim.x) {
-      sv::RowWork w;
-      const bool ok = sv::row_work(R, b, &w);
-      const int i0 = ok ? w.m : 0;
-      const uint32_t v = ok ? 0u : 0x7fff7fffu;                 // NaN in both types
-      uint4* o = reinterpret_cast<uint4*>(P.out) + (static_cast<size_t>(b) * R.N + i0) * per;
-      for (int x = tid; x < (R.N - i0) * per; x += kThreads) o[x] = make_uint4(v, v, v, v);
-      if (P.lse) {
-        float* l = P.lse + (static_cast<size_t>(b) * R.N + i0) * P.Hq;
-        for (int x = tid; x < (R.N - i0) * P.Hq; x += kThreads) l[x] = ok ? 0.0f : __int_as_float(0x7fffffff);
-      }
-    }
-  }
+  sv::fill_unused(P, D, tid, kThreads);
 
   sv::Walk W;
   W.begin(R, plan);
   if (warp == kWarps) {
     // ---- Producer: page numbers are read one tile ahead of the copies that need them.
     sv::TileLoader T;
-    T.init(C, 2);
+    T.init(C, 2, kTileLog2);
     int issued = 0;
     bool gone = false;
     while (!gone && W.next(R)) {
@@ -422,69 +373,16 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2)
       continue;
     }
 
-    // An item of several CTAs: the last to arrive joins the parts.
-    const long long item_at = W.at - W.first;
-    const int c0 = sv::tile_owner(item_at, plan), c1 = sv::tile_owner(item_at + W.w.tiles - 1, plan);
-    sv::named_bar_sync(1, kConsumers);
-    if (tid == 0) {
-      __threadfence();
-      const unsigned old = atomicAdd(P.counters + c0, 1u);
-      sm_last = old == static_cast<unsigned>(c1 - c0);
-      if (sm_last) P.counters[c0] = 0u;        // left zero for the next call
-      __threadfence();
-    }
-    sv::named_bar_sync(1, kConsumers);
-    if (!sm_last) continue;
-    float* fin = reinterpret_cast<float*>(scratch_p);          // per row: maximum, 1 / sum
-    if (tid < rows) {
-      float jm = -INFINITY, jl = 0.0f;
-      for (int p = c0; p <= c1; ++p) jm = fmaxf(jm, __ldcg(P.part_ml + (2 * p + (p == c0)) * kRows + tid).x);
-      for (int p = c0; p <= c1; ++p) {
-        const float2 e = __ldcg(P.part_ml + (2 * p + (p == c0)) * kRows + tid);
-        if (e.x > -INFINITY) jl += e.y * sv::ex2((e.x - jm) * c);
-        else jl += e.y;
-      }
-      fin[2 * tid] = jm;
-      fin[2 * tid + 1] = 1.0f / jl;
-      const int i = (row0 + tid) / R.group, hq = W.head * R.group + (row0 + tid) - i * R.group;
-      if (P.lse) P.lse[(static_cast<size_t>(W.row) * R.N + i) * P.Hq + hq] = (jm * c + log2f(jl)) * 0.6931471805599453f;
-    }
-    sv::named_bar_sync(1, kConsumers);
-    for (int x = tid; x < rows * (D / 4); x += kConsumers) {
-      const int r = x / (D / 4), col = (x % (D / 4)) * 4;
-      const float jm = fin[2 * r], inv = fin[2 * r + 1];
-      float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-      for (int p = c0; p <= c1; ++p) {
-        const int sl = 2 * p + (p == c0);
-        const float pm = __ldcg(&P.part_ml[sl * kRows + r].x);
-        const float4 e = __ldcg(reinterpret_cast<const float4*>(P.part_o + (static_cast<size_t>(sl) * kRows + r) * D + col));
-        const float f = pm == -INFINITY ? 0.0f : sv::ex2((pm - jm) * c);
-        a.x += e.x * f;
-        a.y += e.y * f;
-        a.z += e.z * f;
-        a.w += e.w * f;
-      }
-      const int i = (row0 + r) / R.group, hq = W.head * R.group + (row0 + r) - i * R.group;
-      uint2 v;
-      v.x = sv::pack2<F16>(a.x * inv, a.y * inv);
-      v.y = sv::pack2<F16>(a.z * inv, a.w * inv);
-      *reinterpret_cast<uint2*>(static_cast<char*>(P.out) + (((static_cast<size_t>(W.row) * R.N + i) * P.Hq + hq) * D + col) * 2) = v;
-    }
-    sv::named_bar_sync(1, kConsumers);
+    sv::join_parts<F16, D, kRows, kConsumers>(P, W, plan, row0, rows, tid, reinterpret_cast<float*>(scratch_p), &sm_last);
   }
 }
 
-// Query rows of an item: 16 where a key head has no more, else 32 (heads of 256 keep 16: their
-// accumulators fill the registers).
-int row_tiles_of(int N, int group, int D) { return N * group <= 16 || D == 256 ? 1 : 2; }
-
-int grid_limit(int sms, int D) { return sms * (D == 256 ? 1 : 2); }
+// The kernel and the query rows of an item: 16 where a key head has no more, else 128 on the wide
+// kernel; heads of 256, whose accumulators fill the registers here and tensor memory there, take 16.
+bool is_wide(int N, int group, int D) { return N * group > 16 && D < 256; }
+int item_rows(int N, int group, int D) { return is_wide(N, group, D) ? 128 : 16; }
+int grid_limit(int sms, int N, int group, int D) { return sms * (D == 256 || is_wide(N, group, D) ? 1 : 2); }
 constexpr int kMaxSms = 160;
-
-size_t part_bytes(int grid, int MT, int D) {
-  return static_cast<size_t>(2) * grid * 16 * MT * (D * 4 + 8);
-}
 
 template <bool F16, int D, int MT>
 int launch(const AttendParams& P, const CUtensorMap& k, const CUtensorMap& v, int grid, cudaStream_t st) {
@@ -502,8 +400,9 @@ extern "C" size_t spec_verify_paged_attention_workspace_size(int32_t N, int32_t 
   if (!cache || N < 1 || N > SV_MAX_GAMMA + 1 || Hq < 1 || Hq > 1024 || cache->heads < 1 ||
       Hq % cache->heads != 0 || cache->head_dim < 1 || cache->head_dim > 256)
     return 0;
-  const int D = cache->head_dim, MT = row_tiles_of(N, Hq / cache->heads, D);
-  return SV_ATTEND_COUNTER_BYTES + (part_bytes(grid_limit(kMaxSms, D), MT, D) + 255) / 256 * 256;
+  const int D = cache->head_dim, group = Hq / cache->heads;
+  const size_t part = static_cast<size_t>(item_rows(N, group, D)) * (D * 4 + 8);
+  return SV_ATTEND_COUNTER_BYTES + (2 * grid_limit(kMaxSms, N, group, D) * part + 255) / 256 * 256;
 }
 
 extern "C" int spec_verify_paged_attention(const void* q, int64_t q_row_stride,
@@ -529,7 +428,8 @@ extern "C" int spec_verify_paged_attention(const void* q, int64_t q_row_stride,
   int dev = 0;
   st = sv::current_device_status(&dev);
   if (st != SV_OK) return st;
-  const int D = cache->head_dim, group = Hq / cache->heads, MT = row_tiles_of(N, group, D);
+  const int D = cache->head_dim, group = Hq / cache->heads, item = item_rows(N, group, D);
+  const bool wide = is_wide(N, group, D);
   CUtensorMap kmap, vmap;
   st = sv::cache_tensor_map(cache, cache->k, sv::box_rows(cache), &kmap);
   if (st == SV_OK) st = sv::cache_tensor_map(cache, cache->v, sv::box_rows(cache), &vmap);
@@ -539,7 +439,8 @@ extern "C" int spec_verify_paged_attention(const void* q, int64_t q_row_stride,
   P.R.B = B;
   P.R.N = N;
   P.R.group = group;
-  P.R.q_rows = 16 * MT;
+  P.R.q_rows = item;
+  P.R.tile_log2 = wide ? 7 : kTileLog2;
   P.R.none_ok = false;
   P.q = static_cast<const char*>(q);
   P.row_stride = q_row_stride * 2;
@@ -553,22 +454,19 @@ extern "C" int spec_verify_paged_attention(const void* q, int64_t q_row_stride,
   int sms = sv::device_sms(dev);
   if (sms < 1) return SV_ERR_CUDA;
   if (sms > kMaxSms) sms = kMaxSms;
-  const long long most = static_cast<long long>(B) * cache->heads * ((N * group + 16 * MT - 1) / (16 * MT)) *
-                         ((static_cast<long long>(cache->max_pages) * cache->page_size + kTile - 1) / kTile);
-  const int grid = static_cast<int>(most < grid_limit(sms, D) ? most : grid_limit(sms, D));
+  const long long tile = 1 << P.R.tile_log2;
+  const long long most = static_cast<long long>(B) * cache->heads * ((N * group + item - 1) / item) *
+                         ((static_cast<long long>(cache->max_pages) * cache->page_size + tile - 1) / tile);
+  const int limit = grid_limit(sms, N, group, D);
+  const int grid = static_cast<int>(most < limit ? most : limit);
   char* ws = static_cast<char*>(workspace);
   P.counters = reinterpret_cast<unsigned*>(ws);
   P.part_ml = reinterpret_cast<float2*>(ws + SV_ATTEND_COUNTER_BYTES);
-  P.part_o = reinterpret_cast<float*>(ws + SV_ATTEND_COUNTER_BYTES + static_cast<size_t>(2) * grid * 16 * MT * 8);
+  P.part_o = reinterpret_cast<float*>(ws + SV_ATTEND_COUNTER_BYTES + static_cast<size_t>(2) * grid * item * 8);
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   const bool f16 = cache->dtype == SV_DTYPE_F16;
-  if (D == 64) {
-    if (MT == 1) return f16 ? launch<true, 64, 1>(P, kmap, vmap, grid, s) : launch<false, 64, 1>(P, kmap, vmap, grid, s);
-    return f16 ? launch<true, 64, 2>(P, kmap, vmap, grid, s) : launch<false, 64, 2>(P, kmap, vmap, grid, s);
-  }
-  if (D == 128) {
-    if (MT == 1) return f16 ? launch<true, 128, 1>(P, kmap, vmap, grid, s) : launch<false, 128, 1>(P, kmap, vmap, grid, s);
-    return f16 ? launch<true, 128, 2>(P, kmap, vmap, grid, s) : launch<false, 128, 2>(P, kmap, vmap, grid, s);
-  }
+  if (wide) return sv::launch_attend_wide(P, f16, kmap, vmap, grid, s);
+  if (D == 64) return f16 ? launch<true, 64, 1>(P, kmap, vmap, grid, s) : launch<false, 64, 1>(P, kmap, vmap, grid, s);
+  if (D == 128) return f16 ? launch<true, 128, 1>(P, kmap, vmap, grid, s) : launch<false, 128, 1>(P, kmap, vmap, grid, s);
   return f16 ? launch<true, 256, 1>(P, kmap, vmap, grid, s) : launch<false, 256, 1>(P, kmap, vmap, grid, s);
 }

@@ -7,11 +7,9 @@
 
 namespace sv {
 
-constexpr int kTile = 64;                 // entries of a key tile
-
 // The round a batch is in, and how its work divides. A row's work is one item per key head and tile of
 // query rows (row r = token r / group, query head r % group of the key head's); an item is
-// ceil((n + m) / kTile) key tiles. The batch's tiles, in the order (row, head, query tile, key tile),
+// ceil((n + m) / tile) key tiles. The batch's tiles, in the order (row, head, query tile, key tile),
 // are cut into equal runs, one per CTA: no CTA gets over one tile more than another, whatever the
 // lengths are, and only the items at a run's ends are shared with another CTA.
 struct Round {
@@ -19,6 +17,7 @@ struct Round {
   const int32_t* prefix;
   const int32_t* num;
   int B, N, group, q_rows;                // q_rows: query rows of a query tile
+  int tile_log2;                          // entries of a key tile
   bool none_ok;                           // num = -1 counts as no token
 };
 
@@ -30,7 +29,7 @@ struct RowWork {
 __device__ __forceinline__ bool row_work(const Round& R, int b, RowWork* w) {
   const bool ok = round_lengths(R.C, R.prefix, R.num, b, R.N, R.none_ok, &w->n, &w->m);
   const bool some = ok && w->m > 0;
-  w->tiles = some ? (w->n + w->m + kTile - 1) / kTile : 0;
+  w->tiles = some ? (w->n + w->m + (1 << R.tile_log2) - 1) >> R.tile_log2 : 0;
   w->q_tiles = some ? (w->m * R.group + R.q_rows - 1) / R.q_rows : 0;
   return ok;
 }
@@ -151,31 +150,32 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, i
 // The page numbers of a tile's boxes for lane `lane` of the producer warp: box x of an array covers
 // `rows` entries of one page and 64 of the D elements. Lanes take (array, box, 64 elements) in order.
 struct TileLoader {
-  int boxes_log2, halves_log2, rows_log2, ops;
+  int boxes_log2, halves_log2, rows_log2, tile_log2, ops;
 
-  __device__ __forceinline__ void init(const Cache& C, int arrays) {
+  __device__ __forceinline__ void init(const Cache& C, int arrays, int log2_entries) {
+    tile_log2 = log2_entries;
     rows_log2 = C.page_log2 < 6 ? C.page_log2 : 6;
-    boxes_log2 = 6 - rows_log2;
+    boxes_log2 = tile_log2 - rows_log2;
     halves_log2 = C.head_dim == 64 ? 0 : (C.head_dim == 128 ? 1 : 2);
     ops = arrays << (boxes_log2 + halves_log2);
   }
   // Page of operation `op` of a tile: -1 when it lies behind the row's entries, -2 when out of range.
   __device__ __forceinline__ int page(const Cache& C, int row, int tile, int entries, int op) const {
     const int box = (op >> halves_log2) & ((1 << boxes_log2) - 1);
-    const int j = tile * kTile + (box << rows_log2);
+    const int j = (tile << tile_log2) + (box << rows_log2);
     if (op >= ops || j >= entries) return -1;
     const int p = cache_page(C, row, j);
     return page_ok(C, p) ? p : -2;
   }
-  // The copy of operation `op`: stage holds the arrays one after the other, each [D / 64][kTile][64].
+  // The copy of operation `op`: stage holds the arrays one after the other, each [D / 64][tile][64].
   __device__ __forceinline__ void load(const Cache& C, const CUtensorMap* k, const CUtensorMap* v,
                                        int tile, int head, int p, int op, uint32_t stage,
                                        uint32_t bar) const {
     const int half = op & ((1 << halves_log2) - 1);
     const int box = (op >> halves_log2) & ((1 << boxes_log2) - 1);
     const int array = op >> (halves_log2 + boxes_log2);
-    const int j = tile * kTile + (box << rows_log2);
-    const uint32_t dst = stage + (((array << halves_log2) + half) << 13) + (box << (rows_log2 + 7));
+    const int j = (tile << tile_log2) + (box << rows_log2);
+    const uint32_t dst = stage + (((array << halves_log2) + half) << (tile_log2 + 7)) + (box << (rows_log2 + 7));
     tma_load(dst, array ? v : k, half * 64, j & (C.page_size - 1), head, p, bar);
   }
 };
