@@ -75,6 +75,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2)
   sv::make_plan<kThreads>(R, scan, &plan);
 
   sv::fill_unused(P, D, tid, kThreads);
+  if (P.shared && tid == 0) P.shared[blockIdx.x].x = -1;
 
   sv::Walk W;
   W.begin(R, plan);
@@ -383,6 +384,8 @@ bool is_wide(int N, int group, int D) { return N * group > 16 && D < 256; }
 int item_rows(int N, int group, int D) { return is_wide(N, group, D) ? 128 : 16; }
 int grid_limit(int sms, int N, int group, int D) { return sms * (D == 256 || is_wide(N, group, D) ? 1 : 2); }
 constexpr int kMaxSms = 160;
+constexpr size_t kSharedBytes = 2 * kMaxSms * sizeof(int4);
+static_assert(2 * kMaxSms * sizeof(unsigned) <= SV_ATTEND_COUNTER_BYTES, "a counter per CTA");
 
 template <bool F16, int D, int MT>
 int launch(const AttendParams& P, const CUtensorMap& k, const CUtensorMap& v, int grid, cudaStream_t st) {
@@ -402,7 +405,7 @@ extern "C" size_t spec_verify_paged_attention_workspace_size(int32_t N, int32_t 
     return 0;
   const int D = cache->head_dim, group = Hq / cache->heads;
   const size_t part = static_cast<size_t>(item_rows(N, group, D)) * (D * 4 + 8);
-  return SV_ATTEND_COUNTER_BYTES + (2 * grid_limit(kMaxSms, N, group, D) * part + 255) / 256 * 256;
+  return SV_ATTEND_COUNTER_BYTES + kSharedBytes + (2 * grid_limit(kMaxSms, N, group, D) * part + 255) / 256 * 256;
 }
 
 extern "C" int spec_verify_paged_attention(const void* q, int64_t q_row_stride,
@@ -441,6 +444,7 @@ extern "C" int spec_verify_paged_attention(const void* q, int64_t q_row_stride,
   P.R.group = group;
   P.R.q_rows = item;
   P.R.tile_log2 = wide ? 7 : kTileLog2;
+  P.R.extra = wide ? 2 : 1;
   P.R.none_ok = false;
   P.q = static_cast<const char*>(q);
   P.row_stride = q_row_stride * 2;
@@ -461,12 +465,19 @@ extern "C" int spec_verify_paged_attention(const void* q, int64_t q_row_stride,
   const int grid = static_cast<int>(most < limit ? most : limit);
   char* ws = static_cast<char*>(workspace);
   P.counters = reinterpret_cast<unsigned*>(ws);
-  P.part_ml = reinterpret_cast<float2*>(ws + SV_ATTEND_COUNTER_BYTES);
-  P.part_o = reinterpret_cast<float*>(ws + SV_ATTEND_COUNTER_BYTES + static_cast<size_t>(2) * grid * item * 8);
+  ws += SV_ATTEND_COUNTER_BYTES;
+  // Fewer items than a quarter of the CTAs: each has many parts, which the join kernel takes.
+  const long long items = static_cast<long long>(B) * cache->heads * ((N * group + item - 1) / item);
+  P.shared = items * 4 <= grid ? reinterpret_cast<int4*>(ws) : nullptr;
+  ws += kSharedBytes;
+  P.part_ml = reinterpret_cast<float2*>(ws);
+  P.part_o = reinterpret_cast<float*>(ws + static_cast<size_t>(2) * grid * item * 8);
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   const bool f16 = cache->dtype == SV_DTYPE_F16;
-  if (wide) return sv::launch_attend_wide(P, f16, kmap, vmap, grid, s);
-  if (D == 64) return f16 ? launch<true, 64, 1>(P, kmap, vmap, grid, s) : launch<false, 64, 1>(P, kmap, vmap, grid, s);
-  if (D == 128) return f16 ? launch<true, 128, 1>(P, kmap, vmap, grid, s) : launch<false, 128, 1>(P, kmap, vmap, grid, s);
-  return f16 ? launch<true, 256, 1>(P, kmap, vmap, grid, s) : launch<false, 256, 1>(P, kmap, vmap, grid, s);
+  if (wide) st = sv::launch_attend_wide(P, f16, kmap, vmap, grid, s);
+  else if (D == 64) st = f16 ? launch<true, 64, 1>(P, kmap, vmap, grid, s) : launch<false, 64, 1>(P, kmap, vmap, grid, s);
+  else if (D == 128) st = f16 ? launch<true, 128, 1>(P, kmap, vmap, grid, s) : launch<false, 128, 1>(P, kmap, vmap, grid, s);
+  else st = f16 ? launch<true, 256, 1>(P, kmap, vmap, grid, s) : launch<false, 256, 1>(P, kmap, vmap, grid, s);
+  if (st == SV_OK && P.shared) st = sv::launch_attend_join(P, f16, item, grid, s);
+  return st;
 }

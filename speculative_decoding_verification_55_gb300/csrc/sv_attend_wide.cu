@@ -165,6 +165,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   sv::make_plan<kThreads>(R, scan, &plan);
   sv::fill_unused(P, D, tid, kThreads);
+  if (P.shared && tid == 0) P.shared[blockIdx.x].x = -1;
   fence_after();
   const uint32_t tm = sm_tm;
   volatile int* const lost = &sm_lost;
@@ -255,15 +256,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n = W.w.n, m = W.w.m, entries = n + m;
       const int row0 = W.q_tile * kRows, rows = min(kRows, m * R.group - row0);
       const char* qb = P.q + W.row * P.row_stride + static_cast<long long>(W.head) * R.group * (D * 2);
-      for (int x = tid; x < kRows * (D / 8); x += kSoft) {
-        const int r = x / (D / 8), ch = x % (D / 8);
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (r < rows) {
-          const int i = (row0 + r) / R.group, hg = (row0 + r) - i * R.group;
-          v = __ldg(reinterpret_cast<const uint4*>(qb + i * P.token_stride + hg * (D * 2)) + ch);
+      {
+        constexpr int kEach = kRows * (D / 8) / kSoft;   // all of a thread's loads in flight at once
+        uint4 v[kEach];
+#pragma unroll
+        for (int y = 0; y < kEach; ++y) {
+          const int x = y * kSoft + tid, r = x / (D / 8), ch = x % (D / 8);
+          v[y] = make_uint4(0u, 0u, 0u, 0u);
+          if (r < rows) {
+            const int i = (row0 + r) / R.group, hg = (row0 + r) - i * R.group;
+            v[y] = __ldg(reinterpret_cast<const uint4*>(qb + i * P.token_stride + hg * (D * 2)) + ch);
+          }
         }
-        const uint32_t a = sv::swizzled(qs + (ch >> 3) * (kRows * 128), r, ch & 7);
-        *reinterpret_cast<uint4*>(qs_p + (a - qs)) = v;
+#pragma unroll
+        for (int y = 0; y < kEach; ++y) {
+          const int x = y * kSoft + tid, r = x / (D / 8), ch = x % (D / 8);
+          const uint32_t a = sv::swizzled(qs + (ch >> 3) * (kRows * 128), r, ch & 7);
+          *reinterpret_cast<uint4*>(qs_p + (a - qs)) = v[y];
+        }
       }
       if (tid == 0) sm_flags = 0;
       bool bad = false;
@@ -297,21 +307,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (active) {
           // 64 scores at a time, read twice: for the maximum, then for the exponentials (all 128 at
           // once would not fit the registers).
-          const int a0 = j0 - n;               // place in the round of the tile's first entry
-          const unsigned long long seen = edge && par ? masks[tok] : 0;
+          const uint64_t see[2] = {edge ? sv::seen_bits(j0 - n, tok, par ? masks[tok] : ~0ull, par) : ~0ull,
+                                   edge ? sv::seen_bits(j0 + 64 - n, tok, par ? masks[tok] : ~0ull, par) : ~0ull};
           auto load = [&](uint32_t (&sc)[64], int y) {
             tm_load64(sc, ts + y);
             if (!edge) return;
-            if (par) {
+            const uint32_t lo = static_cast<uint32_t>(see[y >> 6]), hi = static_cast<uint32_t>(see[y >> 6] >> 32);
 #pragma unroll
-              for (int z = 0; z < 64; ++z) {
-                const int a = a0 + y + z;
-                if (!(a <= 0 || (a < m && ((seen >> ((a - 1) & 63)) & 1)))) sc[z] = 0xff800000u;
-              }
-            } else {
-#pragma unroll
-              for (int z = 0; z < 64; ++z)
-                if (a0 + y + z > tok) sc[z] = 0xff800000u;
+            for (int z = 0; z < 32; ++z) {
+              if (!((lo >> z) & 1)) sc[z] = 0xff800000u;
+              if (!((hi >> z) & 1)) sc[32 + z] = 0xff800000u;
             }
           };
           float v[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -363,20 +368,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           l += s0 + s1;
           tm_wait_store();
         }
-        if (edge && j0 + wtid >= n) {          // a value row of the round's own, or behind the last
+        if (edge) {
+          // Value rows of the round's own entries: what is not finite is cleared; rows behind the last
+          // entry are cleared whole.
           unsigned char* vb = ring_p + s * kStageBytes<D> + kTile * D * 2;
-          const bool behind = j0 + wtid >= entries;
-          for (int ch = 0; ch < D / 8; ++ch) {
-            uint4* at = reinterpret_cast<uint4*>(vb + (ch >> 3) * (kTile * 128) + wtid * 128 + (((ch & 7) ^ (wtid & 7)) << 4));
+          const int r0 = max(n - j0, 0);
+          for (int y = r0 * (D / 8) + wtid; y < kTile * (D / 8); y += 128) {
+            const int r = y / (D / 8), ch = y % (D / 8);
+            uint4* at = reinterpret_cast<uint4*>(vb + (ch >> 3) * (kTile * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
             uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (!behind) {
+            bool clear = true;
+            if (j0 + r < entries) {
+              clear = false;
               v = *at;
-              v.x = sv::finite2<F16>(v.x, ~0u, odd);
-              v.y = sv::finite2<F16>(v.y, ~0u, odd);
-              v.z = sv::finite2<F16>(v.z, ~0u, odd);
-              v.w = sv::finite2<F16>(v.w, ~0u, odd);
+              v.x = sv::finite2<F16>(v.x, ~0u, clear);
+              v.y = sv::finite2<F16>(v.y, ~0u, clear);
+              v.z = sv::finite2<F16>(v.z, ~0u, clear);
+              v.w = sv::finite2<F16>(v.w, ~0u, clear);
+              odd |= clear;
             }
-            if (behind || odd) *at = v;
+            if (clear) *at = v;
           }
         }
         if (edge) fence_async();

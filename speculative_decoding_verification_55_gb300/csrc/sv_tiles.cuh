@@ -9,15 +9,17 @@ namespace sv {
 
 // The round a batch is in, and how its work divides. A row's work is one item per key head and tile of
 // query rows (row r = token r / group, query head r % group of the key head's); an item is
-// ceil((n + m) / tile) key tiles. The batch's tiles, in the order (row, head, query tile, key tile),
-// are cut into equal runs, one per CTA: no CTA gets over one tile more than another, whatever the
-// lengths are, and only the items at a run's ends are shared with another CTA.
+// ceil((n + m) / tile) key tiles. The batch's work in units of a tile, in the order (row, head, query
+// tile, key tile), each item's tiles preceded by `extra` units for its queries and its end, is cut into
+// equal runs, one per CTA: no CTA gets over one unit more than another, whatever the lengths are, and
+// only the items at a run's ends are shared with another CTA.
 struct Round {
   Cache C;
   const int32_t* prefix;
   const int32_t* num;
   int B, N, group, q_rows;                // q_rows: query rows of a query tile
   int tile_log2;                          // entries of a key tile
+  int extra;                              // what an item costs besides its tiles, in tiles
   bool none_ok;                           // num = -1 counts as no token
 };
 
@@ -33,15 +35,15 @@ __device__ __forceinline__ bool row_work(const Round& R, int b, RowWork* w) {
   w->q_tiles = some ? (w->m * R.group + R.q_rows - 1) / R.q_rows : 0;
   return ok;
 }
-__device__ __forceinline__ long long row_tiles(const Round& R, const RowWork& w) {
-  return static_cast<long long>(w.tiles) * w.q_tiles * R.C.heads;
+__device__ __forceinline__ long long row_units(const Round& R, const RowWork& w) {
+  return static_cast<long long>(w.tiles + R.extra) * w.q_tiles * R.C.heads;
 }
 
 struct Plan {
-  long long total;                        // tiles of the batch
-  long long parts;                        // CTAs with work: each of them has a tile at least
-  long long at;                           // first tile of this CTA's run
-  long long row_at;                       // first tile of the row that holds it
+  long long total;                        // units of the batch
+  long long parts;                        // CTAs with work: each of them has a unit at least
+  long long at;                           // first unit of this CTA's run
+  long long row_at;                       // first unit of the row that holds it
   int row;
 };
 
@@ -56,7 +58,7 @@ __device__ void make_plan(const Round& R, long long (&sh)[kThreads / 32], Plan* 
   RowWork w;
   for (int b = b0; b < b1; ++b) {
     row_work(R, b, &w);
-    sum += row_tiles(R, w);
+    sum += row_units(R, w);
   }
   long long incl = sum;
 #pragma unroll
@@ -85,7 +87,7 @@ __device__ void make_plan(const Round& R, long long (&sh)[kThreads / 32], Plan* 
     long long run = before;
     for (int b = b0; b < b1; ++b) {
       row_work(R, b, &w);
-      const long long t = row_tiles(R, w);
+      const long long t = row_units(R, w);
       if (at < run + t) {
         plan->row = b;
         plan->row_at = run;
@@ -97,14 +99,14 @@ __device__ void make_plan(const Round& R, long long (&sh)[kThreads / 32], Plan* 
   __syncthreads();
 }
 
-// The CTA that holds tile t of the batch.
-__device__ __forceinline__ int tile_owner(long long t, const Plan& p) {
+// The CTA that holds unit t of the batch.
+__device__ __forceinline__ int unit_owner(long long t, const Plan& p) {
   return static_cast<int>(((t + 1) * p.parts - 1) / p.total);
 }
 
 // A walk over the items of this CTA's run: begin(), then next() while it returns true.
 struct Walk {
-  long long at, end, row_at;
+  long long at, end, row_at, item_at;     // item_at: the unit of the item's first tile
   int row, head, q_tile, first, count;    // key tiles [first, first + count) of the item
   RowWork w;
 
@@ -113,23 +115,26 @@ struct Walk {
     end = blockIdx.x < p.parts ? p.total * (blockIdx.x + 1) / p.parts : at;
     row = p.row;
     row_at = p.row_at;
-    count = 0;
     if (at < end) row_work(R, row, &w);
   }
   __device__ __forceinline__ bool next(const Round& R) {
-    at += count;
-    if (at >= end) return false;
-    while (at - row_at >= row_tiles(R, w)) {     // past this row: the next one with work
-      row_at += row_tiles(R, w);
-      ++row;
-      row_work(R, row, &w);
-    }
-    const int in_row = static_cast<int>(at - row_at), item = in_row / w.tiles;
-    first = in_row - item * w.tiles;
-    head = item / w.q_tiles;
-    q_tile = item - head * w.q_tiles;
-    const long long left = end - at;
-    count = left < w.tiles - first ? static_cast<int>(left) : w.tiles - first;
+    do {
+      if (at >= end) return false;
+      while (at - row_at >= row_units(R, w)) {     // past this row: the next one with work
+        row_at += row_units(R, w);
+        ++row;
+        row_work(R, row, &w);
+      }
+      const int per = w.tiles + R.extra;
+      const int in_row = static_cast<int>(at - row_at), item = in_row / per, in_item = in_row - item * per;
+      head = item / w.q_tiles;
+      q_tile = item - head * w.q_tiles;
+      item_at = at - in_item + R.extra;
+      const int stop = end - at < per - in_item ? in_item + static_cast<int>(end - at) : per;
+      first = in_item > R.extra ? in_item - R.extra : 0;
+      count = stop - R.extra - first;
+      at += stop - in_item;
+    } while (count <= 0);                 // the run ended before the item's first tile
     return true;
   }
 };
@@ -241,6 +246,18 @@ __device__ __forceinline__ bool tree_masks(const int32_t* parents, int m, unsign
     masks[t] = s;
   }
   return ok;
+}
+
+// Which of 64 entries a token attends, as bits: a0 is the place in the round of the first of them (below
+// 0: an entry before the round), i the token; in a tree `mask` is the token's from tree_masks.
+__device__ __forceinline__ uint64_t seen_bits(int a0, int i, unsigned long long mask, bool tree) {
+  const int all = (tree ? 0 : i) - a0 + 1;       // places up to this one are attended: token 0's, or i's
+  uint64_t s = all >= 64 ? ~0ull : (all > 0 ? (1ull << all) - 1 : 0ull);
+  if (tree) {                                    // place a >= 1 is bit a - 1 of the mask
+    if (a0 <= 0) s |= 1 - a0 < 64 ? mask << (1 - a0) : 0ull;
+    else s = a0 - 1 < 64 ? mask >> (a0 - 1) : 0ull;
+  }
+  return s;
 }
 
 }  // namespace sv
