@@ -3,19 +3,22 @@
 // run on the fifth-generation tensor cores with accumulators in tensor memory.
 //
 // One CTA per SM: a producer warp copying tiles of 128 entries from the pages, a warp whose one thread
-// issues the matrix products, and two groups of four softmax warps. An item is up to 128 query rows of
-// a key head; the groups take its tiles in turn, each with scores S [128 rows, 128 entries] and an
-// accumulator O [128 rows, D] of its own in tensor memory (2 x (128 + D) of 512 columns), a thread per
-// row. While one group computes the exponentials of its tile the tensor core multiplies the other's:
-//   S = Q K^T        Q and K from shared memory;
+// issues the matrix products, and eight softmax warps. An item is up to 128 query rows of a key head.
+// Tensor memory holds the scores S [128 rows, 128 entries] of two tiles and the accumulator
+// O [128 rows, D]: 2 x 128 + D of 512 columns.
+//   S = Q K^T        Q and K from shared memory, up to two tiles ahead;
 //   P = 2^(c S - c m) in the cache's type, written over S, with the row's sum in fp32;
 //   O += P V         P from tensor memory, V from shared memory.
-// A row's m is its running maximum up to a slack of 2^8: the accumulator is only rescaled when the
-// maximum has grown by more (probabilities up to 2^8 are as exact in both types, and the sums are
-// fp32). The groups' parts are joined at the item's end, and the parts of several CTAs as in
-// sv_attend.cu.
-// Bound: the bytes of the cache. 128 x 128 x D products take about a third of the time that a tile's
-// 4 x 128 x D bytes take from HBM, exponentials a sixth.
+// Two threads share a row, 64 entries each, and meet once a tile for its maximum. A row's m is its running
+// maximum up to a slack of 2^8: the accumulator is only rescaled when the maximum has grown by more
+// (probabilities up to 2^8 are as exact in both types, and the sums are fp32). The parts of several
+// CTAs are joined as in sv_attend.cu.
+// Bound: the bytes of the cache. The 128 x 128 x D products of a tile take about a third of the time
+// that its 4 x 128 x D bytes take from HBM. With two groups of warps on a tile each (a row a thread, two
+// accumulators, S and P sharing one buffer a group) a tile's chain of S, softmax, P V and the next S took
+// 3900 cycles, two tiles at a time; here a tile takes about 1100. Keys and values have slots of the ring
+// of their own, given back when their product is done: with one slot for both, the products waited for
+// the next keys before they gave back the last values (B = 19, 8000 entries: 172 us against XX).
 
 #include <cmath>
 
@@ -32,19 +35,29 @@ constexpr int kSoftWarps = 8, kSoft = 32 * kSoftWarps;
 constexpr int kThreads = kSoft + 64;                   // and the producer's and the products' warps
 constexpr int kProducer = kSoftWarps, kProducts = kSoftWarps + 1;
 constexpr float kSlack = 8.0f;
+constexpr int kScoreTiles = 2;                         // tiles of scores in tensor memory
+constexpr int kPieces = 8;                             // items the producer may be ahead, and one
 constexpr int kColumns = 512;                          // tensor memory columns of the CTA
 
 template <int D>
-constexpr int kStageBytes = 2 * kTile * D * 2;
+constexpr int kSlotBytes = kTile * D * 2;              // a tile's keys or its values
 template <int D>
-constexpr int kStageCount = D == 64 ? 6 : 3;
-// The queries; after them the exchange of accumulators: 16 columns of 128 rows each way, then the
-// rows' maxima and sums.
-constexpr int kExchange = 2 * 16 * kRows * 4;
+constexpr int kSlotCount = D == 64 ? 12 : 6;           // keys and values of a tile in turn
+
+// Shared memory behind the ring and the queries.
+template <int kSlots>
+struct Control {
+  unsigned long long full[kSlots], empty[kSlots], s_full[kScoreTiles], p_ready[kScoreTiles], o_full, q_full,
+      drained;
+  unsigned long long masks[sv::kMaxTreeNodes];
+  long long scan[kThreads / 32];
+  sv::Plan plan;
+  float row_max[2][2][kRows];                          // by the tile's parity and half
+  int bad[kPieces], last, flags, lost;
+  uint32_t tm;
+};
 template <int D>
-constexpr int kQueryBytes = kRows * D * 2 > kExchange + 2 * kRows * 8 ? kRows * D * 2 : kExchange + 2 * kRows * 8;
-template <int D>
-constexpr int kSmemBytes = 1024 + kStageCount<D> * kStageBytes<D> + kQueryBytes<D>;
+constexpr int kSmemBytes = kSlotCount<D> * kSlotBytes<D> + kRows * D * 2 + sizeof(Control<kSlotCount<D>>);
 
 __device__ __forceinline__ uint64_t matrix_desc(uint32_t addr, uint32_t lead, uint32_t stride) {
   // Start, leading and stride offsets in 16-byte units; version 1; 128-byte swizzle.
@@ -82,7 +95,7 @@ __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.
 
 #define SV_R8(x, o) "=r"(x[o]), "=r"(x[o + 1]), "=r"(x[o + 2]), "=r"(x[o + 3]), "=r"(x[o + 4]), "=r"(x[o + 5]), "=r"(x[o + 6]), "=r"(x[o + 7])
 #define SV_W8(x, o) "r"(x[o]), "r"(x[o + 1]), "r"(x[o + 2]), "r"(x[o + 3]), "r"(x[o + 4]), "r"(x[o + 5]), "r"(x[o + 6]), "r"(x[o + 7])
-// 16, 32 or 64 columns of this thread's lane of tensor memory, loaded when the call returns (the wait
+// 16 or 64 columns of this thread's lane of tensor memory, loaded when the call returns (the wait
 // is part of the statement, so that no use of the registers can move before it).
 __device__ __forceinline__ void tm_load64(uint32_t* r, uint32_t at) {
   asm volatile(
@@ -93,18 +106,16 @@ __device__ __forceinline__ void tm_load64(uint32_t* r, uint32_t at) {
       : SV_R8(r, 0), SV_R8(r, 8), SV_R8(r, 16), SV_R8(r, 24), SV_R8(r, 32), SV_R8(r, 40), SV_R8(r, 48), SV_R8(r, 56)
       : "r"(at) : "memory");
 }
-__device__ __forceinline__ void tm_load32(uint32_t* r, uint32_t at) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : SV_R8(r, 0), SV_R8(r, 8), SV_R8(r, 16), SV_R8(r, 24) : "r"(at) : "memory");
-}
 __device__ __forceinline__ void tm_load16(uint32_t* r, uint32_t at) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
       : SV_R8(r, 0), SV_R8(r, 8) : "r"(at) : "memory");
+}
+__device__ __forceinline__ void tm_store16(uint32_t at, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+      ::"r"(at), SV_W8(r, 0), SV_W8(r, 8) : "memory");
 }
 __device__ __forceinline__ void tm_store32(uint32_t at, const uint32_t* r) {
   asm volatile(
@@ -116,6 +127,7 @@ __device__ __forceinline__ void tm_wait_store() { asm volatile("tcgen05.wait::st
 
 // A bounded wait; the first that gives up makes every later one return at once.
 __device__ __forceinline__ bool wait_unless_lost(uint32_t bar, uint32_t parity, volatile int* lost) {
+  if (sv::mbar_try_wait(bar, parity)) return true;
   if (*lost) return false;
   if (sv::mbar_wait(bar, parity)) return true;
   *lost = 1;
@@ -126,132 +138,133 @@ template <bool F16, int D>
 __global__ void __launch_bounds__(kThreads, 1)
     sv_attend_wide_kernel(const AttendParams P, const __grid_constant__ CUtensorMap kmap,
                           const __grid_constant__ CUtensorMap vmap) {
-  constexpr int kStages = kStageCount<D>;
-  constexpr int kScores = 0, kAccum = 2 * kTile;       // columns: S0, S1, O0, O1
-  extern __shared__ unsigned char dyn[];
-  __shared__ __align__(8) unsigned long long full[kStages], empty[kStages], s_full[2], p_ready[2], o_full, q_full, drained;
-  __shared__ unsigned long long masks[sv::kMaxTreeNodes];
-  __shared__ long long scan[kThreads / 32];
-  __shared__ sv::Plan plan;
-  __shared__ int bad_stage[kStages], sm_last, sm_flags, sm_lost;
-  __shared__ uint32_t sm_tm;
+  constexpr int kSlots = kSlotCount<D>;
+  constexpr int kAccum = kScoreTiles * kTile;          // columns: S0, S1, O
+  extern __shared__ __align__(1024) unsigned char dyn[];
+  auto& S = *reinterpret_cast<Control<kSlots>*>(dyn + kSlots * kSlotBytes<D> + kRows * D * 2);
   const sv::Round& R = P.R;
   const sv::Cache& C = R.C;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t ring = (sv::smem_addr(dyn) + 1023u) & ~1023u;
-  const uint32_t qs = ring + kStages * kStageBytes<D>;
-  unsigned char* const ring_p = dyn + (ring - sv::smem_addr(dyn));
-  unsigned char* const qs_p = dyn + (qs - sv::smem_addr(dyn));
+  const uint32_t ring = sv::smem_addr(dyn), qs = ring + kSlots * kSlotBytes<D>;
+  unsigned char* const qs_p = dyn + kSlots * kSlotBytes<D>;
   if (tid == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      sv::mbar_init(sv::smem_addr(full + s), 1);
-      sv::mbar_init(sv::smem_addr(empty + s), 1);
+    for (int s = 0; s < kSlots; ++s) {
+      sv::mbar_init(sv::smem_addr(S.full + s), 1);
+      sv::mbar_init(sv::smem_addr(S.empty + s), 1);
     }
-    for (int w = 0; w < 2; ++w) {
-      sv::mbar_init(sv::smem_addr(s_full + w), 1);
-      sv::mbar_init(sv::smem_addr(p_ready + w), kSoftWarps / 2);
+    for (int w = 0; w < kScoreTiles; ++w) {
+      sv::mbar_init(sv::smem_addr(S.s_full + w), 1);
+      sv::mbar_init(sv::smem_addr(S.p_ready + w), kSoftWarps);
     }
-    sv::mbar_init(sv::smem_addr(&o_full), 1);
-    sv::mbar_init(sv::smem_addr(&drained), 1);
-    sv::mbar_init(sv::smem_addr(&q_full), kSoftWarps);
-    sm_lost = 0;
+    sv::mbar_init(sv::smem_addr(&S.o_full), 1);
+    sv::mbar_init(sv::smem_addr(&S.drained), 1);
+    sv::mbar_init(sv::smem_addr(&S.q_full), kSoftWarps);
+    S.lost = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == kProducts) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
-                 ::"r"(sv::smem_addr(&sm_tm)), "r"(static_cast<uint32_t>(kColumns)) : "memory");
+                 ::"r"(sv::smem_addr(&S.tm)), "r"(static_cast<uint32_t>(kColumns)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     fence_before();
   }
-  sv::make_plan<kThreads>(R, scan, &plan);
+  sv::make_plan<kThreads>(R, S.scan, &S.plan);
   sv::fill_unused(P, D, tid, kThreads);
   if (P.shared && tid == 0) P.shared[blockIdx.x].x = -1;
   fence_after();
-  const uint32_t tm = sm_tm;
-  volatile int* const lost = &sm_lost;
+  const uint32_t tm = S.tm;
+  volatile int* const lost = &S.lost;
 
   sv::Walk W;
-  W.begin(R, plan);
+  W.begin(R, S.plan);
   if (warp == kProducer) {
     // ---- Copies: page numbers are read one tile ahead of the copies that need them.
     sv::TileLoader T;
-    T.init(C, 2, kTileLog2);
-    int issued = 0;
-    while (!*lost && W.next(R)) {
+    T.init(C, 1, kTileLog2);
+    int armed = 0, items = 0;                  // slots (tile x: 2 x and 2 x + 1) and items so far
+    bool gone = false;
+    while (!gone && W.next(R)) {
       const int entries = W.w.n + W.w.m;
       int p = T.page(C, W.row, W.first, entries, lane);
-      for (int t = W.first; t < W.first + W.count; ++t) {
+      if (lane == 0) S.bad[items % kPieces] = 0;
+      for (int t = W.first; t < W.first + W.count && !gone; ++t) {
         const int p_next = t + 1 < W.first + W.count ? T.page(C, W.row, t + 1, entries, lane) : -1;
-        const int s = issued % kStages;
-        const uint32_t bar = sv::smem_addr(full + s);
-        if (issued >= kStages &&
-            !__all_sync(kFull, wait_unless_lost(sv::smem_addr(empty + s), (issued / kStages - 1) & 1, lost)))
-          break;
         const unsigned go = __ballot_sync(kFull, p >= 0), out = __ballot_sync(kFull, p == -2);
-        if (lane == 0) {
-          bad_stage[s] = out != 0;
-          sv::mbar_arrive_expect_tx(bar, static_cast<uint32_t>(__popc(go)) << (T.rows_log2 + 7));
+        if (lane == 0 && out) S.bad[items % kPieces] = 1;
+#pragma unroll
+        for (int array = 0; array < 2; ++array) {
+          const int e = armed, s = e % kSlots;
+          const uint32_t bar = sv::smem_addr(S.full + s);
+          if (e >= kSlots &&
+              !__all_sync(kFull, wait_unless_lost(sv::smem_addr(S.empty + s), (e / kSlots - 1) & 1, lost))) {
+            gone = true;
+            break;
+          }
+          if (lane == 0) sv::mbar_arrive_expect_tx(bar, static_cast<uint32_t>(__popc(go)) << (T.rows_log2 + 7));
+          __syncwarp();
+          if (p >= 0) T.load(C, array ? &vmap : &kmap, nullptr, t, W.head, p, lane, ring + s * kSlotBytes<D>, bar);
+          ++armed;
         }
-        __syncwarp();
-        if (p >= 0) T.load(C, &kmap, &vmap, t, W.head, p, lane, ring + s * kStageBytes<D>, bar);
-        ++issued;
         p = p_next;
       }
+      ++items;
     }
     // No copy is in flight when the CTA ends.
-    for (int x = issued < kStages ? 0 : issued - kStages; x < issued; ++x)
-      sv::mbar_wait_drain(sv::smem_addr(full + x % kStages), (x / kStages) & 1);
+    for (int e = max(0, armed - kSlots); e < armed; ++e)
+      sv::mbar_wait_drain(sv::smem_addr(S.full + e % kSlots), (e / kSlots) & 1);
   } else if (warp == kProducts) {
-    // ---- Products, by one thread: scores run two tiles ahead of the products with the values.
+    // ---- Products, by one thread: scores run three tiles ahead of the products with the values.
     if (lane == 0) {
       constexpr uint32_t ds = product_desc<F16>(kTile, false), dp = product_desc<F16>(D, true);
-      int base = 0, items = 0, ready[2] = {0, 0};
+      int base = 0, items = 0;
       auto scores = [&](int idx) {
-        const int x = base + idx, s = x % kStages, w = idx & 1;
-        if (!wait_unless_lost(sv::smem_addr(full + s), (x / kStages) & 1, lost)) return;
+        const int x = base + idx, s = (2 * x) % kSlots, w = x % kScoreTiles;
+        if (!wait_unless_lost(sv::smem_addr(S.full + s), (2 * x / kSlots) & 1, lost)) return;
         fence_after();
-        const uint32_t kb = ring + s * kStageBytes<D>;
+        const uint32_t kb = ring + s * kSlotBytes<D>;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
-          product_ss(tm + kScores + w * kTile,
+          product_ss(tm + w * kTile,
                      matrix_desc(qs + (k >> 2) * (kRows * 128) + (k & 3) * 32, 16, 1024),
                      matrix_desc(kb + (k >> 2) * (kTile * 128) + (k & 3) * 32, 16, 1024), ds, k > 0);
-        products_done(sv::smem_addr(s_full + w));
+        products_done(sv::smem_addr(S.s_full + w));
+        products_done(sv::smem_addr(S.empty + s));
       };
       while (!*lost && W.next(R)) {
-        if (!wait_unless_lost(sv::smem_addr(&q_full), items & 1, lost)) break;
+        if (!wait_unless_lost(sv::smem_addr(&S.q_full), items & 1, lost)) break;
         fence_after();
-        scores(0);
-        if (W.count > 1) scores(1);
-        for (int idx = 0; idx < W.count && !*lost; ++idx) {
-          const int x = base + idx, s = x % kStages, w = idx & 1;
-          if (!wait_unless_lost(sv::smem_addr(p_ready + w), ready[w]++ & 1, lost)) break;
+        for (int idx = 0; idx < W.count && idx < kScoreTiles; ++idx) scores(idx);
+        for (int idx = 0; idx < W.count; ++idx) {
+          const int x = base + idx, s = (2 * x + 1) % kSlots, w = x % kScoreTiles;
+          if (!wait_unless_lost(sv::smem_addr(S.full + s), ((2 * x + 1) / kSlots) & 1, lost) ||
+              !wait_unless_lost(sv::smem_addr(S.p_ready + w), (x / kScoreTiles) & 1, lost))
+            break;
           fence_after();
-          const uint32_t vb = ring + s * kStageBytes<D> + kTile * D * 2;
+          const uint32_t vb = ring + s * kSlotBytes<D>;
 #pragma unroll
           for (int k = 0; k < kTile / 16; ++k)
-            product_ts(tm + kAccum + w * D, tm + kScores + w * kTile + k * 8,
-                       matrix_desc(vb + k * 2048, kTile * 128, 1024), dp, idx > 1 || k > 0);
-          products_done(sv::smem_addr(empty + s));
-          if (idx + 2 < W.count) scores(idx + 2);
+            product_ts(tm + kAccum, tm + w * kTile + k * 8, matrix_desc(vb + k * 2048, kTile * 128, 1024), dp,
+                       idx > 0 || k > 0);
+          products_done(sv::smem_addr(S.empty + s));
+          if (idx + kScoreTiles < W.count) scores(idx + kScoreTiles);
         }
-        products_done(sv::smem_addr(&o_full));
+        products_done(sv::smem_addr(&S.o_full));
         base += W.count;
         ++items;
       }
       if (*lost) {              // products in flight end before the tensor memory is given back
-        products_done(sv::smem_addr(&drained));
-        sv::mbar_wait_drain(sv::smem_addr(&drained), 0);
+        products_done(sv::smem_addr(&S.drained));
+        sv::mbar_wait_drain(sv::smem_addr(&S.drained), 0);
       }
     }
     __syncwarp();
   } else {
     // ---- Softmax
-    const int wg = warp >> 2, wq = warp & 3, row = 32 * wq + lane, wtid = tid & 127;
+    const int half = warp >> 2, wq = warp & 3, row = 32 * wq + lane;   // half: of a tile's entries, of D
     const uint32_t lanes = static_cast<uint32_t>(32 * wq) << 16;
-    const uint32_t ts = tm + lanes + kScores + wg * kTile, to = tm + lanes + kAccum + wg * D;
+    const uint32_t to = tm + lanes + kAccum + half * (D / 2);
     const float c = P.c;
-    int base = 0, items = 0, seen_s = 0;
+    int base = 0, items = 0;
     while (W.next(R)) {
       const int n = W.w.n, m = W.w.m, entries = n + m;
       const int row0 = W.q_tile * kRows, rows = min(kRows, m * R.group - row0);
@@ -275,12 +288,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           *reinterpret_cast<uint4*>(qs_p + (a - qs)) = v[y];
         }
       }
-      if (tid == 0) sm_flags = 0;
+      if (tid == 0) S.flags = 0;
       bool bad = false;
       const int last = W.first + W.count;
       const bool tail = last * kTile > n;      // the run reaches the round's own entries
       const int32_t* par = P.parents ? P.parents + static_cast<size_t>(W.row) * R.N : nullptr;
-      if (par && tail) bad = !sv::tree_masks(par, m, masks, tid, kSoft);
+      if (par && tail) bad = !sv::tree_masks(par, m, S.masks, tid, kSoft);
       else if (par)
         for (int x = tid; x < m; x += kSoft) {
           const int p = __ldg(par + x);
@@ -289,80 +302,79 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_async();
       fence_before();
       sv::named_bar_sync(1, kSoft);
-      if (lane == 0) sv::mbar_arrive(sv::smem_addr(&q_full));
+      if (lane == 0) sv::mbar_arrive(sv::smem_addr(&S.q_full));
       const int tok = min((row0 + row) / R.group, m - 1);
       const bool active = 32 * wq < rows;      // the warp has a query row
       float mx = -INFINITY, l = 0.0f;
       bool odd = false;
 
-      for (int idx = wg; idx < W.count; idx += 2) {
-        const int x = base + idx, s = x % kStages;
-        bool go = wait_unless_lost(sv::smem_addr(s_full + wg), seen_s++ & 1, lost);
-        go = go && wait_unless_lost(sv::smem_addr(full + s), (x / kStages) & 1, lost);
-        if (!__all_sync(kFull, go)) break;
-        fence_after();
-        bad |= bad_stage[s] != 0;
+      for (int idx = 0; idx < W.count; ++idx) {
+        const int x = base + idx, s = (2 * x + 1) % kSlots, w = x % kScoreTiles;
         const int j0 = (W.first + idx) * kTile;
         const bool edge = j0 + kTile > n;      // entries of the round itself, or behind the last
+        bool go = wait_unless_lost(sv::smem_addr(S.s_full + w), (x / kScoreTiles) & 1, lost);
+        if (edge || idx + 1 == W.count)        // the values are in, and the producer has seen all pages
+          go = go && wait_unless_lost(sv::smem_addr(S.full + s), ((2 * x + 1) / kSlots) & 1, lost);
+        if (!__all_sync(kFull, go)) break;
+        fence_after();
+        if (idx + 1 == W.count) bad |= S.bad[items % kPieces] != 0;
         if (active) {
-          // 64 scores at a time, read twice: for the maximum, then for the exponentials (all 128 at
-          // once would not fit the registers).
-          const uint64_t see[2] = {edge ? sv::seen_bits(j0 - n, tok, par ? masks[tok] : ~0ull, par) : ~0ull,
-                                   edge ? sv::seen_bits(j0 + 64 - n, tok, par ? masks[tok] : ~0ull, par) : ~0ull};
-          auto load = [&](uint32_t (&sc)[64], int y) {
-            tm_load64(sc, ts + y);
-            if (!edge) return;
-            const uint32_t lo = static_cast<uint32_t>(see[y >> 6]), hi = static_cast<uint32_t>(see[y >> 6] >> 32);
+          const uint32_t ts = tm + lanes + w * kTile;
+          uint32_t sc[64];
+          tm_load64(sc, ts + 64 * half);
+          if (edge) {
+            const uint64_t see = sv::seen_bits(j0 + 64 * half - n, tok, par ? S.masks[tok] : 0ull, par);
+            const uint32_t lo = static_cast<uint32_t>(see), hi = static_cast<uint32_t>(see >> 32);
 #pragma unroll
             for (int z = 0; z < 32; ++z) {
               if (!((lo >> z) & 1)) sc[z] = 0xff800000u;
               if (!((hi >> z) & 1)) sc[32 + z] = 0xff800000u;
             }
-          };
+          }
           float v[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int y = 0; y < kTile; y += 64) {
-            uint32_t sc[64];
-            load(sc, y);
-#pragma unroll
-            for (int z = 0; z < 64; ++z) v[z & 3] = fmaxf(v[z & 3], __uint_as_float(sc[z]));
-          }
-          const float top = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+          for (int z = 0; z < 64; ++z) v[z & 3] = fmaxf(v[z & 3], __uint_as_float(sc[z]));
+          float top = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+          S.row_max[x & 1][half][row] = top;
+          fence_before();
+          sv::named_bar_sync(2 + wq, 64);      // the two warps of these rows: both have read their scores
+          fence_after();
+          top = fmaxf(top, S.row_max[x & 1][half ^ 1][row]);
           // The first tile sets the maximum; later ones move it when it has grown by over kSlack.
           const bool grew = top > mx && (mx == -INFINITY || (top - mx) * c > kSlack);
           if (__any_sync(kFull, grew)) {
             const float f = !grew ? 1.0f : (mx == -INFINITY ? 0.0f : sv::ex2((mx - top) * c));
             if (grew) mx = top;
             l *= f;
-            if (idx > 1) {                     // products with earlier tiles' values are done
+            if (idx > 0) {                     // the products with the tiles before are done
+              const int e = 2 * x - 1;
+              wait_unless_lost(sv::smem_addr(S.empty + e % kSlots), (e / kSlots) & 1, lost);
+              __syncwarp();
+              fence_after();
 #pragma unroll
-              for (int y = 0; y < D; y += 32) {
-                uint32_t o[32];
-                tm_load32(o, to + y);
+              for (int y = 0; y < D / 2; y += 16) {
+                uint32_t o[16];
+                tm_load16(o, to + y);
 #pragma unroll
-                for (int z = 0; z < 32; ++z) o[z] = __float_as_uint(__uint_as_float(o[z]) * f);
-                tm_store32(to + y, o);
+                for (int z = 0; z < 16; ++z) o[z] = __float_as_uint(__uint_as_float(o[z]) * f);
+                tm_store16(to + y, o);
               }
             }
           }
           const float b = mx == -INFINITY ? 0.0f : -mx * c;
           const sv::f32x2 c2 = sv::pk(c, c), b2 = sv::pk(b, b);
           sv::f32x2 sum[2] = {sv::pk(0.0f, 0.0f), sv::pk(0.0f, 0.0f)};
+          uint32_t p[32];
 #pragma unroll
-          for (int y = 0; y < kTile; y += 64) {
-            uint32_t sc[64], p[32];
-            load(sc, y);
-#pragma unroll
-            for (int z = 0; z < 32; ++z) {
-              float p0, p1;
-              sv::upk(sv::fma2(sv::pk(__uint_as_float(sc[2 * z]), __uint_as_float(sc[2 * z + 1])), c2, b2), p0, p1);
-              p0 = sv::ex2(p0);
-              p1 = sv::ex2(p1);
-              sum[z & 1] = sv::add2(sum[z & 1], sv::pk(p0, p1));
-              p[z] = sv::pack2<F16>(p0, p1);
-            }
-            tm_store32(ts + y / 2, p);
+          for (int z = 0; z < 32; ++z) {
+            float p0, p1;
+            sv::upk(sv::fma2(sv::pk(__uint_as_float(sc[2 * z]), __uint_as_float(sc[2 * z + 1])), c2, b2), p0, p1);
+            p0 = sv::ex2(p0);
+            p1 = sv::ex2(p1);
+            sum[z & 1] = sv::add2(sum[z & 1], sv::pk(p0, p1));
+            p[z] = sv::pack2<F16>(p0, p1);
           }
+          tm_store32(ts + 32 * half, p);
           float s0, s1;
           sv::upk(sv::add2(sum[0], sum[1]), s0, s1);
           l += s0 + s1;
@@ -371,9 +383,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (edge) {
           // Value rows of the round's own entries: what is not finite is cleared; rows behind the last
           // entry are cleared whole.
-          unsigned char* vb = ring_p + s * kStageBytes<D> + kTile * D * 2;
+          unsigned char* vb = dyn + s * kSlotBytes<D>;
           const int r0 = max(n - j0, 0);
-          for (int y = r0 * (D / 8) + wtid; y < kTile * (D / 8); y += 128) {
+          for (int y = r0 * (D / 8) + tid; y < kTile * (D / 8); y += kSoft) {
             const int r = y / (D / 8), ch = y % (D / 8);
             uint4* at = reinterpret_cast<uint4*>(vb + (ch >> 3) * (kTile * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
             uint4 v = make_uint4(0u, 0u, 0u, 0u);
@@ -393,54 +405,42 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (edge) fence_async();
         fence_before();
         __syncwarp();
-        if (lane == 0) sv::mbar_arrive(sv::smem_addr(p_ready + wg));
+        if (lane == 0) sv::mbar_arrive(sv::smem_addr(S.p_ready + w));
       }
-      wait_unless_lost(sv::smem_addr(&o_full), items & 1, lost);
+      wait_unless_lost(sv::smem_addr(&S.o_full), items & 1, lost);
+      __syncwarp();
       fence_after();
-      if (bad || *lost) atomicOr(&sm_flags, 1);
-      if (odd) atomicOr(&sm_flags, 2);
+      if (bad || *lost) atomicOr(&S.flags, 1);
+      if (odd) atomicOr(&S.flags, 2);
       base += W.count;
       ++items;
 
-      // The two groups' parts of a row: each group finishes half of the columns.
-      float2* ml = reinterpret_cast<float2*>(qs_p + kExchange);       // [2][kRows]
-      float* give = reinterpret_cast<float*>(qs_p) + wg * 16 * kRows; // [16][kRows]
-      const float* take = reinterpret_cast<const float*>(qs_p) + (wg ^ 1) * 16 * kRows;
-      sv::named_bar_sync(1, kSoft);            // the queries have been read
-      ml[wg * kRows + row] = make_float2(mx, l);
-      const int flags = sm_flags;
+      // A row's sum is that of its two threads; each finishes half of the row's columns.
+      float* sums = reinterpret_cast<float*>(qs_p);      // [2][kRows]; the queries have been read
+      sums[half * kRows + row] = l;
       sv::named_bar_sync(1, kSoft);
-      const float2 other = ml[(wg ^ 1) * kRows + row];
-      const float jm = fmaxf(mx, other.x);
-      const float mine = mx == -INFINITY ? 0.0f : sv::ex2((mx - jm) * c);
-      float jl = (mx == -INFINITY ? l : l * mine) +
-                 (other.x == -INFINITY ? other.y : other.y * sv::ex2((other.x - jm) * c));
-      if (flags & 1) jl = __int_as_float(0x7fffffff);
-      const bool any = W.count > wg;           // the group had a tile: its accumulator is set
+      const int flags = S.flags;
+      const float jl = (flags & 1) ? __int_as_float(0x7fffffff) : sums[row] + sums[kRows + row];
       const bool whole = W.count == W.w.tiles;
       const int slot = 2 * blockIdx.x + (W.first == 0 ? 1 : 0);
       const int i = (row0 + row) / R.group, hq = W.head * R.group + (row0 + row) - i * R.group;
       const size_t at = (static_cast<size_t>(W.row) * R.N + i) * P.Hq + hq;
       const float inv = 1.0f / jl;
-      for (int k = 0; k < D / 32; ++k) {
-        const int mycol = wg * (D / 2) + 16 * k, theirs = (wg ^ 1) * (D / 2) + 16 * k;
-        uint32_t g[16], o[16];
-        tm_load16(g, to + theirs);
-        tm_load16(o, to + mycol);
-#pragma unroll
-        for (int z = 0; z < 16; ++z) give[z * kRows + row] = any ? __uint_as_float(g[z]) * mine : 0.0f;
-        sv::named_bar_sync(1, kSoft);
+      if (active)
+        for (int k = 0; k < D / 2; k += 16) {
+        const int mycol = half * (D / 2) + k;
+        uint32_t o[16];
+        tm_load16(o, to + k);
         float f[16];
 #pragma unroll
-        for (int z = 0; z < 16; ++z)
-          f[z] = (any ? __uint_as_float(o[z]) * mine : 0.0f) + take[z * kRows + row];
+        for (int z = 0; z < 16; ++z) f[z] = __uint_as_float(o[z]);
         // Values that are not finite were left out of the products, where a zero probability would have
         // made NaN of them: they are added to the rows that attend them.
         if (flags & 2) {
           for (int j = max(n, W.first * kTile); j < min(entries, last * kTile); ++j) {
             const int page = sv::cache_page(C, W.row, j), a = j - n;
             if (!sv::page_ok(C, page)) continue;
-            if (!(par ? a <= 0 || ((masks[tok] >> (a - 1)) & 1) : a <= tok)) continue;
+            if (!(par ? a <= 0 || ((S.masks[tok] >> (a - 1)) & 1) : a <= tok)) continue;
             const unsigned short* v = reinterpret_cast<const unsigned short*>(C.v + sv::entry_offset(C, page, W.head, j)) + mycol;
 #pragma unroll
             for (int z = 0; z < 16; ++z) {
@@ -463,14 +463,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int z = 0; z < 4; ++z) out[z] = make_float4(f[4 * z], f[4 * z + 1], f[4 * z + 2], f[4 * z + 3]);
           }
         }
-        sv::named_bar_sync(1, kSoft);
       }
-      if (wg == 0 && row < rows) {
-        if (!whole) P.part_ml[slot * kRows + row] = make_float2(jm, jl);
-        else if (P.lse) P.lse[at] = (jm * c + log2f(jl)) * 0.6931471805599453f;
+      if (half == 0 && row < rows) {
+        if (!whole) P.part_ml[slot * kRows + row] = make_float2(mx, jl);
+        else if (P.lse) P.lse[at] = (mx * c + log2f(jl)) * 0.6931471805599453f;
       }
+      fence_before();
+      sv::named_bar_sync(1, kSoft);            // the sums have been read
       if (whole) continue;
-      sv::join_parts<F16, D, kRows, kSoft>(P, W, plan, row0, rows, tid, reinterpret_cast<float*>(qs_p), &sm_last);
+      sv::join_parts<F16, D, kRows, kSoft>(P, W, S.plan, row0, rows, tid, reinterpret_cast<float*>(qs_p), &S.last);
     }
     fence_before();
   }
