@@ -348,12 +348,10 @@ int spec_verify_kv_append(const void* k_new, const void* v_new, int64_t row_stri
  * out            [B, N, Hq, D] of the cache's dtype, contiguous; 0 for i >= m_b
  * out_lse        [B, N, Hq] fp32, contiguous; 0 for i >= m_b. May be NULL.
  * workspace      device scratch of spec_verify_paged_attention_workspace_size(...) bytes, 256-byte
- *                aligned. Its first SV_ATTEND_COUNTER_BYTES must be zero before its first use, and
- *                every call leaves them zero; one workspace serves one call at a time, of any sizes.
+ *                aligned. It needs no setup; one workspace serves one call at a time, of any sizes.
  * A row in error gets NaN in all its outputs (a bad page or tree: in those of its m_b tokens).
  * The softmax and the sums run in fp32; the probabilities are rounded to the cache's dtype for the
  * product with the values. 1 <= N <= SV_MAX_GAMMA + 1, Hq <= 1024. */
-#define SV_ATTEND_COUNTER_BYTES 4096
 size_t spec_verify_paged_attention_workspace_size(int32_t N, int32_t Hq,
                                                   const sv_paged_cache* cache);
 int spec_verify_paged_attention(const void* q, int64_t q_row_stride, int64_t q_token_stride,

@@ -15,7 +15,7 @@ from ._binding import (SV_DTYPE_BF16, SV_DTYPE_F32, SV_MAX_GAMMA, SV_OK, SpecVer
                        spec_verify_staging_size, spec_verify_staged, spec_verify_staged_h2d_bytes,
                        verify_staged)
 from ._binding import SV_DTYPE_F16  # noqa: F401
-from ._cache import (SV_ATTEND_COUNTER_BYTES, PagedCache, attend, spec_verify_kv_append,  # noqa: F401
+from ._cache import (PagedCache, attend, spec_verify_kv_append,  # noqa: F401
                      spec_verify_kv_evict, spec_verify_kv_weights, spec_verify_paged_attention,
                      spec_verify_paged_attention_workspace_size)
 from .build import LIB_PATH, build_library  # noqa: F401

@@ -10,8 +10,6 @@ import math
 from ._binding import (SV_DTYPE_BF16, SV_DTYPE_F16, SV_OK, SpecVerifyError, _on, _ptr,
                        _stream_handle, lib)
 
-SV_ATTEND_COUNTER_BYTES = 4096
-
 
 class _CacheStruct(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("weight", ctypes.c_void_p),
@@ -188,18 +186,16 @@ _attend_ws = {}
 
 
 def _attend_workspace(N, Hq, cache, stream):
-    """A workspace with zeroed counters, cached per (device, stream) and grown on demand. A call that
-    is being captured gets one of its own, zeroed by the graph: replays of two graphs may overlap."""
+    """A workspace cached per (device, stream) and grown on demand. A call that is being captured gets
+    one of its own: replays of two graphs may overlap."""
     import torch
     need = spec_verify_paged_attention_workspace_size(N, Hq, cache)
     if torch.cuda.is_current_stream_capturing():
-        ws = torch.empty(max(need, SV_ATTEND_COUNTER_BYTES), dtype=torch.uint8, device=cache.device)
-        ws[:SV_ATTEND_COUNTER_BYTES].zero_()
-        return ws
+        return torch.empty(need, dtype=torch.uint8, device=cache.device)
     key = (cache.device, _stream_handle(stream, cache.device))
     ws = _attend_ws.get(key)
     if ws is None or ws.numel() < need:
-        ws = torch.zeros(max(need, SV_ATTEND_COUNTER_BYTES), dtype=torch.uint8, device=cache.device)
+        ws = torch.empty(need, dtype=torch.uint8, device=cache.device)
         _attend_ws[key] = ws
     return ws
 

@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2)
   __shared__ unsigned long long masks[sv::kMaxTreeNodes];
   __shared__ long long scan[kThreads / 32];
   __shared__ sv::Plan plan;
-  __shared__ int sm_last, sm_flags;
+  __shared__ int sm_flags;
   const sv::Round& R = P.R;
   const sv::Cache& C = R.C;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -74,8 +74,8 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2)
   }
   sv::make_plan<kThreads>(R, scan, &plan);
 
-  sv::fill_unused(P, D, tid, kThreads);
-  if (P.shared && tid == 0) P.shared[blockIdx.x].x = -1;
+  asm volatile("griddepcontrol.launch_dependents;");   // the join kernel's CTAs, which wait for this grid's end
+  if (tid == 0) P.shared[blockIdx.x].x = -1;
 
   sv::Walk W;
   W.begin(R, plan);
@@ -107,6 +107,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2)
         p = p_next;
       }
     }
+    sv::fill_unused(P, D, lane, 32);           // while the last tiles are computed
     // No copy is in flight when the CTA ends.
     for (int x = issued < kStages ? 0 : issued - kStages; x < issued; ++x)
       sv::mbar_wait_drain(sv::smem_addr(full + x % kStages), (x / kStages) & 1);
@@ -360,8 +361,11 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2)
           }
           if (whole)
             *reinterpret_cast<uint32_t*>(static_cast<char*>(P.out) + (at * D + 16 * y + jc) * 2) = sv::pack2<F16>(s0 * inv, s1 * inv);
-          else
-            *reinterpret_cast<float2*>(P.part_o + (static_cast<size_t>(slot) * kRows + r) * D + 16 * y + jc) = make_float2(s0, s1);
+          else {
+            float* part = P.part_o + (static_cast<size_t>(slot) * D + 16 * y + jc) * kRows + r;
+            part[0] = s0;
+            part[kRows] = s1;
+          }
         }
       }
       if ((tid & 7) == 0 && r < rows) {
@@ -369,12 +373,8 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2)
         else if (P.lse) P.lse[at] = (jm * c + log2f(jl)) * 0.6931471805599453f;
       }
     }
-    if (whole) {
-      sv::named_bar_sync(1, kConsumers);       // the scratch is free for the next item's queries
-      continue;
-    }
-
-    sv::join_parts<F16, D, kRows, kConsumers>(P, W, plan, row0, rows, tid, reinterpret_cast<float*>(scratch_p), &sm_last);
+    if (!whole && tid == 0) sv::tell_shared(P, W, plan);
+    sv::named_bar_sync(1, kConsumers);         // the scratch is free for the next item's queries
   }
 }
 
@@ -385,7 +385,6 @@ int item_rows(int N, int group, int D) { return is_wide(N, group, D) ? 128 : 16;
 int grid_limit(int sms, int N, int group, int D) { return sms * (D == 256 || is_wide(N, group, D) ? 1 : 2); }
 constexpr int kMaxSms = 160;
 constexpr size_t kSharedBytes = 2 * kMaxSms * sizeof(int4);
-static_assert(2 * kMaxSms * sizeof(unsigned) <= SV_ATTEND_COUNTER_BYTES, "a counter per CTA");
 
 template <bool F16, int D, int MT>
 int launch(const AttendParams& P, const CUtensorMap& k, const CUtensorMap& v, int grid, cudaStream_t st) {
@@ -405,7 +404,7 @@ extern "C" size_t spec_verify_paged_attention_workspace_size(int32_t N, int32_t 
     return 0;
   const int D = cache->head_dim, group = Hq / cache->heads;
   const size_t part = static_cast<size_t>(item_rows(N, group, D)) * (D * 4 + 8);
-  return SV_ATTEND_COUNTER_BYTES + kSharedBytes + (2 * grid_limit(kMaxSms, N, group, D) * part + 255) / 256 * 256;
+  return kSharedBytes + (2 * grid_limit(kMaxSms, N, group, D) * part + 255) / 256 * 256;
 }
 
 extern "C" int spec_verify_paged_attention(const void* q, int64_t q_row_stride,
@@ -464,11 +463,7 @@ extern "C" int spec_verify_paged_attention(const void* q, int64_t q_row_stride,
   const int limit = grid_limit(sms, N, group, D);
   const int grid = static_cast<int>(most < limit ? most : limit);
   char* ws = static_cast<char*>(workspace);
-  P.counters = reinterpret_cast<unsigned*>(ws);
-  ws += SV_ATTEND_COUNTER_BYTES;
-  // Fewer items than a quarter of the CTAs: each has many parts, which the join kernel takes.
-  const long long items = static_cast<long long>(B) * cache->heads * ((N * group + item - 1) / item);
-  P.shared = items * 4 <= grid ? reinterpret_cast<int4*>(ws) : nullptr;
+  P.shared = reinterpret_cast<int4*>(ws);
   ws += kSharedBytes;
   P.part_ml = reinterpret_cast<float2*>(ws);
   P.part_o = reinterpret_cast<float*>(ws + static_cast<size_t>(2) * grid * item * 8);
@@ -478,6 +473,7 @@ extern "C" int spec_verify_paged_attention(const void* q, int64_t q_row_stride,
   else if (D == 64) st = f16 ? launch<true, 64, 1>(P, kmap, vmap, grid, s) : launch<false, 64, 1>(P, kmap, vmap, grid, s);
   else if (D == 128) st = f16 ? launch<true, 128, 1>(P, kmap, vmap, grid, s) : launch<false, 128, 1>(P, kmap, vmap, grid, s);
   else st = f16 ? launch<true, 256, 1>(P, kmap, vmap, grid, s) : launch<false, 256, 1>(P, kmap, vmap, grid, s);
-  if (st == SV_OK && P.shared) st = sv::launch_attend_join(P, f16, item, grid, s);
-  return st;
+  // Fewer items than a quarter of the CTAs: each has many parts.
+  const long long items = static_cast<long long>(B) * cache->heads * ((N * group + item - 1) / item);
+  return st == SV_OK ? sv::launch_attend_join(P, f16, items * 4 <= grid, grid, s) : st;
 }

@@ -1,25 +1,28 @@
-// Join of the parts of attention items that many CTAs share (few rows and heads with long caches).
+// Join of the parts of attention items that several CTAs shared.
 //
 //   out = sum_p 2^(c (m_p - M)) o_p / sum_p 2^(c (m_p - M)) l_p,  M = max_p m_p,  over an item's parts p.
 //
-// One CTA per item and group of rows: 128 threads take four columns of a row each, and four such sets
-// of threads a quarter of the parts, with eight loads in flight each. The last arrival of an item joins
-// alone otherwise (sv_attend.cuh): as fast for a few parts and one launch less, but with 76 parts
-// of 40 rows it took 30 us, this kernel 4.
+// A part is o [D][rows] and (m, l) [rows] in fp32: a lane has a row (and reads whole lines with its
+// neighbours) and 16 columns. 16 warps a CTA divide its columns and the parts among them, each with a
+// running maximum over its parts, and meet in shared memory. With few items, which then have many
+// parts, a CTA takes 16 or 32 columns and its warps a sixteenth of the parts each; otherwise all columns.
+// Every item that is not whole goes through here. Joining in the last CTA to arrive instead kept that
+// CTA 10 us (3 parts of 128 rows) to 30 us (76 parts of 40 rows); this kernel is launched ahead (its
+// CTAs wait for the attention's end) and takes 3 to 4.
 
 #include "sv_attend.cuh"
 
 namespace {
 
-constexpr int kSets = 4, kSetThreads = 128, kThreads = kSets * kSetThreads;
-constexpr int kMaxParts = 320;
+constexpr int kWarps = 16, kThreads = 32 * kWarps, kCols = 16;
 
-template <bool F16, int D>
-__global__ void __launch_bounds__(kThreads) sv_attend_join_kernel(const sv::AttendParams P, int item_rows) {
-  constexpr int kAcross = D / 4, kRowsHere = kSetThreads / kAcross;   // threads of a row; rows of the CTA
-  __shared__ float factor[kRowsHere][kMaxParts];
-  __shared__ float4 part[kSets - 1][kSetThreads];
-  __shared__ float total[kRowsHere];
+template <bool F16, int D, int kRows, int kAcross>    // kAcross: warps across the columns
+__global__ void __launch_bounds__(kThreads) sv_attend_join_kernel(const sv::AttendParams P) {
+  constexpr int kRowLanes = kRows < 32 ? kRows : 32, kColLanes = 32 / kRowLanes;
+  constexpr int kPartGroups = kWarps / kAcross, kColsHere = kAcross * kColLanes * kCols;
+  constexpr int kColBlocks = D / kColsHere;
+  __shared__ float acc[kWarps][kCols][33];
+  __shared__ float2 ml[kWarps][32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const sv::Round& R = P.R;
   const int c0 = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -27,67 +30,77 @@ __global__ void __launch_bounds__(kThreads) sv_attend_join_kernel(const sv::Atte
   if (it.x < 0) return;                                // no shared item begins in this CTA's run
   sv::RowWork w;
   sv::row_work(R, it.x, &w);
-  const int row0 = it.z * item_rows, rows = min(item_rows, w.m * R.group - row0);
-  const int r0 = blockIdx.y * kRowsHere, parts = it.w - c0 + 1;
-  if (r0 >= rows) return;
+  const int row0 = it.z * kRows, rows = min(kRows, w.m * R.group - row0);
+  const int g0 = (blockIdx.y / kColBlocks) * kRowLanes, col0 = (blockIdx.y % kColBlocks) * kColsHere;
+  if (g0 >= rows) return;
   const float c = P.c;
-  for (int x = warp; x < kRowsHere && r0 + x < rows; x += kThreads / 32) {
-    float M = -INFINITY, L = 0.0f;
-    for (int p = lane; p < parts; p += 32)
-      M = fmaxf(M, __ldcg(&P.part_ml[(2 * (c0 + p) + (p == 0)) * item_rows + r0 + x].x));
-    M = sv::warp_max(M);
-    for (int p = lane; p < parts; p += 32) {
-      const float2 e = __ldcg(P.part_ml + (2 * (c0 + p) + (p == 0)) * item_rows + r0 + x);
-      const float f = e.x > -INFINITY ? sv::ex2((e.x - M) * c) : 0.0f;
-      factor[x][p] = f;
-      L += e.x > -INFINITY ? e.y * f : e.y;            // 0, or NaN
-    }
-    L = sv::warp_sum_lane0(L);
-    if (lane == 0) {
-      total[x] = L;
-      const int i = (row0 + r0 + x) / R.group, hq = it.y * R.group + (row0 + r0 + x) - i * R.group;
-      if (P.lse) P.lse[(static_cast<size_t>(it.x) * R.N + i) * P.Hq + hq] = (M * c + log2f(L)) * 0.6931471805599453f;
-    }
-  }
-  __syncthreads();
-  const int set = tid / kSetThreads, s = tid % kSetThreads, x = s / kAcross, col = (s % kAcross) * 4;
-  float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  if (r0 + x < rows) {
-#pragma unroll 8
-    for (int p = set; p < parts; p += kSets) {
-      const float4 e = __ldcg(reinterpret_cast<const float4*>(
-          P.part_o + (static_cast<size_t>(2 * (c0 + p) + (p == 0)) * item_rows + r0 + x) * D + col));
-      const float f = factor[x][p];
-      a.x += e.x * f;
-      a.y += e.y * f;
-      a.z += e.z * f;
-      a.w += e.w * f;
-    }
-  }
-  if (set) part[set - 1][s] = a;
-  __syncthreads();
-  if (set || r0 + x >= rows) return;
+  {
+    const int r = g0 + lane % kRowLanes, pg = warp / kAcross;
+    const int col = col0 + ((warp % kAcross) * kColLanes + lane / kRowLanes) * kCols;
+    float M = -INFINITY, L = 0.0f, a[kCols];
 #pragma unroll
-  for (int y = 0; y < kSets - 1; ++y) {
-    const float4 e = part[y][s];
-    a.x += e.x;
-    a.y += e.y;
-    a.z += e.z;
-    a.w += e.w;
+    for (int x = 0; x < kCols; ++x) a[x] = 0.0f;
+#pragma unroll 2
+    for (int p = c0 + pg; p <= it.w; p += kPartGroups) {
+      const size_t part = 2 * p + (p == c0);
+      const float2 e = __ldcg(P.part_ml + part * kRows + r);
+      float o[kCols];
+#pragma unroll
+      for (int x = 0; x < kCols; ++x) o[x] = __ldcg(P.part_o + (part * D + col + x) * kRows + r);
+      const float top = fmaxf(M, e.x);
+      const float f = M == top ? 1.0f : (M == -INFINITY ? 0.0f : sv::ex2((M - top) * c));
+      const float g = e.x == -INFINITY ? 0.0f : sv::ex2((e.x - top) * c);
+      M = top;
+      L = L * f + (e.x == -INFINITY ? e.y : e.y * g);  // the former: 0, or NaN
+#pragma unroll
+      for (int x = 0; x < kCols; ++x) a[x] = a[x] * f + (g == 0.0f ? 0.0f : o[x] * g);
+    }
+#pragma unroll
+    for (int x = 0; x < kCols; ++x) acc[warp][x][lane] = a[x];
+    ml[warp][lane] = make_float2(M, L);
   }
-  const float inv = 1.0f / total[x];
-  const int i = (row0 + r0 + x) / R.group, hq = it.y * R.group + (row0 + r0 + x) - i * R.group;
-  uint2 v;
-  v.x = sv::pack2<F16>(a.x * inv, a.y * inv);
-  v.y = sv::pack2<F16>(a.z * inv, a.w * inv);
-  *reinterpret_cast<uint2*>(static_cast<char*>(P.out) + (((static_cast<size_t>(it.x) * R.N + i) * P.Hq + hq) * D + col) * 2) = v;
+  __syncthreads();
+  // kAcross columns of a row a thread.
+  constexpr int kChunks = kColsHere / kAcross;
+  const int r = tid / kChunks, first = (tid % kChunks) * kAcross;
+  if (g0 + r >= rows) return;
+  float M = -INFINITY, L = 0.0f, f[kPartGroups], v[kAcross];
+#pragma unroll
+  for (int g = 0; g < kPartGroups; ++g) M = fmaxf(M, ml[g * kAcross][r].x);
+#pragma unroll
+  for (int g = 0; g < kPartGroups; ++g) {
+    const float2 e = ml[g * kAcross][r];
+    f[g] = e.x == -INFINITY ? 0.0f : sv::ex2((e.x - M) * c);
+    L += e.x == -INFINITY ? e.y : e.y * f[g];
+  }
+  const float inv = 1.0f / L;
+  const int i = (row0 + g0 + r) / R.group, hq = it.y * R.group + (row0 + g0 + r) - i * R.group;
+  const size_t at = (static_cast<size_t>(it.x) * R.N + i) * P.Hq + hq;
+#pragma unroll
+  for (int x = 0; x < kAcross; ++x) {
+    const int col = first + x, wc = col / (kColLanes * kCols), cl = (col / kCols) % kColLanes;
+    float s = 0.0f;
+#pragma unroll
+    for (int g = 0; g < kPartGroups; ++g) s += acc[g * kAcross + wc][col % kCols][cl * kRowLanes + r] * f[g];
+    v[x] = s * inv;
+  }
+  char* out = static_cast<char*>(P.out) + (at * D + col0 + first) * 2;
+  if constexpr (kAcross == 1) {
+    if (F16) *reinterpret_cast<__half*>(out) = __float2half_rn(v[0]);
+    else *reinterpret_cast<__nv_bfloat16*>(out) = __float2bfloat16_rn(v[0]);
+  } else {
+#pragma unroll
+    for (int x = 0; x < kAcross; x += 2) reinterpret_cast<uint32_t*>(out)[x / 2] = sv::pack2<F16>(v[x], v[x + 1]);
+  }
+  if (P.lse && col0 + first == 0) P.lse[at] = (M * c + log2f(L)) * 0.6931471805599453f;
 }
 
-template <bool F16, int D>
-int launch(const sv::AttendParams& P, int item_rows, int grid, cudaStream_t st) {
-  const int most = min(item_rows, P.R.N * P.R.group), here = kSetThreads / (D / 4);
+template <bool F16, int D, int kRows, int kAcross>
+int launch2(const sv::AttendParams& P, int grid, cudaStream_t st) {
+  constexpr int kRowLanes = kRows < 32 ? kRows : 32, kColsHere = kAcross * (32 / kRowLanes) * kCols;
+  const int most = min(kRows, P.R.N * P.R.group);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, (most + here - 1) / here);
+  cfg.gridDim = dim3(grid, (most + kRowLanes - 1) / kRowLanes * (D / kColsHere));
   cfg.blockDim = dim3(kThreads);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
@@ -95,18 +108,31 @@ int launch(const sv::AttendParams& P, int item_rows, int grid, cudaStream_t st) 
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, sv_attend_join_kernel<F16, D>, P, item_rows) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, sv_attend_join_kernel<F16, D, kRows, kAcross>, P) == cudaSuccess ? SV_OK
+                                                                                                   : SV_ERR_CUDA;
+}
+
+template <bool F16, int D, int kRows>
+int launch(const sv::AttendParams& P, bool many_parts, int grid, cudaStream_t st) {
+  constexpr int kAll = D / kCols / (kRows < 32 ? 32 / kRows : 1);
+  return many_parts ? launch2<F16, D, kRows, 1>(P, grid, st) : launch2<F16, D, kRows, kAll>(P, grid, st);
 }
 
 }  // namespace
 
 namespace sv {
 
-int launch_attend_join(const AttendParams& P, bool f16, int item_rows, int grid, cudaStream_t st) {
+int launch_attend_join(const AttendParams& P, bool f16, bool many_parts, int grid, cudaStream_t st) {
+  const bool wide = P.R.q_rows == 128;
   switch (P.R.C.head_dim) {
-    case 64: return f16 ? launch<true, 64>(P, item_rows, grid, st) : launch<false, 64>(P, item_rows, grid, st);
-    case 128: return f16 ? launch<true, 128>(P, item_rows, grid, st) : launch<false, 128>(P, item_rows, grid, st);
-    default: return f16 ? launch<true, 256>(P, item_rows, grid, st) : launch<false, 256>(P, item_rows, grid, st);
+    case 64:
+      if (wide) return f16 ? launch<true, 64, 128>(P, many_parts, grid, st) : launch<false, 64, 128>(P, many_parts, grid, st);
+      return f16 ? launch<true, 64, 16>(P, many_parts, grid, st) : launch<false, 64, 16>(P, many_parts, grid, st);
+    case 128:
+      if (wide) return f16 ? launch<true, 128, 128>(P, many_parts, grid, st) : launch<false, 128, 128>(P, many_parts, grid, st);
+      return f16 ? launch<true, 128, 16>(P, many_parts, grid, st) : launch<false, 128, 16>(P, many_parts, grid, st);
+    default:
+      return f16 ? launch<true, 256, 16>(P, many_parts, grid, st) : launch<false, 256, 16>(P, many_parts, grid, st);
   }
 }
 

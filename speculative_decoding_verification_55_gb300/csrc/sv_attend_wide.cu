@@ -53,7 +53,7 @@ struct Control {
   long long scan[kThreads / 32];
   sv::Plan plan;
   float row_max[2][2][kRows];                          // by the tile's parity and half
-  int bad[kPieces], last, flags, lost;
+  int bad[kPieces], flags, lost;
   uint32_t tm;
 };
 template <int D>
@@ -169,8 +169,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_before();
   }
   sv::make_plan<kThreads>(R, S.scan, &S.plan);
-  sv::fill_unused(P, D, tid, kThreads);
-  if (P.shared && tid == 0) P.shared[blockIdx.x].x = -1;
+  asm volatile("griddepcontrol.launch_dependents;");   // the join kernel's CTAs, which wait for this grid's end
+  if (tid == 0) P.shared[blockIdx.x].x = -1;
   fence_after();
   const uint32_t tm = S.tm;
   volatile int* const lost = &S.lost;
@@ -209,6 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ++items;
     }
+    sv::fill_unused(P, D, lane, 32);           // while the last tiles are computed
     // No copy is in flight when the CTA ends.
     for (int e = max(0, armed - kSlots); e < armed; ++e)
       sv::mbar_wait_drain(sv::smem_addr(S.full + e % kSlots), (e / kSlots) & 1);
@@ -265,44 +266,43 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t to = tm + lanes + kAccum + half * (D / 2);
     const float c = P.c;
     int base = 0, items = 0;
-    while (W.next(R)) {
+    // An item's queries, copied once the score products of the item before are done.
+    auto copy_q = [&](const sv::Walk& I) {
+      const int r0 = I.q_tile * kRows, nr = min(kRows, I.w.m * R.group - r0);
+      const char* qb = P.q + I.row * P.row_stride + static_cast<long long>(I.head) * R.group * (D * 2);
+#pragma unroll
+      for (int y = 0; y < kRows * (D / 8) / kSoft; ++y) {
+        const int x = y * kSoft + tid, r = x / (D / 8), ch = x % (D / 8);
+        const int rr = r0 + min(r, nr - 1), i = rr / R.group, hg = rr - i * R.group;
+        const char* from = qb + i * P.token_stride + hg * (D * 2) + ch * 16;
+        const uint32_t to = sv::swizzled(qs + (ch >> 3) * (kRows * 128), r, ch & 7), bytes = r < nr ? 16u : 0u;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+      }
+    };
+    auto queries_in = [&]() {
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      fence_async();
+    };
+    bool have = W.next(R);
+    if (have) {
+      copy_q(W);
+      queries_in();
+      sv::named_bar_sync(1, kSoft);
+      if (lane == 0) sv::mbar_arrive(sv::smem_addr(&S.q_full));
+    }
+    while (have) {
+      sv::Walk next = W;
+      const bool more = next.next(R);
       const int n = W.w.n, m = W.w.m, entries = n + m;
       const int row0 = W.q_tile * kRows, rows = min(kRows, m * R.group - row0);
-      const char* qb = P.q + W.row * P.row_stride + static_cast<long long>(W.head) * R.group * (D * 2);
-      {
-        constexpr int kEach = kRows * (D / 8) / kSoft;   // all of a thread's loads in flight at once
-        uint4 v[kEach];
-#pragma unroll
-        for (int y = 0; y < kEach; ++y) {
-          const int x = y * kSoft + tid, r = x / (D / 8), ch = x % (D / 8);
-          v[y] = make_uint4(0u, 0u, 0u, 0u);
-          if (r < rows) {
-            const int i = (row0 + r) / R.group, hg = (row0 + r) - i * R.group;
-            v[y] = __ldg(reinterpret_cast<const uint4*>(qb + i * P.token_stride + hg * (D * 2)) + ch);
-          }
-        }
-#pragma unroll
-        for (int y = 0; y < kEach; ++y) {
-          const int x = y * kSoft + tid, r = x / (D / 8), ch = x % (D / 8);
-          const uint32_t a = sv::swizzled(qs + (ch >> 3) * (kRows * 128), r, ch & 7);
-          *reinterpret_cast<uint4*>(qs_p + (a - qs)) = v[y];
-        }
-      }
       if (tid == 0) S.flags = 0;
       bool bad = false;
       const int last = W.first + W.count;
-      const bool tail = last * kTile > n;      // the run reaches the round's own entries
       const int32_t* par = P.parents ? P.parents + static_cast<size_t>(W.row) * R.N : nullptr;
-      if (par && tail) bad = !sv::tree_masks(par, m, S.masks, tid, kSoft);
-      else if (par)
-        for (int x = tid; x < m; x += kSoft) {
-          const int p = __ldg(par + x);
-          bad |= x == 0 ? p != -1 : (p < 0 || p >= x);
-        }
-      fence_async();
-      fence_before();
-      sv::named_bar_sync(1, kSoft);
-      if (lane == 0) sv::mbar_arrive(sv::smem_addr(&S.q_full));
+      if (par) {
+        bad = !sv::tree_masks(par, m, S.masks, tid, kSoft);
+        sv::named_bar_sync(1, kSoft);
+      }
       const int tok = min((row0 + row) / R.group, m - 1);
       const bool active = 32 * wq < rows;      // the warp has a query row
       float mx = -INFINITY, l = 0.0f;
@@ -410,15 +410,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       wait_unless_lost(sv::smem_addr(&S.o_full), items & 1, lost);
       __syncwarp();
       fence_after();
+      if (more) copy_q(next);
       if (bad || *lost) atomicOr(&S.flags, 1);
       if (odd) atomicOr(&S.flags, 2);
       base += W.count;
       ++items;
 
       // A row's sum is that of its two threads; each finishes half of the row's columns.
-      float* sums = reinterpret_cast<float*>(qs_p);      // [2][kRows]; the queries have been read
+      float* sums = &S.row_max[0][0][0];       // [2][kRows]; the tiles are done with it
       sums[half * kRows + row] = l;
+      if (more) queries_in();
       sv::named_bar_sync(1, kSoft);
+      // The next item's score products may begin: they write scores, not the accumulator.
+      if (more && lane == 0) sv::mbar_arrive(sv::smem_addr(&S.q_full));
       const int flags = S.flags;
       const float jl = (flags & 1) ? __int_as_float(0x7fffffff) : sums[row] + sums[kRows + row];
       const bool whole = W.count == W.w.tiles;
@@ -426,8 +430,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int i = (row0 + row) / R.group, hq = W.head * R.group + (row0 + row) - i * R.group;
       const size_t at = (static_cast<size_t>(W.row) * R.N + i) * P.Hq + hq;
       const float inv = 1.0f / jl;
-      if (active)
-        for (int k = 0; k < D / 2; k += 16) {
+#pragma unroll
+      for (int k = 0; k < D / 2; k += 16) {
+        if (!active) break;
         const int mycol = half * (D / 2) + k;
         uint32_t o[16];
         tm_load16(o, to + k);
@@ -458,9 +463,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             out[0] = make_uint4(p[0], p[1], p[2], p[3]);
             out[1] = make_uint4(p[4], p[5], p[6], p[7]);
           } else {
-            float4* out = reinterpret_cast<float4*>(P.part_o + (static_cast<size_t>(slot) * kRows + row) * D + mycol);
+            float* out = P.part_o + (static_cast<size_t>(slot) * D + mycol) * kRows + row;
 #pragma unroll
-            for (int z = 0; z < 4; ++z) out[z] = make_float4(f[4 * z], f[4 * z + 1], f[4 * z + 2], f[4 * z + 3]);
+            for (int z = 0; z < 16; ++z) out[z * kRows] = f[z];
           }
         }
       }
@@ -470,8 +475,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       fence_before();
       sv::named_bar_sync(1, kSoft);            // the sums have been read
-      if (whole) continue;
-      sv::join_parts<F16, D, kRows, kSoft>(P, W, S.plan, row0, rows, tid, reinterpret_cast<float*>(qs_p), &S.last);
+      if (!whole && tid == 0) sv::tell_shared(P, W, S.plan);
+      W = next;
+      have = more;
     }
     fence_before();
   }

@@ -172,9 +172,8 @@ def test_argument_refusals(L):
 
 
 def test_workspace_size(L):
-    import speculative_decoding_verification_55_gb300 as sv
     f = L.spec_verify_paged_attention_workspace_size
-    assert f(9, 32, ctypes.byref(cache_struct())) >= sv.SV_ATTEND_COUNTER_BYTES
+    assert f(9, 32, ctypes.byref(cache_struct())) >= 2 * 9 * 4 * 128 * 4
     assert f(0, 32, ctypes.byref(cache_struct())) == 0
     assert f(9, 30, ctypes.byref(cache_struct())) == 0
     assert f(9, 32, None) == 0
@@ -662,22 +661,22 @@ def test_gpu_captured_and_streams(sv):
 
 
 @pytest.mark.gpu
-def test_gpu_workspace_left_ready(sv):
-    """Calls of several sizes on one workspace: its counters are zero after each."""
+def test_gpu_workspace_of_any_contents(sv):
+    """Calls of several sizes on one workspace that holds anything: the same results."""
     ws = None
     for prefix, N, H, G, D in (((900, 3), 1, 1, 2, 64), ((2000, 1000, 7), 9, 4, 8, 128), ((300,) * 40, 1, 2, 4, 256),
                                ((64,), 65, 1, 4, 128)):
         a = Batch(prefix, N, H, G, D, 16, seed=N)
         c = a.cache(sv)
         if ws is None:
-            ws = torch.zeros(1 << 28, dtype=torch.uint8, device="cuda")
+            ws = torch.full((1 << 28,), 255, dtype=torch.uint8, device="cuda")
         assert sv.spec_verify_paged_attention_workspace_size(N, H * G, c) <= ws.numel()
         B = len(prefix)
         out = torch.empty((B, N, H * G, D), dtype=a.t, device="cuda")
         lse = torch.empty((B, N, H * G), device="cuda")
         sv.spec_verify_paged_attention(a.q, c, dev(a.prefix), None, None, out, lse, ws)
         check_attention(a, out, lse, a.prefix, np.full(B, N), None)
-        assert int(ws[:sv.SV_ATTEND_COUNTER_BYTES].sum()) == 0
+        ws.random_(0, 256)
         out2 = torch.empty_like(out)
         sv.spec_verify_paged_attention(a.q, c, dev(a.prefix), None, None, out2, None, ws)
         assert torch.equal(out, out2)
