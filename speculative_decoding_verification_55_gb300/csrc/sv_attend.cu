@@ -373,15 +373,17 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2)
         else if (P.lse) P.lse[at] = (jm * c + log2f(jl)) * 0.6931471805599453f;
       }
     }
-    if (!whole && tid == 0) sv::tell_shared(P, W, plan);
+    if (!whole && tid == 0 && W.first == 0) sv::tell_shared(P, W.row, W.head, W.q_tile, W.item_at, W.w.tiles, plan);
     sv::named_bar_sync(1, kConsumers);         // the scratch is free for the next item's queries
   }
 }
 
-// The kernel and the query rows of an item: 16 where a key head has no more, else 128 on the wide
-// kernel; heads of 256, whose accumulators fill the registers here and tensor memory there, take 16.
-bool is_wide(int N, int group, int D) { return N * group > 16 && D < 256; }
-int item_rows(int N, int group, int D) { return is_wide(N, group, D) ? 128 : 16; }
+// The kernel and the query rows of an item: 16 where a key head has no more, else up to 128, whole tokens,
+// on the wide kernel; heads of 256, whose accumulators fill the registers here and tensor memory there,
+// and more than 128 query heads a key head take 16.
+bool is_wide(int N, int group, int D) { return N * group > 16 && D < 256 && group <= 128; }
+int item_rows(int N, int group, int D) { return is_wide(N, group, D) ? 128 / group * group : 16; }
+int part_rows(int N, int group, int D) { return is_wide(N, group, D) ? 128 : 16; }
 int grid_limit(int sms, int N, int group, int D) { return sms * (D == 256 || is_wide(N, group, D) ? 1 : 2); }
 constexpr int kMaxSms = 160;
 constexpr size_t kSharedBytes = 2 * kMaxSms * sizeof(int4);
@@ -403,7 +405,7 @@ extern "C" size_t spec_verify_paged_attention_workspace_size(int32_t N, int32_t 
       Hq % cache->heads != 0 || cache->head_dim < 1 || cache->head_dim > 256)
     return 0;
   const int D = cache->head_dim, group = Hq / cache->heads;
-  const size_t part = static_cast<size_t>(item_rows(N, group, D)) * (D * 4 + 8);
+  const size_t part = static_cast<size_t>(part_rows(N, group, D)) * (D * 4 + 8);
   return kSharedBytes + (2 * grid_limit(kMaxSms, N, group, D) * part + 255) / 256 * 256;
 }
 
@@ -466,14 +468,20 @@ extern "C" int spec_verify_paged_attention(const void* q, int64_t q_row_stride,
   P.shared = reinterpret_cast<int4*>(ws);
   ws += kSharedBytes;
   P.part_ml = reinterpret_cast<float2*>(ws);
-  P.part_o = reinterpret_cast<float*>(ws + static_cast<size_t>(2) * grid * item * 8);
+  P.part_o = reinterpret_cast<float*>(ws + static_cast<size_t>(2) * grid * part_rows(N, group, D) * 8);
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   const bool f16 = cache->dtype == SV_DTYPE_F16;
-  if (wide) st = sv::launch_attend_wide(P, f16, kmap, vmap, grid, s);
+  if (wide) {
+    CUtensorMap qmap;
+    const int tokens = item / group < N ? item / group : N;
+    st = sv::query_tensor_map(q, q_row_stride, q_token_stride, B, N, Hq, D, cache->dtype, group, tokens, &qmap);
+    if (st != SV_OK) return st;
+    st = sv::launch_attend_wide(P, f16, kmap, vmap, qmap, tokens, grid, s);
+  }
   else if (D == 64) st = f16 ? launch<true, 64, 1>(P, kmap, vmap, grid, s) : launch<false, 64, 1>(P, kmap, vmap, grid, s);
   else if (D == 128) st = f16 ? launch<true, 128, 1>(P, kmap, vmap, grid, s) : launch<false, 128, 1>(P, kmap, vmap, grid, s);
   else st = f16 ? launch<true, 256, 1>(P, kmap, vmap, grid, s) : launch<false, 256, 1>(P, kmap, vmap, grid, s);
   // Fewer items than a quarter of the CTAs: each has many parts.
   const long long items = static_cast<long long>(B) * cache->heads * ((N * group + item - 1) / item);
-  return st == SV_OK ? sv::launch_attend_join(P, f16, items * 4 <= grid, grid, s) : st;
+  return st == SV_OK ? sv::launch_attend_join(P, f16, wide, items * 4 <= grid, grid, s) : st;
 }

@@ -64,16 +64,17 @@ __device__ __forceinline__ void fill_unused(const AttendParams& P, int D, int ti
 }
 
 // The item that this CTA begins and does not end, for the join kernel (one thread).
-__device__ __forceinline__ void tell_shared(const AttendParams& P, const Walk& W, const Plan& plan) {
-  if (W.first == 0)
-    P.shared[blockIdx.x] = make_int4(W.row, W.head, W.q_tile, unit_owner(W.item_at + W.w.tiles - 1, plan));
+__device__ __forceinline__ void tell_shared(const AttendParams& P, int row, int head, int q_tile,
+                                            long long item_at, int tiles, const Plan& plan) {
+  P.shared[blockIdx.x] = make_int4(row, head, q_tile, unit_owner(item_at + tiles - 1, plan));
 }
 
 // Joins the parts of the items that the attention kernel's `grid` CTAs shared.
-int launch_attend_join(const AttendParams& P, bool f16, bool many_parts, int grid, cudaStream_t st);
+int launch_attend_join(const AttendParams& P, bool f16, bool wide, bool many_parts, int grid, cudaStream_t st);
 
-// The wide kernel (64 or 128 elements a head; query rows and tiles of 128).
-int launch_attend_wide(const AttendParams& P, bool f16, const CUtensorMap& k, const CUtensorMap& v, int grid,
-                       cudaStream_t st);
+// The wide kernel (64 or 128 elements a head, at most 128 query heads a key head; query tiles of
+// q_rows <= 128 rows, whole tokens of which q's boxes hold q_tokens; key tiles of 128).
+int launch_attend_wide(const AttendParams& P, bool f16, const CUtensorMap& k, const CUtensorMap& v,
+                       const CUtensorMap& q, int q_tokens, int grid, cudaStream_t st);
 
 }  // namespace sv

@@ -30,7 +30,7 @@ __global__ void __launch_bounds__(kThreads) sv_attend_join_kernel(const sv::Atte
   if (it.x < 0) return;                                // no shared item begins in this CTA's run
   sv::RowWork w;
   sv::row_work(R, it.x, &w);
-  const int row0 = it.z * kRows, rows = min(kRows, w.m * R.group - row0);
+  const int row0 = it.z * R.q_rows, rows = min(R.q_rows, w.m * R.group - row0);
   const int g0 = (blockIdx.y / kColBlocks) * kRowLanes, col0 = (blockIdx.y % kColBlocks) * kColsHere;
   if (g0 >= rows) return;
   const float c = P.c;
@@ -122,8 +122,8 @@ int launch(const sv::AttendParams& P, bool many_parts, int grid, cudaStream_t st
 
 namespace sv {
 
-int launch_attend_join(const AttendParams& P, bool f16, bool many_parts, int grid, cudaStream_t st) {
-  const bool wide = P.R.q_rows == 128;
+int launch_attend_join(const AttendParams& P, bool f16, bool wide, bool many_parts, int grid,
+                       cudaStream_t st) {
   switch (P.R.C.head_dim) {
     case 64:
       if (wide) return f16 ? launch<true, 64, 128>(P, many_parts, grid, st) : launch<false, 64, 128>(P, many_parts, grid, st);

@@ -3,7 +3,8 @@
 // run on the fifth-generation tensor cores with accumulators in tensor memory.
 //
 // One CTA per SM: a producer warp copying tiles of 128 entries from the pages, a warp whose one thread
-// issues the matrix products, and eight softmax warps. An item is up to 128 query rows of a key head.
+// issues the matrix products, a warp that copies an item's queries and tells the others what the item is,
+// and eight softmax warps. An item is up to 128 query rows of a key head.
 // Tensor memory holds the scores S [128 rows, 128 entries] of two tiles and the accumulator
 // O [128 rows, D]: 2 x 128 + D of 512 columns.
 //   S = Q K^T        Q and K from shared memory, up to two tiles ahead;
@@ -32,11 +33,11 @@ using sv::kFull;
 constexpr int kTileLog2 = 7, kTile = 1 << kTileLog2;   // entries of a key tile
 constexpr int kRows = 128;                             // query rows of an item
 constexpr int kSoftWarps = 8, kSoft = 32 * kSoftWarps;
-constexpr int kThreads = kSoft + 64;                   // and the producer's and the products' warps
-constexpr int kProducer = kSoftWarps, kProducts = kSoftWarps + 1;
+constexpr int kThreads = kSoft + 96;                   // and the producer's, the products' and the items' warps
+constexpr int kProducer = kSoftWarps, kProducts = kSoftWarps + 1, kItems = kSoftWarps + 2;
 constexpr float kSlack = 8.0f;
 constexpr int kScoreTiles = 2;                         // tiles of scores in tensor memory
-constexpr int kPieces = 8;                             // items the producer may be ahead, and one
+constexpr int kPieces = 8;                             // items that the warps may be apart, and one
 constexpr int kColumns = 512;                          // tensor memory columns of the CTA
 
 template <int D>
@@ -44,14 +45,22 @@ constexpr int kSlotBytes = kTile * D * 2;              // a tile's keys or its v
 template <int D>
 constexpr int kSlotCount = D == 64 ? 12 : 6;           // keys and values of a tile in turn
 
+// An item, or a CTA's part of one, as the items' warp found it: read from shared memory by the others, so
+// that none of them waits for lengths from global memory (2 us a load while the cache streams).
+struct Item {
+  int row, head, q_tile, first, count;                 // count 0: the end
+  int n, m, tiles, bad;                                // bad: the row's tree is not valid
+  long long item_at;
+};
+
 // Shared memory behind the ring and the queries.
 template <int kSlots>
 struct Control {
   unsigned long long full[kSlots], empty[kSlots], s_full[kScoreTiles], p_ready[kScoreTiles], o_full, q_full,
-      drained;
-  unsigned long long masks[sv::kMaxTreeNodes];
+      q_empty, told[kPieces], drained;
   long long scan[kThreads / 32];
   sv::Plan plan;
+  Item items[kPieces];
   float row_max[2][2][kRows];                          // by the tile's parity and half
   int bad[kPieces], flags, lost;
   uint32_t tm;
@@ -137,7 +146,8 @@ __device__ __forceinline__ bool wait_unless_lost(uint32_t bar, uint32_t parity, 
 template <bool F16, int D>
 __global__ void __launch_bounds__(kThreads, 1)
     sv_attend_wide_kernel(const AttendParams P, const __grid_constant__ CUtensorMap kmap,
-                          const __grid_constant__ CUtensorMap vmap) {
+                          const __grid_constant__ CUtensorMap vmap,
+                          const __grid_constant__ CUtensorMap qmap, int q_tokens) {
   constexpr int kSlots = kSlotCount<D>;
   constexpr int kAccum = kScoreTiles * kTile;          // columns: S0, S1, O
   extern __shared__ __align__(1024) unsigned char dyn[];
@@ -158,7 +168,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     sv::mbar_init(sv::smem_addr(&S.o_full), 1);
     sv::mbar_init(sv::smem_addr(&S.drained), 1);
-    sv::mbar_init(sv::smem_addr(&S.q_full), kSoftWarps);
+    sv::mbar_init(sv::smem_addr(&S.q_full), 1);
+    sv::mbar_init(sv::smem_addr(&S.q_empty), 1);
+    for (int x = 0; x < kPieces; ++x) sv::mbar_init(sv::smem_addr(S.told + x), 1);
     S.lost = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -175,9 +187,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tm = S.tm;
   volatile int* const lost = &S.lost;
 
-  sv::Walk W;
-  W.begin(R, S.plan);
+  // The next item's description.
+  auto told = [&](int k) {
+    Item I;
+    if (wait_unless_lost(sv::smem_addr(S.told + k % kPieces), (k / kPieces) & 1, lost)) I = S.items[k % kPieces];
+    else I.count = 0;
+    return I;
+  };
   if (warp == kProducer) {
+    sv::Walk W;
+    W.begin(R, S.plan);
     // ---- Copies: page numbers are read one tile ahead of the copies that need them.
     sv::TileLoader T;
     T.init(C, 1, kTileLog2);
@@ -231,11 +250,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         products_done(sv::smem_addr(S.s_full + w));
         products_done(sv::smem_addr(S.empty + s));
       };
-      while (!*lost && W.next(R)) {
-        if (!wait_unless_lost(sv::smem_addr(&S.q_full), items & 1, lost)) break;
+      for (;;) {
+        const int count = told(items).count;
+        if (count == 0 || !wait_unless_lost(sv::smem_addr(&S.q_full), items & 1, lost)) break;
         fence_after();
-        for (int idx = 0; idx < W.count && idx < kScoreTiles; ++idx) scores(idx);
-        for (int idx = 0; idx < W.count; ++idx) {
+        for (int idx = 0; idx < count && idx < kScoreTiles; ++idx) scores(idx);
+        if (count <= kScoreTiles) products_done(sv::smem_addr(&S.q_empty));
+        for (int idx = 0; idx < count; ++idx) {
           const int x = base + idx, s = (2 * x + 1) % kSlots, w = x % kScoreTiles;
           if (!wait_unless_lost(sv::smem_addr(S.full + s), ((2 * x + 1) / kSlots) & 1, lost) ||
               !wait_unless_lost(sv::smem_addr(S.p_ready + w), (x / kScoreTiles) & 1, lost))
@@ -247,10 +268,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             product_ts(tm + kAccum, tm + w * kTile + k * 8, matrix_desc(vb + k * 2048, kTile * 128, 1024), dp,
                        idx > 0 || k > 0);
           products_done(sv::smem_addr(S.empty + s));
-          if (idx + kScoreTiles < W.count) scores(idx + kScoreTiles);
+          if (idx + kScoreTiles < count) {
+            scores(idx + kScoreTiles);
+            if (idx + kScoreTiles + 1 == count) products_done(sv::smem_addr(&S.q_empty));
+          }
         }
         products_done(sv::smem_addr(&S.o_full));
-        base += W.count;
+        base += count;
         ++items;
       }
       if (*lost) {              // products in flight end before the tensor memory is given back
@@ -259,6 +283,36 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
+  } else if (warp == kItems) {
+    // ---- Items: the next one's description, then, the score products of the one before being done, its
+    // queries: q_tokens tokens of the key head's query heads as rows.
+    sv::Walk W;
+    W.begin(R, S.plan);
+    for (int k = 0;; ++k) {
+      const bool more = W.next(R);
+      bool bad = false;
+      if (more && P.parents)
+        for (int t = lane; t < W.w.m; t += 32) {
+          const int p = __ldg(P.parents + static_cast<size_t>(W.row) * R.N + t);
+          bad |= t == 0 ? p != -1 : (p < 0 || p >= t);
+        }
+      bad = __any_sync(kFull, bad);
+      if (lane == 0) {
+        S.items[k % kPieces] = Item{W.row, W.head, W.q_tile, W.first, more ? W.count : 0, W.w.n, W.w.m, W.w.tiles,
+                                    bad ? 1 : 0, W.item_at};
+        sv::mbar_arrive(sv::smem_addr(S.told + k % kPieces));
+      }
+      if (!more || !__all_sync(kFull, k == 0 || wait_unless_lost(sv::smem_addr(&S.q_empty), (k - 1) & 1, lost))) {
+        if (k > 0) sv::mbar_wait_drain(sv::smem_addr(&S.q_full), (k - 1) & 1);   // the last queries are in
+        break;
+      }
+      if (lane == 0) {
+        sv::mbar_arrive_expect_tx(sv::smem_addr(&S.q_full), q_tokens * R.group * D * 2);
+        for (int half = 0; half < D / 64; ++half)
+          sv::tma_load(qs + half * (kRows * 128), &qmap, half * 64, W.head * R.group, W.q_tile * (R.q_rows / R.group),
+                       W.row, sv::smem_addr(&S.q_full));
+      }
+    }
   } else {
     // ---- Softmax
     const int half = warp >> 2, wq = warp & 3, row = 32 * wq + lane;   // half: of a tile's entries, of D
@@ -266,45 +320,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t to = tm + lanes + kAccum + half * (D / 2);
     const float c = P.c;
     int base = 0, items = 0;
-    // An item's queries, copied once the score products of the item before are done.
-    auto copy_q = [&](const sv::Walk& I) {
-      const int r0 = I.q_tile * kRows, nr = min(kRows, I.w.m * R.group - r0);
-      const char* qb = P.q + I.row * P.row_stride + static_cast<long long>(I.head) * R.group * (D * 2);
-#pragma unroll
-      for (int y = 0; y < kRows * (D / 8) / kSoft; ++y) {
-        const int x = y * kSoft + tid, r = x / (D / 8), ch = x % (D / 8);
-        const int rr = r0 + min(r, nr - 1), i = rr / R.group, hg = rr - i * R.group;
-        const char* from = qb + i * P.token_stride + hg * (D * 2) + ch * 16;
-        const uint32_t to = sv::swizzled(qs + (ch >> 3) * (kRows * 128), r, ch & 7), bytes = r < nr ? 16u : 0u;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
-      }
-    };
-    auto queries_in = [&]() {
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      fence_async();
-    };
-    bool have = W.next(R);
-    if (have) {
-      copy_q(W);
-      queries_in();
-      sv::named_bar_sync(1, kSoft);
-      if (lane == 0) sv::mbar_arrive(sv::smem_addr(&S.q_full));
-    }
-    while (have) {
-      sv::Walk next = W;
-      const bool more = next.next(R);
-      const int n = W.w.n, m = W.w.m, entries = n + m;
-      const int row0 = W.q_tile * kRows, rows = min(kRows, m * R.group - row0);
-      if (tid == 0) S.flags = 0;
-      bool bad = false;
+    for (;;) {
+      const Item W = told(items);
+      if (W.count == 0) break;
+      const int n = W.n, m = W.m, entries = n + m;
+      const int row0 = W.q_tile * R.q_rows, rows = min(R.q_rows, m * R.group - row0);
+      if (tid == 0) S.flags = 0;                // nobody sets one before this thread's first tile is used
+      bool bad = W.bad != 0;
       const int last = W.first + W.count;
       const int32_t* par = P.parents ? P.parents + static_cast<size_t>(W.row) * R.N : nullptr;
-      if (par) {
-        bad = !sv::tree_masks(par, m, S.masks, tid, kSoft);
-        sv::named_bar_sync(1, kSoft);
-      }
       const int tok = min((row0 + row) / R.group, m - 1);
       const bool active = 32 * wq < rows;      // the warp has a query row
+      const unsigned long long mask = par && last * kTile > n && !bad ? sv::tree_mask(par, tok) : 0ull;
       float mx = -INFINITY, l = 0.0f;
       bool odd = false;
 
@@ -323,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t sc[64];
           tm_load64(sc, ts + 64 * half);
           if (edge) {
-            const uint64_t see = sv::seen_bits(j0 + 64 * half - n, tok, par ? S.masks[tok] : 0ull, par);
+            const uint64_t see = sv::seen_bits(j0 + 64 * half - n, tok, mask, par);
             const uint32_t lo = static_cast<uint32_t>(see), hi = static_cast<uint32_t>(see >> 32);
 #pragma unroll
             for (int z = 0; z < 32; ++z) {
@@ -410,7 +437,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       wait_unless_lost(sv::smem_addr(&S.o_full), items & 1, lost);
       __syncwarp();
       fence_after();
-      if (more) copy_q(next);
       if (bad || *lost) atomicOr(&S.flags, 1);
       if (odd) atomicOr(&S.flags, 2);
       base += W.count;
@@ -419,13 +445,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       // A row's sum is that of its two threads; each finishes half of the row's columns.
       float* sums = &S.row_max[0][0][0];       // [2][kRows]; the tiles are done with it
       sums[half * kRows + row] = l;
-      if (more) queries_in();
       sv::named_bar_sync(1, kSoft);
-      // The next item's score products may begin: they write scores, not the accumulator.
-      if (more && lane == 0) sv::mbar_arrive(sv::smem_addr(&S.q_full));
       const int flags = S.flags;
       const float jl = (flags & 1) ? __int_as_float(0x7fffffff) : sums[row] + sums[kRows + row];
-      const bool whole = W.count == W.w.tiles;
+      const bool whole = W.count == W.tiles;
       const int slot = 2 * blockIdx.x + (W.first == 0 ? 1 : 0);
       const int i = (row0 + row) / R.group, hq = W.head * R.group + (row0 + row) - i * R.group;
       const size_t at = (static_cast<size_t>(W.row) * R.N + i) * P.Hq + hq;
@@ -445,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int j = max(n, W.first * kTile); j < min(entries, last * kTile); ++j) {
             const int page = sv::cache_page(C, W.row, j), a = j - n;
             if (!sv::page_ok(C, page)) continue;
-            if (!(par ? a <= 0 || ((S.masks[tok] >> (a - 1)) & 1) : a <= tok)) continue;
+            if (!(par ? a <= 0 || ((mask >> (a - 1)) & 1) : a <= tok)) continue;
             const unsigned short* v = reinterpret_cast<const unsigned short*>(C.v + sv::entry_offset(C, page, W.head, j)) + mycol;
 #pragma unroll
             for (int z = 0; z < 16; ++z) {
@@ -475,13 +498,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       fence_before();
       sv::named_bar_sync(1, kSoft);            // the sums have been read
-      if (!whole && tid == 0) sv::tell_shared(P, W, S.plan);
-      W = next;
-      have = more;
+      if (!whole && tid == 0 && W.first == 0) sv::tell_shared(P, W.row, W.head, W.q_tile, W.item_at, W.tiles, S.plan);
     }
     fence_before();
   }
   __syncthreads();
+  if (S.lost) {                                // a wait gave up: NaN for the whole run
+    sv::Walk W;
+    W.begin(R, S.plan);
+    while (W.next(R)) {
+      const int row0 = W.q_tile * R.q_rows, rows = min(R.q_rows, W.w.m * R.group - row0);
+      const bool whole = W.count == W.w.tiles;
+      for (int x = tid; x < rows * D; x += kThreads) {
+        const int r = x / D, i = (row0 + r) / R.group, hq = W.head * R.group + (row0 + r) - i * R.group;
+        const size_t at = (static_cast<size_t>(W.row) * R.N + i) * P.Hq + hq;
+        if (whole) static_cast<unsigned short*>(P.out)[at * D + x % D] = 0x7fffu;
+        if (x % D == 0 && whole && P.lse) P.lse[at] = __int_as_float(0x7fffffff);
+        if (x % D == 0 && !whole) P.part_ml[(2 * blockIdx.x + (W.first == 0 ? 1 : 0)) * kRows + r].y = __int_as_float(0x7fffffff);
+      }
+      if (!whole && tid == 0 && W.first == 0) sv::tell_shared(P, W.row, W.head, W.q_tile, W.item_at, W.w.tiles, S.plan);
+    }
+  }
   if (warp == kProducts) {
     fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;"
@@ -490,11 +527,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <bool F16, int D>
-int launch(const AttendParams& P, const CUtensorMap& k, const CUtensorMap& v, int grid, cudaStream_t st) {
+int launch(const AttendParams& P, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& q, int q_tokens,
+           int grid, cudaStream_t st) {
   auto kern = sv_attend_wide_kernel<F16, D>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes<D>) != cudaSuccess)
     return SV_ERR_CUDA;
-  kern<<<grid, kThreads, kSmemBytes<D>, st>>>(P, k, v);
+  kern<<<grid, kThreads, kSmemBytes<D>, st>>>(P, k, v, q, q_tokens);
   return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 
@@ -502,10 +540,11 @@ int launch(const AttendParams& P, const CUtensorMap& k, const CUtensorMap& v, in
 
 namespace sv {
 
-int launch_attend_wide(const AttendParams& P, bool f16, const CUtensorMap& k, const CUtensorMap& v, int grid,
-                       cudaStream_t st) {
-  if (P.R.C.head_dim == 64) return f16 ? launch<true, 64>(P, k, v, grid, st) : launch<false, 64>(P, k, v, grid, st);
-  return f16 ? launch<true, 128>(P, k, v, grid, st) : launch<false, 128>(P, k, v, grid, st);
+int launch_attend_wide(const AttendParams& P, bool f16, const CUtensorMap& k, const CUtensorMap& v,
+                       const CUtensorMap& q, int q_tokens, int grid, cudaStream_t st) {
+  if (P.R.C.head_dim == 64)
+    return f16 ? launch<true, 64>(P, k, v, q, q_tokens, grid, st) : launch<false, 64>(P, k, v, q, q_tokens, grid, st);
+  return f16 ? launch<true, 128>(P, k, v, q, q_tokens, grid, st) : launch<false, 128>(P, k, v, q, q_tokens, grid, st);
 }
 
 }  // namespace sv

@@ -111,6 +111,9 @@ inline int check_tokens(const void* x, int64_t row_stride, int64_t token_stride,
 // A tensor map over the cache's keys or values (dimensions D, slot, head, page) whose boxes are 64
 // elements (128 bytes, swizzled) of `rows` slots of one page and head.
 int cache_tensor_map(const sv_paged_cache* c, const void* base, int rows, CUtensorMap* map);
+// The same over a round's tokens (dimensions D, head, token, row): boxes of `heads` heads of `tokens` tokens.
+int query_tensor_map(const void* q, int64_t row_stride, int64_t token_stride, int32_t B, int32_t N, int32_t Hq,
+                     int32_t D, int32_t dtype, int heads, int tokens, CUtensorMap* map);
 // Slots of one box: a page's, at most 64.
 inline int box_rows(const sv_paged_cache* c) { return c->page_size < 64 ? c->page_size : 64; }
 // Multiprocessors of a device (sv_api.cu).

@@ -248,6 +248,13 @@ __device__ __forceinline__ bool tree_masks(const int32_t* parents, int m, unsign
   return ok;
 }
 
+// The same of one token t of a valid tree.
+__device__ __forceinline__ unsigned long long tree_mask(const int32_t* parents, int t) {
+  unsigned long long s = 0;
+  for (int x = t; x > 0; x = __ldg(parents + x)) s |= 1ull << (x - 1);
+  return s;
+}
+
 // Which of 64 entries a token attends, as bits: a0 is the place in the round of the first of them (below
 // 0: an entry before the round), i the token; in a tree `mask` is the token's from tree_masks.
 __device__ __forceinline__ uint64_t seen_bits(int a0, int i, unsigned long long mask, bool tree) {
