@@ -297,7 +297,7 @@ int spec_verify_kv_rollback(const int32_t* prefix_len, const int32_t* draft_len,
  * weight       [num_pages, heads, page_size] fp32, contiguous, or NULL.
  * page_table   [B, max_pages] int32; only the entries that a row's length reaches are read.
  * heads        key heads; a call's query heads are a multiple of it (query head h reads key head
- *              h / (query heads / heads)).
+ *              h / (query heads / heads)) and at most 128 times it.
  * head_dim     64, 128 or 256. page_size: 16, 32, 64, 128 or 256. dtype: SV_DTYPE_BF16 or SV_DTYPE_F16.
  *              max_pages * page_size <= 1048576 entries a row.
  * The struct is host memory, read before the call returns; the arrays are caller-owned device memory.

@@ -14,7 +14,7 @@ SOURCES = [CSRC / "sv_api.cu", CSRC / "sv_stream.cu", CSRC / "sv_element.cu", CS
            CSRC / "sv_staged.cu", CSRC / "sv_append.cu", CSRC / "sv_attend.cu", CSRC / "sv_weigh.cu",
            CSRC / "sv_evict.cu", CSRC / "sv_tma.cu", CSRC / "sv_attend_wide.cu",
            CSRC / "sv_attend_join.cu"]
-DEPS = [CSRC / "sv_common.cuh", CSRC / "sv_cache.cuh", CSRC / "sv_tiles.cuh", CSRC / "sv_attend.cuh", PKG_DIR.parent / "include" / "spec_verify.h"]
+DEPS = [CSRC / "sv_common.cuh", CSRC / "sv_cache.cuh", CSRC / "sv_tiles.cuh", CSRC / "sv_attend.cuh", CSRC / "sv_tmem.cuh", PKG_DIR.parent / "include" / "spec_verify.h"]
 LIB_NAME = "libspecverify.so"
 LIB_PATH = PKG_DIR / LIB_NAME
 

@@ -380,8 +380,8 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2)
 
 // The kernel and the query rows of an item: 16 where a key head has no more, else up to 128, whole tokens,
 // on the wide kernel; heads of 256, whose accumulators fill the registers here and tensor memory there,
-// and more than 128 query heads a key head take 16.
-bool is_wide(int N, int group, int D) { return N * group > 16 && D < 256 && group <= 128; }
+// take 16.
+bool is_wide(int N, int group, int D) { return N * group > 16 && D < 256; }
 int item_rows(int N, int group, int D) { return is_wide(N, group, D) ? 128 / group * group : 16; }
 int part_rows(int N, int group, int D) { return is_wide(N, group, D) ? 128 : 16; }
 int grid_limit(int sms, int N, int group, int D) { return sms * (D == 256 || is_wide(N, group, D) ? 1 : 2); }
@@ -402,7 +402,7 @@ int launch(const AttendParams& P, const CUtensorMap& k, const CUtensorMap& v, in
 extern "C" size_t spec_verify_paged_attention_workspace_size(int32_t N, int32_t Hq,
                                                              const sv_paged_cache* cache) {
   if (!cache || N < 1 || N > SV_MAX_GAMMA + 1 || Hq < 1 || Hq > 1024 || cache->heads < 1 ||
-      Hq % cache->heads != 0 || cache->head_dim < 1 || cache->head_dim > 256)
+      Hq % cache->heads != 0 || Hq / cache->heads > 128 || cache->head_dim < 1 || cache->head_dim > 256)
     return 0;
   const int D = cache->head_dim, group = Hq / cache->heads;
   const size_t part = static_cast<size_t>(part_rows(N, group, D)) * (D * 4 + 8);
@@ -422,7 +422,7 @@ extern "C" int spec_verify_paged_attention(const void* q, int64_t q_row_stride,
   if (!q || !prefix_len || !out) return SV_ERR_NULL_POINTER;
   st = sv::check_tokens(q, q_row_stride, q_token_stride, B, N, Hq, cache->head_dim);
   if (st != SV_OK) return st;
-  if (Hq % cache->heads != 0 || !(scale > 0.0f) || !std::isfinite(scale)) return SV_ERR_BAD_SHAPE;
+  if (Hq % cache->heads != 0 || Hq / cache->heads > 128 || !(scale > 0.0f) || !std::isfinite(scale)) return SV_ERR_BAD_SHAPE;
   if (sv::misaligned(out, 16) || sv::misaligned(out_lse, 4) || sv::misaligned(prefix_len, 4) ||
       sv::misaligned(num_queries, 4) || sv::misaligned(tree_parents, 4) ||
       sv::misaligned(workspace, 256))

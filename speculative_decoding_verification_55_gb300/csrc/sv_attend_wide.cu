@@ -24,10 +24,12 @@
 #include <cmath>
 
 #include "sv_attend.cuh"
+#include "sv_tmem.cuh"
 
 namespace {
 
 using sv::AttendParams;
+using namespace sv::tmem;
 using sv::kFull;
 
 constexpr int kTileLog2 = 7, kTile = 1 << kTileLog2;   // entries of a key tile
@@ -38,7 +40,6 @@ constexpr int kProducer = kSoftWarps, kProducts = kSoftWarps + 1, kItems = kSoft
 constexpr float kSlack = 8.0f;
 constexpr int kScoreTiles = 2;                         // tiles of scores in tensor memory
 constexpr int kPieces = 8;                             // items that the warps may be apart, and one
-constexpr int kColumns = 512;                          // tensor memory columns of the CTA
 
 template <int D>
 constexpr int kSlotBytes = kTile * D * 2;              // a tile's keys or its values
@@ -67,81 +68,6 @@ struct Control {
 };
 template <int D>
 constexpr int kSmemBytes = kSlotCount<D> * kSlotBytes<D> + kRows * D * 2 + sizeof(Control<kSlotCount<D>>);
-
-__device__ __forceinline__ uint64_t matrix_desc(uint32_t addr, uint32_t lead, uint32_t stride) {
-  // Start, leading and stride offsets in 16-byte units; version 1; 128-byte swizzle.
-  return static_cast<uint64_t>((addr & 0x3ffffu) >> 4) | (static_cast<uint64_t>(lead >> 4) << 16) |
-         (static_cast<uint64_t>(stride >> 4) << 32) | (1ull << 46) | (2ull << 61);
-}
-
-// fp32 accumulators, operands of one 16-bit type; M = 128; b_rows: B's rows are its contraction index.
-template <bool F16>
-__device__ __forceinline__ constexpr uint32_t product_desc(int n, bool b_rows) {
-  return (1u << 4) | (F16 ? 0u : (1u << 7) | (1u << 10)) | (b_rows ? 1u << 16 : 0u) |
-         (static_cast<uint32_t>(n >> 3) << 17) | ((kRows >> 4) << 24);
-}
-
-__device__ __forceinline__ void product_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool add) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-      ::"r"(d), "l"(a), "l"(b), "r"(desc), "r"(add ? 1u : 0u) : "memory");
-}
-__device__ __forceinline__ void product_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t desc, bool add) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-      ::"r"(d), "r"(a), "l"(b), "r"(desc), "r"(add ? 1u : 0u) : "memory");
-}
-// The barrier gets an arrival when every product issued so far is done.
-__device__ __forceinline__ void products_done(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
-               ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-
-#define SV_R8(x, o) "=r"(x[o]), "=r"(x[o + 1]), "=r"(x[o + 2]), "=r"(x[o + 3]), "=r"(x[o + 4]), "=r"(x[o + 5]), "=r"(x[o + 6]), "=r"(x[o + 7])
-#define SV_W8(x, o) "r"(x[o]), "r"(x[o + 1]), "r"(x[o + 2]), "r"(x[o + 3]), "r"(x[o + 4]), "r"(x[o + 5]), "r"(x[o + 6]), "r"(x[o + 7])
-// 16 or 64 columns of this thread's lane of tensor memory, loaded when the call returns (the wait
-// is part of the statement, so that no use of the registers can move before it).
-__device__ __forceinline__ void tm_load64(uint32_t* r, uint32_t at) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,"
-      "%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : SV_R8(r, 0), SV_R8(r, 8), SV_R8(r, 16), SV_R8(r, 24), SV_R8(r, 32), SV_R8(r, 40), SV_R8(r, 48), SV_R8(r, 56)
-      : "r"(at) : "memory");
-}
-__device__ __forceinline__ void tm_load16(uint32_t* r, uint32_t at) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : SV_R8(r, 0), SV_R8(r, 8) : "r"(at) : "memory");
-}
-__device__ __forceinline__ void tm_store16(uint32_t at, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
-      ::"r"(at), SV_W8(r, 0), SV_W8(r, 8) : "memory");
-}
-__device__ __forceinline__ void tm_store32(uint32_t at, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
-      ::"r"(at), SV_W8(r, 0), SV_W8(r, 8), SV_W8(r, 16), SV_W8(r, 24) : "memory");
-}
-__device__ __forceinline__ void tm_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// A bounded wait; the first that gives up makes every later one return at once.
-__device__ __forceinline__ bool wait_unless_lost(uint32_t bar, uint32_t parity, volatile int* lost) {
-  if (sv::mbar_try_wait(bar, parity)) return true;
-  if (*lost) return false;
-  if (sv::mbar_wait(bar, parity)) return true;
-  *lost = 1;
-  return false;
-}
 
 template <bool F16, int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -174,12 +100,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     S.lost = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == kProducts) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
-                 ::"r"(sv::smem_addr(&S.tm)), "r"(static_cast<uint32_t>(kColumns)) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-    fence_before();
-  }
+  if (warp == kProducts) tm_alloc(&S.tm);
   sv::make_plan<kThreads>(R, S.scan, &S.plan);
   asm volatile("griddepcontrol.launch_dependents;");   // the join kernel's CTAs, which wait for this grid's end
   if (tid == 0) P.shared[blockIdx.x].x = -1;
@@ -187,10 +108,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tm = S.tm;
   volatile int* const lost = &S.lost;
 
-  // The next item's description.
+  // The next item's description: the items' warp always tells an end.
   auto told = [&](int k) {
     Item I;
-    if (wait_unless_lost(sv::smem_addr(S.told + k % kPieces), (k / kPieces) & 1, lost)) I = S.items[k % kPieces];
+    if (sv::mbar_wait(sv::smem_addr(S.told + k % kPieces), (k / kPieces) & 1)) I = S.items[k % kPieces];
     else I.count = 0;
     return I;
   };
@@ -288,8 +209,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // queries: q_tokens tokens of the key head's query heads as rows.
     sv::Walk W;
     W.begin(R, S.plan);
+    int copies = 0;
     for (int k = 0;; ++k) {
-      const bool more = W.next(R);
+      const bool more = !__any_sync(kFull, *lost != 0) && W.next(R);
       bool bad = false;
       if (more && P.parents)
         for (int t = lane; t < W.w.m; t += 32) {
@@ -302,17 +224,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     bad ? 1 : 0, W.item_at};
         sv::mbar_arrive(sv::smem_addr(S.told + k % kPieces));
       }
-      if (!more || !__all_sync(kFull, k == 0 || wait_unless_lost(sv::smem_addr(&S.q_empty), (k - 1) & 1, lost))) {
-        if (k > 0) sv::mbar_wait_drain(sv::smem_addr(&S.q_full), (k - 1) & 1);   // the last queries are in
-        break;
-      }
+      if (!more) break;
+      if (!__all_sync(kFull, k == 0 || wait_unless_lost(sv::smem_addr(&S.q_empty), (k - 1) & 1, lost))) continue;
       if (lane == 0) {
         sv::mbar_arrive_expect_tx(sv::smem_addr(&S.q_full), q_tokens * R.group * D * 2);
         for (int half = 0; half < D / 64; ++half)
           sv::tma_load(qs + half * (kRows * 128), &qmap, half * 64, W.head * R.group, W.q_tile * (R.q_rows / R.group),
                        W.row, sv::smem_addr(&S.q_full));
       }
+      ++copies;
     }
+    if (copies > 0) sv::mbar_wait_drain(sv::smem_addr(&S.q_full), (copies - 1) & 1);   // the last queries are in
   } else {
     // ---- Softmax
     const int half = warp >> 2, wq = warp & 3, row = 32 * wq + lane;   // half: of a tile's entries, of D
@@ -342,7 +264,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool go = wait_unless_lost(sv::smem_addr(S.s_full + w), (x / kScoreTiles) & 1, lost);
         if (edge || idx + 1 == W.count)        // the values are in, and the producer has seen all pages
           go = go && wait_unless_lost(sv::smem_addr(S.full + s), ((2 * x + 1) / kSlots) & 1, lost);
-        if (!__all_sync(kFull, go)) break;
+        if (!__all_sync(kFull, go)) {          // a wait gave up: the barriers alone
+          if (active) sv::named_bar_sync(2 + wq, 64);
+          continue;
+        }
         fence_after();
         if (idx + 1 == W.count) bad |= S.bad[items % kPieces] != 0;
         if (active) {
@@ -519,11 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!whole && tid == 0 && W.first == 0) sv::tell_shared(P, W.row, W.head, W.q_tile, W.item_at, W.w.tiles, S.plan);
     }
   }
-  if (warp == kProducts) {
-    fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;"
-                 ::"r"(tm), "r"(static_cast<uint32_t>(kColumns)) : "memory");
-  }
+  if (warp == kProducts) tm_free(tm);
 }
 
 template <bool F16, int D>

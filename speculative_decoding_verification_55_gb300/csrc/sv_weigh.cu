@@ -3,67 +3,310 @@
 //   weight_j += sum over kept tokens d with n_b + d >= j, and the key head's query heads, of
 //               exp(scale q . k_j - lse).
 //
-// The simplest form: one CTA per row, key head and block of 64 entries; a warp takes every fourth entry
-// of it and all its tokens, a lane D / 32 of the elements.
+// One pass over the keys. The scores are S^T = K Q^T on the fifth-generation tensor cores: 128 entries
+// are the rows and a key head's queries (tokens times heads, up to 128 at a time) the columns, so that
+// a thread has one entry, adds up its row alone, and no thread needs another's numbers.
+// Persistent CTAs take equal runs of the batch's key tiles (sv_tiles.cuh). Warps: one copies key tiles
+// into a ring, one copies queries and tells the others what the item is, one thread issues the products
+// into four buffers of tensor memory, and two groups of four take the tiles in turn. More than 128
+// query rows go in chunks, whose queries are then copied again for every tile (from L2); an entry's sum
+// over its chunks stays with its thread, so that every entry gets a single addition.
+// Bound: the bytes of the keys (32 KB a tile of 128 x 128 against 0.73 us of an SM's share of HBM; the
+// products take 0.15 us at 72 rows, the exponentials 0.2).
 
 #include <cmath>
 
-#include "sv_cache.cuh"
-#include "sv_common.cuh"
+#include "sv_tiles.cuh"
+#include "sv_tmem.cuh"
 
 namespace {
 
-constexpr int kWarps = 4, kBlock = 64;
+using namespace sv::tmem;
+using sv::kFull;
+
+constexpr int kTileLog2 = 7, kTile = 1 << kTileLog2;   // entries of a key tile
+constexpr int kRows = 128;                             // query rows of a chunk
+constexpr int kGroups = 2, kSoftWarps = 4 * kGroups, kSoft = 32 * kSoftWarps;
+constexpr int kThreads = kSoft + 96;
+constexpr int kProducer = kSoftWarps, kProducts = kSoftWarps + 1, kItems = kSoftWarps + 2;
+constexpr int kOwn = 2, kScores = kOwn * kGroups;      // buffers of scores in tensor memory: of a group, all
+constexpr int kPieces = 16;                            // items that the warps may be apart, and one
 
 struct WeighParams {
-  sv::Cache C;
-  const char* q;
-  long long row_stride, token_stride;   // bytes
+  sv::Round R;
   const float* lse;
-  const int32_t* prefix;
-  const int32_t* num;
   const int32_t* path;
-  float c;                              // scale * log2(e)
-  int N, Hq, group;
+  float c;                                             // scale * log2(e)
+  int Hq, tokens;                                      // tokens of a chunk
 };
 
-template <typename T, int D>
-__global__ void __launch_bounds__(32 * kWarps) sv_weigh_plain_kernel(const WeighParams P) {
-  const sv::Cache& C = P.C;
-  const int h = blockIdx.y, b = blockIdx.z;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  constexpr int E = D / 32;
-  int n, m;
-  bool bad = !sv::round_lengths(C, P.prefix, P.num, b, P.N, true, &n, &m);
-  if (!bad && P.path && threadIdx.x < m) {
-    const int i = __ldg(P.path + static_cast<size_t>(b) * P.N + threadIdx.x);
-    bad = i < 0 || i >= P.N;
+template <int D>
+constexpr int kSlotBytes = kTile * D * 2;
+template <int D>
+constexpr int kKeySlots = D == 64 ? 10 : (D == 128 ? 5 : 2);
+template <int D>
+constexpr int kQuerySlots = D == 256 ? 1 : 2;
+
+struct Item {
+  int row, head, first, count;                         // count 0: the end
+  int n, m, bad;                                       // bad: a path entry out of range
+};
+
+template <int kK, int kQ>
+struct Control {
+  unsigned long long k_full[kK], k_empty[kK], q_full[kQ], q_empty[kQ], s_full[kScores], s_empty[kScores],
+      told[kPieces], drained;
+  long long scan[kThreads / 32];
+  sv::Plan plan;
+  Item items[kPieces];
+  alignas(16) float nl[kGroups][kRows];                // -lse log2(e) of the chunk's rows, by group
+  int lost;
+  uint32_t tm;
+};
+template <int D>
+constexpr int kSmemBytes = (kKeySlots<D> + kQuerySlots<D>)*kSlotBytes<D> + sizeof(Control<kKeySlots<D>, kQuerySlots<D>>);
+
+template <bool F16, int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    sv_weigh_kernel(const WeighParams P, const __grid_constant__ CUtensorMap kmap,
+                    const __grid_constant__ CUtensorMap qmap) {
+  constexpr int kK = kKeySlots<D>, kQ = kQuerySlots<D>;
+  extern __shared__ __align__(1024) unsigned char dyn[];
+  auto& S = *reinterpret_cast<Control<kK, kQ>*>(dyn + (kK + kQ) * kSlotBytes<D>);
+  const sv::Round& R = P.R;
+  const sv::Cache& C = R.C;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t ring = sv::smem_addr(dyn), qring = ring + kK * kSlotBytes<D>;
+  if (tid == 0) {
+    for (int s = 0; s < kK; ++s) {
+      sv::mbar_init(sv::smem_addr(S.k_full + s), 1);
+      sv::mbar_init(sv::smem_addr(S.k_empty + s), 1);
+    }
+    for (int s = 0; s < kQ; ++s) {
+      sv::mbar_init(sv::smem_addr(S.q_full + s), 1);
+      sv::mbar_init(sv::smem_addr(S.q_empty + s), 1);
+    }
+    for (int s = 0; s < kScores; ++s) {
+      sv::mbar_init(sv::smem_addr(S.s_full + s), 1);
+      sv::mbar_init(sv::smem_addr(S.s_empty + s), 4);
+    }
+    for (int s = 0; s < kPieces; ++s) sv::mbar_init(sv::smem_addr(S.told + s), 1);
+    sv::mbar_init(sv::smem_addr(&S.drained), 1);
+    S.lost = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (__syncthreads_or(bad)) return;
-  for (int j0 = blockIdx.x * kBlock; j0 < n + m; j0 += gridDim.x * kBlock)
-    for (int j = j0 + warp; j < min(j0 + kBlock, n + m); j += kWarps) {
-      const int page = sv::cache_page(C, b, j);
-      if (!sv::page_ok(C, page)) continue;
-      const T* k = reinterpret_cast<const T*>(C.k + sv::entry_offset(C, page, h, j)) + lane * E;
-      float kf[E];
+  if (warp == kProducts) tm_alloc(&S.tm);
+  sv::make_plan<kThreads>(R, S.scan, &S.plan);
+  fence_after();
+  const uint32_t tm = S.tm;
+  volatile int* const lost = &S.lost;
+  const int chunk_rows = P.tokens * R.group;
+  auto told = [&](int k) {
+    Item I;
+    if (sv::mbar_wait(sv::smem_addr(S.told + k % kPieces), (k / kPieces) & 1)) I = S.items[k % kPieces];
+    else I.count = 0;
+    return I;
+  };
+  // Chunks of an item; its queries are copied once when there is one, else for every tile.
+  auto chunks_of = [&](const Item& I) { return (I.m + P.tokens - 1) / P.tokens; };
+
+  if (warp == kProducer) {
+    sv::Walk W;
+    W.begin(R, S.plan);
+    sv::TileLoader T;
+    T.init(C, 1, kTileLog2);
+    int armed = 0;
+    bool gone = false;
+    while (!gone && W.next(R)) {
+      const int entries = W.w.n + W.w.m;
+      int p = T.page(C, W.row, W.first, entries, lane);
+      for (int t = W.first; t < W.first + W.count; ++t) {
+        const int p_next = t + 1 < W.first + W.count ? T.page(C, W.row, t + 1, entries, lane) : -1;
+        const int s = armed % kK;
+        const uint32_t bar = sv::smem_addr(S.k_full + s);
+        if (armed >= kK &&
+            !__all_sync(kFull, wait_unless_lost(sv::smem_addr(S.k_empty + s), (armed / kK - 1) & 1, lost))) {
+          gone = true;
+          break;
+        }
+        const int boxes = __popc(__ballot_sync(kFull, p >= 0));
+        if (lane == 0) sv::mbar_arrive_expect_tx(bar, static_cast<uint32_t>(boxes) << (T.rows_log2 + 7));
+        __syncwarp();
+        if (p >= 0) T.load(C, &kmap, nullptr, t, W.head, p, lane, ring + s * kSlotBytes<D>, bar);
+        ++armed;
+        p = p_next;
+      }
+    }
+    for (int e = max(0, armed - kK); e < armed; ++e)       // no copy is in flight when the CTA ends
+      sv::mbar_wait_drain(sv::smem_addr(S.k_full + e % kK), (e / kK) & 1);
+  } else if (warp == kProducts) {
+    if (lane == 0) {
+      int tile = 0, q = 0, units[kGroups] = {0, 0};      // units: chunks of a group's tiles so far
+      bool ok = true;
+      for (int k = 0; ok; ++k) {
+        const Item I = told(k);
+        if (I.count == 0) break;
+        const int chunks = chunks_of(I), rows = I.m * R.group;
+        for (int t = 0; t < I.count && ok; ++t, ++tile) {
+          const int ks = tile % kK, g = tile & 1;
+          ok = wait_unless_lost(sv::smem_addr(S.k_full + ks), (tile / kK) & 1, lost);
+          for (int x = 0; x < chunks && ok; ++x) {
+            const int unit = g ? units[1]++ : units[0]++, w = g * kOwn + unit % kOwn, qi = q % kQ;
+            const bool last_use = chunks > 1 || t + 1 == I.count;
+            ok = wait_unless_lost(sv::smem_addr(S.q_full + qi), (q / kQ) & 1, lost) &&
+                 (unit < kOwn || wait_unless_lost(sv::smem_addr(S.s_empty + w), (unit / kOwn - 1) & 1, lost));
+            if (!ok) break;
+            fence_after();
+            const int n = (min(chunk_rows, rows - x * chunk_rows) + 15) & ~15;
+            const uint32_t desc = product_desc<F16>(0, false) | (static_cast<uint32_t>(n >> 3) << 17);
+            const uint32_t kb = ring + ks * kSlotBytes<D>, qb = qring + qi * kSlotBytes<D>;
 #pragma unroll
-      for (int e = 0; e < E; ++e) kf[e] = static_cast<float>(k[e]);
-      float w = 0.0f;
-      for (int d = max(0, j - n); d < m; ++d) {
-        const int i = P.path ? __ldg(P.path + static_cast<size_t>(b) * P.N + d) : d;
-        for (int g = 0; g < P.group; ++g) {
-          const int hq = h * P.group + g;
-          const T* q = reinterpret_cast<const T*>(P.q + b * P.row_stride + i * P.token_stride) + hq * D + lane * E;
-          float s = 0.0f;
-#pragma unroll
-          for (int e = 0; e < E; ++e) s = fmaf(static_cast<float>(q[e]), kf[e], s);
-#pragma unroll
-          for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-          w += exp2f(s * P.c - __ldg(P.lse + (static_cast<size_t>(b) * P.N + i) * P.Hq + hq) * sv::kLog2e);
+            for (int y = 0; y < D / 16; ++y)
+              product_ss(tm + w * kRows, matrix_desc(kb + (y >> 2) * (kTile * 128) + (y & 3) * 32, 16, 1024),
+                         matrix_desc(qb + (y >> 2) * (kRows * 128) + (y & 3) * 32, 16, 1024), desc, y > 0);
+            products_done(sv::smem_addr(S.s_full + w));
+            if (x + 1 == chunks) products_done(sv::smem_addr(S.k_empty + ks));
+            if (last_use) {
+              products_done(sv::smem_addr(S.q_empty + qi));
+              ++q;
+            }
+          }
         }
       }
-      if (lane == 0) atomicAdd(C.weight + sv::weight_index(C, page, h, j), w);
+      if (*lost) {              // products in flight end before the tensor memory is given back
+        products_done(sv::smem_addr(&S.drained));
+        sv::mbar_wait_drain(sv::smem_addr(&S.drained), 0);
+      }
     }
+    __syncwarp();
+  } else if (warp == kItems) {
+    sv::Walk W;
+    W.begin(R, S.plan);
+    int q = 0;
+    for (int k = 0;; ++k) {
+      const bool more = !__any_sync(kFull, *lost != 0) && W.next(R);
+      bool bad = false;
+      if (more && P.path)
+        for (int d = lane; d < W.w.m; d += 32) {
+          const int i = __ldg(P.path + static_cast<size_t>(W.row) * R.N + d);
+          bad |= i < 0 || i >= R.N;
+        }
+      bad = __any_sync(kFull, bad);
+      const Item I{W.row, W.head, W.first, more ? W.count : 0, W.w.n, W.w.m, bad ? 1 : 0};
+      if (lane == 0) {
+        S.items[k % kPieces] = I;
+        sv::mbar_arrive(sv::smem_addr(S.told + k % kPieces));
+      }
+      if (!more) break;
+      const int chunks = chunks_of(I);
+      for (int x = 0; x < (chunks > 1 ? chunks * I.count : 1); ++x, ++q) {
+        const int qi = q % kQ;
+        if (q >= kQ &&
+            !__all_sync(kFull, wait_unless_lost(sv::smem_addr(S.q_empty + qi), (q / kQ - 1) & 1, lost)))
+          break;
+        const int d0 = (x % chunks) * P.tokens, nt = min(P.tokens, I.m - d0);
+        const uint32_t bar = sv::smem_addr(S.q_full + qi);
+        if (lane == 0) sv::mbar_arrive_expect_tx(bar, nt * R.group * D * 2);
+        __syncwarp();
+        for (int y = lane; y < nt * (D / 64); y += 32) {     // a token's heads, 64 elements of each
+          const int d = y / (D / 64), half = y % (D / 64);
+          int i = d0 + d;
+          if (P.path) i = min(max(__ldg(P.path + static_cast<size_t>(I.row) * R.N + i), 0), R.N - 1);
+          sv::tma_load(qring + qi * kSlotBytes<D> + half * (kRows * 128) + d * R.group * 128, &qmap, half * 64,
+                       I.head * R.group, i, I.row, bar);
+        }
+      }
+    }
+    for (int e = max(0, q - kQ); e < q; ++e)
+      sv::mbar_wait_drain(sv::smem_addr(S.q_full + e % kQ), (e / kQ) & 1);
+  } else {
+    // ---- Sums: a thread an entry; the groups take the tiles in turn.
+    const int g = warp >> 2, wq = warp & 3, wtid = tid & 127;
+    const uint32_t lanes = static_cast<uint32_t>(32 * wq) << 16;
+    float* const nl = S.nl[g];
+    int tile = 0, unit = 0;
+    bool ok = true;
+    for (int k = 0;; ++k) {
+      const Item I = told(k);
+      if (I.count == 0) break;
+      const int chunks = chunks_of(I), rows = I.m * R.group;
+      bool loaded = false;                     // nl holds the item's single chunk
+      for (int t = 0; t < I.count; ++t, ++tile) {
+        if ((tile & 1) != g) continue;
+        const int j = (I.first + t) * kTile + wtid;
+        int page = -1;
+        if (j < I.n + I.m) page = sv::cache_page(C, I.row, j);
+        const bool mine = sv::page_ok(C, page) && !I.bad;
+        float w = 0.0f;
+        for (int x = 0; x < chunks; ++x, ++unit) {
+          const int b = g * kOwn + unit % kOwn, r0 = x * chunk_rows, nr = min(chunk_rows, rows - r0);
+          if (!loaded) {
+            sv::named_bar_sync(1 + g, 128);    // the group has read the last chunk's
+            float v = 0.0f;
+            if (wtid < nr) {
+              const int d = (r0 + wtid) / R.group, hg = (r0 + wtid) - d * R.group;
+              int i = d;
+              if (P.path) i = min(max(__ldg(P.path + static_cast<size_t>(I.row) * R.N + d), 0), R.N - 1);
+              v = -sv::kLog2e * __ldg(P.lse + (static_cast<size_t>(I.row) * R.N + i) * P.Hq + I.head * R.group + hg);
+            }
+            nl[wtid] = v;
+            sv::named_bar_sync(1 + g, 128);
+            loaded = chunks == 1;
+          }
+          ok = ok && __all_sync(kFull, wait_unless_lost(sv::smem_addr(S.s_full + b), (unit / kOwn) & 1, lost));
+          if (!ok) continue;                   // a wait gave up: the barriers alone
+          fence_after();
+          // Rows before `lo` belong to tokens before the entry; rows from nr on are not there.
+          const int lo = max(j - I.n, 0) * R.group - r0;
+          const bool plain = __all_sync(kFull, lo <= 0);
+          const sv::f32x2 c2 = sv::pk(P.c, P.c);
+          sv::f32x2 sum = sv::pk(0.0f, 0.0f);
+          for (int y = 0; y < nr; y += 16) {
+            uint32_t s[16];
+            tm_load16(s, tm + lanes + b * kRows + y);
+            if (plain && y + 16 <= nr) {
+#pragma unroll
+              for (int z = 0; z < 16; z += 4) {
+                const float4 e = *reinterpret_cast<const float4*>(nl + y + z);
+                float p0, p1, p2, p3;
+                sv::upk(sv::fma2(sv::pk(__uint_as_float(s[z]), __uint_as_float(s[z + 1])), c2, sv::pk(e.x, e.y)), p0, p1);
+                sv::upk(sv::fma2(sv::pk(__uint_as_float(s[z + 2]), __uint_as_float(s[z + 3])), c2, sv::pk(e.z, e.w)), p2, p3);
+                sum = sv::add2(sum, sv::pk(sv::ex2(p0), sv::ex2(p1)));
+                sum = sv::add2(sum, sv::pk(sv::ex2(p2), sv::ex2(p3)));
+              }
+            } else {
+              float a = 0.0f;
+#pragma unroll
+              for (int z = 0; z < 16; ++z) {
+                const float p = sv::ex2(fmaf(__uint_as_float(s[z]), P.c, nl[y + z]));
+                if (y + z >= lo && y + z < nr) a += p;
+              }
+              sum = sv::add2(sum, sv::pk(a, 0.0f));
+            }
+          }
+          float s0, s1;
+          sv::upk(sum, s0, s1);
+          w += s0 + s1;
+          fence_before();
+          __syncwarp();
+          if (lane == 0) sv::mbar_arrive(sv::smem_addr(S.s_empty + b));
+        }
+        if (ok && mine) atomicAdd(C.weight + sv::weight_index(C, page, I.head, j), w);
+      }
+    }
+    fence_before();
+  }
+  __syncthreads();
+  if (warp == kProducts) tm_free(tm);
+}
+
+template <bool F16, int D>
+int launch(const WeighParams& P, const CUtensorMap& k, const CUtensorMap& q, int grid, cudaStream_t st) {
+  auto kern = sv_weigh_kernel<F16, D>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes<D>) != cudaSuccess)
+    return SV_ERR_CUDA;
+  kern<<<grid, kThreads, kSmemBytes<D>, st>>>(P, k, q);
+  return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 
 }  // namespace
@@ -74,38 +317,46 @@ extern "C" int spec_verify_kv_weights(const void* q, int64_t q_row_stride, int64
                                       const int32_t* path, float scale, int32_t B, int32_t N,
                                       int32_t Hq, void* cuda_stream) {
   WeighParams P;
-  int st = sv::check_cache(cache, B, true, &P.C);
+  int st = sv::check_cache(cache, B, true, &P.R.C);
   if (st != SV_OK) return st;
   if (!q || !lse || !prefix_len) return SV_ERR_NULL_POINTER;
   st = sv::check_tokens(q, q_row_stride, q_token_stride, B, N, Hq, cache->head_dim);
   if (st != SV_OK) return st;
-  if (Hq % cache->heads != 0 || !(scale > 0.0f) || !std::isfinite(scale)) return SV_ERR_BAD_SHAPE;
+  if (Hq % cache->heads != 0 || Hq / cache->heads > kRows || !(scale > 0.0f) || !std::isfinite(scale))
+    return SV_ERR_BAD_SHAPE;
   if (sv::misaligned(lse, 4) || sv::misaligned(prefix_len, 4) || sv::misaligned(num_kept, 4) ||
       sv::misaligned(path, 4))
     return SV_ERR_MISALIGNED;
   int dev = 0;
   st = sv::current_device_status(&dev);
   if (st != SV_OK) return st;
-  P.q = static_cast<const char*>(q);
-  P.row_stride = q_row_stride * 2;
-  P.token_stride = q_token_stride * 2;
+  const int D = cache->head_dim, group = Hq / cache->heads;
+  CUtensorMap kmap, qmap;
+  st = sv::cache_tensor_map(cache, cache->k, sv::box_rows(cache), &kmap);
+  if (st == SV_OK) st = sv::query_tensor_map(q, q_row_stride, q_token_stride, B, N, Hq, D, cache->dtype, group, 1, &qmap);
+  if (st != SV_OK) return st;
+  P.R.prefix = prefix_len;
+  P.R.num = num_kept;
+  P.R.B = B;
+  P.R.N = N;
+  P.R.group = group;
+  P.R.q_rows = N * group;                  // one item per row and key head
+  P.R.tile_log2 = kTileLog2;
+  P.R.extra = 2;
+  P.R.none_ok = true;
   P.lse = lse;
-  P.prefix = prefix_len;
-  P.num = num_kept;
   P.path = path;
   P.c = scale * sv::kLog2e;
-  P.N = N;
   P.Hq = Hq;
-  P.group = Hq / cache->heads;
+  P.tokens = kRows / group;
+  const int sms = sv::device_sms(dev);
+  if (sms < 1) return SV_ERR_CUDA;
+  const long long most = static_cast<long long>(B) * cache->heads *
+                         ((static_cast<long long>(cache->max_pages) * cache->page_size + kTile - 1) / kTile);
+  const int grid = static_cast<int>(most < sms ? most : sms);
+  cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   const bool f16 = cache->dtype == SV_DTYPE_F16;
-  void (*kern)(const WeighParams) = nullptr;
-  switch (cache->head_dim) {
-    case 64: kern = f16 ? sv_weigh_plain_kernel<__half, 64> : sv_weigh_plain_kernel<__nv_bfloat16, 64>; break;
-    case 128: kern = f16 ? sv_weigh_plain_kernel<__half, 128> : sv_weigh_plain_kernel<__nv_bfloat16, 128>; break;
-    default: kern = f16 ? sv_weigh_plain_kernel<__half, 256> : sv_weigh_plain_kernel<__nv_bfloat16, 256>; break;
-  }
-  const long long cap = static_cast<long long>(P.C.max_pages) * P.C.page_size;
-  const int blocks = static_cast<int>((cap + kBlock - 1) / kBlock < 256 ? (cap + kBlock - 1) / kBlock : 256);
-  kern<<<dim3(blocks, P.C.heads, B), 32 * kWarps, 0, static_cast<cudaStream_t>(cuda_stream)>>>(P);
-  return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+  if (D == 64) return f16 ? launch<true, 64>(P, kmap, qmap, grid, s) : launch<false, 64>(P, kmap, qmap, grid, s);
+  if (D == 128) return f16 ? launch<true, 128>(P, kmap, qmap, grid, s) : launch<false, 128>(P, kmap, qmap, grid, s);
+  return f16 ? launch<true, 256>(P, kmap, qmap, grid, s) : launch<false, 256>(P, kmap, qmap, grid, s);
 }

@@ -150,7 +150,7 @@ def test_argument_refusals(L):
                            (dict(par=FAKE + 2), 5)):
         got = calls(L, c, **change)
         assert (got["attend"], got["weigh"], got["append"]) == (status,) * 3, (change, got)
-    for change, status in ((dict(Hq=0), 2), (dict(Hq=30), 2), (dict(scale=0.0), 2),
+    for change, status in ((dict(Hq=0), 2), (dict(Hq=30), 2), (dict(Hq=1024 + 8), 2), (dict(scale=0.0), 2),
                            (dict(scale=-1.0), 2), (dict(scale=math.inf), 2), (dict(scale=math.nan), 2)):
         got = calls(L, c, **change)
         assert (got["attend"], got["weigh"]) == (status,) * 2, (change, got)
