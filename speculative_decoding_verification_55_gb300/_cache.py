@@ -7,8 +7,7 @@ from __future__ import annotations
 import ctypes
 import math
 
-from ._binding import (SV_DTYPE_BF16, SV_DTYPE_F16, SV_OK, SpecVerifyError, _on, _ptr,
-                       _stream_handle, lib)
+from ._binding import SV_DTYPE_BF16, SV_DTYPE_F16, SV_OK, SpecVerifyError, _on, _stream_handle, lib
 
 
 class _CacheStruct(ctypes.Structure):
@@ -57,49 +56,58 @@ class PagedCache:
             page_table.data_ptr(), steps[0][0], steps[0][1], steps[0][2], P, S, page_table.shape[1],
             H, D, SV_DTYPE_BF16 if k.dtype == torch.bfloat16 else SV_DTYPE_F16)
         self.ref = ctypes.addressof(self.struct)
+        self.workspace_need = {}
 
 
-def _tokens(x, name, cache, B=None, N=None):
-    """Checks a round's [B, N, heads, D] tensor; returns its strides over rows and tokens."""
-    if x.dim() != 4 or x.shape[0] != cache.B or x.shape[3] != cache.head_dim \
-            or (N is not None and x.shape[1] != N):
+def _tokens(x, name, cache, N=None):
+    """Checks a round's [B, N, heads, D] tensor; returns (N, heads, strides over rows and tokens)."""
+    shape = x.shape
+    if len(shape) != 4 or shape[0] != cache.B or shape[3] != cache.head_dim \
+            or (N is not None and shape[1] != N):
         raise ValueError(f"{name} must be [{cache.B}, {'N' if N is None else N}, heads, "
-                         f"{cache.head_dim}], got {tuple(x.shape)}")
-    if x.dtype != cache.dtype:
+                         f"{cache.head_dim}], got {tuple(shape)}")
+    if x.dtype is not cache.dtype:
         raise TypeError(f"{name} must be {cache.dtype}, got {x.dtype}")
     if x.device != cache.device:
         raise ValueError(f"{name} must be on {cache.device}, got {x.device}")
+    B, n, heads, D = shape
     s = x.stride()
-    heads, D = x.shape[2], x.shape[3]
     if s[3] != 1 or (heads > 1 and s[2] != D):
         raise ValueError(f"the heads of a token of {name} must be contiguous")
-    return (s[0] if x.shape[0] > 1 else heads * D * x.shape[1]), (s[1] if x.shape[1] > 1 else heads * D)
+    return n, heads, (s[0] if B > 1 else heads * D * n), (s[1] if n > 1 else heads * D)
 
 
-def _ints(t, name, shape, device):
+def _small(t, name, dtype, shape, device):
+    """Address of a contiguous tensor of this type, shape and device (None -> NULL)."""
     if t is None:
         return None
-    import torch
-    if t.dtype != torch.int32:
-        raise TypeError(f"{name} must be torch.int32, got {t.dtype}")
-    if tuple(t.shape) != shape or not t.is_contiguous():
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous with shape {shape}, got {tuple(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
     return t.data_ptr()
 
 
-def _floats(t, name, shape, device):
+def _raw_stream(stream, device):
     import torch
-    if t is None:
-        return None
-    if t.dtype != torch.float32:
-        raise TypeError(f"{name} must be torch.float32, got {t.dtype}")
-    if tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous with shape {shape}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-    return t.data_ptr()
+    if stream is None and device.type == "cuda":
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return _stream_handle(stream, device)
+
+
+def _call(f, cache, stream, *args):
+    """Calls f(*args, stream) with the cache's device current and raises on a nonzero status."""
+    import torch
+    dev = cache.device
+    if dev.type == "cuda" and torch._C._cuda_getDevice() == dev.index:
+        st = f(*args, _raw_stream(stream, dev))
+    else:
+        with _on(dev):
+            st = f(*args, _raw_stream(stream, dev))
+    if st != SV_OK:
+        raise SpecVerifyError(st, f.__name__)
 
 
 def spec_verify_paged_attention_workspace_size(N: int, Hq: int, cache: PagedCache) -> int:
@@ -110,44 +118,34 @@ def spec_verify_kv_append(k_new, v_new, cache, prefix_len, num_new=None, path=No
                           stream=None) -> None:
     """Calls the C ABI spec_verify_kv_append on torch tensors: token d (or path[:, d]) of k_new and
     v_new [B, N, heads, D] becomes entry prefix_len + d. Raises SpecVerifyError on a nonzero status."""
-    dev, B, N = cache.device, cache.B, k_new.shape[1]
-    strides = _tokens(k_new, "k_new", cache)
-    if _tokens(v_new, "v_new", cache, N=N) != strides or k_new.shape[2] != cache.heads \
-            or v_new.shape[2] != cache.heads:
+    import torch
+    dev, B = cache.device, cache.B
+    N, heads, rs, ts = _tokens(k_new, "k_new", cache)
+    if _tokens(v_new, "v_new", cache, N) != (N, heads, rs, ts) or heads != cache.heads:
         raise ValueError(f"k_new and v_new must have {cache.heads} heads and the same strides")
-    args = (_ints(prefix_len, "prefix_len", (B,), dev), _ints(num_new, "num_new", (B,), dev),
-            _ints(path, "path", (B, N), dev), _ints(out_len, "out_len", (B,), dev))
-    with _on(dev):
-        st = lib().spec_verify_kv_append(k_new.data_ptr(), v_new.data_ptr(), *strides, cache.ref, *args,
-                                         B, N, _stream_handle(stream, dev))
-    if st != SV_OK:
-        raise SpecVerifyError(st, "spec_verify_kv_append")
+    i32 = torch.int32
+    _call(lib().spec_verify_kv_append, cache, stream, k_new.data_ptr(), v_new.data_ptr(), rs, ts, cache.ref,
+          _small(prefix_len, "prefix_len", i32, (B,), dev), _small(num_new, "num_new", i32, (B,), dev),
+          _small(path, "path", i32, (B, N), dev), _small(out_len, "out_len", i32, (B,), dev), B, N)
 
 
 def spec_verify_paged_attention(q, cache, prefix_len, num_queries, tree_parents, out, out_lse,
                                 workspace, scale=None, stream=None) -> None:
     """Calls the C ABI spec_verify_paged_attention on torch tensors: q [B, N, Hq, D] (heads of a token
     together), scale 1 / sqrt(D) unless given. Raises SpecVerifyError on a nonzero status."""
+    import torch
     dev, B = cache.device, cache.B
-    strides = _tokens(q, "q", cache)
-    N, Hq = q.shape[1], q.shape[2]
-    if out.dtype != cache.dtype or tuple(out.shape) != (B, N, Hq, cache.head_dim) \
-            or not out.is_contiguous() or out.device != dev:
-        raise ValueError(f"out must be a contiguous {(B, N, Hq, cache.head_dim)} {cache.dtype} tensor "
-                         f"on {dev}")
+    N, Hq, rs, ts = _tokens(q, "q", cache)
+    i32 = torch.int32
+    o = _small(out, "out", cache.dtype, (B, N, Hq, cache.head_dim), dev)
     if workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous and on {dev}")
-    if scale is None:
-        scale = 1.0 / math.sqrt(cache.head_dim)
-    args = (_ints(prefix_len, "prefix_len", (B,), dev), _ints(num_queries, "num_queries", (B,), dev),
-            _ints(tree_parents, "tree_parents", (B, N), dev))
-    with _on(dev):
-        st = lib().spec_verify_paged_attention(
-            q.data_ptr(), *strides, cache.ref, *args, scale, out.data_ptr(),
-            _floats(out_lse, "out_lse", (B, N, Hq), dev), B, N, Hq, workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), _stream_handle(stream, dev))
-    if st != SV_OK:
-        raise SpecVerifyError(st, "spec_verify_paged_attention")
+    _call(lib().spec_verify_paged_attention, cache, stream, q.data_ptr(), rs, ts, cache.ref,
+          _small(prefix_len, "prefix_len", i32, (B,), dev), _small(num_queries, "num_queries", i32, (B,), dev),
+          _small(tree_parents, "tree_parents", i32, (B, N), dev),
+          1.0 / math.sqrt(cache.head_dim) if scale is None else scale, o,
+          _small(out_lse, "out_lse", torch.float32, (B, N, Hq), dev), B, N, Hq, workspace.data_ptr(),
+          workspace.nbytes)
 
 
 def spec_verify_kv_weights(q, lse, cache, prefix_len, num_kept=None, path=None, scale=None,
@@ -155,61 +153,58 @@ def spec_verify_kv_weights(q, lse, cache, prefix_len, num_kept=None, path=None, 
     """Calls the C ABI spec_verify_kv_weights on torch tensors: cache.weight gains what the kept tokens
     of q [B, N, Hq, D] gave to each entry (lse: spec_verify_paged_attention's out_lse). Raises
     SpecVerifyError on a nonzero status."""
+    import torch
     dev, B = cache.device, cache.B
-    strides = _tokens(q, "q", cache)
-    N, Hq = q.shape[1], q.shape[2]
-    if scale is None:
-        scale = 1.0 / math.sqrt(cache.head_dim)
-    args = (_ints(prefix_len, "prefix_len", (B,), dev), _ints(num_kept, "num_kept", (B,), dev),
-            _ints(path, "path", (B, N), dev))
-    with _on(dev):
-        st = lib().spec_verify_kv_weights(q.data_ptr(), *strides, _floats(lse, "lse", (B, N, Hq), dev),
-                                          cache.ref, *args, scale, B, N, Hq, _stream_handle(stream, dev))
-    if st != SV_OK:
-        raise SpecVerifyError(st, "spec_verify_kv_weights")
+    N, Hq, rs, ts = _tokens(q, "q", cache)
+    i32 = torch.int32
+    _call(lib().spec_verify_kv_weights, cache, stream, q.data_ptr(), rs, ts,
+          _small(lse, "lse", torch.float32, (B, N, Hq), dev), cache.ref,
+          _small(prefix_len, "prefix_len", i32, (B,), dev), _small(num_kept, "num_kept", i32, (B,), dev),
+          _small(path, "path", i32, (B, N), dev),
+          1.0 / math.sqrt(cache.head_dim) if scale is None else scale, B, N, Hq)
 
 
 def spec_verify_kv_evict(cache, length, budget, recent, out_len, stream=None) -> None:
     """Calls the C ABI spec_verify_kv_evict on torch tensors: rows with more than budget entries keep
     the last ``recent`` and, per head, the others of the largest cache.weight. Raises SpecVerifyError on
     a nonzero status."""
+    import torch
     dev, B = cache.device, cache.B
-    with _on(dev):
-        st = lib().spec_verify_kv_evict(cache.ref, _ints(length, "length", (B,), dev), budget, recent,
-                                        _ints(out_len, "out_len", (B,), dev), B,
-                                        _stream_handle(stream, dev))
-    if st != SV_OK:
-        raise SpecVerifyError(st, "spec_verify_kv_evict")
+    _call(lib().spec_verify_kv_evict, cache, stream, cache.ref, _small(length, "length", torch.int32, (B,), dev),
+          budget, recent, _small(out_len, "out_len", torch.int32, (B,), dev), B)
 
 
 _attend_ws = {}
 
 
-def _attend_workspace(N, Hq, cache, stream):
-    """A workspace cached per (device, stream) and grown on demand. A call that is being captured gets
-    one of its own: replays of two graphs may overlap."""
+def _attend_workspace(N, Hq, cache):
+    """A workspace cached per (device, current stream) and grown on demand. A call that is being captured
+    gets one of its own: replays of two graphs may overlap."""
     import torch
-    need = spec_verify_paged_attention_workspace_size(N, Hq, cache)
+    need = cache.workspace_need.get((N, Hq))
+    if need is None:
+        need = cache.workspace_need[N, Hq] = spec_verify_paged_attention_workspace_size(N, Hq, cache)
     if torch.cuda.is_current_stream_capturing():
         return torch.empty(need, dtype=torch.uint8, device=cache.device)
-    key = (cache.device, _stream_handle(stream, cache.device))
+    key = (cache.device, _raw_stream(None, cache.device))
     ws = _attend_ws.get(key)
-    if ws is None or ws.numel() < need:
-        ws = torch.empty(need, dtype=torch.uint8, device=cache.device)
-        _attend_ws[key] = ws
+    if ws is None or ws.nbytes < need:
+        ws = _attend_ws[key] = torch.empty(need, dtype=torch.uint8, device=cache.device)
     return ws
 
 
 def attend(q, cache, prefix_len, num_queries=None, tree_parents=None, scale=None, stream=None):
     """Allocates the outputs, runs spec_verify_paged_attention and returns (out [B, N, Hq, D],
-    lse [B, N, Hq])."""
+    lse [B, N, Hq]), both of the given stream (the current one unless given)."""
     import torch
     if stream is not None:
-        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), cache.device)
-        with torch.cuda.stream(s):
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), cache.device)
+        with torch.cuda.stream(stream):
             return attend(q, cache, prefix_len, num_queries, tree_parents, scale)
-    out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
-    ws = _attend_workspace(q.shape[1], q.shape[2], cache, None)
-    spec_verify_paged_attention(q, cache, prefix_len, num_queries, tree_parents, out, lse, ws, scale)
+    B, N, Hq, D = q.shape
+    out = torch.empty((B, N, Hq, D), dtype=q.dtype, device=q.device)
+    lse = torch.empty((B, N, Hq), dtype=torch.float32, device=q.device)
+    spec_verify_paged_attention(q, cache, prefix_len, num_queries, tree_parents, out, lse,
+                                _attend_workspace(N, Hq, cache), scale)
     return out, lse

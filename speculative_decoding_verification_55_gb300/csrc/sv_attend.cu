@@ -391,8 +391,8 @@ constexpr size_t kSharedBytes = 2 * kMaxSms * sizeof(int4);
 template <bool F16, int D, int MT>
 int launch(const AttendParams& P, const CUtensorMap& k, const CUtensorMap& v, int grid, cudaStream_t st) {
   auto kern = sv_attend_kernel<F16, D, MT>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (kSmemBytes<D, MT>)) != cudaSuccess)
-    return SV_ERR_CUDA;
+  static std::atomic<unsigned long long> allowed{0};
+  if (sv::allow_shared(kern, (kSmemBytes<D, MT>), allowed) != SV_OK) return SV_ERR_CUDA;
   kern<<<grid, kThreads, (kSmemBytes<D, MT>), st>>>(P, k, v);
   return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }

@@ -451,8 +451,8 @@ template <bool F16, int D>
 int launch(const AttendParams& P, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& q, int q_tokens,
            int grid, cudaStream_t st) {
   auto kern = sv_attend_wide_kernel<F16, D>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes<D>) != cudaSuccess)
-    return SV_ERR_CUDA;
+  static std::atomic<unsigned long long> allowed{0};
+  if (sv::allow_shared(kern, (kSmemBytes<D>), allowed) != SV_OK) return SV_ERR_CUDA;
   kern<<<grid, kThreads, kSmemBytes<D>, st>>>(P, k, v, q, q_tokens);
   return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }

@@ -7,6 +7,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "../../include/spec_verify.h"
@@ -116,6 +117,17 @@ int query_tensor_map(const void* q, int64_t row_stride, int64_t token_stride, in
                      int32_t D, int32_t dtype, int heads, int tokens, CUtensorMap* map);
 // Slots of one box: a page's, at most 64.
 inline int box_rows(const sv_paged_cache* c) { return c->page_size < 64 ? c->page_size : 64; }
+// Allows a kernel its dynamic shared memory on the current device, once (`done`: a bit per device).
+template <typename K>
+inline int allow_shared(K kern, size_t bytes, std::atomic<unsigned long long>& done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SV_ERR_CUDA;
+  if ((done.load(std::memory_order_acquire) >> dev) & 1) return SV_OK;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) != cudaSuccess)
+    return SV_ERR_CUDA;
+  done.fetch_or(1ull << dev, std::memory_order_release);
+  return SV_OK;
+}
 // Multiprocessors of a device (sv_api.cu).
 int device_sms(int dev);
 

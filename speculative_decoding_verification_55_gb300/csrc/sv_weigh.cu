@@ -303,8 +303,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <bool F16, int D>
 int launch(const WeighParams& P, const CUtensorMap& k, const CUtensorMap& q, int grid, cudaStream_t st) {
   auto kern = sv_weigh_kernel<F16, D>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes<D>) != cudaSuccess)
-    return SV_ERR_CUDA;
+  static std::atomic<unsigned long long> allowed{0};
+  if (sv::allow_shared(kern, (kSmemBytes<D>), allowed) != SV_OK) return SV_ERR_CUDA;
   kern<<<grid, kThreads, kSmemBytes<D>, st>>>(P, k, q);
   return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
