@@ -80,16 +80,18 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2)
   sv::Walk W;
   W.begin(R, plan);
   if (warp == kWarps) {
-    // ---- Producer: page numbers are read one tile ahead of the copies that need them.
+    // ---- Producer
     sv::TileLoader T;
     T.init(C, 2, kTileLog2);
     int issued = 0;
     bool gone = false;
     while (!gone && W.next(R)) {
       const int entries = W.w.n + W.w.m;
-      int p = T.page(C, W.row, W.first, entries, lane);
-      for (int t = W.first; t < W.first + W.count; ++t) {
-        const int p_next = t + 1 < W.first + W.count ? T.page(C, W.row, t + 1, entries, lane) : -1;
+      const int last = W.first + W.count;
+      sv::PagesAhead pages;
+      pages.begin(T, C, W.row, W.first, last, entries, lane);
+      for (int t = W.first; t < last; ++t) {
+        const int p = pages.next(T, C, W.row, t, last, entries, lane);
         const int s = issued % kStages;
         const uint32_t bar = sv::smem_addr(full + s);
         if (issued >= kStages && !sv::mbar_wait(sv::smem_addr(empty + s), (issued / kStages - 1) & 1)) {
@@ -104,7 +106,6 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2)
         __syncwarp();
         if (p >= 0) T.load(C, &kmap, &vmap, t, W.head, p, lane, ring + s * kStageBytes<D>, bar);
         ++issued;
-        p = p_next;
       }
     }
     sv::fill_unused(P, D, lane, 32);           // while the last tiles are computed
@@ -373,20 +374,26 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2)
         else if (P.lse) P.lse[at] = (jm * c + log2f(jl)) * 0.6931471805599453f;
       }
     }
-    if (!whole && tid == 0 && W.first == 0) sv::tell_shared(P, W.row, W.head, W.q_tile, W.item_at, W.w.tiles, plan);
+    if (!whole && tid == 0 && W.first == 0) sv::tell_shared(P, 0, W.row, W.head, W.q_tile, W.item_at, W.w.tiles, plan);
     sv::named_bar_sync(1, kConsumers);         // the scratch is free for the next item's queries
   }
 }
 
-// The kernel and the query rows of an item: 16 where a key head has no more, else up to 128, whole tokens,
-// on the wide kernel; heads of 256, whose accumulators fill the registers here and tensor memory there,
-// take 16.
-bool is_wide(int N, int group, int D) { return N * group > 16 && D < 256; }
-int item_rows(int N, int group, int D) { return is_wide(N, group, D) ? 128 / group * group : 16; }
-int part_rows(int N, int group, int D) { return is_wide(N, group, D) ? 128 : 16; }
-int grid_limit(int sms, int N, int group, int D) { return sms * (D == 256 || is_wide(N, group, D) ? 1 : 2); }
+// The kernel and its query tiles: 16 rows where a key head has no more, else on the wide kernel up to 128 rows,
+// whole tokens, and two such tiles at once where there are more (the keys and values are then read once for
+// both; heads of 256 have no room for two accumulators). 4 rows of 32,000 entries with 248 query rows took
+// XX us a tile at a time, YY two at a time.
+struct Kernel {
+  bool wide;
+  int tile_rows, part_rows, ways, key_log2, ctas;     // CTAs: of an SM
+};
+Kernel kernel_for(int N, int group, int D) {
+  if (N * group <= 16) return {false, 16, 16, 1, kTileLog2, D == 256 ? 1 : 2};
+  const int rows = 128 / group * group;
+  return {true, rows, 128, N * group > rows && D < 256 ? 2 : 1, D == 256 ? 6 : 7, 1};
+}
 constexpr int kMaxSms = 160;
-constexpr size_t kSharedBytes = 2 * kMaxSms * sizeof(int4);
+constexpr size_t kSharedBytes = 2 * kMaxSms * sizeof(int4);   // two ways or two CTAs an SM
 
 template <bool F16, int D, int MT>
 int launch(const AttendParams& P, const CUtensorMap& k, const CUtensorMap& v, int grid, cudaStream_t st) {
@@ -404,9 +411,9 @@ extern "C" size_t spec_verify_paged_attention_workspace_size(int32_t N, int32_t 
   if (!cache || N < 1 || N > SV_MAX_GAMMA + 1 || Hq < 1 || Hq > 1024 || cache->heads < 1 ||
       Hq % cache->heads != 0 || Hq / cache->heads > 128 || cache->head_dim < 1 || cache->head_dim > 256)
     return 0;
-  const int D = cache->head_dim, group = Hq / cache->heads;
-  const size_t part = static_cast<size_t>(part_rows(N, group, D)) * (D * 4 + 8);
-  return kSharedBytes + (2 * grid_limit(kMaxSms, N, group, D) * part + 255) / 256 * 256;
+  const Kernel k = kernel_for(N, Hq / cache->heads, cache->head_dim);
+  const size_t part = static_cast<size_t>(k.ways) * k.part_rows * (cache->head_dim * 4 + 8);
+  return kSharedBytes + (2 * k.ctas * kMaxSms * part + 255) / 256 * 256;
 }
 
 extern "C" int spec_verify_paged_attention(const void* q, int64_t q_row_stride,
@@ -432,8 +439,8 @@ extern "C" int spec_verify_paged_attention(const void* q, int64_t q_row_stride,
   int dev = 0;
   st = sv::current_device_status(&dev);
   if (st != SV_OK) return st;
-  const int D = cache->head_dim, group = Hq / cache->heads, item = item_rows(N, group, D);
-  const bool wide = is_wide(N, group, D);
+  const int D = cache->head_dim, group = Hq / cache->heads;
+  const Kernel k = kernel_for(N, group, D);
   CUtensorMap kmap, vmap;
   st = sv::cache_tensor_map(cache, cache->k, sv::box_rows(cache), &kmap);
   if (st == SV_OK) st = sv::cache_tensor_map(cache, cache->v, sv::box_rows(cache), &vmap);
@@ -443,9 +450,9 @@ extern "C" int spec_verify_paged_attention(const void* q, int64_t q_row_stride,
   P.R.B = B;
   P.R.N = N;
   P.R.group = group;
-  P.R.q_rows = item;
-  P.R.tile_log2 = wide ? 7 : kTileLog2;
-  P.R.extra = wide ? 2 : 1;
+  P.R.q_rows = k.tile_rows * k.ways;
+  P.R.tile_log2 = k.key_log2;
+  P.R.extra = k.wide ? 2 : 1;
   P.R.none_ok = false;
   P.q = static_cast<const char*>(q);
   P.row_stride = q_row_stride * 2;
@@ -455,25 +462,26 @@ extern "C" int spec_verify_paged_attention(const void* q, int64_t q_row_stride,
   P.lse = out_lse;
   P.c = scale * sv::kLog2e;
   P.Hq = Hq;
+  P.tile_rows = k.tile_rows;
+  P.ways = k.ways;
   // As many CTAs as the GPU holds, or as many as the batch can have tiles.
   int sms = sv::device_sms(dev);
   if (sms < 1) return SV_ERR_CUDA;
   if (sms > kMaxSms) sms = kMaxSms;
   const long long tile = 1 << P.R.tile_log2;
-  const long long most = static_cast<long long>(B) * cache->heads * ((N * group + item - 1) / item) *
-                         ((static_cast<long long>(cache->max_pages) * cache->page_size + tile - 1) / tile);
-  const int limit = grid_limit(sms, N, group, D);
-  const int grid = static_cast<int>(most < limit ? most : limit);
+  const long long items = static_cast<long long>(B) * cache->heads * ((N * group + P.R.q_rows - 1) / P.R.q_rows);
+  const long long most = items * ((static_cast<long long>(cache->max_pages) * cache->page_size + tile - 1) / tile);
+  const int grid = static_cast<int>(most < sms * k.ctas ? most : sms * k.ctas);
   char* ws = static_cast<char*>(workspace);
   P.shared = reinterpret_cast<int4*>(ws);
   ws += kSharedBytes;
   P.part_ml = reinterpret_cast<float2*>(ws);
-  P.part_o = reinterpret_cast<float*>(ws + static_cast<size_t>(2) * grid * part_rows(N, group, D) * 8);
+  P.part_o = reinterpret_cast<float*>(ws + static_cast<size_t>(2) * grid * k.ways * k.part_rows * 8);
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   const bool f16 = cache->dtype == SV_DTYPE_F16;
-  if (wide) {
+  if (k.wide) {
     CUtensorMap qmap;
-    const int tokens = item / group < N ? item / group : N;
+    const int tokens = k.tile_rows / group < N ? k.tile_rows / group : N;
     st = sv::query_tensor_map(q, q_row_stride, q_token_stride, B, N, Hq, D, cache->dtype, group, tokens, &qmap);
     if (st != SV_OK) return st;
     st = sv::launch_attend_wide(P, f16, kmap, vmap, qmap, tokens, grid, s);
@@ -482,6 +490,5 @@ extern "C" int spec_verify_paged_attention(const void* q, int64_t q_row_stride,
   else if (D == 128) st = f16 ? launch<true, 128, 1>(P, kmap, vmap, grid, s) : launch<false, 128, 1>(P, kmap, vmap, grid, s);
   else st = f16 ? launch<true, 256, 1>(P, kmap, vmap, grid, s) : launch<false, 256, 1>(P, kmap, vmap, grid, s);
   // Fewer items than a quarter of the CTAs: each has many parts.
-  const long long items = static_cast<long long>(B) * cache->heads * ((N * group + item - 1) / item);
-  return st == SV_OK ? sv::launch_attend_join(P, f16, wide, items * 4 <= grid, grid, s) : st;
+  return st == SV_OK ? sv::launch_attend_join(P, f16, k.wide, items * 4 <= grid, grid, s) : st;
 }

@@ -14,12 +14,14 @@ struct AttendParams {
   float* lse;
   float c;                                     // scale * log2(e)
   int Hq;
+  int tile_rows, ways;                         // query rows of a query tile, query tiles of an item
   // Items that several CTAs share leave a part each, which the join kernel puts together. An item's
-  // first part is part 2 p + 1 of the CTA p that holds its first tile, the others part 2 p of theirs.
-  int4* shared;                                // [grid] the shared item whose first tile a CTA holds: row
-                                               // (-1: none), head, query tile, the last CTA
-  float* part_o;                               // [2 grid][D][rows]
-  float2* part_ml;                             // [2 grid][rows] maximum and sum
+  // first part is part 2 p + 1 of the CTA p that holds its first tile, the others part 2 p of theirs, each a
+  // tile of rows per way.
+  int4* shared;                                // [grid][ways] the shared item whose first tile a CTA holds:
+                                               // row (-1: none), head, query tile, the last CTA
+  float* part_o;                               // [2 grid][ways][D][rows]
+  float2* part_ml;                             // [2 grid][ways][rows] maximum and sum
 };
 
 template <bool F16>
@@ -64,16 +66,16 @@ __device__ __forceinline__ void fill_unused(const AttendParams& P, int D, int ti
 }
 
 // The item that this CTA begins and does not end, for the join kernel (one thread).
-__device__ __forceinline__ void tell_shared(const AttendParams& P, int row, int head, int q_tile,
+__device__ __forceinline__ void tell_shared(const AttendParams& P, int way, int row, int head, int q_tile,
                                             long long item_at, int tiles, const Plan& plan) {
-  P.shared[blockIdx.x] = make_int4(row, head, q_tile, unit_owner(item_at + tiles - 1, plan));
+  P.shared[blockIdx.x * P.ways + way] = make_int4(row, head, q_tile, unit_owner(item_at + tiles - 1, plan));
 }
 
 // Joins the parts of the items that the attention kernel's `grid` CTAs shared.
 int launch_attend_join(const AttendParams& P, bool f16, bool wide, bool many_parts, int grid, cudaStream_t st);
 
-// The wide kernel (64 or 128 elements a head, at most 128 query heads a key head; query tiles of
-// q_rows <= 128 rows, whole tokens of which q's boxes hold q_tokens; key tiles of 128).
+// The wide kernel (at most 128 query heads a key head; query tiles of tile_rows <= 128 rows, whole tokens of
+// which q's boxes hold q_tokens; key tiles of 128, or of 64 for heads of 256; two ways up to heads of 128).
 int launch_attend_wide(const AttendParams& P, bool f16, const CUtensorMap& k, const CUtensorMap& v,
                        const CUtensorMap& q, int q_tokens, int grid, cudaStream_t st);
 

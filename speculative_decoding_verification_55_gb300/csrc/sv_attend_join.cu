@@ -25,12 +25,13 @@ __global__ void __launch_bounds__(kThreads) sv_attend_join_kernel(const sv::Atte
   __shared__ float2 ml[kWarps][32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const sv::Round& R = P.R;
-  const int c0 = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int4 it = __ldcg(P.shared + c0);
+  const int c0 = blockIdx.x / P.ways, way = blockIdx.x % P.ways;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int4 it = __ldcg(P.shared + blockIdx.x);
   if (it.x < 0) return;                                // no shared item begins in this CTA's run
   sv::RowWork w;
   sv::row_work(R, it.x, &w);
-  const int row0 = it.z * R.q_rows, rows = min(R.q_rows, w.m * R.group - row0);
+  const int row0 = it.z * P.tile_rows, rows = min(P.tile_rows, w.m * R.group - row0);
   const int g0 = (blockIdx.y / kColBlocks) * kRowLanes, col0 = (blockIdx.y % kColBlocks) * kColsHere;
   if (g0 >= rows) return;
   const float c = P.c;
@@ -42,7 +43,7 @@ __global__ void __launch_bounds__(kThreads) sv_attend_join_kernel(const sv::Atte
     for (int x = 0; x < kCols; ++x) a[x] = 0.0f;
 #pragma unroll 2
     for (int p = c0 + pg; p <= it.w; p += kPartGroups) {
-      const size_t part = 2 * p + (p == c0);
+      const size_t part = static_cast<size_t>(2 * p + (p == c0)) * P.ways + way;
       const float2 e = __ldcg(P.part_ml + part * kRows + r);
       float o[kCols];
 #pragma unroll
@@ -100,7 +101,7 @@ int launch2(const sv::AttendParams& P, int grid, cudaStream_t st) {
   constexpr int kRowLanes = kRows < 32 ? kRows : 32, kColsHere = kAcross * (32 / kRowLanes) * kCols;
   const int most = min(kRows, P.R.N * P.R.group);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, (most + kRowLanes - 1) / kRowLanes * (D / kColsHere));
+  cfg.gridDim = dim3(grid * P.ways, (most + kRowLanes - 1) / kRowLanes * (D / kColsHere));
   cfg.blockDim = dim3(kThreads);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
@@ -132,6 +133,7 @@ int launch_attend_join(const AttendParams& P, bool f16, bool wide, bool many_par
       if (wide) return f16 ? launch<true, 128, 128>(P, many_parts, grid, st) : launch<false, 128, 128>(P, many_parts, grid, st);
       return f16 ? launch<true, 128, 16>(P, many_parts, grid, st) : launch<false, 128, 16>(P, many_parts, grid, st);
     default:
+      if (wide) return f16 ? launch<true, 256, 128>(P, many_parts, grid, st) : launch<false, 256, 128>(P, many_parts, grid, st);
       return f16 ? launch<true, 256, 16>(P, many_parts, grid, st) : launch<false, 256, 16>(P, many_parts, grid, st);
   }
 }

@@ -32,19 +32,27 @@ using sv::AttendParams;
 using namespace sv::tmem;
 using sv::kFull;
 
-constexpr int kTileLog2 = 7, kTile = 1 << kTileLog2;   // entries of a key tile
-constexpr int kRows = 128;                             // query rows of an item
+constexpr int kRows = 128;                             // query rows of a product
 constexpr int kSoftWarps = 8, kSoft = 32 * kSoftWarps;
 constexpr int kThreads = kSoft + 96;                   // and the producer's, the products' and the items' warps
 constexpr int kProducer = kSoftWarps, kProducts = kSoftWarps + 1, kItems = kSoftWarps + 2;
 constexpr float kSlack = 8.0f;
-constexpr int kScoreTiles = 2;                         // tiles of scores in tensor memory
+constexpr int kScores = 2;                             // buffers of scores in tensor memory
 constexpr int kPieces = 8;                             // items that the warps may be apart, and one
 
-template <int D>
-constexpr int kSlotBytes = kTile * D * 2;              // a tile's keys or its values
-template <int D>
-constexpr int kSlotCount = D == 64 ? 12 : 6;           // keys and values of a tile in turn
+// kWays: query tiles of 128 rows that a CTA works on at once.
+template <int D, int kWays>
+struct Shape {
+  static constexpr int kTileLog2 = D == 256 ? 6 : 7, kTile = 1 << kTileLog2;   // entries of a key tile
+  static constexpr int kSlotBytes = kTile * D * 2;     // a tile's keys or its values
+  static constexpr int kQueryBytes = kWays * kRows * D * 2;
+  static constexpr int kSlots = D == 64 ? 12 : (D == 128 && kWays == 1 ? 6 : 5);   // keys and values in turn
+  static constexpr int kAccum = kScores * kTile;       // tensor memory columns: S0, S1, then an O a way
+  static constexpr int kCols = kWays == 2 ? kTile : kTile / 2;   // scores of a thread
+  static constexpr int kChunk = kCols < 64 ? kCols : 64;         // scores of a thread in registers
+  static constexpr int kOut = kWays == 2 ? D : D / 2;            // columns of O of a thread
+  static_assert(kAccum + kWays * D <= kColumns, "tensor memory");
+};
 
 // An item, or a CTA's part of one, as the items' warp found it: read from shared memory by the others, so
 // that none of them waits for lengths from global memory (2 us a load while the cache streams).
@@ -57,7 +65,7 @@ struct Item {
 // Shared memory behind the ring and the queries.
 template <int kSlots>
 struct Control {
-  unsigned long long full[kSlots], empty[kSlots], s_full[kScoreTiles], p_ready[kScoreTiles], o_full, q_full,
+  unsigned long long full[kSlots], empty[kSlots], s_full[kScores], p_ready[kScores], o_full, q_full,
       q_empty, told[kPieces], drained;
   long long scan[kThreads / 32];
   sv::Plan plan;
@@ -66,31 +74,31 @@ struct Control {
   int bad[kPieces], flags, lost;
   uint32_t tm;
 };
-template <int D>
-constexpr int kSmemBytes = kSlotCount<D> * kSlotBytes<D> + kRows * D * 2 + sizeof(Control<kSlotCount<D>>);
+template <int D, int kWays>
+constexpr int kSmemBytes = Shape<D, kWays>::kSlots * Shape<D, kWays>::kSlotBytes + Shape<D, kWays>::kQueryBytes +
+                           sizeof(Control<Shape<D, kWays>::kSlots>);
 
-template <bool F16, int D>
+template <bool F16, int D, int kWays>
 __global__ void __launch_bounds__(kThreads, 1)
     sv_attend_wide_kernel(const AttendParams P, const __grid_constant__ CUtensorMap kmap,
                           const __grid_constant__ CUtensorMap vmap,
                           const __grid_constant__ CUtensorMap qmap, int q_tokens) {
-  constexpr int kSlots = kSlotCount<D>;
-  constexpr int kAccum = kScoreTiles * kTile;          // columns: S0, S1, O
+  using H = Shape<D, kWays>;
+  constexpr int kSlots = H::kSlots, kTile = H::kTile, kAccum = H::kAccum;
   extern __shared__ __align__(1024) unsigned char dyn[];
-  auto& S = *reinterpret_cast<Control<kSlots>*>(dyn + kSlots * kSlotBytes<D> + kRows * D * 2);
+  auto& S = *reinterpret_cast<Control<kSlots>*>(dyn + kSlots * H::kSlotBytes + H::kQueryBytes);
   const sv::Round& R = P.R;
   const sv::Cache& C = R.C;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t ring = sv::smem_addr(dyn), qs = ring + kSlots * kSlotBytes<D>;
-  unsigned char* const qs_p = dyn + kSlots * kSlotBytes<D>;
+  const uint32_t ring = sv::smem_addr(dyn), qs = ring + kSlots * H::kSlotBytes;
   if (tid == 0) {
     for (int s = 0; s < kSlots; ++s) {
       sv::mbar_init(sv::smem_addr(S.full + s), 1);
       sv::mbar_init(sv::smem_addr(S.empty + s), 1);
     }
-    for (int w = 0; w < kScoreTiles; ++w) {
+    for (int w = 0; w < kScores; ++w) {
       sv::mbar_init(sv::smem_addr(S.s_full + w), 1);
-      sv::mbar_init(sv::smem_addr(S.p_ready + w), kSoftWarps);
+      sv::mbar_init(sv::smem_addr(S.p_ready + w), kSoftWarps / kWays);
     }
     sv::mbar_init(sv::smem_addr(&S.o_full), 1);
     sv::mbar_init(sv::smem_addr(&S.drained), 1);
@@ -103,7 +111,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kProducts) tm_alloc(&S.tm);
   sv::make_plan<kThreads>(R, S.scan, &S.plan);
   asm volatile("griddepcontrol.launch_dependents;");   // the join kernel's CTAs, which wait for this grid's end
-  if (tid == 0) P.shared[blockIdx.x].x = -1;
+  if (tid < kWays) P.shared[blockIdx.x * kWays + tid].x = -1;
   fence_after();
   const uint32_t tm = S.tm;
   volatile int* const lost = &S.lost;
@@ -118,17 +126,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kProducer) {
     sv::Walk W;
     W.begin(R, S.plan);
-    // ---- Copies: page numbers are read one tile ahead of the copies that need them.
+    // ---- Copies
     sv::TileLoader T;
-    T.init(C, 1, kTileLog2);
+    T.init(C, 1, H::kTileLog2);
     int armed = 0, items = 0;                  // slots (tile x: 2 x and 2 x + 1) and items so far
     bool gone = false;
     while (!gone && W.next(R)) {
       const int entries = W.w.n + W.w.m;
-      int p = T.page(C, W.row, W.first, entries, lane);
+      const int last = W.first + W.count;
+      sv::PagesAhead pages;
+      pages.begin(T, C, W.row, W.first, last, entries, lane);
       if (lane == 0) S.bad[items % kPieces] = 0;
-      for (int t = W.first; t < W.first + W.count && !gone; ++t) {
-        const int p_next = t + 1 < W.first + W.count ? T.page(C, W.row, t + 1, entries, lane) : -1;
+      for (int t = W.first; t < last && !gone; ++t) {
+        const int p = pages.next(T, C, W.row, t, last, entries, lane);
         const unsigned go = __ballot_sync(kFull, p >= 0), out = __ballot_sync(kFull, p == -2);
         if (lane == 0 && out) S.bad[items % kPieces] = 1;
 #pragma unroll
@@ -142,10 +152,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (lane == 0) sv::mbar_arrive_expect_tx(bar, static_cast<uint32_t>(__popc(go)) << (T.rows_log2 + 7));
           __syncwarp();
-          if (p >= 0) T.load(C, array ? &vmap : &kmap, nullptr, t, W.head, p, lane, ring + s * kSlotBytes<D>, bar);
+          if (p >= 0) T.load(C, array ? &vmap : &kmap, nullptr, t, W.head, p, lane, ring + s * H::kSlotBytes, bar);
           ++armed;
         }
-        p = p_next;
       }
       ++items;
     }
@@ -154,44 +163,48 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int e = max(0, armed - kSlots); e < armed; ++e)
       sv::mbar_wait_drain(sv::smem_addr(S.full + e % kSlots), (e / kSlots) & 1);
   } else if (warp == kProducts) {
-    // ---- Products, by one thread: scores run three tiles ahead of the products with the values.
+    // ---- Products, by one thread. Score buffer w of tile x: one way, w = x % 2, two tiles ahead of the
+    // products with the values; two ways, w the way, a tile ahead.
     if (lane == 0) {
       constexpr uint32_t ds = product_desc<F16>(kTile, false), dp = product_desc<F16>(D, true);
-      int base = 0, items = 0;
-      auto scores = [&](int idx) {
-        const int x = base + idx, s = (2 * x) % kSlots, w = x % kScoreTiles;
-        if (!wait_unless_lost(sv::smem_addr(S.full + s), (2 * x / kSlots) & 1, lost)) return;
+      int base = 0, items = 0, count = 0;
+      auto scores = [&](int idx, int way) {
+        const int x = base + idx, s = (2 * x) % kSlots, w = kWays == 2 ? way : x % kScores;
+        if (way == 0 && !wait_unless_lost(sv::smem_addr(S.full + s), (2 * x / kSlots) & 1, lost)) return;
         fence_after();
-        const uint32_t kb = ring + s * kSlotBytes<D>;
+        const uint32_t kb = ring + s * H::kSlotBytes, qb = qs + way * (kRows * D * 2);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
-          product_ss(tm + w * kTile,
-                     matrix_desc(qs + (k >> 2) * (kRows * 128) + (k & 3) * 32, 16, 1024),
+          product_ss(tm + w * kTile, matrix_desc(qb + (k >> 2) * (kRows * 128) + (k & 3) * 32, 16, 1024),
                      matrix_desc(kb + (k >> 2) * (kTile * 128) + (k & 3) * 32, 16, 1024), ds, k > 0);
         products_done(sv::smem_addr(S.s_full + w));
+        if (way + 1 < kWays) return;
         products_done(sv::smem_addr(S.empty + s));
+        if (idx + 1 == count) products_done(sv::smem_addr(&S.q_empty));
       };
+      constexpr int kAhead = kWays == 2 ? 1 : kScores;
       for (;;) {
-        const int count = told(items).count;
+        count = told(items).count;
         if (count == 0 || !wait_unless_lost(sv::smem_addr(&S.q_full), items & 1, lost)) break;
         fence_after();
-        for (int idx = 0; idx < count && idx < kScoreTiles; ++idx) scores(idx);
-        if (count <= kScoreTiles) products_done(sv::smem_addr(&S.q_empty));
-        for (int idx = 0; idx < count; ++idx) {
-          const int x = base + idx, s = (2 * x + 1) % kSlots, w = x % kScoreTiles;
-          if (!wait_unless_lost(sv::smem_addr(S.full + s), ((2 * x + 1) / kSlots) & 1, lost) ||
-              !wait_unless_lost(sv::smem_addr(S.p_ready + w), (x / kScoreTiles) & 1, lost))
-            break;
-          fence_after();
-          const uint32_t vb = ring + s * kSlotBytes<D>;
+        for (int idx = 0; idx < count && idx < kAhead; ++idx)
+          for (int way = 0; way < kWays; ++way) scores(idx, way);
+        for (int idx = 0; idx < count && !*lost; ++idx) {
+          const int x = base + idx, s = (2 * x + 1) % kSlots;
+          const uint32_t vb = ring + s * H::kSlotBytes;
 #pragma unroll
-          for (int k = 0; k < kTile / 16; ++k)
-            product_ts(tm + kAccum, tm + w * kTile + k * 8, matrix_desc(vb + k * 2048, kTile * 128, 1024), dp,
-                       idx > 0 || k > 0);
-          products_done(sv::smem_addr(S.empty + s));
-          if (idx + kScoreTiles < count) {
-            scores(idx + kScoreTiles);
-            if (idx + kScoreTiles + 1 == count) products_done(sv::smem_addr(&S.q_empty));
+          for (int way = 0; way < kWays; ++way) {
+            const int w = kWays == 2 ? way : x % kScores, turn = kWays == 2 ? x : x / kScores;
+            if ((way == 0 && !wait_unless_lost(sv::smem_addr(S.full + s), ((2 * x + 1) / kSlots) & 1, lost)) ||
+                !wait_unless_lost(sv::smem_addr(S.p_ready + w), turn & 1, lost))
+              break;
+            fence_after();
+#pragma unroll
+            for (int k = 0; k < kTile / 16; ++k)
+              product_ts(tm + kAccum + way * D, tm + w * kTile + k * 8, matrix_desc(vb + k * 2048, kTile * 128, 1024),
+                         dp, idx > 0 || k > 0);
+            if (way + 1 == kWays) products_done(sv::smem_addr(S.empty + s));
+            if (idx + kAhead < count) scores(idx + kAhead, way);
           }
         }
         products_done(sv::smem_addr(&S.o_full));
@@ -227,26 +240,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!more) break;
       if (!__all_sync(kFull, k == 0 || wait_unless_lost(sv::smem_addr(&S.q_empty), (k - 1) & 1, lost))) continue;
       if (lane == 0) {
-        sv::mbar_arrive_expect_tx(sv::smem_addr(&S.q_full), q_tokens * R.group * D * 2);
-        for (int half = 0; half < D / 64; ++half)
-          sv::tma_load(qs + half * (kRows * 128), &qmap, half * 64, W.head * R.group, W.q_tile * (R.q_rows / R.group),
-                       W.row, sv::smem_addr(&S.q_full));
+        sv::mbar_arrive_expect_tx(sv::smem_addr(&S.q_full), kWays * q_tokens * R.group * D * 2);
+        for (int x = 0; x < kWays * (D / 64); ++x)
+          sv::tma_load(qs + x * (kRows * 128), &qmap, x % (D / 64) * 64, W.head * R.group,
+                       (W.q_tile * kWays + x / (D / 64)) * (P.tile_rows / R.group), W.row, sv::smem_addr(&S.q_full));
       }
       ++copies;
     }
     if (copies > 0) sv::mbar_wait_drain(sv::smem_addr(&S.q_full), (copies - 1) & 1);   // the last queries are in
   } else {
     // ---- Softmax
-    const int half = warp >> 2, wq = warp & 3, row = 32 * wq + lane;   // half: of a tile's entries, of D
+    // One way: two warps share rows, `half` a tile's entries and D each. Two ways: four warps have a way.
+    const int half = kWays == 2 ? 0 : warp >> 2, way = kWays == 2 ? warp >> 2 : 0;
+    const int wq = warp & 3, row = 32 * wq + lane;
     const uint32_t lanes = static_cast<uint32_t>(32 * wq) << 16;
-    const uint32_t to = tm + lanes + kAccum + half * (D / 2);
+    const uint32_t to = tm + lanes + kAccum + way * D + half * H::kOut;
     const float c = P.c;
     int base = 0, items = 0;
     for (;;) {
       const Item W = told(items);
       if (W.count == 0) break;
       const int n = W.n, m = W.m, entries = n + m;
-      const int row0 = W.q_tile * R.q_rows, rows = min(R.q_rows, m * R.group - row0);
+      const int row0 = (W.q_tile * kWays + way) * P.tile_rows, rows = min(P.tile_rows, m * R.group - row0);
       if (tid == 0) S.flags = 0;                // nobody sets one before this thread's first tile is used
       bool bad = W.bad != 0;
       const int last = W.first + W.count;
@@ -258,40 +273,44 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool odd = false;
 
       for (int idx = 0; idx < W.count; ++idx) {
-        const int x = base + idx, s = (2 * x + 1) % kSlots, w = x % kScoreTiles;
+        const int x = base + idx, s = (2 * x + 1) % kSlots;
+        const int w = kWays == 2 ? way : x % kScores, turn = kWays == 2 ? x : x / kScores;
         const int j0 = (W.first + idx) * kTile;
         const bool edge = j0 + kTile > n;      // entries of the round itself, or behind the last
-        bool go = wait_unless_lost(sv::smem_addr(S.s_full + w), (x / kScoreTiles) & 1, lost);
+        bool go = wait_unless_lost(sv::smem_addr(S.s_full + w), turn & 1, lost);
         if (edge || idx + 1 == W.count)        // the values are in, and the producer has seen all pages
           go = go && wait_unless_lost(sv::smem_addr(S.full + s), ((2 * x + 1) / kSlots) & 1, lost);
         if (!__all_sync(kFull, go)) {          // a wait gave up: the barriers alone
-          if (active) sv::named_bar_sync(2 + wq, 64);
+          if (active && kWays == 1) sv::named_bar_sync(2 + wq, 64);
           continue;
         }
         fence_after();
         if (idx + 1 == W.count) bad |= S.bad[items % kPieces] != 0;
         if (active) {
           const uint32_t ts = tm + lanes + w * kTile;
-          uint32_t sc[64];
-          tm_load64(sc, ts + 64 * half);
-          if (edge) {
-            const uint64_t see = sv::seen_bits(j0 + 64 * half - n, tok, mask, par);
+          uint32_t sc[H::kChunk];
+          auto load = [&](int y) {               // scores y.. of this thread's
+            tm_load<H::kChunk>(sc, ts + half * H::kCols + y);
+            if (!edge) return;
+            const uint64_t see = sv::seen_bits(j0 + half * H::kCols + y - n, tok, mask, par);
             const uint32_t lo = static_cast<uint32_t>(see), hi = static_cast<uint32_t>(see >> 32);
 #pragma unroll
-            for (int z = 0; z < 32; ++z) {
-              if (!((lo >> z) & 1)) sc[z] = 0xff800000u;
-              if (!((hi >> z) & 1)) sc[32 + z] = 0xff800000u;
-            }
-          }
+            for (int z = 0; z < H::kChunk; ++z)
+              if (!(((z < 32 ? lo : hi) >> (z & 31)) & 1)) sc[z] = 0xff800000u;
+          };
           float v[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int z = 0; z < 64; ++z) v[z & 3] = fmaxf(v[z & 3], __uint_as_float(sc[z]));
+          for (int y = 0; y < H::kCols; y += H::kChunk) {
+            load(y);
+#pragma unroll
+            for (int z = 0; z < H::kChunk; ++z) v[z & 3] = fmaxf(v[z & 3], __uint_as_float(sc[z]));
+          }
           float top = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
-          S.row_max[x & 1][half][row] = top;
-          fence_before();
-          sv::named_bar_sync(2 + wq, 64);      // the two warps of these rows: both have read their scores
-          fence_after();
-          top = fmaxf(top, S.row_max[x & 1][half ^ 1][row]);
+          if (kWays == 1) {
+            S.row_max[x & 1][half][row] = top;
+            sv::named_bar_sync(2 + wq, 64);      // the two warps of these rows: both have read their scores
+            top = fmaxf(top, S.row_max[x & 1][half ^ 1][row]);
+          }
           // The first tile sets the maximum; later ones move it when it has grown by over kSlack.
           const bool grew = top > mx && (mx == -INFINITY || (top - mx) * c > kSlack);
           if (__any_sync(kFull, grew)) {
@@ -304,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               __syncwarp();
               fence_after();
 #pragma unroll
-              for (int y = 0; y < D / 2; y += 16) {
+              for (int y = 0; y < H::kOut; y += 16) {
                 uint32_t o[16];
                 tm_load16(o, to + y);
 #pragma unroll
@@ -316,17 +335,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float b = mx == -INFINITY ? 0.0f : -mx * c;
           const sv::f32x2 c2 = sv::pk(c, c), b2 = sv::pk(b, b);
           sv::f32x2 sum[2] = {sv::pk(0.0f, 0.0f), sv::pk(0.0f, 0.0f)};
-          uint32_t p[32];
 #pragma unroll
-          for (int z = 0; z < 32; ++z) {
-            float p0, p1;
-            sv::upk(sv::fma2(sv::pk(__uint_as_float(sc[2 * z]), __uint_as_float(sc[2 * z + 1])), c2, b2), p0, p1);
-            p0 = sv::ex2(p0);
-            p1 = sv::ex2(p1);
-            sum[z & 1] = sv::add2(sum[z & 1], sv::pk(p0, p1));
-            p[z] = sv::pack2<F16>(p0, p1);
+          for (int y = 0; y < H::kCols; y += H::kChunk) {
+            if (H::kCols > H::kChunk) load(y);   // read again: all of a row would not fit the registers
+            uint32_t p[H::kChunk / 2];
+#pragma unroll
+            for (int z = 0; z < H::kChunk / 2; ++z) {
+              float p0, p1;
+              sv::upk(sv::fma2(sv::pk(__uint_as_float(sc[2 * z]), __uint_as_float(sc[2 * z + 1])), c2, b2), p0, p1);
+              p0 = sv::ex2(p0);
+              p1 = sv::ex2(p1);
+              sum[z & 1] = sv::add2(sum[z & 1], sv::pk(p0, p1));
+              p[z] = sv::pack2<F16>(p0, p1);
+            }
+            tm_store<H::kChunk / 2>(ts + (half * H::kCols + y) / 2, p);
           }
-          tm_store32(ts + 32 * half, p);
           float s0, s1;
           sv::upk(sv::add2(sum[0], sum[1]), s0, s1);
           l += s0 + s1;
@@ -335,9 +358,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (edge) {
           // Value rows of the round's own entries: what is not finite is cleared; rows behind the last
           // entry are cleared whole.
-          unsigned char* vb = dyn + s * kSlotBytes<D>;
+          unsigned char* vb = dyn + s * H::kSlotBytes;
           const int r0 = max(n - j0, 0);
-          for (int y = r0 * (D / 8) + tid; y < kTile * (D / 8); y += kSoft) {
+          // (Two ways: the first way's warps, whose product comes first.)
+          for (int y = r0 * (D / 8) + tid; way == 0 && y < kTile * (D / 8); y += kSoft / kWays) {
             const int r = y / (D / 8), ch = y % (D / 8);
             uint4* at = reinterpret_cast<uint4*>(vb + (ch >> 3) * (kTile * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
             uint4 v = make_uint4(0u, 0u, 0u, 0u);
@@ -367,21 +391,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       base += W.count;
       ++items;
 
-      // A row's sum is that of its two threads; each finishes half of the row's columns.
+      // One way: a row's sum is that of its two threads; each finishes half of the row's columns.
       float* sums = &S.row_max[0][0][0];       // [2][kRows]; the tiles are done with it
-      sums[half * kRows + row] = l;
+      if (kWays == 1) sums[half * kRows + row] = l;
       sv::named_bar_sync(1, kSoft);
       const int flags = S.flags;
-      const float jl = (flags & 1) ? __int_as_float(0x7fffffff) : sums[row] + sums[kRows + row];
+      const float jl = (flags & 1) ? __int_as_float(0x7fffffff) : (kWays == 1 ? sums[row] + sums[kRows + row] : l);
       const bool whole = W.count == W.tiles;
-      const int slot = 2 * blockIdx.x + (W.first == 0 ? 1 : 0);
+      const int slot = (2 * blockIdx.x + (W.first == 0 ? 1 : 0)) * kWays + way;
       const int i = (row0 + row) / R.group, hq = W.head * R.group + (row0 + row) - i * R.group;
       const size_t at = (static_cast<size_t>(W.row) * R.N + i) * P.Hq + hq;
       const float inv = 1.0f / jl;
 #pragma unroll
-      for (int k = 0; k < D / 2; k += 16) {
+      for (int k = 0; k < H::kOut; k += 16) {
         if (!active) break;
-        const int mycol = half * (D / 2) + k;
+        const int mycol = half * H::kOut + k;
         uint32_t o[16];
         tm_load16(o, to + k);
         float f[16];
@@ -423,7 +447,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       fence_before();
       sv::named_bar_sync(1, kSoft);            // the sums have been read
-      if (!whole && tid == 0 && W.first == 0) sv::tell_shared(P, W.row, W.head, W.q_tile, W.item_at, W.tiles, S.plan);
+      if (!whole && (tid & 127) == 0 && half == 0 && W.first == 0 && rows > 0)
+        sv::tell_shared(P, way, W.row, W.head, W.q_tile * kWays + way, W.item_at, W.tiles, S.plan);
     }
     fence_before();
   }
@@ -431,30 +456,44 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (S.lost) {                                // a wait gave up: NaN for the whole run
     sv::Walk W;
     W.begin(R, S.plan);
-    while (W.next(R)) {
-      const int row0 = W.q_tile * R.q_rows, rows = min(R.q_rows, W.w.m * R.group - row0);
-      const bool whole = W.count == W.w.tiles;
-      for (int x = tid; x < rows * D; x += kThreads) {
-        const int r = x / D, i = (row0 + r) / R.group, hq = W.head * R.group + (row0 + r) - i * R.group;
-        const size_t at = (static_cast<size_t>(W.row) * R.N + i) * P.Hq + hq;
-        if (whole) static_cast<unsigned short*>(P.out)[at * D + x % D] = 0x7fffu;
-        if (x % D == 0 && whole && P.lse) P.lse[at] = __int_as_float(0x7fffffff);
-        if (x % D == 0 && !whole) P.part_ml[(2 * blockIdx.x + (W.first == 0 ? 1 : 0)) * kRows + r].y = __int_as_float(0x7fffffff);
+    while (W.next(R))
+      for (int way = 0; way < kWays; ++way) {
+        const int q_tile = W.q_tile * kWays + way, row0 = q_tile * P.tile_rows;
+        const int rows = min(P.tile_rows, W.w.m * R.group - row0);
+        const bool whole = W.count == W.w.tiles;
+        for (int x = tid; x < rows * D; x += kThreads) {
+          const int r = x / D, i = (row0 + r) / R.group, hq = W.head * R.group + (row0 + r) - i * R.group;
+          const size_t at = (static_cast<size_t>(W.row) * R.N + i) * P.Hq + hq;
+          const int slot = (2 * blockIdx.x + (W.first == 0 ? 1 : 0)) * kWays + way;
+          if (whole) static_cast<unsigned short*>(P.out)[at * D + x % D] = 0x7fffu;
+          if (x % D == 0 && whole && P.lse) P.lse[at] = __int_as_float(0x7fffffff);
+          if (x % D == 0 && !whole) P.part_ml[slot * kRows + r].y = __int_as_float(0x7fffffff);
+        }
+        if (!whole && tid == 0 && W.first == 0 && rows > 0)
+          sv::tell_shared(P, way, W.row, W.head, q_tile, W.item_at, W.w.tiles, S.plan);
       }
-      if (!whole && tid == 0 && W.first == 0) sv::tell_shared(P, W.row, W.head, W.q_tile, W.item_at, W.w.tiles, S.plan);
-    }
   }
   if (warp == kProducts) tm_free(tm);
 }
 
-template <bool F16, int D>
+template <bool F16, int D, int kWays>
 int launch(const AttendParams& P, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& q, int q_tokens,
            int grid, cudaStream_t st) {
-  auto kern = sv_attend_wide_kernel<F16, D>;
+  auto kern = sv_attend_wide_kernel<F16, D, kWays>;
   static std::atomic<unsigned long long> allowed{0};
-  if (sv::allow_shared(kern, (kSmemBytes<D>), allowed) != SV_OK) return SV_ERR_CUDA;
-  kern<<<grid, kThreads, kSmemBytes<D>, st>>>(P, k, v, q, q_tokens);
+  if (sv::allow_shared(kern, (kSmemBytes<D, kWays>), allowed) != SV_OK) return SV_ERR_CUDA;
+  kern<<<grid, kThreads, (kSmemBytes<D, kWays>), st>>>(P, k, v, q, q_tokens);
   return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+}
+
+template <bool F16>
+int launch_type(const AttendParams& P, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& q, int q_tokens,
+                int grid, cudaStream_t st) {
+  const int D = P.R.C.head_dim;
+  if (D == 256) return launch<F16, 256, 1>(P, k, v, q, q_tokens, grid, st);
+  if (D == 128)
+    return P.ways == 2 ? launch<F16, 128, 2>(P, k, v, q, q_tokens, grid, st) : launch<F16, 128, 1>(P, k, v, q, q_tokens, grid, st);
+  return P.ways == 2 ? launch<F16, 64, 2>(P, k, v, q, q_tokens, grid, st) : launch<F16, 64, 1>(P, k, v, q, q_tokens, grid, st);
 }
 
 }  // namespace
@@ -463,9 +502,7 @@ namespace sv {
 
 int launch_attend_wide(const AttendParams& P, bool f16, const CUtensorMap& k, const CUtensorMap& v,
                        const CUtensorMap& q, int q_tokens, int grid, cudaStream_t st) {
-  if (P.R.C.head_dim == 64)
-    return f16 ? launch<true, 64>(P, k, v, q, q_tokens, grid, st) : launch<false, 64>(P, k, v, q, q_tokens, grid, st);
-  return f16 ? launch<true, 128>(P, k, v, q, q_tokens, grid, st) : launch<false, 128>(P, k, v, q, q_tokens, grid, st);
+  return f16 ? launch_type<true>(P, k, v, q, q_tokens, grid, st) : launch_type<false>(P, k, v, q, q_tokens, grid, st);
 }
 
 }  // namespace sv

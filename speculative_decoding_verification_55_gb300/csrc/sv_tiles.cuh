@@ -164,13 +164,15 @@ struct TileLoader {
     halves_log2 = C.head_dim == 64 ? 0 : (C.head_dim == 128 ? 1 : 2);
     ops = arrays << (boxes_log2 + halves_log2);
   }
-  // Page of operation `op` of a tile: -1 when it lies behind the row's entries, -2 when out of range.
-  __device__ __forceinline__ int page(const Cache& C, int row, int tile, int entries, int op) const {
+  // Whether operation `op` of a tile copies entries of the row, and the page number it then has (unchecked: a
+  // use of the number waits for its load).
+  __device__ __forceinline__ bool has(int tile, int entries, int op) const {
     const int box = (op >> halves_log2) & ((1 << boxes_log2) - 1);
-    const int j = (tile << tile_log2) + (box << rows_log2);
-    if (op >= ops || j >= entries) return -1;
-    const int p = cache_page(C, row, j);
-    return page_ok(C, p) ? p : -2;
+    return op < ops && (tile << tile_log2) + (box << rows_log2) < entries;
+  }
+  __device__ __forceinline__ int page(const Cache& C, int row, int tile, int op) const {
+    const int box = (op >> halves_log2) & ((1 << boxes_log2) - 1);
+    return cache_page(C, row, (tile << tile_log2) + (box << rows_log2));
   }
   // The copy of operation `op`: stage holds the arrays one after the other, each [D / 64][tile][64].
   __device__ __forceinline__ void load(const Cache& C, const CUtensorMap* k, const CUtensorMap* v,
@@ -182,6 +184,30 @@ struct TileLoader {
     const int j = (tile << tile_log2) + (box << rows_log2);
     const uint32_t dst = stage + (((array << halves_log2) + half) << (tile_log2 + 7)) + (box << (rows_log2 + 7));
     tma_load(dst, array ? v : k, half * 64, j & (C.page_size - 1), head, p, bar);
+  }
+};
+
+// A lane's pages of the tiles of a run, read kPagesAhead tiles before the copies that need them: a load
+// takes about as long as a tile while the cache streams (one tile ahead, a tile took 0.85 us whatever its size).
+constexpr int kPagesAhead = 4;
+struct PagesAhead {
+  int p[kPagesAhead];
+
+  __device__ __forceinline__ void begin(const TileLoader& T, const Cache& C, int row, int first, int last,
+                                        int entries, int op) {
+#pragma unroll
+    for (int x = 0; x < kPagesAhead; ++x)
+      p[x] = first + x < last && T.has(first + x, entries, op) ? T.page(C, row, first + x, op) : 0;
+  }
+  // The page of `tile`: -1 where the operation copies nothing, -2 when it is out of range. Reads that of
+  // tile + kPagesAhead.
+  __device__ __forceinline__ int next(const TileLoader& T, const Cache& C, int row, int tile, int last,
+                                      int entries, int op) {
+    const int now = p[0], ahead = tile + kPagesAhead;
+#pragma unroll
+    for (int x = 0; x + 1 < kPagesAhead; ++x) p[x] = p[x + 1];
+    p[kPagesAhead - 1] = ahead < last && T.has(ahead, entries, op) ? T.page(C, row, ahead, op) : 0;
+    return !T.has(tile, entries, op) ? -1 : (page_ok(C, now) ? now : -2);
   }
 };
 

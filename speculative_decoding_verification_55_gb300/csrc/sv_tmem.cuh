@@ -47,7 +47,7 @@ __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.
 
 #define SV_R8(x, o) "=r"(x[o]), "=r"(x[o + 1]), "=r"(x[o + 2]), "=r"(x[o + 3]), "=r"(x[o + 4]), "=r"(x[o + 5]), "=r"(x[o + 6]), "=r"(x[o + 7])
 #define SV_W8(x, o) "r"(x[o]), "r"(x[o + 1]), "r"(x[o + 2]), "r"(x[o + 3]), "r"(x[o + 4]), "r"(x[o + 5]), "r"(x[o + 6]), "r"(x[o + 7])
-// 16 or 64 columns of this thread's lane of tensor memory, loaded when the call returns (the wait
+// 16, 32 or 64 columns of this thread's lane of tensor memory, loaded when the call returns (the wait
 // is part of the statement, so that no use of the registers can move before it).
 __device__ __forceinline__ void tm_load64(uint32_t* r, uint32_t at) {
   asm volatile(
@@ -74,6 +74,25 @@ __device__ __forceinline__ void tm_store32(uint32_t at, const uint32_t* r) {
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
       "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
       ::"r"(at), SV_W8(r, 0), SV_W8(r, 8), SV_W8(r, 16), SV_W8(r, 24) : "memory");
+}
+__device__ __forceinline__ void tm_load32(uint32_t* r, uint32_t at) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : SV_R8(r, 0), SV_R8(r, 8), SV_R8(r, 16), SV_R8(r, 24) : "r"(at) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void tm_load(uint32_t* r, uint32_t at) {
+  static_assert(N == 32 || N == 64, "columns");
+  if (N == 32) tm_load32(r, at);
+  else tm_load64(r, at);
+}
+template <int N>
+__device__ __forceinline__ void tm_store(uint32_t at, const uint32_t* r) {
+  static_assert(N == 16 || N == 32, "columns");
+  if (N == 16) tm_store16(at, r);
+  else tm_store32(at, r);
 }
 __device__ __forceinline__ void tm_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 

@@ -119,9 +119,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool gone = false;
     while (!gone && W.next(R)) {
       const int entries = W.w.n + W.w.m;
-      int p = T.page(C, W.row, W.first, entries, lane);
-      for (int t = W.first; t < W.first + W.count; ++t) {
-        const int p_next = t + 1 < W.first + W.count ? T.page(C, W.row, t + 1, entries, lane) : -1;
+      const int last = W.first + W.count;
+      sv::PagesAhead pages;
+      pages.begin(T, C, W.row, W.first, last, entries, lane);
+      for (int t = W.first; t < last; ++t) {
+        const int p = pages.next(T, C, W.row, t, last, entries, lane);
         const int s = armed % kK;
         const uint32_t bar = sv::smem_addr(S.k_full + s);
         if (armed >= kK &&
@@ -134,7 +136,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (p >= 0) T.load(C, &kmap, nullptr, t, W.head, p, lane, ring + s * kSlotBytes<D>, bar);
         ++armed;
-        p = p_next;
       }
     }
     for (int e = max(0, armed - kK); e < armed; ++e)       // no copy is in flight when the CTA ends
