@@ -166,49 +166,68 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- Products, by one thread. Score buffer w of tile x: one way, w = x % 2, two tiles ahead of the
     // products with the values; two ways, w the way, a tile ahead.
     if (lane == 0) {
+      // This thread's own instructions take much of a tile's time (100 cycles a wait, 60 a product): places in
+      // the ring and barriers are counted on, not computed.
       constexpr uint32_t ds = product_desc<F16>(kTile, false), dp = product_desc<F16>(D, true);
-      int base = 0, items = 0, count = 0;
-      auto scores = [&](int idx, int way) {
-        const int x = base + idx, s = (2 * x) % kSlots, w = kWays == 2 ? way : x % kScores;
-        if (way == 0 && !wait_unless_lost(sv::smem_addr(S.full + s), (2 * x / kSlots) & 1, lost)) return;
+      const uint32_t full = sv::smem_addr(S.full), empty = sv::smem_addr(S.empty);
+      const uint32_t s_full = sv::smem_addr(S.s_full), p_ready = sv::smem_addr(S.p_ready);
+      const Matrix ring_k = matrix(ring, 16, 1024), ring_v = matrix(ring, kTile * 128, 1024), queries = matrix(qs, 16, 1024);
+      struct Place {
+        int slot;
+        uint32_t phase;
+        __device__ __forceinline__ void step() {         // to the same array of the next tile
+          slot += 2;
+          if (slot >= kSlots) {
+            slot -= kSlots;
+            phase ^= 1u;
+          }
+        }
+      } pk{0, 0u}, pv{1, 0u};
+      uint32_t ws = 0, wp = 0, turn = 0;                 // score buffers next written and next read, and its phase
+      int items = 0, left = 0;                           // left: score products of the item still to come
+      auto scores = [&](int way) {
+        if (way == 0 && !wait_unless_lost(full + 8 * pk.slot, pk.phase, lost)) return;
         fence_after();
-        const uint32_t kb = ring + s * H::kSlotBytes, qb = qs + way * (kRows * D * 2);
+        const uint32_t w = kWays == 2 ? way : ws;
+        const Matrix km = ring_k.at(pk.slot * H::kSlotBytes), qm = queries.at(way * (kRows * D * 2));
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
-          product_ss(tm + w * kTile, matrix_desc(qb + (k >> 2) * (kRows * 128) + (k & 3) * 32, 16, 1024),
-                     matrix_desc(kb + (k >> 2) * (kTile * 128) + (k & 3) * 32, 16, 1024), ds, k > 0);
-        products_done(sv::smem_addr(S.s_full + w));
+          product_ss(tm + w * kTile, qm.at((k >> 2) * (kRows * 128) + (k & 3) * 32),
+                     km.at((k >> 2) * (kTile * 128) + (k & 3) * 32), ds, k > 0);
+        products_done(s_full + 8 * w);
         if (way + 1 < kWays) return;
-        products_done(sv::smem_addr(S.empty + s));
-        if (idx + 1 == count) products_done(sv::smem_addr(&S.q_empty));
+        products_done(empty + 8 * pk.slot);
+        pk.step();
+        ws ^= 1;
+        if (--left == 0) products_done(sv::smem_addr(&S.q_empty));
       };
       constexpr int kAhead = kWays == 2 ? 1 : kScores;
       for (;;) {
-        count = told(items).count;
+        const int count = told(items).count;
         if (count == 0 || !wait_unless_lost(sv::smem_addr(&S.q_full), items & 1, lost)) break;
-        fence_after();
+        left = count;
         for (int idx = 0; idx < count && idx < kAhead; ++idx)
-          for (int way = 0; way < kWays; ++way) scores(idx, way);
-        for (int idx = 0; idx < count && !*lost; ++idx) {
-          const int x = base + idx, s = (2 * x + 1) % kSlots;
-          const uint32_t vb = ring + s * H::kSlotBytes;
+          for (int way = 0; way < kWays; ++way) scores(way);
+        for (int idx = 0; idx < count; ++idx) {
+          if (!wait_unless_lost(full + 8 * pv.slot, pv.phase, lost)) break;
+          const Matrix vm = ring_v.at(pv.slot * H::kSlotBytes);
 #pragma unroll
           for (int way = 0; way < kWays; ++way) {
-            const int w = kWays == 2 ? way : x % kScores, turn = kWays == 2 ? x : x / kScores;
-            if ((way == 0 && !wait_unless_lost(sv::smem_addr(S.full + s), ((2 * x + 1) / kSlots) & 1, lost)) ||
-                !wait_unless_lost(sv::smem_addr(S.p_ready + w), turn & 1, lost))
-              break;
+            const uint32_t w = kWays == 2 ? way : wp;
+            if (!wait_unless_lost(p_ready + 8 * w, turn, lost)) break;
             fence_after();
 #pragma unroll
             for (int k = 0; k < kTile / 16; ++k)
-              product_ts(tm + kAccum + way * D, tm + w * kTile + k * 8, matrix_desc(vb + k * 2048, kTile * 128, 1024),
-                         dp, idx > 0 || k > 0);
-            if (way + 1 == kWays) products_done(sv::smem_addr(S.empty + s));
-            if (idx + kAhead < count) scores(idx + kAhead, way);
+              product_ts(tm + kAccum + way * D, tm + w * kTile + k * 8, vm.at(k * 2048), dp, idx > 0 || k > 0);
+            if (way + 1 == kWays) products_done(empty + 8 * pv.slot);
+            if (left > 0) scores(way);
           }
+          pv.step();
+          wp ^= 1;
+          if (kWays == 2 || wp == 0) turn ^= 1u;
         }
+        if (*lost) break;
         products_done(sv::smem_addr(&S.o_full));
-        base += count;
         ++items;
       }
       if (*lost) {              // products in flight end before the tensor memory is given back

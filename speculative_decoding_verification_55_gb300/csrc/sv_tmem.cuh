@@ -9,12 +9,15 @@ namespace tmem {
 
 constexpr int kColumns = 512;              // tensor memory columns: a CTA of these kernels takes all
 
-// A matrix in shared memory whose rows of 128 bytes are swizzled. Rows along the result: `stride` is
-// the distance of eight rows. Rows along the contraction: `lead` is the distance of 64 columns.
-__device__ __forceinline__ uint64_t matrix_desc(uint32_t addr, uint32_t lead, uint32_t stride) {
-  // Start, leading and stride offsets in 16-byte units; version 1; 128-byte swizzle.
-  return static_cast<uint64_t>((addr & 0x3ffffu) >> 4) | (static_cast<uint64_t>(lead >> 4) << 16) |
-         (static_cast<uint64_t>(stride >> 4) << 32) | (1ull << 46) | (2ull << 61);
+// Descriptor of a matrix in shared memory whose rows of 128 bytes are swizzled, in two words; an offset of
+// n bytes adds n / 16 to the low one. Rows along the result: `stride` is the distance of eight rows. Rows
+// along the contraction: `lead` is the distance of 64 columns.
+struct Matrix {
+  uint32_t lo, hi;
+  __device__ __forceinline__ Matrix at(uint32_t bytes) const { return {lo + (bytes >> 4), hi}; }
+};
+__device__ __forceinline__ Matrix matrix(uint32_t addr, uint32_t lead, uint32_t stride) {
+  return {((addr & 0x3ffffu) >> 4) | ((lead >> 4) << 16), (stride >> 4) | (1u << 14) | (2u << 29)};
 }
 
 // fp32 accumulators, operands of one 16-bit type; M = 128; b_rows: B's rows are its contraction index.
@@ -24,17 +27,18 @@ __device__ __forceinline__ constexpr uint32_t product_desc(int n, bool b_rows) {
          (static_cast<uint32_t>(n >> 3) << 17) | ((128 >> 4) << 24);
 }
 
-__device__ __forceinline__ void product_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool add) {
+__device__ __forceinline__ void product_ss(uint32_t d, Matrix a, Matrix b, uint32_t desc, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-      ::"r"(d), "l"(a), "l"(b), "r"(desc), "r"(add ? 1u : 0u) : "memory");
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.u32 p, %6, 0;\n\t"
+      "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}"
+      ::"r"(d), "r"(a.lo), "r"(a.hi), "r"(b.lo), "r"(b.hi), "r"(desc), "r"(add ? 1u : 0u) : "memory");
 }
-__device__ __forceinline__ void product_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t desc, bool add) {
+__device__ __forceinline__ void product_ts(uint32_t d, uint32_t a, Matrix b, uint32_t desc, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-      ::"r"(d), "r"(a), "l"(b), "r"(desc), "r"(add ? 1u : 0u) : "memory");
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.u32 p, %5, 0;\n\tmov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}"
+      ::"r"(d), "r"(a), "r"(b.lo), "r"(b.hi), "r"(desc), "r"(add ? 1u : 0u) : "memory");
 }
 // The barrier gets an arrival when every product issued so far is done.
 __device__ __forceinline__ void products_done(uint32_t bar) {

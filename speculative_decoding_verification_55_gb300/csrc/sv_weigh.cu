@@ -160,11 +160,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             fence_after();
             const int n = (min(chunk_rows, rows - x * chunk_rows) + 15) & ~15;
             const uint32_t desc = product_desc<F16>(0, false) | (static_cast<uint32_t>(n >> 3) << 17);
-            const uint32_t kb = ring + ks * kSlotBytes<D>, qb = qring + qi * kSlotBytes<D>;
+            const Matrix km = matrix(ring + ks * kSlotBytes<D>, 16, 1024);
+            const Matrix qm = matrix(qring + qi * (kRows * D * 2), 16, 1024);
 #pragma unroll
             for (int y = 0; y < D / 16; ++y)
-              product_ss(tm + w * kRows, matrix_desc(kb + (y >> 2) * (kTile * 128) + (y & 3) * 32, 16, 1024),
-                         matrix_desc(qb + (y >> 2) * (kRows * 128) + (y & 3) * 32, 16, 1024), desc, y > 0);
+              product_ss(tm + w * kRows, km.at((y >> 2) * (kTile * 128) + (y & 3) * 32),
+                         qm.at((y >> 2) * (kRows * 128) + (y & 3) * 32), desc, y > 0);
             products_done(sv::smem_addr(S.s_full + w));
             if (x + 1 == chunks) products_done(sv::smem_addr(S.k_empty + ks));
             if (last_use) {
