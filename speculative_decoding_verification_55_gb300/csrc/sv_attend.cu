@@ -380,17 +380,26 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2)
 }
 
 // The kernel and its query tiles: 16 rows where a key head has no more, else on the wide kernel up to 128 rows,
-// whole tokens, and two such tiles at once where there are more (the keys and values are then read once for
-// both; heads of 256 have no room for two accumulators). 4 rows of 32,000 entries with 248 query rows took
-// XX us a tile at a time, YY two at a time.
+// whole tokens. Where there are more, it can work on two tiles at once, which then read the keys and values
+// once (heads of 256 have no room for two accumulators). That pays when the second reading would come from
+// HBM, or when there are items for every SM; with fewer and shorter ones, of which many CTAs then take a
+// part, two tiles' parts cost more than the second reading from L2. Measured with 4 key heads and trees of
+// 31 nodes, 8 query heads a key head, one tile at a time against two: 38 rows of 2000 entries 74 against
+// 61 us, of 32,000 675 against 482; 8 rows of 64,000 301 against 227, of 16,000 92 against 94, of 4000
+// 39 against 53; 24 rows of 500 to 6000 68 against 80.
 struct Kernel {
   bool wide;
   int tile_rows, part_rows, ways, key_log2, ctas;     // CTAs: of an SM
 };
-Kernel kernel_for(int N, int group, int D) {
+constexpr long long kBeyondL2 = 512ll << 20;           // bytes of keys and values, about four times L2
+Kernel kernel_for(int N, int group, const sv_paged_cache* c, long long B, int sms) {
+  const int D = c->head_dim;
   if (N * group <= 16) return {false, 16, 16, 1, kTileLog2, D == 256 ? 1 : 2};
   const int rows = 128 / group * group;
-  return {true, rows, 128, N * group > rows && D < 256 ? 2 : 1, D == 256 ? 6 : 7, 1};
+  const long long pairs = B * c->heads * ((N * group + 2 * rows - 1) / (2 * rows));
+  const long long bytes = B * c->heads * c->max_pages * c->page_size * D * 4;
+  const bool two = N * group > rows && D < 256 && (pairs >= sms || bytes >= kBeyondL2);
+  return {true, rows, 128, two ? 2 : 1, D == 256 ? 6 : 7, 1};
 }
 constexpr int kMaxSms = 160;
 constexpr size_t kSharedBytes = 2 * kMaxSms * sizeof(int4);   // two ways or two CTAs an SM
@@ -411,7 +420,8 @@ extern "C" size_t spec_verify_paged_attention_workspace_size(int32_t N, int32_t 
   if (!cache || N < 1 || N > SV_MAX_GAMMA + 1 || Hq < 1 || Hq > 1024 || cache->heads < 1 ||
       Hq % cache->heads != 0 || Hq / cache->heads > 128 || cache->head_dim < 1 || cache->head_dim > 256)
     return 0;
-  const Kernel k = kernel_for(N, Hq / cache->heads, cache->head_dim);
+  // Two query tiles' parts where two could be worked on at once, whatever the batch.
+  const Kernel k = kernel_for(N, Hq / cache->heads, cache, 1 << 20, 1);
   const size_t part = static_cast<size_t>(k.ways) * k.part_rows * (cache->head_dim * 4 + 8);
   return kSharedBytes + (2 * k.ctas * kMaxSms * part + 255) / 256 * 256;
 }
@@ -440,7 +450,10 @@ extern "C" int spec_verify_paged_attention(const void* q, int64_t q_row_stride,
   st = sv::current_device_status(&dev);
   if (st != SV_OK) return st;
   const int D = cache->head_dim, group = Hq / cache->heads;
-  const Kernel k = kernel_for(N, group, D);
+  int sms = sv::device_sms(dev);
+  if (sms < 1) return SV_ERR_CUDA;
+  if (sms > kMaxSms) sms = kMaxSms;
+  const Kernel k = kernel_for(N, group, cache, B, sms);
   CUtensorMap kmap, vmap;
   st = sv::cache_tensor_map(cache, cache->k, sv::box_rows(cache), &kmap);
   if (st == SV_OK) st = sv::cache_tensor_map(cache, cache->v, sv::box_rows(cache), &vmap);
@@ -465,9 +478,6 @@ extern "C" int spec_verify_paged_attention(const void* q, int64_t q_row_stride,
   P.tile_rows = k.tile_rows;
   P.ways = k.ways;
   // As many CTAs as the GPU holds, or as many as the batch can have tiles.
-  int sms = sv::device_sms(dev);
-  if (sms < 1) return SV_ERR_CUDA;
-  if (sms > kMaxSms) sms = kMaxSms;
   const long long tile = 1 << P.R.tile_log2;
   const long long items = static_cast<long long>(B) * cache->heads * ((N * group + P.R.q_rows - 1) / P.R.q_rows);
   const long long most = items * ((static_cast<long long>(cache->max_pages) * cache->page_size + tile - 1) / tile);
@@ -489,6 +499,6 @@ extern "C" int spec_verify_paged_attention(const void* q, int64_t q_row_stride,
   else if (D == 64) st = f16 ? launch<true, 64, 1>(P, kmap, vmap, grid, s) : launch<false, 64, 1>(P, kmap, vmap, grid, s);
   else if (D == 128) st = f16 ? launch<true, 128, 1>(P, kmap, vmap, grid, s) : launch<false, 128, 1>(P, kmap, vmap, grid, s);
   else st = f16 ? launch<true, 256, 1>(P, kmap, vmap, grid, s) : launch<false, 256, 1>(P, kmap, vmap, grid, s);
-  // Fewer items than a quarter of the CTAs: each has many parts.
-  return st == SV_OK ? sv::launch_attend_join(P, f16, k.wide, items * 4 <= grid, grid, s) : st;
+  // Few items against the CTAs: each has many parts.
+  return st == SV_OK ? sv::launch_attend_join(P, f16, k.wide, items * (k.ways == 2 ? 16 : 4) <= grid, grid, s) : st;
 }

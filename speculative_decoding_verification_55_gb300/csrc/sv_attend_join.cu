@@ -5,7 +5,7 @@
 // A part is o [D][rows] and (m, l) [rows] in fp32: a lane has a row (and reads whole lines with its
 // neighbours) and 16 columns. 16 warps a CTA divide its columns and the parts among them, each with a
 // running maximum over its parts, and meet in shared memory. With few items, which then have many
-// parts, a CTA takes 16 or 32 columns and its warps a sixteenth of the parts each; otherwise all columns.
+// parts, a CTA takes 16 to 64 columns and its warps a fourth to a sixteenth of the parts; otherwise all columns.
 // Every item that is not whole goes through here. Joining in the last CTA to arrive instead kept that
 // CTA 10 us (3 parts of 128 rows) to 30 us (76 parts of 40 rows); this kernel is launched ahead (its
 // CTAs wait for the attention's end) and takes 3 to 4.
@@ -116,7 +116,9 @@ int launch2(const sv::AttendParams& P, int grid, cudaStream_t st) {
 template <bool F16, int D, int kRows>
 int launch(const sv::AttendParams& P, bool many_parts, int grid, cudaStream_t st) {
   constexpr int kAll = D / kCols / (kRows < 32 ? 32 / kRows : 1);
-  return many_parts ? launch2<F16, D, kRows, 1>(P, grid, st) : launch2<F16, D, kRows, kAll>(P, grid, st);
+  if (!many_parts) return launch2<F16, D, kRows, kAll>(P, grid, st);
+  // Two ways have four times the CTAs for a part's rows, most of them with nothing to do: fewer, larger ones.
+  return P.ways == 2 ? launch2<F16, D, kRows, 4>(P, grid, st) : launch2<F16, D, kRows, 1>(P, grid, st);
 }
 
 }  // namespace
