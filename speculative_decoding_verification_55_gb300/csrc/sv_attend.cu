@@ -7,13 +7,18 @@
 // One pass over keys and values with a running maximum and sum per query row. The query rows of a key
 // head (its query heads times the row's tokens) are the rows of the matrix products, so grouped heads
 // and a round's tokens share every key and value that is read. Persistent CTAs take equal runs of the
-// batch's key tiles (sv_tiles.cuh); an item that several CTAs share is joined by the last of them to
-// arrive, from partial sums in the workspace.
+// batch's key tiles (sv_tiles.cuh); an item that several CTAs share is joined from partial sums in the
+// workspace (sv_attend_join.cu). This file holds the kernel for up to 16 query rows a key head, the others
+// are in sv_attend_wide.cu.
 //
 // A CTA is one producer warp, which copies key tiles from the pages into a ring, and four consumer
 // warps. Each takes 16 of a tile's 64 entries with a maximum, a sum and an accumulator of its own, so
 // that warps meet only at an item's end: S = Q K^T and O += P V are 16 x 8 x 16 matrix instructions, P
-// staying in registers between them.
+// staying in registers between them. 16 rows of a 128-row product would be a waste that the tensor cores
+// can afford, but a warp that needs no other's numbers keeps more copies in flight: 16-row products issue
+// 700 of an SM's 8300 instructions a microsecond.
+// Bound: the bytes of keys and values. Decode batch of 64 rows (17 to 8191 entries, 8 key heads of 128, one
+// token, bf16; 1.08 GB): 172 us, 6.2 TB/s, 0.92 of the measured copy peak.
 // Rounding: probabilities go to the cache's type for the product with the values (half a step of 2^-8
 // or 2^-11 relative, as the output's own rounding); maxima, sums, scores and accumulators are fp32.
 
@@ -38,20 +43,20 @@ template <int D>
 constexpr int kStageBytes = 2 * kTile * D * 2;
 template <int D>
 constexpr int kStageCount = D == 64 ? 6 : 3;
+constexpr int kRows = 16;                      // query rows of an item
 // Queries of an item, then (the queries being read) the join of the warps' accumulators: maxima and
 // sums per warp and row, and two buffers of 16 rows by 16 columns per warp.
-template <int D, int MT>
-constexpr int kScratchBytes = MT * 16 * D * 2 > kWarps * MT * 16 * 8 + 2 * kWarps * 16 * 16 * 4
-                                  ? MT * 16 * D * 2
-                                  : kWarps * MT * 16 * 8 + 2 * kWarps * 16 * 16 * 4;
-template <int D, int MT>
-constexpr int kSmemBytes = 1024 + kStageCount<D> * kStageBytes<D> + kScratchBytes<D, MT>;
+constexpr int kJoinBytes = kWarps * kRows * 8 + 2 * kWarps * kRows * 16 * 4;
+template <int D>
+constexpr int kScratchBytes = kRows * D * 2 > kJoinBytes ? kRows * D * 2 : kJoinBytes;
+template <int D>
+constexpr int kSmemBytes = 1024 + kStageCount<D> * kStageBytes<D> + kScratchBytes<D>;
 
-template <bool F16, int D, int MT>
+template <bool F16, int D>
 __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2)
     sv_attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap) {
-  constexpr int kRows = 16 * MT, kStages = kStageCount<D>;
+  constexpr int kStages = kStageCount<D>;
   extern __shared__ unsigned char dyn[];
   __shared__ __align__(8) unsigned long long full[kStages], empty[kStages];
   __shared__ int bad_stage[kStages];
@@ -94,7 +99,8 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2)
         const int p = pages.next(T, C, W.row, t, last, entries, lane);
         const int s = issued % kStages;
         const uint32_t bar = sv::smem_addr(full + s);
-        if (issued >= kStages && !sv::mbar_wait(sv::smem_addr(empty + s), (issued / kStages - 1) & 1)) {
+        if (issued >= kStages &&
+            !__all_sync(kFull, sv::mbar_wait(sv::smem_addr(empty + s), (issued / kStages - 1) & 1))) {
           gone = true;
           break;
         }
@@ -148,74 +154,55 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2)
         bad |= x == 0 ? p != -1 : (p < 0 || p >= x);
       }
     sv::named_bar_sync(1, kConsumers);
-    int tok[2 * MT];                           // token of each of this thread's query rows
+    int tok[2];                                // token of each of this thread's query rows, g and g + 8
+    float mx[2], l[2], o[D / 8][4];
 #pragma unroll
-    for (int x = 0; x < 2 * MT; ++x)
-      tok[x] = min((row0 + 16 * (x >> 1) + 8 * (x & 1) + g) / R.group, m - 1);
-
-    float mx[2 * MT], l[2 * MT], o[MT][D / 8][4];
-#pragma unroll
-    for (int x = 0; x < 2 * MT; ++x) {
+    for (int x = 0; x < 2; ++x) {
+      tok[x] = min((row0 + 8 * x + g) / R.group, m - 1);
       mx[x] = -INFINITY;
       l[x] = 0.0f;
     }
 #pragma unroll
-    for (int x = 0; x < MT; ++x)
+    for (int y = 0; y < D / 8; ++y)
 #pragma unroll
-      for (int y = 0; y < D / 8; ++y)
-#pragma unroll
-        for (int z = 0; z < 4; ++z) o[x][y][z] = 0.0f;
+      for (int z = 0; z < 4; ++z) o[y][z] = 0.0f;
     bool odd = false;                          // values that are not finite among the round's own
 
     for (int t = W.first; t < last; ++t, ++done) {
       const int s = done % kStages;
-      if (!lost && !sv::mbar_wait(sv::smem_addr(full + s), (done / kStages) & 1)) lost = true;
+      if (!lost) lost = !__all_sync(kFull, sv::mbar_wait(sv::smem_addr(full + s), (done / kStages) & 1));
       bad |= bad_stage[s] != 0;
       const int j0 = t * kTile + 16 * warp;
       if (j0 < entries && !lost) {
         const uint32_t kb = ring + s * kStageBytes<D>, vb = kb + kTile * D * 2;
-        float sc[MT][2][4];
-#pragma unroll
-        for (int x = 0; x < MT; ++x)
-#pragma unroll
-          for (int y = 0; y < 2; ++y)
-#pragma unroll
-            for (int z = 0; z < 4; ++z) sc[x][y][z] = 0.0f;
+        float sc[2][4] = {};
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          uint32_t kf[4];
+          uint32_t kf[4], qf[4];
           sv::ldsm4(kf, sv::swizzled(kb + (kk >> 2) * (kTile * 128), 16 * warp + (lane & 7) + ((lane >> 4) << 3),
                                      ((kk & 3) << 1) + ((lane >> 3) & 1)));
-#pragma unroll
-          for (int x = 0; x < MT; ++x) {
-            uint32_t qf[4];
-            sv::ldsm4(qf, sv::swizzled(scratch + (kk >> 2) * (kRows * 128), 16 * x + (lane & 15),
-                                       ((kk & 3) << 1) + (lane >> 4)));
-            sv::mma<F16>(sc[x][0], qf, kf[0], kf[1]);
-            sv::mma<F16>(sc[x][1], qf, kf[2], kf[3]);
-          }
+          sv::ldsm4(qf, sv::swizzled(scratch + (kk >> 2) * (kRows * 128), lane & 15, ((kk & 3) << 1) + (lane >> 4)));
+          sv::mma<F16>(sc[0], qf, kf[0], kf[1]);
+          sv::mma<F16>(sc[1], qf, kf[2], kf[3]);
         }
         const bool edge = j0 + 16 > n;         // entries of the round itself, or behind the last
         if (edge) {
 #pragma unroll
-          for (int x = 0; x < MT; ++x)
+          for (int y = 0; y < 2; ++y)
 #pragma unroll
-            for (int y = 0; y < 2; ++y)
-#pragma unroll
-              for (int z = 0; z < 4; ++z) {
-                const int a = j0 + 8 * y + 2 * t4 + (z & 1) - n, i = tok[2 * x + (z >> 1)];
-                bool see = a <= i;
-                if (P.parents) see = a <= 0 || (a < m && ((masks[i] >> (a - 1)) & 1));
-                if (!see) sc[x][y][z] = -INFINITY;
-              }
+            for (int z = 0; z < 4; ++z) {
+              const int a = j0 + 8 * y + 2 * t4 + (z & 1) - n, i = tok[z >> 1];
+              bool see = a <= i;
+              if (P.parents) see = a <= 0 || (a < m && ((masks[i] >> (a - 1)) & 1));
+              if (!see) sc[y][z] = -INFINITY;
+            }
         }
         // Running maximum; accumulators are rescaled only when one of the warp's rows grew.
-        float grow[2 * MT];
+        float grow[2];
         bool any = false;
 #pragma unroll
-        for (int x = 0; x < 2 * MT; ++x) {
-          const int a = x >> 1, z = (x & 1) * 2;
-          float v = fmaxf(fmaxf(sc[a][0][z], sc[a][0][z + 1]), fmaxf(sc[a][1][z], sc[a][1][z + 1]));
+        for (int x = 0; x < 2; ++x) {
+          float v = fmaxf(fmaxf(sc[0][2 * x], sc[0][2 * x + 1]), fmaxf(sc[1][2 * x], sc[1][2 * x + 1]));
           v = fmaxf(v, __shfl_xor_sync(kFull, v, 1));
           v = fmaxf(v, __shfl_xor_sync(kFull, v, 2));
           grow[x] = fmaxf(mx[x], v);
@@ -223,30 +210,27 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2)
         }
         if (__any_sync(kFull, any)) {
 #pragma unroll
-          for (int x = 0; x < 2 * MT; ++x) {
+          for (int x = 0; x < 2; ++x) {
             const float f = grow[x] == mx[x] ? 1.0f : sv::ex2((mx[x] - grow[x]) * c);
             mx[x] = grow[x];
             l[x] *= f;
 #pragma unroll
             for (int y = 0; y < D / 8; ++y) {
-              o[x >> 1][y][(x & 1) * 2] *= f;
-              o[x >> 1][y][(x & 1) * 2 + 1] *= f;
+              o[y][2 * x] *= f;
+              o[y][2 * x + 1] *= f;
             }
           }
         }
-        uint32_t pf[MT][4];
+        uint32_t pf[4];
 #pragma unroll
-        for (int x = 0; x < MT; ++x)
+        for (int y = 0; y < 2; ++y)
 #pragma unroll
-          for (int y = 0; y < 2; ++y)
-#pragma unroll
-            for (int z = 0; z < 4; z += 2) {
-              const int r = 2 * x + (z >> 1);
-              const float b = mx[r] == -INFINITY ? 0.0f : mx[r] * c;
-              const float p0 = sv::ex2(fmaf(sc[x][y][z], c, -b)), p1 = sv::ex2(fmaf(sc[x][y][z + 1], c, -b));
-              l[r] += p0 + p1;
-              pf[x][2 * y + (z >> 1)] = sv::pack2<F16>(p0, p1);
-            }
+          for (int x = 0; x < 2; ++x) {
+            const float b = mx[x] == -INFINITY ? 0.0f : mx[x] * c;
+            const float p0 = sv::ex2(fmaf(sc[y][2 * x], c, -b)), p1 = sv::ex2(fmaf(sc[y][2 * x + 1], c, -b));
+            l[x] += p0 + p1;
+            pf[2 * y + x] = sv::pack2<F16>(p0, p1);
+          }
         const uint32_t keep0 = edge ? (j0 + 2 * t4 < entries ? 0xffffu : 0u) | (j0 + 2 * t4 + 1 < entries ? 0xffff0000u : 0u) : 0u;
         const uint32_t keep1 = edge ? (j0 + 8 + 2 * t4 < entries ? 0xffffu : 0u) | (j0 + 9 + 2 * t4 < entries ? 0xffff0000u : 0u) : 0u;
 #pragma unroll
@@ -260,11 +244,8 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2)
             vf[2] = finite2<F16>(vf[2], keep0, odd);
             vf[3] = finite2<F16>(vf[3], keep1, odd);
           }
-#pragma unroll
-          for (int x = 0; x < MT; ++x) {
-            sv::mma<F16>(o[x][2 * y], pf[x], vf[0], vf[1]);
-            sv::mma<F16>(o[x][2 * y + 1], pf[x], vf[2], vf[3]);
-          }
+          sv::mma<F16>(o[2 * y], pf, vf[0], vf[1]);
+          sv::mma<F16>(o[2 * y + 1], pf, vf[2], vf[3]);
         }
       }
       __syncwarp();
@@ -286,13 +267,10 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2)
           for (int z = 0; z < 4; ++z) {
             const float f = value_of<F16>(v[8 * y + 2 * t4 + (z & 1)]);
             if (isfinite(f)) continue;
-#pragma unroll
-            for (int x = 0; x < MT; ++x) {
-              const int i = tok[2 * x + (z >> 1)];
-              bool see = a <= i;
-              if (P.parents) see = a <= 0 || ((masks[i] >> (a - 1)) & 1);
-              if (see) o[x][y][z] += f;
-            }
+            const int i = tok[z >> 1];
+            bool see = a <= i;
+            if (P.parents) see = a <= 0 || ((masks[i] >> (a - 1)) & 1);
+            if (see) o[y][z] += f;
           }
       }
     }
@@ -300,79 +278,70 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2)
 
     // Join of the four warps: maxima and sums, then 16 columns at a time through two buffers.
 #pragma unroll
-    for (int x = 0; x < 2 * MT; ++x) {
+    for (int x = 0; x < 2; ++x) {
       l[x] += __shfl_xor_sync(kFull, l[x], 1);
       l[x] += __shfl_xor_sync(kFull, l[x], 2);
     }
     sv::named_bar_sync(1, kConsumers);         // the queries have been read
     float2* ml = reinterpret_cast<float2*>(scratch_p);                       // [kWarps][kRows]
     float* buf = reinterpret_cast<float*>(scratch_p + kWarps * kRows * 8);   // [2][kWarps][16][16]
-    if (t4 == 0)
-#pragma unroll
-      for (int x = 0; x < 2 * MT; ++x)
-        ml[warp * kRows + 16 * (x >> 1) + 8 * (x & 1) + g] = make_float2(mx[x], l[x]);
+    if (t4 == 0) {
+      ml[warp * kRows + g] = make_float2(mx[0], l[0]);
+      ml[warp * kRows + 8 + g] = make_float2(mx[1], l[1]);
+    }
     sv::named_bar_sync(1, kConsumers);
     const bool nan_item = sm_flags != 0;
-    float M[2 * MT], fw[2 * MT];
+    float fw[2];
 #pragma unroll
-    for (int x = 0; x < 2 * MT; ++x) {
-      const int r = 16 * (x >> 1) + 8 * (x & 1) + g;
-      M[x] = -INFINITY;
+    for (int x = 0; x < 2; ++x) {
+      float M = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) M[x] = fmaxf(M[x], ml[w * kRows + r].x);
-      fw[x] = mx[x] == -INFINITY ? 0.0f : sv::ex2((mx[x] - M[x]) * c);
+      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, ml[w * kRows + 8 * x + g].x);
+      fw[x] = mx[x] == -INFINITY ? 0.0f : sv::ex2((mx[x] - M) * c);
     }
     const bool whole = W.count == W.w.tiles;
     const int slot = 2 * blockIdx.x + (W.first == 0 ? 1 : 0);
     // This thread's place in the joined chunks: a row and two columns of each.
-    const int jr = tid >> 3, jc = (tid & 7) * 2;
+    const int r = tid >> 3, jc = (tid & 7) * 2;
+    float jm = -INFINITY, jl = 0.0f;
+    for (int w = 0; w < kWarps; ++w) jm = fmaxf(jm, ml[w * kRows + r].x);
+    for (int w = 0; w < kWarps; ++w) {
+      const float2 e = ml[w * kRows + r];
+      jl += e.x > -INFINITY ? e.y * sv::ex2((e.x - jm) * c) : e.y;           // the latter: 0, or NaN
+    }
+    if (nan_item) jl = __int_as_float(0x7fffffff);
+    const int i = (row0 + r) / R.group, hq = W.head * R.group + (row0 + r) - i * R.group;
+    const size_t at = (static_cast<size_t>(W.row) * R.N + i) * P.Hq + hq;
+    const float inv = 1.0f / jl;
 #pragma unroll
-    for (int x = 0; x < MT; ++x) {
-      const int r = 16 * x + jr;
-      float jm = -INFINITY, jl = 0.0f;
-      for (int w = 0; w < kWarps; ++w) jm = fmaxf(jm, ml[w * kRows + r].x);
+    for (int y = 0; y < D / 16; ++y) {
+      float* bw = buf + (y & 1) * (kWarps * 256);
+#pragma unroll
+      for (int z = 0; z < 2; ++z)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          *reinterpret_cast<float2*>(bw + warp * 256 + (8 * e + g) * 16 + ((8 * z + 2 * t4) ^ ((g & 1) << 3))) =
+              make_float2(o[2 * y + z][2 * e] * fw[e], o[2 * y + z][2 * e + 1] * fw[e]);
+      sv::named_bar_sync(1, kConsumers);
+      if (r >= rows) continue;
+      float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float2 e = ml[w * kRows + r];
-        if (e.x > -INFINITY) jl += e.y * sv::ex2((e.x - jm) * c);
-        else jl += e.y;                        // 0, or NaN
+        const float2 e = *reinterpret_cast<const float2*>(bw + w * 256 + r * 16 + (jc ^ ((r & 1) << 3)));
+        s0 += e.x;
+        s1 += e.y;
       }
-      if (nan_item) jl = __int_as_float(0x7fffffff);
-      const int i = (row0 + r) / R.group, hq = W.head * R.group + (row0 + r) - i * R.group;
-      const size_t at = (static_cast<size_t>(W.row) * R.N + i) * P.Hq + hq;
-      const float inv = 1.0f / jl;
-#pragma unroll
-      for (int y = 0; y < D / 16; ++y) {
-        float* bw = buf + ((x * (D / 16) + y) & 1) * (kWarps * 256);
-#pragma unroll
-        for (int z = 0; z < 2; ++z)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float f = fw[2 * x + e];
-            *reinterpret_cast<float2*>(bw + warp * 256 + (8 * e + g) * 16 + ((8 * z + 2 * t4) ^ ((g & 1) << 3))) =
-                make_float2(o[x][2 * y + z][2 * e] * f, o[x][2 * y + z][2 * e + 1] * f);
-          }
-        sv::named_bar_sync(1, kConsumers);
-        if (r < rows) {
-          float s0 = 0.0f, s1 = 0.0f;
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) {
-            const float2 e = *reinterpret_cast<const float2*>(bw + w * 256 + jr * 16 + (jc ^ ((jr & 1) << 3)));
-            s0 += e.x;
-            s1 += e.y;
-          }
-          if (whole)
-            *reinterpret_cast<uint32_t*>(static_cast<char*>(P.out) + (at * D + 16 * y + jc) * 2) = sv::pack2<F16>(s0 * inv, s1 * inv);
-          else {
-            float* part = P.part_o + (static_cast<size_t>(slot) * D + 16 * y + jc) * kRows + r;
-            part[0] = s0;
-            part[kRows] = s1;
-          }
-        }
+      if (whole) {
+        *reinterpret_cast<uint32_t*>(static_cast<char*>(P.out) + (at * D + 16 * y + jc) * 2) = sv::pack2<F16>(s0 * inv, s1 * inv);
+      } else {
+        float* part = P.part_o + (static_cast<size_t>(slot) * D + 16 * y + jc) * kRows + r;
+        part[0] = s0;
+        part[kRows] = s1;
       }
-      if ((tid & 7) == 0 && r < rows) {
-        if (!whole) P.part_ml[slot * kRows + r] = make_float2(jm, jl);
-        else if (P.lse) P.lse[at] = (jm * c + log2f(jl)) * 0.6931471805599453f;
-      }
+    }
+    if ((tid & 7) == 0 && r < rows) {
+      if (!whole) P.part_ml[slot * kRows + r] = make_float2(jm, jl);
+      else if (P.lse) P.lse[at] = (jm * c + log2f(jl)) * 0.6931471805599453f;
     }
     if (!whole && tid == 0 && W.first == 0) sv::tell_shared(P, 0, W.row, W.head, W.q_tile, W.item_at, W.w.tiles, plan);
     sv::named_bar_sync(1, kConsumers);         // the scratch is free for the next item's queries
@@ -404,12 +373,12 @@ Kernel kernel_for(int N, int group, const sv_paged_cache* c, long long B, int sm
 constexpr int kMaxSms = 160;
 constexpr size_t kSharedBytes = 2 * kMaxSms * sizeof(int4);   // two ways or two CTAs an SM
 
-template <bool F16, int D, int MT>
+template <bool F16, int D>
 int launch(const AttendParams& P, const CUtensorMap& k, const CUtensorMap& v, int grid, cudaStream_t st) {
-  auto kern = sv_attend_kernel<F16, D, MT>;
+  auto kern = sv_attend_kernel<F16, D>;
   static std::atomic<unsigned long long> allowed{0};
-  if (sv::allow_shared(kern, (kSmemBytes<D, MT>), allowed) != SV_OK) return SV_ERR_CUDA;
-  kern<<<grid, kThreads, (kSmemBytes<D, MT>), st>>>(P, k, v);
+  if (sv::allow_shared(kern, kSmemBytes<D>, allowed) != SV_OK) return SV_ERR_CUDA;
+  kern<<<grid, kThreads, kSmemBytes<D>, st>>>(P, k, v);
   return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 
@@ -496,9 +465,9 @@ extern "C" int spec_verify_paged_attention(const void* q, int64_t q_row_stride,
     if (st != SV_OK) return st;
     st = sv::launch_attend_wide(P, f16, kmap, vmap, qmap, tokens, grid, s);
   }
-  else if (D == 64) st = f16 ? launch<true, 64, 1>(P, kmap, vmap, grid, s) : launch<false, 64, 1>(P, kmap, vmap, grid, s);
-  else if (D == 128) st = f16 ? launch<true, 128, 1>(P, kmap, vmap, grid, s) : launch<false, 128, 1>(P, kmap, vmap, grid, s);
-  else st = f16 ? launch<true, 256, 1>(P, kmap, vmap, grid, s) : launch<false, 256, 1>(P, kmap, vmap, grid, s);
+  else if (D == 64) st = f16 ? launch<true, 64>(P, kmap, vmap, grid, s) : launch<false, 64>(P, kmap, vmap, grid, s);
+  else if (D == 128) st = f16 ? launch<true, 128>(P, kmap, vmap, grid, s) : launch<false, 128>(P, kmap, vmap, grid, s);
+  else st = f16 ? launch<true, 256>(P, kmap, vmap, grid, s) : launch<false, 256>(P, kmap, vmap, grid, s);
   // Few items against the CTAs: each has many parts.
   return st == SV_OK ? sv::launch_attend_join(P, f16, k.wide, items * (k.ways == 2 ? 16 : 4) <= grid, grid, s) : st;
 }

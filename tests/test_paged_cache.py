@@ -154,6 +154,8 @@ def test_argument_refusals(L):
                            (dict(scale=-1.0), 2), (dict(scale=math.inf), 2), (dict(scale=math.nan), 2)):
         got = calls(L, c, **change)
         assert (got["attend"], got["weigh"]) == (status,) * 2, (change, got)
+    got = calls(L, cache_struct(heads=4), Hq=1024, ts=1024 * 128, rs=9 * 1024 * 128)     # 256 heads a key head
+    assert (got["attend"], got["weigh"]) == (2, 2)
     assert calls(L, c, out=None)["attend"] == 1
     assert calls(L, c, out=FAKE + 8)["attend"] == 5
     assert calls(L, c, lse=None)["weigh"] == 1
@@ -348,6 +350,39 @@ def test_gpu_attention_many_rows(sv):
     num = rng.integers(0, 3, 700).astype(np.int32)
     out, lse = sv.attend(a.q, a.cache(sv), dev(a.prefix), dev(num))
     check_attention(a, out, lse, a.prefix, num, None)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D,dtype", [(64, "bf16"), (128, "f16")])
+def test_gpu_attention_large_trees_many_rows(sv, D, dtype):
+    """More than 128 query rows a key head and an item for every SM: two query tiles at once."""
+    rng = np.random.default_rng(7)
+    prefix = rng.integers(0, 200, 170)
+    a = Batch(prefix, 17, 1, 11, D, 16, dtype, seed=D)
+    num = rng.integers(0, 18, 170).astype(np.int32)
+    tree = random_tree(rng, 170, 17)
+    out, lse = sv.attend(a.q, a.cache(sv), dev(a.prefix), dev(num), dev(tree))
+    check_attention(a, out, lse, a.prefix, num, tree)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N,G,D", [(31, 8, 128), (65, 7, 64), (9, 16, 128)])
+def test_gpu_attention_large_trees_in_parts(sv, N, G, D):
+    """The same for a few long rows in tables with room for many more: two query tiles in parts."""
+    a = Batch((3000, 129, 0), N, 1, G, D, 16, seed=N)
+    table = np.full((3, 65536), 1 << 30, np.int32)
+    table[:, :a.table.shape[1]] = a.table
+    a.table = table
+    tree = random_tree(np.random.default_rng(N), 3, N)
+    num = np.array([N, N - 3, N], np.int32)
+    for parents in (None, tree):
+        out, lse = sv.attend(a.q, a.cache(sv), dev(a.prefix), dev(num), dev(parents))
+        check_attention(a, out, lse, a.prefix, num, parents)
+    a.v[oracle.place(a.table, 0, 3000 + N - 1, 16)[0]] = math.inf      # entries of the round's last page
+    out, lse = sv.attend(a.q, a.cache(sv), dev(a.prefix), dev(num))
+    seen = 3000 // 16 * 16 + 16 if (3000 + N - 1) // 16 == 3000 // 16 else (3000 + N - 1) // 16 * 16
+    first = max(0, seen - 3000)                            # tokens before it attend no entry of that page
+    assert np.isfinite(host(out)[0, :first]).all() and np.isinf(host(out)[0, N - 1]).all()
 
 
 @pytest.mark.gpu
