@@ -129,6 +129,17 @@ def spec_verify_kv_append(k_new, v_new, cache, prefix_len, num_new=None, path=No
           _small(path, "path", i32, (B, N), dev), _small(out_len, "out_len", i32, (B,), dev), B, N)
 
 
+def _attention(q, cache, prefix_len, num_queries, tree_parents, N, Hq, rs, ts, out, out_lse, workspace,
+               workspace_bytes, scale, stream):
+    import torch
+    dev, B, i32 = cache.device, cache.B, torch.int32
+    _call(lib().spec_verify_paged_attention, cache, stream, q.data_ptr(), rs, ts, cache.ref,
+          _small(prefix_len, "prefix_len", i32, (B,), dev), _small(num_queries, "num_queries", i32, (B,), dev),
+          _small(tree_parents, "tree_parents", i32, (B, N), dev),
+          1.0 / math.sqrt(cache.head_dim) if scale is None else scale, out, out_lse, B, N, Hq, workspace,
+          workspace_bytes)
+
+
 def spec_verify_paged_attention(q, cache, prefix_len, num_queries, tree_parents, out, out_lse,
                                 workspace, scale=None, stream=None) -> None:
     """Calls the C ABI spec_verify_paged_attention on torch tensors: q [B, N, Hq, D] (heads of a token
@@ -136,16 +147,12 @@ def spec_verify_paged_attention(q, cache, prefix_len, num_queries, tree_parents,
     import torch
     dev, B = cache.device, cache.B
     N, Hq, rs, ts = _tokens(q, "q", cache)
-    i32 = torch.int32
-    o = _small(out, "out", cache.dtype, (B, N, Hq, cache.head_dim), dev)
     if workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous and on {dev}")
-    _call(lib().spec_verify_paged_attention, cache, stream, q.data_ptr(), rs, ts, cache.ref,
-          _small(prefix_len, "prefix_len", i32, (B,), dev), _small(num_queries, "num_queries", i32, (B,), dev),
-          _small(tree_parents, "tree_parents", i32, (B, N), dev),
-          1.0 / math.sqrt(cache.head_dim) if scale is None else scale, o,
-          _small(out_lse, "out_lse", torch.float32, (B, N, Hq), dev), B, N, Hq, workspace.data_ptr(),
-          workspace.nbytes)
+    _attention(q, cache, prefix_len, num_queries, tree_parents, N, Hq, rs, ts,
+               _small(out, "out", cache.dtype, (B, N, Hq, cache.head_dim), dev),
+               _small(out_lse, "out_lse", torch.float32, (B, N, Hq), dev), workspace.data_ptr(),
+               workspace.nbytes, scale, stream)
 
 
 def spec_verify_kv_weights(q, lse, cache, prefix_len, num_kept=None, path=None, scale=None,
@@ -202,9 +209,10 @@ def attend(q, cache, prefix_len, num_queries=None, tree_parents=None, scale=None
             stream = torch.cuda.ExternalStream(int(stream), cache.device)
         with torch.cuda.stream(stream):
             return attend(q, cache, prefix_len, num_queries, tree_parents, scale)
-    B, N, Hq, D = q.shape
-    out = torch.empty((B, N, Hq, D), dtype=q.dtype, device=q.device)
-    lse = torch.empty((B, N, Hq), dtype=torch.float32, device=q.device)
-    spec_verify_paged_attention(q, cache, prefix_len, num_queries, tree_parents, out, lse,
-                                _attend_workspace(N, Hq, cache), scale)
+    N, Hq, rs, ts = _tokens(q, "q", cache)
+    out = torch.empty((cache.B, N, Hq, cache.head_dim), dtype=q.dtype, device=cache.device)
+    lse = torch.empty((cache.B, N, Hq), dtype=torch.float32, device=cache.device)
+    ws = _attend_workspace(N, Hq, cache)
+    _attention(q, cache, prefix_len, num_queries, tree_parents, N, Hq, rs, ts, out.data_ptr(), lse.data_ptr(),
+               ws.data_ptr(), ws.nbytes, scale, None)
     return out, lse
