@@ -715,3 +715,123 @@ def test_gpu_workspace_of_any_contents(sv):
         out2 = torch.empty_like(out)
         sv.spec_verify_paged_attention(a.q, c, dev(a.prefix), None, None, out2, None, ws)
         assert torch.equal(out, out2)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N,G,D", [(1, 4, 128), (9, 4, 64), (31, 8, 128), (5, 2, 256)])
+def test_gpu_other_strides(sv, N, G, D):
+    """Keys and values interleaved in one tensor with room between slots, a key head of one, queries with
+    gaps between tokens: every call reads and writes its own elements alone."""
+    for H in (1, 3):
+        a = Batch((60, 0, 129), N, H, G, D, 32, seed=N)
+        both = torch.full((len(a.k), 32, H + 1, 3, D), 7.0, dtype=a.t, device="cuda")
+        k, v = both[:, :, :H, 0].transpose(1, 2), both[:, :, :H, 2].transpose(1, 2)
+        k.copy_(a.k)
+        v.copy_(a.v)
+        a.k, a.v = k, v
+        wide = torch.zeros((3, N, H * G + 2, D), dtype=a.t, device="cuda")
+        wide[:, :, :H * G] = a.q
+        a.q = wide[:, :, :H * G]
+        c = a.cache(sv)
+        out, lse = sv.attend(a.q, c, dev(a.prefix))
+        check_attention(a, out, lse, a.prefix, np.full(3, N), None)
+        before = host(a.weight)
+        sv.spec_verify_kv_weights(a.q, lse, c, dev(a.prefix))
+        want = oracle.weights(host(a.q), host(lse), host(a.k), before, a.table, a.prefix, [N] * 3, None, a.scale)
+        assert np.allclose(host(a.weight), want, rtol=1e-4, atol=1e-7)
+        want = oracle.append(host(a.k), host(a.v), host(a.weight), host(a.k_new), host(a.v_new), a.table, a.prefix, [N] * 3, None)
+        sv.spec_verify_kv_append(a.k_new, a.v_new, c, dev(a.prefix))
+        for x, w in zip((a.k, a.v, a.weight), want):
+            assert np.array_equal(host(x), w, equal_nan=True)
+        a.k.nan_to_num_(0.5)
+        a.v.nan_to_num_(0.25)
+        check_evict(sv, a, a.prefix + N, 40, 7)
+        assert (both[:, :, H:] == 7).all() and (both[:, :, :, 1] == 7).all()
+
+
+@pytest.mark.gpu
+def test_gpu_shared_pages(sv):
+    """Rows with a common prefix on the same pages: read by all, their weights take every row's part."""
+    a = Batch((90, 90, 90), 4, 2, 4, 128, 16, seed=11)
+    a.table[1, :4] = a.table[0, :4]
+    a.table[2, :5] = a.table[0, :5]
+    c = a.cache(sv)
+    out, lse = sv.attend(a.q, c, dev(a.prefix))
+    check_attention(a, out, lse, a.prefix, np.full(3, 4), None)
+    before = host(a.weight)
+    sv.spec_verify_kv_weights(a.q, lse, c, dev(a.prefix))
+    want = oracle.weights(host(a.q), host(lse), host(a.k), before, a.table, a.prefix, [4] * 3, None, a.scale)
+    assert np.allclose(host(a.weight), want, rtol=1e-4, atol=1e-7)
+
+
+@pytest.mark.gpu
+def test_gpu_calls_at_once(sv):
+    """Calls in flight on three streams, each with its own workspace, give what they give alone."""
+    batches = [Batch(p, N, H, G, D, 16, seed=N) for p, N, H, G, D in
+               (((3000, 50, 700), 1, 2, 8, 128), ((900, 2000), 9, 2, 4, 64), ((64,) * 30, 31, 1, 8, 128))]
+    caches = [b.cache(sv) for b in batches]
+    alone = [sv.attend(b.q, c, dev(b.prefix)) for b, c in zip(batches, caches)]
+    prefix = [dev(b.prefix) for b in batches]
+    streams = [torch.cuda.Stream() for _ in batches]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(20):
+        for b, c, p, s in zip(batches, caches, prefix, streams):
+            got.append(sv.attend(b.q, c, p, stream=s))
+    torch.cuda.synchronize()
+    for x, (out, lse) in enumerate(got):
+        assert torch.equal(out, alone[x % 3][0]) and torch.equal(lse, alone[x % 3][1])
+
+
+@pytest.mark.gpu
+def test_gpu_captured_append_and_evict(sv):
+    """Append along a path and eviction in one graph, replayed on new contents and lengths."""
+    a = Batch((100, 40, 70), 6, 2, 2, 64, 16, seed=13, poison=False, extra=1)
+    c = a.cache(sv)
+    pre, num = dev(a.prefix), dev([6, 6, 6])
+    path = np.array([[0, 2, 3, -1, -1, -1], [0, 1, 2, 3, 4, 5], [0, 5, -1, -1, -1, -1]], np.int32)
+    length, kept = dev([0] * 3), dev([0] * 3)
+    d_path = dev(path)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        sv.spec_verify_kv_append(a.k_new, a.v_new, c, pre, num, d_path, length)
+        sv.spec_verify_kv_evict(c, length, 60, 9, kept)
+    for prefix, m in (((100, 40, 70), (3, 6, 2)), ((60, 59, 3), (3, 1, 2))):
+        pre.copy_(dev(prefix))
+        num.copy_(dev(m))
+        a.weight.uniform_()
+        k, v, w, n = oracle.append(host(a.k), host(a.v), host(a.weight), host(a.k_new), host(a.v_new), a.table, prefix, m, path)
+        k, v, w, on = oracle.evict(k, v, w, a.table, n.tolist(), 60, 9)
+        graph.replay()
+        torch.cuda.synchronize()
+        for x, y in zip((a.k, a.v, a.weight), (k, v, w)):
+            assert np.array_equal(host(x), y)
+        assert length.tolist() == n.tolist() and kept.tolist() == on.tolist()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H,D", [(1, 64), (2, 128)])
+def test_gpu_evict_long_rows(sv, H, D):
+    """Rows longer than a block holds keys of: the cluster selects together; equal weights across its runs."""
+    lengths = np.array([40000, 16385, 20000])
+    a = Batch(lengths, 1, H, 1, D, 128, seed=D, poison=False)
+    a.weight.mul_(3000).floor_()
+    for b, n in ((1, 16385),):                                   # one row of equal weights alone
+        for p in range(-(-n // 128)):
+            a.weight[int(a.table[b, p])] = 1.0
+    old = [x.clone() for x in (a.k, a.v, a.weight)]
+    olen = dev([0] * 3)
+    budget, recent = 12001, 300
+    sv.spec_verify_kv_evict(a.cache(sv), dev(lengths), budget, recent, olen)
+    assert olen.tolist() == [budget] * 3
+    for b, n in enumerate(lengths):
+        ids = torch.as_tensor(a.table[b, :-(-int(n) // 128)].astype(np.int64), device="cuda")
+        rows = lambda x: x[ids].transpose(0, 1).flatten(1, 2)[:, :int(n)]
+        w = host(rows(old[2]))
+        for h in range(H):
+            keep = torch.as_tensor(oracle.kept_entries(w[h], budget, recent), device="cuda")
+            for x, o in zip((a.k, a.v, a.weight), old):
+                assert torch.equal(rows(x)[h, :budget], rows(o)[h][keep])
+                assert torch.equal(rows(x)[h, budget:], rows(o)[h, budget:])
