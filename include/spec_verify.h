@@ -326,7 +326,8 @@ typedef struct {
  *                writes nothing and is not an error here: out_len is prefix_len.
  * path           [B, N] int32 or NULL.
  * out_len        [B] int32, entries after the call: prefix_len + num_new; -1 for a row in error, or one
- *                with a path entry outside [0, N), of which nothing is written. May be NULL.
+ *                with a path entry outside [0, N), of which nothing is written. May be NULL; shares no
+ *                memory with the other int32 arrays (SV_ERR_OVERLAP).
  * 1 <= N <= SV_MAX_GAMMA + 1. One launch on cuda_stream. */
 int spec_verify_kv_append(const void* k_new, const void* v_new, int64_t row_stride,
                           int64_t token_stride, const sv_paged_cache* cache,
@@ -349,6 +350,7 @@ int spec_verify_kv_append(const void* k_new, const void* v_new, int64_t row_stri
  * out_lse        [B, N, Hq] fp32, contiguous; 0 for i >= m_b. May be NULL.
  * workspace      device scratch of spec_verify_paged_attention_workspace_size(...) bytes, 256-byte
  *                aligned. It needs no setup; one workspace serves one call at a time, of any sizes.
+ * out and out_lse must not share memory with q, from its first element to its last (SV_ERR_OVERLAP).
  * A row in error gets NaN in all its outputs (a bad page or tree: in those of its m_b tokens).
  * The softmax and the sums run in fp32; the probabilities are rounded to the cache's dtype for the
  * product with the values. 1 <= N <= SV_MAX_GAMMA + 1, Hq <= 1024. */
@@ -385,8 +387,8 @@ int spec_verify_kv_weights(const void* q, int64_t q_row_stride, int64_t q_token_
  * A row with length[b] <= budget is left alone.
  *
  * length         [B] int32, entries per row
- * out_len        [B] int32: min(length, budget); -1 for a row in error, which is left alone. Not the
- *                same array as length (SV_ERR_OVERLAP).
+ * out_len        [B] int32: min(length, budget); -1 for a row in error, which is left alone. Shares
+ *                no memory with length (SV_ERR_OVERLAP).
  * budget >= 1, 0 <= recent <= budget (else SV_ERR_BAD_SHAPE). cache->weight is required. One launch. */
 int spec_verify_kv_evict(const sv_paged_cache* cache, const int32_t* length, int32_t budget,
                          int32_t recent, int32_t* out_len, int32_t B, void* cuda_stream);

@@ -92,16 +92,22 @@ def _small(t, name, dtype, shape, device):
 
 def _raw_stream(stream, device):
     import torch
-    if stream is None and device.type == "cuda":
+    if stream is None:
         return torch._C._cuda_getCurrentRawStream(device.index)
     return _stream_handle(stream, device)
+
+
+def _on_gpu(device):
+    if device.type != "cuda":
+        raise ValueError(f"the cache must be on a CUDA device, got {device}")
 
 
 def _call(f, cache, stream, *args):
     """Calls f(*args, stream) with the cache's device current and raises on a nonzero status."""
     import torch
     dev = cache.device
-    if dev.type == "cuda" and torch._C._cuda_getDevice() == dev.index:
+    _on_gpu(dev)
+    if torch._C._cuda_getDevice() == dev.index:
         st = f(*args, _raw_stream(stream, dev))
     else:
         with _on(dev):
@@ -210,6 +216,7 @@ def attend(q, cache, prefix_len, num_queries=None, tree_parents=None, scale=None
         with torch.cuda.stream(stream):
             return attend(q, cache, prefix_len, num_queries, tree_parents, scale)
     N, Hq, rs, ts = _tokens(q, "q", cache)
+    _on_gpu(cache.device)
     out = torch.empty((cache.B, N, Hq, cache.head_dim), dtype=q.dtype, device=cache.device)
     lse = torch.empty((cache.B, N, Hq), dtype=torch.float32, device=cache.device)
     ws = _attend_workspace(N, Hq, cache)

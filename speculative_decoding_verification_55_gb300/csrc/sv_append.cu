@@ -93,7 +93,10 @@ extern "C" int spec_verify_kv_append(const void* k_new, const void* v_new, int64
   if (sv::misaligned(v_new, 16) || sv::misaligned(prefix_len, 4) || sv::misaligned(num_new, 4) ||
       sv::misaligned(path, 4) || sv::misaligned(out_len, 4))
     return SV_ERR_MISALIGNED;
-  if (out_len && (out_len == prefix_len || out_len == num_new || out_len == path)) return SV_ERR_OVERLAP;
+  const long long rows = 4ll * B;
+  if (sv::overlap(out_len, rows, prefix_len, rows) || sv::overlap(out_len, rows, num_new, rows) ||
+      sv::overlap(out_len, rows, path, rows * N))
+    return SV_ERR_OVERLAP;
   int dev = 0;
   st = sv::current_device_status(&dev);
   if (st != SV_OK) return st;

@@ -413,6 +413,11 @@ extern "C" int spec_verify_paged_attention(const void* q, int64_t q_row_stride,
       sv::misaligned(num_queries, 4) || sv::misaligned(tree_parents, 4) ||
       sv::misaligned(workspace, 256))
     return SV_ERR_MISALIGNED;
+  const long long q_bytes = 2 * ((B - 1) * static_cast<long long>(q_row_stride) + (N - 1) * static_cast<long long>(q_token_stride) +
+                                 static_cast<long long>(Hq) * cache->head_dim);
+  const long long tokens = static_cast<long long>(B) * N * Hq;
+  if (sv::overlap(out, tokens * cache->head_dim * 2, q, q_bytes) || sv::overlap(out_lse, tokens * 4, q, q_bytes))
+    return SV_ERR_OVERLAP;
   if (!workspace || workspace_bytes < spec_verify_paged_attention_workspace_size(N, Hq, cache))
     return SV_ERR_WORKSPACE_TOO_SMALL;
   int dev = 0;

@@ -57,6 +57,12 @@ inline bool misaligned(const void* p, uintptr_t a) {
   return p && (reinterpret_cast<uintptr_t>(p) % a) != 0;
 }
 
+// Whether arrays of these sizes share memory (null: no array).
+inline bool overlap(const void* a, long long a_bytes, const void* b, long long b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && (x < y ? y - x < static_cast<uintptr_t>(a_bytes) : x - y < static_cast<uintptr_t>(b_bytes));
+}
+
 // The checks of a cache argument; fills the device form. need_weight: the call reads or writes weights.
 inline int check_cache(const sv_paged_cache* c, int32_t B, bool need_weight, Cache* out) {
   if (!c || !c->k || !c->v || !c->page_table || (need_weight && !c->weight))

@@ -418,7 +418,7 @@ extern "C" int spec_verify_kv_evict(const sv_paged_cache* cache, const int32_t* 
   if (!length || !out_len) return SV_ERR_NULL_POINTER;
   if (budget < 1 || recent < 0 || recent > budget) return SV_ERR_BAD_SHAPE;
   if (sv::misaligned(length, 4) || sv::misaligned(out_len, 4)) return SV_ERR_MISALIGNED;
-  if (length == out_len) return SV_ERR_OVERLAP;
+  if (sv::overlap(out_len, 4ll * B, length, 4ll * B)) return SV_ERR_OVERLAP;
   int dev = 0;
   st = sv::current_device_status(&dev);
   if (st != SV_OK) return st;
@@ -447,9 +447,8 @@ extern "C" int spec_verify_kv_evict(const sv_paged_cache* cache, const int32_t* 
   const long long room = (all - static_cast<long long>(fixed) - 4 * P.pages) / 16 * 4;
   P.held = static_cast<int>(room < least ? least : (room < most ? room : most));
   const size_t smem = fixed + 4 * static_cast<size_t>(P.pages) + static_cast<size_t>(P.held) * 4;
-  if (cudaFuncSetAttribute(sv_evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(smem)) != cudaSuccess)
-    return SV_ERR_CUDA;
+  static std::atomic<unsigned long long> allowed{0};
+  if (sv::allow_shared(sv_evict_kernel, kSharedMost, allowed) != SV_OK) return SV_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(items * P.S));
   cfg.blockDim = dim3(kThreads);

@@ -1,7 +1,5 @@
 // Tensor maps of the paged cache for bulk tensor copies.
 
-#include <mutex>
-
 #include "sv_cache.cuh"
 
 namespace {
@@ -11,18 +9,17 @@ typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void
                              CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
                              CUtensorMapFloatOOBfill);
 
+EncodeFn find_encoder() {
+  void* p = nullptr;
+  cudaDriverEntryPointQueryResult got = cudaDriverEntryPointSymbolNotFound;
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &got) != cudaSuccess ||
+      got != cudaDriverEntryPointSuccess)
+    return nullptr;
+  return reinterpret_cast<EncodeFn>(p);
+}
 // The driver's encoder, looked up once (a host function: the same for every device).
 EncodeFn encode_fn() {
-  static std::once_flag once;
-  static EncodeFn fn = nullptr;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult got = cudaDriverEntryPointSymbolNotFound;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &got) == cudaSuccess &&
-        got == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeFn>(p);
-  });
+  static const EncodeFn fn = find_encoder();
   return fn;
 }
 

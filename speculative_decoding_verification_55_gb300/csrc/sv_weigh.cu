@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) sv::mbar_arrive(sv::smem_addr(S.s_empty + b));
         }
-        if (ok && mine) atomicAdd(C.weight + sv::weight_index(C, page, I.head, j), w);
+        if (mine) atomicAdd(C.weight + sv::weight_index(C, page, I.head, j), ok ? w : __int_as_float(0x7fffffff));
       }
     }
     fence_before();

@@ -835,3 +835,62 @@ def test_gpu_evict_long_rows(sv, H, D):
             for x, o in zip((a.k, a.v, a.weight), old):
                 assert torch.equal(rows(x)[h, :budget], rows(o)[h][keep])
                 assert torch.equal(rows(x)[h, budget:], rows(o)[h, budget:])
+
+
+def test_overlap_refusals(L):
+    """Arrays that share a part of their memory: refused as whole ones are (SV_ERR_OVERLAP)."""
+    c = cache_struct()
+    pre = FAKE + (5 << 20)
+    assert calls(L, c, olen=pre + 4)["evict"] == 9 and calls(L, c, olen=pre - 4)["evict"] == 9
+    got = calls(L, c, olen=pre + 4)
+    assert got["append"] == 9
+    assert calls(L, c, par=FAKE + (10 << 20), olen=FAKE + (10 << 20) + 4 * 17)["append"] == 9
+    q, size = FAKE + (4 << 20), 2 * (9 * 32 * 128 * 2)
+    assert calls(L, c, out=q)["attend"] == 9
+    assert calls(L, c, out=q + size - 16)["attend"] == 9 and calls(L, c, out=q - size + 16)["attend"] == 9
+    assert calls(L, c, lse=q + 64)["attend"] == 9
+
+
+def test_cache_on_the_host():
+    """Every call of the binding refuses a cache in host memory."""
+    import speculative_decoding_verification_55_gb300 as sv
+    sv.build_library()
+    k = torch.zeros((5, 2, 16, 64), dtype=torch.bfloat16)
+    c = sv.PagedCache(k, k.clone(), torch.zeros((3, 2), dtype=torch.int32), torch.zeros((5, 2, 16)))
+    q = torch.zeros((3, 4, 8, 64), dtype=torch.bfloat16)
+    n = torch.zeros(3, dtype=torch.int32)
+    lse = torch.zeros((3, 4, 8))
+    for call in (lambda: sv.attend(q, c, n), lambda: sv.spec_verify_kv_weights(q, lse, c, n),
+                 lambda: sv.spec_verify_kv_append(q[:, :, :2], q[:, :, :2], c, n),
+                 lambda: sv.spec_verify_kv_evict(c, n, 4, 1, n.clone()),
+                 lambda: sv.spec_verify_paged_attention(q, c, n, None, None, q.clone(), lse, torch.zeros(1 << 20))):
+        with pytest.raises(ValueError, match="CUDA device"):
+            call()
+
+
+@pytest.mark.gpu
+def test_gpu_evict_from_threads(sv):
+    """Evictions of caches that need different amounts of shared memory, from host threads at once."""
+    from concurrent.futures import ThreadPoolExecutor
+    jobs = []
+    for x, n in enumerate((70, 700, 5000, 20000)):
+        a = Batch((n, n // 2), 1, 2, 1, 64, 16, seed=x, poison=False)
+        jobs.append((a, a.cache(sv), dev([n, n // 2]), dev([0, 0]), n // 3, torch.cuda.Stream()))
+    want = [oracle.evict(host(a.k), host(a.v), host(a.weight), a.table, n.tolist(), budget, 5)
+            for a, c, n, o, budget, s in jobs]
+    torch.cuda.synchronize()
+
+    def run(job):
+        a, c, n, o, budget, s = job
+        for _ in range(30):                    # the first evicts, the others find rows in their budget
+            sv.spec_verify_kv_evict(c, n, budget, 5, o, stream=s)
+            with torch.cuda.stream(s):
+                n.copy_(o)
+
+    with ThreadPoolExecutor(4) as pool:
+        list(pool.map(run, jobs))
+    torch.cuda.synchronize()
+    for (a, c, n, o, budget, s), (k, v, w, on) in zip(jobs, want):
+        assert o.tolist() == on.tolist()
+        for x, y in zip((a.k, a.v, a.weight), (k, v, w)):
+            assert np.array_equal(host(x), y)
