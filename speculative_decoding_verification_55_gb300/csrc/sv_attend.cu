@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2)
       if (!whole) P.part_ml[slot * kRows + r] = make_float2(jm, jl);
       else if (P.lse) P.lse[at] = (jm * c + log2f(jl)) * 0.6931471805599453f;
     }
-    if (!whole && tid == 0 && W.first == 0) sv::tell_shared(P, 0, W.row, W.head, W.q_tile, W.item_at, W.w.tiles, plan);
+    if (!whole && tid == 0 && W.first == 0) sv::tell_shared(P, 0, W.row, W.head, W.q_tile, rows, W.item_at, W.w.tiles, plan);
     sv::named_bar_sync(1, kConsumers);         // the scratch is free for the next item's queries
   }
 }

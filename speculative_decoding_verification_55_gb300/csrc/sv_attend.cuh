@@ -19,7 +19,7 @@ struct AttendParams {
   // first part is part 2 p + 1 of the CTA p that holds its first tile, the others part 2 p of theirs, each a
   // tile of rows per way.
   int4* shared;                                // [grid][ways] the shared item whose first tile a CTA holds:
-                                               // row (-1: none), head, query tile, the last CTA
+                                               // row (-1: none), head, 256 x query tile + its rows, the last CTA
   float* part_o;                               // [2 grid][ways][D][rows]
   float2* part_ml;                             // [2 grid][ways][rows] maximum and sum
 };
@@ -66,9 +66,9 @@ __device__ __forceinline__ void fill_unused(const AttendParams& P, int D, int ti
 }
 
 // The item that this CTA begins and does not end, for the join kernel (one thread).
-__device__ __forceinline__ void tell_shared(const AttendParams& P, int way, int row, int head, int q_tile,
+__device__ __forceinline__ void tell_shared(const AttendParams& P, int way, int row, int head, int q_tile, int rows,
                                             long long item_at, int tiles, const Plan& plan) {
-  P.shared[blockIdx.x * P.ways + way] = make_int4(row, head, q_tile, unit_owner(item_at + tiles - 1, plan));
+  P.shared[blockIdx.x * P.ways + way] = make_int4(row, head, q_tile << 8 | rows, unit_owner(item_at + tiles - 1, plan));
 }
 
 // Joins the parts of the items that the attention kernel's `grid` CTAs shared.

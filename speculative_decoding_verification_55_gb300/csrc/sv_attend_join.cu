@@ -29,9 +29,7 @@ __global__ void __launch_bounds__(kThreads) sv_attend_join_kernel(const sv::Atte
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int4 it = __ldcg(P.shared + blockIdx.x);
   if (it.x < 0) return;                                // no shared item begins in this CTA's run
-  sv::RowWork w;
-  sv::row_work(R, it.x, &w);
-  const int row0 = it.z * P.tile_rows, rows = min(P.tile_rows, w.m * R.group - row0);
+  const int row0 = (it.z >> 8) * P.tile_rows, rows = it.z & 255;
   const int g0 = (blockIdx.y / kColBlocks) * kRowLanes, col0 = (blockIdx.y % kColBlocks) * kColsHere;
   if (g0 >= rows) return;
   const float c = P.c;
@@ -41,7 +39,7 @@ __global__ void __launch_bounds__(kThreads) sv_attend_join_kernel(const sv::Atte
     float M = -INFINITY, L = 0.0f, a[kCols];
 #pragma unroll
     for (int x = 0; x < kCols; ++x) a[x] = 0.0f;
-#pragma unroll 2
+#pragma unroll(kAcross == 1 ? 4 : 2)
     for (int p = c0 + pg; p <= it.w; p += kPartGroups) {
       const size_t part = static_cast<size_t>(2 * p + (p == c0)) * P.ways + way;
       const float2 e = __ldcg(P.part_ml + part * kRows + r);
@@ -118,7 +116,9 @@ int launch(const sv::AttendParams& P, bool many_parts, int grid, cudaStream_t st
   constexpr int kAll = D / kCols / (kRows < 32 ? 32 / kRows : 1);
   if (!many_parts) return launch2<F16, D, kRows, kAll>(P, grid, st);
   // Two ways have four times the CTAs for a part's rows, most of them with nothing to do: fewer, larger ones.
-  return P.ways == 2 ? launch2<F16, D, kRows, 4>(P, grid, st) : launch2<F16, D, kRows, 1>(P, grid, st);
+  if constexpr (kRows == 128 && D < 256)
+    if (P.ways == 2) return launch2<F16, D, kRows, 4>(P, grid, st);
+  return launch2<F16, D, kRows, 1>(P, grid, st);
 }
 
 }  // namespace

@@ -34,8 +34,9 @@ using sv::kFull;
 
 constexpr int kRows = 128;                             // query rows of a product
 constexpr int kSoftWarps = 8, kSoft = 32 * kSoftWarps;
-constexpr int kThreads = kSoft + 96;                   // and the producer's, the products' and the items' warps
-constexpr int kProducer = kSoftWarps, kProducts = kSoftWarps + 1, kItems = kSoftWarps + 2;
+constexpr int kCopyWarps = 2;
+constexpr int kThreads = kSoft + 32 * (kCopyWarps + 2);   // and the copies', the products' and the items' warps
+constexpr int kCopies = kSoftWarps, kItems = kCopies + kCopyWarps, kProducts = kItems + 1;
 constexpr float kSlack = 8.0f;
 constexpr int kScores = 2;                             // buffers of scores in tensor memory
 constexpr int kPieces = 8;                             // items that the warps may be apart, and one
@@ -58,7 +59,7 @@ struct Shape {
 // that none of them waits for lengths from global memory (2 us a load while the cache streams).
 struct Item {
   int row, head, q_tile, first, count;                 // count 0: the end
-  int n, m, tiles, bad;                                // bad: the row's tree is not valid
+  int n, m, tiles;
   long long item_at;
 };
 
@@ -71,7 +72,7 @@ struct Control {
   sv::Plan plan;
   Item items[kPieces];
   float row_max[2][2][kRows];                          // by the tile's parity and half
-  int bad[kPieces], flags, lost;
+  int bad[kCopyWarps][kPieces], flags, lost;
   uint32_t tm;
 };
 template <int D, int kWays>
@@ -93,7 +94,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t ring = sv::smem_addr(dyn), qs = ring + kSlots * H::kSlotBytes;
   if (tid == 0) {
     for (int s = 0; s < kSlots; ++s) {
-      sv::mbar_init(sv::smem_addr(S.full + s), 1);
+      sv::mbar_init(sv::smem_addr(S.full + s), kCopyWarps);
       sv::mbar_init(sv::smem_addr(S.empty + s), 1);
     }
     for (int w = 0; w < kScores; ++w) {
@@ -123,24 +124,51 @@ __global__ void __launch_bounds__(kThreads, 1)
     else I.count = 0;
     return I;
   };
-  if (warp == kProducer) {
+  if (warp >= kCopies && warp <= kItems) {
+    // ---- Items, and their copies. These warps walk the items by the same instructions: a kernel's first pass
+    // through any code waits for it to come from memory, and a walk of each warp's own took 2 us more.
     sv::Walk W;
     W.begin(R, S.plan);
-    // ---- Copies
     sv::TileLoader T;
     T.init(C, 1, H::kTileLog2);
+    const int mine = warp - kCopies, op = kCopyWarps * lane + mine;   // the boxes are divided among the copy warps
     int armed = 0, items = 0;                  // slots (tile x: 2 x and 2 x + 1) and items so far
     bool gone = false;
-    while (!gone && W.next(R)) {
+    for (;; ++items) {
+      const bool more = !gone && W.next(R);
+      if (warp == kItems) {
+        // The item's description, then, the score products of the one before being done, its queries:
+        // q_tokens tokens of the key head's query heads as rows.
+        if (lane == 0) {
+          S.items[items % kPieces] = Item{W.row, W.head, W.q_tile, W.first, more ? W.count : 0, W.w.n, W.w.m,
+                                          W.w.tiles, W.item_at};
+          sv::mbar_arrive(sv::smem_addr(S.told + items % kPieces));
+        }
+        if (!more) break;
+        if (items > 0 &&
+            !__all_sync(kFull, wait_unless_lost(sv::smem_addr(&S.q_empty), (items - 1) & 1, lost))) {
+          gone = true;                         // the next turn tells the end
+          continue;
+        }
+        if (lane == 0) {
+          sv::mbar_arrive_expect_tx(sv::smem_addr(&S.q_full), kWays * q_tokens * R.group * D * 2);
+          for (int x = 0; x < kWays * (D / 64); ++x)
+            sv::tma_load(qs + x * (kRows * 128), &qmap, x % (D / 64) * 64, W.head * R.group,
+                         (W.q_tile * kWays + x / (D / 64)) * (P.tile_rows / R.group), W.row, sv::smem_addr(&S.q_full));
+        }
+        ++armed;
+        continue;
+      }
+      if (!more) break;
       const int entries = W.w.n + W.w.m;
       const int last = W.first + W.count;
       sv::PagesAhead pages;
-      pages.begin(T, C, W.row, W.first, last, entries, lane);
-      if (lane == 0) S.bad[items % kPieces] = 0;
+      pages.begin(T, C, W.row, W.first, last, entries, op);
+      if (lane == 0) S.bad[mine][items % kPieces] = 0;
       for (int t = W.first; t < last && !gone; ++t) {
-        const int p = pages.next(T, C, W.row, t, last, entries, lane);
+        const int p = pages.next(T, C, W.row, t, last, entries, op);
         const unsigned go = __ballot_sync(kFull, p >= 0), out = __ballot_sync(kFull, p == -2);
-        if (lane == 0 && out) S.bad[items % kPieces] = 1;
+        if (lane == 0 && out) S.bad[mine][items % kPieces] = 1;
 #pragma unroll
         for (int array = 0; array < 2; ++array) {
           const int e = armed, s = e % kSlots;
@@ -152,16 +180,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (lane == 0) sv::mbar_arrive_expect_tx(bar, static_cast<uint32_t>(__popc(go)) << (T.rows_log2 + 7));
           __syncwarp();
-          if (p >= 0) T.load(C, array ? &vmap : &kmap, nullptr, t, W.head, p, lane, ring + s * H::kSlotBytes, bar);
+          if (p >= 0) T.load(C, array ? &vmap : &kmap, nullptr, t, W.head, p, op, ring + s * H::kSlotBytes, bar);
           ++armed;
         }
       }
-      ++items;
     }
-    sv::fill_unused(P, D, lane, 32);           // while the last tiles are computed
     // No copy is in flight when the CTA ends.
-    for (int e = max(0, armed - kSlots); e < armed; ++e)
-      sv::mbar_wait_drain(sv::smem_addr(S.full + e % kSlots), (e / kSlots) & 1);
+    if (warp == kItems) {
+      if (armed > 0) sv::mbar_wait_drain(sv::smem_addr(&S.q_full), (armed - 1) & 1);
+    } else {
+      sv::fill_unused(P, D, op, 32 * kCopyWarps);   // while the last tiles are computed
+      for (int e = max(0, armed - kSlots); e < armed; ++e)
+        sv::mbar_wait_drain(sv::smem_addr(S.full + e % kSlots), (e / kSlots) & 1);
+    }
   } else if (warp == kProducts) {
     // ---- Products, by one thread. Score buffer w of tile x: one way, w = x % 2, two tiles ahead of the
     // products with the values; two ways, w the way, a tile ahead.
@@ -236,37 +267,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp == kItems) {
-    // ---- Items: the next one's description, then, the score products of the one before being done, its
-    // queries: q_tokens tokens of the key head's query heads as rows.
-    sv::Walk W;
-    W.begin(R, S.plan);
-    int copies = 0;
-    for (int k = 0;; ++k) {
-      const bool more = !__any_sync(kFull, *lost != 0) && W.next(R);
-      bool bad = false;
-      if (more && P.parents)
-        for (int t = lane; t < W.w.m; t += 32) {
-          const int p = __ldg(P.parents + static_cast<size_t>(W.row) * R.N + t);
-          bad |= t == 0 ? p != -1 : (p < 0 || p >= t);
-        }
-      bad = __any_sync(kFull, bad);
-      if (lane == 0) {
-        S.items[k % kPieces] = Item{W.row, W.head, W.q_tile, W.first, more ? W.count : 0, W.w.n, W.w.m, W.w.tiles,
-                                    bad ? 1 : 0, W.item_at};
-        sv::mbar_arrive(sv::smem_addr(S.told + k % kPieces));
-      }
-      if (!more) break;
-      if (!__all_sync(kFull, k == 0 || wait_unless_lost(sv::smem_addr(&S.q_empty), (k - 1) & 1, lost))) continue;
-      if (lane == 0) {
-        sv::mbar_arrive_expect_tx(sv::smem_addr(&S.q_full), kWays * q_tokens * R.group * D * 2);
-        for (int x = 0; x < kWays * (D / 64); ++x)
-          sv::tma_load(qs + x * (kRows * 128), &qmap, x % (D / 64) * 64, W.head * R.group,
-                       (W.q_tile * kWays + x / (D / 64)) * (P.tile_rows / R.group), W.row, sv::smem_addr(&S.q_full));
-      }
-      ++copies;
-    }
-    if (copies > 0) sv::mbar_wait_drain(sv::smem_addr(&S.q_full), (copies - 1) & 1);   // the last queries are in
   } else {
     // ---- Softmax
     // One way: two warps share rows, `half` a tile's entries and D each. Two ways: four warps have a way.
@@ -282,12 +282,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n = W.n, m = W.m, entries = n + m;
       const int row0 = (W.q_tile * kWays + way) * P.tile_rows, rows = min(P.tile_rows, m * R.group - row0);
       if (tid == 0) S.flags = 0;                // nobody sets one before this thread's first tile is used
-      bool bad = W.bad != 0;
       const int last = W.first + W.count;
       const int32_t* par = P.parents ? P.parents + static_cast<size_t>(W.row) * R.N : nullptr;
+      bool bad = false;                        // the row's tree is not valid (a thread a node), or a page
+      if (par && tid < m) {
+        const int p = __ldg(par + tid);
+        bad = tid == 0 ? p != -1 : (p < 0 || p >= tid);
+      }
       const int tok = min((row0 + row) / R.group, m - 1);
       const bool active = 32 * wq < rows;      // the warp has a query row
-      const unsigned long long mask = par && last * kTile > n && !bad ? sv::tree_mask(par, tok) : 0ull;
+      const unsigned long long mask = par && last * kTile > n ? sv::tree_mask(par, tok) : 0ull;
       float mx = -INFINITY, l = 0.0f;
       bool odd = false;
 
@@ -304,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           continue;
         }
         fence_after();
-        if (idx + 1 == W.count) bad |= S.bad[items % kPieces] != 0;
+        if (idx + 1 == W.count) bad |= (S.bad[0][items % kPieces] | S.bad[1][items % kPieces]) != 0;
         if (active) {
           const uint32_t ts = tm + lanes + w * kTile;
           uint32_t sc[H::kChunk];
@@ -467,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_before();
       sv::named_bar_sync(1, kSoft);            // the sums have been read
       if (!whole && (tid & 127) == 0 && half == 0 && W.first == 0 && rows > 0)
-        sv::tell_shared(P, way, W.row, W.head, W.q_tile * kWays + way, W.item_at, W.tiles, S.plan);
+        sv::tell_shared(P, way, W.row, W.head, W.q_tile * kWays + way, rows, W.item_at, W.tiles, S.plan);
     }
     fence_before();
   }
@@ -489,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (x % D == 0 && !whole) P.part_ml[slot * kRows + r].y = __int_as_float(0x7fffffff);
         }
         if (!whole && tid == 0 && W.first == 0 && rows > 0)
-          sv::tell_shared(P, way, W.row, W.head, q_tile, W.item_at, W.w.tiles, S.plan);
+          sv::tell_shared(P, way, W.row, W.head, q_tile, rows, W.item_at, W.w.tiles, S.plan);
       }
   }
   if (warp == kProducts) tm_free(tm);
@@ -498,6 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <bool F16, int D, int kWays>
 int launch(const AttendParams& P, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& q, int q_tokens,
            int grid, cudaStream_t st) {
+  static_assert(kSmemBytes<D, kWays> <= 232448, "shared memory");
   auto kern = sv_attend_wide_kernel<F16, D, kWays>;
   static std::atomic<unsigned long long> allowed{0};
   if (sv::allow_shared(kern, (kSmemBytes<D, kWays>), allowed) != SV_OK) return SV_ERR_CUDA;

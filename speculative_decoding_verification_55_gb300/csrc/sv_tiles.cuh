@@ -274,10 +274,15 @@ __device__ __forceinline__ bool tree_masks(const int32_t* parents, int m, unsign
   return ok;
 }
 
-// The same of one token t of a valid tree.
+// The same of one token t.
 __device__ __forceinline__ unsigned long long tree_mask(const int32_t* parents, int t) {
   unsigned long long s = 0;
-  for (int x = t; x > 0; x = __ldg(parents + x)) s |= 1ull << (x - 1);
+  for (int x = t; x > 0;) {
+    s |= 1ull << (x - 1);
+    const int up = __ldg(parents + x);
+    if (up >= x) break;
+    x = up;
+  }
   return s;
 }
 
