@@ -18,7 +18,7 @@
 // not move. The cluster fills the GPU when rows and heads are few.
 // Measured on fresh caches, with the launch, from a flushed L2 (D = 128, bf16, 8 heads): 32 rows of 2000 to 8190
 // entries cut to 2048 101 us (5.2 TB/s), of which the selection takes 10; 3 rows of 1030 to 1501 cut to 1024
-// 19 us; one row of 130,000 cut to 65,000 326 us, bound by the batches' round trips of 64 CTAs.
+// 19 us; one row of 130,000 cut to 65,000 255 us, bound by the batches' round trips of 64 CTAs.
 // A selection on the whole cluster for every length took 60 us of 8 us (two barriers of the cluster a level),
 // one without it 600 us at 130,000 entries.
 
@@ -29,10 +29,9 @@
 
 namespace {
 
-constexpr int kThreads = 512;
 constexpr int kInFlight = 8;               // 16-byte loads in flight per thread
 constexpr int kMinCols = 2;                // columns of a CTA: at least a sector of an entry
-constexpr int kMaxBatch = 1024;            // entries of a batch
+constexpr int kBatchEach = 2;              // entries of a batch per thread, at most
 constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxRun = 1 << 18;           // entries of a run where rows are longest
@@ -83,11 +82,10 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(const void* p, int rank) {
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(sv::map_to_rank(sv::smem_addr(p), rank)) : "memory");
   return v;
 }
-__device__ __forceinline__ int4 ld_cluster_v4(const void* p, int rank) {
-  int4 v;
-  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(sv::map_to_rank(sv::smem_addr(p), rank)) : "memory");
+__device__ __forceinline__ uint2 ld_cluster_v2(const void* p, int rank) {
+  uint2 v;
+  asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];"
+               : "=r"(v.x), "=r"(v.y) : "r"(sv::map_to_rank(sv::smem_addr(p), rank)) : "memory");
   return v;
 }
 // The cluster's barrier, or the CTA's where it is alone.
@@ -96,7 +94,8 @@ __device__ __forceinline__ void meet(int S) {
   else __syncthreads();
 }
 
-// Exclusive prefix sum over the CTA; *total gets the sum. tmp: one int per warp and one more.
+// Exclusive prefix sum over the CTA; *total gets the sum. tmp: one int per warp.
+template <int kThreads>
 __device__ __forceinline__ int block_excl_scan(int v, int* tmp, int* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int x = v;
@@ -123,7 +122,9 @@ __device__ __forceinline__ int block_excl_scan(int v, int* tmp, int* total) {
   return before + x - v;
 }
 
-__global__ void __launch_bounds__(kThreads, 2) sv_evict_kernel(const EvictParams P) {
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) sv_evict_kernel(const EvictParams P) {
+  constexpr int kMaxBatch = kBatchEach * kThreads;
   extern __shared__ __align__(16) unsigned char dyn[];
   const sv::Cache& C = P.C;
   const int tid = threadIdx.x;
@@ -232,21 +233,24 @@ __global__ void __launch_bounds__(kThreads, 2) sv_evict_kernel(const EvictParams
       }
       meet(S);
       constexpr int kEach = kBins / kThreads;
-      static_assert(kEach == 4, "four bins a thread");
-      int4 bins = make_int4(0, 0, 0, 0);
+      int c[kEach] = {};
       if (tid * kEach < nb) {
         if (S > 1)
-          for (int r = 0; r < S; ++r) {
-            const int4 v = ld_cluster_v4(hist + tid * kEach, r);
-            bins = make_int4(bins.x + v.x, bins.y + v.y, bins.z + v.z, bins.w + v.w);
-          }
-        else bins = *reinterpret_cast<const int4*>(hist + tid * kEach);
+          for (int r = 0; r < S; ++r)
+#pragma unroll
+            for (int x = 0; x < kEach; x += 2) {
+              const uint2 v = ld_cluster_v2(hist + tid * kEach + x, r);
+              c[x] += v.x;
+              c[x + 1] += v.y;
+            }
+        else
+#pragma unroll
+          for (int x = 0; x < kEach; ++x) c[x] = hist[tid * kEach + x];
       }
-      const int c[kEach] = {bins.x, bins.y, bins.z, bins.w};
       int sum = 0, total;
 #pragma unroll
       for (int x = 0; x < kEach; ++x) sum += c[x];
-      int at = block_excl_scan(sum, tmp, &total);
+      int at = block_excl_scan<kThreads>(sum, tmp, &total);
 #pragma unroll
       for (int x = 0; x < kEach; ++x) {
         if (at < left && at + c[x] >= left) {      // one thread and bin
@@ -288,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 2) sv_evict_kernel(const EvictParams
     }
   }
   int tie_run = 0, total;
-  block_excl_scan(count, tmp, &total);
+  block_excl_scan<kThreads>(count, tmp, &total);
   if (S > 1) {
     if (tid == 0) mine.ties = total;
     meet(S);
@@ -303,14 +307,14 @@ __global__ void __launch_bounds__(kThreads, 2) sv_evict_kernel(const EvictParams
   for (int x0 = w0; x0 < w1; x0 += kThreads) {
     const int w = x0 + tid;
     uint32_t keep = w < w1 ? bits[w] : 0u, tie = w < w1 ? ties[w - w0] : 0u;
-    int t = tie_run + block_excl_scan(__popc(tie), tmp, &total);
+    int t = tie_run + block_excl_scan<kThreads>(__popc(tie), tmp, &total);
     tie_run += total;
     while (tie && t < left) {
       keep |= tie & -tie;
       tie &= tie - 1;
       ++t;
     }
-    const int k = kept_run + block_excl_scan(__popc(keep), tmp, &total);
+    const int k = kept_run + block_excl_scan<kThreads>(__popc(keep), tmp, &total);
     kept_run += total;
     if (w < w1) {
       bits[w] = keep;
@@ -378,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 2) sv_evict_kernel(const EvictParams
     const int* L = list + cur * kMaxBatch;
     const int here = min(batch, P.budget - d0);
     uint4 x[kInFlight];
-    float w[kMaxBatch / kThreads];
+    float w[kBatchEach];
 #pragma unroll
     for (int u = 0; u < kInFlight; ++u) {
       const int e = u * per + slot0;
@@ -386,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 2) sv_evict_kernel(const EvictParams
     }
     if (rank == 0)                           // the weights are the first CTA's
 #pragma unroll
-      for (int y = 0; y < kMaxBatch / kThreads; ++y) {
+      for (int y = 0; y < kBatchEach; ++y) {
         const int e = y * kThreads + tid;
         if (e < here) w[y] = *(C.weight + sv::weight_index(C, page_at(L[e]), h, L[e]));
       }
@@ -399,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 2) sv_evict_kernel(const EvictParams
     }
     if (rank == 0)
 #pragma unroll
-      for (int y = 0; y < kMaxBatch / kThreads; ++y) {
+      for (int y = 0; y < kBatchEach; ++y) {
         const int e = y * kThreads + tid;
         if (e < here) C.weight[sv::weight_index(C, page_at(d0 + e), h, d0 + e)] = w[y];
       }
@@ -428,18 +432,29 @@ extern "C" int spec_verify_kv_evict(const sv_paged_cache* cache, const int32_t* 
   P.recent = recent;
   const long long items = static_cast<long long>(B) * P.C.heads;
   if (items > (1 << 27)) return SV_ERR_BAD_SHAPE;
-  // A cluster as large as leaves the GPU's two CTAs an SM, or as the longest rows need.
+  // Clusters as large as the SMs leave, or as the longest rows need. CTAs of 1024 threads, an SM each, where
+  // that takes no threads away from the moves, else two of 512 an SM: a selection takes each CTA's threads
+  // alone (16 rows of 5000 to 16,000 weights 33 us against 46, 8 of 130,000 255 against 326), but 64 rows and heads
+  // of 9000 entries moved by 64 CTAs took 95 us, by 256 of half the size 67. A third of the SMs is left out: 16
+  // clusters of 8 CTAs of 1024 threads did not run at once.
   const long long cap = static_cast<long long>(P.C.max_pages) * P.C.page_size;
   const int sms = sv::device_sms(dev);
-  P.S = 1;
-  while (P.S < kMaxCluster && 2 * P.C.head_dim / 8 / (2 * P.S) >= kMinCols &&
-         (items * P.S * 2 <= 2 * sms || cap > static_cast<long long>(kMaxRun) * P.S))
-    P.S *= 2;
+  auto cluster = [&](long long most_ctas) {
+    int S = 1;
+    while (S < kMaxCluster && 2 * P.C.head_dim / 8 / (2 * S) >= kMinCols &&
+           (2 * items * S <= most_ctas || cap > static_cast<long long>(kMaxRun) * S))
+      S *= 2;
+    return S;
+  };
+  const int large = cluster(2 * sms / 3), small = cluster(2 * sms);
+  const bool alone = 3 * items <= 2 * sms && 2 * large >= small;
+  P.S = alone ? large : small;
   P.words = static_cast<int>((cap / 32 + 15) / 16 * 16 + 16);
   // Two CTAs an SM, or all of its shared memory where there are no more CTAs than SMs: page numbers first,
   // then keys. Keys that are not held leave their place to a run's words of equals.
-  const size_t fixed = 2 * kMaxBatch * sizeof(int) + static_cast<size_t>(P.words) * 4 + P.words + 2 * kBins * sizeof(int);
-  const long long all = items * P.S <= sms ? kSharedMost : kSharedOfTwo, most_pages = items * P.S <= sms ? 16384 : 4096;
+  const int threads = alone ? 1024 : 512;
+  const size_t fixed = 2 * kBatchEach * threads * sizeof(int) + static_cast<size_t>(P.words) * 4 + P.words + 2 * kBins * sizeof(int);
+  const long long all = alone ? kSharedMost : kSharedOfTwo, most_pages = alone ? 16384 : 4096;
   const long long most = cap < 16384 ? cap : 16384, least = cap > 16384 ? ((cap + P.S - 1) / P.S + 127) / 128 * 4 : 0;
   const long long ids = (P.C.max_pages + 3) / 4 * 4, fit = (static_cast<long long>(kSharedMost - fixed) - 4 * least) / 16 * 4;
   P.pages = static_cast<int>(ids < most_pages ? ids : most_pages);
@@ -447,11 +462,12 @@ extern "C" int spec_verify_kv_evict(const sv_paged_cache* cache, const int32_t* 
   const long long room = (all - static_cast<long long>(fixed) - 4 * P.pages) / 16 * 4;
   P.held = static_cast<int>(room < least ? least : (room < most ? room : most));
   const size_t smem = fixed + 4 * static_cast<size_t>(P.pages) + static_cast<size_t>(P.held) * 4;
-  static std::atomic<unsigned long long> allowed{0};
-  if (sv::allow_shared(sv_evict_kernel, kSharedMost, allowed) != SV_OK) return SV_ERR_CUDA;
+  static std::atomic<unsigned long long> allowed[2] = {};
+  const auto kern = alone ? sv_evict_kernel<1024> : sv_evict_kernel<512>;
+  if (sv::allow_shared(kern, kSharedMost, allowed[alone]) != SV_OK) return SV_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(items * P.S));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = static_cast<cudaStream_t>(cuda_stream);
   cudaLaunchAttribute at[1];
@@ -461,7 +477,7 @@ extern "C" int spec_verify_kv_evict(const sv_paged_cache* cache, const int32_t* 
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, sv_evict_kernel, static_cast<const EvictParams>(P)) == cudaSuccess
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<const EvictParams>(P)) == cudaSuccess
              ? SV_OK
              : SV_ERR_CUDA;
 }
