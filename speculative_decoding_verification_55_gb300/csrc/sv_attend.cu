@@ -351,23 +351,25 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2)
 // The kernel and its query tiles: 16 rows where a key head has no more, else on the wide kernel up to 128 rows,
 // whole tokens. Where there are more, it can work on two tiles at once, which then read the keys and values
 // once (heads of 256 have no room for two accumulators). That pays when the second reading would come from
-// HBM, or when there are items for every SM; with fewer and shorter ones, of which many CTAs then take a
-// part, two tiles' parts cost more than the second reading from L2. Measured with 4 key heads and trees of
-// 31 nodes, 8 query heads a key head, one tile at a time against two: 38 rows of 2000 entries 74 against
-// 61 us, of 32,000 675 against 482; 8 rows of 64,000 301 against 227, of 16,000 92 against 94, of 4000
-// 39 against 53; 24 rows of 500 to 6000 68 against 80.
+// HBM, or when there are items for every SM that are long against their start and end; with fewer and
+// shorter ones, of which many CTAs then take a part, two tiles' parts cost more than the second reading from L2.
+// Measured with 4 key heads and trees of 31 nodes, 8 query heads a key head, one tile at a time against two: 38
+// rows of 2000 entries 72 against 59 us, of 32,000 619 against 475; 76 rows of 1000 76 against 84; 8 rows of
+// 64,000 266 against 223, of 16,000 78 against 90, of 4000 37 against 49; 24 rows of 12,000 135 against 153, of
+// 500 to 6000 61 against 74.
 struct Kernel {
   bool wide;
   int tile_rows, part_rows, ways, key_log2, ctas;     // CTAs: of an SM
 };
-constexpr long long kBeyondL2 = 512ll << 20;           // bytes of keys and values, about four times L2
+constexpr long long kBeyondL2 = 768ll << 20;           // bytes of keys and values, about six times L2
+constexpr long long kLongRow = 12 << 7;                // entries
 Kernel kernel_for(int N, int group, const sv_paged_cache* c, long long B, int sms) {
   const int D = c->head_dim;
   if (N * group <= 16) return {false, 16, 16, 1, kTileLog2, D == 256 ? 1 : 2};
   const int rows = 128 / group * group;
   const long long pairs = B * c->heads * ((N * group + 2 * rows - 1) / (2 * rows));
-  const long long bytes = B * c->heads * c->max_pages * c->page_size * D * 4;
-  const bool two = N * group > rows && D < 256 && (pairs >= sms || bytes >= kBeyondL2);
+  const long long entries = static_cast<long long>(c->max_pages) * c->page_size, bytes = B * c->heads * entries * D * 4;
+  const bool two = N * group > rows && D < 256 && ((pairs >= sms && entries >= kLongRow) || bytes >= kBeyondL2);
   return {true, rows, 128, two ? 2 : 1, D == 256 ? 6 : 7, 1};
 }
 constexpr int kMaxSms = 160;

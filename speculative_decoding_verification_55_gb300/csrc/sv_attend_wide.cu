@@ -2,9 +2,10 @@
 // 16-row matrix instruction holds (rounds and trees; the mathematics as in sv_attend.cu): the products
 // run on the fifth-generation tensor cores with accumulators in tensor memory.
 //
-// One CTA per SM: a producer warp copying tiles of 128 entries from the pages, a warp whose one thread
+// One CTA per SM: two warps copying tiles of 128 entries from the pages, a warp whose one thread
 // issues the matrix products, a warp that copies an item's queries and tells the others what the item is,
-// and eight softmax warps. An item is up to 128 query rows of a key head.
+// and eight softmax warps. An item is up to 128 query rows of a key head. (A warp takes 48 ns to issue a box: one
+// alone took 1.55 us for a tile from pages of 16, in boxes of 2 KB, longer than the tile takes from HBM.)
 // Tensor memory holds the scores S [128 rows, 128 entries] of two tiles and the accumulator
 // O [128 rows, D]: 2 x 128 + D of 512 columns.
 //   S = Q K^T        Q and K from shared memory, up to two tiles ahead;
@@ -17,7 +18,7 @@
 // Bound: the bytes of the cache. The 128 x 128 x D products of a tile take about a third of the time
 // that its 4 x 128 x D bytes take from HBM. With two groups of warps on a tile each (a row a thread, two
 // accumulators, S and P sharing one buffer a group) a tile's chain of S, softmax, P V and the next S took
-// 3900 cycles, two tiles at a time; here 128 rows take 1700. Keys and values have slots of the ring
+// 3900 cycles, two tiles at a time; here 128 rows take 1700 to 2000. Keys and values have slots of the ring
 // of their own, given back when their product is done: with one slot for both, the products waited for
 // the next keys before they gave back the last values (19 rows of 8000 entries: 172 us against 118).
 

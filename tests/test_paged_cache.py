@@ -894,3 +894,25 @@ def test_gpu_evict_from_threads(sv):
         assert o.tolist() == on.tolist()
         for x, y in zip((a.k, a.v, a.weight), (k, v, w)):
             assert np.array_equal(host(x), y)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D,dtype", [(64, "bf16"), (128, "f16")])
+def test_gpu_attention_large_trees_long_tables(sv, D, dtype):
+    """More than 128 query rows a key head and an item for every SM in tables with room for long rows: two query
+    tiles at once, of which many rows fill one alone."""
+    rng = np.random.default_rng(8)
+    prefix = rng.integers(0, 400, 170)
+    a = Batch(prefix, 17, 1, 11, D, 16, dtype, seed=D, extra=120)
+    num = rng.integers(0, 18, 170).astype(np.int32)
+    tree = random_tree(rng, 170, 17)
+    tree[5, 3] = 3                                         # a row in error
+    out, lse = sv.attend(a.q, a.cache(sv), dev(a.prefix), dev(num), dev(tree))
+    if num[5] > 3:
+        assert np.isnan(host(out)[5, :num[5]]).all() and np.isnan(host(lse)[5, :num[5]]).all()
+    tree[5] = [-1] + [0] * 16
+    keep = np.arange(170) != 5
+    want, got = sv.attend(a.q, a.cache(sv), dev(a.prefix), dev(num), dev(tree)), (out, lse)
+    for x, y in zip(got, want):
+        assert torch.equal(x[dev(np.flatnonzero(keep)).long()], y[dev(np.flatnonzero(keep)).long()])
+    check_attention(a, *want, a.prefix, num, tree)
