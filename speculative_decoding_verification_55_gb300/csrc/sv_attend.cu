@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2)
   sv::make_plan<kThreads>(R, scan, &plan);
 
   asm volatile("griddepcontrol.launch_dependents;");   // the join kernel's CTAs, which wait for this grid's end
-  if (tid == 0) P.shared[blockIdx.x].x = -1;
+  if (tid == 0 && !P.by_item) P.shared[blockIdx.x].x = -1;
 
   sv::Walk W;
   W.begin(R, plan);
@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2)
       if (!whole) P.part_ml[slot * kRows + r] = make_float2(jm, jl);
       else if (P.lse) P.lse[at] = (jm * c + log2f(jl)) * 0.6931471805599453f;
     }
-    if (!whole && tid == 0 && W.first == 0) sv::tell_shared(P, 0, W.row, W.head, W.q_tile, rows, W.item_at, W.w.tiles, plan);
+    if (tid == 0 && W.first == 0) sv::tell_shared(P, 0, W.row, W.head, W.q_tile, rows, whole, W.item_at, W.w.tiles, plan);
     sv::named_bar_sync(1, kConsumers);         // the scratch is free for the next item's queries
   }
 }
@@ -458,6 +458,9 @@ extern "C" int spec_verify_paged_attention(const void* q, int64_t q_row_stride,
   const long long items = static_cast<long long>(B) * cache->heads * ((N * group + P.R.q_rows - 1) / P.R.q_rows);
   const long long most = items * ((static_cast<long long>(cache->max_pages) * cache->page_size + tile - 1) / tile);
   const int grid = static_cast<int>(most < sms * k.ctas ? most : sms * k.ctas);
+  // Few items against the CTAs: each has many parts, and their records are by item.
+  const int tiles = (N * group + k.tile_rows - 1) / k.tile_rows;
+  P.by_item = static_cast<long long>(B) * cache->heads * tiles * 4 <= grid ? tiles : 0;
   char* ws = static_cast<char*>(workspace);
   P.shared = reinterpret_cast<int4*>(ws);
   ws += kSharedBytes;
@@ -475,6 +478,5 @@ extern "C" int spec_verify_paged_attention(const void* q, int64_t q_row_stride,
   else if (D == 64) st = f16 ? launch<true, 64>(P, kmap, vmap, grid, s) : launch<false, 64>(P, kmap, vmap, grid, s);
   else if (D == 128) st = f16 ? launch<true, 128>(P, kmap, vmap, grid, s) : launch<false, 128>(P, kmap, vmap, grid, s);
   else st = f16 ? launch<true, 256>(P, kmap, vmap, grid, s) : launch<false, 256>(P, kmap, vmap, grid, s);
-  // Few items against the CTAs: each has many parts.
-  return st == SV_OK ? sv::launch_attend_join(P, f16, k.wide, items * (k.ways == 2 ? 16 : 4) <= grid, grid, s) : st;
+  return st == SV_OK ? sv::launch_attend_join(P, f16, k.wide, grid, s) : st;
 }

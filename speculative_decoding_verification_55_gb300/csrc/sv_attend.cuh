@@ -18,8 +18,10 @@ struct AttendParams {
   // Items that several CTAs share leave a part each, which the join kernel puts together. An item's
   // first part is part 2 p + 1 of the CTA p that holds its first tile, the others part 2 p of theirs, each a
   // tile of rows per way.
-  int4* shared;                                // [grid][ways] the shared item whose first tile a CTA holds:
-                                               // row (-1: none), head, 256 x query tile + its rows, the last CTA
+  int by_item;                                 // query tiles of a row and head, where records are by item
+  int4* shared;                                // [grid][ways] the shared item whose first tile a CTA holds: row
+                                               // (-1: none), head, 256 x query tile + its rows, the last CTA; or
+                                               // by item: the first CTA (-1: it is whole), 0, rows, the last CTA
   float* part_o;                               // [2 grid][ways][D][rows]
   float2* part_ml;                             // [2 grid][ways][rows] maximum and sum
 };
@@ -65,14 +67,19 @@ __device__ __forceinline__ void fill_unused(const AttendParams& P, int D, int ti
   }
 }
 
-// The item that this CTA begins and does not end, for the join kernel (one thread).
+// The item that this CTA begins, for the join kernel (one thread).
 __device__ __forceinline__ void tell_shared(const AttendParams& P, int way, int row, int head, int q_tile, int rows,
-                                            long long item_at, int tiles, const Plan& plan) {
-  P.shared[blockIdx.x * P.ways + way] = make_int4(row, head, q_tile << 8 | rows, unit_owner(item_at + tiles - 1, plan));
+                                            bool whole, long long item_at, int tiles, const Plan& plan) {
+  if (whole && !P.by_item) return;
+  const int cta = blockIdx.x, last = unit_owner(item_at + tiles - 1, plan);
+  if (P.by_item)
+    P.shared[(row * P.R.C.heads + head) * P.by_item + q_tile] = make_int4(whole ? -1 : cta, 0, rows, last);
+  else
+    P.shared[cta * P.ways + way] = make_int4(row, head, q_tile << 8 | rows, last);
 }
 
 // Joins the parts of the items that the attention kernel's `grid` CTAs shared.
-int launch_attend_join(const AttendParams& P, bool f16, bool wide, bool many_parts, int grid, cudaStream_t st);
+int launch_attend_join(const AttendParams& P, bool f16, bool wide, int grid, cudaStream_t st);
 
 // The wide kernel (at most 128 query heads a key head; query tiles of tile_rows <= 128 rows, whole tokens of
 // which q's boxes hold q_tokens; key tiles of 128, or of 64 for heads of 256; two ways up to heads of 128).

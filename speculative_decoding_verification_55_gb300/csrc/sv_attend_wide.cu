@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kProducts) tm_alloc(&S.tm);
   sv::make_plan<kThreads>(R, S.scan, &S.plan);
   asm volatile("griddepcontrol.launch_dependents;");   // the join kernel's CTAs, which wait for this grid's end
-  if (tid < kWays) P.shared[blockIdx.x * kWays + tid].x = -1;
+  if (tid < kWays && !P.by_item) P.shared[blockIdx.x * kWays + tid].x = -1;
   fence_after();
   const uint32_t tm = S.tm;
   volatile int* const lost = &S.lost;
@@ -122,7 +122,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto told = [&](int k) {
     Item I;
     if (sv::mbar_wait(sv::smem_addr(S.told + k % kPieces), (k / kPieces) & 1)) I = S.items[k % kPieces];
-    else I.count = 0;
+    else {
+      I.count = 0;
+      *lost = 1;
+    }
     return I;
   };
   if (warp >= kCopies && warp <= kItems) {
@@ -471,8 +474,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       fence_before();
       sv::named_bar_sync(1, kSoft);            // the sums have been read
-      if (!whole && (tid & 127) == 0 && half == 0 && W.first == 0 && rows > 0)
-        sv::tell_shared(P, way, W.row, W.head, W.q_tile * kWays + way, rows, W.item_at, W.tiles, S.plan);
+      if ((tid & 127) == 0 && half == 0 && W.first == 0 && rows > 0)
+        sv::tell_shared(P, way, W.row, W.head, W.q_tile * kWays + way, rows, whole, W.item_at, W.tiles, S.plan);
     }
     fence_before();
   }
@@ -493,8 +496,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (x % D == 0 && whole && P.lse) P.lse[at] = __int_as_float(0x7fffffff);
           if (x % D == 0 && !whole) P.part_ml[slot * kRows + r].y = __int_as_float(0x7fffffff);
         }
-        if (!whole && tid == 0 && W.first == 0 && rows > 0)
-          sv::tell_shared(P, way, W.row, W.head, q_tile, rows, W.item_at, W.w.tiles, S.plan);
+        if (tid == 0 && W.first == 0 && rows > 0)
+          sv::tell_shared(P, way, W.row, W.head, q_tile, rows, whole, W.item_at, W.w.tiles, S.plan);
       }
   }
   if (warp == kProducts) tm_free(tm);
