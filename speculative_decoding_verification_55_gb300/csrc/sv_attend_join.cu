@@ -9,7 +9,7 @@
 // possible item and not a CTA of the attention's; otherwise all columns.
 // Every item that is not whole goes through here. Joining in the last CTA to arrive instead kept that
 // CTA 10 us (3 parts of 128 rows) to 30 us (76 parts of 40 rows); this kernel is launched ahead (its
-// CTAs wait for the attention's end) and takes 3 to 4.
+// CTAs wait for the attention's end) and takes 2 to 4.
 
 #include "sv_attend.cuh"
 

@@ -450,7 +450,7 @@ extern "C" int spec_verify_kv_evict(const sv_paged_cache* cache, const int32_t* 
   const bool alone = 3 * items <= 2 * sms && 2 * large >= small;
   P.S = alone ? large : small;
   P.words = static_cast<int>((cap / 32 + 15) / 16 * 16 + 16);
-  // Two CTAs an SM, or all of its shared memory where there are no more CTAs than SMs: page numbers first,
+  // A half of an SM's shared memory, or all where a CTA has the SM alone: page numbers first,
   // then keys. Keys that are not held leave their place to a run's words of equals.
   const int threads = alone ? 1024 : 512;
   const size_t fixed = 2 * kBatchEach * threads * sizeof(int) + static_cast<size_t>(P.words) * 4 + P.words + 2 * kBins * sizeof(int);
