@@ -916,3 +916,24 @@ def test_gpu_attention_large_trees_long_tables(sv, D, dtype):
     for x, y in zip(got, want):
         assert torch.equal(x[dev(np.flatnonzero(keep)).long()], y[dev(np.flatnonzero(keep)).long()])
     check_attention(a, *want, a.prefix, num, tree)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N,G", [(1, 4), (9, 4), (31, 8)])
+def test_gpu_attention_one_workspace_other_lengths(sv, N, G):
+    """Few rows, one graph replayed on lengths that leave rows short, without tokens and in error: nothing of an
+    earlier call's parts is joined."""
+    a = Batch((5000, 3000, 4000), N, 2, G, 128, 16, seed=N, poison=False)
+    c, pre, num = a.cache(sv), dev(a.prefix), dev([N] * 3)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        out, lse = sv.attend(a.q, c, pre, num)
+    for prefix, m in (((5000, 3000, 4000), (N, N, N)), ((5000, 20, 4000), (0, N, N + 1)), ((0, 3000, 90), (1, 0, N)),
+                      ((5000, 3000, 4000), (N, N, N))):
+        pre.copy_(dev(prefix))
+        num.copy_(dev(m))
+        graph.replay()
+        torch.cuda.synchronize()
+        check_attention(a, out, lse, np.array(prefix), np.array(m), None)
