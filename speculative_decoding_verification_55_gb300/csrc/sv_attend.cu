@@ -231,18 +231,21 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2)
             l[x] += p0 + p1;
             pf[2 * y + x] = sv::pack2<F16>(p0, p1);
           }
-        const uint32_t keep0 = edge ? (j0 + 2 * t4 < entries ? 0xffffu : 0u) | (j0 + 2 * t4 + 1 < entries ? 0xffff0000u : 0u) : 0u;
-        const uint32_t keep1 = edge ? (j0 + 8 + 2 * t4 < entries ? 0xffffu : 0u) | (j0 + 9 + 2 * t4 < entries ? 0xffff0000u : 0u) : 0u;
+        // Bit masks of this thread's entries that are there, and of those that are the round's own (from n on).
+        auto below = [&](int j, int x) { return (j < x ? 0xffffu : 0u) | (j + 1 < x ? 0xffff0000u : 0u); };
+        const int jv = j0 + 2 * t4;
+        const uint32_t keep0 = edge ? below(jv, entries) : 0u, keep1 = edge ? below(jv + 8, entries) : 0u;
+        const uint32_t own0 = edge ? ~below(jv, n) : 0u, own1 = edge ? ~below(jv + 8, n) : 0u;
 #pragma unroll
         for (int y = 0; y < D / 16; ++y) {
           uint32_t vf[4];
           sv::ldsm4_t(vf, sv::swizzled(vb + (y >> 2) * (kTile * 128), 16 * warp + (lane & 15),
                                        ((y & 3) << 1) + (lane >> 4)));
           if (edge) {
-            vf[0] = finite2<F16>(vf[0], keep0, odd);
-            vf[1] = finite2<F16>(vf[1], keep1, odd);
-            vf[2] = finite2<F16>(vf[2], keep0, odd);
-            vf[3] = finite2<F16>(vf[3], keep1, odd);
+            vf[0] = finite2<F16>(vf[0] & keep0, own0, odd);
+            vf[1] = finite2<F16>(vf[1] & keep1, own1, odd);
+            vf[2] = finite2<F16>(vf[2] & keep0, own0, odd);
+            vf[3] = finite2<F16>(vf[3] & keep1, own1, odd);
           }
           sv::mma<F16>(o[2 * y], pf, vf[0], vf[1]);
           sv::mma<F16>(o[2 * y + 1], pf, vf[2], vf[3]);

@@ -32,17 +32,17 @@ __device__ __forceinline__ float value_of(uint32_t h) {
   return __uint_as_float(h << 16);
 }
 
-// A register of two values with those of entries >= `total` (bit masks keep_lo, keep_hi) cleared, and
-// those that are not finite cleared and reported.
+// A register of two values, of which `own` (a mask of bits) marks those of the round's own entries: of these, what
+// is not finite is cleared and reported. The others are attended by every token and stay as they are.
 template <bool F16>
-__device__ __forceinline__ uint32_t finite2(uint32_t x, uint32_t keep, bool& odd) {
+__device__ __forceinline__ uint32_t finite2(uint32_t x, uint32_t own, bool& odd) {
   constexpr uint32_t e = F16 ? 0x7c00u : 0x7f80u;
-  x &= keep;
-  if ((x & e) == e) {
+  const uint32_t y = x & own;
+  if ((y & e) == e) {
     odd = true;
     x &= 0xffff0000u;
   }
-  if (((x >> 16) & e) == e) {
+  if (((y >> 16) & e) == e) {
     odd = true;
     x &= 0xffffu;
   }

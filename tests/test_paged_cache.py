@@ -937,3 +937,30 @@ def test_gpu_attention_one_workspace_other_lengths(sv, N, G):
         graph.replay()
         torch.cuda.synchronize()
         check_attention(a, out, lse, np.array(prefix), np.array(m), None)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N,G,dtype", [(1, 4, "bf16"), (1, 8, "f16"), (3, 5, "bf16"), (9, 4, "bf16"), (9, 4, "f16")])
+def test_gpu_values_before_the_round_that_are_not_finite(sv, N, G, dtype):
+    """Infinities and NaN in the last entries before the round, which every token attends."""
+    prefix = (100, 111, 64, 97)
+    for back in (1, 2, 7, 15):
+        a = Batch(prefix, N, 2, G, 128, 16, dtype, seed=back)
+        for b, n in enumerate(prefix):
+            p, s = oracle.place(a.table, b, n - back, 16)
+            a.v[p, 0, s, 3] = math.inf
+            a.v[p, 0, s, 64] = -math.inf
+            a.v[p, 1, s, 17] = math.nan
+        out, lse = sv.attend(a.q, a.cache(sv), dev(a.prefix))
+        got = host(out)
+        assert np.isposinf(got[:, :, :G, 3]).all() and np.isneginf(got[:, :, :G, 64]).all()
+        assert np.isnan(got[:, :, G:, 17]).all() and np.isfinite(host(lse)).all()
+        got[:, :, :G, 3] = got[:, :, :G, 64] = got[:, :, G:, 17] = 0.0
+        a.v[a.v.isinf()] = 0.0
+        for b, n in enumerate(prefix):
+            p, s = oracle.place(a.table, b, n - back, 16)
+            a.v[p, 1, s, 17] = 0.0
+        want, _ = sv.attend(a.q, a.cache(sv), dev(a.prefix))
+        want = host(want)
+        want[:, :, :G, 3] = want[:, :, :G, 64] = want[:, :, G:, 17] = 0.0
+        assert np.array_equal(got, want)                   # nothing else is changed
