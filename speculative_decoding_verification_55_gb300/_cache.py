@@ -6,6 +6,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import threading
 
 from ._binding import SV_DTYPE_BF16, SV_DTYPE_F16, SV_OK, SpecVerifyError, _on, _stream_handle, lib
 
@@ -188,6 +189,8 @@ def spec_verify_kv_evict(cache, length, budget, recent, out_len, stream=None) ->
 
 
 _attend_ws = {}
+# A call makes two launches on its stream's workspace: another thread's must not come in between.
+_attend_lock = threading.Lock()
 
 
 def _attend_workspace(N, Hq, cache):
@@ -208,7 +211,7 @@ def _attend_workspace(N, Hq, cache):
 
 def attend(q, cache, prefix_len, num_queries=None, tree_parents=None, scale=None, stream=None):
     """Allocates the outputs, runs spec_verify_paged_attention and returns (out [B, N, Hq, D],
-    lse [B, N, Hq]), both of the given stream (the current one unless given)."""
+    lse [B, N, Hq]), both of the given stream (the current one unless given). Host threads may call it at once."""
     import torch
     if stream is not None:
         if not isinstance(stream, torch.cuda.Stream):
@@ -219,7 +222,8 @@ def attend(q, cache, prefix_len, num_queries=None, tree_parents=None, scale=None
     _on_gpu(cache.device)
     out = torch.empty((cache.B, N, Hq, cache.head_dim), dtype=q.dtype, device=cache.device)
     lse = torch.empty((cache.B, N, Hq), dtype=torch.float32, device=cache.device)
-    ws = _attend_workspace(N, Hq, cache)
-    _attention(q, cache, prefix_len, num_queries, tree_parents, N, Hq, rs, ts, out.data_ptr(), lse.data_ptr(),
-               ws.data_ptr(), ws.nbytes, scale, None)
+    with _attend_lock:
+        ws = _attend_workspace(N, Hq, cache)
+        _attention(q, cache, prefix_len, num_queries, tree_parents, N, Hq, rs, ts, out.data_ptr(), lse.data_ptr(),
+                   ws.data_ptr(), ws.nbytes, scale, None)
     return out, lse

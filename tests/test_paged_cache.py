@@ -964,3 +964,58 @@ def test_gpu_values_before_the_round_that_are_not_finite(sv, N, G, dtype):
         want = host(want)
         want[:, :, :G, 3] = want[:, :, :G, 64] = want[:, :, G:, 17] = 0.0
         assert np.array_equal(got, want)                   # nothing else is changed
+
+
+def test_attend_from_threads_on_one_stream(monkeypatch):
+    """Calls of attend from several host threads share a stream's workspace: one is done with its launches before the
+    next has the workspace (no GPU: the call itself is stood in for)."""
+    import threading
+    import time
+    from concurrent.futures import ThreadPoolExecutor
+    from speculative_decoding_verification_55_gb300 import _cache
+    k = torch.zeros((5, 2, 16, 64), dtype=torch.bfloat16)
+    c = _cache.PagedCache(k, k.clone(), torch.zeros((3, 2), dtype=torch.int32))
+    q, n = torch.zeros((3, 4, 8, 64), dtype=torch.bfloat16), torch.zeros(3, dtype=torch.int32)
+    shared, inside, most, failing = torch.zeros(64, dtype=torch.uint8), [], [], threading.Event()
+
+    def workspace(*args):
+        inside.append(1)
+        return shared
+
+    def launches(*args):
+        time.sleep(0.002)
+        most.append(len(inside))
+        inside.pop()
+        if failing.is_set():
+            raise RuntimeError("refused")
+
+    monkeypatch.setattr(_cache, "_on_gpu", lambda device: None)
+    monkeypatch.setattr(_cache, "_attend_workspace", workspace)
+    monkeypatch.setattr(_cache, "_attention", launches)
+    with ThreadPoolExecutor(4) as pool:
+        list(pool.map(lambda x: _cache.attend(q, c, n), range(40)))
+    assert most == [1] * 40
+    failing.set()                                          # a refused call leaves the workspace to others
+    for _ in range(2):
+        with pytest.raises(RuntimeError, match="refused"):
+            _cache.attend(q, c, n)
+
+
+@pytest.mark.gpu
+def test_gpu_attend_from_threads_on_one_stream(sv):
+    """The same on the GPU: threads on the default stream, batches whose items have many parts."""
+    from concurrent.futures import ThreadPoolExecutor
+    jobs = []
+    for prefix, N, H, G, D in (((9000,), 1, 2, 8, 128), ((4000, 900), 9, 2, 4, 64), ((700, 64, 3000), 31, 1, 8, 128)):
+        a = Batch(prefix, N, H, G, D, 16, seed=N)
+        c, n = a.cache(sv), dev(a.prefix)
+        jobs.append((a, c, n, sv.attend(a.q, c, n)))
+    torch.cuda.synchronize()
+
+    def run(x):
+        a, c, n, (out, lse) = jobs[x % 3]
+        got = [sv.attend(a.q, c, n) for _ in range(60)]
+        return all(torch.equal(o, out) and torch.equal(s, lse) for o, s in got)
+
+    with ThreadPoolExecutor(6) as pool:
+        assert all(pool.map(run, range(6)))
