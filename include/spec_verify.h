@@ -69,7 +69,7 @@ typedef enum {
   SV_ERR_UNSUPPORTED_DEVICE = 7,  /* the current device is not compute capability 10.3           */
   SV_ERR_SCRATCH_TOO_SMALL = 8,   /* spec_verify_noalloc: the sizes need more scratch than
                                      SV_NOALLOC_SCRATCH_BYTES                                     */
-  SV_ERR_OVERLAP = 9              /* an output array is also an input that the call reads         */
+  SV_ERR_OVERLAP = 9              /* an output array shares memory with another array of the call  */
 } sv_status;
 
 /* Logits are SV_DTYPE_F32 or SV_DTYPE_BF16, paged caches SV_DTYPE_BF16 or SV_DTYPE_F16. */
@@ -303,6 +303,8 @@ int spec_verify_kv_rollback(const int32_t* prefix_len, const int32_t* draft_len,
  * The struct is host memory, read before the call returns; the arrays are caller-owned device memory.
  * Rows may share pages that are only read (a common prefix); spec_verify_kv_append and
  * spec_verify_kv_evict need the pages they write to be the row's own.
+ * out_len, out, out_lse, the workspace and, where a call adds to it, weight share no memory with any other array of
+ * the call, strided ones from their first element to their last (SV_ERR_OVERLAP).
  *
  * Data errors never trap. A row is in error when a length or count is out of range, its entries
  * exceed max_pages * page_size, or a page number that its entries reach is outside [0, num_pages). */
@@ -326,8 +328,7 @@ typedef struct {
  *                writes nothing and is not an error here: out_len is prefix_len.
  * path           [B, N] int32 or NULL.
  * out_len        [B] int32, entries after the call: prefix_len + num_new; -1 for a row in error, or one
- *                with a path entry outside [0, N), of which nothing is written. May be NULL; shares no
- *                memory with the other int32 arrays (SV_ERR_OVERLAP).
+ *                with a path entry outside [0, N), of which nothing is written. May be NULL.
  * 1 <= N <= SV_MAX_GAMMA + 1. One launch on cuda_stream. */
 int spec_verify_kv_append(const void* k_new, const void* v_new, int64_t row_stride,
                           int64_t token_stride, const sv_paged_cache* cache,
@@ -350,7 +351,6 @@ int spec_verify_kv_append(const void* k_new, const void* v_new, int64_t row_stri
  * out_lse        [B, N, Hq] fp32, contiguous; 0 for i >= m_b. May be NULL.
  * workspace      device scratch of spec_verify_paged_attention_workspace_size(...) bytes, 256-byte
  *                aligned. It needs no setup; one workspace serves one call at a time, of any sizes.
- * out and out_lse must not share memory with q, from its first element to its last (SV_ERR_OVERLAP).
  * A row in error gets NaN in all its outputs (a bad page or tree: in those of its m_b tokens).
  * The softmax and the sums run in fp32; the probabilities are rounded to the cache's dtype for the
  * product with the values. 1 <= N <= SV_MAX_GAMMA + 1, Hq <= 1024. */
@@ -387,8 +387,7 @@ int spec_verify_kv_weights(const void* q, int64_t q_row_stride, int64_t q_token_
  * A row with length[b] <= budget is left alone.
  *
  * length         [B] int32, entries per row
- * out_len        [B] int32: min(length, budget); -1 for a row in error, which is left alone. Shares
- *                no memory with length (SV_ERR_OVERLAP).
+ * out_len        [B] int32: min(length, budget); -1 for a row in error, which is left alone.
  * budget >= 1, 0 <= recent <= budget (else SV_ERR_BAD_SHAPE). cache->weight is required. One launch. */
 int spec_verify_kv_evict(const sv_paged_cache* cache, const int32_t* length, int32_t budget,
                          int32_t recent, int32_t* out_len, int32_t B, void* cuda_stream);

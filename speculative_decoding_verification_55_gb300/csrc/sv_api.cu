@@ -189,7 +189,7 @@ const char* spec_verify_status_string(int status) {
     case SV_ERR_SCRATCH_TOO_SMALL:
       return "SV_ERR_SCRATCH_TOO_SMALL: the sizes need more than the library's static scratch "
              "(SV_NOALLOC_SCRATCH_BYTES)";
-    case SV_ERR_OVERLAP: return "SV_ERR_OVERLAP: an output array is also an input";
+    case SV_ERR_OVERLAP: return "SV_ERR_OVERLAP: an output array shares memory with another array of the call";
     default: return "unknown sv_status";
   }
 }

@@ -93,9 +93,13 @@ extern "C" int spec_verify_kv_append(const void* k_new, const void* v_new, int64
   if (sv::misaligned(v_new, 16) || sv::misaligned(prefix_len, 4) || sv::misaligned(num_new, 4) ||
       sv::misaligned(path, 4) || sv::misaligned(out_len, 4))
     return SV_ERR_MISALIGNED;
-  const long long rows = 4ll * B;
-  if (sv::overlap(out_len, rows, prefix_len, rows) || sv::overlap(out_len, rows, num_new, rows) ||
-      sv::overlap(out_len, rows, path, rows * N))
+  const unsigned long long rows = 4ull * B;
+  const int32_t H = cache->heads, D = cache->head_dim;
+  if (sv::overlap({{out_len, rows}},
+                  {{prefix_len, rows}, {num_new, rows}, {path, rows * N}, sv::table_of(cache, B), sv::weights_of(cache),
+                   sv::pages_of(cache, cache->k), sv::pages_of(cache, cache->v),
+                   sv::tokens_of(k_new, row_stride, token_stride, B, N, H, D),
+                   sv::tokens_of(v_new, row_stride, token_stride, B, N, H, D)}))
     return SV_ERR_OVERLAP;
   int dev = 0;
   st = sv::current_device_status(&dev);

@@ -418,13 +418,14 @@ extern "C" int spec_verify_paged_attention(const void* q, int64_t q_row_stride,
       sv::misaligned(num_queries, 4) || sv::misaligned(tree_parents, 4) ||
       sv::misaligned(workspace, 256))
     return SV_ERR_MISALIGNED;
-  const long long q_bytes = 2 * ((B - 1) * static_cast<long long>(q_row_stride) + (N - 1) * static_cast<long long>(q_token_stride) +
-                                 static_cast<long long>(Hq) * cache->head_dim);
-  const long long tokens = static_cast<long long>(B) * N * Hq;
-  if (sv::overlap(out, tokens * cache->head_dim * 2, q, q_bytes) || sv::overlap(out_lse, tokens * 4, q, q_bytes))
+  const size_t need = spec_verify_paged_attention_workspace_size(N, Hq, cache);
+  if (!workspace || workspace_bytes < need) return SV_ERR_WORKSPACE_TOO_SMALL;
+  const unsigned long long rows = 4ull * B, tokens = rows * N * Hq;
+  if (sv::overlap({{out, tokens / 2 * cache->head_dim}, {out_lse, tokens}, {workspace, need}},
+                  {sv::tokens_of(q, q_row_stride, q_token_stride, B, N, Hq, cache->head_dim), {prefix_len, rows},
+                   {num_queries, rows}, {tree_parents, rows * N}, sv::table_of(cache, B),
+                   sv::weights_of(cache), sv::pages_of(cache, cache->k), sv::pages_of(cache, cache->v)}))
     return SV_ERR_OVERLAP;
-  if (!workspace || workspace_bytes < spec_verify_paged_attention_workspace_size(N, Hq, cache))
-    return SV_ERR_WORKSPACE_TOO_SMALL;
   int dev = 0;
   st = sv::current_device_status(&dev);
   if (st != SV_OK) return st;

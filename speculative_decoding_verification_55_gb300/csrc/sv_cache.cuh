@@ -9,6 +9,7 @@
 
 #include <atomic>
 #include <cstdint>
+#include <initializer_list>
 
 #include "../../include/spec_verify.h"
 
@@ -57,10 +58,45 @@ inline bool misaligned(const void* p, uintptr_t a) {
   return p && (reinterpret_cast<uintptr_t>(p) % a) != 0;
 }
 
-// Whether arrays of these sizes share memory (null: no array).
-inline bool overlap(const void* a, long long a_bytes, const void* b, long long b_bytes) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return a && b && (x < y ? y - x < static_cast<uintptr_t>(a_bytes) : x - y < static_cast<uintptr_t>(b_bytes));
+// An array of a call, from its first byte to its last (null: none).
+struct Span {
+  const void* p;
+  unsigned long long bytes;
+};
+inline bool overlap(const Span& a, const Span& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return a.p && b.p && (x < y ? y - x < a.bytes : x - y < b.bytes);
+}
+// Whether one of the arrays that a call writes shares memory with another of them or with one that it reads.
+inline bool overlap(std::initializer_list<Span> written, std::initializer_list<Span> read) {
+  for (const Span* w = written.begin(); w != written.end(); ++w) {
+    for (const Span* x = w + 1; x != written.end(); ++x)
+      if (overlap(*w, *x)) return true;
+    for (const Span& r : read)
+      if (overlap(*w, r)) return true;
+  }
+  return false;
+}
+// From the first element to the last of 16-bit elements, `inner` of them together, over three strided dimensions.
+inline Span span_of(const void* p, int64_t inner, int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t n2, int64_t s2) {
+  const __int128 e = static_cast<__int128>(n0 - 1) * s0 + static_cast<__int128>(n1 - 1) * s1 +
+                     static_cast<__int128>(n2 - 1) * s2 + inner;
+  const __int128 most = static_cast<__int128>(1) << 62;
+  return {p, static_cast<unsigned long long>(2 * e < most ? 2 * e : most)};
+}
+// A cache's keys or values, its weights and its page table.
+inline Span pages_of(const sv_paged_cache* c, const void* base) {
+  return span_of(base, c->head_dim, c->num_pages, c->page_stride, c->heads, c->head_stride, c->page_size, c->slot_stride);
+}
+inline Span weights_of(const sv_paged_cache* c) {
+  return {c->weight, 4ull * static_cast<unsigned>(c->num_pages) * static_cast<unsigned>(c->heads * c->page_size)};
+}
+inline Span table_of(const sv_paged_cache* c, int32_t B) {
+  return {c->page_table, 4ull * static_cast<unsigned>(B) * static_cast<unsigned>(c->max_pages)};
+}
+// A round's [B, N, heads, D] input.
+inline Span tokens_of(const void* x, int64_t row_stride, int64_t token_stride, int32_t B, int32_t N, int32_t heads, int32_t D) {
+  return span_of(x, static_cast<int64_t>(heads) * D, B, row_stride, N, token_stride, 1, 0);
 }
 
 // The checks of a cache argument; fills the device form. need_weight: the call reads or writes weights.

@@ -422,7 +422,10 @@ extern "C" int spec_verify_kv_evict(const sv_paged_cache* cache, const int32_t* 
   if (!length || !out_len) return SV_ERR_NULL_POINTER;
   if (budget < 1 || recent < 0 || recent > budget) return SV_ERR_BAD_SHAPE;
   if (sv::misaligned(length, 4) || sv::misaligned(out_len, 4)) return SV_ERR_MISALIGNED;
-  if (sv::overlap(out_len, 4ll * B, length, 4ll * B)) return SV_ERR_OVERLAP;
+  const unsigned long long rows = 4ull * B;
+  if (sv::overlap({{out_len, rows}}, {{length, rows}, sv::table_of(cache, B), sv::weights_of(cache),
+                                      sv::pages_of(cache, cache->k), sv::pages_of(cache, cache->v)}))
+    return SV_ERR_OVERLAP;
   int dev = 0;
   st = sv::current_device_status(&dev);
   if (st != SV_OK) return st;

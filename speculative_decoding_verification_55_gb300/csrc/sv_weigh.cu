@@ -354,6 +354,12 @@ extern "C" int spec_verify_kv_weights(const void* q, int64_t q_row_stride, int64
   if (sv::misaligned(lse, 4) || sv::misaligned(prefix_len, 4) || sv::misaligned(num_kept, 4) ||
       sv::misaligned(path, 4))
     return SV_ERR_MISALIGNED;
+  const unsigned long long row_bytes = 4ull * B;
+  if (sv::overlap({sv::weights_of(cache)},
+                  {sv::tokens_of(q, q_row_stride, q_token_stride, B, N, Hq, cache->head_dim), {lse, row_bytes * N * Hq},
+                   {prefix_len, row_bytes}, {num_kept, row_bytes}, {path, row_bytes * N}, sv::table_of(cache, B),
+                   sv::pages_of(cache, cache->k), sv::pages_of(cache, cache->v)}))
+    return SV_ERR_OVERLAP;
   int dev = 0;
   st = sv::current_device_status(&dev);
   if (st != SV_OK) return st;

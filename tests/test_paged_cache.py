@@ -1019,3 +1019,32 @@ def test_gpu_attend_from_threads_on_one_stream(sv):
 
     with ThreadPoolExecutor(6) as pool:
         assert all(pool.map(run, range(6)))
+
+
+def test_overlap_refusals_of_every_array(L):
+    """An array that a call writes shares memory with one that it reads, or with another it writes."""
+    M = 1 << 20
+    table, pre, num, par, out, lse, ws, olen = (FAKE + x * M for x in (3, 5, 11, 12, 6, 7, 8, 9))
+    c = cache_struct()
+    base = dict(num=num, par=par)
+    # Two rows of five pages: 40 bytes of page table; 7 pages of 8 heads of 16 slots: 3584 bytes of weights.
+    for at in (table + 36, table - 4, FAKE + 2 * M + 3580, FAKE + 64, FAKE + M + 7 * 8 * 16 * 128 * 2 - 4):
+        got = calls(L, c, olen=at, **base)
+        assert (got["append"], got["evict"]) == (9, 9), hex(at)
+    for at in (pre, num + 4, par + 4 * 17):
+        assert calls(L, c, olen=at, **base)["append"] == 9
+    assert calls(L, c, olen=FAKE + 4 * M, **base)["append"] == 9      # the tokens
+    size = 2 * 9 * 32 * 128 * 2                            # of the queries and the output, one row after the other
+    for at in (table - 16, table, pre, num, par, FAKE + 2 * M, FAKE + M, FAKE + M - size + 16, FAKE + 4 * M + size - 16, lse, ws):
+        assert calls(L, c, out=at, **base)["attend"] == 9, hex(at)
+    for at in (table + 36, pre + 4, num, par + 4 * 17, FAKE + 16, out + size - 4, ws + 512):
+        assert calls(L, c, lse=at, **base)["attend"] == 9, hex(at)
+    for at in (table & ~255, pre, num, par, FAKE + 4 * M, FAKE + M):
+        assert calls(L, c, ws=at, **base)["attend"] == 9, hex(at)
+    for name, at in (("q", 64), ("lse", 3580), ("pre", 0), ("num", 4), ("par", 3584 - 4 * 18)):
+        kw = {**base, name: FAKE + 2 * M + at}
+        assert calls(L, c, **kw)["weigh"] == 9, name
+    assert calls(L, cache_struct(page_table=FAKE + 2 * M + 4), **base)["weigh"] == 9
+    # The extent of pages with large strides is not cut off at 64 bits.
+    far = cache_struct(num_pages=(1 << 31) - 1, page_stride=(1 << 38) - 8)
+    assert calls(L, far, **base)["attend"] == 9
