@@ -339,7 +339,8 @@ int spec_verify_kv_append(const void* k_new, const void* v_new, int64_t row_stri
  * Token i < m_b = num_queries[b] of row b attends the n_b entries before the round, itself, and of the
  * round's other tokens those before it (a chain), or its ancestors when tree_parents is given:
  *   s_ij = scale * q_i . k_j,  lse_i = log sum_j exp(s_ij),  out_i = sum_j exp(s_ij - lse_i) v_j.
- * An entry that a token does not attend has no part in its outputs, whatever it holds (NaN included).
+ * An entry that a token does not attend has no part in its outputs, whatever it holds (NaN included). An attended
+ * value that is not finite leaves the output not finite: NaN where its probability is too small for fp32.
  * m_b = 1 is the attention of one new token.
  *
  * q              [B, N, Hq, D] of the cache's dtype, strides as k_new's in spec_verify_kv_append

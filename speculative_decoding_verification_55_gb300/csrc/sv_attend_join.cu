@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(kThreads) sv_attend_join_kernel(const sv::Atte
       M = top;
       L = L * f + (e.x == -INFINITY ? e.y : e.y * g);  // the former: 0, or NaN
 #pragma unroll
-      for (int x = 0; x < kCols; ++x) a[x] = a[x] * f + (g == 0.0f ? 0.0f : o[x] * g);
+      for (int x = 0; x < kCols; ++x) a[x] = a[x] * f + o[x] * g;   // (an infinity times a weight of 0: NaN)
     }
 #pragma unroll
     for (int x = 0; x < kCols; ++x) acc[warp][x][lane] = a[x];

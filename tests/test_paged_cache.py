@@ -1048,3 +1048,23 @@ def test_overlap_refusals_of_every_array(L):
     # The extent of pages with large strides is not cut off at 64 bits.
     far = cache_struct(num_pages=(1 << 31) - 1, page_stride=(1 << 38) - 8)
     assert calls(L, far, **base)["attend"] == 9
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N,G,rows", [(1, 4, 1), (1, 4, 3), (9, 4, 1), (9, 4, 3), (1, 4, 90)])
+def test_gpu_infinities_in_a_part_that_weighs_nothing(sv, N, G, rows):
+    """Infinite values in blocks' parts of a row whose maxima lie so far below another part's that their weight is 0
+    in fp32: what comes of them is not finite, whichever block had them."""
+    a = Batch((12000,) * rows, N, 1, G, 64, 128, seed=N, poison=False)
+    a.q[:] = 1.0
+    a.k.clamp_(-0.1, 0.1)
+    for b in range(rows):
+        p, s = oracle.place(a.table, b, 128 * 40, 128)
+        a.k[p, :, s] = 40.0                                # its score is 320, the others' below 1
+        for t in range(41, 93):
+            p, s = oracle.place(a.table, b, 128 * t + 1, 128)
+            a.v[p, 0, s, t - 41] = math.inf
+    out, lse = sv.attend(a.q, a.cache(sv), dev(a.prefix))
+    got = host(out)
+    assert not np.isfinite(got[..., :52]).any() and np.isfinite(got[..., 52:]).all()
+    assert np.isfinite(host(lse)).all()
