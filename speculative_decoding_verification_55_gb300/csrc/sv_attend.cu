@@ -57,6 +57,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2)
     sv_attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap) {
   constexpr int kStages = kStageCount<D>;
+  constexpr float kBits = sv::kProbBits<F16, false>;
   extern __shared__ unsigned char dyn[];
   __shared__ __align__(8) unsigned long long full[kStages], empty[kStages];
   __shared__ int bad_stage[kStages];
@@ -226,8 +227,8 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2)
         for (int y = 0; y < 2; ++y)
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            const float b = mx[x] == -INFINITY ? 0.0f : mx[x] * c;
-            const float p0 = sv::ex2(fmaf(sc[y][2 * x], c, -b)), p1 = sv::ex2(fmaf(sc[y][2 * x + 1], c, -b));
+            const float b = mx[x] == -INFINITY ? 0.0f : kBits - mx[x] * c;
+            const float p0 = sv::ex2(fmaf(sc[y][2 * x], c, b)), p1 = sv::ex2(fmaf(sc[y][2 * x + 1], c, b));
             l[x] += p0 + p1;
             pf[2 * y + x] = sv::pack2<F16>(p0, p1);
           }
@@ -344,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2)
     }
     if ((tid & 7) == 0 && r < rows) {
       if (!whole) P.part_ml[slot * kRows + r] = make_float2(jm, jl);
-      else if (P.lse) P.lse[at] = (jm * c + log2f(jl)) * 0.6931471805599453f;
+      else if (P.lse) P.lse[at] = (jm * c + (log2f(jl) - kBits)) * 0.6931471805599453f;
     }
     if (tid == 0 && W.first == 0) sv::tell_shared(P, 0, W.row, W.head, W.q_tile, rows, whole, W.item_at, W.w.tiles, plan);
     sv::named_bar_sync(1, kConsumers);         // the scratch is free for the next item's queries

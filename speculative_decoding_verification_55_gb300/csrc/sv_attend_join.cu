@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kThreads) sv_attend_join_kernel(const sv::Atte
 #pragma unroll
     for (int x = 0; x < kAcross; x += 2) reinterpret_cast<uint32_t*>(out)[x / 2] = sv::pack2<F16>(v[x], v[x + 1]);
   }
-  if (P.lse && col0 + first == 0) P.lse[at] = (M * c + log2f(L)) * 0.6931471805599453f;
+  if (P.lse && col0 + first == 0) P.lse[at] = (M * c + (log2f(L) - sv::kProbBits<F16, kRows == 128>)) * 0.6931471805599453f;
 }
 
 template <bool F16, int D, int kRows, int kAcross, int kCols>

@@ -12,9 +12,9 @@
 //   P = 2^(c S - c m) in the cache's type, written over S, with the row's sum in fp32;
 //   O += P V         P from tensor memory, V from shared memory.
 // Two threads share a row, 64 entries each, and meet once a tile for its maximum. A row's m is its running
-// maximum up to a slack of 2^8: the accumulator is only rescaled when the maximum has grown by more
-// (probabilities up to 2^8 are as exact in both types, and the sums are fp32). The parts of several
-// CTAs are joined as in sv_attend.cu.
+// maximum up to a slack of 2^8 (2^4 in fp16, sv_attend.cuh): the accumulator is only rescaled when the maximum has
+// grown by more, a published method (probabilities above 1 are as exact, and the sums are fp32). The parts of
+// several CTAs are joined as in sv_attend.cu.
 // Bound: the bytes of the cache. The 128 x 128 x D products of a tile take about a third of the time
 // that its 4 x 128 x D bytes take from HBM. With two groups of warps on a tile each (a row a thread, two
 // accumulators, S and P sharing one buffer a group) a tile's chain of S, softmax, P V and the next S took
@@ -38,7 +38,6 @@ constexpr int kSoftWarps = 8, kSoft = 32 * kSoftWarps;
 constexpr int kCopyWarps = 2;
 constexpr int kThreads = kSoft + 32 * (kCopyWarps + 2);   // and the copies', the products' and the items' warps
 constexpr int kCopies = kSoftWarps, kItems = kCopies + kCopyWarps, kProducts = kItems + 1;
-constexpr float kSlack = 8.0f;
 constexpr int kScores = 2;                             // buffers of scores in tensor memory
 constexpr int kPieces = 8;                             // items that the warps may be apart, and one
 
@@ -87,6 +86,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                           const __grid_constant__ CUtensorMap qmap, int q_tokens) {
   using H = Shape<D, kWays>;
   constexpr int kSlots = H::kSlots, kTile = H::kTile, kAccum = H::kAccum;
+  constexpr float kBits = sv::kProbBits<F16, true>;
   extern __shared__ __align__(1024) unsigned char dyn[];
   auto& S = *reinterpret_cast<Control<kSlots>*>(dyn + kSlots * H::kSlotBytes + H::kQueryBytes);
   const sv::Round& R = P.R;
@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             top = fmaxf(top, S.row_max[x & 1][half ^ 1][row]);
           }
           // The first tile sets the maximum; later ones move it when it has grown by over kSlack.
-          const bool grew = top > mx && (mx == -INFINITY || (top - mx) * c > kSlack);
+          const bool grew = top > mx && (mx == -INFINITY || (top - mx) * c > sv::kSlack<F16>);
           if (__any_sync(kFull, grew)) {
             const float f = !grew ? 1.0f : (mx == -INFINITY ? 0.0f : sv::ex2((mx - top) * c));
             if (grew) mx = top;
@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          const float b = mx == -INFINITY ? 0.0f : -mx * c;
+          const float b = mx == -INFINITY ? 0.0f : kBits - mx * c;
           const sv::f32x2 c2 = sv::pk(c, c), b2 = sv::pk(b, b);
           sv::f32x2 sum[2] = {sv::pk(0.0f, 0.0f), sv::pk(0.0f, 0.0f)};
 #pragma unroll
@@ -470,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (half == 0 && row < rows) {
         if (!whole) P.part_ml[slot * kRows + row] = make_float2(mx, jl);
-        else if (P.lse) P.lse[at] = (mx * c + log2f(jl)) * 0.6931471805599453f;
+        else if (P.lse) P.lse[at] = (mx * c + (log2f(jl) - kBits)) * 0.6931471805599453f;
       }
       fence_before();
       sv::named_bar_sync(1, kSoft);            // the sums have been read

@@ -1068,3 +1068,31 @@ def test_gpu_infinities_in_a_part_that_weighs_nothing(sv, N, G, rows):
     got = host(out)
     assert not np.isfinite(got[..., :52]).any() and np.isfinite(got[..., 52:]).all()
     assert np.isfinite(host(lse)).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("top", [14.0, 17.0, 18.5])
+@pytest.mark.parametrize("rows,n,N,G", [(1, 60000, 1, 2), (1, 60000, 9, 4), (1, 60000, 31, 8), (320, 3000, 1, 4),
+                                        (320, 3000, 4, 4), (160, 3000, 9, 4), (80, 3000, 31, 8)])
+def test_gpu_halves_of_small_probabilities(sv, rows, n, N, G, top):
+    """One entry far above equal ones, whose probabilities lie among a half's smallest numbers: they keep their
+    precision. A probability and the output are each rounded by half a step, e relative, and the sums are fp32 (1e-5).
+    Probabilities are kept times 2^11 or more, where a half's smallest step is 2^-24: half of it is 2^-36 of the
+    largest probability, for each entry; the output's own smallest step is 2^-24."""
+    a = Batch((n,) * rows, N, 1, G, 64, 128, "f16", seed=N, poison=False)
+    a.q[:] = 0.0
+    a.q[..., 0] = 1.0
+    a.k[:] = 0.0
+    a.v[:] = 1.0
+    for b in range(rows):
+        p, s = oracle.place(a.table, b, 77, 128)
+        a.k[p, :, s, 0] = top
+        a.v[p, :, s] = 0.0
+    out, lse = sv.attend(a.q, a.cache(sv), dev(a.prefix), scale=1.0)
+    e = 2.0 ** -11
+    for i in range(N):
+        rest = (n + i) * math.exp(-top)
+        want = rest / (1 + rest)
+        err = np.abs(host(out)[:, i] - want).max()
+        assert err <= want * (2 * e + 1e-5) * (1 + e) + (n + i) * 2.0 ** -36 + 2.0 ** -25, (err / want, i)
+        assert np.abs(host(lse)[:, i] - (top + math.log1p(rest))).max() <= 2.0 ** -22 * (top + 2)
