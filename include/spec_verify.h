@@ -353,6 +353,7 @@ int spec_verify_kv_append(const void* k_new, const void* v_new, int64_t row_stri
  * workspace      device scratch of spec_verify_paged_attention_workspace_size(...) bytes, 256-byte
  *                aligned. It needs no setup; one workspace serves one call at a time, of any sizes.
  * A row in error gets NaN in all its outputs (a bad page or tree: in those of its m_b tokens).
+ * The kernels' own waits are bounded: should one run out, the rows that its block had a part of get NaN.
  * The softmax and the sums run in fp32; the probabilities are rounded to the cache's dtype for the
  * product with the values. 1 <= N <= SV_MAX_GAMMA + 1, Hq <= 1024. */
 size_t spec_verify_paged_attention_workspace_size(int32_t N, int32_t Hq,

@@ -253,7 +253,8 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2)
         }
       }
       __syncwarp();
-      if (lane == 0) sv::mbar_arrive(sv::smem_addr(empty + s));
+      // A warp that gave up has not seen the tile's copies land: it gives no slot back, and the producer gives up too.
+      if (lane == 0 && !lost) sv::mbar_arrive(sv::smem_addr(empty + s));
     }
 
     // Values of the round's own entries that are not finite were left out of the products, where their
