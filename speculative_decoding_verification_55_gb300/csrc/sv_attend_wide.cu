@@ -72,7 +72,7 @@ struct Control {
   sv::Plan plan;
   Item items[kPieces];
   float row_max[2][2][kRows];                          // by the tile's parity and half
-  int bad[kCopyWarps][kPieces], flags, lost;
+  int bad[kCopyWarps][kPieces], armed[kCopyWarps], flags, lost;
   uint32_t tm;
 };
 template <int D, int kWays>
@@ -118,10 +118,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tm = S.tm;
   volatile int* const lost = &S.lost;
 
-  // The next item's description: the items' warp always tells an end.
+  // The next item's description. The items' warp always tells an end, however its own waits end: this wait is longer than
+  // they can be, so that all warps know of the same items and meet at the same barriers.
   auto told = [&](int k) {
     Item I;
-    if (sv::mbar_wait(sv::smem_addr(S.told + k % kPieces), (k / kPieces) & 1)) I = S.items[k % kPieces];
+    if (sv::mbar_wait_drain(sv::smem_addr(S.told + k % kPieces), (k / kPieces) & 1)) I = S.items[k % kPieces];
     else {
       I.count = 0;
       *lost = 1;
@@ -194,7 +195,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (armed > 0) sv::mbar_wait_drain(sv::smem_addr(&S.q_full), (armed - 1) & 1);
     } else {
       sv::fill_unused(P, D, op, 32 * kCopyWarps);   // while the last tiles are computed
-      for (int e = max(0, armed - kSlots); e < armed; ++e)
+      // A slot is full when both warps have armed it. One whose wait gave up may be behind the other (by at most the
+      // ring: the other's slots were given back full): it arrives for the slots that it has not armed.
+      if (lane == 0) S.armed[mine] = armed;
+      __syncwarp();
+      sv::named_bar_sync(6, 32 * kCopyWarps);
+      const int most = max(S.armed[0], S.armed[1]);
+      if (lane == 0)
+        for (int e = armed; e < most; ++e) sv::mbar_arrive(sv::smem_addr(S.full + e % kSlots));
+      for (int e = max(0, most - kSlots); e < most; ++e)
         sv::mbar_wait_drain(sv::smem_addr(S.full + e % kSlots), (e / kSlots) & 1);
     }
   } else if (warp == kProducts) {
@@ -265,10 +274,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         products_done(sv::smem_addr(&S.o_full));
         ++items;
       }
-      if (*lost) {              // products in flight end before the tensor memory is given back
-        products_done(sv::smem_addr(&S.drained));
-        sv::mbar_wait_drain(sv::smem_addr(&S.drained), 0);
-      }
+      // Products in flight end before the tensor memory is given back, whoever else has given up.
+      products_done(sv::smem_addr(&S.drained));
+      sv::mbar_wait_drain(sv::smem_addr(&S.drained), 0);
     }
     __syncwarp();
   } else {

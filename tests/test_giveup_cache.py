@@ -63,6 +63,8 @@ def bounded(f):
 LONG = (9000, 30, 4000, 0, 777)
 ATTEND = [                                     # prefix lengths, N, key heads, group, D
     (LONG, 1, 2, 4, 128), ((3000,) * 200, 1, 2, 4, 64), ((20,) * 900, 1, 2, 1, 64), (LONG, 4, 2, 4, 256),
+    (LONG, 9, 2, 4, 128), ((3000,) * 100, 9, 2, 4, 64), ((20,) * 900, 17, 1, 1, 128), (LONG, 9, 1, 8, 256),
+    (LONG, 31, 2, 8, 128), ((1600,) * 152, 31, 1, 8, 64), ((1600,) * 152, 31, 1, 8, 128),   # the latter: two query tiles
 ]
 
 
