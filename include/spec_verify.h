@@ -376,7 +376,8 @@ int spec_verify_paged_attention(const void* q, int64_t q_row_stride, int64_t q_t
  * A row whose length or count is out of range, or with a path entry outside [0, N), adds nothing;
  * entries on a page number out of range are passed over. Weights of entries that rows share take every
  * row's part, in any order (the only case in which two equal calls may round differently). One launch.
- * cache->weight is required. */
+ * cache->weight is required. Should one of the kernel's own bounded waits run out, the weights of the entries that
+ * its block had become NaN. */
 int spec_verify_kv_weights(const void* q, int64_t q_row_stride, int64_t q_token_stride,
                            const float* lse, const sv_paged_cache* cache, const int32_t* prefix_len,
                            const int32_t* num_kept, const int32_t* path, float scale, int32_t B,

@@ -103,10 +103,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tm = S.tm;
   volatile int* const lost = &S.lost;
   const int chunk_rows = P.tokens * R.group;
+  // The next item's description. The items' warp always tells an end, however its own waits end: this wait is longer than
+  // they can be, so that all warps know of the same items and meet at the same barriers.
   auto told = [&](int k) {
     Item I;
-    if (sv::mbar_wait(sv::smem_addr(S.told + k % kPieces), (k / kPieces) & 1)) I = S.items[k % kPieces];
-    else I.count = 0;
+    if (sv::mbar_wait_drain(sv::smem_addr(S.told + k % kPieces), (k / kPieces) & 1)) I = S.items[k % kPieces];
+    else {
+      I.count = 0;
+      *lost = 1;
+    }
     return I;
   };
   // Chunks of an item; its queries are copied once when there is room for all, else for every tile.
@@ -198,18 +203,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (stay) q += chunks;
       }
-      if (*lost) {              // products in flight end before the tensor memory is given back
-        products_done(sv::smem_addr(&S.drained));
-        sv::mbar_wait_drain(sv::smem_addr(&S.drained), 0);
-      }
+      // Products in flight end before the tensor memory is given back, whoever else has given up.
+      products_done(sv::smem_addr(&S.drained));
+      sv::mbar_wait_drain(sv::smem_addr(&S.drained), 0);
     }
     __syncwarp();
   } else if (warp == kItems) {
     sv::Walk W;
     W.begin(R, S.plan);
     int q = 0;
+    bool gone = false;
     for (int k = 0;; ++k) {
-      const bool more = !__any_sync(kFull, *lost != 0) && W.next(R);
+      gone = __any_sync(kFull, gone || *lost != 0);
+      const bool more = !gone && W.next(R);
       bool bad = false;
       if (more && P.path)
         for (int d = lane; d < W.w.m; d += 32) {
@@ -227,8 +233,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int x = 0; x < (chunks > kQ ? chunks * I.count : chunks); ++x, ++q) {
         const int qi = q % kQ;
         if (q >= kQ &&
-            !__all_sync(kFull, wait_unless_lost(sv::smem_addr(S.q_empty + qi), (q / kQ - 1) & 1, lost)))
+            !__all_sync(kFull, wait_unless_lost(sv::smem_addr(S.q_empty + qi), (q / kQ - 1) & 1, lost))) {
+          gone = true;                         // the next turn tells the end
           break;
+        }
         const int d0 = (x % chunks) * P.tokens;
         const uint32_t bar = sv::smem_addr(S.q_full + qi), to = qring + qi * (kRows * D * 2);
         // A chunk's tokens, q_tokens of them in a box; along a path, one by one.
@@ -318,12 +326,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) sv::mbar_arrive(sv::smem_addr(S.s_empty + b));
         }
-        if (mine) atomicAdd(C.weight + sv::weight_index(C, page, I.head, j), ok ? w : __int_as_float(0x7fffffff));
+        if (mine) atomicAdd(C.weight + sv::weight_index(C, page, I.head, j), w);
       }
     }
     fence_before();
   }
   __syncthreads();
+  if (S.lost) {                                // a wait gave up: NaN for the whole run, whatever was added
+    sv::Walk W;
+    W.begin(R, S.plan);
+    while (W.next(R)) {
+      bool bad = false;                        // a row in error has no additions
+      for (int d = 0; P.path && d < W.w.m; ++d) {
+        const int i = __ldg(P.path + static_cast<size_t>(W.row) * R.N + d);
+        bad |= i < 0 || i >= R.N;
+      }
+      const int stop = min((W.first + W.count) * kTile, W.w.n + W.w.m);
+      for (int j = W.first * kTile + tid; j < stop && !bad; j += kThreads) {
+        const int page = sv::cache_page(C, W.row, j);
+        if (sv::page_ok(C, page))
+          atomicAdd(C.weight + sv::weight_index(C, page, W.head, j), __int_as_float(0x7fffffff));
+      }
+    }
+  }
   if (warp == kProducts) tm_free(tm);
 }
 

@@ -87,3 +87,39 @@ def test_attention_gives_up(sv, hasty, prefix, N, H, G, D):
         assert limit > 0 or lost.any()         # with no polls at all, some wait did run out
     got, got_lse = sv.attend(q, cache, n)      # the context and the workspace of the next call are usable
     assert torch.equal(got, want) and torch.equal(got_lse, want_lse)
+
+
+WEIGH = [                                      # prefix lengths, N, key heads, group, D, along a path
+    (LONG, 1, 2, 4, 128, False), ((3000,) * 100, 9, 2, 4, 64, False), ((20,) * 900, 17, 1, 1, 128, True),
+    (LONG, 9, 1, 8, 256, True), (LONG, 31, 2, 8, 128, False), ((900,) * 40, 40, 1, 16, 128, False),
+    ((900,) * 40, 33, 1, 8, 256, True),
+]
+
+
+@pytest.mark.parametrize("prefix,N,H,G,D,along", WEIGH)
+def test_weights_give_up(sv, hasty, prefix, N, H, G, D, along):
+    L, limit = hasty
+    q, cache, n = batch(sv, prefix, N, H, G, D, N)
+    B, Hq = len(prefix), H * G
+    path = torch.stack([torch.randperm(N) for _ in prefix]).sort(1)[0].to(torch.int32).cuda() if along else None
+    num = torch.arange(B, dtype=torch.int32, device="cuda") % (N + 1)
+    lse = torch.full((B, N, Hq), 5.0, device="cuda")
+    before = cache.weight.clone()
+    sv.spec_verify_kv_weights(q, lse, cache, n, num, path)
+    want = cache.weight.clone()
+    added = torch.zeros_like(want, dtype=torch.bool)       # entries that the call adds to
+    for b, (k, m) in enumerate(zip(prefix, num.tolist())):
+        for j in range(0, k + m if m else 0, 16):
+            added[int(cache.page_table[b, j // 16]), :, :min(16, k + m - j)] = True
+    for _ in range(5):
+        cache.weight.copy_(before)
+        bounded(lambda: L.spec_verify_kv_weights(
+            q.data_ptr(), q.stride(0), q.stride(1), lse.data_ptr(), cache.ref, n.data_ptr(), num.data_ptr(),
+            None if path is None else path.data_ptr(), 1 / math.sqrt(D), B, N, Hq,
+            torch.cuda.current_stream().cuda_stream))
+        lost = cache.weight.isnan()
+        assert torch.equal(cache.weight[~lost], want[~lost]) and not (lost & ~added).any()
+        assert limit > 0 or lost.any()
+    cache.weight.copy_(before)
+    sv.spec_verify_kv_weights(q, lse, cache, n, num, path)
+    assert torch.equal(cache.weight, want)
