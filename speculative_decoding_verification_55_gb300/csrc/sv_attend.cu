@@ -22,8 +22,8 @@
 // Rounding: probabilities go to the cache's type for the product with the values (half a step of 2^-8
 // or 2^-11 relative, as the output's own rounding); maxima, sums, scores and accumulators are fp32.
 
+#include <algorithm>
 #include <cmath>
-#include <type_traits>
 
 #include "sv_attend.cuh"
 
@@ -358,6 +358,10 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2)
 // once (heads of 256 have no room for two accumulators). That pays when the second reading would come from
 // HBM, or when there are items for every SM that are long against their start and end; with fewer and
 // shorter ones, of which many CTAs then take a part, two tiles' parts cost more than the second reading from L2.
+// Lengths are on the device: the rule takes what the tables have room for, and no more than there are pages, for the
+// rows' entries (24 rows of 500 to 6000 in tables for 131,072 take 56 us so, 66 by the tables alone). Two tiles are still
+// taken too often where the pages have room for much more than the rows, or a batch with an item for every SM has tables
+// far wider than its rows: 76 rows of 1000 entries in tables for 131,072 81 us against 67.
 // Measured with 4 key heads and trees of 31 nodes, 8 query heads a key head, one tile at a time against two: 38
 // rows of 2000 entries 72 against 59 us, of 32,000 619 against 475; 76 rows of 1000 76 against 84; 8 rows of
 // 64,000 266 against 223, of 16,000 78 against 90, of 4000 37 against 49; 24 rows of 12,000 135 against 153, of
@@ -367,13 +371,15 @@ struct Kernel {
   int tile_rows, part_rows, ways, key_log2, ctas;     // CTAs: of an SM
 };
 constexpr long long kBeyondL2 = 768ll << 20;           // bytes of keys and values, about six times L2
-constexpr long long kLongRow = 12 << 7;                // entries
+constexpr long long kLongRow = 12 << 7;                // entries of a row
 Kernel kernel_for(int N, int group, const sv_paged_cache* c, long long B, int sms) {
   const int D = c->head_dim;
   if (N * group <= 16) return {false, 16, 16, 1, kTileLog2, D == 256 ? 1 : 2};
   const int rows = 128 / group * group;
   const long long pairs = B * c->heads * ((N * group + 2 * rows - 1) / (2 * rows));
-  const long long entries = static_cast<long long>(c->max_pages) * c->page_size, bytes = B * c->heads * entries * D * 4;
+  const long long pages = B * c->max_pages < c->num_pages ? B * c->max_pages : c->num_pages;
+  const long long entries = std::min<long long>(c->max_pages, c->num_pages) * c->page_size;
+  const long long bytes = pages * c->page_size * c->heads * D * 4;
   const bool two = N * group > rows && D < 256 && ((pairs >= sms && entries >= kLongRow) || bytes >= kBeyondL2);
   return {true, rows, 128, two ? 2 : 1, D == 256 ? 6 : 7, 1};
 }

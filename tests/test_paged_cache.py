@@ -1096,3 +1096,37 @@ def test_gpu_halves_of_small_probabilities(sv, rows, n, N, G, top):
         err = np.abs(host(out)[:, i] - want).max()
         assert err <= want * (2 * e + 1e-5) * (1 + e) + (n + i) * 2.0 ** -36 + 2.0 ** -25, (err / want, i)
         assert np.abs(host(lse)[:, i] - (top + math.log1p(rest))).max() <= 2.0 ** -22 * (top + 2)
+
+
+@pytest.mark.gpu
+def test_gpu_tables_wider_than_their_rows(sv):
+    """A batch in a table with room for rows far longer than all its pages hold is worked on as in one that fits."""
+    a = Batch((500, 900, 130, 1000, 77, 640, 300, 800), 31, 4, 8, 128, 16, seed=1, poison=False)
+    fits = sv.attend(a.q, a.cache(sv), dev(a.prefix))
+    check_attention(a, *fits, a.prefix, np.full(8, 31), None)
+    table = np.full((8, 4096), 1 << 30, np.int32)
+    table[:, :a.table.shape[1]] = a.table
+    a.table = table
+    wide = sv.attend(a.q, a.cache(sv), dev(a.prefix))
+    assert torch.equal(wide[0], fits[0]) and torch.equal(wide[1], fits[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N,G,D", [(31, 8, 128), (65, 7, 64), (9, 16, 128)])
+def test_gpu_attention_large_trees_in_a_large_pool(sv, N, G, D):
+    """A few rows in tables and among pages with room for more keys and values than L2 holds: two query tiles at once,
+    in parts."""
+    a = Batch((3000, 129, 0), N, 1, G, D, 16, seed=N)
+    pages = (800 << 20) // (16 * D * 4)
+    at = pages - len(a.k)
+    big = [torch.zeros((pages, 1, 16, D), dtype=a.t, device="cuda") for _ in range(2)]
+    for x, y in zip(big, (a.k, a.v)):
+        x[at:] = y
+    table = np.full((3, 65536), 1 << 30, np.int64)
+    table[:, :a.table.shape[1]] = np.where(a.table < pages, a.table.astype(np.int64) + at, 1 << 30)
+    c = sv.PagedCache(*big, dev(table))
+    tree = random_tree(np.random.default_rng(N), 3, N)
+    num = np.array([N, N - 3, N], np.int32)
+    for parents in (None, tree):
+        out, lse = sv.attend(a.q, c, dev(a.prefix), dev(num), dev(parents))
+        check_attention(a, out, lse, a.prefix, num, parents)
