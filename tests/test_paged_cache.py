@@ -1130,3 +1130,55 @@ def test_gpu_attention_large_trees_in_a_large_pool(sv, N, G, D):
     for parents in (None, tree):
         out, lse = sv.attend(a.q, c, dev(a.prefix), dev(num), dev(parents))
         check_attention(a, out, lse, a.prefix, num, parents)
+
+
+WIDE_HEADS = [
+    # prefix lengths, N, Hkv, group, D, page, dtype, nhd: more than 128 query rows a key head of 256
+    ((40, 257, 0, 1000), 33, 2, 8, 256, 16, "bf16", False),
+    ((63, 64, 700), 65, 1, 3, 256, 64, "f16", True),
+    ((300, 5), 9, 1, 128, 256, 32, "f16", False),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("prefix,N,H,G,D,S,dtype,nhd", WIDE_HEADS)
+def test_gpu_heads_of_256_in_several_query_tiles(sv, prefix, N, H, G, D, S, dtype, nhd):
+    test_gpu_attention(sv, prefix, N, H, G, D, S, dtype, nhd)
+    test_gpu_weights(sv, prefix, N, H, G, D, S, dtype, nhd)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lengths,H,D,S,budget,recent", [
+    (tuple(range(16500, 20000, 90)), 8, 64, 128, 9001, 200),      # a block a row and head: keys not held
+    ((140000, 500, 131073), 2, 64, 16, 70001, 77),                # clusters whose runs' keys are not held
+    ((300000, 262145, 70), 1, 64, 16, 200003, 0),                 # nor page numbers
+    ((1 << 20,), 1, 64, 16, 999999, 1000), ((1 << 20,), 1, 128, 16, 12345, 0),   # the longest rows
+    (tuple(range(66000, 69900, 300)), 8, 64, 16, 66100, 30),      # page numbers not held, two blocks an SM
+])
+def test_gpu_evict_of_rows_that_shared_memory_does_not_hold(sv, lengths, H, D, S, budget, recent):
+    """Rows whose order keys or page numbers are read again from memory; equal weights across runs."""
+    g = torch.Generator(device="cuda").manual_seed(budget)
+    used = [-(-n // S) for n in lengths]
+    ids = torch.randperm(sum(used) + 1, generator=g, device="cuda").to(torch.int32)
+    table = torch.full((len(lengths), max(used)), 1 << 30, dtype=torch.int32, device="cuda")
+    at = 0
+    for b, u in enumerate(used):
+        table[b, :u] = ids[at:at + u]
+        at += u
+    shape = (len(ids), H, S, D)
+    k, v = (torch.randn(shape, generator=g, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    w = torch.rand(shape[:3], generator=g, device="cuda").mul_(500).floor_()
+    old = [x.clone() for x in (k, v, w)]
+    olen = dev([0] * len(lengths))
+    sv.spec_verify_kv_evict(sv.PagedCache(k, v, table, w), dev(lengths), budget, recent, olen)
+    assert olen.tolist() == [min(n, budget) for n in lengths]
+    for b, n in enumerate(lengths):
+        row = lambda x: x[table[b, :used[b]].long()].transpose(0, 1).flatten(1, 2)[:, :n]   # noqa: E731
+        for h in range(H):
+            keep = torch.ones(n, dtype=torch.bool, device="cuda")
+            if n > budget:
+                order = torch.sort(row(old[2])[h, :n - recent], descending=True, stable=True)[1]
+                keep[order[budget - recent:]] = False
+            for x, o in zip((k, v, w), old):
+                assert torch.equal(row(x)[h, :budget], row(o)[h][keep])
+                assert torch.equal(row(x)[h, budget:], row(o)[h, budget:])
