@@ -274,9 +274,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         products_done(sv::smem_addr(&S.o_full));
         ++items;
       }
-      // Products in flight end before the tensor memory is given back, whoever else has given up.
-      products_done(sv::smem_addr(&S.drained));
-      sv::mbar_wait_drain(sv::smem_addr(&S.drained), 0);
     }
     __syncwarp();
   } else {
@@ -488,6 +485,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_before();
   }
   __syncthreads();
+  if (warp == kProducts) {
+    if (S.lost && lane == 0) {                 // products in flight end before the tensor memory is given back
+      products_done(sv::smem_addr(&S.drained));
+      sv::mbar_wait_drain(sv::smem_addr(&S.drained), 0);
+    }
+    __syncwarp();
+    tm_free(tm);
+  }
   if (S.lost) {                                // a wait gave up: NaN for the whole run
     sv::Walk W;
     W.begin(R, S.plan);
@@ -508,7 +513,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           sv::tell_shared(P, way, W.row, W.head, q_tile, rows, whole, W.item_at, W.w.tiles, S.plan);
       }
   }
-  if (warp == kProducts) tm_free(tm);
 }
 
 template <bool F16, int D, int kWays>

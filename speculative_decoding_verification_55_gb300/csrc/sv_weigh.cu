@@ -203,19 +203,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (stay) q += chunks;
       }
-      // Products in flight end before the tensor memory is given back, whoever else has given up.
-      products_done(sv::smem_addr(&S.drained));
-      sv::mbar_wait_drain(sv::smem_addr(&S.drained), 0);
     }
     __syncwarp();
   } else if (warp == kItems) {
     sv::Walk W;
     W.begin(R, S.plan);
     int q = 0;
-    bool gone = false;
     for (int k = 0;; ++k) {
-      gone = __any_sync(kFull, gone || *lost != 0);
-      const bool more = !gone && W.next(R);
+      const bool more = !__any_sync(kFull, *lost != 0) && W.next(R);
       bool bad = false;
       if (more && P.path)
         for (int d = lane; d < W.w.m; d += 32) {
@@ -233,10 +228,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int x = 0; x < (chunks > kQ ? chunks * I.count : chunks); ++x, ++q) {
         const int qi = q % kQ;
         if (q >= kQ &&
-            !__all_sync(kFull, wait_unless_lost(sv::smem_addr(S.q_empty + qi), (q / kQ - 1) & 1, lost))) {
-          gone = true;                         // the next turn tells the end
-          break;
-        }
+            !__all_sync(kFull, wait_unless_lost(sv::smem_addr(S.q_empty + qi), (q / kQ - 1) & 1, lost)))
+          break;                               // the next turn tells the end
         const int d0 = (x % chunks) * P.tokens;
         const uint32_t bar = sv::smem_addr(S.q_full + qi), to = qring + qi * (kRows * D * 2);
         // A chunk's tokens, q_tokens of them in a box; along a path, one by one.
@@ -332,6 +325,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_before();
   }
   __syncthreads();
+  if (warp == kProducts) {
+    if (S.lost && lane == 0) {                 // products in flight end before the tensor memory is given back
+      products_done(sv::smem_addr(&S.drained));
+      sv::mbar_wait_drain(sv::smem_addr(&S.drained), 0);
+    }
+    __syncwarp();
+    tm_free(tm);
+  }
   if (S.lost) {                                // a wait gave up: NaN for the whole run, whatever was added
     sv::Walk W;
     W.begin(R, S.plan);
@@ -349,7 +350,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   }
-  if (warp == kProducts) tm_free(tm);
 }
 
 template <bool F16, int D>
