@@ -28,12 +28,12 @@ struct AttendParams {
 
 // Probabilities are kept times a power of two: relative to a row's running maximum they go down to 2^-25 and less in
 // long rows, and a half's steps below 2^-14 are all 2^-24. The largest are 2^15 (a half ends at 65,504): the 16-row
-// kernel's maximum is the true one, the wide kernel's may lag by kSlack. Accumulators and sums have the factor too; it
-// leaves with their quotient and is taken out of the lse. bf16 has fp32's exponents and needs none.
-template <bool F16>
-constexpr float kSlack = F16 ? 4.0f : 8.0f;
+// kernel's maximum is the true one, the wide kernel's may lag by kSlack, which leaves it 2^7, half a step of 2^-32 of the
+// maximum. (A slack of 2^4 and a factor of 2^11 cost a long row 1.2 of 39 us.) Accumulators and sums have the factor too;
+// it leaves with their quotient and is taken out of the lse. bf16 has fp32's exponents and needs none.
+constexpr float kSlack = 8.0f;
 template <bool F16, bool kWide>
-constexpr float kProbBits = F16 ? (kWide ? 15.0f - kSlack<F16> : 15.0f) : 0.0f;
+constexpr float kProbBits = F16 ? (kWide ? 15.0f - kSlack : 15.0f) : 0.0f;
 
 template <bool F16>
 __device__ __forceinline__ float value_of(uint32_t h) {

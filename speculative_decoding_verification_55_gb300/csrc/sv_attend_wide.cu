@@ -4,17 +4,19 @@
 //
 // One CTA per SM: two warps copying tiles of 128 entries from the pages, a warp whose one thread
 // issues the matrix products, a warp that copies an item's queries and tells the others what the item is,
-// and eight softmax warps. An item is up to 128 query rows of a key head. (A warp takes 48 ns to issue a box: one
-// alone took 1.55 us for a tile from pages of 16, in boxes of 2 KB, longer than the tile takes from HBM.)
-// Tensor memory holds the scores S [128 rows, 128 entries] of two tiles and the accumulator
-// O [128 rows, D]: 2 x 128 + D of 512 columns.
+// and eight softmax warps. An item is up to 128 query rows of a key head, or two such query tiles at once. (A warp
+// takes 48 ns to issue a box: one alone took 1.55 us for a tile from pages of 16, in boxes of 2 KB, longer than the
+// tile takes from HBM.)
+// Tensor memory holds the scores S [128 rows, 128 entries] of two tiles, or of one for each of two query tiles, and
+// an accumulator O [128 rows, D] a query tile: 2 x 128 + D or 2 x 128 + 2 D of 512 columns (key tiles of heads of 256
+// have 64 entries: 2 x 64 + 256).
 //   S = Q K^T        Q and K from shared memory, up to two tiles ahead;
 //   P = 2^(c S - c m) in the cache's type, written over S, with the row's sum in fp32;
 //   O += P V         P from tensor memory, V from shared memory.
-// Two threads share a row, 64 entries each, and meet once a tile for its maximum. A row's m is its running
-// maximum up to a slack of 2^8 (2^4 in fp16, sv_attend.cuh): the accumulator is only rescaled when the maximum has
-// grown by more, a published method (probabilities above 1 are as exact, and the sums are fp32). The parts of
-// several CTAs are joined as in sv_attend.cu.
+// Two threads share a row, 64 entries each, and meet once a tile for its maximum (two query tiles: a thread has a
+// row). A row's m is its running maximum up to a slack of 2^8: the accumulator is only rescaled when the maximum has
+// grown by more, a published method (probabilities above 1 are as exact, and the sums are fp32). The parts of several
+// CTAs are joined as in sv_attend.cu.
 // Bound: the bytes of the cache. The 128 x 128 x D products of a tile take about a third of the time
 // that its 4 x 128 x D bytes take from HBM. With two groups of warps on a tile each (a row a thread, two
 // accumulators, S and P sharing one buffer a group) a tile's chain of S, softmax, P V and the next S took
@@ -344,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             top = fmaxf(top, S.row_max[x & 1][half ^ 1][row]);
           }
           // The first tile sets the maximum; later ones move it when it has grown by over kSlack.
-          const bool grew = top > mx && (mx == -INFINITY || (top - mx) * c > sv::kSlack<F16>);
+          const bool grew = top > mx && (mx == -INFINITY || (top - mx) * c > sv::kSlack);
           if (__any_sync(kFull, grew)) {
             const float f = !grew ? 1.0f : (mx == -INFINITY ? 0.0f : sv::ex2((mx - top) * c));
             if (grew) mx = top;
