@@ -15,8 +15,8 @@
 
 namespace sv {
 
-// Entries a row of the cache may hold: the eviction keeps one bit and one count per 32 of them in
-// shared memory.
+// Entries a row of the cache may hold: the eviction keeps a bit for each and a count for each 128 of them in shared
+// memory.
 constexpr int kMaxEntries = 1 << 20;
 
 struct Cache {

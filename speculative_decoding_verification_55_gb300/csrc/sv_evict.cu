@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sv_evict_kernel(con
   // Every CTA of the cluster has read the weights, and the others' bits, before any moves or leaves.
   meet(P.S);
 
-  // 3. The moves, from the first dropped entry on.
+  // 2. The moves, from the first dropped entry on.
   const int cols_log2 = (C.head_dim == 64 ? 4 : (C.head_dim == 128 ? 5 : 6)) - (31 - __clz(P.S));
   const int cols = 1 << cols_log2, vecs = C.head_dim / 8;
   const int per = kThreads >> cols_log2, batch = min(per * kInFlight, kMaxBatch);
@@ -440,6 +440,9 @@ extern "C" int spec_verify_kv_evict(const sv_paged_cache* cache, const int32_t* 
   // alone (16 rows of 5000 to 16,000 weights 33 us against 46, 8 of 130,000 255 against 326), but 64 rows and heads
   // of 9000 entries moved by 64 CTAs took 95 us, by 256 of half the size 67. A third of the SMs is left out: 16
   // clusters of 8 CTAs of 1024 threads did not run at once.
+  // Lengths are on the device: what shared memory has to hold goes by the tables' room, and a table far wider than its
+  // rows leaves less for keys and page numbers. 32 rows of 2000 to 8190 entries cut to 2048 take 111 us in tables that fit,
+  // 137 in tables for 32,768 or 131,072 entries and 209 for 1,048,576; one row of 130,000 264 and, for 1,048,576, 450.
   const long long cap = static_cast<long long>(P.C.max_pages) * P.C.page_size;
   const int sms = sv::device_sms(dev);
   auto cluster = [&](long long most_ctas) {
