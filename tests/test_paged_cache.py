@@ -1182,3 +1182,45 @@ def test_gpu_evict_of_rows_that_shared_memory_does_not_hold(sv, lengths, H, D, S
             for x, o in zip((k, v, w), old):
                 assert torch.equal(row(x)[h, :budget], row(o)[h][keep])
                 assert torch.equal(row(x)[h, budget:], row(o)[h, budget:])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N,G,S", [(1, 4, 16), (9, 4, 128)])
+def test_gpu_the_longest_row(sv, N, G, S):
+    """A row of 1,048,576 entries, the most that there may be, beside a short one: attention and weights against 64 bits.
+    Half a step of the probabilities and of the output, and 1e-5 for scores, exponentials and sums."""
+    n, D = (1 << 20) - N, 64
+    g = torch.Generator(device="cuda").manual_seed(N)
+    pages = (1 << 20) // S
+    k, v = (torch.randn((pages + 1, 1, S, D), generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    q = torch.randn((2, N, G, D), generator=g, device="cuda").to(torch.bfloat16)
+    table = torch.randperm(pages, generator=g, device="cuda").to(torch.int32).repeat(2, 1)
+    table[1, 0] = pages
+    w = torch.zeros((pages + 1, 1, S), device="cuda")
+    c = sv.PagedCache(k, v, table, w)
+    prefix = dev([n, 3])
+    out, lse = sv.attend(q, c, prefix)
+    sv.spec_verify_kv_weights(q, lse, c, prefix)
+    K, V = (x[table[0].long(), 0].reshape(-1, D).double() for x in (k, v))
+    s = (q[0].double().reshape(N * G, D) @ K.T / 8).reshape(N, G, -1)
+    s.masked_fill_(torch.arange(1 << 20, device="cuda") > n + torch.arange(N, device="cuda")[:, None, None], -math.inf)
+    want_lse = torch.logsumexp(s, -1)
+    p = torch.exp(s - want_lse[..., None])
+    want, mag = p @ V, p @ V.abs()
+    e = 2.0 ** -8
+    assert ((out[0].double() - want).abs() <= e * want.abs() + (e + 1e-5) * mag).all()
+    assert (lse[0].double() - want_lse).abs().max() <= 1e-5
+    got = w[table[0].long(), 0].reshape(-1).double()
+    assert ((got - p.sum((0, 1))).abs() <= 1e-4 * p.sum((0, 1))).all()
+    assert abs(float(w.double().sum()) - 2 * N * G) <= 1e-4 * N * G and torch.isfinite(out[1]).all()
+
+
+@pytest.mark.gpu
+def test_gpu_weights_along_a_path_that_names_a_token_twice(sv):
+    a = Batch((40, 7, 130), 5, 2, 4, 64, 16, seed=2)
+    path = np.array([[0, 0, 3, 3, 3], [4, 4, 4, 4, 4], [1, 0, 1, 0, 2]], np.int32)
+    lse = torch.full((3, 5, 8), 2.0, device="cuda")
+    before = host(a.weight)
+    sv.spec_verify_kv_weights(a.q, lse, a.cache(sv), dev(a.prefix), None, dev(path))
+    want = oracle.weights(host(a.q), host(lse), host(a.k), before, a.table, a.prefix, [5] * 3, path, a.scale)
+    assert np.allclose(host(a.weight), want, rtol=1e-5, atol=0)
