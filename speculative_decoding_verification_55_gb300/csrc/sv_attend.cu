@@ -227,8 +227,8 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2)
         for (int y = 0; y < 2; ++y)
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            const float b = mx[x] == -INFINITY ? 0.0f : kBits - mx[x] * c;
-            const float p0 = sv::ex2(fmaf(sc[y][2 * x], c, b)), p1 = sv::ex2(fmaf(sc[y][2 * x + 1], c, b));
+            const float m0 = mx[x] == -INFINITY ? 0.0f : mx[x], b = F16 ? kBits : -m0 * c, sub = F16 ? m0 : 0.0f;
+            const float p0 = sv::ex2(fmaf(sc[y][2 * x] - sub, c, b)), p1 = sv::ex2(fmaf(sc[y][2 * x + 1] - sub, c, b));
             l[x] += p0 + p1;
             pf[2 * y + x] = sv::pack2<F16>(p0, p1);
           }

@@ -366,8 +366,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          const float b = mx == -INFINITY ? 0.0f : kBits - mx * c;
-          const sv::f32x2 c2 = sv::pk(c, c), b2 = sv::pk(b, b);
+          const float m0 = mx == -INFINITY ? 0.0f : mx, b = F16 ? kBits : -m0 * c;
+          const sv::f32x2 m2 = sv::pk(m0, m0), c2 = sv::pk(c, c), b2 = sv::pk(b, b);
           sv::f32x2 sum[2] = {sv::pk(0.0f, 0.0f), sv::pk(0.0f, 0.0f)};
 #pragma unroll
           for (int y = 0; y < H::kCols; y += H::kChunk) {
@@ -376,7 +376,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int z = 0; z < H::kChunk / 2; ++z) {
               float p0, p1;
-              sv::upk(sv::fma2(sv::pk(__uint_as_float(sc[2 * z]), __uint_as_float(sc[2 * z + 1])), c2, b2), p0, p1);
+              sv::f32x2 s2 = sv::pk(__uint_as_float(sc[2 * z]), __uint_as_float(sc[2 * z + 1]));
+              if (F16) s2 = sv::sub2(s2, m2);
+              sv::upk(sv::fma2(s2, c2, b2), p0, p1);
               p0 = sv::ex2(p0);
               p1 = sv::ex2(p1);
               sum[z & 1] = sv::add2(sum[z & 1], sv::pk(p0, p1));

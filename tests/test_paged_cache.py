@@ -1224,3 +1224,26 @@ def test_gpu_weights_along_a_path_that_names_a_token_twice(sv):
     sv.spec_verify_kv_weights(a.q, lse, a.cache(sv), dev(a.prefix), None, dev(path))
     want = oracle.weights(host(a.q), host(lse), host(a.k), before, a.table, a.prefix, [5] * 3, path, a.scale)
     assert np.allclose(host(a.weight), want, rtol=1e-5, atol=0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N,G", [(1, 4), (9, 4), (31, 8)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_gpu_scores_of_tens_of_millions(sv, N, G, dtype):
+    """One entry whose score is far beyond all others and beyond what fp32 has fractions for: its value, its score. Its
+    probability and the output are each rounded by half a step; the lse by two roundings, a product and a logarithm."""
+    B, D = 12, 128
+    a = Batch((200,) * B, N, 1, G, D, 16, dtype, seed=N, poison=False)
+    a.q[:] = 1500.0
+    a.k[:] = 0.0
+    a.scale = 0.09
+    for b in range(B):
+        p, s = oracle.place(a.table, b, 17 * b, 16)
+        a.k[p, :, s] = 1000.0 + 117.0 * b                  # exact in fp32: the sum of 128 products, up to 4.4e8
+    out, lse = sv.attend(a.q, a.cache(sv), dev(a.prefix), scale=a.scale)
+    for b in range(B):
+        p, s = oracle.place(a.table, b, 17 * b, 16)
+        v, e = host(a.v[p, 0, s]), torch.finfo(a.t).eps / 2
+        assert (np.abs(host(out)[b] - v) <= 2 * e * (1 + e) * np.abs(v) + 1e-6).all(), b
+        want = 0.09 * 128 * float(a.q[0, 0, 0, 0]) * float(a.k[p, 0, s, 0])
+        assert np.abs(host(lse)[b] / want - 1).max() <= 2.0 ** -22
