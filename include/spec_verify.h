@@ -395,6 +395,57 @@ int spec_verify_kv_weights(const void* q, int64_t q_row_stride, int64_t q_token_
 int spec_verify_kv_evict(const sv_paged_cache* cache, const int32_t* length, int32_t budget,
                          int32_t recent, int32_t* out_len, int32_t B, void* cuda_stream);
 
+/* ------------------------------------------------------------------------------------------------
+ * What the rule is given: penalties, biases and masks on a round's logits.
+ *
+ * [R] "Speculative decoding", rayaq.ca ml-models -- Why the output is exactly the target's: temperature, top-p and
+ * any penalties are applied to p and q before the test. A call shapes one tensor; the target's and the drafter's
+ * logits take one each, before any of the verification calls. */
+
+/* Shapes logits [B, N, V] in place. Position i of row b follows the row's text and the round's tokens before it: of
+ * a chain tokens[b, 0 .. i - 1], of a tree the tokens of node i and of its ancestors. Per token t, with n its
+ * occurrences in the row's output (counts) and among those tokens of the round:
+ *   z  = z > 0 ? z / repetition[b] : z * repetition[b]   where n > 0 or t is in the prompt (counts)
+ *   z -= frequency[b] * n;   z -= presence[b]   where n > 0
+ *   z += bias[b, k]   for each k with bias_tokens[b, k] = t, in their order
+ *   z  = -inf         where the mask bars t, whatever z was (NaN included)
+ * in fp32, rounded once to the logits' type. A logit that none of this concerns keeps its bits. (A position whose
+ * mask bars everything holds only -inf: the verification marks its row as a row error.)
+ *
+ * logits         [B, N, V] dtype (SV_DTYPE_F32 or SV_DTYPE_BF16), contiguous
+ * num_positions  [B] int32, the row's positions, 0..N (the target's: draft_len + 1, the drafter's: draft_len, a tree:
+ *                tree_size); NULL: N. Positions from there on are left as they are, as is a row with a number out of
+ *                range or whose tree is not valid.
+ * tokens         [B, T] int32, T >= N - 1 (a tree: T >= N), or NULL: none. Tokens outside [0, V) are passed over.
+ * tree_parents   [B, N] int32 as in spec_verify_tree_greedy, or NULL for a chain. Needs tokens.
+ * counts         [B, V] int16, or NULL: no text. Bit 15: the token is in the prompt; the others: its occurrences in
+ *                the output (spec_verify_count_tokens).
+ * repetition, frequency, presence
+ *                [B] fp32, or NULL: 1, 0, 0. All three NULL: tokens and counts are not read.
+ * bias_tokens, bias
+ *                [B, K] int32 and fp32, both or neither, 0 <= K <= 1024. Tokens outside [0, V) are passed over.
+ * mask           [B, mask_positions, (V + 31) / 32] int32 words, or NULL: token t is allowed where bit t % 32 of word
+ *                t / 32 is 1. mask_positions: N, or 1 for one mask at all of a row's positions.
+ * 1 <= N <= SV_MAX_GAMMA + 1, V <= 2^24. logits share no memory with another array of the call (SV_ERR_OVERLAP). One
+ * launch. Rows of whole 16-byte words (V a multiple of 8, aligned logits and counts) are moved in such words, others
+ * element by element. */
+int spec_verify_shape_logits(void* logits, const int32_t* num_positions, const int32_t* tokens, int32_t T,
+                             const int32_t* tree_parents, const int16_t* counts, const float* repetition,
+                             const float* frequency, const float* presence, const int32_t* bias_tokens,
+                             const float* bias, int32_t K, const int32_t* mask, int32_t mask_positions,
+                             int32_t B, int32_t N, int32_t V, int32_t dtype, void* cuda_stream);
+
+/* Counts tokens for the penalties: the first num[b] of tokens [B, M] go into counts [B, V] int16, as occurrences in
+ * the row's output (up to 32,767, where a count stays) or, where `prompt` is not 0, as tokens of its prompt (bit 15).
+ * After a round: out_tokens and out_num_emitted of the verification. A new row starts from zeros.
+ *
+ * num            [B] int32, 0..M; NULL: M. A row with -1 (a row error of the verification) or another number out of
+ *                range counts nothing. Tokens outside [0, V) (the verification's -1 padding) are passed over.
+ * M >= 1, V <= 2^24. counts share no memory with tokens or num (SV_ERR_OVERLAP). One launch; the result does not
+ * depend on the order in which threads come. */
+int spec_verify_count_tokens(const int32_t* tokens, const int32_t* num, int16_t* counts, int32_t prompt, int32_t B,
+                             int32_t M, int32_t V, void* cuda_stream);
+
 /* spec_verify_ex for callers that cannot allocate device memory. The pages have no counterpart:
  * this is a deployment convenience, not part of the method.
  *

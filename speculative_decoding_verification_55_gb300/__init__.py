@@ -18,4 +18,5 @@ from ._binding import SV_DTYPE_F16  # noqa: F401
 from ._cache import (PagedCache, attend, spec_verify_kv_append,  # noqa: F401
                      spec_verify_kv_evict, spec_verify_kv_weights, spec_verify_paged_attention,
                      spec_verify_paged_attention_workspace_size)
+from ._logits import spec_verify_count_tokens, spec_verify_shape_logits  # noqa: F401
 from .build import LIB_PATH, build_library  # noqa: F401

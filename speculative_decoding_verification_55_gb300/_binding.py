@@ -30,7 +30,7 @@ EXPORTED = ("spec_verify", "spec_verify_ex", "spec_verify_noalloc", "spec_verify
             "spec_verify_filtered", "spec_verify_filter_thresholds", "spec_verify_tree_greedy",
             "spec_verify_kv_rollback", "spec_verify_kv_append", "spec_verify_paged_attention",
             "spec_verify_paged_attention_workspace_size", "spec_verify_kv_weights",
-            "spec_verify_kv_evict",
+            "spec_verify_kv_evict", "spec_verify_shape_logits", "spec_verify_count_tokens",
             "spec_verify_workspace_size", "spec_verify_filtered_workspace_size",
             "spec_verify_workspace_status", "spec_verify_status_string",
             "spec_verify_version")
@@ -109,6 +109,11 @@ def lib() -> ctypes.CDLL:
             L.spec_verify_kv_weights.restype = ctypes.c_int
             L.spec_verify_kv_evict.argtypes = [vp, i32p, i32, i32, i32p, i32, vp]
             L.spec_verify_kv_evict.restype = ctypes.c_int
+            L.spec_verify_shape_logits.argtypes = [vp, i32p, i32p, i32, i32p, vp, f32p, f32p, f32p, i32p, f32p, i32,
+                                                   i32p, i32, i32, i32, i32, i32, vp]
+            L.spec_verify_shape_logits.restype = ctypes.c_int
+            L.spec_verify_count_tokens.argtypes = [i32p, i32p, vp, i32, i32, i32, i32, vp]
+            L.spec_verify_count_tokens.restype = ctypes.c_int
             _lib = L
     return _lib
 
