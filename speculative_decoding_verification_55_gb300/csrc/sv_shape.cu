@@ -6,11 +6,12 @@
 //   z' = z / rep where z > 0, else z * rep, if n > 0 or t is in the prompt (else z);
 //   z'' = z' - freq n - pres [n > 0] + sum of t's biases;  -inf where the mask bars t.
 //
-// In place, one pass, one launch. A thread owns 8 neighbouring tokens of a row (16 bytes of counts, a byte of a mask,
-// 16 or 32 bytes of logits) at all of the round's positions: the counts are read once a row, and no two threads share
-// a logit. Logits are read only where something changes them, and written only where something does: a group of 8 that
-// a mask bars is written without being read.
-// Bound: the writes of barred logits, or the reads of the counts where there is no mask.
+// In place, one launch. A CTA owns a run of a row's tokens at all of the round's positions, in two passes. First, 8
+// neighbouring tokens a thread (16 bytes of counts, a byte of a mask, 16 or 32 bytes of logits): the tokens that
+// penalties or biases concern go into a list, and what the masks bar is written, groups barred whole without being
+// read. Then the list's tokens at each position, one a lane. (Worked on in the first pass, where a warp's 256 tokens
+// hold one or two of them, they cost 269 us for 256 rows of 8 x 152064 fp32, bound by the instructions of idle lanes.)
+// Bound: the writes of barred logits; else the reads of the counts and the sectors of the logits that change.
 // Rounding: fp32 throughout, one rounding to the logits' type at the end. Logits that nothing changes keep their bits.
 
 #include <cuda_bf16.h>
@@ -22,6 +23,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxBias = 1024, kMaxRound = SV_MAX_GAMMA + 1;
+constexpr int kPositions = 9;                  // of a CTA at most: a round of eight drafts
 
 struct ShapeParams {
   void* logits;
@@ -34,10 +36,10 @@ struct ShapeParams {
   const float* pres;
   const int32_t* bias_tokens;
   const float* bias;
-  const uint8_t* mask;
-  long long mask_row, mask_position;           // bytes
-  int T, K, N, V, chunks;
-  bool penalties;
+  const int32_t* mask;
+  long long mask_row, mask_position;           // words
+  int B, T, K, N, V, blocks, per;              // blocks of `per` positions
+  bool penalties, mask_whole;                  // mask rows of whole 16-byte words
 };
 
 template <typename T>
@@ -53,160 +55,235 @@ __device__ __forceinline__ float from_float<float>(float x) { return x; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
-// kW logits or counts of a thread, moved in words of up to 16 bytes.
+// kW logits or counts of a thread, moved in words of up to 32 bytes.
 template <typename T, int kW>
-struct alignas(sizeof(T) * kW < 16 ? sizeof(T) * kW : 16) Group {
+struct alignas(sizeof(T) * kW) Group {
   T x[kW];
 };
+template <typename T, int kW>
+__device__ __forceinline__ void put(void* at, const Group<T, kW>& g) {
+  if constexpr (sizeof(g) == 32) {             // (two words of 16 bytes would each fill half of what a warp's store touches)
+    const uint32_t* const w = reinterpret_cast<const uint32_t*>(g.x);
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                 ::"l"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
+  } else {
+    *static_cast<Group<T, kW>*>(at) = g;
+  }
+}
 
-// The round's tokens or the row's biases that fall into a CTA's tokens, in their order; one warp.
-__device__ __forceinline__ int gather(const int32_t* from, int n, int v0, int v1, int lane, int* token, int* index,
-                                      unsigned* special, int width_log2) {
+// The round's tokens or the row's biases that fall into a CTA's tokens, in their order; one warp. `next`: the lane's
+// among the first 32.
+__device__ __forceinline__ int gather(const int32_t* from, int next, int n, int v0, int v1, int lane, int* token,
+                                      unsigned short* index, unsigned* special) {
   int have = 0;
   for (int x0 = 0; x0 < n; x0 += 32) {
-    const int t = x0 + lane < n ? __ldg(from + x0 + lane) : -1;
+    const int t = x0 + lane < n ? next : -1;
+    next = x0 + 32 + lane < n ? __ldg(from + x0 + 32 + lane) : -1;
     const bool in = t >= v0 && t < v1;         // (v0 >= 0: a token below 0 is in no CTA's)
     const unsigned all = __ballot_sync(sv::kFull, in);
     if (in) {
       const int at = have + __popc(all & ((1u << lane) - 1));
-      token[at] = t;
-      index[at] = x0 + lane;
-      const int g = (t - v0) >> width_log2;
-      atomicOr(special + (g >> 5), 1u << (g & 31));
+      token[at] = t - v0;
+      index[at] = static_cast<unsigned short>(x0 + lane);
+      atomicOr(special + ((t - v0) >> 5), 1u << ((t - v0) & 31));
     }
     have += __popc(all);
   }
   return have;
 }
 
-// kW: tokens of a thread, 8 or (rows that are not of whole 16-byte words) 1; kU: groups of a thread.
+// A token of the list: its place in the CTA's run, whether the round's tokens or the biases have it, its count.
+constexpr int kPlaceBits = 13;
+constexpr unsigned kSpecial = 1u << kPlaceBits;
+__device__ __forceinline__ unsigned listed(int place, bool special, int16_t count) {
+  return static_cast<unsigned>(place) | (special ? kSpecial : 0u) | static_cast<unsigned>(static_cast<unsigned short>(count)) << 16;
+}
+
+// kW: tokens of a thread, 8 or (rows that are not of whole words) 1; kU: groups of a thread.
 template <typename T, int kW, int kU>
-__global__ void __launch_bounds__(kThreads) sv_shape_kernel(const ShapeParams P) {
+__global__ void __launch_bounds__(kThreads, 5) sv_shape_kernel(const ShapeParams P) {
   using G = Group<T, kW>;
   constexpr int kSpan = kThreads * kW * kU;    // tokens of a CTA
-  constexpr int kLog2 = kW == 8 ? 3 : 0;
   constexpr unsigned kAll = (1u << kW) - 1;
-  __shared__ unsigned special[kThreads * kU / 32];
-  __shared__ int said[kMaxRound], said_at[kMaxRound], lists[2];
-  __shared__ int biased[kMaxBias], biased_at[kMaxBias];
+  static_assert(kSpan <= 1 << kPlaceBits, "a place in the list");
+  __shared__ unsigned special[kSpan / 32];     // a bit a token
+  __shared__ __align__(16) unsigned masks[kPositions][kSpan / 32];
+  __shared__ unsigned list[kSpan];
+  __shared__ int said[kMaxRound], biased[kMaxBias], up[kMaxRound], lists[2], length;
+  __shared__ unsigned short said_at[kMaxRound], biased_at[kMaxBias];
   __shared__ unsigned long long above[sv::kMaxTreeNodes];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int b = blockIdx.x / P.chunks, v0 = (blockIdx.x - b * P.chunks) * kSpan, v1 = min(v0 + kSpan, P.V);
-  const int m = P.num ? __ldg(P.num + b) : P.N;
+  const int run = blockIdx.x / P.blocks;       // the rows' first runs first: a text's tokens have low numbers
+  const int b = run % P.B, v0 = run / P.B * kSpan, v1 = min(v0 + kSpan, P.V);
+  const int first = (blockIdx.x - run * P.blocks) * P.per, most = min(P.per, P.N - first);
 
-  // Counts first: they take the longest to come.
-  Group<int16_t, kW> n0[kU];
+  // What takes long to come is asked for at once: the row's positions, its masks, its counts, its tree.
+  const int m = P.num ? __ldg(P.num + b) : P.N;
+  constexpr int kWords = kSpan / 32;           // of a mask
+  if (P.mask) {
+    const int words = (v1 - v0 + 31) >> 5;
+    const int32_t* const from = P.mask + b * P.mask_row + (v0 >> 5);
+    for (int y = warp; y < most; y += kThreads / 32) {
+      const int32_t* const f = from + (first + y) * P.mask_position;
+      const uint32_t to = sv::smem_addr(masks[y]);
+      if (P.mask_whole) {
+        for (int w = 4 * lane; w < kWords; w += 128)
+          if (w < words) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + 4 * w), "l"(f + w) : "memory");
+      } else {
+        for (int w = lane; w < kWords; w += 32)
+          if (w < words) asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + 4 * w), "l"(f + w) : "memory");
+      }
+    }
+  }
+  Group<int16_t, kW> count[kU];
 #pragma unroll
   for (int u = 0; u < kU; ++u) {
     const int v = v0 + (u * kThreads + tid) * kW;
 #pragma unroll
-    for (int k = 0; k < kW; ++k) n0[u].x[k] = 0;
+    for (int k = 0; k < kW; ++k) count[u].x[k] = 0;
     if (P.counts && v < v1)
-      n0[u] = *reinterpret_cast<const Group<int16_t, kW>*>(P.counts + static_cast<size_t>(b) * P.V + v);
+      count[u] = *reinterpret_cast<const Group<int16_t, kW>*>(P.counts + static_cast<size_t>(b) * P.V + v);
   }
-  for (int x = tid; x < kThreads * kU / 32; x += kThreads) special[x] = 0;
-  bool ok = m >= 0 && m <= P.N;
-  if (ok && P.parents) ok = sv::tree_masks(P.parents + static_cast<size_t>(b) * P.N, m, above, tid, kThreads);
-  if (!__syncthreads_and(ok) || m == 0) return;
-  // A chain's position i follows tokens 0 .. i - 1, a tree's node i follows its ancestors and itself.
-  if (warp == 0) {
-    const int have = P.tokens && P.penalties
-                         ? gather(P.tokens + static_cast<size_t>(b) * P.T, P.parents ? m : m - 1, v0, v1, lane, said, said_at, special, kLog2)
-                         : 0;
-    if (lane == 0) lists[0] = have;
-  } else if (warp == 1) {
-    const int have = gather(P.bias_tokens + static_cast<size_t>(b) * P.K, P.K, v0, v1, lane, biased, biased_at, special, kLog2);
-    if (lane == 0) lists[1] = have;
-  }
+  const int32_t* const from = warp == 0 ? P.tokens + static_cast<size_t>(b) * P.T : P.bias_tokens + static_cast<size_t>(b) * P.K;
+  const int lists_most = warp == 0 ? (P.tokens && P.penalties ? P.T : 0) : (warp == 1 ? P.K : 0);
+  const int next = lane < lists_most ? __ldg(from + lane) : -1;
   const float rep = P.rep ? __ldg(P.rep + b) : 1.0f, freq = P.freq ? __ldg(P.freq + b) : 0.0f;
   const float pres = P.pres ? __ldg(P.pres + b) : 0.0f;
-  __syncthreads();
+  bool ok = true;
+  if (P.parents && tid < P.N) {
+    const int parent = __ldg(P.parents + static_cast<size_t>(b) * P.N + tid);
+    up[tid] = parent;
+    ok = tid >= m || (tid == 0 ? parent == -1 : (parent >= 0 && parent < tid));
+  }
+  for (int x = tid; x < kSpan / 32; x += kThreads) special[x] = 0;
+  if (tid == 0) length = 0;
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  if (!__syncthreads_and(ok && m >= 0 && m <= P.N) || first >= m) return;
+  const int here = min(m - first, most);       // positions of this CTA
+  // A chain's position i follows tokens 0 .. i - 1, a tree's node i follows its ancestors and itself.
+  if (warp == 0) {
+    const int have = gather(from, next, min(lists_most, P.parents ? m : m - 1), v0, v1, lane, said, said_at, special);
+    if (lane == 0) lists[0] = have;
+  } else if (warp == 1) {
+    const int have = gather(from, next, lists_most, v0, v1, lane, biased, biased_at, special);
+    if (lane == 0) lists[1] = have;
+  } else if (P.parents && tid - 64 < m) {      // warps 2 to 4: places 1.. of the tree that a node follows, as bits from 0
+    unsigned long long set = 0;
+    for (int x = tid - 64; x > 0; x = up[x]) set |= 1ull << (x - 1);     // (parents lie below their nodes)
+    above[tid - 64] = set;
+  }
 
-  const uint8_t* const mask = P.mask ? P.mask + b * P.mask_row : nullptr;
-  T* const row = static_cast<T*>(P.logits) + static_cast<size_t>(b) * P.N * P.V;
-  const float inf = __int_as_float(0x7f800000);
+  T* const row = static_cast<T*>(P.logits) + (static_cast<size_t>(b) * P.N + first) * P.V + v0;
+  if (P.mask) {
+    const T barred = from_float<T>(__int_as_float(0xff800000));
+    G all;
+#pragma unroll
+    for (int k = 0; k < kW; ++k) all.x[k] = barred;
 #pragma unroll 1
-  for (int u = 0; u < kU; ++u) {
-    const int g = u * kThreads + tid, v = v0 + g * kW;
-    if (v >= v1) break;
-    const bool odd = (special[g >> 5] >> (g & 31)) & 1;
-    bool any = odd;
+    for (int u = 0; u < kU; ++u) {
+      const int at = (u * kThreads + tid) * kW;
+      if (v0 + at >= v1) break;
+      T* to = row + at;
+#pragma unroll 2
+      for (int y = 0; y < here; ++y, to += P.V) {
+        unsigned bar = ~(masks[y][at >> 5] >> (at & 31)) & kAll;
+        if (bar == kAll) {
+          put(to, all);
+        } else if (kW == 8 && bar) {
+          // Barred in part: read and written where that is fewer accesses than the barred ones alone.
+          if (__popc(bar) > 2 && __popc(bar) < 6) {
+            G z = *reinterpret_cast<const G*>(to);
 #pragma unroll
-    for (int k = 0; k < kW; ++k) any |= n0[u].x[k] != 0;
-    if (!any && !mask) continue;
-    float add[kW];
-    unsigned touched = 0;
-#pragma unroll
-    for (int k = 0; k < kW; ++k) add[k] = 0.0f;
-    if (odd)
-      for (int e = 0; e < lists[1]; ++e) {
-        const float f = __ldg(P.bias + static_cast<size_t>(b) * P.K + biased_at[e]);
-#pragma unroll
-        for (int k = 0; k < kW; ++k)
-          if (biased[e] == v + k) {
-            add[k] += f;
-            touched |= 1u << k;
-          }
-      }
-    constexpr int kBatch = 4;                  // positions whose loads are in flight together
-    for (int i0 = 0; i0 < m; i0 += kBatch) {
-      unsigned allowed[kBatch];
-      G z[kBatch];
-#pragma unroll
-      for (int y = 0; y < kBatch; ++y) {
-        allowed[y] = kAll;
-        if (mask && i0 + y < m) allowed[y] = __ldg(mask + (i0 + y) * P.mask_position + (v >> 3)) >> (kW == 8 ? 0 : v & 7) & kAll;
-      }
-#pragma unroll
-      for (int y = 0; y < kBatch; ++y)
-        if (i0 + y < m && allowed[y] && (any || allowed[y] != kAll))
-          z[y] = *reinterpret_cast<const G*>(row + static_cast<size_t>(i0 + y) * P.V + v);
-#pragma unroll
-      for (int y = 0; y < kBatch; ++y) {
-        const int i = i0 + y;
-        if (i >= m || (!any && allowed[y] == kAll)) continue;
-        if (any && allowed[y]) {
-          int n[kW];
-#pragma unroll
-          for (int k = 0; k < kW; ++k) n[k] = n0[u].x[k] & 32767;
-          if (odd)
-            for (int e = 0; e < lists[0]; ++e) {
-              const int a = said_at[e];        // (place 0 of a tree, the root, is above every node)
-              const bool follows = P.parents ? a == 0 || ((above[i] >> (a - 1)) & 1) : a < i;
-#pragma unroll
-              for (int k = 0; k < kW; ++k) n[k] += follows && said[e] == v + k;
-            }
-#pragma unroll
-          for (int k = 0; k < kW; ++k) {
-            const bool seen = n[k] > 0 || n0[u].x[k] < 0;
-            if (!seen && !((touched >> k) & 1)) continue;
-            float x = to_float<T>(z[y].x[k]);
-            if (seen) x = x > 0.0f ? x / rep : x * rep;
-            x -= freq * static_cast<float>(n[k]);
-            if (n[k] > 0) x -= pres;
-            z[y].x[k] = from_float<T>(x + add[k]);
+            for (int k = 0; k < kW; ++k)
+              if ((bar >> k) & 1) z.x[k] = barred;
+            put(to, z);
+          } else {
+            for (; bar; bar &= bar - 1) to[__ffs(bar) - 1] = barred;
           }
         }
-#pragma unroll
-        for (int k = 0; k < kW; ++k)
-          if (!((allowed[y] >> k) & 1)) z[y].x[k] = from_float<T>(-inf);
-        *reinterpret_cast<G*>(row + static_cast<size_t>(i) * P.V + v) = z[y];
       }
+    }
+  }
+  __syncthreads();
+
+#pragma unroll
+  for (int u = 0; u < kU; ++u) {
+    const int at = (u * kThreads + tid) * kW;  // (behind the row's last token nothing is counted or special)
+    const unsigned marks = special[at >> 5] >> (at & 31) & kAll;
+    unsigned touched = marks;
+#pragma unroll
+    for (int k = 0; k < kW; ++k) touched |= (count[u].x[k] != 0 ? 1u : 0u) << k;
+    if (!touched) continue;
+    int to = atomicAdd(&length, __popc(touched));
+#pragma unroll
+    for (int k = 0; k < kW; ++k)
+      if ((touched >> k) & 1) list[to++] = listed(at + k, (marks >> k) & 1, count[u].x[k]);
+  }
+  __syncthreads();
+
+  // 32 of the list's tokens a warp, at as many positions as leave every warp some (all of them where the list is long):
+  // their logits are in flight together.
+  constexpr int kWarps = kThreads / 32;
+  const int len = length, segments = (len + 31) >> 5;
+  const int step = segments >= kWarps ? here : (here * segments + kWarps - 1) / kWarps;
+  const int units = segments ? segments * ((here + step - 1) / step) : 0;
+  for (int x = warp; x < units; x += kWarps) {
+    const int y0 = x / segments * step, l = x % segments * 32 + lane, steps = min(step, here - y0);
+    if (l >= len) continue;
+    const unsigned e = list[l];
+    const int place = e & (kSpecial - 1), n = (e >> 16) & 32767;
+    T* const at = row + static_cast<size_t>(y0) * P.V + place;
+    float z[kPositions];
+    unsigned allowed = 0;                      // a bit a position
+#pragma unroll
+    for (int y = 0; y < kPositions; ++y) {
+      if (y >= steps) break;
+      if (P.mask && !((masks[y0 + y][place >> 5] >> (place & 31)) & 1)) continue;
+      allowed |= 1u << y;
+      z[y] = to_float<T>(at[static_cast<size_t>(y) * P.V]);
+    }
+    bool any = (e >> 16) != 0;                 // concerned at every position
+    unsigned long long more = 0;               // what the round adds to n, seven bits a position
+    float add = 0.0f;
+    if (e & kSpecial) {
+      for (int s = 0; s < lists[0]; ++s) {
+        if (said[s] != place) continue;
+        const int a = said_at[s];              // (place 0 of a tree, the root, is above every node)
+        for (int y = 0; y < steps; ++y)
+          if (P.parents ? a == 0 || ((above[first + y0 + y] >> (a - 1)) & 1) : a < first + y0 + y) more += 1ull << (7 * y);
+      }
+      for (int s = 0; s < lists[1]; ++s)
+        if (biased[s] == place) {
+          add += __ldg(P.bias + static_cast<size_t>(b) * P.K + biased_at[s]);
+          any = true;
+        }
+    }
+#pragma unroll
+    for (int y = 0; y < kPositions; ++y) {
+      if (y >= steps) break;
+      const int uses = n + (static_cast<int>(more >> (7 * y)) & 127);
+      if (!((allowed >> y) & 1) || !(any || uses > 0)) continue;
+      float v = z[y];
+      if (uses > 0 || e >> 31) v = v > 0.0f ? v / rep : v * rep;
+      v -= freq * static_cast<float>(uses);
+      if (uses > 0) v -= pres;
+      at[static_cast<size_t>(y) * P.V] = from_float<T>(v + add);
     }
   }
 }
 
 template <typename T>
-int launch_shape(ShapeParams& P, int B, bool whole, int sms, cudaStream_t st) {
-  // Four groups a thread where that still leaves eight CTAs an SM, else one.
-  const long long groups = static_cast<long long>(B) * ((P.V + 7) / 8);
-  const bool four = groups / (4 * kThreads) >= 8ll * sms;
-  const int span = kThreads * (whole ? (four ? 32 : 8) : 8);
-  P.chunks = (P.V + span - 1) / span;
-  const long long grid = static_cast<long long>(B) * P.chunks;
+int launch_shape(ShapeParams& P, bool whole, int sms, cudaStream_t st) {
+  // Two groups a thread where that still leaves eight CTAs an SM, else one.
+  P.blocks = (P.N + kPositions - 1) / kPositions;
+  P.per = (P.N + P.blocks - 1) / P.blocks;
+  const long long groups = static_cast<long long>(P.B) * P.blocks * ((P.V + 7) / 8);
+  const bool two = whole && groups / (2 * kThreads) >= 8ll * sms;
+  const int span = kThreads * (two ? 16 : 8);
+  const long long grid = static_cast<long long>(P.B) * ((P.V + span - 1) / span) * P.blocks;
   if (grid > 0x7fffffffll) return SV_ERR_BAD_SHAPE;
   if (!whole) sv_shape_kernel<T, 1, 8><<<static_cast<unsigned>(grid), kThreads, 0, st>>>(P);
-  else if (four) sv_shape_kernel<T, 8, 4><<<static_cast<unsigned>(grid), kThreads, 0, st>>>(P);
+  else if (two) sv_shape_kernel<T, 8, 2><<<static_cast<unsigned>(grid), kThreads, 0, st>>>(P);
   else sv_shape_kernel<T, 8, 1><<<static_cast<unsigned>(grid), kThreads, 0, st>>>(P);
   return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
@@ -301,18 +378,19 @@ extern "C" int spec_verify_shape_logits(void* logits, const int32_t* num_positio
   P.pres = presence;
   P.bias_tokens = bias_tokens;
   P.bias = bias;
-  P.mask = reinterpret_cast<const uint8_t*>(mask);
-  P.mask_row = static_cast<long long>(4 * words) * mask_positions;
-  P.mask_position = mask_positions == 1 ? 0 : static_cast<long long>(4 * words);
+  P.mask = mask;
+  P.mask_whole = words % 4 == 0 && !sv::misaligned(mask, 16);
+  P.mask_row = static_cast<long long>(words) * mask_positions;
+  P.mask_position = mask_positions == 1 ? 0 : static_cast<long long>(words);
+  P.B = B;
   P.T = T;
   P.K = bias ? K : 0;
   P.N = N;
   P.V = V;
   if (!P.penalties && P.K == 0 && !mask) return SV_OK;
-  // Whole 16-byte words of counts are whole ones of logits too.
-  const bool whole = V % 8 == 0 && !sv::misaligned(logits, 16) && !sv::misaligned(P.counts, 16);
+  const bool whole = V % 8 == 0 && !sv::misaligned(logits, 8 * size) && !sv::misaligned(P.counts, 16);
   const cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
-  return dtype == SV_DTYPE_F32 ? launch_shape<float>(P, B, whole, sms, s) : launch_shape<__nv_bfloat16>(P, B, whole, sms, s);
+  return dtype == SV_DTYPE_F32 ? launch_shape<float>(P, whole, sms, s) : launch_shape<__nv_bfloat16>(P, whole, sms, s);
 }
 
 extern "C" int spec_verify_count_tokens(const int32_t* tokens, const int32_t* num, int16_t* counts, int32_t prompt,
