@@ -364,6 +364,30 @@ int spec_verify_paged_attention(const void* q, int64_t q_row_stride, int64_t q_t
                                 void* out, float* out_lse, int32_t B, int32_t N, int32_t Hq,
                                 void* workspace, size_t workspace_bytes, void* cuda_stream);
 
+/* spec_verify_paged_attention of a batch whose rows share the fronts of their contexts (a common prompt or document):
+ * each front's keys and values are read once for all tokens of its rows, not once a row. What a row attends, and what
+ * the outputs are, is as in spec_verify_paged_attention on the same tables.
+ *
+ * q              [B, N, Hq, D] as there; its rows follow one another (q_row_stride = N * q_token_stride where B and N are
+ *                above 1, else SV_ERR_BAD_SHAPE: a slice of a fused projection has it)
+ * shared_len     [B] int32: the first shared_len[b] entries of row b are those of its group's first row, in the first
+ *                row's pages (a row's own page numbers for them are not read). A multiple of page_size, at most
+ *                prefix_len[b], and within a group the same; or 0, for a row that attends its own entries alone.
+ * group_start    [groups + 1] int32, ascending from at least 0 to at most B: group g is rows group_start[g] ..
+ *                group_start[g + 1] - 1 (it may be empty). Rows in no group have shared_len 0.
+ * workspace      spec_verify_shared_attention_workspace_size(...) bytes, 256-byte aligned, without setup: among them two
+ *                fp32 results of each query, 8 B N Hq (D + 2) bytes.
+ * A row whose shared_len is none of that is in error; all are where group_start does not ascend within 0 .. B. A page
+ * number out of range in a front puts NaN into the outputs of all its rows' tokens.
+ * B N Hq <= 2^28. Three launches. Other arguments, errors and limits as in spec_verify_paged_attention. */
+size_t spec_verify_shared_attention_workspace_size(int32_t B, int32_t N, int32_t Hq, const sv_paged_cache* cache);
+int spec_verify_shared_attention(const void* q, int64_t q_row_stride, int64_t q_token_stride,
+                                 const sv_paged_cache* cache, const int32_t* prefix_len,
+                                 const int32_t* shared_len, const int32_t* group_start, int32_t groups,
+                                 const int32_t* num_queries, const int32_t* tree_parents, float scale,
+                                 void* out, float* out_lse, int32_t B, int32_t N, int32_t Hq,
+                                 void* workspace, size_t workspace_bytes, void* cuda_stream);
+
 /* Adds to the cache's weights what the kept tokens of a round gave to each entry: for every entry j and
  * key head of row b, weight_j += sum over the kept tokens d < num_kept[b] with n_b + d >= j and over the
  * query heads of that key head of exp(scale * q . k_j - lse), where q and lse are those of token d, or

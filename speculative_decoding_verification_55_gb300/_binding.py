@@ -30,6 +30,7 @@ EXPORTED = ("spec_verify", "spec_verify_ex", "spec_verify_noalloc", "spec_verify
             "spec_verify_filtered", "spec_verify_filter_thresholds", "spec_verify_tree_greedy",
             "spec_verify_kv_rollback", "spec_verify_kv_append", "spec_verify_paged_attention",
             "spec_verify_paged_attention_workspace_size", "spec_verify_kv_weights",
+            "spec_verify_shared_attention", "spec_verify_shared_attention_workspace_size",
             "spec_verify_kv_evict", "spec_verify_shape_logits", "spec_verify_count_tokens",
             "spec_verify_workspace_size", "spec_verify_filtered_workspace_size",
             "spec_verify_workspace_status", "spec_verify_status_string",
@@ -104,6 +105,11 @@ def lib() -> ctypes.CDLL:
             L.spec_verify_paged_attention.restype = ctypes.c_int
             L.spec_verify_paged_attention_workspace_size.argtypes = [i32, i32, vp]
             L.spec_verify_paged_attention_workspace_size.restype = sz
+            L.spec_verify_shared_attention.argtypes = [vp, i64, i64, vp, i32p, i32p, i32p, i32, i32p, i32p,
+                                                       ctypes.c_float, vp, f32p, i32, i32, i32, vp, sz, vp]
+            L.spec_verify_shared_attention.restype = ctypes.c_int
+            L.spec_verify_shared_attention_workspace_size.argtypes = [i32, i32, i32, vp]
+            L.spec_verify_shared_attention_workspace_size.restype = sz
             L.spec_verify_kv_weights.argtypes = [vp, i64, i64, f32p, vp, i32p, i32p, i32p, ctypes.c_float,
                                                  i32, i32, i32, vp]
             L.spec_verify_kv_weights.restype = ctypes.c_int

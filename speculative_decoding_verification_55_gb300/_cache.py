@@ -188,18 +188,62 @@ def spec_verify_kv_evict(cache, length, budget, recent, out_len, stream=None) ->
           budget, recent, _small(out_len, "out_len", torch.int32, (B,), dev), B)
 
 
+def spec_verify_shared_attention_workspace_size(B: int, N: int, Hq: int, cache: PagedCache) -> int:
+    return int(lib().spec_verify_shared_attention_workspace_size(B, N, Hq, cache.ref))
+
+
+def _starts(group_start, device):
+    """(address, number of groups) of group_start [groups + 1]."""
+    import torch
+    if group_start.dim() != 1 or group_start.shape[0] < 2:
+        raise ValueError(f"group_start must be [groups + 1], got {tuple(group_start.shape)}")
+    return _small(group_start, "group_start", torch.int32, group_start.shape, device), group_start.shape[0] - 1
+
+
+def _shared_attention(q, cache, prefix_len, shared_len, group_start, num_queries, tree_parents, N, Hq, rs, ts, out,
+                      out_lse, workspace, workspace_bytes, scale, stream):
+    import torch
+    dev, B, i32 = cache.device, cache.B, torch.int32
+    if B > 1 and N > 1 and rs != N * ts:
+        raise ValueError(f"the rows of q must follow one another: strides {q.stride()}")
+    start, groups = _starts(group_start, dev)
+    _call(lib().spec_verify_shared_attention, cache, stream, q.data_ptr(), rs, ts, cache.ref,
+          _small(prefix_len, "prefix_len", i32, (B,), dev), _small(shared_len, "shared_len", i32, (B,), dev), start, groups,
+          _small(num_queries, "num_queries", i32, (B,), dev), _small(tree_parents, "tree_parents", i32, (B, N), dev),
+          1.0 / math.sqrt(cache.head_dim) if scale is None else scale, out, out_lse, B, N, Hq, workspace,
+          workspace_bytes)
+
+
+def spec_verify_shared_attention(q, cache, prefix_len, shared_len, group_start, num_queries, tree_parents, out, out_lse,
+                                 workspace, scale=None, stream=None) -> None:
+    """Calls the C ABI spec_verify_shared_attention on torch tensors: spec_verify_paged_attention of rows
+    group_start[g] .. group_start[g + 1] - 1 whose first shared_len entries are the same pages. The rows of q [B, N, Hq,
+    D] follow one another. Raises SpecVerifyError on a nonzero status."""
+    import torch
+    dev, B = cache.device, cache.B
+    N, Hq, rs, ts = _tokens(q, "q", cache)
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {dev}")
+    _shared_attention(q, cache, prefix_len, shared_len, group_start, num_queries, tree_parents, N, Hq, rs, ts,
+                      _small(out, "out", cache.dtype, (B, N, Hq, cache.head_dim), dev),
+                      _small(out_lse, "out_lse", torch.float32, (B, N, Hq), dev), workspace.data_ptr(),
+                      workspace.nbytes, scale, stream)
+
+
 _attend_ws = {}
-# A call makes two launches on its stream's workspace: another thread's must not come in between.
+# A call makes two or three launches on its stream's workspace: another thread's must not come in between.
 _attend_lock = threading.Lock()
 
 
-def _attend_workspace(N, Hq, cache):
+def _attend_workspace(N, Hq, cache, shared=False):
     """A workspace cached per (device, current stream) and grown on demand. A call that is being captured
     gets one of its own: replays of two graphs may overlap."""
     import torch
-    need = cache.workspace_need.get((N, Hq))
+    need = cache.workspace_need.get((N, Hq, shared))
     if need is None:
-        need = cache.workspace_need[N, Hq] = spec_verify_paged_attention_workspace_size(N, Hq, cache)
+        need = spec_verify_shared_attention_workspace_size(cache.B, N, Hq, cache) if shared \
+            else spec_verify_paged_attention_workspace_size(N, Hq, cache)
+        cache.workspace_need[N, Hq, shared] = need
     if torch.cuda.is_current_stream_capturing():
         return torch.empty(need, dtype=torch.uint8, device=cache.device)
     key = (cache.device, _raw_stream(None, cache.device))
@@ -226,4 +270,25 @@ def attend(q, cache, prefix_len, num_queries=None, tree_parents=None, scale=None
         ws = _attend_workspace(N, Hq, cache)
         _attention(q, cache, prefix_len, num_queries, tree_parents, N, Hq, rs, ts, out.data_ptr(), lse.data_ptr(),
                    ws.data_ptr(), ws.nbytes, scale, None)
+    return out, lse
+
+
+def attend_shared(q, cache, prefix_len, shared_len, group_start, num_queries=None, tree_parents=None, scale=None, stream=None):
+    """attend of a batch whose rows share the fronts of their contexts, each front read once for all of its rows: rows
+    group_start[g] .. group_start[g + 1] - 1 have their first shared_len[b] entries, whole pages, in common. Returns
+    (out, lse) as attend does."""
+    import torch
+    if stream is not None:
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), cache.device)
+        with torch.cuda.stream(stream):
+            return attend_shared(q, cache, prefix_len, shared_len, group_start, num_queries, tree_parents, scale)
+    N, Hq, rs, ts = _tokens(q, "q", cache)
+    _on_gpu(cache.device)
+    out = torch.empty((cache.B, N, Hq, cache.head_dim), dtype=q.dtype, device=cache.device)
+    lse = torch.empty((cache.B, N, Hq), dtype=torch.float32, device=cache.device)
+    with _attend_lock:
+        ws = _attend_workspace(N, Hq, cache, shared=True)
+        _shared_attention(q, cache, prefix_len, shared_len, group_start, num_queries, tree_parents, N, Hq, rs, ts,
+                          out.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.nbytes, scale, None)
     return out, lse

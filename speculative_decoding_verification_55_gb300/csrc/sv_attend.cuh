@@ -5,8 +5,9 @@
 
 namespace sv {
 
-struct AttendParams {
-  Round R;
+template <bool kShared>
+struct AttendParamsOf {
+  typename Batch<kShared>::Rows R;
   const char* q;
   long long row_stride, token_stride;          // bytes
   const int32_t* parents;
@@ -25,6 +26,20 @@ struct AttendParams {
   float* part_o;                               // [2 grid][ways][D][rows]
   float2* part_ml;                             // [2 grid][ways][rows] maximum and sum
 };
+typedef AttendParamsOf<false> AttendParams;
+
+// Of rows that share fronts: an item's result, whole or joined, is a side of its queries' (0: the fronts', 1: the rows'
+// own entries'), which the merge kernel puts together. A record of `shared` has 2 x the first token + the side as its row.
+struct SharedParams : AttendParamsOf<true> {
+  float* side_o;                               // [2][B N Hq][D]
+  float2* side_ml;                             // [2][B N Hq] maximum and sum
+  int* bad_groups;                             // not 0: group_start does not ascend within 0 .. B
+  __device__ __forceinline__ size_t side_at(int side, size_t at) const {
+    return static_cast<size_t>(side) * R.B * R.N * Hq + at;
+  }
+};
+template <bool kShared>
+using ParamsOf = typename std::conditional<kShared, SharedParams, AttendParams>::type;
 
 // Probabilities are kept times a power of two: relative to a row's running maximum they go down to 2^-25 and less in
 // long rows, and a half's steps below 2^-14 are all 2^-24. The largest are 2^15 (a half ends at 65,504): the 16-row
@@ -80,7 +95,8 @@ __device__ __forceinline__ void fill_unused(const AttendParams& P, int D, int ti
 }
 
 // The item that this CTA begins, for the join kernel (one thread).
-__device__ __forceinline__ void tell_shared(const AttendParams& P, int way, int row, int head, int q_tile, int rows,
+template <class Params>
+__device__ __forceinline__ void tell_shared(const Params& P, int way, int row, int head, int q_tile, int rows,
                                             bool whole, long long item_at, int tiles, const Plan& plan) {
   if (whole && !P.by_item) return;
   const int cta = blockIdx.x, last = unit_owner(item_at + tiles - 1, plan);
@@ -92,10 +108,14 @@ __device__ __forceinline__ void tell_shared(const AttendParams& P, int way, int 
 
 // Joins the parts of the items that the attention kernel's `grid` CTAs shared.
 int launch_attend_join(const AttendParams& P, bool f16, bool wide, int grid, cudaStream_t st);
+int launch_attend_join(const SharedParams& P, bool f16, int grid, cudaStream_t st);
 
 // The wide kernel (at most 128 query heads a key head; query tiles of tile_rows <= 128 rows, whole tokens of
 // which q's boxes hold q_tokens; key tiles of 128, or of 64 for heads of 256; two ways up to heads of 128).
 int launch_attend_wide(const AttendParams& P, bool f16, const CUtensorMap& k, const CUtensorMap& v,
                        const CUtensorMap& q, int q_tokens, int grid, cudaStream_t st);
+// The same of rows that share fronts (q's boxes run over all of the batch's tokens).
+int launch_attend_shared(const SharedParams& P, bool f16, const CUtensorMap& k, const CUtensorMap& v,
+                         const CUtensorMap& q, int q_tokens, int grid, cudaStream_t st);
 
 }  // namespace sv

@@ -17,18 +17,31 @@ namespace {
 
 constexpr int kWarps = 16, kThreads = 32 * kWarps;
 
-template <bool F16, int D, int kRows, int kAcross, int kCols>    // kAcross: warps across the columns
-__global__ void __launch_bounds__(kThreads) sv_attend_join_kernel(const sv::AttendParams P) {
+// kAcross: warps across the columns. kShared: of rows that share fronts, to the sides of their queries.
+template <bool F16, int D, int kRows, int kAcross, int kCols, bool kShared>
+__global__ void __launch_bounds__(kThreads) sv_attend_join_kernel(const sv::ParamsOf<kShared> P) {
   constexpr int kRowLanes = kRows < 32 ? kRows : 32, kColLanes = 32 / kRowLanes;
   constexpr int kPartGroups = kWarps / kAcross, kColsHere = kAcross * kColLanes * kCols;
   constexpr int kColBlocks = D / kColsHere;
   __shared__ float acc[kWarps][kCols][33];
   __shared__ float2 ml[kWarps][32];
-  const sv::Round& R = P.R;
+  const auto& R = P.R;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if constexpr (kShared) {
+    asm volatile("griddepcontrol.launch_dependents;");   // the merge kernel's CTAs, which wait for this grid's end
+    if (blockIdx.x == 0 && blockIdx.y == 0) {  // (the attention kernel takes no group that is out of range)
+      bool bad = false;
+      for (int g = tid; g <= R.groups; g += kThreads) {
+        const int s = __ldg(R.start + g);
+        bad |= s > R.B || (g == 0 ? s < 0 : __ldg(R.start + g - 1) > s);
+      }
+      bad = __syncthreads_or(bad);
+      if (tid == 0) *P.bad_groups = bad;
+    }
+  }
   int4 it;                                             // row, head, query tile, the last CTA
   int c0, way, rows;
-  if (kCols == 8) {                                    // records by item; the lengths were there before the attention
+  if constexpr (kCols == 8) {                          // records by item; the lengths were there before the attention
     const int id = blockIdx.x, pair = id / P.by_item;
     it = make_int4(pair / R.C.heads, pair % R.C.heads, id % P.by_item, 0);
     way = it.z % P.ways;
@@ -95,14 +108,21 @@ __global__ void __launch_bounds__(kThreads) sv_attend_join_kernel(const sv::Atte
   }
   const float inv = 1.0f / L;
   const int i = (row0 + g0 + r) / R.group, hq = it.y * R.group + (row0 + g0 + r) - i * R.group;
-  const size_t at = (static_cast<size_t>(it.x) * R.N + i) * P.Hq + hq;
+  const size_t at = (kShared ? static_cast<size_t>(it.x >> 1) + i : static_cast<size_t>(it.x) * R.N + i) * P.Hq + hq;
 #pragma unroll
   for (int x = 0; x < kAcross; ++x) {
     const int col = first + x, wc = col / (kColLanes * kCols), cl = (col / kCols) % kColLanes;
     float s = 0.0f;
 #pragma unroll
     for (int g = 0; g < kPartGroups; ++g) s += acc[g * kAcross + wc][col % kCols][cl * kRowLanes + r] * f[g];
-    v[x] = s * inv;
+    v[x] = kShared ? s : s * inv;
+  }
+  if constexpr (kShared) {
+    float* o = P.side_o + P.side_at(it.x & 1, at) * D + col0 + first;
+#pragma unroll
+    for (int x = 0; x < kAcross; x += 4) *reinterpret_cast<float4*>(o + x) = make_float4(v[x], v[x + 1], v[x + 2], v[x + 3]);
+    if (col0 + first == 0) P.side_ml[P.side_at(it.x & 1, at)] = make_float2(M, L);
+    return;
   }
   char* out = static_cast<char*>(P.out) + (at * D + col0 + first) * 2;
   if constexpr (kAcross == 1) {
@@ -115,10 +135,10 @@ __global__ void __launch_bounds__(kThreads) sv_attend_join_kernel(const sv::Atte
   if (P.lse && col0 + first == 0) P.lse[at] = (M * c + (log2f(L) - sv::kProbBits<F16, kRows == 128>)) * 0.6931471805599453f;
 }
 
-template <bool F16, int D, int kRows, int kAcross, int kCols>
-int launch2(const sv::AttendParams& P, int blocks, cudaStream_t st) {
+template <bool F16, int D, int kRows, int kAcross, int kCols, bool kShared>
+int launch2(const sv::ParamsOf<kShared>& P, int blocks, cudaStream_t st) {
   constexpr int kRowLanes = kRows < 32 ? kRows : 32, kColsHere = kAcross * (32 / kRowLanes) * kCols;
-  const int most = min(kRows, P.R.N * P.R.group);
+  const int most = min(kRows, (kShared ? P.R.B : 1) * P.R.N * P.R.group);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(blocks, (most + kRowLanes - 1) / kRowLanes * (D / kColsHere));
   cfg.blockDim = dim3(kThreads);
@@ -128,7 +148,7 @@ int launch2(const sv::AttendParams& P, int blocks, cudaStream_t st) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, sv_attend_join_kernel<F16, D, kRows, kAcross, kCols>, P) == cudaSuccess
+  return cudaLaunchKernelEx(&cfg, sv_attend_join_kernel<F16, D, kRows, kAcross, kCols, kShared>, P) == cudaSuccess
              ? SV_OK
              : SV_ERR_CUDA;
 }
@@ -136,8 +156,8 @@ int launch2(const sv::AttendParams& P, int blocks, cudaStream_t st) {
 template <bool F16, int D, int kRows>
 int launch(const sv::AttendParams& P, int grid, cudaStream_t st) {
   constexpr int kAll = D / 16 / (kRows < 32 ? 32 / kRows : 1);
-  return P.by_item ? launch2<F16, D, kRows, 1, 8>(P, P.R.B * P.R.C.heads * P.by_item, st)
-                   : launch2<F16, D, kRows, kAll, 16>(P, grid * P.ways, st);
+  return P.by_item ? launch2<F16, D, kRows, 1, 8, false>(P, P.R.B * P.R.C.heads * P.by_item, st)
+                   : launch2<F16, D, kRows, kAll, 16, false>(P, grid * P.ways, st);
 }
 
 }  // namespace
@@ -157,6 +177,17 @@ int launch_attend_join(const AttendParams& P, bool f16, bool wide, int grid,
       if (wide) return f16 ? launch<true, 256, 128>(P, grid, st) : launch<false, 256, 128>(P, grid, st);
       return f16 ? launch<true, 256, 16>(P, grid, st) : launch<false, 256, 16>(P, grid, st);
   }
+}
+
+template <bool F16>
+int launch_shared(const SharedParams& P, int grid, cudaStream_t st) {
+  const int blocks = grid * P.ways;
+  if (P.R.C.head_dim == 64) return launch2<F16, 64, 128, 4, 16, true>(P, blocks, st);
+  if (P.R.C.head_dim == 128) return launch2<F16, 128, 128, 8, 16, true>(P, blocks, st);
+  return launch2<F16, 256, 128, 16, 16, true>(P, blocks, st);
+}
+int launch_attend_join(const SharedParams& P, bool f16, int grid, cudaStream_t st) {
+  return f16 ? launch_shared<true>(P, grid, st) : launch_shared<false>(P, grid, st);
 }
 
 }  // namespace sv

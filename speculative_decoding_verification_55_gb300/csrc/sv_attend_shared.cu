@@ -1,0 +1,223 @@
+// Attention of a round's tokens in a batch whose rows share the fronts of their contexts (a common prompt or document;
+// [R] "Speculative decoding", rayaq.ca ml-models -- Verification attention and the cache).
+//
+// A row's entries are those that its group shares, A, and its own, B. With m = max s_ij, l = sum exp(s_ij - m) and
+// o = sum exp(s_ij - m) v_j over each of the two,
+//   M = max(m_A, m_B),  L = l_A e^(m_A - M) + l_B e^(m_B - M),  out = (o_A e^(m_A - M) + o_B e^(m_B - M)) / L.
+// A of all the group's rows and tokens is one set of products with the group's keys and values, read once for up to
+// 128 or 256 query rows, not once a row. One launch of the wide kernel (sv_attend_wide.cuh) does the fronts and the
+// rows' own entries, cut into equal runs of tiles; the join kernel puts together what several CTAs did of one; the merge
+// kernel here puts the two sides of each query together.
+// Bound: the bytes of the entries, each read once, or for large groups the products (4 D a query head and entry).
+// Rounding: the sides are fp32 sums and maxima; the output is rounded once.
+
+#include <algorithm>
+
+#include "sv_attend_wide.cuh"
+
+namespace {
+
+using sv::SharedParams;
+
+constexpr int kMergeWarps = 8;
+
+// The group that holds row b, -1 for none: the starts up to b, 32 places at a time; one warp.
+__device__ __forceinline__ int group_of(const int32_t* start, int groups, int b, int lane) {
+  int lo = 0, hi = groups + 1;                 // how many of the groups + 1 starts are at most b lies in [lo, hi]
+  while (lo < hi) {
+    const int step = (hi - lo + 31) / 32, at = lo + (lane + 1) * step - 1;
+    const unsigned up = __ballot_sync(kFull, at < hi && __ldg(start + at) <= b);
+    const int n = __popc(up);                  // the starts ascend
+    lo += n * step;
+    hi = min(hi, lo + step - 1);
+  }
+  return lo > groups ? -1 : lo - 1;
+}
+
+// A warp a query: its two sides, from the join and the attention kernel.
+template <bool F16, int D>
+__global__ void __launch_bounds__(32 * kMergeWarps) sv_attend_merge_kernel(const SharedParams P) {
+  constexpr int kCols = D / 32;
+  const sv::SharedRound& R = P.R;
+  const int lane = threadIdx.x & 31, at = blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
+  const int token = at / P.Hq, b = token / R.N, i = token - b * R.N;
+  if (b >= R.B) return;
+  sv::SharedWork w;
+  bool ok = sv::row_work(R, R.groups + b, &w);
+  const int s = __ldg(R.common + b), g = group_of(R.start, R.groups, b, lane);
+  if (s > 0) {
+    const int a = g >= 0 ? __ldg(R.start + g) : -1;
+    ok = ok && a >= 0 && a <= b && __ldg(R.common + a) == s;
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  ok = ok && __ldcg(P.bad_groups) == 0;
+  float v[kCols], L = 1.0f, M = 0.0f;
+#pragma unroll
+  for (int x = 0; x < kCols; ++x) v[x] = ok ? 0.0f : __int_as_float(0x7fffffff);
+  float lse = v[0];
+  if (ok && i < w.m) {
+    L = 0.0f;
+    const float2 a = s > 0 ? __ldcg(P.side_ml + P.side_at(0, at)) : make_float2(-INFINITY, 0.0f);
+    const float2 e = __ldcg(P.side_ml + P.side_at(1, at));
+    M = fmaxf(a.x, e.x);
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+      if (side == 0 && s == 0) continue;
+      const float2 x = side ? e : a;
+      const float f = x.x == -INFINITY ? 0.0f : sv::ex2((x.x - M) * P.c);
+      L += x.x == -INFINITY ? x.y : x.y * f;   // the former: 0, or NaN
+      const float* o = P.side_o + P.side_at(side, at) * D + lane * kCols;
+#pragma unroll
+      for (int y = 0; y < kCols; y += 2) {
+        const float2 z = __ldcg(reinterpret_cast<const float2*>(o + y));
+        v[y] += z.x * f;
+        v[y + 1] += z.y * f;
+      }
+    }
+    const float inv = 1.0f / L;
+#pragma unroll
+    for (int x = 0; x < kCols; ++x) v[x] *= inv;
+    lse = (M * P.c + (log2f(L) - sv::kProbBits<F16, true>)) * 0.6931471805599453f;
+  }
+  uint32_t* out = reinterpret_cast<uint32_t*>(P.out) + (static_cast<size_t>(at) * D + lane * kCols) / 2;
+#pragma unroll
+  for (int x = 0; x < kCols; x += 2) out[x / 2] = sv::pack2<F16>(v[x], v[x + 1]);
+  if (P.lse && lane == 0) P.lse[at] = lse;
+}
+
+template <bool F16, int D>
+int merge(const SharedParams& P, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  const long long queries = static_cast<long long>(P.R.B) * P.R.N * P.Hq;
+  cfg.gridDim = dim3(static_cast<unsigned>((queries + kMergeWarps - 1) / kMergeWarps));
+  cfg.blockDim = dim3(32 * kMergeWarps);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, sv_attend_merge_kernel<F16, D>, P) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+}
+template <bool F16>
+int merge(const SharedParams& P, cudaStream_t st) {
+  const int D = P.R.C.head_dim;
+  return D == 64 ? merge<F16, 64>(P, st) : (D == 128 ? merge<F16, 128>(P, st) : merge<F16, 256>(P, st));
+}
+
+constexpr int kMaxSms = 160;
+constexpr size_t kSharedBytes = 2 * kMaxSms * sizeof(int4), kFlagBytes = 256;
+constexpr long long kMaxQueries = 1ll << 28;   // query heads of all tokens
+
+bool sizes_ok(int32_t B, int32_t N, int32_t Hq, const sv_paged_cache* c) {
+  return B >= 1 && B <= (1 << 20) && N >= 1 && N <= SV_MAX_GAMMA + 1 && Hq >= 1 && Hq <= 1024 && c->heads >= 1 &&
+         Hq % c->heads == 0 && Hq / c->heads <= 128 && static_cast<long long>(B) * N * Hq <= kMaxQueries;
+}
+size_t part_bytes(int ways, int D) { return static_cast<size_t>(2 * kMaxSms) * ways * 128 * (D * 4 + 8); }
+int ways_most(int D) { return D < 256 ? 2 : 1; }
+
+}  // namespace
+
+namespace sv {
+
+int launch_attend_shared(const SharedParams& P, bool f16, const CUtensorMap& k, const CUtensorMap& v,
+                         const CUtensorMap& q, int q_tokens, int grid, cudaStream_t st) {
+  return f16 ? launch_type<true, true>(P, k, v, q, q_tokens, grid, st) : launch_type<false, true>(P, k, v, q, q_tokens, grid, st);
+}
+
+}  // namespace sv
+
+extern "C" size_t spec_verify_shared_attention_workspace_size(int32_t B, int32_t N, int32_t Hq, const sv_paged_cache* cache) {
+  if (!cache || !sizes_ok(B, N, Hq, cache) || cache->head_dim < 1 || cache->head_dim > 256) return 0;
+  const int D = cache->head_dim;
+  const size_t sides = static_cast<size_t>(2) * B * N * Hq * (D * 4 + 8);
+  return kSharedBytes + kFlagBytes + part_bytes(ways_most(D), D) + (sides + 255) / 256 * 256;
+}
+
+extern "C" int spec_verify_shared_attention(const void* q, int64_t q_row_stride, int64_t q_token_stride,
+                                            const sv_paged_cache* cache, const int32_t* prefix_len,
+                                            const int32_t* shared_len, const int32_t* group_start, int32_t groups,
+                                            const int32_t* num_queries, const int32_t* tree_parents, float scale, void* out,
+                                            float* out_lse, int32_t B, int32_t N, int32_t Hq, void* workspace,
+                                            size_t workspace_bytes, void* cuda_stream) {
+  SharedParams P;
+  int st = sv::check_cache(cache, B, false, &P.R.C);
+  if (st != SV_OK) return st;
+  if (!q || !prefix_len || !shared_len || !group_start || !out) return SV_ERR_NULL_POINTER;
+  st = sv::check_tokens(q, q_row_stride, q_token_stride, B, N, Hq, cache->head_dim);
+  if (st != SV_OK) return st;
+  if (!sizes_ok(B, N, Hq, cache) || groups < 1 || groups > (1 << 20) || !(scale > 0.0f) || !std::isfinite(scale)) return SV_ERR_BAD_SHAPE;
+  if (B > 1 && N > 1 && q_row_stride != N * q_token_stride) return SV_ERR_BAD_SHAPE;
+  if (sv::misaligned(out, 16) || sv::misaligned(out_lse, 4) || sv::misaligned(prefix_len, 4) ||
+      sv::misaligned(shared_len, 4) || sv::misaligned(group_start, 4) || sv::misaligned(num_queries, 4) ||
+      sv::misaligned(tree_parents, 4) || sv::misaligned(workspace, 256))
+    return SV_ERR_MISALIGNED;
+  const size_t need = spec_verify_shared_attention_workspace_size(B, N, Hq, cache);
+  if (!workspace || workspace_bytes < need) return SV_ERR_WORKSPACE_TOO_SMALL;
+  const unsigned long long rows = 4ull * B, tokens = rows * N * Hq;
+  if (sv::overlap({{out, tokens / 2 * cache->head_dim}, {out_lse, tokens}, {workspace, need}},
+                  {sv::tokens_of(q, q_row_stride, q_token_stride, B, N, Hq, cache->head_dim), {prefix_len, rows},
+                   {shared_len, rows}, {group_start, 4ull * groups + 4}, {num_queries, rows}, {tree_parents, rows * N},
+                   sv::table_of(cache, B), sv::weights_of(cache), sv::pages_of(cache, cache->k), sv::pages_of(cache, cache->v)}))
+    return SV_ERR_OVERLAP;
+  int dev = 0;
+  st = sv::current_device_status(&dev);
+  if (st != SV_OK) return st;
+  int sms = sv::device_sms(dev);
+  if (sms < 1) return SV_ERR_CUDA;
+  if (sms > kMaxSms) sms = kMaxSms;
+  const int D = cache->head_dim, group = Hq / cache->heads, rows_tile = 128 / group * group;
+  // Two query tiles at once where a group has more than one's rows.
+  const long long all = static_cast<long long>(B) * N * group;
+  const int ways = D < 256 && all > static_cast<long long>(groups) * rows_tile ? 2 : 1;
+  const int q_tokens = static_cast<int>(std::min<long long>(rows_tile / group, static_cast<long long>(B) * N));
+  CUtensorMap kmap, vmap, qmap;
+  st = sv::cache_tensor_map(cache, cache->k, sv::box_rows(cache), &kmap);
+  if (st == SV_OK) st = sv::cache_tensor_map(cache, cache->v, sv::box_rows(cache), &vmap);
+  if (st == SV_OK)
+    st = sv::query_tensor_map(q, 0, N > 1 ? q_token_stride : q_row_stride, 1, B * N, Hq, D, cache->dtype, group, q_tokens, &qmap);
+  if (st != SV_OK) return st;
+  P.R.prefix = prefix_len;
+  P.R.num = num_queries;
+  P.R.B = B;
+  P.R.N = N;
+  P.R.group = group;
+  P.R.q_rows = rows_tile * ways;
+  P.R.tile_log2 = D == 256 ? 6 : 7;
+  P.R.extra = 2;
+  P.R.none_ok = false;
+  P.R.start = group_start;
+  P.R.common = shared_len;
+  P.R.groups = groups;
+  P.q = static_cast<const char*>(q);
+  P.row_stride = q_row_stride * 2;
+  P.token_stride = q_token_stride * 2;
+  P.parents = tree_parents;
+  P.out = out;
+  P.lse = out_lse;
+  P.c = scale * sv::kLog2e;
+  P.Hq = Hq;
+  P.tile_rows = rows_tile;
+  P.ways = ways;
+  P.by_item = 0;
+  // As many CTAs as the GPU holds, or as many as the batch can have tiles.
+  const long long tile = 1 << P.R.tile_log2, per = P.R.q_rows;
+  const long long items = cache->heads * (B * ((N * static_cast<long long>(group) + per - 1) / per) + (all + per - 1) / per + groups);
+  const long long most = items * ((static_cast<long long>(cache->max_pages) * cache->page_size + tile - 1) / tile);
+  const int grid = static_cast<int>(std::min<long long>(most, sms));
+  char* ws = static_cast<char*>(workspace);
+  P.shared = reinterpret_cast<int4*>(ws);
+  P.bad_groups = reinterpret_cast<int*>(ws + kSharedBytes);
+  ws += kSharedBytes + kFlagBytes;
+  P.part_ml = reinterpret_cast<float2*>(ws);
+  P.part_o = reinterpret_cast<float*>(ws + static_cast<size_t>(2) * grid * ways * 128 * 8);
+  ws += part_bytes(ways_most(D), D);
+  P.side_o = reinterpret_cast<float*>(ws);
+  P.side_ml = reinterpret_cast<float2*>(ws + static_cast<size_t>(2) * B * N * Hq * D * 4);
+  const cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+  const bool f16 = cache->dtype == SV_DTYPE_F16;
+  st = sv::launch_attend_shared(P, f16, kmap, vmap, qmap, q_tokens, grid, s);
+  if (st == SV_OK) st = sv::launch_attend_join(P, f16, grid, s);
+  if (st != SV_OK) return st;
+  return f16 ? merge<true>(P, s) : merge<false>(P, s);
+}

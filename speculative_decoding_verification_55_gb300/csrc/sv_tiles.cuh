@@ -2,6 +2,8 @@
 // copies of a tile from the pages, and the matrix instructions.
 #pragma once
 
+#include <type_traits>
+
 #include "sv_cache.cuh"
 #include "sv_common.cuh"
 
@@ -39,6 +41,73 @@ __device__ __forceinline__ long long row_units(const Round& R, const RowWork& w)
   return static_cast<long long>(w.tiles + R.extra) * w.q_tiles * R.C.heads;
 }
 
+// A batch whose rows share the fronts of their contexts: its work is that of the groups (the queries of all tokens of
+// a group's rows, N a row, against the entries that the rows share, from the first row's table), then that of the rows
+// (a row's tokens against its entries from common[b] on). A group's front is, for the masks, a row's whose last entry
+// is the round's only one: every query attends it.
+struct SharedRound : Round {
+  const int32_t* start;                   // [groups + 1]: a group's rows are start[g] .. start[g + 1] - 1
+  const int32_t* common;                  // [B]
+  int groups;
+};
+struct SharedWork : RowWork {
+  int tokens, token0;                     // query tokens, the first of them among the batch's B N
+  int table_row, page0;                   // the first entry's page: that of this row, from this one on
+};
+__device__ __forceinline__ bool front_ok(const Cache& C, int s) {
+  return s >= 0 && (s & (C.page_size - 1)) == 0 && s <= C.max_pages * C.page_size;
+}
+// False for a row in error, and for a group without a front.
+__device__ __forceinline__ bool row_work(const SharedRound& R, int v, SharedWork* w) {
+  bool ok;
+  if (v < R.groups) {
+    const int a = __ldg(R.start + v), e = __ldg(R.start + v + 1);
+    ok = a >= 0 && a < e && e <= R.B;
+    const int s = ok ? __ldg(R.common + a) : 0;
+    ok = s > 0 && front_ok(R.C, s);
+    w->n = s - 1;
+    w->m = 1;
+    w->tokens = (e - a) * R.N;
+    w->token0 = a * R.N;
+    w->table_row = a;
+    w->page0 = 0;
+  } else {
+    const int b = v - R.groups, s = __ldg(R.common + b);
+    ok = round_lengths(R.C, R.prefix, R.num, b, R.N, R.none_ok, &w->n, &w->m) && front_ok(R.C, s) && s <= w->n;
+    w->n -= s;
+    w->tokens = w->m;
+    w->token0 = b * R.N;
+    w->table_row = b;
+    w->page0 = s >> R.C.page_log2;
+  }
+  const bool some = ok && w->m > 0;
+  w->tiles = some ? (w->n + w->m + (1 << R.tile_log2) - 1) >> R.tile_log2 : 0;
+  w->q_tiles = some ? static_cast<int>((static_cast<long long>(w->tokens) * R.group + R.q_rows - 1) / R.q_rows) : 0;
+  return ok;
+}
+__device__ __forceinline__ int work_rows(const Round& R) { return R.B; }
+__device__ __forceinline__ int work_rows(const SharedRound& R) { return R.groups + R.B; }
+// What the two kinds of batches differ in: the tokens of an item's queries, their first one, the tree of its row, and
+// the table of its pages.
+template <bool kShared>
+struct Batch {
+  typedef Round Rows;
+  typedef RowWork Work;
+};
+template <>
+struct Batch<true> {
+  typedef SharedRound Rows;
+  typedef SharedWork Work;
+};
+__device__ __forceinline__ const int32_t* pages_of(const Round& R, int row, const RowWork&) {
+  return R.C.table + static_cast<size_t>(row) * R.C.max_pages;
+}
+__device__ __forceinline__ const int32_t* pages_of(const SharedRound& R, int, const SharedWork& w) {
+  return R.C.table + static_cast<size_t>(w.table_row) * R.C.max_pages + w.page0;
+}
+__device__ __forceinline__ int tokens_of(const RowWork& w) { return w.m; }
+__device__ __forceinline__ int tokens_of(const SharedWork& w) { return w.tokens; }
+
 struct Plan {
   long long total;                        // units of the batch
   long long parts;                        // CTAs with work: each of them has a unit at least
@@ -49,13 +118,14 @@ struct Plan {
 
 // Where this CTA's run begins; every thread of the CTA calls it (kThreads of them), `sh` and `plan` in
 // shared memory.
-template <int kThreads>
-__device__ void make_plan(const Round& R, long long (&sh)[kThreads / 32], Plan* plan) {
+template <int kThreads, class Rows>
+__device__ void make_plan(const Rows& R, long long (&sh)[kThreads / 32], Plan* plan) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = (R.B + kThreads - 1) / kThreads;
-  const int b0 = min(tid * per, R.B), b1 = min(b0 + per, R.B);
+  constexpr bool kShared = !std::is_same<Rows, Round>::value;
+  const int n = work_rows(R), per = (n + kThreads - 1) / kThreads;
+  const int b0 = min(tid * per, n), b1 = min(b0 + per, n);
   long long sum = 0;
-  RowWork w;
+  typename Batch<kShared>::Work w;
   for (int b = b0; b < b1; ++b) {
     row_work(R, b, &w);
     sum += row_units(R, w);
@@ -80,7 +150,7 @@ __device__ void make_plan(const Round& R, long long (&sh)[kThreads / 32], Plan* 
     plan->total = total;
     plan->parts = parts;
     plan->at = at;
-    plan->row = R.B;
+    plan->row = n;
   }
   __syncthreads();
   if (at >= before && at < before + sum) {
@@ -105,19 +175,22 @@ __device__ __forceinline__ int unit_owner(long long t, const Plan& p) {
 }
 
 // A walk over the items of this CTA's run: begin(), then next() while it returns true.
-struct Walk {
+template <bool kShared>
+struct WalkOf {
+  typedef typename Batch<kShared>::Rows Rows;
   long long at, end, row_at, item_at;     // item_at: the unit of the item's first tile
   int row, head, q_tile, first, count;    // key tiles [first, first + count) of the item
-  RowWork w;
+  typename Batch<kShared>::Work w;
 
-  __device__ __forceinline__ void begin(const Round& R, const Plan& p) {
+  __device__ __forceinline__ void begin(const Rows& R, const Plan& p) {
     at = p.at;
     end = blockIdx.x < p.parts ? p.total * (blockIdx.x + 1) / p.parts : at;
     row = p.row;
     row_at = p.row_at;
     if (at < end) row_work(R, row, &w);
   }
-  __device__ __forceinline__ bool next(const Round& R) {
+  __device__ __forceinline__ bool next(const Rows& R) {
+    typedef typename std::conditional<kShared, long long, int>::type Unit;   // (a group has any number of queries)
     do {
       if (at >= end) return false;
       while (at - row_at >= row_units(R, w)) {     // past this row: the next one with work
@@ -126,7 +199,8 @@ struct Walk {
         row_work(R, row, &w);
       }
       const int per = w.tiles + R.extra;
-      const int in_row = static_cast<int>(at - row_at), item = in_row / per, in_item = in_row - item * per;
+      const Unit in_row = static_cast<Unit>(at - row_at);
+      const int item = static_cast<int>(in_row / per), in_item = static_cast<int>(in_row - static_cast<Unit>(item) * per);
       head = item / w.q_tiles;
       q_tile = item - head * w.q_tiles;
       item_at = at - in_item + R.extra;
@@ -138,6 +212,7 @@ struct Walk {
     return true;
   }
 };
+typedef WalkOf<false> Walk;
 
 // ------------------------------------------------------------------------------------------------
 // Copies
@@ -170,9 +245,9 @@ struct TileLoader {
     const int box = (op >> halves_log2) & ((1 << boxes_log2) - 1);
     return op < ops && (tile << tile_log2) + (box << rows_log2) < entries;
   }
-  __device__ __forceinline__ int page(const Cache& C, int row, int tile, int op) const {
+  __device__ __forceinline__ int page(const Cache& C, const int32_t* pages, int tile, int op) const {
     const int box = (op >> halves_log2) & ((1 << boxes_log2) - 1);
-    return cache_page(C, row, (tile << tile_log2) + (box << rows_log2));
+    return __ldg(pages + (((tile << tile_log2) + (box << rows_log2)) >> C.page_log2));
   }
   // The copy of operation `op`: stage holds the arrays one after the other, each [D / 64][tile][64].
   __device__ __forceinline__ void load(const Cache& C, const CUtensorMap* k, const CUtensorMap* v,
@@ -193,20 +268,21 @@ constexpr int kPagesAhead = 4;
 struct PagesAhead {
   int p[kPagesAhead];
 
-  __device__ __forceinline__ void begin(const TileLoader& T, const Cache& C, int row, int first, int last,
+  // pages: the table of the row (pages_of).
+  __device__ __forceinline__ void begin(const TileLoader& T, const Cache& C, const int32_t* pages, int first, int last,
                                         int entries, int op) {
 #pragma unroll
     for (int x = 0; x < kPagesAhead; ++x)
-      p[x] = first + x < last && T.has(first + x, entries, op) ? T.page(C, row, first + x, op) : 0;
+      p[x] = first + x < last && T.has(first + x, entries, op) ? T.page(C, pages, first + x, op) : 0;
   }
   // The page of `tile`: -1 where the operation copies nothing, -2 when it is out of range. Reads that of
   // tile + kPagesAhead.
-  __device__ __forceinline__ int next(const TileLoader& T, const Cache& C, int row, int tile, int last,
+  __device__ __forceinline__ int next(const TileLoader& T, const Cache& C, const int32_t* pages, int tile, int last,
                                       int entries, int op) {
     const int now = p[0], ahead = tile + kPagesAhead;
 #pragma unroll
     for (int x = 0; x + 1 < kPagesAhead; ++x) p[x] = p[x + 1];
-    p[kPagesAhead - 1] = ahead < last && T.has(ahead, entries, op) ? T.page(C, row, ahead, op) : 0;
+    p[kPagesAhead - 1] = ahead < last && T.has(ahead, entries, op) ? T.page(C, pages, ahead, op) : 0;
     return !T.has(tile, entries, op) ? -1 : (page_ok(C, now) ? now : -2);
   }
 };

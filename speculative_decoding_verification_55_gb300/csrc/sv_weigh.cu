@@ -127,10 +127,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (!gone && W.next(R)) {
       const int entries = W.w.n + W.w.m;
       const int last = W.first + W.count;
+      const int32_t* const table = sv::pages_of(R, W.row, W.w);
       sv::PagesAhead pages;
-      pages.begin(T, C, W.row, W.first, last, entries, lane);
+      pages.begin(T, C, table, W.first, last, entries, lane);
       for (int t = W.first; t < last; ++t) {
-        const int p = pages.next(T, C, W.row, t, last, entries, lane);
+        const int p = pages.next(T, C, table, t, last, entries, lane);
         const int s = armed % kK;
         const uint32_t bar = sv::smem_addr(S.k_full + s);
         if (armed >= kK &&
