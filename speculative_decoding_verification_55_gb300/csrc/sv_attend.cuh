@@ -33,6 +33,7 @@ typedef AttendParamsOf<false> AttendParams;
 struct SharedParams : AttendParamsOf<true> {
   float* side_o;                               // [2][B N Hq][D]
   float2* side_ml;                             // [2][B N Hq] maximum and sum
+  int records;                                 // in `shared`
   int* bad_groups;                             // not 0: group_start does not ascend within 0 .. B
   __device__ __forceinline__ size_t side_at(int side, size_t at) const {
     return static_cast<size_t>(side) * R.B * R.N * Hq + at;
@@ -108,7 +109,8 @@ __device__ __forceinline__ void tell_shared(const Params& P, int way, int row, i
 
 // Joins the parts of the items that the attention kernel's `grid` CTAs shared.
 int launch_attend_join(const AttendParams& P, bool f16, bool wide, int grid, cudaStream_t st);
-int launch_attend_join(const SharedParams& P, bool f16, int grid, cudaStream_t st);
+// (items: the query tiles of fronts and rows, at most)
+int launch_attend_join(const SharedParams& P, bool f16, int grid, long long items, cudaStream_t st);
 
 // The wide kernel (at most 128 query heads a key head; query tiles of tile_rows <= 128 rows, whole tokens of
 // which q's boxes hold q_tokens; key tiles of 128, or of 64 for heads of 256; two ways up to heads of 128).

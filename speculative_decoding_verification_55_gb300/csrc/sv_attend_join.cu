@@ -17,6 +17,31 @@ namespace {
 
 constexpr int kWarps = 16, kThreads = 32 * kWarps;
 
+// The record of the k-th item that is shared, if there are so many (x < 0: no), and its place; every thread of the CTA.
+__device__ __forceinline__ int4 shared_item(const int4* records, int n, int k, int tid, int* place) {
+  __shared__ int in_warp[kWarps], found_at;
+  __shared__ int4 found;
+  const int4 e = tid < n ? __ldcg(records + tid) : make_int4(-1, 0, 0, 0);
+  const unsigned valid = __ballot_sync(sv::kFull, e.x >= 0);
+  if ((tid & 31) == 0) in_warp[tid >> 5] = __popc(valid);
+  if (tid == 0) {
+    found = make_int4(-1, 0, 0, 0);
+    found_at = 0;
+  }
+  __syncthreads();
+  int before = __popc(valid & ((1u << (tid & 31)) - 1));
+  for (int w = 0; w < (tid >> 5); ++w) before += in_warp[w];
+  if (e.x >= 0 && before == k) {
+    found = e;
+    found_at = tid;
+  }
+  __syncthreads();
+  *place = found_at;
+  return found;
+}
+constexpr int kMaxRecords = 320;
+static_assert(kMaxRecords <= kThreads, "a thread a record");
+
 // kAcross: warps across the columns. kShared: of rows that share fronts, to the sides of their queries.
 template <bool F16, int D, int kRows, int kAcross, int kCols, bool kShared>
 __global__ void __launch_bounds__(kThreads) sv_attend_join_kernel(const sv::ParamsOf<kShared> P) {
@@ -41,7 +66,16 @@ __global__ void __launch_bounds__(kThreads) sv_attend_join_kernel(const sv::Para
   }
   int4 it;                                             // row, head, query tile, the last CTA
   int c0, way, rows;
-  if constexpr (kCols == 8) {                          // records by item; the lengths were there before the attention
+  if constexpr (kShared && kCols == 8) {               // few items with many parts: a CTA a possible one
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    int place;
+    it = shared_item(P.shared, P.records, blockIdx.x, tid, &place);
+    if (it.x < 0) return;
+    c0 = place / P.ways;
+    way = place % P.ways;
+    rows = it.z & 255;
+    it.z >>= 8;
+  } else if constexpr (kCols == 8) {                   // records by item; the lengths were there before the attention
     const int id = blockIdx.x, pair = id / P.by_item;
     it = make_int4(pair / R.C.heads, pair % R.C.heads, id % P.by_item, 0);
     way = it.z % P.ways;
@@ -120,7 +154,7 @@ __global__ void __launch_bounds__(kThreads) sv_attend_join_kernel(const sv::Para
   if constexpr (kShared) {
     float* o = P.side_o + P.side_at(it.x & 1, at) * D + col0 + first;
 #pragma unroll
-    for (int x = 0; x < kAcross; x += 4) *reinterpret_cast<float4*>(o + x) = make_float4(v[x], v[x + 1], v[x + 2], v[x + 3]);
+    for (int x = 0; x < kAcross; ++x) o[x] = v[x];
     if (col0 + first == 0) P.side_ml[P.side_at(it.x & 1, at)] = make_float2(M, L);
     return;
   }
@@ -179,15 +213,17 @@ int launch_attend_join(const AttendParams& P, bool f16, bool wide, int grid,
   }
 }
 
-template <bool F16>
-int launch_shared(const SharedParams& P, int grid, cudaStream_t st) {
-  const int blocks = grid * P.ways;
-  if (P.R.C.head_dim == 64) return launch2<F16, 64, 128, 4, 16, true>(P, blocks, st);
-  if (P.R.C.head_dim == 128) return launch2<F16, 128, 128, 8, 16, true>(P, blocks, st);
-  return launch2<F16, 256, 128, 16, 16, true>(P, blocks, st);
+template <bool F16, int D>
+int launch_shared(const SharedParams& P, int grid, long long items, cudaStream_t st) {
+  return items * 4 <= grid ? launch2<F16, D, 128, 1, 8, true>(P, static_cast<int>(items), st)
+                           : launch2<F16, D, 128, D / 16, 16, true>(P, grid * P.ways, st);
 }
-int launch_attend_join(const SharedParams& P, bool f16, int grid, cudaStream_t st) {
-  return f16 ? launch_shared<true>(P, grid, st) : launch_shared<false>(P, grid, st);
+int launch_attend_join(const SharedParams& P, bool f16, int grid, long long items, cudaStream_t st) {
+  if (P.records > kMaxRecords) return SV_ERR_CUDA;
+  const int D = P.R.C.head_dim;
+  if (D == 64) return f16 ? launch_shared<true, 64>(P, grid, items, st) : launch_shared<false, 64>(P, grid, items, st);
+  if (D == 128) return f16 ? launch_shared<true, 128>(P, grid, items, st) : launch_shared<false, 128>(P, grid, items, st);
+  return f16 ? launch_shared<true, 256>(P, grid, items, st) : launch_shared<false, 256>(P, grid, items, st);
 }
 
 }  // namespace sv

@@ -201,10 +201,12 @@ extern "C" int spec_verify_shared_attention(const void* q, int64_t q_row_stride,
   P.ways = ways;
   P.by_item = 0;
   // As many CTAs as the GPU holds, or as many as the batch can have tiles.
-  const long long tile = 1 << P.R.tile_log2, per = P.R.q_rows;
-  const long long items = cache->heads * (B * ((N * static_cast<long long>(group) + per - 1) / per) + (all + per - 1) / per + groups);
+  const long long tile = 1 << P.R.tile_log2;
+  const long long own = static_cast<long long>(B) * ((N * group + rows_tile - 1) / rows_tile);
+  const long long items = cache->heads * (own + all / rows_tile + std::min<long long>(groups, all));   // query tiles
   const long long most = items * ((static_cast<long long>(cache->max_pages) * cache->page_size + tile - 1) / tile);
   const int grid = static_cast<int>(std::min<long long>(most, sms));
+  P.records = grid * ways;
   char* ws = static_cast<char*>(workspace);
   P.shared = reinterpret_cast<int4*>(ws);
   P.bad_groups = reinterpret_cast<int*>(ws + kSharedBytes);
@@ -217,7 +219,7 @@ extern "C" int spec_verify_shared_attention(const void* q, int64_t q_row_stride,
   const cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   const bool f16 = cache->dtype == SV_DTYPE_F16;
   st = sv::launch_attend_shared(P, f16, kmap, vmap, qmap, q_tokens, grid, s);
-  if (st == SV_OK) st = sv::launch_attend_join(P, f16, grid, s);
+  if (st == SV_OK) st = sv::launch_attend_join(P, f16, grid, items, s);
   if (st != SV_OK) return st;
   return f16 ? merge<true>(P, s) : merge<false>(P, s);
 }

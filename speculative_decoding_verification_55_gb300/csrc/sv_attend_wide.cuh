@@ -85,7 +85,9 @@ constexpr int kSmemBytes = Shape<D, kWays>::kSlots * Shape<D, kWays>::kSlotBytes
                            sizeof(Control<Shape<D, kWays>::kSlots>);
 
 // kShared: a batch whose rows share the fronts of their contexts (SharedRound); an item's whole result then goes to
-// its side, as a part's would.
+// its side, as a part's would. Where two ways are for the fronts' many queries, an item of one query tile (a row's own
+// entries) has its key tiles in turn on both, each with a maximum, a sum and an accumulator of its own, which meet at the
+// end: a tile's chain of S, softmax, P V and the next S takes longer than its bytes from HBM.
 template <bool F16, int D, int kWays, bool kShared>
 __global__ void __launch_bounds__(kThreads, 1)
     sv_attend_wide_kernel(const ParamsOf<kShared> P, const __grid_constant__ CUtensorMap kmap,
@@ -125,6 +127,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tm = S.tm;
   volatile int* const lost = &S.lost;
 
+  constexpr bool kSplit = kShared && kWays == 2;
+  auto one_tile = [&](const Item& I) { return I.tokens * R.group - I.q_tile * kWays * P.tile_rows <= P.tile_rows; };
   // The next item's description. The items' warp always tells an end, however its own waits end: this wait is longer than
   // they can be, so that all warps know of the same items and meet at the same barriers.
   auto told = [&](int k) {
@@ -242,19 +246,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       } pk{0, 0u}, pv{1, 0u};
-      uint32_t ws = 0, wp = 0, turn = 0;                 // score buffers next written and next read, and its phase
+      uint32_t ws = 0, wp = 0, turn = 0;                 // score buffers next written and next read, and its phase (a bit a way)
       int items = 0, left = 0;                           // left: score products of the item still to come
+      bool split = false;                                // the item's tiles are on both ways in turn
       auto scores = [&](int way) {
-        if (way == 0 && !wait_unless_lost(full + 8 * pk.slot, pk.phase, lost)) return;
+        if ((way == 0 || split) && !wait_unless_lost(full + 8 * pk.slot, pk.phase, lost)) return;
         fence_after();
         const uint32_t w = kWays == 2 ? way : ws;
-        const Matrix km = ring_k.at(pk.slot * H::kSlotBytes), qm = queries.at(way * (kRows * D * 2));
+        const Matrix km = ring_k.at(pk.slot * H::kSlotBytes), qm = queries.at(split ? 0 : way * (kRows * D * 2));
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
           product_ss(tm + w * kTile, qm.at((k >> 2) * (kRows * 128) + (k & 3) * 32),
                      km.at((k >> 2) * (kTile * 128) + (k & 3) * 32), ds, k > 0);
         products_done(s_full + 8 * w);
-        if (way + 1 < kWays) return;
+        if (way + 1 < kWays && !split) return;
         products_done(empty + 8 * pk.slot);
         pk.step();
         ws ^= 1;
@@ -262,28 +267,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       constexpr int kAhead = kWays == 2 ? 1 : kScores;
       for (;;) {
-        const int count = told(items).count;
+        const Item I = told(items);
+        const int count = I.count;
+        split = kSplit && one_tile(I);
         if (count == 0 || !wait_unless_lost(sv::smem_addr(&S.q_full), items & 1, lost)) break;
         left = count;
-        for (int idx = 0; idx < count && idx < kAhead; ++idx)
-          for (int way = 0; way < kWays; ++way) scores(way);
-        for (int idx = 0; idx < count; ++idx) {
-          if (!wait_unless_lost(full + 8 * pv.slot, pv.phase, lost)) break;
+        for (int idx = -kAhead; idx < count; ++idx) {      // (below 0: the first score products alone)
+          if (idx >= 0 && !wait_unless_lost(full + 8 * pv.slot, pv.phase, lost)) break;
           const Matrix vm = ring_v.at(pv.slot * H::kSlotBytes);
-#pragma unroll
+#pragma unroll 1
           for (int way = 0; way < kWays; ++way) {
-            const uint32_t w = kWays == 2 ? way : wp;
-            if (!wait_unless_lost(p_ready + 8 * w, turn, lost)) break;
-            fence_after();
+            if (idx >= 0) {
+              if (split && way != (idx & 1)) continue;
+              const uint32_t w = kWays == 2 ? way : wp;
+              if (!wait_unless_lost(p_ready + 8 * w, kWays == 2 ? turn >> way & 1 : turn, lost)) break;
+              fence_after();
 #pragma unroll
-            for (int k = 0; k < kTile / 16; ++k)
-              product_ts(tm + kAccum + way * D, tm + w * kTile + k * 8, vm.at(k * 2048), dp, idx > 0 || k > 0);
-            if (way + 1 == kWays) products_done(empty + 8 * pv.slot);
+              for (int k = 0; k < kTile / 16; ++k)
+                product_ts(tm + kAccum + way * D, tm + w * kTile + k * 8, vm.at(k * 2048), dp, idx > (split ? 1 : 0) || k > 0);
+              if (way + 1 == kWays || split) products_done(empty + 8 * pv.slot);
+              if (kWays == 2) turn ^= 1u << way;
+            }
             if (left > 0) scores(way);
           }
+          if (idx < 0) continue;
           pv.step();
           wp ^= 1;
-          if (kWays == 2 || wp == 0) turn ^= 1u;
+          if (kWays == 1 && wp == 0) turn ^= 1u;
         }
         if (*lost) break;
         products_done(sv::smem_addr(&S.o_full));
@@ -299,12 +309,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>(32 * wq) << 16;
     const uint32_t to = tm + lanes + kAccum + way * D + half * H::kOut;
     const float c = P.c;
-    int base = 0, items = 0;
+    int base = 0, used = 0, items = 0;          // tiles before the item: the CTA's, and (two ways) this way's
     for (;;) {
       const Item W = told(items);
       if (W.count == 0) break;
+      const bool split = kSplit && one_tile(W);
       const int n = W.n, m = W.m, entries = n + m;
-      const int row0 = (W.q_tile * kWays + way) * P.tile_rows, rows = min(P.tile_rows, W.tokens * R.group - row0);
+      const int row0 = (W.q_tile * kWays + (split ? 0 : way)) * P.tile_rows, rows = min(P.tile_rows, W.tokens * R.group - row0);
       if (tid == 0) S.flags = 0;                // nobody sets one before this thread's first tile is used
       const int last = W.first + W.count;
       int side = 0;
@@ -326,9 +337,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       float mx = -INFINITY, l = 0.0f;
       bool odd = false;
 
-      for (int idx = 0; idx < W.count; ++idx) {
+      for (int idx = split ? way : 0; idx < W.count; idx += split ? 2 : 1) {
         const int x = base + idx, s = (2 * x + 1) % kSlots;
-        const int w = kWays == 2 ? way : x % kScores, turn = kWays == 2 ? x : x / kScores;
+        const int w = kWays == 2 ? way : x % kScores, turn = kWays == 2 ? used++ : x / kScores;
         const int j0 = (W.first + idx) * kTile;
         const bool edge = j0 + kTile > n;      // entries of the round itself, or behind the last
         bool go = wait_unless_lost(sv::smem_addr(S.s_full + w), turn & 1, lost);
@@ -353,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!(((z < 32 ? lo : hi) >> (z & 31)) & 1)) sc[z] = 0xff800000u;
           };
           float v[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
+#pragma unroll 1
           for (int y = 0; y < H::kCols; y += H::kChunk) {
             load(y);
 #pragma unroll
@@ -371,12 +382,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float f = !grew ? 1.0f : (mx == -INFINITY ? 0.0f : sv::ex2((mx - top) * c));
             if (grew) mx = top;
             l *= f;
-            if (idx > 0) {                     // the products with the tiles before are done
-              const int e = 2 * x - 1;
-              wait_unless_lost(sv::smem_addr(S.empty + e % kSlots), (e / kSlots) & 1, lost);
+            if (idx > (split ? 1 : 0)) {       // the products with the tiles before are done
+              if (!split) {                    // (split: they were issued before this tile's scores)
+                const int e = 2 * x - 1;
+                wait_unless_lost(sv::smem_addr(S.empty + e % kSlots), (e / kSlots) & 1, lost);
+              }
               __syncwarp();
               fence_after();
-#pragma unroll
+#pragma unroll 1
               for (int y = 0; y < H::kOut; y += 16) {
                 uint32_t o[16];
                 tm_load16(o, to + y);
@@ -389,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float m0 = mx == -INFINITY ? 0.0f : mx, b = F16 ? kBits : -m0 * c;
           const sv::f32x2 m2 = sv::pk(m0, m0), c2 = sv::pk(c, c), b2 = sv::pk(b, b);
           sv::f32x2 sum[2] = {sv::pk(0.0f, 0.0f), sv::pk(0.0f, 0.0f)};
-#pragma unroll
+#pragma unroll 1
           for (int y = 0; y < H::kCols; y += H::kChunk) {
             if (H::kCols > H::kChunk) load(y);   // read again: all of a row would not fit the registers
             uint32_t p[H::kChunk / 2];
@@ -416,8 +429,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           // entry are cleared whole.
           unsigned char* vb = dyn + s * H::kSlotBytes;
           const int r0 = max(n - j0, 0);
-          // (Two ways: the first way's warps, whose product comes first.)
-          for (int y = r0 * (D / 8) + tid; way == 0 && y < kTile * (D / 8); y += kSoft / kWays) {
+          // (Two ways: the first way's warps, whose product comes first, or those that have the tile.)
+          for (int y = r0 * (D / 8) + tid % (kSoft / kWays); (way == 0 || split) && y < kTile * (D / 8); y += kSoft / kWays) {
             const int r = y / (D / 8), ch = y % (D / 8);
             uint4* at = reinterpret_cast<uint4*>(vb + (ch >> 3) * (kTile * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
             uint4 v = make_uint4(0u, 0u, 0u, 0u);
@@ -450,23 +463,47 @@ __global__ void __launch_bounds__(kThreads, 1)
       // One way: a row's sum is that of its two threads; each finishes half of the row's columns.
       float* sums = &S.row_max[0][0][0];       // [2][kRows]; the tiles are done with it
       if (kWays == 1) sums[half * kRows + row] = l;
+      if (kSplit && split) {
+        S.row_max[0][way][row] = l;
+        S.row_max[1][way][row] = mx;
+      }
       sv::named_bar_sync(1, kSoft);
       const int flags = S.flags;
+      // Split: what the two ways' accumulators are multiplied by.
+      float f0 = 1.0f, f1 = 0.0f;
+      if (kSplit && split) {
+        const float m0 = S.row_max[1][0][row], m1 = S.row_max[1][1][row];
+        mx = fmaxf(m0, m1);
+        f0 = m0 == -INFINITY ? 0.0f : sv::ex2((m0 - mx) * c);
+        f1 = m1 == -INFINITY ? 0.0f : sv::ex2((m1 - mx) * c);
+        const float l0 = S.row_max[0][0][row], l1 = S.row_max[0][1][row];
+        l = (m0 == -INFINITY ? l0 : l0 * f0) + (m1 == -INFINITY ? l1 : l1 * f1);   // (the former: 0, or NaN)
+      }
       const float jl = (flags & 1) ? __int_as_float(0x7fffffff) : (kWays == 1 ? sums[row] + sums[kRows + row] : l);
       const bool whole = W.count == W.tiles;
-      const int slot = (2 * blockIdx.x + (W.first == 0 ? 1 : 0)) * kWays + way;
+      const int slot = (2 * blockIdx.x + (W.first == 0 ? 1 : 0)) * kWays + (split ? 0 : way);
       const int i = (row0 + row) / R.group, hq = W.head * R.group + (row0 + row) - i * R.group;
       const size_t at = (static_cast<size_t>(kShared ? W.token0 : W.row * static_cast<size_t>(R.N)) + i) * P.Hq + hq;
       const float inv = 1.0f / jl;
-#pragma unroll
+#pragma unroll 1
       for (int k = 0; k < H::kOut; k += 16) {
-        if (!active) break;
-        const int mycol = half * H::kOut + k;
+        if (!active || (split && k >= D / 2)) break;
+        // Split: each way's thread of a row finishes half of its columns.
+        const int mycol = split ? way * (D / 2) + k : half * H::kOut + k;
         uint32_t o[16];
-        tm_load16(o, to + k);
+        tm_load16(o, split ? tm + lanes + kAccum + mycol : to + k);
         float f[16];
 #pragma unroll
         for (int z = 0; z < 16; ++z) f[z] = __uint_as_float(o[z]);
+        if (kSplit && split) {
+#pragma unroll
+          for (int z = 0; z < 16; ++z) f[z] *= f0;
+          if (W.count > 1) {                   // (else the second way's accumulator holds something else)
+            tm_load16(o, tm + lanes + kAccum + D + mycol);
+#pragma unroll
+            for (int z = 0; z < 16; ++z) f[z] += __uint_as_float(o[z]) * f1;
+          }
+        }
         // Values that are not finite were left out of the products, where a zero probability would have
         // made NaN of them: they are added to the rows that attend them.
         if (flags & 2) {
@@ -509,14 +546,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (half == 0 && row < rows) {
+      if (half == 0 && row < rows && !(split && way == 1)) {
         if (!whole) P.part_ml[slot * kRows + row] = make_float2(mx, jl);
         else if constexpr (kShared) P.side_ml[P.side_at(side, at)] = make_float2(mx, jl);
         else if (P.lse) P.lse[at] = (mx * c + (log2f(jl) - kBits)) * 0.6931471805599453f;
       }
       fence_before();
       sv::named_bar_sync(1, kSoft);            // the sums have been read
-      if ((tid & 127) == 0 && half == 0 && W.first == 0 && rows > 0)
+      if ((tid & 127) == 0 && half == 0 && W.first == 0 && rows > 0 && !(split && way == 1))
         sv::tell_shared(P, way, kShared ? 2 * W.token0 + side : W.row, W.head, W.q_tile * kWays + way, rows, whole, W.item_at,
                         W.tiles, S.plan);
     }
@@ -535,6 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     sv::WalkOf<kShared> W;
     W.begin(R, S.plan);
     while (W.next(R))
+#pragma unroll 1
       for (int way = 0; way < kWays; ++way) {
         const int q_tile = W.q_tile * kWays + way, row0 = q_tile * P.tile_rows;
         const int rows = min(P.tile_rows, sv::tokens_of(W.w) * R.group - row0);
@@ -545,6 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           token0 = W.w.token0;
           tell = 2 * W.w.token0 + (W.row >= R.groups);
         }
+#pragma unroll 1
         for (int x = tid; x < rows * D; x += kThreads) {
           const int r = x / D, i = (row0 + r) / R.group, hq = W.head * R.group + (row0 + r) - i * R.group;
           const size_t at = (token0 + i) * P.Hq + hq;

@@ -317,18 +317,21 @@ constexpr int kSpinLimit = SV_SPIN_LIMIT;
 constexpr int kDrainLimit = 1 << 26;
 
 __device__ __forceinline__ bool mbar_wait_drain(uint32_t bar, uint32_t parity) {
+#pragma unroll 1
   for (int n = 0; n < kDrainLimit; ++n)
     if (mbar_try_wait(bar, parity)) return true;
   return false;
 }
 
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
+#pragma unroll 1
   for (int n = 0; n < kSpinLimit; ++n)
     if (mbar_try_wait(bar, parity)) return true;
   return false;
 }
 
 __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity) {
+#pragma unroll 1
   for (int n = 0; n < kSpinLimit; ++n)
     if (mbar_try_wait_cluster(bar, parity)) return true;
   return false;

@@ -126,6 +126,7 @@ __device__ void make_plan(const Rows& R, long long (&sh)[kThreads / 32], Plan* p
   const int b0 = min(tid * per, n), b1 = min(b0 + per, n);
   long long sum = 0;
   typename Batch<kShared>::Work w;
+#pragma unroll 1
   for (int b = b0; b < b1; ++b) {
     row_work(R, b, &w);
     sum += row_units(R, w);
@@ -155,6 +156,7 @@ __device__ void make_plan(const Rows& R, long long (&sh)[kThreads / 32], Plan* p
   __syncthreads();
   if (at >= before && at < before + sum) {
     long long run = before;
+#pragma unroll 1
     for (int b = b0; b < b1; ++b) {
       row_work(R, b, &w);
       const long long t = row_units(R, w);
