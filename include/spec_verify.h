@@ -376,11 +376,12 @@ int spec_verify_paged_attention(const void* q, int64_t q_row_stride, int64_t q_t
  * group_start    [groups + 1] int32, ascending from at least 0 to at most B: group g is rows group_start[g] ..
  *                group_start[g + 1] - 1 (it may be empty). Rows in no group have shared_len 0.
  * workspace      spec_verify_shared_attention_workspace_size(...) bytes, 256-byte aligned, without setup: among them two
- *                fp32 results of each query, 8 B N Hq (D + 2) bytes.
+ *                fp32 results of each query, 8 B N Hq (D + 2) bytes. One workspace serves one call at a time.
  * A row whose shared_len is none of that is in error; all are where group_start does not ascend within 0 .. B. A page
  * number out of range in a front puts NaN into the outputs of all its rows' tokens.
- * B N Hq <= 2^28. Three launches. Other arguments, errors and limits as in spec_verify_paged_attention. */
-size_t spec_verify_shared_attention_workspace_size(int32_t B, int32_t N, int32_t Hq, const sv_paged_cache* cache);
+ * B N Hq <= 2^28. Two launches. Other arguments, errors and limits as in spec_verify_paged_attention. */
+size_t spec_verify_shared_attention_workspace_size(int32_t B, int32_t N, int32_t Hq, int32_t groups,
+                                                   const sv_paged_cache* cache);
 int spec_verify_shared_attention(const void* q, int64_t q_row_stride, int64_t q_token_stride,
                                  const sv_paged_cache* cache, const int32_t* prefix_len,
                                  const int32_t* shared_len, const int32_t* group_start, int32_t groups,

@@ -108,7 +108,7 @@ def lib() -> ctypes.CDLL:
             L.spec_verify_shared_attention.argtypes = [vp, i64, i64, vp, i32p, i32p, i32p, i32, i32p, i32p,
                                                        ctypes.c_float, vp, f32p, i32, i32, i32, vp, sz, vp]
             L.spec_verify_shared_attention.restype = ctypes.c_int
-            L.spec_verify_shared_attention_workspace_size.argtypes = [i32, i32, i32, vp]
+            L.spec_verify_shared_attention_workspace_size.argtypes = [i32, i32, i32, i32, vp]
             L.spec_verify_shared_attention_workspace_size.restype = sz
             L.spec_verify_kv_weights.argtypes = [vp, i64, i64, f32p, vp, i32p, i32p, i32p, ctypes.c_float,
                                                  i32, i32, i32, vp]

@@ -188,8 +188,8 @@ def spec_verify_kv_evict(cache, length, budget, recent, out_len, stream=None) ->
           budget, recent, _small(out_len, "out_len", torch.int32, (B,), dev), B)
 
 
-def spec_verify_shared_attention_workspace_size(B: int, N: int, Hq: int, cache: PagedCache) -> int:
-    return int(lib().spec_verify_shared_attention_workspace_size(B, N, Hq, cache.ref))
+def spec_verify_shared_attention_workspace_size(B: int, N: int, Hq: int, groups: int, cache: PagedCache) -> int:
+    return int(lib().spec_verify_shared_attention_workspace_size(B, N, Hq, groups, cache.ref))
 
 
 def _starts(group_start, device):
@@ -231,19 +231,19 @@ def spec_verify_shared_attention(q, cache, prefix_len, shared_len, group_start, 
 
 
 _attend_ws = {}
-# A call makes two or three launches on its stream's workspace: another thread's must not come in between.
+# A call makes two launches on its stream's workspace: another thread's must not come in between.
 _attend_lock = threading.Lock()
 
 
-def _attend_workspace(N, Hq, cache, shared=False):
+def _attend_workspace(N, Hq, cache, groups=0):
     """A workspace cached per (device, current stream) and grown on demand. A call that is being captured
     gets one of its own: replays of two graphs may overlap."""
     import torch
-    need = cache.workspace_need.get((N, Hq, shared))
+    need = cache.workspace_need.get((N, Hq, groups))
     if need is None:
-        need = spec_verify_shared_attention_workspace_size(cache.B, N, Hq, cache) if shared \
+        need = spec_verify_shared_attention_workspace_size(cache.B, N, Hq, groups, cache) if groups \
             else spec_verify_paged_attention_workspace_size(N, Hq, cache)
-        cache.workspace_need[N, Hq, shared] = need
+        cache.workspace_need[N, Hq, groups] = need
     if torch.cuda.is_current_stream_capturing():
         return torch.empty(need, dtype=torch.uint8, device=cache.device)
     key = (cache.device, _raw_stream(None, cache.device))
@@ -288,7 +288,7 @@ def attend_shared(q, cache, prefix_len, shared_len, group_start, num_queries=Non
     out = torch.empty((cache.B, N, Hq, cache.head_dim), dtype=q.dtype, device=cache.device)
     lse = torch.empty((cache.B, N, Hq), dtype=torch.float32, device=cache.device)
     with _attend_lock:
-        ws = _attend_workspace(N, Hq, cache, shared=True)
+        ws = _attend_workspace(N, Hq, cache, _starts(group_start, cache.device)[1])
         _shared_attention(q, cache, prefix_len, shared_len, group_start, num_queries, tree_parents, N, Hq, rs, ts,
                           out.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.nbytes, scale, None)
     return out, lse

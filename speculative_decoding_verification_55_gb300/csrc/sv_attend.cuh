@@ -28,15 +28,29 @@ struct AttendParamsOf {
 };
 typedef AttendParamsOf<false> AttendParams;
 
-// Of rows that share fronts: an item's result, whole or joined, is a side of its queries' (0: the fronts', 1: the rows'
-// own entries'), which the merge kernel puts together. A record of `shared` has 2 x the first token + the side as its row.
+// Of rows that share fronts. An item's result, of a query tile of 128 rows, is sums, a maximum and a sum of weights a
+// row: where a CTA has all of it, at its queries' place on a side (0: the fronts', 1: the rows' own entries'), else in a
+// part each of the CTAs that share it. Every item leaves a record; the merge kernel puts the parts and sides of each
+// query together.
 struct SharedParams : AttendParamsOf<true> {
   float* side_o;                               // [2][B N Hq][D]
   float2* side_ml;                             // [2][B N Hq] maximum and sum
-  int records;                                 // in `shared`
+  int2* records;                               // (by record_at) first and last CTA; first -1: one CTA has all of it
   int* bad_groups;                             // not 0: group_start does not ascend within 0 .. B
+  int own_tiles, front_tiles;                  // records of a row's key head; of the fronts' key head
   __device__ __forceinline__ size_t side_at(int side, size_t at) const {
     return static_cast<size_t>(side) * R.B * R.N * Hq + at;
+  }
+  // The rows' records, then the fronts': group g, whose first token is token0, has its from token0 x group / tile_rows
+  // + g on (its last query tile may be short, which the + g makes up for).
+  __device__ __forceinline__ size_t record_at(int row, int head, int q_tile, int token0) const {
+    const size_t own = static_cast<size_t>(R.B) * R.C.heads * own_tiles;
+    if (row >= R.groups) return (static_cast<size_t>(row - R.groups) * R.C.heads + head) * own_tiles + q_tile;
+    return own + static_cast<size_t>(head) * front_tiles + token0 * R.group / tile_rows + row + q_tile;
+  }
+  // Row r of a part, among all of them ([2 grid][ways][128]): the part of CTA p in an item that begins in CTA first.
+  __device__ __forceinline__ size_t part_row(int p, int first, int way, int r) const {
+    return (static_cast<size_t>(2 * p + (p == first)) * ways + way) * 128 + r;
   }
 };
 template <bool kShared>
@@ -96,8 +110,7 @@ __device__ __forceinline__ void fill_unused(const AttendParams& P, int D, int ti
 }
 
 // The item that this CTA begins, for the join kernel (one thread).
-template <class Params>
-__device__ __forceinline__ void tell_shared(const Params& P, int way, int row, int head, int q_tile, int rows,
+__device__ __forceinline__ void tell_shared(const AttendParams& P, int way, int row, int head, int q_tile, int rows,
                                             bool whole, long long item_at, int tiles, const Plan& plan) {
   if (whole && !P.by_item) return;
   const int cta = blockIdx.x, last = unit_owner(item_at + tiles - 1, plan);
@@ -106,11 +119,14 @@ __device__ __forceinline__ void tell_shared(const Params& P, int way, int row, i
   else
     P.shared[cta * P.ways + way] = make_int4(row, head, q_tile << 8 | rows, last);
 }
+__device__ __forceinline__ void tell_shared(const SharedParams& P, int row, int head, int q_tile, int token0, bool whole,
+                                            long long item_at, int tiles, const Plan& plan) {
+  P.records[P.record_at(row, head, q_tile, token0)] =
+      make_int2(whole ? -1 : static_cast<int>(blockIdx.x), whole ? 0 : unit_owner(item_at + tiles - 1, plan));
+}
 
 // Joins the parts of the items that the attention kernel's `grid` CTAs shared.
 int launch_attend_join(const AttendParams& P, bool f16, bool wide, int grid, cudaStream_t st);
-// (items: the query tiles of fronts and rows, at most)
-int launch_attend_join(const SharedParams& P, bool f16, int grid, long long items, cudaStream_t st);
 
 // The wide kernel (at most 128 query heads a key head; query tiles of tile_rows <= 128 rows, whole tokens of
 // which q's boxes hold q_tokens; key tiles of 128, or of 64 for heads of 256; two ways up to heads of 128).

@@ -17,65 +17,18 @@ namespace {
 
 constexpr int kWarps = 16, kThreads = 32 * kWarps;
 
-// The record of the k-th item that is shared, if there are so many (x < 0: no), and its place; every thread of the CTA.
-__device__ __forceinline__ int4 shared_item(const int4* records, int n, int k, int tid, int* place) {
-  __shared__ int in_warp[kWarps], found_at;
-  __shared__ int4 found;
-  const int4 e = tid < n ? __ldcg(records + tid) : make_int4(-1, 0, 0, 0);
-  const unsigned valid = __ballot_sync(sv::kFull, e.x >= 0);
-  if ((tid & 31) == 0) in_warp[tid >> 5] = __popc(valid);
-  if (tid == 0) {
-    found = make_int4(-1, 0, 0, 0);
-    found_at = 0;
-  }
-  __syncthreads();
-  int before = __popc(valid & ((1u << (tid & 31)) - 1));
-  for (int w = 0; w < (tid >> 5); ++w) before += in_warp[w];
-  if (e.x >= 0 && before == k) {
-    found = e;
-    found_at = tid;
-  }
-  __syncthreads();
-  *place = found_at;
-  return found;
-}
-constexpr int kMaxRecords = 320;
-static_assert(kMaxRecords <= kThreads, "a thread a record");
-
-// kAcross: warps across the columns. kShared: of rows that share fronts, to the sides of their queries.
-template <bool F16, int D, int kRows, int kAcross, int kCols, bool kShared>
-__global__ void __launch_bounds__(kThreads) sv_attend_join_kernel(const sv::ParamsOf<kShared> P) {
+template <bool F16, int D, int kRows, int kAcross, int kCols>    // kAcross: warps across the columns
+__global__ void __launch_bounds__(kThreads) sv_attend_join_kernel(const sv::AttendParams P) {
   constexpr int kRowLanes = kRows < 32 ? kRows : 32, kColLanes = 32 / kRowLanes;
   constexpr int kPartGroups = kWarps / kAcross, kColsHere = kAcross * kColLanes * kCols;
   constexpr int kColBlocks = D / kColsHere;
   __shared__ float acc[kWarps][kCols][33];
   __shared__ float2 ml[kWarps][32];
-  const auto& R = P.R;
+  const sv::Round& R = P.R;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if constexpr (kShared) {
-    asm volatile("griddepcontrol.launch_dependents;");   // the merge kernel's CTAs, which wait for this grid's end
-    if (blockIdx.x == 0 && blockIdx.y == 0) {  // (the attention kernel takes no group that is out of range)
-      bool bad = false;
-      for (int g = tid; g <= R.groups; g += kThreads) {
-        const int s = __ldg(R.start + g);
-        bad |= s > R.B || (g == 0 ? s < 0 : __ldg(R.start + g - 1) > s);
-      }
-      bad = __syncthreads_or(bad);
-      if (tid == 0) *P.bad_groups = bad;
-    }
-  }
   int4 it;                                             // row, head, query tile, the last CTA
   int c0, way, rows;
-  if constexpr (kShared && kCols == 8) {               // few items with many parts: a CTA a possible one
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    int place;
-    it = shared_item(P.shared, P.records, blockIdx.x, tid, &place);
-    if (it.x < 0) return;
-    c0 = place / P.ways;
-    way = place % P.ways;
-    rows = it.z & 255;
-    it.z >>= 8;
-  } else if constexpr (kCols == 8) {                   // records by item; the lengths were there before the attention
+  if (kCols == 8) {                                    // records by item; the lengths were there before the attention
     const int id = blockIdx.x, pair = id / P.by_item;
     it = make_int4(pair / R.C.heads, pair % R.C.heads, id % P.by_item, 0);
     way = it.z % P.ways;
@@ -142,21 +95,14 @@ __global__ void __launch_bounds__(kThreads) sv_attend_join_kernel(const sv::Para
   }
   const float inv = 1.0f / L;
   const int i = (row0 + g0 + r) / R.group, hq = it.y * R.group + (row0 + g0 + r) - i * R.group;
-  const size_t at = (kShared ? static_cast<size_t>(it.x >> 1) + i : static_cast<size_t>(it.x) * R.N + i) * P.Hq + hq;
+  const size_t at = (static_cast<size_t>(it.x) * R.N + i) * P.Hq + hq;
 #pragma unroll
   for (int x = 0; x < kAcross; ++x) {
     const int col = first + x, wc = col / (kColLanes * kCols), cl = (col / kCols) % kColLanes;
     float s = 0.0f;
 #pragma unroll
     for (int g = 0; g < kPartGroups; ++g) s += acc[g * kAcross + wc][col % kCols][cl * kRowLanes + r] * f[g];
-    v[x] = kShared ? s : s * inv;
-  }
-  if constexpr (kShared) {
-    float* o = P.side_o + P.side_at(it.x & 1, at) * D + col0 + first;
-#pragma unroll
-    for (int x = 0; x < kAcross; ++x) o[x] = v[x];
-    if (col0 + first == 0) P.side_ml[P.side_at(it.x & 1, at)] = make_float2(M, L);
-    return;
+    v[x] = s * inv;
   }
   char* out = static_cast<char*>(P.out) + (at * D + col0 + first) * 2;
   if constexpr (kAcross == 1) {
@@ -169,10 +115,10 @@ __global__ void __launch_bounds__(kThreads) sv_attend_join_kernel(const sv::Para
   if (P.lse && col0 + first == 0) P.lse[at] = (M * c + (log2f(L) - sv::kProbBits<F16, kRows == 128>)) * 0.6931471805599453f;
 }
 
-template <bool F16, int D, int kRows, int kAcross, int kCols, bool kShared>
-int launch2(const sv::ParamsOf<kShared>& P, int blocks, cudaStream_t st) {
+template <bool F16, int D, int kRows, int kAcross, int kCols>
+int launch2(const sv::AttendParams& P, int blocks, cudaStream_t st) {
   constexpr int kRowLanes = kRows < 32 ? kRows : 32, kColsHere = kAcross * (32 / kRowLanes) * kCols;
-  const int most = min(kRows, (kShared ? P.R.B : 1) * P.R.N * P.R.group);
+  const int most = min(kRows, P.R.N * P.R.group);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(blocks, (most + kRowLanes - 1) / kRowLanes * (D / kColsHere));
   cfg.blockDim = dim3(kThreads);
@@ -182,7 +128,7 @@ int launch2(const sv::ParamsOf<kShared>& P, int blocks, cudaStream_t st) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, sv_attend_join_kernel<F16, D, kRows, kAcross, kCols, kShared>, P) == cudaSuccess
+  return cudaLaunchKernelEx(&cfg, sv_attend_join_kernel<F16, D, kRows, kAcross, kCols>, P) == cudaSuccess
              ? SV_OK
              : SV_ERR_CUDA;
 }
@@ -190,8 +136,8 @@ int launch2(const sv::ParamsOf<kShared>& P, int blocks, cudaStream_t st) {
 template <bool F16, int D, int kRows>
 int launch(const sv::AttendParams& P, int grid, cudaStream_t st) {
   constexpr int kAll = D / 16 / (kRows < 32 ? 32 / kRows : 1);
-  return P.by_item ? launch2<F16, D, kRows, 1, 8, false>(P, P.R.B * P.R.C.heads * P.by_item, st)
-                   : launch2<F16, D, kRows, kAll, 16, false>(P, grid * P.ways, st);
+  return P.by_item ? launch2<F16, D, kRows, 1, 8>(P, P.R.B * P.R.C.heads * P.by_item, st)
+                   : launch2<F16, D, kRows, kAll, 16>(P, grid * P.ways, st);
 }
 
 }  // namespace
@@ -211,19 +157,6 @@ int launch_attend_join(const AttendParams& P, bool f16, bool wide, int grid,
       if (wide) return f16 ? launch<true, 256, 128>(P, grid, st) : launch<false, 256, 128>(P, grid, st);
       return f16 ? launch<true, 256, 16>(P, grid, st) : launch<false, 256, 16>(P, grid, st);
   }
-}
-
-template <bool F16, int D>
-int launch_shared(const SharedParams& P, int grid, long long items, cudaStream_t st) {
-  return items * 4 <= grid ? launch2<F16, D, 128, 1, 8, true>(P, static_cast<int>(items), st)
-                           : launch2<F16, D, 128, D / 16, 16, true>(P, grid * P.ways, st);
-}
-int launch_attend_join(const SharedParams& P, bool f16, int grid, long long items, cudaStream_t st) {
-  if (P.records > kMaxRecords) return SV_ERR_CUDA;
-  const int D = P.R.C.head_dim;
-  if (D == 64) return f16 ? launch_shared<true, 64>(P, grid, items, st) : launch_shared<false, 64>(P, grid, items, st);
-  if (D == 128) return f16 ? launch_shared<true, 128>(P, grid, items, st) : launch_shared<false, 128>(P, grid, items, st);
-  return f16 ? launch_shared<true, 256>(P, grid, items, st) : launch_shared<false, 256>(P, grid, items, st);
 }
 
 }  // namespace sv

@@ -6,8 +6,8 @@
 //   M = max(m_A, m_B),  L = l_A e^(m_A - M) + l_B e^(m_B - M),  out = (o_A e^(m_A - M) + o_B e^(m_B - M)) / L.
 // A of all the group's rows and tokens is one set of products with the group's keys and values, read once for up to
 // 128 or 256 query rows, not once a row. One launch of the wide kernel (sv_attend_wide.cuh) does the fronts and the
-// rows' own entries, cut into equal runs of tiles; the join kernel puts together what several CTAs did of one; the merge
-// kernel here puts the two sides of each query together.
+// rows' own entries, cut into equal runs of tiles, whose results, of several CTAs where an item is cut, the merge kernel
+// here puts together, a query a warp.
 // Bound: the bytes of the entries, each read once, or for large groups the products (4 D a query head and entry).
 // Rounding: the sides are fp32 sums and maxima; the output is rounded once.
 
@@ -34,62 +34,107 @@ __device__ __forceinline__ int group_of(const int32_t* start, int groups, int b,
   return lo > groups ? -1 : lo - 1;
 }
 
-// A warp a query: its two sides, from the join and the attention kernel.
+// `across` warps a query, or one: they divide its parts and sides among them and meet in shared memory.
 template <bool F16, int D>
-__global__ void __launch_bounds__(32 * kMergeWarps) sv_attend_merge_kernel(const SharedParams P) {
+__global__ void __launch_bounds__(32 * kMergeWarps) sv_attend_merge_kernel(const SharedParams P, int across) {
   constexpr int kCols = D / 32;
+  __shared__ float acc[kMergeWarps][D];
+  __shared__ float2 ml[kMergeWarps];
   const sv::SharedRound& R = P.R;
-  const int lane = threadIdx.x & 31, at = blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
-  const int token = at / P.Hq, b = token / R.N, i = token - b * R.N;
-  if (b >= R.B) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, mine = warp % across;
+  const int queries = R.B * R.N * P.Hq, at = min(blockIdx.x * (kMergeWarps / across) + warp / across, queries - 1);
+  const int token = at / P.Hq, hq = at - token * P.Hq, b = token / R.N, i = token - b * R.N, head = hq / R.group;
   sv::SharedWork w;
   bool ok = sv::row_work(R, R.groups + b, &w);
   const int s = __ldg(R.common + b), g = group_of(R.start, R.groups, b, lane);
+  // Where the two items have their records, and the query's row of their query tiles.
+  int row_own = i * R.group + hq - head * R.group, row_front = 0, tile_front = 0;
+  const int tile_own = row_own / P.tile_rows;
+  row_own -= tile_own * P.tile_rows;
+  const size_t at_own = P.record_at(R.groups + b, head, tile_own, 0);
+  size_t at_front = at_own;
   if (s > 0) {
     const int a = g >= 0 ? __ldg(R.start + g) : -1;
     ok = ok && a >= 0 && a <= b && __ldg(R.common + a) == s;
+    if (ok) {
+      row_front = (token - a * R.N) * R.group + hq - head * R.group;
+      tile_front = row_front / P.tile_rows;
+      row_front -= tile_front * P.tile_rows;
+      at_front = P.record_at(g, head, tile_front, a * R.N);
+    }
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  ok = ok && __ldcg(P.bad_groups) == 0;
-  float v[kCols], L = 1.0f, M = 0.0f;
+  float v[kCols], M = -INFINITY, L = 0.0f;
 #pragma unroll
-  for (int x = 0; x < kCols; ++x) v[x] = ok ? 0.0f : __int_as_float(0x7fffffff);
-  float lse = v[0];
+  for (int x = 0; x < kCols; ++x) v[x] = 0.0f;
   if (ok && i < w.m) {
-    L = 0.0f;
-    const float2 a = s > 0 ? __ldcg(P.side_ml + P.side_at(0, at)) : make_float2(-INFINITY, 0.0f);
-    const float2 e = __ldcg(P.side_ml + P.side_at(1, at));
-    M = fmaxf(a.x, e.x);
+    const int2 of = __ldcg(P.records + at_front), oo = __ldcg(P.records + at_own);
+    const int fronts = s > 0 ? (of.x < 0 ? 1 : of.y - of.x + 1) : 0, all = fronts + (oo.x < 0 ? 1 : oo.y - oo.x + 1);
+#pragma unroll 2
+    for (int k = mine; k < all; k += across) {
+      const bool front = k < fronts;
+      const int2 rec = front ? of : oo;
+      const int p = rec.x + (front ? k : k - fronts);
+      const size_t row = rec.x < 0 ? P.side_at(front ? 0 : 1, at)
+                                   : P.part_row(p, rec.x, (front ? tile_front : tile_own) % P.ways, front ? row_front : row_own);
+      const float2 e = __ldcg((rec.x < 0 ? P.side_ml : P.part_ml) + row);
+      const float2* o = reinterpret_cast<const float2*>((rec.x < 0 ? P.side_o : P.part_o) + row * D) + lane;
+      float2 z[kCols / 2];
 #pragma unroll
-    for (int side = 0; side < 2; ++side) {
-      if (side == 0 && s == 0) continue;
-      const float2 x = side ? e : a;
-      const float f = x.x == -INFINITY ? 0.0f : sv::ex2((x.x - M) * P.c);
-      L += x.x == -INFINITY ? x.y : x.y * f;   // the former: 0, or NaN
-      const float* o = P.side_o + P.side_at(side, at) * D + lane * kCols;
+      for (int y = 0; y < kCols / 2; ++y) z[y] = __ldcg(o + 32 * y);
+      const float top = fmaxf(M, e.x);
+      const float f = M == top ? 1.0f : (M == -INFINITY ? 0.0f : sv::ex2((M - top) * P.c));
+      const float t = e.x == -INFINITY ? 0.0f : sv::ex2((e.x - top) * P.c);
+      M = top;
+      L = L * f + (e.x == -INFINITY ? e.y : e.y * t);   // the former: 0, or NaN
 #pragma unroll
-      for (int y = 0; y < kCols; y += 2) {
-        const float2 z = __ldcg(reinterpret_cast<const float2*>(o + y));
-        v[y] += z.x * f;
-        v[y + 1] += z.y * f;
+      for (int y = 0; y < kCols / 2; ++y) {             // (an infinity times a weight of 0: NaN)
+        v[2 * y] = v[2 * y] * f + z[y].x * t;
+        v[2 * y + 1] = v[2 * y + 1] * f + z[y].y * t;
       }
     }
-    const float inv = 1.0f / L;
-#pragma unroll
-    for (int x = 0; x < kCols; ++x) v[x] *= inv;
-    lse = (M * P.c + (log2f(L) - sv::kProbBits<F16, true>)) * 0.6931471805599453f;
   }
-  uint32_t* out = reinterpret_cast<uint32_t*>(P.out) + (static_cast<size_t>(at) * D + lane * kCols) / 2;
+  if (across > 1) {
 #pragma unroll
-  for (int x = 0; x < kCols; x += 2) out[x / 2] = sv::pack2<F16>(v[x], v[x + 1]);
-  if (P.lse && lane == 0) P.lse[at] = lse;
+    for (int y = 0; y < kCols / 2; ++y) *reinterpret_cast<float2*>(&acc[warp][2 * lane + 64 * y]) = make_float2(v[2 * y], v[2 * y + 1]);
+    if (lane == 0) ml[warp] = make_float2(M, L);
+    __syncthreads();
+    if (mine > 0) return;
+    for (int k = 1; k < across; ++k) M = fmaxf(M, ml[warp + k].x);
+    L = 0.0f;
+#pragma unroll
+    for (int x = 0; x < kCols; ++x) v[x] = 0.0f;
+    for (int k = 0; k < across; ++k) {
+      const float2 e = ml[warp + k];
+      const float t = e.x == -INFINITY ? 0.0f : sv::ex2((e.x - M) * P.c);
+      L += e.x == -INFINITY ? e.y : e.y * t;
+#pragma unroll
+      for (int y = 0; y < kCols / 2; ++y) {
+        const float2 z = *reinterpret_cast<const float2*>(&acc[warp + k][2 * lane + 64 * y]);
+        v[2 * y] += z.x * t;
+        v[2 * y + 1] += z.y * t;
+      }
+    }
+  }
+  if (blockIdx.x * (kMergeWarps / across) + warp / across >= queries) return;
+  ok = ok && __ldcg(P.bad_groups) == 0;
+  const bool some = ok && i < w.m;
+  const float inv = some ? 1.0f / L : 0.0f, none = ok ? 0.0f : __int_as_float(0x7fffffff);
+  uint32_t* out = reinterpret_cast<uint32_t*>(P.out) + static_cast<size_t>(at) * (D / 2) + lane;
+#pragma unroll
+  for (int y = 0; y < kCols / 2; ++y)
+    out[32 * y] = some ? sv::pack2<F16>(v[2 * y] * inv, v[2 * y + 1] * inv) : sv::pack2<F16>(none, none);
+  if (P.lse && lane == 0)
+    P.lse[at] = some ? (M * P.c + (log2f(L) - sv::kProbBits<F16, true>)) * 0.6931471805599453f : none;
 }
 
 template <bool F16, int D>
 int merge(const SharedParams& P, cudaStream_t st) {
-  cudaLaunchConfig_t cfg = {};
   const long long queries = static_cast<long long>(P.R.B) * P.R.N * P.Hq;
-  cfg.gridDim = dim3(static_cast<unsigned>((queries + kMergeWarps - 1) / kMergeWarps));
+  // Few queries, whose fronts may be in many parts: eight warps each, else four or one.
+  int across = queries <= 1024 ? 8 : (queries <= 8192 ? 4 : 1);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((queries * across + kMergeWarps - 1) / kMergeWarps));
   cfg.blockDim = dim3(32 * kMergeWarps);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
@@ -97,7 +142,7 @@ int merge(const SharedParams& P, cudaStream_t st) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, sv_attend_merge_kernel<F16, D>, P) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, sv_attend_merge_kernel<F16, D>, P, across) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 template <bool F16>
 int merge(const SharedParams& P, cudaStream_t st) {
@@ -106,15 +151,18 @@ int merge(const SharedParams& P, cudaStream_t st) {
 }
 
 constexpr int kMaxSms = 160;
-constexpr size_t kSharedBytes = 2 * kMaxSms * sizeof(int4), kFlagBytes = 256;
+constexpr size_t kFlagBytes = 256;
 constexpr long long kMaxQueries = 1ll << 28;   // query heads of all tokens
 
 bool sizes_ok(int32_t B, int32_t N, int32_t Hq, const sv_paged_cache* c) {
   return B >= 1 && B <= (1 << 20) && N >= 1 && N <= SV_MAX_GAMMA + 1 && Hq >= 1 && Hq <= 1024 && c->heads >= 1 &&
          Hq % c->heads == 0 && Hq / c->heads <= 128 && static_cast<long long>(B) * N * Hq <= kMaxQueries;
 }
-size_t part_bytes(int ways, int D) { return static_cast<size_t>(2 * kMaxSms) * ways * 128 * (D * 4 + 8); }
-int ways_most(int D) { return D < 256 ? 2 : 1; }
+size_t rounded(size_t bytes) { return (bytes + 255) / 256 * 256; }
+size_t part_rows(int D) { return static_cast<size_t>(2 * kMaxSms) * (D < 256 ? 2 : 1) * 128; }
+// Query tiles of a row's key head, and of the fronts' (each group's last may be short).
+int own_tiles(int N, int group) { return (N * group - 1) / (128 / group * group) + 1; }
+long long front_tiles(long long queries, int groups, int group) { return queries / (128 / group * group) + groups + 1; }
 
 }  // namespace
 
@@ -127,11 +175,14 @@ int launch_attend_shared(const SharedParams& P, bool f16, const CUtensorMap& k, 
 
 }  // namespace sv
 
-extern "C" size_t spec_verify_shared_attention_workspace_size(int32_t B, int32_t N, int32_t Hq, const sv_paged_cache* cache) {
-  if (!cache || !sizes_ok(B, N, Hq, cache) || cache->head_dim < 1 || cache->head_dim > 256) return 0;
-  const int D = cache->head_dim;
-  const size_t sides = static_cast<size_t>(2) * B * N * Hq * (D * 4 + 8);
-  return kSharedBytes + kFlagBytes + part_bytes(ways_most(D), D) + (sides + 255) / 256 * 256;
+extern "C" size_t spec_verify_shared_attention_workspace_size(int32_t B, int32_t N, int32_t Hq, int32_t groups,
+                                                              const sv_paged_cache* cache) {
+  if (!cache || !sizes_ok(B, N, Hq, cache) || cache->head_dim < 1 || cache->head_dim > 256 || groups < 1 || groups > (1 << 20)) return 0;
+  const int D = cache->head_dim, heads = cache->heads, group = Hq / heads;
+  const size_t row = D * 4 + 8, queries = static_cast<size_t>(B) * N * Hq;
+  const size_t records = static_cast<size_t>(heads) * (static_cast<size_t>(B) * own_tiles(N, group) +
+                                                       front_tiles(static_cast<long long>(B) * N * group, groups, group));
+  return kFlagBytes + rounded(records * sizeof(int2)) + rounded(part_rows(D) * row) + rounded(2 * queries * row);
 }
 
 extern "C" int spec_verify_shared_attention(const void* q, int64_t q_row_stride, int64_t q_token_stride,
@@ -152,7 +203,7 @@ extern "C" int spec_verify_shared_attention(const void* q, int64_t q_row_stride,
       sv::misaligned(shared_len, 4) || sv::misaligned(group_start, 4) || sv::misaligned(num_queries, 4) ||
       sv::misaligned(tree_parents, 4) || sv::misaligned(workspace, 256))
     return SV_ERR_MISALIGNED;
-  const size_t need = spec_verify_shared_attention_workspace_size(B, N, Hq, cache);
+  const size_t need = spec_verify_shared_attention_workspace_size(B, N, Hq, groups, cache);
   if (!workspace || workspace_bytes < need) return SV_ERR_WORKSPACE_TOO_SMALL;
   const unsigned long long rows = 4ull * B, tokens = rows * N * Hq;
   if (sv::overlap({{out, tokens / 2 * cache->head_dim}, {out_lse, tokens}, {workspace, need}},
@@ -200,26 +251,27 @@ extern "C" int spec_verify_shared_attention(const void* q, int64_t q_row_stride,
   P.tile_rows = rows_tile;
   P.ways = ways;
   P.by_item = 0;
+  P.own_tiles = own_tiles(N, group);
+  P.front_tiles = static_cast<int>(front_tiles(all, groups, group));
   // As many CTAs as the GPU holds, or as many as the batch can have tiles.
   const long long tile = 1 << P.R.tile_log2;
-  const long long own = static_cast<long long>(B) * ((N * group + rows_tile - 1) / rows_tile);
-  const long long items = cache->heads * (own + all / rows_tile + std::min<long long>(groups, all));   // query tiles
+  const long long items = static_cast<long long>(cache->heads) * (static_cast<long long>(B) * P.own_tiles + P.front_tiles);
   const long long most = items * ((static_cast<long long>(cache->max_pages) * cache->page_size + tile - 1) / tile);
   const int grid = static_cast<int>(std::min<long long>(most, sms));
-  P.records = grid * ways;
   char* ws = static_cast<char*>(workspace);
-  P.shared = reinterpret_cast<int4*>(ws);
-  P.bad_groups = reinterpret_cast<int*>(ws + kSharedBytes);
-  ws += kSharedBytes + kFlagBytes;
-  P.part_ml = reinterpret_cast<float2*>(ws);
-  P.part_o = reinterpret_cast<float*>(ws + static_cast<size_t>(2) * grid * ways * 128 * 8);
-  ws += part_bytes(ways_most(D), D);
+  P.shared = nullptr;
+  P.bad_groups = reinterpret_cast<int*>(ws);
+  ws += kFlagBytes;
+  P.records = reinterpret_cast<int2*>(ws);
+  ws += rounded(static_cast<size_t>(cache->heads) * (static_cast<size_t>(B) * P.own_tiles + P.front_tiles) * sizeof(int2));
+  P.part_o = reinterpret_cast<float*>(ws);
+  P.part_ml = reinterpret_cast<float2*>(P.part_o + part_rows(D) * D);
+  ws += rounded(part_rows(D) * (D * 4 + 8));
   P.side_o = reinterpret_cast<float*>(ws);
-  P.side_ml = reinterpret_cast<float2*>(ws + static_cast<size_t>(2) * B * N * Hq * D * 4);
+  P.side_ml = reinterpret_cast<float2*>(P.side_o + static_cast<size_t>(2) * B * N * Hq * D);
   const cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   const bool f16 = cache->dtype == SV_DTYPE_F16;
   st = sv::launch_attend_shared(P, f16, kmap, vmap, qmap, q_tokens, grid, s);
-  if (st == SV_OK) st = sv::launch_attend_join(P, f16, grid, items, s);
   if (st != SV_OK) return st;
   return f16 ? merge<true>(P, s) : merge<false>(P, s);
 }

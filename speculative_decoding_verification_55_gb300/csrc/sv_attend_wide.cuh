@@ -84,8 +84,14 @@ template <int D, int kWays>
 constexpr int kSmemBytes = Shape<D, kWays>::kSlots * Shape<D, kWays>::kSlotBytes + Shape<D, kWays>::kQueryBytes +
                            sizeof(Control<Shape<D, kWays>::kSlots>);
 
-// kShared: a batch whose rows share the fronts of their contexts (SharedRound); an item's whole result then goes to
-// its side, as a part's would. Where two ways are for the fronts' many queries, an item of one query tile (a row's own
+// 32 bytes at once: a thread's own row, whose neighbours are other threads'.
+__device__ __forceinline__ void store8(float* at, const float* f) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+               ::"l"(at), "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]) : "memory");
+}
+
+// kShared: a batch whose rows share the fronts of their contexts (SharedRound); an item's result, whole or a part, then
+// goes to the merge kernel. Where two ways are for the fronts' many queries, an item of one query tile (a row's own
 // entries) has its key tiles in turn on both, each with a maximum, a sum and an accumulator of its own, which meet at the
 // end: a tile's chain of S, softmax, P V and the next S takes longer than its bytes from HBM.
 template <bool F16, int D, int kWays, bool kShared>
@@ -122,7 +128,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kProducts) tm_alloc(&S.tm);
   sv::make_plan<kThreads>(R, S.scan, &S.plan);
   asm volatile("griddepcontrol.launch_dependents;");   // the join kernel's CTAs, which wait for this grid's end
-  if (tid < kWays && !P.by_item) P.shared[blockIdx.x * kWays + tid].x = -1;
+  if (!kShared && tid < kWays && !P.by_item) P.shared[blockIdx.x * kWays + tid].x = -1;
   fence_after();
   const uint32_t tm = S.tm;
   volatile int* const lost = &S.lost;
@@ -482,8 +488,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float jl = (flags & 1) ? __int_as_float(0x7fffffff) : (kWays == 1 ? sums[row] + sums[kRows + row] : l);
       const bool whole = W.count == W.tiles;
       const int slot = (2 * blockIdx.x + (W.first == 0 ? 1 : 0)) * kWays + (split ? 0 : way);
+      size_t to_row = 0;                       // kShared: the result's row, of a side or a part
+      if constexpr (kShared) {
+        const int r = row0 + row, i = r / R.group;
+        to_row = whole ? P.side_at(side, (static_cast<size_t>(W.token0) + i) * P.Hq + W.head * R.group + r - i * R.group)
+                       : static_cast<size_t>(slot) * kRows + row;
+      }
       const int i = (row0 + row) / R.group, hq = W.head * R.group + (row0 + row) - i * R.group;
-      const size_t at = (static_cast<size_t>(kShared ? W.token0 : W.row * static_cast<size_t>(R.N)) + i) * P.Hq + hq;
+      const size_t at = (static_cast<size_t>(W.row) * R.N + i) * P.Hq + hq;
       const float inv = 1.0f / jl;
 #pragma unroll 1
       for (int k = 0; k < H::kOut; k += 16) {
@@ -526,12 +538,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (row < rows) {
-          if (kShared && whole) {
-            if constexpr (kShared) {
-              float4* out = reinterpret_cast<float4*>(P.side_o + P.side_at(side, at) * D + mycol);
-#pragma unroll
-              for (int z = 0; z < 4; ++z) out[z] = make_float4(f[4 * z], f[4 * z + 1], f[4 * z + 2], f[4 * z + 3]);
-            }
+          if constexpr (kShared) {
+            float* out = (whole ? P.side_o : P.part_o) + to_row * D + mycol;
+            store8(out, f);
+            store8(out + 8, f + 8);
           } else if (whole) {
             uint32_t p[8];
 #pragma unroll
@@ -547,17 +557,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (half == 0 && row < rows && !(split && way == 1)) {
-        if (!whole) P.part_ml[slot * kRows + row] = make_float2(mx, jl);
-        else if constexpr (kShared) P.side_ml[P.side_at(side, at)] = make_float2(mx, jl);
+        if constexpr (kShared) (whole ? P.side_ml : P.part_ml)[to_row] = make_float2(mx, jl);
+        else if (!whole) P.part_ml[slot * kRows + row] = make_float2(mx, jl);
         else if (P.lse) P.lse[at] = (mx * c + (log2f(jl) - kBits)) * 0.6931471805599453f;
       }
       fence_before();
       sv::named_bar_sync(1, kSoft);            // the sums have been read
       if ((tid & 127) == 0 && half == 0 && W.first == 0 && rows > 0 && !(split && way == 1))
-        sv::tell_shared(P, way, kShared ? 2 * W.token0 + side : W.row, W.head, W.q_tile * kWays + way, rows, whole, W.item_at,
-                        W.tiles, S.plan);
+        if constexpr (kShared) sv::tell_shared(P, W.row, W.head, W.q_tile * kWays + way, W.token0, whole, W.item_at, W.tiles, S.plan);
+        else sv::tell_shared(P, way, W.row, W.head, W.q_tile * kWays + way, rows, whole, W.item_at, W.tiles, S.plan);
     }
     fence_before();
+  }
+  if constexpr (kShared) {                     // (no group that is out of range has been taken)
+    if (blockIdx.x == gridDim.x - 1) {
+      bool bad = false;
+#pragma unroll 1
+      for (int g = tid; g <= R.groups; g += kThreads) {
+        const int e = __ldg(R.start + g);
+        bad |= e > R.B || (g == 0 ? e < 0 : __ldg(R.start + g - 1) > e);
+      }
+      bad = __syncthreads_or(bad);
+      if (tid == 0) *P.bad_groups = bad;
+    }
   }
   __syncthreads();
   if (warp == kProducts) {
@@ -577,27 +599,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int q_tile = W.q_tile * kWays + way, row0 = q_tile * P.tile_rows;
         const int rows = min(P.tile_rows, sv::tokens_of(W.w) * R.group - row0);
         const bool whole = W.count == W.w.tiles;
-        int tell = W.row;
-        size_t token0 = static_cast<size_t>(W.row) * R.N;
+        const int slot = (2 * blockIdx.x + (W.first == 0 ? 1 : 0)) * kWays + way;
+        int token0 = 0, side = 0;
         if constexpr (kShared) {
           token0 = W.w.token0;
-          tell = 2 * W.w.token0 + (W.row >= R.groups);
+          side = W.row >= R.groups;
         }
 #pragma unroll 1
         for (int x = tid; x < rows * D; x += kThreads) {
           const int r = x / D, i = (row0 + r) / R.group, hq = W.head * R.group + (row0 + r) - i * R.group;
-          const size_t at = (token0 + i) * P.Hq + hq;
-          const int slot = (2 * blockIdx.x + (W.first == 0 ? 1 : 0)) * kWays + way;
+          const size_t at = ((kShared ? static_cast<size_t>(token0) : static_cast<size_t>(W.row) * R.N) + i) * P.Hq + hq;
           if constexpr (kShared) {
-            if (x % D == 0 && whole) P.side_ml[P.side_at(tell & 1, at)].y = __int_as_float(0x7fffffff);
+            if (x % D == 0 && whole) P.side_ml[P.side_at(side, at)].y = __int_as_float(0x7fffffff);
           } else {
             if (whole) static_cast<unsigned short*>(P.out)[at * D + x % D] = 0x7fffu;
             if (x % D == 0 && whole && P.lse) P.lse[at] = __int_as_float(0x7fffffff);
           }
-          if (x % D == 0 && !whole) P.part_ml[slot * kRows + r].y = __int_as_float(0x7fffffff);
+          if (x % D == 0 && !whole) P.part_ml[static_cast<size_t>(slot) * kRows + r].y = __int_as_float(0x7fffffff);
         }
-        if (tid == 0 && W.first == 0 && rows > 0)
-          sv::tell_shared(P, way, tell, W.head, q_tile, rows, whole, W.item_at, W.w.tiles, S.plan);
+        if (tid == 0 && W.first == 0 && rows > 0) {
+          if constexpr (kShared) sv::tell_shared(P, W.row, W.head, q_tile, token0, whole, W.item_at, W.w.tiles, S.plan);
+          else sv::tell_shared(P, way, W.row, W.head, q_tile, rows, whole, W.item_at, W.w.tiles, S.plan);
+        }
       }
   }
 }

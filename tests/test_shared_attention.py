@@ -62,10 +62,10 @@ def test_cache_refusals(L):
 def test_workspace_size(L):
     f = L.spec_verify_shared_attention_workspace_size
     c = ctypes.byref(cache_struct())
-    assert f(64, 9, 32, c) >= 2 * 64 * 9 * 32 * (128 * 4 + 8) and f(64, 9, 32, c) % 256 == 0
-    for bad in ((0, 9, 32), (64, 0, 32), (64, 66, 32), (64, 9, 30), (1 << 20, 65, 32)):
+    assert f(64, 9, 32, 3, c) >= 2 * 64 * 9 * 32 * (128 * 4 + 8) and f(64, 9, 32, 3, c) % 256 == 0
+    for bad in ((0, 9, 32, 3), (64, 0, 32, 3), (64, 66, 32, 3), (64, 9, 30, 3), (1 << 20, 65, 32, 3), (64, 9, 32, 0)):
         assert f(*bad, c) == 0
-    assert f(64, 9, 32, None) == 0
+    assert f(64, 9, 32, 3, None) == 0
 
 
 def test_binding_refusals():
@@ -317,7 +317,7 @@ def test_gpu_captured_and_streams(sv):
     torch.cuda.synchronize()
     for o, z in results:
         assert torch.equal(o, want) and torch.equal(z, want_lse)
-    need = sv.spec_verify_shared_attention_workspace_size(4, 5, 8, cache)
+    need = sv.spec_verify_shared_attention_workspace_size(4, 5, 8, 1, cache)
     for fill in (0, 255):
         room = torch.full((need + 512,), fill, dtype=torch.uint8, device="cuda")
         out = torch.empty_like(want)
