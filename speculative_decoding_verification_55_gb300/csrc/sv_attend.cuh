@@ -36,6 +36,7 @@ struct SharedParams : AttendParamsOf<true> {
   float* side_o;                               // [2][B N Hq][D]
   float2* side_ml;                             // [2][B N Hq] maximum and sum
   int2* records;                               // (by record_at) first and last CTA; first -1: one CTA has all of it
+  int4* rows;                                  // [B] a row's tokens (-1: in error), its group, the group's first token, shared_len
   int* bad_groups;                             // not 0: group_start does not ascend within 0 .. B
   int own_tiles, front_tiles;                  // records of a row's key head; of the fronts' key head
   __device__ __forceinline__ size_t side_at(int side, size_t at) const {
@@ -119,10 +120,10 @@ __device__ __forceinline__ void tell_shared(const AttendParams& P, int way, int 
   else
     P.shared[cta * P.ways + way] = make_int4(row, head, q_tile << 8 | rows, last);
 }
-__device__ __forceinline__ void tell_shared(const SharedParams& P, int row, int head, int q_tile, int token0, bool whole,
-                                            long long item_at, int tiles, const Plan& plan) {
+__device__ __forceinline__ void tell_shared(const SharedParams& P, int row, int head, int q_tile, int tokens, int token0,
+                                            bool whole, long long item_at, int tiles, const Plan& plan) {
   P.records[P.record_at(row, head, q_tile, token0)] =
-      make_int2(whole ? -1 : static_cast<int>(blockIdx.x), whole ? 0 : unit_owner(item_at + tiles - 1, plan));
+      make_int2(whole ? -1 : static_cast<int>(blockIdx.x), whole ? 0 : unit_owner(item_at + static_cast<long long>(tiles - 1) * P.R.units(tokens), plan));
 }
 
 // Joins the parts of the items that the attention kernel's `grid` CTAs shared.

@@ -19,130 +19,152 @@ namespace {
 
 using sv::SharedParams;
 
-constexpr int kMergeWarps = 8;
+template <int kQueries>
+constexpr int kMergeWarps = kQueries == 1 ? 16 : 8;
+// What the plan takes a tile and an item (its queries and its end) to cost, in units of 0.25 us: a tile on two ways 2 us,
+// on one about what its bytes take from HBM among other CTAs' products. (All tiles alike and an item two of them: 64 rows
+// of one token over 8000 shared entries 78 us against 61, two prompts' rounds of 9 tokens 113 against 92. One-way tiles at
+// 3 units 64 and 102; items at 8 where they have two ways: trees of 31 over three documents 86 us against 80.)
+constexpr int kTwoWays = 8, kOneWay = 4, kOneItem = 10, kTwoItem = 15;
 
-// The group that holds row b, -1 for none: the starts up to b, 32 places at a time; one warp.
-__device__ __forceinline__ int group_of(const int32_t* start, int groups, int b, int lane) {
-  int lo = 0, hi = groups + 1;                 // how many of the groups + 1 starts are at most b lies in [lo, hi]
-  while (lo < hi) {
-    const int step = (hi - lo + 31) / 32, at = lo + (lane + 1) * step - 1;
-    const unsigned up = __ballot_sync(kFull, at < hi && __ldg(start + at) <= b);
-    const int n = __popc(up);                  // the starts ascend
-    lo += n * step;
-    hi = min(hi, lo + step - 1);
-  }
-  return lo > groups ? -1 : lo - 1;
-}
-
-// `across` warps a query, or one: they divide its parts and sides among them and meet in shared memory.
-template <bool F16, int D>
-__global__ void __launch_bounds__(32 * kMergeWarps) sv_attend_merge_kernel(const SharedParams P, int across) {
+// A warp has kQueries of a key head's query heads at one token: they have the same items, and rows of these that follow
+// one another. Or `across` warps have one query: they divide its parts and sides among them and meet in shared memory.
+template <bool F16, int D, int kQueries>
+__global__ void __launch_bounds__(32 * kMergeWarps<kQueries>) sv_attend_merge_kernel(const SharedParams P, int across) {
   constexpr int kCols = D / 32;
-  __shared__ float acc[kMergeWarps][D];
-  __shared__ float2 ml[kMergeWarps];
+  constexpr int kWarps = kMergeWarps<kQueries>;
+  __shared__ float acc[kQueries == 1 ? kWarps : 1][D];
+  __shared__ float2 ml[kWarps];
   const sv::SharedRound& R = P.R;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, mine = warp % across;
-  const int queries = R.B * R.N * P.Hq, at = min(blockIdx.x * (kMergeWarps / across) + warp / across, queries - 1);
-  const int token = at / P.Hq, hq = at - token * P.Hq, b = token / R.N, i = token - b * R.N, head = hq / R.group;
-  sv::SharedWork w;
-  bool ok = sv::row_work(R, R.groups + b, &w);
-  const int s = __ldg(R.common + b), g = group_of(R.start, R.groups, b, lane);
-  // Where the two items have their records, and the query's row of their query tiles.
-  int row_own = i * R.group + hq - head * R.group, row_front = 0, tile_front = 0;
-  const int tile_own = row_own / P.tile_rows;
-  row_own -= tile_own * P.tile_rows;
-  const size_t at_own = P.record_at(R.groups + b, head, tile_own, 0);
-  size_t at_front = at_own;
-  if (s > 0) {
-    const int a = g >= 0 ? __ldg(R.start + g) : -1;
-    ok = ok && a >= 0 && a <= b && __ldg(R.common + a) == s;
-    if (ok) {
-      row_front = (token - a * R.N) * R.group + hq - head * R.group;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, mine = kQueries == 1 ? warp % across : 0;
+  const int bunches = (R.group + kQueries - 1) / kQueries, all_bunches = R.B * R.N * R.C.heads * bunches;
+  const int id = kQueries == 1 ? blockIdx.x * (kWarps / across) + warp / across : blockIdx.x * kWarps + warp;
+  const bool there = id < all_bunches;
+  const int x = there ? id : 0, th = x / bunches, h0 = (x - th * bunches) * kQueries;   // its first query head of the key head's
+  const int token = th / R.C.heads, head = th - token * R.C.heads, b = token / R.N, i = token - b * R.N;
+  const int queries = min(kQueries, R.group - h0);
+  const size_t at = static_cast<size_t>(token) * P.Hq + head * R.group + h0;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int4 row = __ldcg(P.rows + b);
+  const int m = __ldcg(P.bad_groups) == 0 ? row.x : -1, s = row.w;
+  float v[kQueries][kCols], M[kQueries], L[kQueries];
+#pragma unroll
+  for (int q = 0; q < kQueries; ++q) {
+    M[q] = -INFINITY;
+    L[q] = 0.0f;
+#pragma unroll
+    for (int y = 0; y < kCols; ++y) v[q][y] = 0.0f;
+  }
+  if (there && i < m) {
+    // Where the two items have their records, and the first query's row of their query tiles.
+    int row_own = i * R.group + h0, row_front = 0, tile_front = 0;
+    const int tile_own = row_own / P.tile_rows;
+    row_own -= tile_own * P.tile_rows;
+    const int2 oo = __ldcg(P.records + P.record_at(R.groups + b, head, tile_own, 0));
+    int2 of = make_int2(0, -1);
+    if (s > 0) {
+      row_front = (token - row.z) * R.group + h0;
       tile_front = row_front / P.tile_rows;
       row_front -= tile_front * P.tile_rows;
-      at_front = P.record_at(g, head, tile_front, a * R.N);
+      of = __ldcg(P.records + P.record_at(row.y, head, tile_front, row.z));
     }
-  }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  float v[kCols], M = -INFINITY, L = 0.0f;
+    const int fronts = of.x < 0 ? 1 : of.y - of.x + 1, all = fronts + (oo.x < 0 ? 1 : oo.y - oo.x + 1);
+    constexpr int kBatch = kQueries == 1 ? 4 : 1;        // parts in flight together
+    for (int k0 = mine; k0 < all; k0 += kBatch * across) {
+      float2 e[kBatch][kQueries], z[kBatch][kQueries][kCols / 2];
 #pragma unroll
-  for (int x = 0; x < kCols; ++x) v[x] = 0.0f;
-  if (ok && i < w.m) {
-    const int2 of = __ldcg(P.records + at_front), oo = __ldcg(P.records + at_own);
-    const int fronts = s > 0 ? (of.x < 0 ? 1 : of.y - of.x + 1) : 0, all = fronts + (oo.x < 0 ? 1 : oo.y - oo.x + 1);
-#pragma unroll 2
-    for (int k = mine; k < all; k += across) {
-      const bool front = k < fronts;
-      const int2 rec = front ? of : oo;
-      const int p = rec.x + (front ? k : k - fronts);
-      const size_t row = rec.x < 0 ? P.side_at(front ? 0 : 1, at)
-                                   : P.part_row(p, rec.x, (front ? tile_front : tile_own) % P.ways, front ? row_front : row_own);
-      const float2 e = __ldcg((rec.x < 0 ? P.side_ml : P.part_ml) + row);
-      const float2* o = reinterpret_cast<const float2*>((rec.x < 0 ? P.side_o : P.part_o) + row * D) + lane;
-      float2 z[kCols / 2];
+      for (int y = 0; y < kBatch; ++y) {
+        const int k = k0 + y * across;
+        const bool front = k < fronts;
+        const int2 rec = front ? of : oo;
+        const int p = rec.x + (front ? k : k - fronts);
+        const size_t from = rec.x < 0 ? P.side_at(front ? 0 : 1, at)
+                                      : P.part_row(p, rec.x, (front ? tile_front : tile_own) % P.ways, front ? row_front : row_own);
 #pragma unroll
-      for (int y = 0; y < kCols / 2; ++y) z[y] = __ldcg(o + 32 * y);
-      const float top = fmaxf(M, e.x);
-      const float f = M == top ? 1.0f : (M == -INFINITY ? 0.0f : sv::ex2((M - top) * P.c));
-      const float t = e.x == -INFINITY ? 0.0f : sv::ex2((e.x - top) * P.c);
-      M = top;
-      L = L * f + (e.x == -INFINITY ? e.y : e.y * t);   // the former: 0, or NaN
+        for (int q = 0; q < kQueries; ++q) {
+          const bool real = k < all && q < queries;
+          e[y][q] = real ? __ldcg((rec.x < 0 ? P.side_ml : P.part_ml) + from + q) : make_float2(-INFINITY, 0.0f);
+          const float2* o = reinterpret_cast<const float2*>((rec.x < 0 ? P.side_o : P.part_o) + (from + q) * D) + lane;
 #pragma unroll
-      for (int y = 0; y < kCols / 2; ++y) {             // (an infinity times a weight of 0: NaN)
-        v[2 * y] = v[2 * y] * f + z[y].x * t;
-        v[2 * y + 1] = v[2 * y + 1] * f + z[y].y * t;
+          for (int c = 0; c < kCols / 2; ++c) z[y][q][c] = real ? __ldcg(o + 32 * c) : make_float2(0.0f, 0.0f);
+        }
       }
+#pragma unroll
+      for (int y = 0; y < kBatch; ++y)
+#pragma unroll
+        for (int q = 0; q < kQueries; ++q) {
+          const float2 g = e[y][q];
+          const float top = fmaxf(M[q], g.x);
+          const float f = M[q] == top ? 1.0f : (M[q] == -INFINITY ? 0.0f : sv::ex2((M[q] - top) * P.c));
+          const float t = g.x == -INFINITY ? 0.0f : sv::ex2((g.x - top) * P.c);
+          M[q] = top;
+          L[q] = L[q] * f + (g.x == -INFINITY ? g.y : g.y * t);          // the former: 0, or NaN
+#pragma unroll
+          for (int c = 0; c < kCols / 2; ++c) {  // (an infinity times a weight of 0: NaN)
+            v[q][2 * c] = v[q][2 * c] * f + z[y][q][c].x * t;
+            v[q][2 * c + 1] = v[q][2 * c + 1] * f + z[y][q][c].y * t;
+          }
+        }
     }
   }
-  if (across > 1) {
+  if (kQueries == 1 && across > 1) {
 #pragma unroll
-    for (int y = 0; y < kCols / 2; ++y) *reinterpret_cast<float2*>(&acc[warp][2 * lane + 64 * y]) = make_float2(v[2 * y], v[2 * y + 1]);
-    if (lane == 0) ml[warp] = make_float2(M, L);
+    for (int y = 0; y < kCols / 2; ++y) *reinterpret_cast<float2*>(&acc[warp][2 * lane + 64 * y]) = make_float2(v[0][2 * y], v[0][2 * y + 1]);
+    if (lane == 0) ml[warp] = make_float2(M[0], L[0]);
     __syncthreads();
     if (mine > 0) return;
-    for (int k = 1; k < across; ++k) M = fmaxf(M, ml[warp + k].x);
-    L = 0.0f;
+    for (int k = 1; k < across; ++k) M[0] = fmaxf(M[0], ml[warp + k].x);
+    L[0] = 0.0f;
 #pragma unroll
-    for (int x = 0; x < kCols; ++x) v[x] = 0.0f;
+    for (int y = 0; y < kCols; ++y) v[0][y] = 0.0f;
     for (int k = 0; k < across; ++k) {
       const float2 e = ml[warp + k];
-      const float t = e.x == -INFINITY ? 0.0f : sv::ex2((e.x - M) * P.c);
-      L += e.x == -INFINITY ? e.y : e.y * t;
+      const float t = e.x == -INFINITY ? 0.0f : sv::ex2((e.x - M[0]) * P.c);
+      L[0] += e.x == -INFINITY ? e.y : e.y * t;
 #pragma unroll
       for (int y = 0; y < kCols / 2; ++y) {
         const float2 z = *reinterpret_cast<const float2*>(&acc[warp + k][2 * lane + 64 * y]);
-        v[2 * y] += z.x * t;
-        v[2 * y + 1] += z.y * t;
+        v[0][2 * y] += z.x * t;
+        v[0][2 * y + 1] += z.y * t;
       }
     }
   }
-  if (blockIdx.x * (kMergeWarps / across) + warp / across >= queries) return;
-  ok = ok && __ldcg(P.bad_groups) == 0;
-  const bool some = ok && i < w.m;
-  const float inv = some ? 1.0f / L : 0.0f, none = ok ? 0.0f : __int_as_float(0x7fffffff);
-  uint32_t* out = reinterpret_cast<uint32_t*>(P.out) + static_cast<size_t>(at) * (D / 2) + lane;
+  if (!there) return;
+  const bool some = i < m;
+  const float none = m >= 0 ? 0.0f : __int_as_float(0x7fffffff);
 #pragma unroll
-  for (int y = 0; y < kCols / 2; ++y)
-    out[32 * y] = some ? sv::pack2<F16>(v[2 * y] * inv, v[2 * y + 1] * inv) : sv::pack2<F16>(none, none);
-  if (P.lse && lane == 0)
-    P.lse[at] = some ? (M * P.c + (log2f(L) - sv::kProbBits<F16, true>)) * 0.6931471805599453f : none;
+  for (int q = 0; q < kQueries; ++q) {
+    if (q >= queries) break;
+    const float inv = 1.0f / L[q];
+    uint32_t* out = reinterpret_cast<uint32_t*>(P.out) + (at + q) * (D / 2) + lane;
+#pragma unroll
+    for (int y = 0; y < kCols / 2; ++y)
+      out[32 * y] = some ? sv::pack2<F16>(v[q][2 * y] * inv, v[q][2 * y + 1] * inv) : sv::pack2<F16>(none, none);
+    if (P.lse && lane == 0)
+      P.lse[at + q] = some ? (M[q] * P.c + (log2f(L[q]) - sv::kProbBits<F16, true>)) * 0.6931471805599453f : none;
+  }
 }
 
-template <bool F16, int D>
-int merge(const SharedParams& P, cudaStream_t st) {
-  const long long queries = static_cast<long long>(P.R.B) * P.R.N * P.Hq;
-  // Few queries, whose fronts may be in many parts: eight warps each, else four or one.
-  int across = queries <= 1024 ? 8 : (queries <= 8192 ? 4 : 1);
+template <bool F16, int D, int kQueries>
+int merge(const SharedParams& P, int across, cudaStream_t st) {
+  const long long warps = static_cast<long long>(P.R.B) * P.R.N * P.R.C.heads * ((P.R.group + kQueries - 1) / kQueries) * across;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((queries * across + kMergeWarps - 1) / kMergeWarps));
-  cfg.blockDim = dim3(32 * kMergeWarps);
+  cfg.gridDim = dim3(static_cast<unsigned>((warps - 1) / kMergeWarps<kQueries> + 1));
+  cfg.blockDim = dim3(32 * kMergeWarps<kQueries>);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, sv_attend_merge_kernel<F16, D>, P, across) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, sv_attend_merge_kernel<F16, D, kQueries>, P, across) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+}
+template <bool F16, int D>
+int merge(const SharedParams& P, cudaStream_t st) {
+  // Few queries, whose fronts may be in many parts, have sixteen or four warps each.
+  const long long queries = static_cast<long long>(P.R.B) * P.R.N * P.Hq;
+  if (queries > 8192) return merge<F16, D, 4>(P, 1, st);
+  return merge<F16, D, 1>(P, queries <= 1024 ? 16 : 4, st);
 }
 template <bool F16>
 int merge(const SharedParams& P, cudaStream_t st) {
@@ -182,7 +204,7 @@ extern "C" size_t spec_verify_shared_attention_workspace_size(int32_t B, int32_t
   const size_t row = D * 4 + 8, queries = static_cast<size_t>(B) * N * Hq;
   const size_t records = static_cast<size_t>(heads) * (static_cast<size_t>(B) * own_tiles(N, group) +
                                                        front_tiles(static_cast<long long>(B) * N * group, groups, group));
-  return kFlagBytes + rounded(records * sizeof(int2)) + rounded(part_rows(D) * row) + rounded(2 * queries * row);
+  return kFlagBytes + rounded(static_cast<size_t>(B) * sizeof(int4)) + rounded(records * sizeof(int2)) + rounded(part_rows(D) * row) + rounded(2 * queries * row);
 }
 
 extern "C" int spec_verify_shared_attention(const void* q, int64_t q_row_stride, int64_t q_token_stride,
@@ -235,7 +257,11 @@ extern "C" int spec_verify_shared_attention(const void* q, int64_t q_row_stride,
   P.R.group = group;
   P.R.q_rows = rows_tile * ways;
   P.R.tile_log2 = D == 256 ? 6 : 7;
-  P.R.extra = 2;
+  P.R.one_rows = ways == 2 ? rows_tile : static_cast<int>(kMaxQueries);
+  P.R.one_units = kOneWay;
+  P.R.two_units = kTwoWays;
+  P.R.extra = kOneItem;
+  P.R.two_extra = kTwoItem;
   P.R.none_ok = false;
   P.R.start = group_start;
   P.R.common = shared_len;
@@ -262,6 +288,8 @@ extern "C" int spec_verify_shared_attention(const void* q, int64_t q_row_stride,
   P.shared = nullptr;
   P.bad_groups = reinterpret_cast<int*>(ws);
   ws += kFlagBytes;
+  P.rows = reinterpret_cast<int4*>(ws);
+  ws += rounded(static_cast<size_t>(B) * sizeof(int4));
   P.records = reinterpret_cast<int2*>(ws);
   ws += rounded(static_cast<size_t>(cache->heads) * (static_cast<size_t>(B) * P.own_tiles + P.front_tiles) * sizeof(int2));
   P.part_o = reinterpret_cast<float*>(ws);

@@ -53,9 +53,7 @@ struct Shape {
   static constexpr int kQueryBytes = kWays * kRows * D * 2;
   static constexpr int kSlots = D == 64 ? 12 : (D == 128 && kWays == 1 ? 6 : 5);   // keys and values in turn
   static constexpr int kAccum = kScores * kTile;       // tensor memory columns: S0, S1, then an O a way
-  static constexpr int kCols = kWays == 2 ? kTile : kTile / 2;   // scores of a thread
-  static constexpr int kChunk = kCols < 64 ? kCols : 64;         // scores of a thread in registers
-  static constexpr int kOut = kWays == 2 ? D : D / 2;            // columns of O of a thread
+  static constexpr int kChunk = D == 256 ? 32 : 64;    // scores of a thread in registers
   static_assert(kAccum + kWays * D <= kColumns, "tensor memory");
 };
 
@@ -84,6 +82,32 @@ template <int D, int kWays>
 constexpr int kSmemBytes = Shape<D, kWays>::kSlots * Shape<D, kWays>::kSlotBytes + Shape<D, kWays>::kQueryBytes +
                            sizeof(Control<Shape<D, kWays>::kSlots>);
 
+// For the merge kernel: what there is to a row, and its group (by bisection of the starts, which ascend).
+__device__ __forceinline__ void tell_rows(const sv::SharedParams& P, int tid) {
+  const sv::SharedRound& R = P.R;
+#pragma unroll 1
+  for (int b = tid * gridDim.x + blockIdx.x; b < R.B; b += 32 * kCopyWarps * gridDim.x) {
+    sv::SharedWork w;
+    const bool ok = sv::row_work(R, R.groups + b, &w);
+    const int s = __ldg(R.common + b);
+    int4 e = make_int4(ok ? w.m : -1, 0, 0, s);
+    if (s != 0) {
+      int lo = 0, hi = R.groups + 1;                   // how many of the starts are at most b
+#pragma unroll 1
+      while (lo < hi) {
+        const int at = (lo + hi) >> 1;
+        if (__ldg(R.start + at) <= b) lo = at + 1;
+        else hi = at;
+      }
+      const int a = lo > 0 && lo <= R.groups ? __ldg(R.start + lo - 1) : -1;
+      if (a < 0 || a > b || __ldg(R.common + a) != s) e.x = -1;
+      e.y = lo - 1;
+      e.z = a * R.N;
+    }
+    P.rows[b] = e;
+  }
+}
+
 // 32 bytes at once: a thread's own row, whose neighbours are other threads'.
 __device__ __forceinline__ void store8(float* at, const float* f) {
   asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
@@ -92,8 +116,8 @@ __device__ __forceinline__ void store8(float* at, const float* f) {
 
 // kShared: a batch whose rows share the fronts of their contexts (SharedRound); an item's result, whole or a part, then
 // goes to the merge kernel. Where two ways are for the fronts' many queries, an item of one query tile (a row's own
-// entries) has its key tiles in turn on both, each with a maximum, a sum and an accumulator of its own, which meet at the
-// end: a tile's chain of S, softmax, P V and the next S takes longer than its bytes from HBM.
+// entries) is worked on as with one way: two threads a row, two tiles ahead. (With its tiles in turn on both ways, each
+// with a maximum, a sum and an accumulator of its own, 512 such items of 4 or 5 tiles took 42 us of the batch's 76.)
 template <bool F16, int D, int kWays, bool kShared>
 __global__ void __launch_bounds__(kThreads, 1)
     sv_attend_wide_kernel(const ParamsOf<kShared> P, const __grid_constant__ CUtensorMap kmap,
@@ -102,6 +126,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using H = Shape<D, kWays>;
   constexpr int kSlots = H::kSlots, kTile = H::kTile, kAccum = H::kAccum;
   constexpr float kBits = sv::kProbBits<F16, true>;
+  constexpr bool kOne = kShared && kWays == 2;         // items of one way among those of two
   extern __shared__ __align__(1024) unsigned char dyn[];
   auto& S = *reinterpret_cast<Control<kSlots>*>(dyn + kSlots * H::kSlotBytes + H::kQueryBytes);
   const auto& R = P.R;
@@ -115,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int w = 0; w < kScores; ++w) {
       sv::mbar_init(sv::smem_addr(S.s_full + w), 1);
-      sv::mbar_init(sv::smem_addr(S.p_ready + w), kSoftWarps / kWays);
+      sv::mbar_init(sv::smem_addr(S.p_ready + w), kOne ? kSoftWarps : kSoftWarps / kWays);
     }
     sv::mbar_init(sv::smem_addr(&S.o_full), 1);
     sv::mbar_init(sv::smem_addr(&S.drained), 1);
@@ -133,8 +158,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tm = S.tm;
   volatile int* const lost = &S.lost;
 
-  constexpr bool kSplit = kShared && kWays == 2;
-  auto one_tile = [&](const Item& I) { return I.tokens * R.group - I.q_tile * kWays * P.tile_rows <= P.tile_rows; };
+  // Whether an item is worked on with one way: always, never, or where it has one query tile.
+  auto one_way = [&](const Item& I) {
+    return kWays == 1 || (kOne && I.tokens * R.group - I.q_tile * kWays * P.tile_rows <= P.tile_rows);
+  };
   // The next item's description. The items' warp always tells an end, however its own waits end: this wait is longer than
   // they can be, so that all warps know of the same items and meet at the same barriers.
   auto told = [&](int k) {
@@ -219,7 +246,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kItems) {
       if (armed > 0) sv::mbar_wait_drain(sv::smem_addr(&S.q_full), (armed - 1) & 1);
     } else {
-      if constexpr (!kShared) sv::fill_unused(P, D, op, 32 * kCopyWarps);   // while the last tiles are computed
+      if constexpr (kShared) tell_rows(P, op);  // while the last tiles are computed
+      else sv::fill_unused(P, D, op, 32 * kCopyWarps);
       // A slot is full when both warps have armed it. One whose wait gave up may be behind the other (by at most the
       // ring: the other's slots were given back full): it arrives for the slots that it has not armed.
       if (lane == 0) S.armed[mine] = armed;
@@ -254,18 +282,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       } pk{0, 0u}, pv{1, 0u};
       uint32_t ws = 0, wp = 0, turn = 0;                 // score buffers next written and next read, and its phase (a bit a way)
       int items = 0, left = 0;                           // left: score products of the item still to come
-      bool split = false;                                // the item's tiles are on both ways in turn
-      auto scores = [&](int way) {
-        if ((way == 0 || split) && !wait_unless_lost(full + 8 * pk.slot, pk.phase, lost)) return;
+      bool one = kWays == 1;                             // the item has one way
+      auto scores = [&](int way) {                       // (one way of two: the score buffer)
+        if ((way == 0 || one) && !wait_unless_lost(full + 8 * pk.slot, pk.phase, lost)) return;
         fence_after();
         const uint32_t w = kWays == 2 ? way : ws;
-        const Matrix km = ring_k.at(pk.slot * H::kSlotBytes), qm = queries.at(split ? 0 : way * (kRows * D * 2));
+        const Matrix km = ring_k.at(pk.slot * H::kSlotBytes), qm = queries.at(one ? 0 : way * (kRows * D * 2));
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
           product_ss(tm + w * kTile, qm.at((k >> 2) * (kRows * 128) + (k & 3) * 32),
                      km.at((k >> 2) * (kTile * 128) + (k & 3) * 32), ds, k > 0);
         products_done(s_full + 8 * w);
-        if (way + 1 < kWays && !split) return;
+        if (way + 1 < kWays && !one) return;
         products_done(empty + 8 * pk.slot);
         pk.step();
         ws ^= 1;
@@ -275,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (;;) {
         const Item I = told(items);
         const int count = I.count;
-        split = kSplit && one_tile(I);
+        one = one_way(I);
         if (count == 0 || !wait_unless_lost(sv::smem_addr(&S.q_full), items & 1, lost)) break;
         left = count;
         for (int idx = -kAhead; idx < count; ++idx) {      // (below 0: the first score products alone)
@@ -284,14 +312,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int way = 0; way < kWays; ++way) {
             if (idx >= 0) {
-              if (split && way != (idx & 1)) continue;
+              if (kWays == 2 && one && way != (idx & 1)) continue;
               const uint32_t w = kWays == 2 ? way : wp;
               if (!wait_unless_lost(p_ready + 8 * w, kWays == 2 ? turn >> way & 1 : turn, lost)) break;
               fence_after();
 #pragma unroll
               for (int k = 0; k < kTile / 16; ++k)
-                product_ts(tm + kAccum + way * D, tm + w * kTile + k * 8, vm.at(k * 2048), dp, idx > (split ? 1 : 0) || k > 0);
-              if (way + 1 == kWays || split) products_done(empty + 8 * pv.slot);
+                product_ts(tm + kAccum + (one ? 0 : way * D), tm + w * kTile + k * 8, vm.at(k * 2048), dp, idx > 0 || k > 0);
+              if (way + 1 == kWays || one) products_done(empty + 8 * pv.slot);
               if (kWays == 2) turn ^= 1u << way;
             }
             if (left > 0) scores(way);
@@ -309,19 +337,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else {
     // ---- Softmax
-    // One way: two warps share rows, `half` a tile's entries and D each. Two ways: four warps have a way.
-    const int half = kWays == 2 ? 0 : warp >> 2, way = kWays == 2 ? warp >> 2 : 0;
     const int wq = warp & 3, row = 32 * wq + lane;
     const uint32_t lanes = static_cast<uint32_t>(32 * wq) << 16;
-    const uint32_t to = tm + lanes + kAccum + way * D + half * H::kOut;
     const float c = P.c;
-    int base = 0, used = 0, items = 0;          // tiles before the item: the CTA's, and (two ways) this way's
+    int base = 0, items = 0;                   // tiles before the item
+    int used[2] = {0, 0};                      // uses of the score buffers (two ways)
     for (;;) {
       const Item W = told(items);
       if (W.count == 0) break;
-      const bool split = kSplit && one_tile(W);
+      // One way: two warps share rows, `half` a tile's entries and D each. Two ways: four warps have a way.
+      const bool one = one_way(W);
+      const int half = one ? warp >> 2 : 0, way = one ? 0 : warp >> 2;
+      const int cols = one ? kTile / 2 : kTile, outs = one ? D / 2 : D;     // scores and columns of O of a thread
+      const uint32_t to = tm + lanes + kAccum + way * D + half * outs;
       const int n = W.n, m = W.m, entries = n + m;
-      const int row0 = (W.q_tile * kWays + (split ? 0 : way)) * P.tile_rows, rows = min(P.tile_rows, W.tokens * R.group - row0);
+      const int row0 = (W.q_tile * kWays + way) * P.tile_rows, rows = min(P.tile_rows, W.tokens * R.group - row0);
       if (tid == 0) S.flags = 0;                // nobody sets one before this thread's first tile is used
       const int last = W.first + W.count;
       int side = 0;
@@ -343,16 +373,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       float mx = -INFINITY, l = 0.0f;
       bool odd = false;
 
-      for (int idx = split ? way : 0; idx < W.count; idx += split ? 2 : 1) {
+      for (int idx = 0; idx < W.count; ++idx) {
         const int x = base + idx, s = (2 * x + 1) % kSlots;
-        const int w = kWays == 2 ? way : x % kScores, turn = kWays == 2 ? used++ : x / kScores;
+        const int w = kWays == 1 ? x % kScores : (one ? idx & 1 : way);
+        const int turn = kWays == 1 ? x / kScores : (w ? used[1]++ : used[0]++);
         const int j0 = (W.first + idx) * kTile;
         const bool edge = j0 + kTile > n;      // entries of the round itself, or behind the last
         bool go = wait_unless_lost(sv::smem_addr(S.s_full + w), turn & 1, lost);
         if (edge || idx + 1 == W.count)        // the values are in, and the producer has seen all pages
           go = go && wait_unless_lost(sv::smem_addr(S.full + s), ((2 * x + 1) / kSlots) & 1, lost);
         if (!__all_sync(kFull, go)) {          // a wait gave up: the barriers alone
-          if (active && kWays == 1) sv::named_bar_sync(2 + wq, 64);
+          if (active && one) sv::named_bar_sync(2 + wq, 64);
           continue;
         }
         fence_after();
@@ -361,9 +392,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t ts = tm + lanes + w * kTile;
           uint32_t sc[H::kChunk];
           auto load = [&](int y) {               // scores y.. of this thread's
-            tm_load<H::kChunk>(sc, ts + half * H::kCols + y);
+            tm_load<H::kChunk>(sc, ts + half * cols + y);
             if (!edge) return;
-            const uint64_t see = sv::seen_bits(j0 + half * H::kCols + y - n, tok, mask, par);
+            const uint64_t see = sv::seen_bits(j0 + half * cols + y - n, tok, mask, par);
             const uint32_t lo = static_cast<uint32_t>(see), hi = static_cast<uint32_t>(see >> 32);
 #pragma unroll
             for (int z = 0; z < H::kChunk; ++z)
@@ -371,13 +402,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           };
           float v[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
-          for (int y = 0; y < H::kCols; y += H::kChunk) {
+          for (int y = 0; y < cols; y += H::kChunk) {
             load(y);
 #pragma unroll
             for (int z = 0; z < H::kChunk; ++z) v[z & 3] = fmaxf(v[z & 3], __uint_as_float(sc[z]));
           }
           float top = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
-          if (kWays == 1) {
+          if (one) {
             S.row_max[x & 1][half][row] = top;
             sv::named_bar_sync(2 + wq, 64);      // the two warps of these rows: both have read their scores
             top = fmaxf(top, S.row_max[x & 1][half ^ 1][row]);
@@ -388,15 +419,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float f = !grew ? 1.0f : (mx == -INFINITY ? 0.0f : sv::ex2((mx - top) * c));
             if (grew) mx = top;
             l *= f;
-            if (idx > (split ? 1 : 0)) {       // the products with the tiles before are done
-              if (!split) {                    // (split: they were issued before this tile's scores)
-                const int e = 2 * x - 1;
-                wait_unless_lost(sv::smem_addr(S.empty + e % kSlots), (e / kSlots) & 1, lost);
-              }
+            if (idx > 0) {                     // the products with the tiles before are done
+              const int e = 2 * x - 1;
+              wait_unless_lost(sv::smem_addr(S.empty + e % kSlots), (e / kSlots) & 1, lost);
               __syncwarp();
               fence_after();
 #pragma unroll 1
-              for (int y = 0; y < H::kOut; y += 16) {
+              for (int y = 0; y < outs; y += 16) {
                 uint32_t o[16];
                 tm_load16(o, to + y);
 #pragma unroll
@@ -409,8 +438,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const sv::f32x2 m2 = sv::pk(m0, m0), c2 = sv::pk(c, c), b2 = sv::pk(b, b);
           sv::f32x2 sum[2] = {sv::pk(0.0f, 0.0f), sv::pk(0.0f, 0.0f)};
 #pragma unroll 1
-          for (int y = 0; y < H::kCols; y += H::kChunk) {
-            if (H::kCols > H::kChunk) load(y);   // read again: all of a row would not fit the registers
+          for (int y = 0; y < cols; y += H::kChunk) {
+            if (cols > H::kChunk) load(y);       // read again: all of a row would not fit the registers
             uint32_t p[H::kChunk / 2];
 #pragma unroll
             for (int z = 0; z < H::kChunk / 2; ++z) {
@@ -423,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               sum[z & 1] = sv::add2(sum[z & 1], sv::pk(p0, p1));
               p[z] = sv::pack2<F16>(p0, p1);
             }
-            tm_store<H::kChunk / 2>(ts + (half * H::kCols + y) / 2, p);
+            tm_store<H::kChunk / 2>(ts + (half * cols + y) / 2, p);
           }
           float s0, s1;
           sv::upk(sv::add2(sum[0], sum[1]), s0, s1);
@@ -435,8 +464,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           // entry are cleared whole.
           unsigned char* vb = dyn + s * H::kSlotBytes;
           const int r0 = max(n - j0, 0);
-          // (Two ways: the first way's warps, whose product comes first, or those that have the tile.)
-          for (int y = r0 * (D / 8) + tid % (kSoft / kWays); (way == 0 || split) && y < kTile * (D / 8); y += kSoft / kWays) {
+          // (Two ways: the first way's warps, whose product comes first.)
+          const int threads = one ? kSoft : kSoft / 2;
+          for (int y = r0 * (D / 8) + tid; way == 0 && y < kTile * (D / 8); y += threads) {
             const int r = y / (D / 8), ch = y % (D / 8);
             uint4* at = reinterpret_cast<uint4*>(vb + (ch >> 3) * (kTile * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
             uint4 v = make_uint4(0u, 0u, 0u, 0u);
@@ -456,7 +486,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (edge) fence_async();
         fence_before();
         __syncwarp();
-        if (lane == 0) sv::mbar_arrive(sv::smem_addr(S.p_ready + w));
+        if (lane == 0) {
+          sv::mbar_arrive(sv::smem_addr(S.p_ready + w));
+          if (kOne && !one) sv::mbar_arrive(sv::smem_addr(S.p_ready + w));   // (it counts the warps of one way)
+        }
       }
       wait_unless_lost(sv::smem_addr(&S.o_full), items & 1, lost);
       __syncwarp();
@@ -465,29 +498,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (odd) atomicOr(&S.flags, 2);
       base += W.count;
       ++items;
+      if (!one) used[way ^ 1] += W.count;      // the other way's
 
       // One way: a row's sum is that of its two threads; each finishes half of the row's columns.
       float* sums = &S.row_max[0][0][0];       // [2][kRows]; the tiles are done with it
-      if (kWays == 1) sums[half * kRows + row] = l;
-      if (kSplit && split) {
-        S.row_max[0][way][row] = l;
-        S.row_max[1][way][row] = mx;
-      }
+      if (one) sums[half * kRows + row] = l;
       sv::named_bar_sync(1, kSoft);
       const int flags = S.flags;
-      // Split: what the two ways' accumulators are multiplied by.
-      float f0 = 1.0f, f1 = 0.0f;
-      if (kSplit && split) {
-        const float m0 = S.row_max[1][0][row], m1 = S.row_max[1][1][row];
-        mx = fmaxf(m0, m1);
-        f0 = m0 == -INFINITY ? 0.0f : sv::ex2((m0 - mx) * c);
-        f1 = m1 == -INFINITY ? 0.0f : sv::ex2((m1 - mx) * c);
-        const float l0 = S.row_max[0][0][row], l1 = S.row_max[0][1][row];
-        l = (m0 == -INFINITY ? l0 : l0 * f0) + (m1 == -INFINITY ? l1 : l1 * f1);   // (the former: 0, or NaN)
-      }
-      const float jl = (flags & 1) ? __int_as_float(0x7fffffff) : (kWays == 1 ? sums[row] + sums[kRows + row] : l);
+      const float jl = (flags & 1) ? __int_as_float(0x7fffffff) : (one ? sums[row] + sums[kRows + row] : l);
       const bool whole = W.count == W.tiles;
-      const int slot = (2 * blockIdx.x + (W.first == 0 ? 1 : 0)) * kWays + (split ? 0 : way);
+      const int slot = (2 * blockIdx.x + (W.first == 0 ? 1 : 0)) * kWays + way;
       size_t to_row = 0;                       // kShared: the result's row, of a side or a part
       if constexpr (kShared) {
         const int r = row0 + row, i = r / R.group;
@@ -498,24 +518,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const size_t at = (static_cast<size_t>(W.row) * R.N + i) * P.Hq + hq;
       const float inv = 1.0f / jl;
 #pragma unroll 1
-      for (int k = 0; k < H::kOut; k += 16) {
-        if (!active || (split && k >= D / 2)) break;
-        // Split: each way's thread of a row finishes half of its columns.
-        const int mycol = split ? way * (D / 2) + k : half * H::kOut + k;
+      for (int k = 0; k < outs; k += 16) {
+        if (!active) break;
+        const int mycol = half * outs + k;
         uint32_t o[16];
-        tm_load16(o, split ? tm + lanes + kAccum + mycol : to + k);
+        tm_load16(o, to + k);
         float f[16];
 #pragma unroll
         for (int z = 0; z < 16; ++z) f[z] = __uint_as_float(o[z]);
-        if (kSplit && split) {
-#pragma unroll
-          for (int z = 0; z < 16; ++z) f[z] *= f0;
-          if (W.count > 1) {                   // (else the second way's accumulator holds something else)
-            tm_load16(o, tm + lanes + kAccum + D + mycol);
-#pragma unroll
-            for (int z = 0; z < 16; ++z) f[z] += __uint_as_float(o[z]) * f1;
-          }
-        }
         // Values that are not finite were left out of the products, where a zero probability would have
         // made NaN of them: they are added to the rows that attend them.
         if (flags & 2) {
@@ -556,15 +566,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (half == 0 && row < rows && !(split && way == 1)) {
+      if (half == 0 && row < rows) {
         if constexpr (kShared) (whole ? P.side_ml : P.part_ml)[to_row] = make_float2(mx, jl);
         else if (!whole) P.part_ml[slot * kRows + row] = make_float2(mx, jl);
         else if (P.lse) P.lse[at] = (mx * c + (log2f(jl) - kBits)) * 0.6931471805599453f;
       }
       fence_before();
       sv::named_bar_sync(1, kSoft);            // the sums have been read
-      if ((tid & 127) == 0 && half == 0 && W.first == 0 && rows > 0 && !(split && way == 1))
-        if constexpr (kShared) sv::tell_shared(P, W.row, W.head, W.q_tile * kWays + way, W.token0, whole, W.item_at, W.tiles, S.plan);
+      if ((tid & 127) == 0 && half == 0 && W.first == 0 && rows > 0)
+        if constexpr (kShared) sv::tell_shared(P, W.row, W.head, W.q_tile * kWays + way, W.tokens, W.token0, whole, W.item_at, W.tiles, S.plan);
         else sv::tell_shared(P, way, W.row, W.head, W.q_tile * kWays + way, rows, whole, W.item_at, W.tiles, S.plan);
     }
     fence_before();
@@ -618,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (x % D == 0 && !whole) P.part_ml[static_cast<size_t>(slot) * kRows + r].y = __int_as_float(0x7fffffff);
         }
         if (tid == 0 && W.first == 0 && rows > 0) {
-          if constexpr (kShared) sv::tell_shared(P, W.row, W.head, q_tile, token0, whole, W.item_at, W.w.tiles, S.plan);
+          if constexpr (kShared) sv::tell_shared(P, W.row, W.head, q_tile, sv::tokens_of(W.w), token0, whole, W.item_at, W.w.tiles, S.plan);
           else sv::tell_shared(P, way, W.row, W.head, q_tile, rows, whole, W.item_at, W.w.tiles, S.plan);
         }
       }

@@ -37,18 +37,21 @@ __device__ __forceinline__ bool row_work(const Round& R, int b, RowWork* w) {
   w->q_tiles = some ? (w->m * R.group + R.q_rows - 1) / R.q_rows : 0;
   return ok;
 }
-__device__ __forceinline__ long long row_units(const Round& R, const RowWork& w) {
-  return static_cast<long long>(w.tiles + R.extra) * w.q_tiles * R.C.heads;
-}
-
 // A batch whose rows share the fronts of their contexts: its work is that of the groups (the queries of all tokens of
 // a group's rows, N a row, against the entries that the rows share, from the first row's table), then that of the rows
 // (a row's tokens against its entries from common[b] on). A group's front is, for the masks, a row's whose last entry
 // is the round's only one: every query attends it.
+// A unit of this batch's work is a fraction of a tile, since tiles of fronts and rows take different times; a tile is its
+// first unit's CTA's.
 struct SharedRound : Round {
   const int32_t* start;                   // [groups + 1]: a group's rows are start[g] .. start[g + 1] - 1
   const int32_t* common;                  // [B]
   int groups;
+  int one_rows;                           // up to so many query rows, an item is worked on with one way
+  int one_units, two_units;               // of a tile on one way, and on two
+  int two_extra;                          // of an item's queries and its end, on two ways; `extra` on one
+  __device__ __forceinline__ bool two_ways(int tokens) const { return tokens * group > one_rows; }
+  __device__ __forceinline__ int units(int tokens) const { return two_ways(tokens) ? two_units : one_units; }
 };
 struct SharedWork : RowWork {
   int tokens, token0;                     // query tokens, the first of them among the batch's B N
@@ -85,6 +88,14 @@ __device__ __forceinline__ bool row_work(const SharedRound& R, int v, SharedWork
   w->q_tiles = some ? static_cast<int>((static_cast<long long>(w->tokens) * R.group + R.q_rows - 1) / R.q_rows) : 0;
   return ok;
 }
+__device__ __forceinline__ int extra_units(const Round& R, const RowWork&) { return R.extra; }
+__device__ __forceinline__ int extra_units(const SharedRound& R, const SharedWork& w) { return R.two_ways(w.tokens) ? R.two_extra : R.extra; }
+__device__ __forceinline__ int item_units(const Round& R, const RowWork& w) { return w.tiles + R.extra; }
+__device__ __forceinline__ int item_units(const SharedRound& R, const SharedWork& w) {
+  return w.tiles * R.units(w.tokens) + extra_units(R, w);
+}
+__device__ __forceinline__ int most_units(const Round&) { return 1; }
+__device__ __forceinline__ int most_units(const SharedRound& R) { return max(R.one_units, R.two_units); }
 __device__ __forceinline__ int work_rows(const Round& R) { return R.B; }
 __device__ __forceinline__ int work_rows(const SharedRound& R) { return R.groups + R.B; }
 // What the two kinds of batches differ in: the tokens of an item's queries, their first one, the tree of its row, and
@@ -107,6 +118,11 @@ __device__ __forceinline__ const int32_t* pages_of(const SharedRound& R, int, co
 }
 __device__ __forceinline__ int tokens_of(const RowWork& w) { return w.m; }
 __device__ __forceinline__ int tokens_of(const SharedWork& w) { return w.tokens; }
+
+template <class Rows, class Work>
+__device__ __forceinline__ long long row_units(const Rows& R, const Work& w) {
+  return static_cast<long long>(item_units(R, w)) * w.q_tiles * R.C.heads;
+}
 
 struct Plan {
   long long total;                        // units of the batch
@@ -145,7 +161,9 @@ __device__ void make_plan(const Rows& R, long long (&sh)[kThreads / 32], Plan* p
     if (x < warp) before += sh[x];
     total += sh[x];
   }
-  const long long parts = total < gridDim.x ? total : gridDim.x;
+  // (Every run has a tile's first unit where it is inside an item.)
+  const long long runs = kShared ? max(total / most_units(R), min(total, 1ll)) : total;
+  const long long parts = runs < gridDim.x ? runs : gridDim.x;
   const long long at = blockIdx.x < parts ? total * blockIdx.x / parts : total;
   if (tid == 0) {
     plan->total = total;
@@ -200,15 +218,21 @@ struct WalkOf {
         ++row;
         row_work(R, row, &w);
       }
-      const int per = w.tiles + R.extra;
+      const int per = item_units(R, w), extra = extra_units(R, w);
       const Unit in_row = static_cast<Unit>(at - row_at);
       const int item = static_cast<int>(in_row / per), in_item = static_cast<int>(in_row - static_cast<Unit>(item) * per);
       head = item / w.q_tiles;
       q_tile = item - head * w.q_tiles;
-      item_at = at - in_item + R.extra;
+      item_at = at - in_item + extra;
       const int stop = end - at < per - in_item ? in_item + static_cast<int>(end - at) : per;
-      first = in_item > R.extra ? in_item - R.extra : 0;
-      count = stop - R.extra - first;
+      first = in_item > extra ? in_item - extra : 0;
+      if constexpr (kShared) {
+        const int u = R.units(w.tokens);
+        first = (first + u - 1) / u;
+        count = stop > extra ? (stop - extra + u - 1) / u - first : 0;
+      } else {
+        count = stop - extra - first;
+      }
       at += stop - in_item;
     } while (count <= 0);                 // the run ended before the item's first tile
     return true;
