@@ -200,13 +200,12 @@ def _starts(group_start, device):
     return _small(group_start, "group_start", torch.int32, group_start.shape, device), group_start.shape[0] - 1
 
 
-def _shared_attention(q, cache, prefix_len, shared_len, group_start, num_queries, tree_parents, N, Hq, rs, ts, out,
+def _shared_attention(q, cache, prefix_len, shared_len, start, groups, num_queries, tree_parents, N, Hq, rs, ts, out,
                       out_lse, workspace, workspace_bytes, scale, stream):
     import torch
     dev, B, i32 = cache.device, cache.B, torch.int32
     if B > 1 and N > 1 and rs != N * ts:
         raise ValueError(f"the rows of q must follow one another: strides {q.stride()}")
-    start, groups = _starts(group_start, dev)
     _call(lib().spec_verify_shared_attention, cache, stream, q.data_ptr(), rs, ts, cache.ref,
           _small(prefix_len, "prefix_len", i32, (B,), dev), _small(shared_len, "shared_len", i32, (B,), dev), start, groups,
           _small(num_queries, "num_queries", i32, (B,), dev), _small(tree_parents, "tree_parents", i32, (B, N), dev),
@@ -224,7 +223,7 @@ def spec_verify_shared_attention(q, cache, prefix_len, shared_len, group_start, 
     N, Hq, rs, ts = _tokens(q, "q", cache)
     if workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous and on {dev}")
-    _shared_attention(q, cache, prefix_len, shared_len, group_start, num_queries, tree_parents, N, Hq, rs, ts,
+    _shared_attention(q, cache, prefix_len, shared_len, *_starts(group_start, dev), num_queries, tree_parents, N, Hq, rs, ts,
                       _small(out, "out", cache.dtype, (B, N, Hq, cache.head_dim), dev),
                       _small(out_lse, "out_lse", torch.float32, (B, N, Hq), dev), workspace.data_ptr(),
                       workspace.nbytes, scale, stream)
@@ -285,10 +284,11 @@ def attend_shared(q, cache, prefix_len, shared_len, group_start, num_queries=Non
             return attend_shared(q, cache, prefix_len, shared_len, group_start, num_queries, tree_parents, scale)
     N, Hq, rs, ts = _tokens(q, "q", cache)
     _on_gpu(cache.device)
+    start, groups = _starts(group_start, cache.device)
     out = torch.empty((cache.B, N, Hq, cache.head_dim), dtype=q.dtype, device=cache.device)
     lse = torch.empty((cache.B, N, Hq), dtype=torch.float32, device=cache.device)
     with _attend_lock:
-        ws = _attend_workspace(N, Hq, cache, _starts(group_start, cache.device)[1])
-        _shared_attention(q, cache, prefix_len, shared_len, group_start, num_queries, tree_parents, N, Hq, rs, ts,
+        ws = _attend_workspace(N, Hq, cache, groups)
+        _shared_attention(q, cache, prefix_len, shared_len, start, groups, num_queries, tree_parents, N, Hq, rs, ts,
                           out.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.nbytes, scale, None)
     return out, lse

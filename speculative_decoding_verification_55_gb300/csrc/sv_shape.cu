@@ -101,7 +101,7 @@ __device__ __forceinline__ unsigned listed(int place, bool special, int16_t coun
 
 // kW: tokens of a thread, 8 or (rows that are not of whole words) 1; kU: groups of a thread.
 template <typename T, int kW, int kU>
-__global__ void __launch_bounds__(kThreads, 5) sv_shape_kernel(const ShapeParams P) {
+__global__ void __launch_bounds__(kThreads, 6) sv_shape_kernel(const ShapeParams P) {
   using G = Group<T, kW>;
   constexpr int kSpan = kThreads * kW * kU;    // tokens of a CTA
   constexpr unsigned kAll = (1u << kW) - 1;
@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, 5) sv_shape_kernel(const ShapeParams
           put(to, all);
         } else if (kW == 8 && bar) {
           // Barred in part: read and written where that is fewer accesses than the barred ones alone.
-          if (__popc(bar) > 2 && __popc(bar) < 6) {
+          if (__popc(bar) > 2 && __popc(bar) < 7) {
             G z = *reinterpret_cast<const G*>(to);
 #pragma unroll
             for (int k = 0; k < kW; ++k)
@@ -221,15 +221,15 @@ __global__ void __launch_bounds__(kThreads, 5) sv_shape_kernel(const ShapeParams
   }
   __syncthreads();
 
-  // 32 of the list's tokens a warp, at as many positions as leave every warp some (all of them where the list is long):
-  // their logits are in flight together.
-  constexpr int kWarps = kThreads / 32;
-  const int len = length, segments = (len + 31) >> 5;
-  const int step = segments >= kWarps ? here : (here * segments + kWarps - 1) / kWarps;
-  const int units = segments ? segments * ((here + step - 1) / step) : 0;
-  for (int x = warp; x < units; x += kWarps) {
-    const int y0 = x / segments * step, l = x % segments * 32 + lane, steps = min(step, here - y0);
-    if (l >= len) continue;
+  // A token of the list a lane, at one position, or at more of them where the list is long: their logits are then in
+  // flight together.
+  const int len = length;
+  if (len == 0) return;
+  const int step = min(max(len * here / kThreads, 1), here), items = len * ((here + step - 1) / step);
+  const unsigned inv = 0xffffffffu / len + 1;  // (x inv / 2^32 is x / len for x len < 2^32; 1 / 1 is 2^32)
+  for (int x = tid; x < items; x += kThreads) {
+    const int block = len == 1 ? x : __umulhi(x, inv), l = x - block * len;
+    const int y0 = block * step, steps = min(step, here - y0);
     const unsigned e = list[l];
     const int place = e & (kSpecial - 1), n = (e >> 16) & 32767;
     T* const at = row + static_cast<size_t>(y0) * P.V + place;
@@ -274,11 +274,14 @@ __global__ void __launch_bounds__(kThreads, 5) sv_shape_kernel(const ShapeParams
 
 template <typename T>
 int launch_shape(ShapeParams& P, bool whole, int sms, cudaStream_t st) {
-  // Two groups a thread where that still leaves eight CTAs an SM, else one.
-  P.blocks = (P.N + kPositions - 1) / kPositions;
-  P.per = (P.N + P.blocks - 1) / P.blocks;
-  const long long groups = static_cast<long long>(P.B) * P.blocks * ((P.V + 7) / 8);
-  const bool two = whole && groups / (2 * kThreads) >= 8ll * sms;
+  // Blocks of at most kPositions positions, and so many that there are four CTAs an SM (8 rows of 5 positions, V 32000,
+  // open masks: 9.2 us so, 12.3 with blocks of 5); two groups a thread where that still leaves eight (64 rows of 6 positions,
+  // V 128256, narrow masks: 28 us so, 30 with one).
+  const long long runs = static_cast<long long>(P.B) * ((P.V - 1) / (8 * kThreads) + 1);
+  P.per = (P.N - 1) / ((P.N - 1) / kPositions + 1) + 1;
+  if (runs * P.N < 4ll * sms * P.per) P.per = static_cast<int>(runs * P.N / (4ll * sms)) + 1;
+  P.blocks = (P.N - 1) / P.per + 1;
+  const bool two = whole && runs * P.blocks >= 16ll * sms;
   const int span = kThreads * (two ? 16 : 8);
   const long long grid = static_cast<long long>(P.B) * ((P.V + span - 1) / span) * P.blocks;
   if (grid > 0x7fffffffll) return SV_ERR_BAD_SHAPE;
