@@ -370,16 +370,15 @@ int spec_verify_paged_attention(const void* q, int64_t q_row_stride, int64_t q_t
  *
  * q              [B, N, Hq, D] as there; its rows follow one another (q_row_stride = N * q_token_stride where B and N are
  *                above 1, else SV_ERR_BAD_SHAPE: a slice of a fused projection has it)
- * shared_len     [B] int32: the first shared_len[b] entries of row b are those of its group's first row, in the first
- *                row's pages (a row's own page numbers for them are not read). A multiple of page_size, at most
+ * shared_len     [B] int32: the first shared_len[b] entries of row b are those of its group's first row, and its page table
+ *                begins with the same page numbers (either row's may be read). A multiple of page_size, at most
  *                prefix_len[b], and within a group the same; or 0, for a row that attends its own entries alone.
  * group_start    [groups + 1] int32, ascending from at least 0 to at most B: group g is rows group_start[g] ..
  *                group_start[g + 1] - 1 (it may be empty). Rows in no group have shared_len 0.
  * workspace      spec_verify_shared_attention_workspace_size(...) bytes, 256-byte aligned, without setup: among them two
  *                fp32 results of each query, 8 B N Hq (D + 2) bytes. One workspace serves one call at a time.
- * A row whose shared_len is none of that is in error; all are where group_start does not ascend within 0 .. B. A page
- * number out of range in a front puts NaN into the outputs of all its rows' tokens.
- * B N Hq <= 2^28. Two launches. Other arguments, errors and limits as in spec_verify_paged_attention. */
+ * A row whose shared_len is none of that is in error; all are where group_start does not ascend within 0 .. B.
+ * B N Hq <= 2^28. Two or three launches. Other arguments, errors and limits as in spec_verify_paged_attention. */
 size_t spec_verify_shared_attention_workspace_size(int32_t B, int32_t N, int32_t Hq, int32_t groups,
                                                    const sv_paged_cache* cache);
 int spec_verify_shared_attention(const void* q, int64_t q_row_stride, int64_t q_token_stride,

@@ -38,16 +38,16 @@ struct SharedParams : AttendParamsOf<true> {
   int2* records;                               // (by record_at) first and last CTA; first -1: one CTA has all of it
   int4* rows;                                  // [B] a row's tokens (-1: in error), its group, the group's first token, shared_len
   int* bad_groups;                             // not 0: group_start does not ascend within 0 .. B
-  int own_tiles, front_tiles;                  // records of a row's key head; of the fronts' key head
+  int front_tiles;                             // records of a key head's fronts (a row's key head has one: one query tile)
   __device__ __forceinline__ size_t side_at(int side, size_t at) const {
     return static_cast<size_t>(side) * R.B * R.N * Hq + at;
   }
   // The rows' records, then the fronts': group g, whose first token is token0, has its from token0 x group / tile_rows
   // + g on (its last query tile may be short, which the + g makes up for).
   __device__ __forceinline__ size_t record_at(int row, int head, int q_tile, int token0) const {
-    const size_t own = static_cast<size_t>(R.B) * R.C.heads * own_tiles;
-    if (row >= R.groups) return (static_cast<size_t>(row - R.groups) * R.C.heads + head) * own_tiles + q_tile;
-    return own + static_cast<size_t>(head) * front_tiles + token0 * R.group / tile_rows + row + q_tile;
+    if (row >= R.groups) return static_cast<size_t>(row - R.groups) * R.C.heads + head;
+    return static_cast<size_t>(R.B) * R.C.heads + static_cast<size_t>(head) * front_tiles +
+           token0 * R.group / tile_rows + row + q_tile;
   }
   // Row r of a part, among all of them ([2 grid][ways][128]): the part of CTA p in an item that begins in CTA first.
   __device__ __forceinline__ size_t part_row(int p, int first, int way, int r) const {

@@ -6,9 +6,13 @@
 //   M = max(m_A, m_B),  L = l_A e^(m_A - M) + l_B e^(m_B - M),  out = (o_A e^(m_A - M) + o_B e^(m_B - M)) / L.
 // A of all the group's rows and tokens is one set of products with the group's keys and values, read once for up to
 // 128 or 256 query rows, not once a row. One launch of the wide kernel (sv_attend_wide.cuh) does the fronts and the
-// rows' own entries, cut into equal runs of tiles, whose results, of several CTAs where an item is cut, the merge kernel
-// here puts together, a query a warp.
-// Bound: the bytes of the entries, each read once, or for large groups the products (4 D a query head and entry).
+// rows' own entries, cut into runs of equal time, whose results, of several CTAs where an item is cut, the merge kernel
+// here puts together, a query or four a warp.
+// Bound: the bytes of the entries, each read once, or for large groups the products (4 D a query head and entry). 64 rows
+// of one token over 8000 shared and 17 to 1000 own entries, 32/8 heads of 128: 58 us (floor 25; 225 by rows that each read
+// all of it): 45 of the attention, of which about 14 are its start and end, then the merge.
+// Two launches of each (the fronts, their join, the rows' own entries with the front added at an item's end, their join)
+// took 99 us: each launch's start and end cost more than the rows' own entries gained by kernels of their own.
 // Rounding: the sides are fp32 sums and maxima; the output is rounded once.
 
 #include <algorithm>
@@ -24,7 +28,7 @@ constexpr int kMergeWarps = kQueries == 1 ? 16 : 8;
 // What the plan takes a tile and an item (its queries and its end) to cost, in units of 0.25 us: a tile on two ways 2 us,
 // on one about what its bytes take from HBM among other CTAs' products. (All tiles alike and an item two of them: 64 rows
 // of one token over 8000 shared entries 78 us against 61, two prompts' rounds of 9 tokens 113 against 92. One-way tiles at
-// 3 units 64 and 102; items at 8 where they have two ways: trees of 31 over three documents 86 us against 80.)
+// 3 or 5 units, items at 6 to 20: 61 to 65 and 93 to 98.)
 constexpr int kTwoWays = 8, kOneWay = 4, kOneItem = 10, kTwoItem = 15;
 
 // A warp has kQueries of a key head's query heads at one token: they have the same items, and rows of these that follow
@@ -57,10 +61,9 @@ __global__ void __launch_bounds__(32 * kMergeWarps<kQueries>) sv_attend_merge_ke
   }
   if (there && i < m) {
     // Where the two items have their records, and the first query's row of their query tiles.
-    int row_own = i * R.group + h0, row_front = 0, tile_front = 0;
-    const int tile_own = row_own / P.tile_rows;
-    row_own -= tile_own * P.tile_rows;
-    const int2 oo = __ldcg(P.records + P.record_at(R.groups + b, head, tile_own, 0));
+    int row_front = 0, tile_front = 0;
+    const int row_own = i * R.group + h0;
+    const int2 oo = __ldcg(P.records + P.record_at(R.groups + b, head, 0, 0));
     int2 of = make_int2(0, -1);
     if (s > 0) {
       row_front = (token - row.z) * R.group + h0;
@@ -79,7 +82,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps<kQueries>) sv_attend_merge_ke
         const int2 rec = front ? of : oo;
         const int p = rec.x + (front ? k : k - fronts);
         const size_t from = rec.x < 0 ? P.side_at(front ? 0 : 1, at)
-                                      : P.part_row(p, rec.x, (front ? tile_front : tile_own) % P.ways, front ? row_front : row_own);
+                                      : P.part_row(p, rec.x, front ? tile_front % P.ways : 0, front ? row_front : row_own);
 #pragma unroll
         for (int q = 0; q < kQueries; ++q) {
           const bool real = k < all && q < queries;
@@ -172,6 +175,28 @@ int merge(const SharedParams& P, cudaStream_t st) {
   return D == 64 ? merge<F16, 64>(P, st) : (D == 128 ? merge<F16, 128>(P, st) : merge<F16, 256>(P, st));
 }
 
+// Where rows attend all of their entries by themselves: NaN for the rows whose shared_len is none, or all where
+// group_start does not ascend.
+constexpr int kMarkThreads = 256;
+__global__ void __launch_bounds__(kMarkThreads) sv_attend_mark_kernel(const SharedParams P, int D) {
+  const sv::SharedRound& R = P.R;
+  const int tid = threadIdx.x;
+  bool all = false;
+  for (int g = tid; g <= R.groups; g += kMarkThreads) {
+    const int e = __ldg(R.start + g);
+    all |= e > R.B || (g == 0 ? e < 0 : __ldg(R.start + g - 1) > e);
+  }
+  all = __syncthreads_or(all);
+  for (int b = blockIdx.x; b < R.B; b += gridDim.x) {
+    if (!all && sv::row_of_group(R, b).x >= 0) continue;
+    const size_t queries = static_cast<size_t>(R.N) * P.Hq;
+    uint4* o = reinterpret_cast<uint4*>(P.out) + b * queries * D / 8;
+    for (size_t x = tid; x < queries * D / 8; x += kMarkThreads) o[x] = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+    if (P.lse)
+      for (size_t x = tid; x < queries; x += kMarkThreads) P.lse[b * queries + x] = __int_as_float(0x7fffffff);
+  }
+}
+
 constexpr int kMaxSms = 160;
 constexpr size_t kFlagBytes = 256;
 constexpr long long kMaxQueries = 1ll << 28;   // query heads of all tokens
@@ -182,8 +207,7 @@ bool sizes_ok(int32_t B, int32_t N, int32_t Hq, const sv_paged_cache* c) {
 }
 size_t rounded(size_t bytes) { return (bytes + 255) / 256 * 256; }
 size_t part_rows(int D) { return static_cast<size_t>(2 * kMaxSms) * (D < 256 ? 2 : 1) * 128; }
-// Query tiles of a row's key head, and of the fronts' (each group's last may be short).
-int own_tiles(int N, int group) { return (N * group - 1) / (128 / group * group) + 1; }
+// Query tiles of a key head's fronts, at most (each group's last may be short).
 long long front_tiles(long long queries, int groups, int group) { return queries / (128 / group * group) + groups + 1; }
 
 }  // namespace
@@ -202,9 +226,10 @@ extern "C" size_t spec_verify_shared_attention_workspace_size(int32_t B, int32_t
   if (!cache || !sizes_ok(B, N, Hq, cache) || cache->head_dim < 1 || cache->head_dim > 256 || groups < 1 || groups > (1 << 20)) return 0;
   const int D = cache->head_dim, heads = cache->heads, group = Hq / heads;
   const size_t row = D * 4 + 8, queries = static_cast<size_t>(B) * N * Hq;
-  const size_t records = static_cast<size_t>(heads) * (static_cast<size_t>(B) * own_tiles(N, group) +
-                                                       front_tiles(static_cast<long long>(B) * N * group, groups, group));
-  return kFlagBytes + rounded(static_cast<size_t>(B) * sizeof(int4)) + rounded(records * sizeof(int2)) + rounded(part_rows(D) * row) + rounded(2 * queries * row);
+  const size_t records = static_cast<size_t>(heads) * (B + front_tiles(static_cast<long long>(B) * N * group, groups, group));
+  return std::max(spec_verify_paged_attention_workspace_size(N, Hq, cache),
+                  kFlagBytes + rounded(static_cast<size_t>(B) * sizeof(int4)) + rounded(records * sizeof(int2)) +
+                      rounded(part_rows(D) * row) + rounded(2 * queries * row));
 }
 
 extern "C" int spec_verify_shared_attention(const void* q, int64_t q_row_stride, int64_t q_token_stride,
@@ -213,8 +238,8 @@ extern "C" int spec_verify_shared_attention(const void* q, int64_t q_row_stride,
                                             const int32_t* num_queries, const int32_t* tree_parents, float scale, void* out,
                                             float* out_lse, int32_t B, int32_t N, int32_t Hq, void* workspace,
                                             size_t workspace_bytes, void* cuda_stream) {
-  SharedParams P;
-  int st = sv::check_cache(cache, B, false, &P.R.C);
+  sv::Cache C;
+  int st = sv::check_cache(cache, B, false, &C);
   if (st != SV_OK) return st;
   if (!q || !prefix_len || !shared_len || !group_start || !out) return SV_ERR_NULL_POINTER;
   st = sv::check_tokens(q, q_row_stride, q_token_stride, B, N, Hq, cache->head_dim);
@@ -233,6 +258,7 @@ extern "C" int spec_verify_shared_attention(const void* q, int64_t q_row_stride,
                    {shared_len, rows}, {group_start, 4ull * groups + 4}, {num_queries, rows}, {tree_parents, rows * N},
                    sv::table_of(cache, B), sv::weights_of(cache), sv::pages_of(cache, cache->k), sv::pages_of(cache, cache->v)}))
     return SV_ERR_OVERLAP;
+  SharedParams P;
   int dev = 0;
   st = sv::current_device_status(&dev);
   if (st != SV_OK) return st;
@@ -240,6 +266,34 @@ extern "C" int spec_verify_shared_attention(const void* q, int64_t q_row_stride,
   if (sms < 1) return SV_ERR_CUDA;
   if (sms > kMaxSms) sms = kMaxSms;
   const int D = cache->head_dim, group = Hq / cache->heads, rows_tile = 128 / group * group;
+  const cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+  P.R.C = C;
+  P.R.prefix = prefix_len;
+  P.R.num = num_queries;
+  P.R.B = B;
+  P.R.N = N;
+  P.R.group = group;
+  P.R.none_ok = false;
+  P.R.start = group_start;
+  P.R.common = shared_len;
+  P.R.groups = groups;
+  P.out = out;
+  P.lse = out_lse;
+  P.Hq = Hq;
+  // A group's queries fill the query tiles that its front is read for; so do a row's where they are more than half of one.
+  // Then the products take the time, a front's second reading comes from L2 or is hidden behind them, and the rows go by
+  // themselves (which also leaves out the tokens behind a row's: a front's tiles have them all). Measured over 24 rows in
+  // two groups with up to 600 entries of their own, 4 key heads of 128, by fronts against by rows, tokens behind a row's
+  // among them: fronts of 4000 entries, 4 query rows a row and key head 29 against 39 us, 36 rows 45 against 43, 72 rows
+  // 59 against 43; fronts of 32,000, 36 rows 92 against 188, 144 rows 248 against 213; heads of 256, fronts of 4000,
+  // 36 rows 57 against 72, 72 rows 84 against 74.
+  if (2 * N * group > 128) {
+    st = spec_verify_paged_attention(q, q_row_stride, q_token_stride, cache, prefix_len, num_queries, tree_parents, scale, out,
+                                     out_lse, B, N, Hq, workspace, workspace_bytes, cuda_stream);
+    if (st != SV_OK) return st;
+    sv_attend_mark_kernel<<<std::min(B, 4 * sms), kMarkThreads, 0, s>>>(P, D);
+    return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+  }
   // Two query tiles at once where a group has more than one's rows.
   const long long all = static_cast<long long>(B) * N * group;
   const int ways = D < 256 && all > static_cast<long long>(groups) * rows_tile ? 2 : 1;
@@ -250,11 +304,6 @@ extern "C" int spec_verify_shared_attention(const void* q, int64_t q_row_stride,
   if (st == SV_OK)
     st = sv::query_tensor_map(q, 0, N > 1 ? q_token_stride : q_row_stride, 1, B * N, Hq, D, cache->dtype, group, q_tokens, &qmap);
   if (st != SV_OK) return st;
-  P.R.prefix = prefix_len;
-  P.R.num = num_queries;
-  P.R.B = B;
-  P.R.N = N;
-  P.R.group = group;
   P.R.q_rows = rows_tile * ways;
   P.R.tile_log2 = D == 256 ? 6 : 7;
   P.R.one_rows = ways == 2 ? rows_tile : static_cast<int>(kMaxQueries);
@@ -262,26 +311,18 @@ extern "C" int spec_verify_shared_attention(const void* q, int64_t q_row_stride,
   P.R.two_units = kTwoWays;
   P.R.extra = kOneItem;
   P.R.two_extra = kTwoItem;
-  P.R.none_ok = false;
-  P.R.start = group_start;
-  P.R.common = shared_len;
-  P.R.groups = groups;
   P.q = static_cast<const char*>(q);
   P.row_stride = q_row_stride * 2;
   P.token_stride = q_token_stride * 2;
   P.parents = tree_parents;
-  P.out = out;
-  P.lse = out_lse;
   P.c = scale * sv::kLog2e;
-  P.Hq = Hq;
   P.tile_rows = rows_tile;
   P.ways = ways;
   P.by_item = 0;
-  P.own_tiles = own_tiles(N, group);
   P.front_tiles = static_cast<int>(front_tiles(all, groups, group));
   // As many CTAs as the GPU holds, or as many as the batch can have tiles.
   const long long tile = 1 << P.R.tile_log2;
-  const long long items = static_cast<long long>(cache->heads) * (static_cast<long long>(B) * P.own_tiles + P.front_tiles);
+  const long long items = static_cast<long long>(cache->heads) * (B + P.front_tiles);
   const long long most = items * ((static_cast<long long>(cache->max_pages) * cache->page_size + tile - 1) / tile);
   const int grid = static_cast<int>(std::min<long long>(most, sms));
   char* ws = static_cast<char*>(workspace);
@@ -291,13 +332,12 @@ extern "C" int spec_verify_shared_attention(const void* q, int64_t q_row_stride,
   P.rows = reinterpret_cast<int4*>(ws);
   ws += rounded(static_cast<size_t>(B) * sizeof(int4));
   P.records = reinterpret_cast<int2*>(ws);
-  ws += rounded(static_cast<size_t>(cache->heads) * (static_cast<size_t>(B) * P.own_tiles + P.front_tiles) * sizeof(int2));
+  ws += rounded(static_cast<size_t>(items) * sizeof(int2));
   P.part_o = reinterpret_cast<float*>(ws);
   P.part_ml = reinterpret_cast<float2*>(P.part_o + part_rows(D) * D);
   ws += rounded(part_rows(D) * (D * 4 + 8));
   P.side_o = reinterpret_cast<float*>(ws);
   P.side_ml = reinterpret_cast<float2*>(P.side_o + static_cast<size_t>(2) * B * N * Hq * D);
-  const cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   const bool f16 = cache->dtype == SV_DTYPE_F16;
   st = sv::launch_attend_shared(P, f16, kmap, vmap, qmap, q_tokens, grid, s);
   if (st != SV_OK) return st;

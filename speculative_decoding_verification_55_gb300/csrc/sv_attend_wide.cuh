@@ -82,30 +82,10 @@ template <int D, int kWays>
 constexpr int kSmemBytes = Shape<D, kWays>::kSlots * Shape<D, kWays>::kSlotBytes + Shape<D, kWays>::kQueryBytes +
                            sizeof(Control<Shape<D, kWays>::kSlots>);
 
-// For the merge kernel: what there is to a row, and its group (by bisection of the starts, which ascend).
+// For the merge kernel: what there is to the rows.
 __device__ __forceinline__ void tell_rows(const sv::SharedParams& P, int tid) {
-  const sv::SharedRound& R = P.R;
 #pragma unroll 1
-  for (int b = tid * gridDim.x + blockIdx.x; b < R.B; b += 32 * kCopyWarps * gridDim.x) {
-    sv::SharedWork w;
-    const bool ok = sv::row_work(R, R.groups + b, &w);
-    const int s = __ldg(R.common + b);
-    int4 e = make_int4(ok ? w.m : -1, 0, 0, s);
-    if (s != 0) {
-      int lo = 0, hi = R.groups + 1;                   // how many of the starts are at most b
-#pragma unroll 1
-      while (lo < hi) {
-        const int at = (lo + hi) >> 1;
-        if (__ldg(R.start + at) <= b) lo = at + 1;
-        else hi = at;
-      }
-      const int a = lo > 0 && lo <= R.groups ? __ldg(R.start + lo - 1) : -1;
-      if (a < 0 || a > b || __ldg(R.common + a) != s) e.x = -1;
-      e.y = lo - 1;
-      e.z = a * R.N;
-    }
-    P.rows[b] = e;
-  }
+  for (int b = tid * gridDim.x + blockIdx.x; b < P.R.B; b += 32 * kCopyWarps * gridDim.x) P.rows[b] = sv::row_of_group(P.R, b);
 }
 
 // 32 bytes at once: a thread's own row, whose neighbours are other threads'.

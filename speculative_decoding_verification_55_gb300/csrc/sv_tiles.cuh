@@ -88,6 +88,28 @@ __device__ __forceinline__ bool row_work(const SharedRound& R, int v, SharedWork
   w->q_tiles = some ? static_cast<int>((static_cast<long long>(w->tokens) * R.group + R.q_rows - 1) / R.q_rows) : 0;
   return ok;
 }
+// A row's tokens (-1: in error), its group (by bisection of the starts, which ascend), the group's first token, and what
+// it shares.
+__device__ __forceinline__ int4 row_of_group(const SharedRound& R, int b) {
+  SharedWork w;
+  const bool ok = row_work(R, R.groups + b, &w);
+  const int s = __ldg(R.common + b);
+  int4 e = make_int4(ok ? w.m : -1, 0, 0, s);
+  if (s != 0) {
+    int lo = 0, hi = R.groups + 1;        // how many of the starts are at most b
+#pragma unroll 1
+    while (lo < hi) {
+      const int at = (lo + hi) >> 1;
+      if (__ldg(R.start + at) <= b) lo = at + 1;
+      else hi = at;
+    }
+    const int a = lo > 0 && lo <= R.groups ? __ldg(R.start + lo - 1) : -1;
+    if (a < 0 || a > b || __ldg(R.common + a) != s) e.x = -1;
+    e.y = lo - 1;
+    e.z = a * R.N;
+  }
+  return e;
+}
 __device__ __forceinline__ int extra_units(const Round& R, const RowWork&) { return R.extra; }
 __device__ __forceinline__ int extra_units(const SharedRound& R, const SharedWork& w) { return R.two_ways(w.tokens) ? R.two_extra : R.extra; }
 __device__ __forceinline__ int item_units(const Round& R, const RowWork& w) { return w.tiles + R.extra; }

@@ -58,7 +58,7 @@ def batch(sv, fronts, rows, own, N, H, G, D, seed):
 
 
 @pytest.mark.parametrize("fronts,rows,own,N,H,G,D", [
-    ((8000,), 64, 300, 1, 2, 4, 128), ((4000, 320, 0), 20, 150, 9, 2, 4, 128), ((1600, 1600), 4, 40, 31, 1, 8, 64),
+    ((8000,), 64, 300, 1, 2, 4, 128), ((4000, 320, 0), 20, 150, 9, 2, 4, 128), ((1600, 1600), 4, 40, 31, 1, 2, 64), ((1600, 320), 4, 40, 31, 1, 8, 128),
     ((30000,), 3, 10, 1, 1, 8, 256), ((64,) * 40, 5, 20, 5, 2, 8, 64),
 ])
 def test_shared_attention_gives_up(sv, hasty, fronts, rows, own, N, H, G, D):

@@ -102,18 +102,14 @@ def sv():
 
 
 def with_fronts(a, start, fronts):
-    """The rows of each group begin with the pages of its first row: shared_len [B]. The other rows' table entries for
-    the front become numbers out of range in the call's table, which the call must not read."""
+    """The rows of each group begin with the pages of its first row: (shared_len [B], a copy of the table)."""
     common = np.zeros(len(a.prefix), np.int32)
-    call = a.table.copy()
     for g, s in enumerate(fronts):
         rows = slice(start[g], start[g + 1])
         common[rows] = s
         if start[g] < start[g + 1]:
             a.table[rows, :s // a.S] = a.table[start[g], :s // a.S]
-            call[rows, :s // a.S] = -5
-            call[start[g], :s // a.S] = a.table[start[g], :s // a.S]
-    return common, call
+    return common, a.table.copy()
 
 
 def attend_shared(sv, a, common, call, start, num=None, parents=None, scale=None):
@@ -132,6 +128,8 @@ CASES = [
     ((257, 300, 270), (0, 3), (256,), 4, 1, 16, 256, 32, "bf16", True),
     ((64, 150), (0, 2), (64,), 17, 2, 3, 256, 16, "f16", False),
     ((140, 300, 170), (0, 3), (128,), 31, 1, 8, 128, 16, "bf16", False),
+    ((140, 300, 170, 128, 200), (0, 5), (128,), 31, 2, 2, 128, 16, "bf16", False),
+    ((100, 80, 90, 95), (0, 3, 4), (64, 80), 64, 1, 1, 64, 16, "f16", True),
     ((530, 512), (0, 2), (512,), 65, 2, 2, 64, 128, "bf16", True),
     ((300, 257), (0, 2), (256,), 3, 1, 128, 128, 256, "f16", False),
     ((2100, 2049, 2500, 2048), (0, 4), (2048,), 2, 1, 5, 128, 16, "bf16", False),
@@ -221,7 +219,7 @@ def test_gpu_row_errors(sv):
     check_attention(a, out, lse, a.prefix, num, None)
     num = np.array([3, 1, 2, 3, 0, 3, 2], np.int32)
     common, call = with_fronts(a, start, (32, 32))
-    call[0, 1] = 1 << 29                       # in the first group's front
+    call[:6, 1] = 1 << 29                      # in the first group's front
     out, lse = attend_shared(sv, a, common, call, start, num)
     o, z = host(out), host(lse)
     for b in range(6):
@@ -242,17 +240,19 @@ def test_gpu_row_errors(sv):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("start", [(0, 5, 3, 7), (-1, 7), (0, 8), (2, 1)])
-def test_gpu_groups_in_error(sv, start):
-    a = Batch((40,) * 7, 2, 1, 4, 64, 16, seed=4, poison=False)
+@pytest.mark.parametrize("N,G", [(2, 4), (31, 8)])
+def test_gpu_groups_in_error(sv, start, N, G):
+    a = Batch((40,) * 7, N, 1, G, 64, 16, seed=4, poison=False)
     out, lse = attend_shared(sv, a, np.full(7, 32, np.int32), a.table, start)
     assert np.isnan(host(out)).all() and np.isnan(host(lse)).all()
 
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("common", [8, 24, -16, 48, 1 << 30, -(1 << 31)])
-def test_gpu_fronts_in_error(sv, common):
+@pytest.mark.parametrize("N,G", [(2, 4), (31, 8)])
+def test_gpu_fronts_in_error(sv, common, N, G):
     """Not whole pages, below zero, longer than the rows."""
-    a = Batch((40,) * 4, 2, 1, 4, 64, 16, seed=4, poison=False)
+    a = Batch((40,) * 4, N, 1, G, 64, 16, seed=4, poison=False)
     out, lse = attend_shared(sv, a, np.array([common] * 3 + [0], np.int32), a.table, (0, 3))
     assert np.isnan(host(out)[:3]).all() and np.isnan(host(lse)[:3]).all() and np.isfinite(host(out)[3]).all()
 
