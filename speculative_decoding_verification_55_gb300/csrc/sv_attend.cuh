@@ -49,10 +49,6 @@ struct SharedParams : AttendParamsOf<true> {
     return static_cast<size_t>(R.B) * R.C.heads + static_cast<size_t>(head) * front_tiles +
            token0 * R.group / tile_rows + row + q_tile;
   }
-  // Row r of a part, among all of them ([2 grid][ways][128]): the part of CTA p in an item that begins in CTA first.
-  __device__ __forceinline__ size_t part_row(int p, int first, int way, int r) const {
-    return (static_cast<size_t>(2 * p + (p == first)) * ways + way) * 128 + r;
-  }
 };
 template <bool kShared>
 using ParamsOf = typename std::conditional<kShared, SharedParams, AttendParams>::type;

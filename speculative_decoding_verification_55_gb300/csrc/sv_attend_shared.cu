@@ -72,30 +72,40 @@ __global__ void __launch_bounds__(32 * kMergeWarps<kQueries>) sv_attend_merge_ke
       of = __ldcg(P.records + P.record_at(row.y, head, tile_front, row.z));
     }
     const int fronts = of.x < 0 ? 1 : of.y - of.x + 1, all = fronts + (oo.x < 0 ? 1 : oo.y - oo.x + 1);
-    constexpr int kBatch = kQueries == 1 ? 4 : 1;        // parts in flight together
+    // The k-th result's first row: a side's, or part k's of those that share the item (the first of them is the later
+    // of its CTA's two).
+    const int part = P.ways * 128;
+    const size_t row_a = of.x < 0 ? P.side_at(0, at) : static_cast<size_t>(2 * of.x * part + tile_front % P.ways * 128 + row_front);
+    const size_t row_b = oo.x < 0 ? P.side_at(1, at) : static_cast<size_t>(2 * oo.x * part + row_own);
+    const float* const o_a = (of.x < 0 ? P.side_o : P.part_o) + row_a * D;
+    const float* const o_b = (oo.x < 0 ? P.side_o : P.part_o) + row_b * D;
+    const float2* const ml_a = (of.x < 0 ? P.side_ml : P.part_ml) + row_a;
+    const float2* const ml_b = (oo.x < 0 ? P.side_ml : P.part_ml) + row_b;
+    constexpr int kBatch = kQueries == 1 ? 4 : 1;        // results in flight together
     for (int k0 = mine; k0 < all; k0 += kBatch * across) {
       float2 e[kBatch][kQueries], z[kBatch][kQueries][kCols / 2];
 #pragma unroll
       for (int y = 0; y < kBatch; ++y) {
         const int k = k0 + y * across;
+        if (k >= all) break;
         const bool front = k < fronts;
-        const int2 rec = front ? of : oo;
-        const int p = rec.x + (front ? k : k - fronts);
-        const size_t from = rec.x < 0 ? P.side_at(front ? 0 : 1, at)
-                                      : P.part_row(p, rec.x, front ? tile_front % P.ways : 0, front ? row_front : row_own);
+        const int j = front ? k : k - fronts, off = (front ? of.x : oo.x) < 0 ? 0 : (2 * j + (j == 0)) * part;
+        const float2* const o = reinterpret_cast<const float2*>((front ? o_a : o_b) + off * D) + lane;
+        const float2* const ml = (front ? ml_a : ml_b) + off;
 #pragma unroll
         for (int q = 0; q < kQueries; ++q) {
-          const bool real = k < all && q < queries;
-          e[y][q] = real ? __ldcg((rec.x < 0 ? P.side_ml : P.part_ml) + from + q) : make_float2(-INFINITY, 0.0f);
-          const float2* o = reinterpret_cast<const float2*>((rec.x < 0 ? P.side_o : P.part_o) + (from + q) * D) + lane;
+          if (q >= queries) break;
+          e[y][q] = __ldcg(ml + q);
 #pragma unroll
-          for (int c = 0; c < kCols / 2; ++c) z[y][q][c] = real ? __ldcg(o + 32 * c) : make_float2(0.0f, 0.0f);
+          for (int c = 0; c < kCols / 2; ++c) z[y][q][c] = __ldcg(o + q * (D / 2) + 32 * c);
         }
       }
 #pragma unroll
-      for (int y = 0; y < kBatch; ++y)
+      for (int y = 0; y < kBatch; ++y) {
+        if (k0 + y * across >= all) break;
 #pragma unroll
         for (int q = 0; q < kQueries; ++q) {
+          if (q >= queries) break;
           const float2 g = e[y][q];
           const float top = fmaxf(M[q], g.x);
           const float f = M[q] == top ? 1.0f : (M[q] == -INFINITY ? 0.0f : sv::ex2((M[q] - top) * P.c));
@@ -108,6 +118,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps<kQueries>) sv_attend_merge_ke
             v[q][2 * c + 1] = v[q][2 * c + 1] * f + z[y][q][c].y * t;
           }
         }
+      }
     }
   }
   if (kQueries == 1 && across > 1) {
@@ -163,16 +174,19 @@ int merge(const SharedParams& P, int across, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, sv_attend_merge_kernel<F16, D, kQueries>, P, across) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 template <bool F16, int D>
-int merge(const SharedParams& P, cudaStream_t st) {
-  // Few queries, whose fronts may be in many parts, have sixteen or four warps each.
-  const long long queries = static_cast<long long>(P.R.B) * P.R.N * P.Hq;
-  if (queries > 8192) return merge<F16, D, 4>(P, 1, st);
-  return merge<F16, D, 1>(P, queries <= 1024 ? 16 : 4, st);
+int merge(const SharedParams& P, int sms, cudaStream_t st) {
+  // Up to as many warps as the GPU holds at once (32 an SM): few queries, whose fronts may be in many parts, have up to
+  // sixteen each.
+  const long long queries = static_cast<long long>(P.R.B) * P.R.N * P.Hq, most = 32ll * sms;
+  if (queries > most) return merge<F16, D, 4>(P, 1, st);
+  int across = 16;
+  while (across > 1 && queries * across > most) across /= 2;
+  return merge<F16, D, 1>(P, across, st);
 }
 template <bool F16>
-int merge(const SharedParams& P, cudaStream_t st) {
+int merge(const SharedParams& P, int sms, cudaStream_t st) {
   const int D = P.R.C.head_dim;
-  return D == 64 ? merge<F16, 64>(P, st) : (D == 128 ? merge<F16, 128>(P, st) : merge<F16, 256>(P, st));
+  return D == 64 ? merge<F16, 64>(P, sms, st) : (D == 128 ? merge<F16, 128>(P, sms, st) : merge<F16, 256>(P, sms, st));
 }
 
 // Where rows attend all of their entries by themselves: NaN for the rows whose shared_len is none, or all where
@@ -341,5 +355,5 @@ extern "C" int spec_verify_shared_attention(const void* q, int64_t q_row_stride,
   const bool f16 = cache->dtype == SV_DTYPE_F16;
   st = sv::launch_attend_shared(P, f16, kmap, vmap, qmap, q_tokens, grid, s);
   if (st != SV_OK) return st;
-  return f16 ? merge<true>(P, s) : merge<false>(P, s);
+  return f16 ? merge<true>(P, sms, s) : merge<false>(P, sms, s);
 }
