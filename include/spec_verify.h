@@ -465,7 +465,7 @@ int spec_verify_shape_logits(void* logits, const int32_t* num_positions, const i
  *
  * num            [B] int32, 0..M; NULL: M. A row with -1 (a row error of the verification) or another number out of
  *                range counts nothing. Tokens outside [0, V) (the verification's -1 padding) are passed over.
- * M >= 1, V <= 2^24. counts share no memory with tokens or num (SV_ERR_OVERLAP). One launch; the result does not
+ * 1 <= M <= 2^30, V <= 2^24. counts share no memory with tokens or num (SV_ERR_OVERLAP). One launch; the result does not
  * depend on the order in which threads come. */
 int spec_verify_count_tokens(const int32_t* tokens, const int32_t* num, int16_t* counts, int32_t prompt, int32_t B,
                              int32_t M, int32_t V, void* cuda_stream);

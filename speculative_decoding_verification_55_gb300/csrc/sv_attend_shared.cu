@@ -288,6 +288,8 @@ extern "C" int spec_verify_shared_attention(const void* q, int64_t q_row_stride,
   P.R.N = N;
   P.R.group = group;
   P.R.none_ok = false;
+  P.R.q_rows = rows_tile;
+  P.R.tile_log2 = D == 256 ? 6 : 7;
   P.R.start = group_start;
   P.R.common = shared_len;
   P.R.groups = groups;
@@ -319,10 +321,9 @@ extern "C" int spec_verify_shared_attention(const void* q, int64_t q_row_stride,
     st = sv::query_tensor_map(q, 0, N > 1 ? q_token_stride : q_row_stride, 1, B * N, Hq, D, cache->dtype, group, q_tokens, &qmap);
   if (st != SV_OK) return st;
   P.R.q_rows = rows_tile * ways;
-  P.R.tile_log2 = D == 256 ? 6 : 7;
   P.R.one_rows = ways == 2 ? rows_tile : static_cast<int>(kMaxQueries);
   P.R.one_units = kOneWay;
-  P.R.two_units = kTwoWays;
+  P.R.two_units = ways == 2 ? kTwoWays : kOneWay;
   P.R.extra = kOneItem;
   P.R.two_extra = kTwoItem;
   P.q = static_cast<const char*>(q);

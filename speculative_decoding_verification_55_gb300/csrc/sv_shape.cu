@@ -417,7 +417,7 @@ extern "C" int spec_verify_shape_logits(void* logits, const int32_t* num_positio
 extern "C" int spec_verify_count_tokens(const int32_t* tokens, const int32_t* num, int16_t* counts, int32_t prompt,
                                         int32_t B, int32_t M, int32_t V, void* cuda_stream) {
   if (!tokens || !counts) return SV_ERR_NULL_POINTER;
-  if (B < 1 || B > (1 << 20) || M < 1 || V < 1 || V > (1 << 24)) return SV_ERR_BAD_SHAPE;
+  if (B < 1 || B > (1 << 20) || M < 1 || M > (1 << 30) || V < 1 || V > (1 << 24)) return SV_ERR_BAD_SHAPE;
   const int chunks = (M - 1) / (kThreads * kPer) + 1;
   if (static_cast<long long>(B) * chunks > 0x7fffffffll) return SV_ERR_BAD_SHAPE;
   if (sv::misaligned(tokens, 4) || sv::misaligned(num, 4) || sv::misaligned(counts, 2)) return SV_ERR_MISALIGNED;

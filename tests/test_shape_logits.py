@@ -89,7 +89,7 @@ def test_shape_refusals(L, change, status):
 
 @pytest.mark.parametrize("change,status", [
     (dict(t=None), 1), (dict(c=None), 1), (dict(B=0), 2), (dict(M=0), 2), (dict(V=0), 2), (dict(V=(1 << 24) + 1), 2),
-    (dict(B=(1 << 20) + 1), 2), (dict(B=1 << 20, M=1 << 30), 2), (dict(t=FAKE + 2), 5), (dict(n=FAKE + (1 << 20) + 1), 5),
+    (dict(B=(1 << 20) + 1), 2), (dict(B=1 << 20, M=1 << 30), 2), (dict(M=(1 << 30) + 1), 2), (dict(t=FAKE + 2), 5), (dict(n=FAKE + (1 << 20) + 1), 5),
     (dict(c=FAKE + (1 << 30) + 1), 5), (dict(c=FAKE + 8), 9), (dict(n=FAKE + (1 << 30) + 8), 9),
 ])
 def test_count_refusals(L, change, status):

@@ -187,6 +187,44 @@ def test_gpu_large_groups(sv, N, G, D, B, front):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("N,G", [(1, 8), (2, 3)])
+def test_gpu_a_very_large_group(sv, N, G):
+    """Thousands of rows of one group, some without tokens, against the paged attention on the same tables."""
+    rng = np.random.default_rng(N)
+    B = 4000
+    prefix = 48 + rng.integers(0, 20, B)
+    a = Batch(prefix, N, 2, G, 64, 16, seed=B, poison=False)
+    common, call = with_fronts(a, (0, B), (48,))
+    num = rng.integers(0, N + 1, B).astype(np.int32)
+    out, lse = attend_shared(sv, a, common, call, (0, B), num)
+    ref, rlse = sv.attend(a.q, a.cache(sv, weight=False), dev(a.prefix), dev(num))
+    # Each is within half a step of the probabilities and of the output of the exact one, whose values are below 8.
+    assert float((out.float() - ref.float()).abs().max()) <= 4 * 2.0 ** -8 * 8
+    assert float((lse - rlse).abs().max()) <= 2 * (66 * 2.0 ** -24 * 600 + 1e-6)
+    pick = [0, 1, 1999, 3998, 3999]
+    b = Batch.__new__(Batch)
+    b.__dict__ = dict(a.__dict__, q=a.q[pick], table=a.table[pick])
+    check_attention(b, out[pick], lse[pick], a.prefix[pick], num[pick], None)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,N", [(5, 1), (1, 4)])
+def test_gpu_query_strides(sv, B, N):
+    """One token a row, or one row: any distance of the rows, and of the tokens, will do."""
+    a = Batch((70,) * B, N, 2, 4, 128, 16, seed=2, poison=False)
+    common, call = with_fronts(a, (0, B), (64,))
+    wide = torch.zeros((B, 3 * N, a.q.shape[2], 128), dtype=a.q.dtype, device="cuda")
+    if B > 1:
+        wide[:, :1] = a.q
+        a.q = wide[:, :1]
+    else:
+        wide[:, ::3] = a.q
+        a.q = wide[:, ::3]
+    out, lse = attend_shared(sv, a, common, call, (0, B))
+    check_attention(a, out, lse, a.prefix, np.full(B, N), None)
+
+
+@pytest.mark.gpu
 def test_gpu_no_fronts(sv):
     """Groups without a front, and rows in no group: the paged attention."""
     a = Batch((40, 0, 130, 65), 3, 2, 4, 128, 16, seed=3)
