@@ -23,6 +23,21 @@ namespace {
 
 using sv::SharedParams;
 
+// A launch whose CTAs may begin before the kernel ahead of it in the stream ends (which they wait for themselves).
+template <class Kern, class... Args>
+int launch_ahead(Kern kern, unsigned grid, int threads, cudaStream_t st, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+}
+
 template <int kQueries>
 constexpr int kMergeWarps = kQueries == 1 ? 16 : 8;
 // What the plan takes a tile and an item (its queries and its end) to cost, in units of 0.25 us: a tile on two ways 2 us,
@@ -162,16 +177,8 @@ __global__ void __launch_bounds__(32 * kMergeWarps<kQueries>) sv_attend_merge_ke
 template <bool F16, int D, int kQueries>
 int merge(const SharedParams& P, int across, cudaStream_t st) {
   const long long warps = static_cast<long long>(P.R.B) * P.R.N * P.R.C.heads * ((P.R.group + kQueries - 1) / kQueries) * across;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((warps - 1) / kMergeWarps<kQueries> + 1));
-  cfg.blockDim = dim3(32 * kMergeWarps<kQueries>);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, sv_attend_merge_kernel<F16, D, kQueries>, P, across) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+  return launch_ahead(sv_attend_merge_kernel<F16, D, kQueries>, static_cast<unsigned>((warps - 1) / kMergeWarps<kQueries> + 1),
+                      32 * kMergeWarps<kQueries>, st, P, across);
 }
 template <bool F16, int D>
 int merge(const SharedParams& P, int sms, cudaStream_t st) {
@@ -189,30 +196,9 @@ int merge(const SharedParams& P, int sms, cudaStream_t st) {
   return D == 64 ? merge<F16, 64>(P, sms, st) : (D == 128 ? merge<F16, 128>(P, sms, st) : merge<F16, 256>(P, sms, st));
 }
 
-// Where rows attend all of their entries by themselves: NaN for the rows whose shared_len is none, or all where
-// group_start does not ascend.
-constexpr int kMarkThreads = 256;
-__global__ void __launch_bounds__(kMarkThreads) sv_attend_mark_kernel(const SharedParams P, int D) {
-  const sv::SharedRound& R = P.R;
-  const int tid = threadIdx.x;
-  bool all = false;
-  for (int g = tid; g <= R.groups; g += kMarkThreads) {
-    const int e = __ldg(R.start + g);
-    all |= e > R.B || (g == 0 ? e < 0 : __ldg(R.start + g - 1) > e);
-  }
-  all = __syncthreads_or(all);
-  for (int b = blockIdx.x; b < R.B; b += gridDim.x) {
-    if (!all && sv::row_of_group(R, b).x >= 0) continue;
-    const size_t queries = static_cast<size_t>(R.N) * P.Hq;
-    uint4* o = reinterpret_cast<uint4*>(P.out) + b * queries * D / 8;
-    for (size_t x = tid; x < queries * D / 8; x += kMarkThreads) o[x] = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
-    if (P.lse)
-      for (size_t x = tid; x < queries; x += kMarkThreads) P.lse[b * queries + x] = __int_as_float(0x7fffffff);
-  }
-}
-
 constexpr int kMaxSms = 160;
 constexpr size_t kFlagBytes = 256;
+constexpr long long kShortRoom = 512, kLittleRoom = 48ll << 20;   // entries of a row; bytes of all rows' keys and values
 constexpr long long kMaxQueries = 1ll << 28;   // query heads of all tokens
 
 bool sizes_ok(int32_t B, int32_t N, int32_t Hq, const sv_paged_cache* c) {
@@ -272,7 +258,6 @@ extern "C" int spec_verify_shared_attention(const void* q, int64_t q_row_stride,
                    {shared_len, rows}, {group_start, 4ull * groups + 4}, {num_queries, rows}, {tree_parents, rows * N},
                    sv::table_of(cache, B), sv::weights_of(cache), sv::pages_of(cache, cache->k), sv::pages_of(cache, cache->v)}))
     return SV_ERR_OVERLAP;
-  SharedParams P;
   int dev = 0;
   st = sv::current_device_status(&dev);
   if (st != SV_OK) return st;
@@ -280,22 +265,6 @@ extern "C" int spec_verify_shared_attention(const void* q, int64_t q_row_stride,
   if (sms < 1) return SV_ERR_CUDA;
   if (sms > kMaxSms) sms = kMaxSms;
   const int D = cache->head_dim, group = Hq / cache->heads, rows_tile = 128 / group * group;
-  const cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
-  P.R.C = C;
-  P.R.prefix = prefix_len;
-  P.R.num = num_queries;
-  P.R.B = B;
-  P.R.N = N;
-  P.R.group = group;
-  P.R.none_ok = false;
-  P.R.q_rows = rows_tile;
-  P.R.tile_log2 = D == 256 ? 6 : 7;
-  P.R.start = group_start;
-  P.R.common = shared_len;
-  P.R.groups = groups;
-  P.out = out;
-  P.lse = out_lse;
-  P.Hq = Hq;
   // A group's queries fill the query tiles that its front is read for; so do a row's where they are more than half of one.
   // Then the products take the time, a front's second reading comes from L2 or is hidden behind them, and the rows go by
   // themselves (which also leaves out the tokens behind a row's: a front's tiles have them all). Measured over 24 rows in
@@ -303,13 +272,15 @@ extern "C" int spec_verify_shared_attention(const void* q, int64_t q_row_stride,
   // among them: fronts of 4000 entries, 4 query rows a row and key head 29 against 39 us, 36 rows 45 against 43, 72 rows
   // 59 against 43; fronts of 32,000, 36 rows 92 against 188, 144 rows 248 against 213; heads of 256, fronts of 4000,
   // 36 rows 57 against 72, 72 rows 84 against 74.
-  if (2 * N * group > 128) {
-    st = spec_verify_paged_attention(q, q_row_stride, q_token_stride, cache, prefix_len, num_queries, tree_parents, scale, out,
-                                     out_lse, B, N, Hq, workspace, workspace_bytes, cuda_stream);
-    if (st != SV_OK) return st;
-    sv_attend_mark_kernel<<<std::min(B, 4 * sms), kMarkThreads, 0, s>>>(P, D);
-    return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
-  }
+  // So do rows of little room, whose fronts cost less than the kernel's longer start and end and the merge: 64 rows of one
+  // token over 256 shared and up to 120 own entries 33 us by fronts, 27 by rows, over 1024 shared ones 34 and 44; 4 rows over
+  // 512 shared ones 17 and 13, over 8192 20 and 26 (32/8 heads of 128); 64 rows over 1024, 16/2 heads of 64, 21 and 17.
+  // (Heads of 256: 4 rows over 8192 22 and 20, 64 rows over 256 21 and 22.)
+  const long long room = std::min<long long>(cache->max_pages, cache->num_pages) * cache->page_size;
+  const bool little = (D < 256 && room <= kShortRoom) || B * room * cache->heads * D * 4 <= (D < 256 ? kLittleRoom : kLittleRoom / 4);
+  if (N * group > 64 || little)
+    return spec_verify_paged_attention(q, q_row_stride, q_token_stride, cache, prefix_len, num_queries, tree_parents, scale, out,
+                                       out_lse, B, N, Hq, workspace, workspace_bytes, cuda_stream);
   // Two query tiles at once where a group has more than one's rows.
   const long long all = static_cast<long long>(B) * N * group;
   const int ways = D < 256 && all > static_cast<long long>(groups) * rows_tile ? 2 : 1;
@@ -320,7 +291,23 @@ extern "C" int spec_verify_shared_attention(const void* q, int64_t q_row_stride,
   if (st == SV_OK)
     st = sv::query_tensor_map(q, 0, N > 1 ? q_token_stride : q_row_stride, 1, B * N, Hq, D, cache->dtype, group, q_tokens, &qmap);
   if (st != SV_OK) return st;
+  const cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+  SharedParams P;
+  P.R.C = C;
+  P.R.prefix = prefix_len;
+  P.R.num = num_queries;
+  P.R.B = B;
+  P.R.N = N;
+  P.R.group = group;
+  P.R.none_ok = false;
+  P.R.start = group_start;
+  P.R.common = shared_len;
+  P.R.groups = groups;
+  P.out = out;
+  P.lse = out_lse;
+  P.Hq = Hq;
   P.R.q_rows = rows_tile * ways;
+  P.R.tile_log2 = D == 256 ? 6 : 7;
   P.R.one_rows = ways == 2 ? rows_tile : static_cast<int>(kMaxQueries);
   P.R.one_units = kOneWay;
   P.R.two_units = ways == 2 ? kTwoWays : kOneWay;

@@ -1,6 +1,9 @@
 """Attention of rows that share the fronts of their contexts: refusals on the CPU, GPU parity against the fp64 oracle
 (the paged attention's, on tables whose rows begin with the same pages).
 
+By the room of the tables and the pool, and by a row's query rows, a call goes by fronts or by rows; the tests of fronts
+give the batches room (roomy).
+
 Tolerances as for the paged attention (test_paged_cache): its parts are joined in fp32 the same way, one more time.
 """
 import ctypes
@@ -112,13 +115,32 @@ def with_fronts(a, start, fronts):
     return common, a.table.copy()
 
 
-def attend_shared(sv, a, common, call, start, num=None, parents=None, scale=None):
-    cache = sv.PagedCache(a.k, a.v, dev(call))
+def roomy(a, *tables):
+    """Pages behind the pool's and columns behind the tables', which nobody reads: room for more than the 48 MB of keys and
+    values, and the 512 entries a row, up to which rows go by themselves."""
+    P, H, S, D = a.k.shape
+    pages = max(-(-(49 << 20) // (len(a.prefix) * H * S * D * 4)), 513 // S + 1) + 1
+    if P < pages:
+        order = (lambda x: x.transpose(1, 2)) if a.k.stride(1) < a.k.stride(2) else (lambda x: x)
+        for name in ("k", "v"):
+            x = torch.full((pages, S, H, D) if a.k.stride(1) < a.k.stride(2) else (pages, H, S, D), math.nan, dtype=a.t, device="cuda")
+            x = order(x)
+            x[:P] = getattr(a, name)
+            setattr(a, name, x)
+    wide = [np.full((t.shape[0], max(pages, t.shape[1])), 1 << 30, np.int32) for t in tables]
+    for w, t in zip(wide, tables):
+        w[:, :t.shape[1]] = t
+    return wide[0] if len(wide) == 1 else wide
+
+
+def attend_shared(sv, a, common, call, start, num=None, parents=None, scale=None, rows=False):
+    table = call if rows else roomy(a, call)   # (before the pool is taken)
+    cache = sv.PagedCache(a.k, a.v, dev(table))
     return sv.attend_shared(a.q, cache, dev(a.prefix), dev(common), dev(start), dev(num), dev(parents), scale)
 
 
 CASES = [
-    # prefix lengths, starts, fronts, N, Hkv, group, D, page, dtype, nhd
+    # prefix lengths, starts, fronts, N, Hkv, group, D, page, dtype, nhd (more than 64 query rows go by rows)
     ((16,), (0, 1), (16,), 1, 1, 1, 64, 16, "bf16", False),                      # a row of its own, nothing behind
     ((20, 16, 33, 48), (0, 4), (16,), 1, 2, 4, 128, 16, "bf16", False),
     ((200, 129, 128, 500), (0, 4), (128,), 1, 2, 4, 128, 64, "f16", True),
@@ -137,20 +159,21 @@ CASES = [
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("rows", [False, True])
 @pytest.mark.parametrize("prefix,start,fronts,N,H,G,D,S,dtype,nhd", CASES)
-def test_gpu_shared(sv, prefix, start, fronts, N, H, G, D, S, dtype, nhd):
+def test_gpu_shared(sv, prefix, start, fronts, N, H, G, D, S, dtype, nhd, rows):
     rng = np.random.default_rng(N * 31 + D)
     a = Batch(prefix, N, H, G, D, S, dtype, nhd, seed=N + D, poison=False)
     B = len(prefix)
     common, call = with_fronts(a, start, fronts)
     num = rng.integers(0, N + 1, B).astype(np.int32)
     num[-1] = N
-    out, lse = attend_shared(sv, a, common, call, start, num)
+    out, lse = attend_shared(sv, a, common, call, start, num, rows=rows)
     check_attention(a, out, lse, a.prefix, num, None)
-    again, lse2 = attend_shared(sv, a, common, call, start, num)
+    again, lse2 = attend_shared(sv, a, common, call, start, num, rows=rows)
     assert torch.equal(again, out) and torch.equal(lse2, lse)          # the same call, the same bits
     tree = random_tree(rng, B, N)
-    out, lse = attend_shared(sv, a, common, call, start, None, tree, 0.25)
+    out, lse = attend_shared(sv, a, common, call, start, None, tree, 0.25, rows=rows)
     check_attention(a, out, lse, a.prefix, np.full(B, N), tree, 0.25)
 
 
@@ -193,7 +216,7 @@ def test_gpu_a_very_large_group(sv, N, G):
     rng = np.random.default_rng(N)
     B = 4000
     prefix = 48 + rng.integers(0, 20, B)
-    a = Batch(prefix, N, 2, G, 64, 16, seed=B, poison=False)
+    a = Batch(prefix, N, 2, G, 64, 16, seed=B, poison=False, extra=40)
     common, call = with_fronts(a, (0, B), (48,))
     num = rng.integers(0, N + 1, B).astype(np.int32)
     out, lse = attend_shared(sv, a, common, call, (0, B), num)
@@ -247,7 +270,8 @@ def test_gpu_row_errors(sv):
     common[4] = 16                             # another front than its group's
     common[5] = 0                              # on its own
     call[5] = a.table[5]
-    cache = sv.PagedCache(a.k, a.v, dev(call))
+    table = roomy(a, call)
+    cache = sv.PagedCache(a.k, a.v, dev(table))
     out, lse = sv.attend_shared(a.q, cache, dev(bad), dev(common), dev(start), dev(num))
     assert np.isnan(host(out)[[1, 2, 3, 4]]).all() and np.isnan(host(lse)[[1, 2, 3, 4]]).all()
     good = [0, 5, 6]
@@ -278,21 +302,32 @@ def test_gpu_row_errors(sv):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("start", [(0, 5, 3, 7), (-1, 7), (0, 8), (2, 1)])
-@pytest.mark.parametrize("N,G", [(2, 4), (31, 8)])
-def test_gpu_groups_in_error(sv, start, N, G):
-    a = Batch((40,) * 7, N, 1, G, 64, 16, seed=4, poison=False)
+def test_gpu_groups_in_error(sv, start):
+    a = Batch((40,) * 7, 2, 1, 4, 64, 16, seed=4, poison=False)
     out, lse = attend_shared(sv, a, np.full(7, 32, np.int32), a.table, start)
     assert np.isnan(host(out)).all() and np.isnan(host(lse)).all()
 
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("common", [8, 24, -16, 48, 1 << 30, -(1 << 31)])
-@pytest.mark.parametrize("N,G", [(2, 4), (31, 8)])
-def test_gpu_fronts_in_error(sv, common, N, G):
+def test_gpu_fronts_in_error(sv, common):
     """Not whole pages, below zero, longer than the rows."""
-    a = Batch((40,) * 4, N, 1, G, 64, 16, seed=4, poison=False)
+    a = Batch((40,) * 4, 2, 1, 4, 64, 16, seed=4, poison=False)
     out, lse = attend_shared(sv, a, np.array([common] * 3 + [0], np.int32), a.table, (0, 3))
     assert np.isnan(host(out)[:3]).all() and np.isnan(host(lse)[:3]).all() and np.isfinite(host(out)[3]).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N,G,rows", [(2, 4, True), (31, 8, False)])
+def test_gpu_by_rows(sv, N, G, rows):
+    """Little room, or many query rows: shared_len and group_start are not read, the outputs are the paged attention's."""
+    a = Batch((40, 0, 300, 77), N, 1, G, 64, 16, seed=4, poison=False)
+    num = np.array([N, 1, N - 1, 0], np.int32)
+    out, lse = attend_shared(sv, a, np.full(4, -7, np.int32), a.table, (3, 9), num, rows=rows)
+    table = a.table if rows else roomy(a, a.table)
+    want, want_lse = sv.attend(a.q, sv.PagedCache(a.k, a.v, dev(table)), dev(a.prefix), dev(num))
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    check_attention(a, out, lse, a.prefix, num, None)
 
 
 @pytest.mark.gpu
@@ -311,7 +346,8 @@ def test_gpu_unattended_values_have_no_part(sv, N, G):
     a.v[p, :, s] = math.inf
     p, s = oracle.place(a.table, 1, 64 + N - 1, 16)
     a.v[p, :, s, 1::2] = math.inf
-    cache = sv.PagedCache(a.k, a.v, dev(a.table))
+    table = roomy(a, a.table)
+    cache = sv.PagedCache(a.k, a.v, dev(table))
     out, lse = sv.attend_shared(q, cache, dev(a.prefix), dev(common), dev((0, 4)), dev(num))
     o = host(out)
     assert np.isfinite(o[0]).all() and np.isfinite(o[2:]).all() and np.isfinite(o[1, :N - 1]).all()
@@ -319,7 +355,7 @@ def test_gpu_unattended_values_have_no_part(sv, N, G):
     ref, _ = sv.attend(q, cache, dev(a.prefix), dev(num))
     r = host(ref)
     fine = np.isfinite(r)
-    assert np.abs(o - r)[fine].max() <= 2.0 ** -7 * 4
+    assert np.abs(o[fine] - r[fine]).max() <= 2.0 ** -7 * 4
     a.v[a.table[0, 3], 0, 15, 5] = math.inf                               # the front's last entry
     out, _ = sv.attend_shared(q, cache, dev(a.prefix), dev(common), dev((0, 4)), dev(num))
     o = host(out)
@@ -333,6 +369,7 @@ def test_gpu_captured_and_streams(sv):
     a = Batch((300, 290, 310, 77), 5, 2, 4, 128, 16, seed=8, poison=False)
     start = (0, 3)
     common, call = with_fronts(a, start, (256,))
+    call = roomy(a, call)
     cache = sv.PagedCache(a.k, a.v, dev(call))
     args = [dev(a.prefix), dev(common), dev(start)]
     want, want_lse = sv.attend_shared(a.q, cache, *args)
@@ -342,7 +379,6 @@ def test_gpu_captured_and_streams(sv):
     other = torch.cuda.Stream()
     for front in (256, 0, 128):
         args[1].copy_(dev(np.where(common > 0, front, 0)))
-        cache.page_table.copy_(dev(a.table))
         graph.replay()
         num = np.full(4, 5)
         check_attention(a, out, lse, a.prefix, num, None)
@@ -369,7 +405,7 @@ def test_gpu_a_round_of_one_prompt(sv):
     rounds on pages of each row's own with the paged attention."""
     B, N, H, G, D, S, V = 12, 5, 2, 4, 64, 16, 512
     g = torch.Generator(device="cuda").manual_seed(4)
-    front, rows = 96, 20
+    front, rows = 96, 700                      # (room for fronts to be worth it)
     table = torch.zeros((B, rows), dtype=torch.int32, device="cuda")
     table[:, :6] = torch.arange(6, device="cuda")
     table[:, 6:] = 6 + torch.arange(B * (rows - 6), device="cuda").view(B, -1)
