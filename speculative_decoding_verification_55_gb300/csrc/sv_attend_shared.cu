@@ -9,8 +9,8 @@
 // rows' own entries, cut into runs of equal time, whose results, of several CTAs where an item is cut, the merge kernel
 // here puts together, a query or four a warp.
 // Bound: the bytes of the entries, each read once, or for large groups the products (4 D a query head and entry). 64 rows
-// of one token over 8000 shared and 17 to 1000 own entries, 32/8 heads of 128: 58 us (floor 25; 225 by rows that each read
-// all of it): 45 of the attention, of which about 14 are its start and end, then the merge.
+// of one token over 8000 shared and 17 to 1000 own entries, 32/8 heads of 128: 54 us (floor 25; 225 by rows that each read
+// all of it): 41 to 46 of the attention, of which about 14 are its start and end, then the merge.
 // Two launches of each (the fronts, their join, the rows' own entries with the front added at an item's end, their join)
 // took 99 us: each launch's start and end cost more than the rows' own entries gained by kernels of their own.
 // Rounding: the sides are fp32 sums and maxima; the output is rounded once.
