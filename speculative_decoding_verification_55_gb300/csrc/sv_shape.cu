@@ -16,6 +16,8 @@
 
 #include <cuda_bf16.h>
 
+#include <algorithm>
+
 #include "sv_cache.cuh"
 #include "sv_tiles.cuh"
 
@@ -71,33 +73,39 @@ __device__ __forceinline__ void put(void* at, const Group<T, kW>& g) {
   }
 }
 
-// The round's tokens or the row's biases that fall into a CTA's tokens, in their order; one warp. `next`: the lane's
-// among the first 32.
-__device__ __forceinline__ int gather(const int32_t* from, int next, int n, int v0, int v1, int lane, int* token,
-                                      unsigned short* index, unsigned* special) {
+// The round's tokens or the row's biases that fall into a CTA's tokens, in their order, with the biases' values; one warp.
+__device__ __forceinline__ int gather(const int32_t* from, const float* values, int n, int v0, int v1, int lane,
+                                      unsigned short* place, unsigned short* index, float* value, unsigned* special) {
+  constexpr int kAtOnce = 4;
   int have = 0;
-  for (int x0 = 0; x0 < n; x0 += 32) {
-    const int t = x0 + lane < n ? next : -1;
-    next = x0 + 32 + lane < n ? __ldg(from + x0 + 32 + lane) : -1;
-    const bool in = t >= v0 && t < v1;         // (v0 >= 0: a token below 0 is in no CTA's)
-    const unsigned all = __ballot_sync(sv::kFull, in);
-    if (in) {
-      const int at = have + __popc(all & ((1u << lane) - 1));
-      token[at] = t - v0;
-      index[at] = static_cast<unsigned short>(x0 + lane);
-      atomicOr(special + ((t - v0) >> 5), 1u << ((t - v0) & 31));
+  for (int x0 = 0; x0 < n; x0 += 32 * kAtOnce) {
+    int t[kAtOnce];
+    float f[kAtOnce];
+#pragma unroll
+    for (int y = 0; y < kAtOnce; ++y) {
+      const int x = x0 + 32 * y + lane;
+      t[y] = x < n ? __ldg(from + x) : -1;
+      f[y] = values && x < n ? __ldg(values + x) : 0.0f;
     }
-    have += __popc(all);
+#pragma unroll
+    for (int y = 0; y < kAtOnce; ++y) {
+      const bool in = t[y] >= v0 && t[y] < v1;         // (v0 >= 0: a token below 0 is in no CTA's)
+      const unsigned all = __ballot_sync(sv::kFull, in);
+      if (in) {
+        const int at = have + __popc(all & ((1u << lane) - 1)), p = t[y] - v0;
+        place[at] = static_cast<unsigned short>(p);
+        index[at] = static_cast<unsigned short>(x0 + 32 * y + lane);
+        if (values) value[at] = f[y];
+        atomicOr(special + (p >> 5), 1u << (p & 31));
+      }
+      have += __popc(all);
+    }
   }
   return have;
 }
 
-// A token of the list: its place in the CTA's run, whether the round's tokens or the biases have it, its count.
+// A token of the list: its place in the CTA's run, and its count.
 constexpr int kPlaceBits = 13;
-constexpr unsigned kSpecial = 1u << kPlaceBits;
-__device__ __forceinline__ unsigned listed(int place, bool special, int16_t count) {
-  return static_cast<unsigned>(place) | (special ? kSpecial : 0u) | static_cast<unsigned>(static_cast<unsigned short>(count)) << 16;
-}
 
 // kW: tokens of a thread, 8 or (rows that are not of whole words) 1; kU: groups of a thread.
 template <typename T, int kW, int kU>
@@ -109,8 +117,19 @@ __global__ void __launch_bounds__(kThreads, 6) sv_shape_kernel(const ShapeParams
   __shared__ unsigned special[kSpan / 32];     // a bit a token
   __shared__ __align__(16) unsigned masks[kPositions][kSpan / 32];
   __shared__ unsigned list[kSpan];
-  __shared__ int said[kMaxRound], biased[kMaxBias], up[kMaxRound], lists[2], length;
-  __shared__ unsigned short said_at[kMaxRound], biased_at[kMaxBias];
+  // The round's tokens and the biases in the run: places in it, in the round and among the biases; then, of the first of
+  // each token, what it is (above the place's bits), its count, the places of the round that say it (a bit each, from place
+  // 1 on), its biases' sum.
+  constexpr int kPlace = (1 << kPlaceBits) - 1, kFirst = 1, kRoot = 2, kBiased = 4;
+  extern __shared__ float dyn[];               // (as many as the call has biases: what is not taken is left to the L1)
+  const int listed = kMaxRound + P.K;
+  float* const value = dyn;                    // [K]
+  float* const sum = value + P.K;              // [listed]
+  unsigned short* const places = reinterpret_cast<unsigned short*>(sum + listed);   // [listed]
+  unsigned short* const indexes = places + listed;
+  int16_t* const counted = reinterpret_cast<int16_t*>(indexes + listed);
+  __shared__ unsigned long long match[kMaxRound];
+  __shared__ int up[kMaxRound], lists[2], length;
   __shared__ unsigned long long above[sv::kMaxTreeNodes];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int run = blockIdx.x / P.blocks;       // the rows' first runs first: a text's tokens have low numbers
@@ -144,9 +163,6 @@ __global__ void __launch_bounds__(kThreads, 6) sv_shape_kernel(const ShapeParams
     if (P.counts && v < v1)
       count[u] = *reinterpret_cast<const Group<int16_t, kW>*>(P.counts + static_cast<size_t>(b) * P.V + v);
   }
-  const int32_t* const from = warp == 0 ? P.tokens + static_cast<size_t>(b) * P.T : P.bias_tokens + static_cast<size_t>(b) * P.K;
-  const int lists_most = warp == 0 ? (P.tokens && P.penalties ? P.T : 0) : (warp == 1 ? P.K : 0);
-  const int next = lane < lists_most ? __ldg(from + lane) : -1;
   const float rep = P.rep ? __ldg(P.rep + b) : 1.0f, freq = P.freq ? __ldg(P.freq + b) : 0.0f;
   const float pres = P.pres ? __ldg(P.pres + b) : 0.0f;
   bool ok = true;
@@ -162,15 +178,19 @@ __global__ void __launch_bounds__(kThreads, 6) sv_shape_kernel(const ShapeParams
   const int here = min(m - first, most);       // positions of this CTA
   // A chain's position i follows tokens 0 .. i - 1, a tree's node i follows its ancestors and itself.
   if (warp == 0) {
-    const int have = gather(from, next, min(lists_most, P.parents ? m : m - 1), v0, v1, lane, said, said_at, special);
+    const int n = P.tokens && P.penalties ? (P.parents ? m : m - 1) : 0;
+    const int have = gather(P.tokens + static_cast<size_t>(b) * P.T, nullptr, n, v0, v1, lane, places, indexes, nullptr, special);
     if (lane == 0) lists[0] = have;
   } else if (warp == 1) {
-    const int have = gather(from, next, lists_most, v0, v1, lane, biased, biased_at, special);
+    const size_t at = static_cast<size_t>(b) * P.K;
+    const int have = gather(P.bias_tokens + at, P.bias + at, P.K, v0, v1, lane, places + kMaxRound, indexes + kMaxRound, value, special);
     if (lane == 0) lists[1] = have;
-  } else if (P.parents && tid - 64 < m) {      // warps 2 to 4: places 1.. of the tree that a node follows, as bits from 0
-    unsigned long long set = 0;
-    for (int x = tid - 64; x > 0; x = up[x]) set |= 1ull << (x - 1);     // (parents lie below their nodes)
-    above[tid - 64] = set;
+  } else if (tid - 64 < m) {                   // warps 2 to 4: the places from 1 on that a position follows, as bits from 0
+    const int i = tid - 64;
+    unsigned long long set = P.parents || i == 0 ? 0 : (1ull << (i - 1)) - 1;
+    if (P.parents)
+      for (int x = i; x > 0; x = up[x]) set |= 1ull << (x - 1);          // (parents lie below their nodes)
+    above[i] = set;
   }
 
   T* const row = static_cast<T*>(P.logits) + (static_cast<size_t>(b) * P.N + first) * P.V + v0;
@@ -224,32 +244,70 @@ __global__ void __launch_bounds__(kThreads, 6) sv_shape_kernel(const ShapeParams
   }
   __syncthreads();
 
+  const int ns = lists[0], nb = lists[1];
 #pragma unroll
   for (int u = 0; u < kU; ++u) {
     const int at = (u * kThreads + tid) * kW;  // (behind the row's last token nothing is counted or special)
-    const unsigned marks = special[at >> 5] >> (at & 31) & kAll;
-    unsigned touched = marks;
+    unsigned touched = 0;
 #pragma unroll
     for (int k = 0; k < kW; ++k) touched |= (count[u].x[k] != 0 ? 1u : 0u) << k;
+    touched &= ~(special[at >> 5] >> (at & 31));
     if (!touched) continue;
     int to = atomicAdd(&length, __popc(touched));
 #pragma unroll
     for (int k = 0; k < kW; ++k)
-      if ((touched >> k) & 1) list[to++] = listed(at + k, (marks >> k) & 1, count[u].x[k]);
+      if ((touched >> k) & 1) list[to++] = static_cast<unsigned>(at + k) | static_cast<unsigned>(static_cast<unsigned short>(count[u].x[k])) << 16;
+  }
+  // (Looked up by each token at each position, 316 rows of 6 positions with 276 biases and V 162 took 52 us; so 36.)
+  for (int x = tid; x < ns + nb; x += kThreads) {
+    const int e = x < ns ? x : kMaxRound + x - ns, place = places[e];
+    int what = kFirst;                         // (its own bits above the place are not set yet, others' may be)
+    unsigned long long bits = 0;
+    float f = 0.0f;
+    for (int r = 0; r < ns; ++r) {
+      if ((places[r] & kPlace) != place) continue;
+      if (r < e) what = 0;
+      const int a = indexes[r];
+      if (a == 0) what |= kRoot;
+      else bits |= 1ull << (a - 1);
+    }
+    for (int r = kMaxRound; r < kMaxRound + nb; ++r) {
+      if ((places[r] & kPlace) != place) continue;
+      if (r < e) what = 0;
+      what |= kBiased;
+      f += value[r - kMaxRound];
+    }
+    places[e] = static_cast<unsigned short>(place | what << kPlaceBits);
+    sum[e] = f;
+    counted[e] = P.counts ? __ldg(P.counts + static_cast<size_t>(b) * P.V + v0 + place) : 0;
+    if (e < kMaxRound) match[e] = bits;
   }
   __syncthreads();
 
-  // A token of the list a lane, at one position, or at more of them where the list is long: their logits are then in
-  // flight together.
-  const int len = length;
-  if (len == 0) return;
-  const int step = min(max(len * here / kThreads, 1), here), items = len * ((here + step - 1) / step);
-  const unsigned inv = 0xffffffffu / len + 1;  // (x inv / 2^32 is x / len for x len < 2^32; 1 / 1 is 2^32)
+  // A token of the list, or of the round's and the biases', a lane, at one position, or at more of them where there are
+  // many: their logits are then in flight together.
+  const int len = length, all = len + ns + nb;
+  if (all == 0) return;
+  const int step = min(max(all * here / kThreads, 1), here), items = all * ((here + step - 1) / step);
+  const unsigned inv = 0xffffffffu / all + 1;  // (x inv / 2^32 is x / all for x all < 2^32; 1 / 1 is 2^32)
   for (int x = tid; x < items; x += kThreads) {
-    const int block = len == 1 ? x : __umulhi(x, inv), l = x - block * len;
+    const int block = all == 1 ? x : __umulhi(x, inv), l = x - block * all;
     const int y0 = block * step, steps = min(step, here - y0);
-    const unsigned e = list[l];
-    const int place = e & (kSpecial - 1), n = (e >> 16) & 32767;
+    int place, n, what = 0;
+    unsigned long long bits = 0;
+    float add = 0.0f;
+    if (l < len) {
+      place = list[l] & kPlace;
+      n = static_cast<int>(list[l]) >> 16;
+    } else {
+      const int e = l - len < ns ? l - len : kMaxRound + l - len - ns;
+      what = places[e] >> kPlaceBits;
+      if (!(what & kFirst)) continue;
+      place = places[e] & kPlace;
+      n = counted[e];
+      add = sum[e];
+      if (e < kMaxRound) bits = match[e];
+    }
     T* const at = row + static_cast<size_t>(y0) * P.V + place;
     float z[kPositions];
     unsigned allowed = 0;                      // a bit a position
@@ -260,29 +318,19 @@ __global__ void __launch_bounds__(kThreads, 6) sv_shape_kernel(const ShapeParams
       allowed |= 1u << y;
       z[y] = to_float<T>(at[static_cast<size_t>(y) * P.V]);
     }
-    bool any = (e >> 16) != 0;                 // concerned at every position
-    unsigned long long more = 0;               // what the round adds to n, seven bits a position
-    float add = 0.0f;
-    if (e & kSpecial) {
-      for (int s = 0; s < lists[0]; ++s) {
-        if (said[s] != place) continue;
-        const int a = said_at[s];              // (place 0 of a tree, the root, is above every node)
-        for (int y = 0; y < steps; ++y)
-          if (P.parents ? a == 0 || ((above[first + y0 + y] >> (a - 1)) & 1) : a < first + y0 + y) more += 1ull << (7 * y);
-      }
-      for (int s = 0; s < lists[1]; ++s)
-        if (biased[s] == place) {
-          add += __ldg(P.bias + static_cast<size_t>(b) * P.K + biased_at[s]);
-          any = true;
-        }
-    }
+    const bool prompt = n < 0;
+    n &= 32767;
 #pragma unroll
     for (int y = 0; y < kPositions; ++y) {
       if (y >= steps) break;
-      const int uses = n + (static_cast<int>(more >> (7 * y)) & 127);
-      if (!((allowed >> y) & 1) || !(any || uses > 0)) continue;
+      if (!((allowed >> y) & 1)) continue;
+      const int i = first + y0 + y;
+      // (Place 0 of a tree, the root, is above every node; of a chain, before every position but its own.)
+      int uses = n;
+      if (what) uses += __popcll(bits & above[i]) + ((what & kRoot) && (P.parents || i > 0));
+      if (!(uses > 0 || prompt || (what & kBiased))) continue;
       float v = z[y];
-      if (uses > 0 || e >> 31) v = v > 0.0f ? v / rep : v * rep;
+      if (uses > 0 || prompt) v = v > 0.0f ? v / rep : v * rep;
       v -= freq * static_cast<float>(uses);
       if (uses > 0) v -= pres;
       at[static_cast<size_t>(y) * P.V] = from_float<T>(v + add);
@@ -303,9 +351,11 @@ int launch_shape(ShapeParams& P, bool whole, int sms, cudaStream_t st) {
   const int span = kThreads * (two ? 16 : 8);
   const long long grid = static_cast<long long>(P.B) * ((P.V + span - 1) / span) * P.blocks;
   if (grid > 0x7fffffffll) return SV_ERR_BAD_SHAPE;
-  if (!whole) sv_shape_kernel<T, 1, 8><<<static_cast<unsigned>(grid), kThreads, 0, st>>>(P);
-  else if (two) sv_shape_kernel<T, 8, 2><<<static_cast<unsigned>(grid), kThreads, 0, st>>>(P);
-  else sv_shape_kernel<T, 8, 1><<<static_cast<unsigned>(grid), kThreads, 0, st>>>(P);
+  const unsigned g = static_cast<unsigned>(grid);
+  const size_t bytes = static_cast<size_t>(P.K) * 4 + static_cast<size_t>(kMaxRound + P.K) * (4 + 3 * 2);
+  if (!whole) sv_shape_kernel<T, 1, 8><<<g, kThreads, bytes, st>>>(P);
+  else if (two) sv_shape_kernel<T, 8, 2><<<g, kThreads, bytes, st>>>(P);
+  else sv_shape_kernel<T, 8, 1><<<g, kThreads, bytes, st>>>(P);
   return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 
@@ -313,45 +363,75 @@ int launch_shape(ShapeParams& P, bool whole, int sms, cudaStream_t st) {
 // Token counts
 // ------------------------------------------------------------------------------------------------
 
-constexpr int kPer = 4;                        // tokens of a thread
+constexpr int kPer = 4;                        // tokens of a thread at a time
 
-// Occurrences of a token among a warp's lanes are added once, by the first of them. The sum and its limit do not
-// depend on the order in which threads come.
+// Adds n occurrences. The sum and its limit do not depend on the order in which threads come.
+__device__ __forceinline__ void add_count(unsigned short* at, int n) {
+  unsigned short old = __ldcg(at);
+  for (;;) {                                   // ends: another thread's addition is what makes a turn fail
+    const int sum = min((old & 32767) + n, 32767);
+    const unsigned short now = atomicCAS(at, old, static_cast<unsigned short>((old & 0x8000) | sum));
+    if (now == old) return;
+    old = now;
+  }
+}
+
+// Occurrences of a token among a warp's lanes are added once, by the first of them; kMany (long rows of output): into a
+// table in shared memory, a slot's first token each, which goes to the counts at the end, other tokens at once. (Straight to
+// the counts, 4 rows of 1,000,000 tokens took 12.8 ms, the warps with a frequent token retrying; so they take 0.6.)
+constexpr int kSlots = 4096;
+template <bool kPrompt, bool kMany>
 __global__ void __launch_bounds__(kThreads) sv_count_kernel(const int32_t* tokens, const int32_t* num, int16_t* counts,
-                                                            int M, int V, int chunks, bool prompt) {
-  const int b = blockIdx.x / chunks, x0 = (blockIdx.x - b * chunks) * (kThreads * kPer);
+                                                            int M, int V, int chunks, int span) {
+  __shared__ int held[kMany ? kSlots : 1], seen[kMany ? kSlots : 1];
+  const int b = blockIdx.x / chunks, begin = (blockIdx.x - b * chunks) * span;
   const int m = num ? __ldg(num + b) : M;
-  if (m > M || x0 >= m) return;
+  if (m > M || begin >= m) return;
+  const int end = min(m, begin + span);
   unsigned short* const row = reinterpret_cast<unsigned short*>(counts) + static_cast<size_t>(b) * V;
-  int t[kPer];
-#pragma unroll
-  for (int y = 0; y < kPer; ++y) {
-    const int x = x0 + y * kThreads + threadIdx.x;
-    t[y] = x < m ? __ldg(tokens + static_cast<size_t>(b) * M + x) : -1;
-    if (static_cast<unsigned>(t[y]) >= static_cast<unsigned>(V)) t[y] = -1;
-  }
-  if (prompt) {
-    unsigned short c[kPer];
-#pragma unroll
-    for (int y = 0; y < kPer; ++y) c[y] = t[y] >= 0 ? __ldcg(row + t[y]) : 0x8000;
-#pragma unroll
-    for (int y = 0; y < kPer; ++y)             // whoever writes a token in this call writes the same
-      if (!(c[y] & 0x8000)) __stcg(row + t[y], static_cast<unsigned short>(c[y] | 0x8000));
-    return;
-  }
-#pragma unroll
-  for (int y = 0; y < kPer; ++y) {
-    const unsigned same = __match_any_sync(sv::kFull, t[y]);
-    if (t[y] < 0 || (threadIdx.x & 31) != __ffs(same) - 1) continue;
-    const int n = __popc(same);
-    unsigned short* const at = row + t[y];
-    unsigned short old = __ldcg(at);
-    for (;;) {                                 // ends: another thread's addition is what makes a turn fail
-      const int sum = min((old & 32767) + n, 32767);
-      const unsigned short now = atomicCAS(at, old, static_cast<unsigned short>((old & 0x8000) | sum));
-      if (now == old) break;
-      old = now;
+  if (kMany) {
+    for (int x = threadIdx.x; x < kSlots; x += kThreads) {
+      held[x] = -1;
+      seen[x] = 0;
     }
+    __syncthreads();
+  }
+  for (int x0 = begin; x0 < end; x0 += kThreads * kPer) {
+    int t[kPer];
+#pragma unroll
+    for (int y = 0; y < kPer; ++y) {
+      const int x = x0 + y * kThreads + threadIdx.x;
+      t[y] = x < end ? __ldg(tokens + static_cast<size_t>(b) * M + x) : -1;
+      if (static_cast<unsigned>(t[y]) >= static_cast<unsigned>(V)) t[y] = -1;
+    }
+    if constexpr (kPrompt) {
+      unsigned short c[kPer];
+#pragma unroll
+      for (int y = 0; y < kPer; ++y) c[y] = t[y] >= 0 ? __ldcg(row + t[y]) : 0x8000;
+#pragma unroll
+      for (int y = 0; y < kPer; ++y)           // whoever writes a token in this call writes the same
+        if (!(c[y] & 0x8000)) __stcg(row + t[y], static_cast<unsigned short>(c[y] | 0x8000));
+    } else {
+#pragma unroll
+      for (int y = 0; y < kPer; ++y) {
+        const unsigned same = __match_any_sync(sv::kFull, t[y]);
+        if (t[y] < 0 || (threadIdx.x & 31) != __ffs(same) - 1) continue;
+        const int n = __popc(same);
+        if (kMany) {
+          const int slot = t[y] % kSlots, was = atomicCAS(held + slot, -1, t[y]);
+          if (was == -1 || was == t[y]) {
+            atomicAdd(seen + slot, n);
+            continue;
+          }
+        }
+        add_count(row + t[y], n);
+      }
+    }
+  }
+  if constexpr (kMany) {
+    __syncthreads();
+    for (int x = threadIdx.x; x < kSlots; x += kThreads)
+      if (seen[x]) add_count(row + held[x], seen[x]);
   }
 }
 
@@ -418,15 +498,25 @@ extern "C" int spec_verify_count_tokens(const int32_t* tokens, const int32_t* nu
                                         int32_t B, int32_t M, int32_t V, void* cuda_stream) {
   if (!tokens || !counts) return SV_ERR_NULL_POINTER;
   if (B < 1 || B > (1 << 20) || M < 1 || M > (1 << 30) || V < 1 || V > (1 << 24)) return SV_ERR_BAD_SHAPE;
-  const int chunks = (M - 1) / (kThreads * kPer) + 1;
-  if (static_cast<long long>(B) * chunks > 0x7fffffffll) return SV_ERR_BAD_SHAPE;
+  // A CTA has as many tokens as leave eight CTAs an SM; its threads four at a time.
+  constexpr int kBatch = kThreads * kPer;
   if (sv::misaligned(tokens, 4) || sv::misaligned(num, 4) || sv::misaligned(counts, 2)) return SV_ERR_MISALIGNED;
   const unsigned long long rows = B;
   if (sv::overlap({{counts, 2 * rows * V}}, {{tokens, 4 * rows * M}, {num, 4 * rows}})) return SV_ERR_OVERLAP;
   int dev = 0;
   const int st = sv::current_device_status(&dev);
   if (st != SV_OK) return st;
-  sv_count_kernel<<<B * chunks, kThreads, 0, static_cast<cudaStream_t>(cuda_stream)>>>(tokens, num, counts, M, V, chunks,
-                                                                                     prompt != 0);
+  const int sms = sv::device_sms(dev);
+  if (sms < 1) return SV_ERR_CUDA;
+  const long long batches = (M - 1) / kBatch + 1, turns = std::max(1ll, B * batches / (8ll * sms));
+  const int span = static_cast<int>(std::min(turns, batches)) * kBatch;
+  const int chunks = (M - 1) / span + 1;
+  const long long grid = static_cast<long long>(B) * chunks;
+  if (grid > 0x7fffffffll) return SV_ERR_BAD_SHAPE;
+  const cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+  const unsigned g = static_cast<unsigned>(grid);
+  if (prompt) sv_count_kernel<true, false><<<g, kThreads, 0, s>>>(tokens, num, counts, M, V, chunks, span);
+  else if (batches > 1) sv_count_kernel<false, true><<<g, kThreads, 0, s>>>(tokens, num, counts, M, V, chunks, span);
+  else sv_count_kernel<false, false><<<g, kThreads, 0, s>>>(tokens, num, counts, M, V, chunks, span);
   return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }

@@ -89,7 +89,7 @@ def test_shape_refusals(L, change, status):
 
 @pytest.mark.parametrize("change,status", [
     (dict(t=None), 1), (dict(c=None), 1), (dict(B=0), 2), (dict(M=0), 2), (dict(V=0), 2), (dict(V=(1 << 24) + 1), 2),
-    (dict(B=(1 << 20) + 1), 2), (dict(B=1 << 20, M=1 << 30), 2), (dict(M=(1 << 30) + 1), 2), (dict(t=FAKE + 2), 5), (dict(n=FAKE + (1 << 20) + 1), 5),
+    (dict(B=(1 << 20) + 1), 2), (dict(M=(1 << 30) + 1), 2), (dict(t=FAKE + 2), 5), (dict(n=FAKE + (1 << 20) + 1), 5),
     (dict(c=FAKE + (1 << 30) + 1), 5), (dict(c=FAKE + 8), 9), (dict(n=FAKE + (1 << 30) + 8), 9),
 ])
 def test_count_refusals(L, change, status):
@@ -264,6 +264,19 @@ def test_shape_parts(sv, left, V):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("B,N,V,K,tree", [(6, 6, 162, 276, False), (4, 46, 256, 236, True), (3, 9, 2050, 1024, False), (2, 65, 70, 1024, True)])
+def test_shape_many_special_tokens(sv, B, N, V, K, tree):
+    """More biases than tokens, most of the tokens in the round: each named many times."""
+    rng = np.random.default_rng(V)
+    a = inputs(rng, B, N, V, "f32", tree, "some", None, K, 20)
+    a["tokens"] = rng.integers(-1, V + 1, (B, N)).astype(np.int32)
+    a["num"][:] = N
+    z = a["logits"].cuda()
+    sv.spec_verify_shape_logits(z, **on_gpu(a))
+    check(z.cpu(), a["logits"], a, 4 + K)
+
+
+@pytest.mark.gpu
 def test_shape_nan(sv):
     """NaN is barred like anything else, stays where nothing concerns it, and stays NaN where something does."""
     z = torch.full((2, 2, 64), float("nan"), dtype=torch.bfloat16, device="cuda")
@@ -333,7 +346,8 @@ def counted(rng, B, M, V, num="some"):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("prompt", [False, True])
-@pytest.mark.parametrize("B,M,V", [(1, 1, 1), (7, 9, 33), (64, 65, 1001), (5, 5000, 100), (3, 1025, 128256), (1024, 9, 32000)])
+@pytest.mark.parametrize("B,M,V", [(1, 1, 1), (7, 9, 33), (64, 65, 1001), (5, 5000, 100), (3, 1025, 128256), (1024, 9, 32000),
+                                   (2, 200000, 9000)])
 def test_count_parity(sv, B, M, V, prompt):
     rng = np.random.default_rng(M + V)
     for num in ("some", None):
