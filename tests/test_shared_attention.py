@@ -152,6 +152,9 @@ CASES = [
     ((140, 300, 170), (0, 3), (128,), 31, 1, 8, 128, 16, "bf16", False),
     ((140, 300, 170, 128, 200), (0, 5), (128,), 31, 2, 2, 128, 16, "bf16", False),
     ((100, 80, 90, 95), (0, 3, 4), (64, 80), 64, 1, 1, 64, 16, "f16", True),
+    ((300, 257, 600), (0, 3), (256,), 3, 2, 4, 128, 256, "bf16", False),
+    ((600, 512, 530, 100), (0, 3), (512,), 8, 2, 4, 64, 128, "f16", True),
+    ((390, 384, 500), (0, 3), (384,), 2, 1, 3, 256, 128, "bf16", True),
     ((530, 512), (0, 2), (512,), 65, 2, 2, 64, 128, "bf16", True),
     ((300, 257), (0, 2), (256,), 3, 1, 128, 128, 256, "f16", False),
     ((2100, 2049, 2500, 2048), (0, 4), (2048,), 2, 1, 5, 128, 16, "bf16", False),
@@ -245,6 +248,42 @@ def test_gpu_query_strides(sv, B, N):
         a.q = wide[:, ::3]
     out, lse = attend_shared(sv, a, common, call, (0, B))
     check_attention(a, out, lse, a.prefix, np.full(B, N), None)
+
+
+@pytest.mark.gpu
+def test_gpu_far_pages(sv):
+    """Offsets past 32 bits: pages that lie over 2^32 bytes into the cache, the front's among them."""
+    S, H, D, P = 16, 8, 128, (1 << 17) + 30                 # 4.3 GB of keys, as much of values
+    a = Batch((50, 40, 33), 3, H, 2, D, S, seed=2, poison=False)
+    common, call = with_fronts(a, (0, 3), (32,))
+    big = [torch.zeros((P, H, S, D), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    n = len(a.k)
+    for x, y in zip(big, (a.k, a.v)):
+        x[P - n:] = y
+    table = np.full((3, 4000), 1 << 30, np.int64)           # (room for fronts)
+    table[:, :call.shape[1]] = call.astype(np.int64) + P - n
+    c = sv.PagedCache(*big, dev(np.minimum(table, 1 << 30)))
+    out, lse = sv.attend_shared(a.q, c, dev(a.prefix), dev(common), dev((0, 3)))
+    check_attention(a, out, lse, a.prefix, np.array([3, 3, 3]), None)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_gpu_scores_of_tens_of_millions(sv, dtype):
+    """Equal keys whose scores are in the tens of millions, in the front and behind it: the mean of the values."""
+    a = Batch((640, 700, 655), 3, 2, 4, 128, 16, dtype, seed=6, poison=False)
+    common, call = with_fronts(a, (0, 3), (640,))
+    a.q.fill_(600.0)
+    a.k.fill_(500.0)
+    out, lse = attend_shared(sv, a, common, call, (0, 3), None, None, 1.0)
+    v = host(a.v)
+    for b in range(3):
+        for i in range(3):
+            e = oracle.entries(v, a.table, b, int(a.prefix[b]) + i + 1).mean(1)        # [heads, D]
+            want = np.repeat(e, 4, 0)
+            # A mean of values below 6 by equal weights: half a step of the output, and fp32 sums.
+            assert np.abs(host(out)[b, i] - want).max() <= torch.finfo(a.t).eps / 2 * 6 + 1e-4
+    assert np.abs(host(lse) / (600.0 * 500 * 128) - 1).max() <= 1e-6
 
 
 @pytest.mark.gpu
