@@ -122,6 +122,22 @@ __device__ __forceinline__ void tell_shared(const SharedParams& P, int row, int 
       make_int2(whole ? -1 : static_cast<int>(blockIdx.x), whole ? 0 : unit_owner(item_at + static_cast<long long>(tiles - 1) * P.R.units(tokens), plan));
 }
 
+// A launch whose CTAs may begin before the kernel ahead of it in the stream ends (which they wait for themselves).
+template <class Kern, class... Args>
+inline int launch_ahead(Kern kern, dim3 grid, int threads, size_t shared, cudaStream_t st, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = shared;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+}
+
 // Joins the parts of the items that the attention kernel's `grid` CTAs shared.
 int launch_attend_join(const AttendParams& P, bool f16, bool wide, int grid, cudaStream_t st);
 

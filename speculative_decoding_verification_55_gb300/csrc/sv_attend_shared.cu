@@ -23,19 +23,34 @@ namespace {
 
 using sv::SharedParams;
 
-// A launch whose CTAs may begin before the kernel ahead of it in the stream ends (which they wait for themselves).
-template <class Kern, class... Args>
-int launch_ahead(Kern kern, unsigned grid, int threads, cudaStream_t st, const Args&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(threads);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+// The tokens that are used, row after row, so that a front's query tiles have no others: 64 rows of 9 tokens, of which 62%
+// are used, over two prompts TODO us so, 86 without. CTA (b, y) copies every gridDim.y-th token of row b.
+constexpr int kPackThreads = 256, kMaxPacked = 1024;   // (each CTA sums up the rows before its own)
+__global__ void __launch_bounds__(kPackThreads) sv_attend_pack_kernel(const SharedParams P, int32_t* first, uint4* packed, int words) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  const sv::SharedRound& R = P.R;
+  const int b = blockIdx.x, tid = threadIdx.x;
+  int n, m, sum = 0;
+  auto tokens = [&](int row) { return sv::round_lengths(R.C, R.prefix, R.num, row, R.N, false, &n, &m) ? m : 0; };
+  const int mine = tokens(b);
+  for (int r = tid; r < b; r += kPackThreads) sum += tokens(r);
+  __shared__ int warps[kPackThreads / 32];
+  sum = __reduce_add_sync(kFull, sum);
+  if ((tid & 31) == 0) warps[tid >> 5] = sum;
+  __syncthreads();
+  int at = 0;
+#pragma unroll
+  for (int w = 0; w < kPackThreads / 32; ++w) at += warps[w];
+  if (blockIdx.y == 0 && tid == 0) {
+    first[b] = at;
+    if (b + 1 == R.B) first[R.B] = at + mine;
+  }
+  for (int i = blockIdx.y; i < mine; i += gridDim.y) {
+    const uint4* from = reinterpret_cast<const uint4*>(P.q + b * P.row_stride + i * P.token_stride);
+    uint4* to = packed + static_cast<size_t>(at + i) * words;
+#pragma unroll 4
+    for (int x = tid; x < words; x += kPackThreads) to[x] = __ldg(from + x);
+  }
 }
 
 template <int kQueries>
@@ -62,9 +77,11 @@ __global__ void __launch_bounds__(32 * kMergeWarps<kQueries>) sv_attend_merge_ke
   const int x = there ? id : 0, th = x / bunches, h0 = (x - th * bunches) * kQueries;   // its first query head of the key head's
   const int token = th / R.C.heads, head = th - token * R.C.heads, b = token / R.N, i = token - b * R.N;
   const int queries = min(kQueries, R.group - h0);
-  const size_t at = static_cast<size_t>(token) * P.Hq + head * R.group + h0;
+  const size_t out_at = static_cast<size_t>(token) * P.Hq + head * R.group + h0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int4 row = __ldcg(P.rows + b);
+  const int own = R.first_token(b) + i;        // its place among the tokens of q
+  const size_t at = static_cast<size_t>(own) * P.Hq + head * R.group + h0;
   const int m = __ldcg(P.bad_groups) == 0 ? row.x : -1, s = row.w;
   float v[kQueries][kCols], M[kQueries], L[kQueries];
 #pragma unroll
@@ -81,7 +98,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps<kQueries>) sv_attend_merge_ke
     const int2 oo = __ldcg(P.records + P.record_at(R.groups + b, head, 0, 0));
     int2 of = make_int2(0, -1);
     if (s > 0) {
-      row_front = (token - row.z) * R.group + h0;
+      row_front = (own - row.z) * R.group + h0;
       tile_front = row_front / P.tile_rows;
       row_front -= tile_front * P.tile_rows;
       of = __ldcg(P.records + P.record_at(row.y, head, tile_front, row.z));
@@ -165,20 +182,20 @@ __global__ void __launch_bounds__(32 * kMergeWarps<kQueries>) sv_attend_merge_ke
   for (int q = 0; q < kQueries; ++q) {
     if (q >= queries) break;
     const float inv = 1.0f / L[q];
-    uint32_t* out = reinterpret_cast<uint32_t*>(P.out) + (at + q) * (D / 2) + lane;
+    uint32_t* out = reinterpret_cast<uint32_t*>(P.out) + (out_at + q) * (D / 2) + lane;
 #pragma unroll
     for (int y = 0; y < kCols / 2; ++y)
       out[32 * y] = some ? sv::pack2<F16>(v[q][2 * y] * inv, v[q][2 * y + 1] * inv) : sv::pack2<F16>(none, none);
     if (P.lse && lane == 0)
-      P.lse[at + q] = some ? (M[q] * P.c + (log2f(L[q]) - sv::kProbBits<F16, true>)) * 0.6931471805599453f : none;
+      P.lse[out_at + q] = some ? (M[q] * P.c + (log2f(L[q]) - sv::kProbBits<F16, true>)) * 0.6931471805599453f : none;
   }
 }
 
 template <bool F16, int D, int kQueries>
 int merge(const SharedParams& P, int across, cudaStream_t st) {
   const long long warps = static_cast<long long>(P.R.B) * P.R.N * P.R.C.heads * ((P.R.group + kQueries - 1) / kQueries) * across;
-  return launch_ahead(sv_attend_merge_kernel<F16, D, kQueries>, static_cast<unsigned>((warps - 1) / kMergeWarps<kQueries> + 1),
-                      32 * kMergeWarps<kQueries>, st, P, across);
+  return sv::launch_ahead(sv_attend_merge_kernel<F16, D, kQueries>, dim3(static_cast<unsigned>((warps - 1) / kMergeWarps<kQueries> + 1)),
+                          32 * kMergeWarps<kQueries>, 0, st, P, across);
 }
 template <bool F16, int D>
 int merge(const SharedParams& P, int sms, cudaStream_t st) {
@@ -198,6 +215,12 @@ int merge(const SharedParams& P, int sms, cudaStream_t st) {
 
 constexpr int kMaxSms = 160;
 constexpr size_t kFlagBytes = 256;
+size_t rounded(size_t bytes) { return (bytes + 255) / 256 * 256; }
+// Tokens packed, and the rows' first ones.
+bool packs(int B, int N) { return N > 1 && B <= kMaxPacked; }
+size_t packed_bytes(int B, int N, int Hq, int D) {
+  return packs(B, N) ? rounded(static_cast<size_t>(B + 1) * 4) + rounded(static_cast<size_t>(B) * N * Hq * D * 2) : 0;
+}
 constexpr long long kShortRoom = 512, kLittleRoom = 48ll << 20;   // entries of a row; bytes of all rows' keys and values
 constexpr long long kMaxQueries = 1ll << 28;   // query heads of all tokens
 
@@ -205,7 +228,6 @@ bool sizes_ok(int32_t B, int32_t N, int32_t Hq, const sv_paged_cache* c) {
   return B >= 1 && B <= (1 << 20) && N >= 1 && N <= SV_MAX_GAMMA + 1 && Hq >= 1 && Hq <= 1024 && c->heads >= 1 &&
          Hq % c->heads == 0 && Hq / c->heads <= 128 && static_cast<long long>(B) * N * Hq <= kMaxQueries;
 }
-size_t rounded(size_t bytes) { return (bytes + 255) / 256 * 256; }
 size_t part_rows(int D) { return static_cast<size_t>(2 * kMaxSms) * (D < 256 ? 2 : 1) * 128; }
 // Query tiles of a key head's fronts, at most (each group's last may be short).
 long long front_tiles(long long queries, int groups, int group) { return queries / (128 / group * group) + groups + 1; }
@@ -229,7 +251,7 @@ extern "C" size_t spec_verify_shared_attention_workspace_size(int32_t B, int32_t
   const size_t records = static_cast<size_t>(heads) * (B + front_tiles(static_cast<long long>(B) * N * group, groups, group));
   return std::max(spec_verify_paged_attention_workspace_size(N, Hq, cache),
                   kFlagBytes + rounded(static_cast<size_t>(B) * sizeof(int4)) + rounded(records * sizeof(int2)) +
-                      rounded(part_rows(D) * row) + rounded(2 * queries * row));
+                      rounded(part_rows(D) * row) + rounded(2 * queries * row) + packed_bytes(B, N, Hq, D));
 }
 
 extern "C" int spec_verify_shared_attention(const void* q, int64_t q_row_stride, int64_t q_token_stride,
@@ -288,8 +310,6 @@ extern "C" int spec_verify_shared_attention(const void* q, int64_t q_row_stride,
   CUtensorMap kmap, vmap, qmap;
   st = sv::cache_tensor_map(cache, cache->k, sv::box_rows(cache), &kmap);
   if (st == SV_OK) st = sv::cache_tensor_map(cache, cache->v, sv::box_rows(cache), &vmap);
-  if (st == SV_OK)
-    st = sv::query_tensor_map(q, 0, N > 1 ? q_token_stride : q_row_stride, 1, B * N, Hq, D, cache->dtype, group, q_tokens, &qmap);
   if (st != SV_OK) return st;
   const cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   SharedParams P;
@@ -340,7 +360,18 @@ extern "C" int spec_verify_shared_attention(const void* q, int64_t q_row_stride,
   ws += rounded(part_rows(D) * (D * 4 + 8));
   P.side_o = reinterpret_cast<float*>(ws);
   P.side_ml = reinterpret_cast<float2*>(P.side_o + static_cast<size_t>(2) * B * N * Hq * D);
-  const bool f16 = cache->dtype == SV_DTYPE_F16;
+  ws += rounded(static_cast<size_t>(2) * B * N * Hq * (D * 4 + 8));
+  const bool f16 = cache->dtype == SV_DTYPE_F16, packed = num_queries && packs(B, N);
+  int32_t* const first = reinterpret_cast<int32_t*>(ws);
+  uint4* const tokens_to = reinterpret_cast<uint4*>(ws + rounded(static_cast<size_t>(B + 1) * 4));
+  P.R.first = packed ? first : nullptr;
+  st = packed ? sv::query_tensor_map(tokens_to, 0, static_cast<int64_t>(Hq) * D, 1, B * N, Hq, D, cache->dtype, group, q_tokens, &qmap)
+              : sv::query_tensor_map(q, 0, N > 1 ? q_token_stride : q_row_stride, 1, B * N, Hq, D, cache->dtype, group, q_tokens, &qmap);
+  if (st != SV_OK) return st;
+  if (packed) {
+    sv_attend_pack_kernel<<<dim3(B, std::min(N, 4)), kPackThreads, 0, s>>>(P, first, tokens_to, Hq * D / 8);
+    if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
+  }
   st = sv::launch_attend_shared(P, f16, kmap, vmap, qmap, q_tokens, grid, s);
   if (st != SV_OK) return st;
   return f16 ? merge<true>(P, sms, s) : merge<false>(P, sms, s);

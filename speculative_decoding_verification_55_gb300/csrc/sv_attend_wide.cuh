@@ -131,6 +131,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == kProducts) tm_alloc(&S.tm);
+  if constexpr (kShared) asm volatile("griddepcontrol.wait;" ::: "memory");   // the packed tokens
   sv::make_plan<kThreads>(R, S.scan, &S.plan);
   asm volatile("griddepcontrol.launch_dependents;");   // the join kernel's CTAs, which wait for this grid's end
   if (!kShared && tid < kWays && !P.by_item) P.shared[blockIdx.x * kWays + tid].x = -1;
@@ -338,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int32_t* par = nullptr;
       if constexpr (kShared) {
         side = W.row >= R.groups;
-        if (P.parents && side) par = P.parents + W.token0;
+        if (P.parents && side) par = P.parents + static_cast<size_t>(W.row - R.groups) * R.N;
       } else if (P.parents) {
         par = P.parents + static_cast<size_t>(W.row) * R.N;
       }
@@ -622,6 +623,8 @@ int launch(const ParamsOf<kShared>& P, const CUtensorMap& k, const CUtensorMap& 
   auto kern = sv_attend_wide_kernel<F16, D, kWays, kShared>;
   static std::atomic<unsigned long long> allowed{0};
   if (sv::allow_shared(kern, (kSmemBytes<D, kWays>), allowed) != SV_OK) return SV_ERR_CUDA;
+  if constexpr (kShared)
+    if (P.R.first) return sv::launch_ahead(kern, dim3(grid), kThreads, kSmemBytes<D, kWays>, st, P, k, v, q, q_tokens);
   kern<<<grid, kThreads, (kSmemBytes<D, kWays>), st>>>(P, k, v, q, q_tokens);
   return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }

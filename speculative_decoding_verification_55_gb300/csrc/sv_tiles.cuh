@@ -46,10 +46,12 @@ __device__ __forceinline__ bool row_work(const Round& R, int b, RowWork* w) {
 struct SharedRound : Round {
   const int32_t* start;                   // [groups + 1]: a group's rows are start[g] .. start[g + 1] - 1
   const int32_t* common;                  // [B]
-  int groups;
+  const int32_t* first;                   // [B + 1] a row's first token where the tokens that are used follow one another
+  int groups;                             // in q, or null: they do not, it is b N
   int one_rows;                           // up to so many query rows, an item is worked on with one way
   int one_units, two_units;               // of a tile on one way, and on two
   int two_extra;                          // of an item's queries and its end, on two ways; `extra` on one
+  __device__ __forceinline__ int first_token(int b) const { return first ? __ldcg(first + b) : b * N; }
   __device__ __forceinline__ bool two_ways(int tokens) const { return tokens * group > one_rows; }
   __device__ __forceinline__ int units(int tokens) const { return two_ways(tokens) ? two_units : one_units; }
 };
@@ -70,8 +72,8 @@ __device__ __forceinline__ bool row_work(const SharedRound& R, int v, SharedWork
     ok = s > 0 && front_ok(R.C, s);
     w->n = s - 1;
     w->m = 1;
-    w->tokens = (e - a) * R.N;
-    w->token0 = a * R.N;
+    w->token0 = ok ? R.first_token(a) : 0;
+    w->tokens = ok ? R.first_token(e) - w->token0 : 0;
     w->table_row = a;
     w->page0 = 0;
   } else {
@@ -79,11 +81,11 @@ __device__ __forceinline__ bool row_work(const SharedRound& R, int v, SharedWork
     ok = round_lengths(R.C, R.prefix, R.num, b, R.N, R.none_ok, &w->n, &w->m) && front_ok(R.C, s) && s <= w->n;
     w->n -= s;
     w->tokens = w->m;
-    w->token0 = b * R.N;
+    w->token0 = R.first_token(b);
     w->table_row = b;
     w->page0 = s >> R.C.page_log2;
   }
-  const bool some = ok && w->m > 0;
+  const bool some = ok && w->m > 0 && w->tokens > 0;
   w->tiles = some ? (w->n + w->m + (1 << R.tile_log2) - 1) >> R.tile_log2 : 0;
   w->q_tiles = some ? static_cast<int>((static_cast<long long>(w->tokens) * R.group + R.q_rows - 1) / R.q_rows) : 0;
   return ok;
@@ -106,7 +108,7 @@ __device__ __forceinline__ int4 row_of_group(const SharedRound& R, int b) {
     const int a = lo > 0 && lo <= R.groups ? __ldg(R.start + lo - 1) : -1;
     if (a < 0 || a > b || __ldg(R.common + a) != s) e.x = -1;
     e.y = lo - 1;
-    e.z = a * R.N;
+    e.z = e.x >= 0 ? R.first_token(a) : 0;
   }
   return e;
 }
