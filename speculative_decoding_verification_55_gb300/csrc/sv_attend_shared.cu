@@ -24,7 +24,7 @@ namespace {
 using sv::SharedParams;
 
 // The tokens that are used, row after row, so that a front's query tiles have no others: 64 rows of 9 tokens, of which 62%
-// are used, over two prompts TODO us so, 86 without. CTA (b, y) copies every gridDim.y-th token of row b.
+// are used, over two prompts 85 us so, 92 without. CTA (b, y) copies every gridDim.y-th token of row b.
 constexpr int kPackThreads = 256, kMaxPacked = 1024;   // (each CTA sums up the rows before its own)
 __global__ void __launch_bounds__(kPackThreads) sv_attend_pack_kernel(const SharedParams P, int32_t* first, uint4* packed, int words) {
   asm volatile("griddepcontrol.launch_dependents;");
@@ -221,7 +221,8 @@ bool packs(int B, int N) { return N > 1 && B <= kMaxPacked; }
 size_t packed_bytes(int B, int N, int Hq, int D) {
   return packs(B, N) ? rounded(static_cast<size_t>(B + 1) * 4) + rounded(static_cast<size_t>(B) * N * Hq * D * 2) : 0;
 }
-constexpr long long kShortRoom = 512, kLittleRoom = 48ll << 20;   // entries of a row; bytes of all rows' keys and values
+// Entries of a row; bytes of all rows' keys and values.
+constexpr long long kShortRoom = 512, kLittleRoom = 48ll << 20, kSomeRoom = 256ll << 20, kMuchRoom = 640ll << 20;
 constexpr long long kMaxQueries = 1ll << 28;   // query heads of all tokens
 
 bool sizes_ok(int32_t B, int32_t N, int32_t Hq, const sv_paged_cache* c) {
@@ -287,20 +288,18 @@ extern "C" int spec_verify_shared_attention(const void* q, int64_t q_row_stride,
   if (sms < 1) return SV_ERR_CUDA;
   if (sms > kMaxSms) sms = kMaxSms;
   const int D = cache->head_dim, group = Hq / cache->heads, rows_tile = 128 / group * group;
-  // A group's queries fill the query tiles that its front is read for; so do a row's where they are more than half of one.
-  // Then the products take the time, a front's second reading comes from L2 or is hidden behind them, and the rows go by
-  // themselves (which also leaves out the tokens behind a row's: a front's tiles have them all). Measured over 24 rows in
-  // two groups with up to 600 entries of their own, 4 key heads of 128, by fronts against by rows, tokens behind a row's
-  // among them: fronts of 4000 entries, 4 query rows a row and key head 29 against 39 us, 36 rows 45 against 43, 72 rows
-  // 59 against 43; fronts of 32,000, 36 rows 92 against 188, 144 rows 248 against 213; heads of 256, fronts of 4000,
-  // 36 rows 57 against 72, 72 rows 84 against 74.
-  // So do rows of little room, whose fronts cost less than the kernel's longer start and end and the merge: 64 rows of one
-  // token over 256 shared and up to 120 own entries 33 us by fronts, 27 by rows, over 1024 shared ones 34 and 44; 4 rows over
-  // 512 shared ones 17 and 13, over 8192 20 and 26 (32/8 heads of 128); 64 rows over 1024, 16/2 heads of 64, 21 and 17.
-  // (Heads of 256: 4 rows over 8192 22 and 20, 64 rows over 256 21 and 22.)
+  // A group's queries fill the query tiles that its front is read for. Where a row's queries alone fill much of one, fronts
+  // gain less, the second reading of their entries coming from L2 or hiding behind the products; and the kernel's start and
+  // end and the merge take longer. So rows go by themselves where they have more than a query tile, and else by the room
+  // that the tables and pages have for their entries (lengths are on the device). Fronts against rows, us, up to 600 entries
+  // a row's own: 32/8 heads of 128, one token a row: 4 rows over 512 shared entries 17 and 13, over 8192 20 and 26; 64 rows
+  // over 256 33 and 27, over 1024 34 and 44. 4 key heads of 128: 36 query rows, 24 rows over 4000 40 and 43, over 32,000 77
+  // and 188; 72 query rows 52 and 43, 122 and 190, 64 rows over 4000 69 and 82; 128 query rows, 64 rows over 4000 95 and 86,
+  // over 32,000 390 and 474. 16/2 heads of 64, one token: 64 rows over 1024 21 and 17, over 4096 23 and 30. One key head of
+  // 256, one token: 4 rows over 512 15 and 15, over 2048 16 and 17.
   const long long room = std::min<long long>(cache->max_pages, cache->num_pages) * cache->page_size;
-  const bool little = (D < 256 && room <= kShortRoom) || B * room * cache->heads * D * 4 <= (D < 256 ? kLittleRoom : kLittleRoom / 4);
-  if (N * group > 64 || little)
+  const long long little = N * group > 96 ? kMuchRoom : (N * group > 64 ? kSomeRoom : (D < 256 ? kLittleRoom : kLittleRoom / 4));
+  if (N * group > rows_tile || (D < 256 && room <= kShortRoom) || B * room * cache->heads * D * 4 <= little)
     return spec_verify_paged_attention(q, q_row_stride, q_token_stride, cache, prefix_len, num_queries, tree_parents, scale, out,
                                        out_lse, B, N, Hq, workspace, workspace_bytes, cuda_stream);
   // Two query tiles at once where a group has more than one's rows.

@@ -115,32 +115,33 @@ def with_fronts(a, start, fronts):
     return common, a.table.copy()
 
 
-def roomy(a, *tables):
-    """Pages behind the pool's and columns behind the tables', which nobody reads: room for more than the 48 MB of keys and
-    values, and the 512 entries a row, up to which rows go by themselves."""
+def roomy(a, table):
+    """(k, v, table) with pages behind the pool's and columns behind the table's, which nobody reads: room for more than the
+    bytes of keys and values, and the 512 entries a row, up to which rows go by themselves."""
     P, H, S, D = a.k.shape
-    pages = max(-(-(49 << 20) // (len(a.prefix) * H * S * D * 4)), 513 // S + 1) + 1
-    if P < pages:
-        order = (lambda x: x.transpose(1, 2)) if a.k.stride(1) < a.k.stride(2) else (lambda x: x)
-        for name in ("k", "v"):
-            x = torch.full((pages, S, H, D) if a.k.stride(1) < a.k.stride(2) else (pages, H, S, D), math.nan, dtype=a.t, device="cuda")
-            x = order(x)
-            x[:P] = getattr(a, name)
-            setattr(a, name, x)
-    wide = [np.full((t.shape[0], max(pages, t.shape[1])), 1 << 30, np.int32) for t in tables]
-    for w, t in zip(wide, tables):
-        w[:, :t.shape[1]] = t
-    return wide[0] if len(wide) == 1 else wide
+    rows = a.q.shape[1] * a.q.shape[2] // H
+    room = (49 if rows <= 64 else 257 if rows <= 96 else 641) << 20
+    pages = max(-(-room // (len(a.prefix) * H * S * D * 4)), 513 // S + 1, P) + 1
+    slots_first = a.k.stride(1) < a.k.stride(2)
+    pools = []
+    for x in (a.k, a.v):
+        big = torch.full((pages, S, H, D) if slots_first else (pages, H, S, D), math.nan, dtype=a.t, device="cuda")
+        big = big.transpose(1, 2) if slots_first else big
+        big[:P] = x
+        pools.append(big)
+    wide = np.full((table.shape[0], max(pages, table.shape[1])), 1 << 30, np.int32)
+    wide[:, :table.shape[1]] = table
+    return pools[0], pools[1], wide
 
 
 def attend_shared(sv, a, common, call, start, num=None, parents=None, scale=None, rows=False):
-    table = call if rows else roomy(a, call)   # (before the pool is taken)
-    cache = sv.PagedCache(a.k, a.v, dev(table))
+    k, v, table = (a.k, a.v, call) if rows else roomy(a, call)
+    cache = sv.PagedCache(k, v, dev(table))
     return sv.attend_shared(a.q, cache, dev(a.prefix), dev(common), dev(start), dev(num), dev(parents), scale)
 
 
 CASES = [
-    # prefix lengths, starts, fronts, N, Hkv, group, D, page, dtype, nhd (more than 64 query rows go by rows)
+    # prefix lengths, starts, fronts, N, Hkv, group, D, page, dtype, nhd (more than a tile's query rows go by rows)
     ((16,), (0, 1), (16,), 1, 1, 1, 64, 16, "bf16", False),                      # a row of its own, nothing behind
     ((20, 16, 33, 48), (0, 4), (16,), 1, 2, 4, 128, 16, "bf16", False),
     ((200, 129, 128, 500), (0, 4), (128,), 1, 2, 4, 128, 64, "f16", True),
@@ -155,6 +156,9 @@ CASES = [
     ((300, 257, 600), (0, 3), (256,), 3, 2, 4, 128, 256, "bf16", False),
     ((600, 512, 530, 100), (0, 3), (512,), 8, 2, 4, 64, 128, "f16", True),
     ((390, 384, 500), (0, 3), (384,), 2, 1, 3, 256, 128, "bf16", True),
+    ((210, 192, 250, 200), (0, 4), (192,), 9, 1, 8, 128, 16, "bf16", False),     # 72 query rows a row
+    ((210, 192, 250), (0, 3), (192,), 8, 1, 16, 64, 32, "f16", True),            # 128
+    ((130, 192, 128), (0, 3), (128,), 17, 1, 7, 256, 16, "bf16", False),         # 119
     ((530, 512), (0, 2), (512,), 65, 2, 2, 64, 128, "bf16", True),
     ((300, 257), (0, 2), (256,), 3, 1, 128, 128, 256, "f16", False),
     ((2100, 2049, 2500, 2048), (0, 4), (2048,), 2, 1, 5, 128, 16, "bf16", False),
@@ -309,8 +313,8 @@ def test_gpu_row_errors(sv):
     common[4] = 16                             # another front than its group's
     common[5] = 0                              # on its own
     call[5] = a.table[5]
-    table = roomy(a, call)
-    cache = sv.PagedCache(a.k, a.v, dev(table))
+    k, v, table = roomy(a, call)
+    cache = sv.PagedCache(k, v, dev(table))
     out, lse = sv.attend_shared(a.q, cache, dev(bad), dev(common), dev(start), dev(num))
     assert np.isnan(host(out)[[1, 2, 3, 4]]).all() and np.isnan(host(lse)[[1, 2, 3, 4]]).all()
     good = [0, 5, 6]
@@ -363,8 +367,8 @@ def test_gpu_by_rows(sv, N, G, rows):
     a = Batch((40, 0, 300, 77), N, 1, G, 64, 16, seed=4, poison=False)
     num = np.array([N, 1, N - 1, 0], np.int32)
     out, lse = attend_shared(sv, a, np.full(4, -7, np.int32), a.table, (3, 9), num, rows=rows)
-    table = a.table if rows else roomy(a, a.table)
-    want, want_lse = sv.attend(a.q, sv.PagedCache(a.k, a.v, dev(table)), dev(a.prefix), dev(num))
+    k, v, table = (a.k, a.v, a.table) if rows else roomy(a, a.table)
+    want, want_lse = sv.attend(a.q, sv.PagedCache(k, v, dev(table)), dev(a.prefix), dev(num))
     assert torch.equal(out, want) and torch.equal(lse, want_lse)
     check_attention(a, out, lse, a.prefix, num, None)
 
@@ -385,8 +389,8 @@ def test_gpu_unattended_values_have_no_part(sv, N, G):
     a.v[p, :, s] = math.inf
     p, s = oracle.place(a.table, 1, 64 + N - 1, 16)
     a.v[p, :, s, 1::2] = math.inf
-    table = roomy(a, a.table)
-    cache = sv.PagedCache(a.k, a.v, dev(table))
+    k, v, table = roomy(a, a.table)
+    cache = sv.PagedCache(k, v, dev(table))
     out, lse = sv.attend_shared(q, cache, dev(a.prefix), dev(common), dev((0, 4)), dev(num))
     o = host(out)
     assert np.isfinite(o[0]).all() and np.isfinite(o[2:]).all() and np.isfinite(o[1, :N - 1]).all()
@@ -395,7 +399,7 @@ def test_gpu_unattended_values_have_no_part(sv, N, G):
     r = host(ref)
     fine = np.isfinite(r)
     assert np.abs(o[fine] - r[fine]).max() <= 2.0 ** -7 * 4
-    a.v[a.table[0, 3], 0, 15, 5] = math.inf                               # the front's last entry
+    v[a.table[0, 3], 0, 15, 5] = math.inf                               # the front's last entry
     out, _ = sv.attend_shared(q, cache, dev(a.prefix), dev(common), dev((0, 4)), dev(num))
     o = host(out)
     for b in range(4):
@@ -408,8 +412,8 @@ def test_gpu_captured_and_streams(sv):
     a = Batch((300, 290, 310, 77), 5, 2, 4, 128, 16, seed=8, poison=False)
     start = (0, 3)
     common, call = with_fronts(a, start, (256,))
-    call = roomy(a, call)
-    cache = sv.PagedCache(a.k, a.v, dev(call))
+    k, v, call = roomy(a, call)
+    cache = sv.PagedCache(k, v, dev(call))
     args = [dev(a.prefix), dev(common), dev(start)]
     want, want_lse = sv.attend_shared(a.q, cache, *args)
     graph = torch.cuda.CUDAGraph()
