@@ -214,6 +214,9 @@ int merge(const SharedParams& P, int sms, cudaStream_t st) {
 }
 
 constexpr int kMaxSms = 160;
+// Query heads times room from which a third launch is worth the products that it saves (a third of 2 us for 256 query rows
+// and 128 entries, over the SMs: about 5 us).
+constexpr long long kWorthPacking = 1ll << 25;
 constexpr size_t kFlagBytes = 256;
 size_t rounded(size_t bytes) { return (bytes + 255) / 256 * 256; }
 // Tokens packed, and the rows' first ones.
@@ -360,7 +363,7 @@ extern "C" int spec_verify_shared_attention(const void* q, int64_t q_row_stride,
   P.side_o = reinterpret_cast<float*>(ws);
   P.side_ml = reinterpret_cast<float2*>(P.side_o + static_cast<size_t>(2) * B * N * Hq * D);
   ws += rounded(static_cast<size_t>(2) * B * N * Hq * (D * 4 + 8));
-  const bool f16 = cache->dtype == SV_DTYPE_F16, packed = num_queries && packs(B, N);
+  const bool f16 = cache->dtype == SV_DTYPE_F16, packed = num_queries && packs(B, N) && all * cache->heads * room >= kWorthPacking;
   int32_t* const first = reinterpret_cast<int32_t*>(ws);
   uint4* const tokens_to = reinterpret_cast<uint4*>(ws + rounded(static_cast<size_t>(B + 1) * 4));
   P.R.first = packed ? first : nullptr;

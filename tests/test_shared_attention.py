@@ -115,13 +115,16 @@ def with_fronts(a, start, fronts):
     return common, a.table.copy()
 
 
-def roomy(a, table):
+def roomy(a, table, packed=False):
     """(k, v, table) with pages behind the pool's and columns behind the table's, which nobody reads: room for more than the
-    bytes of keys and values, and the 512 entries a row, up to which rows go by themselves."""
+    bytes of keys and values, and the 512 entries a row, up to which rows go by themselves; packed: and for more than the
+    2^25 entries times query heads up to which the tokens that are used are not packed."""
     P, H, S, D = a.k.shape
     rows = a.q.shape[1] * a.q.shape[2] // H
     room = (49 if rows <= 64 else 257 if rows <= 96 else 641) << 20
     pages = max(-(-room // (len(a.prefix) * H * S * D * 4)), 513 // S + 1, P) + 1
+    if packed:
+        pages = max(pages, min(-(-(1 << 25) // (a.q[..., 0].numel() * S)) + 1, (1 << 20) // S))
     slots_first = a.k.stride(1) < a.k.stride(2)
     pools = []
     for x in (a.k, a.v):
@@ -134,8 +137,8 @@ def roomy(a, table):
     return pools[0], pools[1], wide
 
 
-def attend_shared(sv, a, common, call, start, num=None, parents=None, scale=None, rows=False):
-    k, v, table = (a.k, a.v, call) if rows else roomy(a, call)
+def attend_shared(sv, a, common, call, start, num=None, parents=None, scale=None, rows=False, packed=False):
+    k, v, table = (a.k, a.v, call) if rows else roomy(a, call, packed)
     cache = sv.PagedCache(k, v, dev(table))
     return sv.attend_shared(a.q, cache, dev(a.prefix), dev(common), dev(start), dev(num), dev(parents), scale)
 
@@ -166,22 +169,23 @@ CASES = [
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("rows", [False, True])
+@pytest.mark.parametrize("by", ["fronts", "packed", "rows"])
 @pytest.mark.parametrize("prefix,start,fronts,N,H,G,D,S,dtype,nhd", CASES)
-def test_gpu_shared(sv, prefix, start, fronts, N, H, G, D, S, dtype, nhd, rows):
+def test_gpu_shared(sv, prefix, start, fronts, N, H, G, D, S, dtype, nhd, by):
+    rows, packed = by == "rows", by == "packed"
     rng = np.random.default_rng(N * 31 + D)
     a = Batch(prefix, N, H, G, D, S, dtype, nhd, seed=N + D, poison=False)
     B = len(prefix)
     common, call = with_fronts(a, start, fronts)
     num = rng.integers(0, N + 1, B).astype(np.int32)
     num[-1] = N
-    out, lse = attend_shared(sv, a, common, call, start, num, rows=rows)
+    out, lse = attend_shared(sv, a, common, call, start, num, rows=rows, packed=packed)
     check_attention(a, out, lse, a.prefix, num, None)
-    again, lse2 = attend_shared(sv, a, common, call, start, num, rows=rows)
+    again, lse2 = attend_shared(sv, a, common, call, start, num, rows=rows, packed=packed)
     assert torch.equal(again, out) and torch.equal(lse2, lse)          # the same call, the same bits
     tree = random_tree(rng, B, N)
-    out, lse = attend_shared(sv, a, common, call, start, None, tree, 0.25, rows=rows)
-    check_attention(a, out, lse, a.prefix, np.full(B, N), tree, 0.25)
+    out, lse = attend_shared(sv, a, common, call, start, num if packed else None, tree, 0.25, rows=rows, packed=packed)
+    check_attention(a, out, lse, a.prefix, num if packed else np.full(B, N), tree, 0.25)
 
 
 @pytest.mark.gpu
@@ -197,8 +201,9 @@ def test_gpu_many_groups(sv, D, dtype, N, G):
     a = Batch(prefix, N, 1, G, D, 16, dtype, seed=D, poison=False)
     common, call = with_fronts(a, start, fronts)
     num = rng.integers(0, N + 1, 400).astype(np.int32)
-    out, lse = attend_shared(sv, a, common, call, start, num)
-    check_attention(a, out, lse, a.prefix, num, None)
+    for packed in (False, True):
+        out, lse = attend_shared(sv, a, common, call, start, num, packed=packed)
+        check_attention(a, out, lse, a.prefix, num, None)
 
 
 @pytest.mark.gpu
@@ -211,8 +216,8 @@ def test_gpu_large_groups(sv, N, G, D, B, front):
     common, call = with_fronts(a, (0, B), (front,))
     num = rng.integers(0, N + 1, B).astype(np.int32)
     tree = random_tree(rng, B, N)
-    for parents in (None, tree):
-        out, lse = attend_shared(sv, a, common, call, (0, B), num, parents)
+    for parents, packed in ((None, False), (tree, False), (None, True), (tree, True)):
+        out, lse = attend_shared(sv, a, common, call, (0, B), num, parents, packed=packed)
         check_attention(a, out, lse, a.prefix, num, parents)
 
 
@@ -238,8 +243,8 @@ def test_gpu_a_very_large_group(sv, N, G):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("B,N", [(5, 1), (1, 4)])
-def test_gpu_query_strides(sv, B, N):
+@pytest.mark.parametrize("B,N,packed", [(5, 1, False), (1, 4, False), (1, 4, True)])
+def test_gpu_query_strides(sv, B, N, packed):
     """One token a row, or one row: any distance of the rows, and of the tokens, will do."""
     a = Batch((70,) * B, N, 2, 4, 128, 16, seed=2, poison=False)
     common, call = with_fronts(a, (0, B), (64,))
@@ -250,8 +255,9 @@ def test_gpu_query_strides(sv, B, N):
     else:
         wide[:, ::3] = a.q
         a.q = wide[:, ::3]
-    out, lse = attend_shared(sv, a, common, call, (0, B))
-    check_attention(a, out, lse, a.prefix, np.full(B, N), None)
+    num = np.full(B, N)
+    out, lse = attend_shared(sv, a, common, call, (0, B), num, packed=packed)
+    check_attention(a, out, lse, a.prefix, num, None)
 
 
 @pytest.mark.gpu
@@ -301,7 +307,8 @@ def test_gpu_no_fronts(sv):
 
 
 @pytest.mark.gpu
-def test_gpu_row_errors(sv):
+@pytest.mark.parametrize("packed", [False, True])
+def test_gpu_row_errors(sv, packed):
     """A row in error gets NaN, the others what they should; a front's bad page concerns all its rows."""
     prefix = np.array([40, 40, 40, 40, 40, 40, 40], np.int32)
     a = Batch(prefix, 3, 2, 4, 128, 16, seed=4, poison=False)
@@ -313,7 +320,7 @@ def test_gpu_row_errors(sv):
     common[4] = 16                             # another front than its group's
     common[5] = 0                              # on its own
     call[5] = a.table[5]
-    k, v, table = roomy(a, call)
+    k, v, table = roomy(a, call, packed)
     cache = sv.PagedCache(k, v, dev(table))
     out, lse = sv.attend_shared(a.q, cache, dev(bad), dev(common), dev(start), dev(num))
     assert np.isnan(host(out)[[1, 2, 3, 4]]).all() and np.isnan(host(lse)[[1, 2, 3, 4]]).all()
@@ -325,7 +332,7 @@ def test_gpu_row_errors(sv):
     num = np.array([3, 1, 2, 3, 0, 3, 2], np.int32)
     common, call = with_fronts(a, start, (32, 32))
     call[:6, 1] = 1 << 29                      # in the first group's front
-    out, lse = attend_shared(sv, a, common, call, start, num)
+    out, lse = attend_shared(sv, a, common, call, start, num, packed=packed)
     o, z = host(out), host(lse)
     for b in range(6):
         assert np.isnan(o[b, :num[b]]).all() and np.isnan(z[b, :num[b]]).all()
@@ -333,13 +340,13 @@ def test_gpu_row_errors(sv):
     assert np.isfinite(o[6]).all()
     common, call = with_fronts(a, start, (32, 32))
     call[2, 2] = -1                            # in the row's own entries
-    out, lse = attend_shared(sv, a, common, call, start, num)
+    out, lse = attend_shared(sv, a, common, call, start, num, packed=packed)
     o = host(out)
     assert np.isnan(o[2, :num[2]]).all() and np.isfinite(o[[0, 1, 3, 4, 5, 6]]).all()
     tree = np.tile(np.array([[-1, 0, 1]], np.int32), (7, 1))
     tree[1, 0] = 0
     call[2] = a.table[2]
-    out, _ = attend_shared(sv, a, common, call, start, num, tree)
+    out, _ = attend_shared(sv, a, common, call, start, num, tree, packed=packed)
     assert np.isnan(host(out)[1, :1]).all() and np.isfinite(host(out)[[0, 2, 3, 4, 5, 6]]).all()
 
 
@@ -374,8 +381,8 @@ def test_gpu_by_rows(sv, N, G, rows):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("N,G", [(3, 2), (9, 8)])
-def test_gpu_unattended_values_have_no_part(sv, N, G):
+@pytest.mark.parametrize("N,G,packed", [(3, 2, False), (9, 4, False), (9, 8, False), (3, 2, True), (9, 4, True)])
+def test_gpu_unattended_values_have_no_part(sv, N, G, packed):
     """Infinities and NaN behind the last entry, in tokens that a token does not attend and in queries without a token;
     an infinity in the front reaches every row."""
     a = Batch((70, 64, 66, 129), N, 2, G, 128, 16, seed=3)                # unused slots hold NaN
@@ -389,7 +396,7 @@ def test_gpu_unattended_values_have_no_part(sv, N, G):
     a.v[p, :, s] = math.inf
     p, s = oracle.place(a.table, 1, 64 + N - 1, 16)
     a.v[p, :, s, 1::2] = math.inf
-    k, v, table = roomy(a, a.table)
+    k, v, table = roomy(a, a.table, packed)
     cache = sv.PagedCache(k, v, dev(table))
     out, lse = sv.attend_shared(q, cache, dev(a.prefix), dev(common), dev((0, 4)), dev(num))
     o = host(out)
@@ -407,14 +414,16 @@ def test_gpu_unattended_values_have_no_part(sv, N, G):
 
 
 @pytest.mark.gpu
-def test_gpu_captured_and_streams(sv):
+@pytest.mark.parametrize("packed", [False, True])
+def test_gpu_captured_and_streams(sv, packed):
     """A graph replayed on new contents; calls on two streams at once; a stream given; a workspace of any contents."""
     a = Batch((300, 290, 310, 77), 5, 2, 4, 128, 16, seed=8, poison=False)
     start = (0, 3)
     common, call = with_fronts(a, start, (256,))
-    k, v, call = roomy(a, call)
+    k, v, call = roomy(a, call, packed)
     cache = sv.PagedCache(k, v, dev(call))
-    args = [dev(a.prefix), dev(common), dev(start)]
+    num = np.array([5, 3, 0, 4], np.int32) if packed else np.full(4, 5, np.int32)
+    args = [dev(a.prefix), dev(common), dev(start), dev(num) if packed else None]
     want, want_lse = sv.attend_shared(a.q, cache, *args)
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
@@ -422,10 +431,13 @@ def test_gpu_captured_and_streams(sv):
     other = torch.cuda.Stream()
     for front in (256, 0, 128):
         args[1].copy_(dev(np.where(common > 0, front, 0)))
+        if packed:                             # other lengths than the captured ones
+            num = np.roll(num, 1)
+            args[3].copy_(dev(num))
         graph.replay()
-        num = np.full(4, 5)
         check_attention(a, out, lse, a.prefix, num, None)
     args[1].copy_(dev(common))
+    want, want_lse = sv.attend_shared(a.q, cache, *args)
     torch.cuda.synchronize()
     results = []
     for _ in range(20):
@@ -438,7 +450,7 @@ def test_gpu_captured_and_streams(sv):
     for fill in (0, 255):
         room = torch.full((need + 512,), fill, dtype=torch.uint8, device="cuda")
         out = torch.empty_like(want)
-        sv.spec_verify_shared_attention(a.q, cache, *args, None, None, out, None, room[:need])
+        sv.spec_verify_shared_attention(a.q, cache, *args, None, out, None, room[:need])
         assert torch.equal(out, want) and bool((room[need:] == fill).all())
 
 
