@@ -230,7 +230,7 @@ def spec_verify_shared_attention(q, cache, prefix_len, shared_len, group_start, 
 
 
 _attend_ws = {}
-# A call makes two launches on its stream's workspace: another thread's must not come in between.
+# A call makes two or three launches on its stream's workspace: another thread's must not come in between.
 _attend_lock = threading.Lock()
 
 
