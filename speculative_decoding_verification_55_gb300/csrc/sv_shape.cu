@@ -4,7 +4,7 @@
 //
 //   n = occurrences of token t in the row's output + among the round's tokens that position i follows,
 //   z' = z / rep where z > 0, else z * rep, if n > 0 or t is in the prompt (else z);
-//   z'' = z' - freq n - pres [n > 0] + sum of t's biases;  -inf where the mask bars t.
+//   z'' = z' - freq n - pres [n > 0], then t's biases added one by one in their order;  -inf where the mask bars t.
 //
 // In place, one launch. A CTA owns a run of a row's tokens at all of the round's positions, in two passes. First, 8
 // neighbouring tokens a thread (16 bytes of counts, a byte of a mask, 16 or 32 bytes of logits): the tokens that
@@ -119,15 +119,15 @@ __global__ void __launch_bounds__(kThreads, 6) sv_shape_kernel(const ShapeParams
   __shared__ unsigned list[kSpan];
   // The round's tokens and the biases in the run: places in it, in the round and among the biases; then, of the first of
   // each token, what it is (above the place's bits), its count, the places of the round that say it (a bit each, from place
-  // 1 on), its biases' sum.
+  // 1 on); of all, the token's next bias (0: none).
   constexpr int kPlace = (1 << kPlaceBits) - 1, kFirst = 1, kRoot = 2, kBiased = 4;
   extern __shared__ float dyn[];               // (as many as the call has biases: what is not taken is left to the L1)
   const int listed = kMaxRound + P.K;
   float* const value = dyn;                    // [K]
-  float* const sum = value + P.K;              // [listed]
-  unsigned short* const places = reinterpret_cast<unsigned short*>(sum + listed);   // [listed]
+  unsigned short* const places = reinterpret_cast<unsigned short*>(value + P.K);    // [listed]
   unsigned short* const indexes = places + listed;
-  int16_t* const counted = reinterpret_cast<int16_t*>(indexes + listed);
+  unsigned short* const biases = indexes + listed;
+  int16_t* const counted = reinterpret_cast<int16_t*>(biases + listed);
   __shared__ unsigned long long match[kMaxRound];
   __shared__ int up[kMaxRound], lists[2], length;
   __shared__ unsigned long long above[sv::kMaxTreeNodes];
@@ -258,12 +258,11 @@ __global__ void __launch_bounds__(kThreads, 6) sv_shape_kernel(const ShapeParams
     for (int k = 0; k < kW; ++k)
       if ((touched >> k) & 1) list[to++] = static_cast<unsigned>(at + k) | static_cast<unsigned>(static_cast<unsigned short>(count[u].x[k])) << 16;
   }
-  // (Looked up by each token at each position, 316 rows of 6 positions with 276 biases and V 162 took 52 us; so 36.)
+  // (Looked up by each token at each position, 316 rows of 6 positions with 276 biases and V 162 took 52 us; so 39.)
   for (int x = tid; x < ns + nb; x += kThreads) {
     const int e = x < ns ? x : kMaxRound + x - ns, place = places[e];
-    int what = kFirst;                         // (its own bits above the place are not set yet, others' may be)
+    int what = kFirst, next = 0;               // (its own bits above the place are not set yet, others' may be)
     unsigned long long bits = 0;
-    float f = 0.0f;
     for (int r = 0; r < ns; ++r) {
       if ((places[r] & kPlace) != place) continue;
       if (r < e) what = 0;
@@ -271,14 +270,13 @@ __global__ void __launch_bounds__(kThreads, 6) sv_shape_kernel(const ShapeParams
       if (a == 0) what |= kRoot;
       else bits |= 1ull << (a - 1);
     }
-    for (int r = kMaxRound; r < kMaxRound + nb; ++r) {
-      if ((places[r] & kPlace) != place) continue;
-      if (r < e) what = 0;
-      what |= kBiased;
-      f += value[r - kMaxRound];
-    }
+    for (int r = kMaxRound; r < e; ++r)
+      if ((places[r] & kPlace) == place) what = 0;
+    for (int r = kMaxRound + nb - 1; r > e && r >= kMaxRound; --r)   // (backwards and to its end: four reads at a time)
+      if ((places[r] & kPlace) == place) next = r;
+    if (what && (next > 0 || e >= kMaxRound)) what |= kBiased;
     places[e] = static_cast<unsigned short>(place | what << kPlaceBits);
-    sum[e] = f;
+    biases[e] = static_cast<unsigned short>(next);
     counted[e] = P.counts ? __ldg(P.counts + static_cast<size_t>(b) * P.V + v0 + place) : 0;
     if (e < kMaxRound) match[e] = bits;
   }
@@ -293,9 +291,8 @@ __global__ void __launch_bounds__(kThreads, 6) sv_shape_kernel(const ShapeParams
   for (int x = tid; x < items; x += kThreads) {
     const int block = all == 1 ? x : __umulhi(x, inv), l = x - block * all;
     const int y0 = block * step, steps = min(step, here - y0);
-    int place, n, what = 0;
+    int place, n, what = 0, bias = 0;          // bias: the token's first
     unsigned long long bits = 0;
-    float add = 0.0f;
     if (l < len) {
       place = list[l] & kPlace;
       n = static_cast<int>(list[l]) >> 16;
@@ -305,11 +302,11 @@ __global__ void __launch_bounds__(kThreads, 6) sv_shape_kernel(const ShapeParams
       if (!(what & kFirst)) continue;
       place = places[e] & kPlace;
       n = counted[e];
-      add = sum[e];
+      bias = e < kMaxRound ? biases[e] : e;
       if (e < kMaxRound) bits = match[e];
     }
     T* const at = row + static_cast<size_t>(y0) * P.V + place;
-    float z[kPositions];
+    float z[kPositions] = {};
     unsigned allowed = 0;                      // a bit a position
 #pragma unroll
     for (int y = 0; y < kPositions; ++y) {
@@ -328,12 +325,25 @@ __global__ void __launch_bounds__(kThreads, 6) sv_shape_kernel(const ShapeParams
       // (Place 0 of a tree, the root, is above every node; of a chain, before every position but its own.)
       int uses = n;
       if (what) uses += __popcll(bits & above[i]) + ((what & kRoot) && (P.parents || i > 0));
-      if (!(uses > 0 || prompt || (what & kBiased))) continue;
+      if (!(uses > 0 || prompt || (what & kBiased))) {
+        allowed &= ~(1u << y);
+        continue;
+      }
       float v = z[y];
       if (uses > 0 || prompt) v = v > 0.0f ? v / rep : v * rep;
       v -= freq * static_cast<float>(uses);
       if (uses > 0) v -= pres;
-      at[static_cast<size_t>(y) * P.V] = from_float<T>(v + add);
+      z[y] = v;
+    }
+    for (; bias > 0; bias = biases[bias]) {    // (their sum, added once, would round and overflow in another way)
+      const float f = value[bias - kMaxRound];
+#pragma unroll
+      for (int y = 0; y < kPositions; ++y) z[y] += f;
+    }
+#pragma unroll
+    for (int y = 0; y < kPositions; ++y) {
+      if (y >= steps) break;
+      if ((allowed >> y) & 1) at[static_cast<size_t>(y) * P.V] = from_float<T>(z[y]);
     }
   }
 }
@@ -352,7 +362,7 @@ int launch_shape(ShapeParams& P, bool whole, int sms, cudaStream_t st) {
   const long long grid = static_cast<long long>(P.B) * ((P.V + span - 1) / span) * P.blocks;
   if (grid > 0x7fffffffll) return SV_ERR_BAD_SHAPE;
   const unsigned g = static_cast<unsigned>(grid);
-  const size_t bytes = static_cast<size_t>(P.K) * 4 + static_cast<size_t>(kMaxRound + P.K) * (4 + 3 * 2);
+  const size_t bytes = static_cast<size_t>(P.K) * 4 + static_cast<size_t>(kMaxRound + P.K) * (4 * 2);
   if (!whole) sv_shape_kernel<T, 1, 8><<<g, kThreads, bytes, st>>>(P);
   else if (two) sv_shape_kernel<T, 8, 2><<<g, kThreads, bytes, st>>>(P);
   else sv_shape_kernel<T, 8, 1><<<g, kThreads, bytes, st>>>(P);
