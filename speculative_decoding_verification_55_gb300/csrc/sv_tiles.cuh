@@ -39,8 +39,8 @@ __device__ __forceinline__ bool row_work(const Round& R, int b, RowWork* w) {
 }
 // A batch whose rows share the fronts of their contexts: its work is that of the groups (the queries of all tokens of
 // a group's rows, N a row, against the entries that the rows share, from the first row's table), then that of the rows
-// (a row's tokens against its entries from common[b] on). A group's front is, for the masks, a row's whose last entry
-// is the round's only one: every query attends it.
+// (a row's tokens against its entries from common[b] on). A front is, for the masks, entries before a round without any of
+// its own: every query attends all of them, and their values stay in the products whatever they are.
 // A unit of this batch's work is a fraction of a tile, since tiles of fronts and rows take different times; a tile is its
 // first unit's CTA's.
 struct SharedRound : Round {
@@ -70,8 +70,8 @@ __device__ __forceinline__ bool row_work(const SharedRound& R, int v, SharedWork
     ok = a >= 0 && a < e && e <= R.B;
     const int s = ok ? __ldg(R.common + a) : 0;
     ok = s > 0 && front_ok(R.C, s);
-    w->n = s - 1;
-    w->m = 1;
+    w->n = s;
+    w->m = 0;
     w->token0 = ok ? R.first_token(a) : 0;
     w->tokens = ok ? R.first_token(e) - w->token0 : 0;
     w->table_row = a;
@@ -85,7 +85,7 @@ __device__ __forceinline__ bool row_work(const SharedRound& R, int v, SharedWork
     w->table_row = b;
     w->page0 = s >> R.C.page_log2;
   }
-  const bool some = ok && w->m > 0 && w->tokens > 0;
+  const bool some = ok && w->tokens > 0;
   w->tiles = some ? (w->n + w->m + (1 << R.tile_log2) - 1) >> R.tile_log2 : 0;
   w->q_tiles = some ? static_cast<int>((static_cast<long long>(w->tokens) * R.group + R.q_rows - 1) / R.q_rows) : 0;
   return ok;

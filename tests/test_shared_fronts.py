@@ -1,0 +1,54 @@
+"""Shared attention: values of a front's last entries that are not finite."""
+import math
+
+import numpy as np
+import pytest
+
+from oracle import paged_cache_oracle as oracle
+from test_paged_cache import Batch, dev, host
+from test_shared_attention import roomy, with_fronts
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module")
+def sv():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import speculative_decoding_verification_55_gb300 as m
+    m.build_library()
+    return m
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("front", [640, 656])              # a whole tile at its end, and a part of one
+@pytest.mark.parametrize("N,G,D,dtype", [(1, 4, 128, "bf16"), (3, 4, 64, "f16"), (9, 8, 128, "bf16"), (2, 4, 256, "bf16")])
+def test_gpu_infinity_in_a_fronts_last_entry(sv, N, G, D, dtype, front, packed):
+    """A front's last entry whose probability is 0 in fp32 and whose value is infinite: NaN, as by the paged attention. So
+    are the entries before it; where the probability is not too small it is infinite."""
+    a = Batch((700, 690, 720), N, 1, G, D, 16, dtype, seed=N, poison=False)
+    common, call = with_fronts(a, (0, 3), (front,))
+    a.q[:] = 1.0
+    a.k.clamp_(-0.1, 0.1)
+    for j, d in ((front - 1, 5), (front - 2, 7), (130, 9)):
+        p, s = oracle.place(a.table, 0, j, 16)
+        a.k[p, :, s] = -100.0                              # scores of -800 and less, the others above -2
+        a.v[p, :, s, d] = math.inf
+    for j, d in ((front - 1, 11), (front - 3, 13)):
+        p, s = oracle.place(a.table, 0, j, 16)
+        a.v[p, :, s, d] = math.inf
+    p, s = oracle.place(a.table, 0, front - 3, 16)
+    a.k[p, :, s] = 0.0
+    num = np.array([N, max(N - 1, 1), N], np.int32)
+    k, v, table = roomy(a, call, packed)
+    cache = sv.PagedCache(k, v, dev(table))
+    out, lse = sv.attend_shared(a.q, cache, dev(a.prefix), dev(common), dev((0, 3)), dev(num))
+    ref, _ = sv.attend(a.q, cache, dev(a.prefix), dev(num))
+    o, r = host(out), host(ref)
+    assert np.array_equal(np.isnan(o), np.isnan(r)) and np.array_equal(np.isinf(o), np.isinf(r))
+    for b in range(3):
+        assert np.isnan(o[b, :num[b]][..., [5, 7, 9, 11]]).all() and (o[b, :num[b], :, 13] == math.inf).all()
+        rest = np.delete(o[b, :num[b]], [5, 7, 9, 11, 13], axis=-1)
+        assert np.isfinite(rest).all()
+    assert np.isfinite(host(lse)).all()
