@@ -560,18 +560,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     fence_before();
   }
-  if constexpr (kShared) {                     // (no group that is out of range has been taken)
-    if (blockIdx.x == gridDim.x - 1) {
-      bool bad = false;
-#pragma unroll 1
-      for (int g = tid; g <= R.groups; g += kThreads) {
-        const int e = __ldg(R.start + g);
-        bad |= e > R.B || (g == 0 ? e < 0 : __ldg(R.start + g - 1) > e);
-      }
-      bad = __syncthreads_or(bad);
-      if (tid == 0) *P.bad_groups = bad;
-    }
-  }
+  if constexpr (kShared)
+    if (blockIdx.x == 0 && tid == 0) *P.bad_groups = S.plan.bad;
   __syncthreads();
   if (warp == kProducts) {
     if (S.lost && lane == 0) {                 // products in flight end before the tensor memory is given back

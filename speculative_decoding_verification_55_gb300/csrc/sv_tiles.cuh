@@ -120,6 +120,14 @@ __device__ __forceinline__ int item_units(const SharedRound& R, const SharedWork
 }
 __device__ __forceinline__ int most_units(const Round&) { return 1; }
 __device__ __forceinline__ int most_units(const SharedRound& R) { return max(R.one_units, R.two_units); }
+// Whether group v's starts are out of order or of range. (Groups that overlap would be worked on once each: with them the
+// work of a batch would not be bounded by its sizes, so that one such group leaves none.)
+__device__ __forceinline__ bool starts_bad(const Round&, int) { return false; }
+__device__ __forceinline__ bool starts_bad(const SharedRound& R, int v) {
+  if (v >= R.groups) return false;
+  const int a = __ldg(R.start + v), e = __ldg(R.start + v + 1);
+  return a < 0 || a > e || e > R.B;
+}
 __device__ __forceinline__ int work_rows(const Round& R) { return R.B; }
 __device__ __forceinline__ int work_rows(const SharedRound& R) { return R.groups + R.B; }
 // What the two kinds of batches differ in: the tokens of an item's queries, their first one, the tree of its row, and
@@ -154,6 +162,7 @@ struct Plan {
   long long at;                           // first unit of this CTA's run
   long long row_at;                       // first unit of the row that holds it
   int row;
+  bool bad;                               // the groups' starts do not ascend within 0 .. B: no work
 };
 
 // Where this CTA's run begins; every thread of the CTA calls it (kThreads of them), `sh` and `plan` in
@@ -165,11 +174,13 @@ __device__ void make_plan(const Rows& R, long long (&sh)[kThreads / 32], Plan* p
   const int n = work_rows(R), per = (n + kThreads - 1) / kThreads;
   const int b0 = min(tid * per, n), b1 = min(b0 + per, n);
   long long sum = 0;
+  bool bad = false;
   typename Batch<kShared>::Work w;
 #pragma unroll 1
   for (int b = b0; b < b1; ++b) {
     row_work(R, b, &w);
     sum += row_units(R, w);
+    bad |= starts_bad(R, b);
   }
   long long incl = sum;
 #pragma unroll
@@ -178,13 +189,15 @@ __device__ void make_plan(const Rows& R, long long (&sh)[kThreads / 32], Plan* p
     if (lane >= o) incl += y;
   }
   if (lane == 31) sh[warp] = incl;
-  __syncthreads();
+  if constexpr (kShared) bad = __syncthreads_or(bad);
+  else __syncthreads();
   long long before = incl - sum, total = 0;
 #pragma unroll
   for (int x = 0; x < kThreads / 32; ++x) {
     if (x < warp) before += sh[x];
     total += sh[x];
   }
+  if (kShared && bad) total = sum = 0;
   // (Every run has a tile's first unit where it is inside an item.)
   const long long runs = kShared ? max(total / most_units(R), min(total, 1ll)) : total;
   const long long parts = runs < gridDim.x ? runs : gridDim.x;
@@ -194,6 +207,7 @@ __device__ void make_plan(const Rows& R, long long (&sh)[kThreads / 32], Plan* p
     plan->parts = parts;
     plan->at = at;
     plan->row = n;
+    plan->bad = bad;
   }
   __syncthreads();
   if (at >= before && at < before + sum) {

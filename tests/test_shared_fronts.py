@@ -1,4 +1,4 @@
-"""Shared attention: values of a front's last entries that are not finite."""
+"""Shared attention: values of a front's last entries that are not finite; starts that do not ascend."""
 import math
 
 import numpy as np
@@ -52,3 +52,37 @@ def test_gpu_infinity_in_a_fronts_last_entry(sv, N, G, D, dtype, front, packed):
         rest = np.delete(o[b, :num[b]], [5, 7, 9, 11, 13], axis=-1)
         assert np.isfinite(rest).all()
     assert np.isfinite(host(lse)).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N", [1, 3])
+def test_gpu_starts_that_do_not_ascend_cost_nothing(sv, N):
+    """Starts that name the whole batch again and again: all rows are in error, and the call is not worked on. (Worked on, it
+    would take what 4000 groups of all rows take, over ten times the call's time.)"""
+    B = 64
+    a = Batch((2100,) * B, N, 2, 4, 128, 16, seed=1, poison=False)
+    common, call = with_fronts(a, (0, B), (2048,))
+    k, v, table = roomy(a, call)
+    cache = sv.PagedCache(k, v, dev(table))
+    args = dev(a.prefix), dev(common)
+    good, bad = dev((0, B)), dev((0, B) * 4000 + (B,))
+
+    def timed(start):
+        best = math.inf
+        for _ in range(5):
+            t0, t1 = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            t0.record()
+            out, lse = sv.attend_shared(a.q, cache, *args, start)
+            t1.record()
+            torch.cuda.synchronize()
+            best = min(best, t0.elapsed_time(t1))
+        return best, out, lse
+    t_good, out, lse = timed(good)
+    want = sv.attend(a.q, cache, args[0])
+    assert float((out.float() - want[0].float()).abs().max()) <= 4 * 2.0 ** -8 * 6
+    t_bad, out, lse = timed(bad)
+    assert bool(out.isnan().all()) and bool(lse.isnan().all())
+    assert t_bad <= 5 * t_good, (t_bad, t_good)
+    again, lse = sv.attend_shared(a.q, cache, *args, good)             # the next call is as it should be
+    assert float((again.float() - want[0].float()).abs().max()) <= 4 * 2.0 ** -8 * 6
+    assert float((lse - want[1]).abs().max()) <= 1e-4
