@@ -232,7 +232,23 @@ __device__ __forceinline__ int unit_owner(long long t, const Plan& p) {
   return static_cast<int>(((t + 1) * p.parts - 1) / p.total);
 }
 
-// A walk over the items of this CTA's run: begin(), then next() while it returns true.
+// The first of the rows from `row` on that has work, by a whole warp (the last row where none has): a batch may have room
+// for many groups and few that hold rows. (One after the other, each waits for its start and its front's length: one group
+// of 64 rows of 4 tokens over 6000 shared entries took 62 us, with 127 empty ones behind it 83.)
+__device__ __forceinline__ int skip_idle(const SharedRound& R, int row) {
+  const int last = work_rows(R) - 1, lane = threadIdx.x & 31;
+  for (;; row += 32) {
+    SharedWork w;
+    w.q_tiles = 0;
+    if (row + lane <= last) row_work(R, row + lane, &w);
+    const unsigned some = __ballot_sync(kFull, w.q_tiles > 0);
+    if (some) return row + __ffs(some) - 1;
+    if (row + 32 > last) return last;
+  }
+}
+
+// A walk over the items of this CTA's run: begin(), then next() while it returns true. (Of a batch that shares fronts, by
+// whole warps.)
 template <bool kShared>
 struct WalkOf {
   typedef typename Batch<kShared>::Rows Rows;
@@ -255,6 +271,11 @@ struct WalkOf {
         row_at += row_units(R, w);
         ++row;
         row_work(R, row, &w);
+        if constexpr (kShared)
+          if (w.q_tiles == 0) {
+            row = skip_idle(R, row);
+            row_work(R, row, &w);
+          }
       }
       const int per = item_units(R, w), extra = extra_units(R, w);
       const Unit in_row = static_cast<Unit>(at - row_at);

@@ -1,12 +1,13 @@
-"""Shared attention: values of a front's last entries that are not finite; starts that do not ascend."""
+"""Shared attention: values of a front's last entries that are not finite; starts that do not ascend; groups
+that hold nothing."""
 import math
 
 import numpy as np
 import pytest
 
 from oracle import paged_cache_oracle as oracle
-from test_paged_cache import Batch, dev, host
-from test_shared_attention import roomy, with_fronts
+from test_paged_cache import Batch, check_attention, dev, host
+from test_shared_attention import attend_shared, roomy, with_fronts
 
 torch = pytest.importorskip("torch")
 
@@ -86,3 +87,47 @@ def test_gpu_starts_that_do_not_ascend_cost_nothing(sv, N):
     again, lse = sv.attend_shared(a.q, cache, *args, good)             # the next call is as it should be
     assert float((again.float() - want[0].float()).abs().max()) <= 4 * 2.0 ** -8 * 6
     assert float((lse - want[1]).abs().max()) <= 1e-4
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("N,G,D,B", [(9, 4, 128, 20), (1, 4, 64, 150), (2, 8, 256, 20)])
+def test_gpu_a_large_group_among_empty_ones(sv, N, G, D, B, packed):
+    """A caller with room for many groups: one that has all the rows, the others empty, before it and behind it."""
+    rng = np.random.default_rng(B)
+    prefix = 1024 + rng.integers(0, 60, B)
+    a = Batch(prefix, N, 1, G, D, 16, seed=B, poison=False)
+    start = (0,) * 30 + (B,) * 40
+    common, call = with_fronts(a, (0, B), (1024,))
+    num = rng.integers(0, N + 1, B).astype(np.int32)
+    out, lse = attend_shared(sv, a, common, call, start, num, packed=packed)
+    check_attention(a, out, lse, a.prefix, num, None)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lone", [0, 5])
+def test_gpu_empty_groups_cost_little(sv, lone):
+    """A group of 64 rows, with 1000 empty ones behind it and without them: the same outputs, in no more than twice the time.
+    (With a wait for each empty group it would be over three times.)"""
+    B = 64
+    a = Batch((2100,) * B, 3, 2, 4, 128, 16, seed=1, poison=False)
+    common, call = with_fronts(a, (0, B - lone), (2048,))
+    k, v, table = roomy(a, call)
+    cache = sv.PagedCache(k, v, dev(table))
+    args = dev(a.prefix), dev(common)
+    starts = dev((0, B - lone)), dev((0,) + (B - lone,) * 1001)
+
+    def timed(start):
+        best = math.inf
+        for _ in range(10):
+            t0, t1 = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            t0.record()
+            out, lse = sv.attend_shared(a.q, cache, *args, start)
+            t1.record()
+            torch.cuda.synchronize()
+            best = min(best, t0.elapsed_time(t1))
+        return best, out, lse
+    (alone, out, lse), (among, out2, lse2) = timed(starts[0]), timed(starts[1])
+    check_attention(a, out, lse, a.prefix, np.full(B, 3), None)
+    check_attention(a, out2, lse2, a.prefix, np.full(B, 3), None)
+    assert among <= 2 * alone, (among, alone)
