@@ -376,7 +376,8 @@ int spec_verify_paged_attention(const void* q, int64_t q_row_stride, int64_t q_t
  * group_start    [groups + 1] int32, ascending from at least 0 to at most B: group g is rows group_start[g] ..
  *                group_start[g + 1] - 1 (it may be empty). Rows in no group have shared_len 0.
  * workspace      spec_verify_shared_attention_workspace_size(...) bytes, 256-byte aligned, without setup: among them two
- *                fp32 results of each query, 8 B N Hq (D + 2) bytes, and q again. One workspace serves one call at a time.
+ *                fp32 results of each query, 8 B N Hq (D + 2) bytes, and q again (with more than 128 query rows of a row's key
+ *                head, below, the paged attention's alone). One workspace serves one call at a time.
  * Where fronts gain nothing (by the call's sizes: more than 128 query rows, tokens times query heads, of a row's key head, or
  * little room in the page tables and pages) every row is attended by its own table, and shared_len and group_start are not read.
  * Else a row whose shared_len is none of the above is in error; all are where group_start does not ascend within 0 .. B.

@@ -232,9 +232,10 @@ bool sizes_ok(int32_t B, int32_t N, int32_t Hq, const sv_paged_cache* c) {
   return B >= 1 && B <= (1 << 20) && N >= 1 && N <= SV_MAX_GAMMA + 1 && Hq >= 1 && Hq <= 1024 && c->heads >= 1 &&
          Hq % c->heads == 0 && Hq / c->heads <= 128 && static_cast<long long>(B) * N * Hq <= kMaxQueries;
 }
+int rows_of_tile(int group) { return 128 / group * group; }   // query rows of a query tile: whole tokens
 size_t part_rows(int D) { return static_cast<size_t>(2 * kMaxSms) * (D < 256 ? 2 : 1) * 128; }
 // Query tiles of a key head's fronts, at most (each group's last may be short).
-long long front_tiles(long long queries, int groups, int group) { return queries / (128 / group * group) + groups + 1; }
+long long front_tiles(long long queries, int groups, int group) { return queries / rows_of_tile(group) + groups + 1; }
 
 }  // namespace
 
@@ -251,6 +252,7 @@ extern "C" size_t spec_verify_shared_attention_workspace_size(int32_t B, int32_t
                                                               const sv_paged_cache* cache) {
   if (!cache || !sizes_ok(B, N, Hq, cache) || cache->head_dim < 1 || cache->head_dim > 256 || groups < 1 || groups > (1 << 20)) return 0;
   const int D = cache->head_dim, heads = cache->heads, group = Hq / heads;
+  if (N * group > rows_of_tile(group)) return spec_verify_paged_attention_workspace_size(N, Hq, cache);   // rows go by themselves
   const size_t row = D * 4 + 8, queries = static_cast<size_t>(B) * N * Hq;
   const size_t records = static_cast<size_t>(heads) * (B + front_tiles(static_cast<long long>(B) * N * group, groups, group));
   return std::max(spec_verify_paged_attention_workspace_size(N, Hq, cache),
@@ -290,7 +292,7 @@ extern "C" int spec_verify_shared_attention(const void* q, int64_t q_row_stride,
   int sms = sv::device_sms(dev);
   if (sms < 1) return SV_ERR_CUDA;
   if (sms > kMaxSms) sms = kMaxSms;
-  const int D = cache->head_dim, group = Hq / cache->heads, rows_tile = 128 / group * group;
+  const int D = cache->head_dim, group = Hq / cache->heads, rows_tile = rows_of_tile(group);
   // A group's queries fill the query tiles that its front is read for. Where a row's queries alone fill much of one, fronts
   // gain less, the second reading of their entries coming from L2 or hiding behind the products; and the kernel's start and
   // end and the merge take longer. So rows go by themselves where they have more than a query tile, and else by the room

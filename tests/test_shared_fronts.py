@@ -1,12 +1,13 @@
 """Shared attention: values of a front's last entries that are not finite; starts that do not ascend; groups
-that hold nothing."""
+that hold nothing; the workspace of calls whose rows go by themselves."""
+import ctypes
 import math
 
 import numpy as np
 import pytest
 
 from oracle import paged_cache_oracle as oracle
-from test_paged_cache import Batch, check_attention, dev, host
+from test_paged_cache import Batch, cache_struct, check_attention, dev, host
 from test_shared_attention import attend_shared, roomy, with_fronts
 
 torch = pytest.importorskip("torch")
@@ -131,3 +132,37 @@ def test_gpu_empty_groups_cost_little(sv, lone):
     check_attention(a, out, lse, a.prefix, np.full(B, 3), None)
     check_attention(a, out2, lse2, a.prefix, np.full(B, 3), None)
     assert among <= 2 * alone, (among, alone)
+
+
+def test_workspace_of_rows_by_themselves():
+    """More than a query tile's rows of a row's key head: the paged attention's workspace, and no more, is asked for."""
+    import speculative_decoding_verification_55_gb300 as m
+    m.build_library()
+    L = m.lib()
+    shared, paged = L.spec_verify_shared_attention_workspace_size, L.spec_verify_paged_attention_workspace_size
+    c = ctypes.byref(cache_struct(max_pages=4096, num_pages=1 << 20))
+    for N, Hq in ((33, 32), (65, 32), (65, 16), (17, 64), (2, 1024)):          # 8 key heads
+        assert shared(64, N, Hq, 3, c) == paged(N, Hq, c) > 0
+    for N, Hq in ((32, 32), (64, 16), (16, 64), (1, 1024)):
+        assert shared(64, N, Hq, 3, c) >= 2 * 64 * N * Hq * (128 * 4 + 8)
+    c = ctypes.byref(cache_struct(max_pages=4096, num_pages=1 << 20, heads=10))          # 3 heads a key head: a tile of 126
+    assert shared(64, 43, 30, 3, c) == paged(43, 30, c) and shared(64, 42, 30, 3, c) > paged(42, 30, c)
+    for bad in ((0, 65, 32, 3), (64, 66, 32, 3), (64, 65, 30, 3), (1 << 20, 65, 32, 3), (64, 65, 32, 0)):
+        assert shared(*bad, ctypes.byref(cache_struct())) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N,G,D", [(33, 4, 128), (65, 2, 64), (17, 16, 256)])
+def test_gpu_workspace_of_rows_by_themselves(sv, N, G, D):
+    """It is enough: nothing behind it is written, whatever it held."""
+    a = Batch((40, 0, 300), N, 1, G, D, 16, seed=4, poison=False)
+    k, v, table = roomy(a, a.table)
+    cache = sv.PagedCache(k, v, dev(table))
+    need = sv.spec_verify_shared_attention_workspace_size(3, N, G, 1, cache)
+    assert need == sv.spec_verify_paged_attention_workspace_size(N, G, cache)
+    for fill in (0, 255):
+        room = torch.full((need + 512,), fill, dtype=torch.uint8, device="cuda")
+        out, lse = torch.empty_like(a.q.contiguous()), torch.empty((3, N, G), device="cuda")
+        sv.spec_verify_shared_attention(a.q, cache, dev(a.prefix), dev(np.zeros(3)), dev((0, 3)), None, None, out, lse, room[:need])
+        check_attention(a, out, lse, a.prefix, np.full(3, N), None)
+        assert bool((room[need:] == fill).all())
