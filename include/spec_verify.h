@@ -340,7 +340,8 @@ int spec_verify_kv_append(const void* k_new, const void* v_new, int64_t row_stri
  * round's other tokens those before it (a chain), or its ancestors when tree_parents is given:
  *   s_ij = scale * q_i . k_j,  lse_i = log sum_j exp(s_ij),  out_i = sum_j exp(s_ij - lse_i) v_j.
  * An entry that a token does not attend has no part in its outputs, whatever it holds (NaN included). An attended
- * value that is not finite leaves the output not finite: NaN where its probability is too small for fp32.
+ * value that is not finite leaves the output not finite: where its probability, as rounded for the product with the values,
+ * is 0, an infinity gives NaN (of the round's own entries: NaN or itself).
  * m_b = 1 is the attention of one new token.
  *
  * q              [B, N, Hq, D] of the cache's dtype, strides as k_new's in spec_verify_kv_append
@@ -365,8 +366,8 @@ int spec_verify_paged_attention(const void* q, int64_t q_row_stride, int64_t q_t
                                 void* workspace, size_t workspace_bytes, void* cuda_stream);
 
 /* spec_verify_paged_attention of a batch whose rows share the fronts of their contexts (a common prompt or document):
- * each front's keys and values are read once for all tokens of its rows, not once a row. What a row attends, and what
- * the outputs are, is as in spec_verify_paged_attention on the same tables.
+ * a front's keys and values are read once for up to 128 or 256 query rows (tokens times query heads of a key head) of its
+ * rows, not once a row. What a row attends, and what the outputs are, is as in spec_verify_paged_attention on the same tables.
  *
  * q              [B, N, Hq, D] as there; its rows follow one another (q_row_stride = N * q_token_stride where B and N are
  *                above 1, else SV_ERR_BAD_SHAPE: a slice of a fused projection has it)
@@ -378,8 +379,9 @@ int spec_verify_paged_attention(const void* q, int64_t q_row_stride, int64_t q_t
  * workspace      spec_verify_shared_attention_workspace_size(...) bytes, 256-byte aligned, without setup: among them two
  *                fp32 results of each query, 8 B N Hq (D + 2) bytes, and q again (with more than 128 query rows of a row's key
  *                head, below, the paged attention's alone). One workspace serves one call at a time.
- * Where fronts gain nothing (by the call's sizes: more than 128 query rows, tokens times query heads, of a row's key head, or
- * little room in the page tables and pages) every row is attended by its own table, and shared_len and group_start are not read.
+ * Where fronts gain nothing (by the call's sizes: more than 128 query rows of a row's key head, or little room, a row's
+ * being the lesser of max_pages and num_pages, in entries, whatever its length is) every row is attended by its own table, and
+ * shared_len and group_start are not read.
  * Else a row whose shared_len is none of the above is in error; all are where group_start does not ascend within 0 .. B.
  * B N Hq <= 2^28. Two or three launches. Other arguments, errors and limits as in spec_verify_paged_attention. */
 size_t spec_verify_shared_attention_workspace_size(int32_t B, int32_t N, int32_t Hq, int32_t groups,

@@ -273,8 +273,8 @@ def attend(q, cache, prefix_len, num_queries=None, tree_parents=None, scale=None
 
 
 def attend_shared(q, cache, prefix_len, shared_len, group_start, num_queries=None, tree_parents=None, scale=None, stream=None):
-    """attend of a batch whose rows share the fronts of their contexts, each front read once for all of its rows: rows
-    group_start[g] .. group_start[g + 1] - 1 have their first shared_len[b] entries, whole pages, in common. Returns
+    """attend of a batch whose rows share the fronts of their contexts, each front read once for many of its rows' queries:
+    rows group_start[g] .. group_start[g + 1] - 1 have their first shared_len[b] entries, whole pages, in common. Returns
     (out, lse) as attend does."""
     import torch
     if stream is not None:

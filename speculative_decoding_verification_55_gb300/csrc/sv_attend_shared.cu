@@ -301,13 +301,19 @@ extern "C" int spec_verify_shared_attention(const void* q, int64_t q_row_stride,
   // over 256 33 and 27, over 1024 34 and 44. 4 key heads of 128: 36 query rows, 24 rows over 4000 40 and 43, over 32,000 77
   // and 188; 72 query rows 52 and 43, 122 and 190, 64 rows over 4000 69 and 82; 128 query rows, 64 rows over 4000 95 and 86,
   // over 32,000 390 and 474. 16/2 heads of 64, one token: 64 rows over 1024 21 and 17, over 4096 23 and 30. One key head of
-  // 256, one token: 4 rows over 512 15 and 15, over 2048 16 and 17.
+  // 256, one token: 4 rows over 512 15 and 15, over 2048 16 and 17. The room is the tables', so that short rows in tables of
+  // a long context go by fronts: 4 rows over 512 in tables of 32,768 20 and 16, 24 rows of 18 tokens over 1000, 16/4 heads, 38
+  // and 27, 64 of 32 over 1000, 8/2 heads, 46 and 33. (More than a query tile a row: not measured by fronts, a row's own
+  // entries have one record and one query tile.)
   const long long room = std::min<long long>(cache->max_pages, cache->num_pages) * cache->page_size;
   const long long little = N * group > 96 ? kMuchRoom : (N * group > 64 ? kSomeRoom : (D < 256 ? kLittleRoom : kLittleRoom / 4));
   if (N * group > rows_tile || (D < 256 && room <= kShortRoom) || B * room * cache->heads * D * 4 <= little)
     return spec_verify_paged_attention(q, q_row_stride, q_token_stride, cache, prefix_len, num_queries, tree_parents, scale, out,
                                        out_lse, B, N, Hq, workspace, workspace_bytes, cuda_stream);
-  // Two query tiles at once where a group has more than one's rows.
+  // Two query tiles at once where groups, the empty ones among them, have more than one's rows on average (they are on the
+  // device). Two at once and one, us: a group of 256 rows of one token over 32,000 186 and 207, 1024 rows over 8000 363 and
+  // 373, 64 of 9 over 16,000 142 and 140, 40 of 5 over 4000 49 and 45, 256 of 2 over 16,000, 64/8 heads of 64, 249 and 236;
+  // groups below a tile: 40 of 3 rows over 4000 127 and 117, 16 of 4 rows of 4 tokens over 3000 68 and 64.
   const long long all = static_cast<long long>(B) * N * group;
   const int ways = D < 256 && all > static_cast<long long>(groups) * rows_tile ? 2 : 1;
   const int q_tokens = static_cast<int>(std::min<long long>(rows_tile / group, static_cast<long long>(B) * N));
